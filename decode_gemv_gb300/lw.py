@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(HERE, "_build", "liblw.so")
 LW_FMT_Q4_PAIR, LW_FMT_Q6, LW_FMT_BF16_EXP = 1, 2, 3
 # device status codes (*d_status), as in include/lw.h
 (LW_DEV_OK, LW_DEV_LANE_LENGTH, LW_DEV_BAD_CODE, LW_DEV_TILE_SIZE, LW_DEV_TIMEOUT,
- LW_DEV_BAD_TABLE, LW_DEV_BAD_STRIPS) = range(7)
+ LW_DEV_BAD_TABLE, LW_DEV_BAD_STRIPS, LW_DEV_BAD_SLOT, LW_DEV_BAD_PAGE,
+ LW_DEV_BAD_SEQ) = range(10)
 (LW_OK, LW_ERR_INVALID_ARG, LW_ERR_SHAPE, LW_ERR_UNSUPPORTED, LW_ERR_ALLOC, LW_ERR_CORRUPT,
  LW_ERR_CUDA, LW_ERR_IO) = range(8)
 SECTION_NAMES = ["words", "tile_off", "lane_bits", "table", "qparams", "signman",
@@ -29,7 +30,7 @@ SECTION_NAMES = ["words", "tile_off", "lane_bits", "table", "qparams", "signman"
 STATUS_NAMES = {0: "LW_OK", 1: "LW_ERR_INVALID_ARG", 2: "LW_ERR_SHAPE", 3: "LW_ERR_UNSUPPORTED",
                 4: "LW_ERR_ALLOC", 5: "LW_ERR_CORRUPT", 6: "LW_ERR_CUDA", 7: "LW_ERR_IO"}
 DEV_STATUS = {0: "ok", 1: "lane length", 2: "bad code", 3: "tile size", 4: "timeout",
-              5: "bad table"}
+              5: "bad table", 6: "bad strips", 7: "bad slot", 8: "bad page", 9: "bad sequence"}
 TABLE_BYTES = 1024
 EXPORTED = ["lw_encode_bundle", "lw_bundle_sections", "lw_bundle_free", "lw_table_from_lengths",
             "lw_validate_sections", "lw_workspace_bytes", "lw_decode", "lw_decode_gemv",
@@ -40,7 +41,10 @@ EXPORTED = ["lw_encode_bundle", "lw_bundle_sections", "lw_bundle_free", "lw_tabl
             "lw_bundle_deserialize", "lw_bundle_save", "lw_bundle_load", "lw_transcode_twin",
             "lw_twin_tile_rows", "lw_decode_gemm_strips", "lw_graph_begin", "lw_graph_end",
             "lw_graph_launch", "lw_graph_free", "lw_decode_gemm_group", "lw_twin_gemm_group",
-            "lw_table_lut_entries", "lw_test_stall_next"]
+            "lw_table_lut_entries", "lw_test_stall_next", "lw_kv_tile_bytes", "lw_kv_page_bytes",
+            "lw_kv_write", "lw_kv_read", "lw_kv_workspace_bytes", "lw_kv_attention"]
+LW_F32, LW_F16, LW_BF16 = 0, 1, 2
+LW_KV_GROUP, LW_KV_TILE, LW_KV_LIMIT = 32, 16, 61440.0
 
 
 class LwError(RuntimeError):
@@ -78,6 +82,31 @@ class LwDevBundle(ctypes.Structure):
                 ("qparams", ctypes.c_void_p), ("signman", ctypes.c_void_p),
                 ("vflags", ctypes.c_void_p), ("vrow_off", ctypes.c_void_p),
                 ("vexp", ctypes.c_void_p), ("lane_mid", ctypes.c_void_p)]
+
+
+class LwKvCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class LwKvRows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class LwKvAttn(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("q_tokens", ctypes.c_int64),
+                ("table_width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -130,6 +159,12 @@ def load():
         "lw_graph_free": ([P], None),
         "lw_table_lut_entries": ([P], i32),
         "lw_test_stall_next": ([i32], i32),
+        "lw_kv_tile_bytes": ([i32], sz),
+        "lw_kv_page_bytes": ([i32, i32, i32], sz),
+        "lw_kv_write": ([P, P, P, P, i64, P, P], i32),
+        "lw_kv_read": ([P, P, i64, P, P, P, P], i32),
+        "lw_kv_workspace_bytes": ([P, i32, i64, i32], sz),
+        "lw_kv_attention": ([P, P, P, sz, P, P], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -702,3 +737,184 @@ def lw_twin_gemv_group(dbs, xs, ys, ws, d_status, stream=None) -> None:
 
 def lw_noalloc_scratch_bytes() -> int:
     return int(load().lw_noalloc_scratch_bytes())
+
+
+# ----------------------------------------------------------------------------
+# the 4-bit key/value cache
+# ----------------------------------------------------------------------------
+
+class KvCache:
+    """Pages of the 4-bit key/value cache (the layout of lw_kv_cache in
+    include/lw.h) in a caller-owned tensor: any dtype and shape, contiguous,
+    a whole number of pages."""
+
+    def __init__(self, pages, kv_heads: int, head_dim: int, page_tokens: int):
+        fn = "KvCache"
+        self.kv_heads, self.head_dim, self.page_tokens = int(kv_heads), int(head_dim), int(page_tokens)
+        size = lw_kv_page_bytes(self.kv_heads, self.head_dim, self.page_tokens)
+        if not size:
+            _refuse(fn, f"{kv_heads} heads of {head_dim} values, pages of {page_tokens} tokens: head_dim "
+                        f"is 64, 96 or 128, page_tokens a positive multiple of {LW_KV_TILE}")
+        ptr = _buf(fn, "pages", pages, size)
+        have = pages.numel() * pages.element_size()
+        if have % size:
+            _refuse(fn, f"pages: {have} bytes, not a multiple of the page size {size}")
+        self.pages, self.device, self.n_pages = pages, pages.device, have // size
+        self.view = LwKvCache(ptr, self.n_pages, self.kv_heads, self.head_dim, self.page_tokens, 0)
+        self.ref = ctypes.byref(self.view)
+
+    @classmethod
+    def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page_tokens: int, device="cuda"):
+        """A cache in new memory, not initialised (keys past a sequence's
+        length are never used)."""
+        import torch
+        size = lw_kv_page_bytes(kv_heads, head_dim, page_tokens)
+        return cls(torch.empty(max(int(n_pages), 0) * size, dtype=torch.uint8, device=device),
+                   kv_heads, head_dim, page_tokens)
+
+
+def lw_kv_tile_bytes(head_dim: int) -> int:
+    return int(load().lw_kv_tile_bytes(head_dim))
+
+
+def lw_kv_page_bytes(kv_heads: int, head_dim: int, page_tokens: int) -> int:
+    return int(load().lw_kv_page_bytes(kv_heads, head_dim, page_tokens))
+
+
+def lw_kv_workspace_bytes(cache: KvCache, q_heads: int, q_tokens: int, batch: int) -> int:
+    return int(load().lw_kv_workspace_bytes(cache.ref, q_heads, q_tokens, batch))
+
+
+_KV_TYPES = {}
+
+
+def _kv_type(fn: str, name: str, t):
+    import torch
+    if not _KV_TYPES:
+        _KV_TYPES.update({torch.float32: LW_F32, torch.float16: LW_F16, torch.bfloat16: LW_BF16})
+    if not isinstance(t, torch.Tensor):
+        _refuse(fn, f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    code = _KV_TYPES.get(t.dtype)
+    if code is None:
+        _refuse(fn, f"{name}: dtype {str(t.dtype).replace('torch.', '')}, expected float32, float16 "
+                    "or bfloat16")
+    return code
+
+
+def _kv_heads(fn: str, name: str, t, tokens, heads, dim):
+    """Type code and strides of rows of heads [tokens][heads][dim]."""
+    code = _kv_type(fn, name, t)
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or \
+            (tokens is not None and t.shape[0] != tokens):
+        want = f"[{'tokens' if tokens is None else tokens}, {heads}, {dim}]"
+        _refuse(fn, f"{name}: shape {list(t.shape)}, expected {want}")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[0]:
+        _refuse(fn, f"{name}: the last dimension is strided")
+    return code, st, sh
+
+
+def _kv_index(fn: str, name: str, t, dtype, n):
+    """Address of a contiguous index vector of n entries."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        _refuse(fn, f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        _refuse(fn, f"{name}: dtype {str(t.dtype).replace('torch.', '')}, expected "
+                    f"{str(dtype).replace('torch.', '')}")
+    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        _refuse(fn, f"{name}: expected a contiguous vector" + ("" if n is None else f" of {n} entries"))
+    return t.data_ptr()
+
+
+def _kv_on(fn: str, cache: KvCache, named):
+    dev = cache.device
+    if dev.type != "cuda":
+        _refuse(fn, f"cache: pages on {dev}, expected a CUDA device")
+    for name, t in named:
+        if t.device != dev:
+            _refuse(fn, f"{name}: on {t.device}, the cache is on {dev}")
+
+
+def _kv_rows(fn: str, cache: KvCache, slots, k, v, d_status, stream, written: bool):
+    import torch
+    sp = _kv_index(fn, "slots", slots, torch.int64, None)
+    n = slots.shape[0]
+    rows = []
+    for name, t in (("k", k), ("v", v)):
+        code, st, sh = _kv_heads(fn, name, t, n, cache.kv_heads, cache.head_dim)
+        if written and n and not _kv_distinct(t):
+            _refuse(fn, f"{name}: rows that are written overlap")
+        rows.append(LwKvRows(t.data_ptr(), st, sh, code, 0))
+    stp = _status_ptr(fn, d_status)
+    _kv_on(fn, cache, (("slots", slots), ("k", k), ("v", v), ("d_status", d_status)))
+    return sp, n, ctypes.byref(rows[0]), ctypes.byref(rows[1]), stp, _stream_ptr(stream), rows
+
+
+def _kv_distinct(t) -> bool:
+    """Whether the rows [tokens][heads][dim] of `t` share no element."""
+    (n, h, d), (st, sh, _) = t.shape, t.stride()
+    if h == 1 or n == 1:
+        return (n == 1 or st >= d) and (h == 1 or sh >= d)
+    return (sh >= d and st >= (h - 1) * sh + d) or (st >= d and sh >= (n - 1) * st + d)
+
+
+def lw_kv_write(cache: KvCache, k, v, slots, d_status, stream=None) -> None:
+    """Quantise k, v [n, kv_heads, head_dim] (one dtype; the last dimension
+    contiguous) into the slots int64 [n]; a negative slot is not stored."""
+    fn = "lw_kv_write"
+    sp, n, kr, vr, stp, st, keep = _kv_rows(fn, cache, slots, k, v, d_status, stream, False)
+    _check(load().lw_kv_write(cache.ref, kr, vr, sp, n, stp, st), fn)
+
+
+def lw_kv_read(cache: KvCache, slots, k, v, d_status, stream=None) -> None:
+    """Read the slots back into k, v [n, kv_heads, head_dim]; a negative slot
+    reads as zeros."""
+    fn = "lw_kv_read"
+    sp, n, kr, vr, stp, st, keep = _kv_rows(fn, cache, slots, k, v, d_status, stream, True)
+    _check(load().lw_kv_read(cache.ref, sp, n, kr, vr, stp, st), fn)
+
+
+def lw_kv_attention(cache: KvCache, q, q_start, kv_len, page_table, out, ws, d_status, *,
+                    max_q: int, scale=None, causal: bool = True, window: int = 0, lse=None,
+                    stream=None) -> None:
+    """Attention of the packed query tokens q [tokens, q_heads, head_dim] over
+    the cache: sequence b owns tokens q_start[b]..q_start[b+1]-1 and kv_len[b]
+    keys in the pages page_table[b]; out as q, lse float32 [tokens, q_heads].
+    scale: 1 / sqrt(head_dim) by default."""
+    import torch
+    fn = "lw_kv_attention"
+    code = _kv_type(fn, "q", q)
+    heads = q.shape[1] if q.dim() == 3 else 0
+    if heads < 1 or heads % cache.kv_heads:
+        _refuse(fn, f"q: shape {list(q.shape)}, expected [tokens, a multiple of {cache.kv_heads}, "
+                    f"{cache.head_dim}]")
+    tokens = q.shape[0]
+    _, qt, qh = _kv_heads(fn, "q", q, None, heads, cache.head_dim)
+    ocode, ot, oh = _kv_heads(fn, "out", out, tokens, heads, cache.head_dim)
+    if ocode != code:
+        _refuse(fn, f"out: dtype {out.dtype}, q has {q.dtype}")
+    if tokens and not _kv_distinct(out):
+        _refuse(fn, "out: rows that are written overlap")
+    lens = _kv_index(fn, "kv_len", kv_len, torch.int32, None)
+    batch = kv_len.shape[0]
+    starts = _kv_index(fn, "q_start", q_start, torch.int32, batch + 1)
+    if not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32:
+        _refuse(fn, "page_table: expected an int32 tensor")
+    if page_table.dim() != 2 or page_table.shape[0] != batch or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        _refuse(fn, f"page_table: expected [{batch}, pages] with contiguous rows")
+    lsep = None
+    if lse is not None:
+        lsep = _buf(fn, "lse", lse, 4 * tokens * heads, (torch.float32,))
+    wp, wb = _ws_ptr(fn, ws)
+    sp = _status_ptr(fn, d_status)
+    named = (("q", q), ("out", out), ("q_start", q_start), ("kv_len", kv_len),
+             ("page_table", page_table), ("ws", ws), ("d_status", d_status))
+    _kv_on(fn, cache, named if lse is None else named + (("lse", lse),))
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    a = LwKvAttn(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, lsep, starts, lens,
+                 page_table.data_ptr(), page_table.stride(0), tokens, page_table.shape[1], code,
+                 batch, heads, int(max_q), int(bool(causal)), int(window), float(scale))
+    _check(load().lw_kv_attention(cache.ref, ctypes.byref(a), wp, wb, sp, _stream_ptr(stream)), fn)

@@ -83,8 +83,14 @@ enum {
   LW_DEV_TIMEOUT = 4,       /* a bounded wait on an asynchronous copy ran out */
   LW_DEV_BAD_TABLE = 5,     /* the device table fails its in-kernel checks, or
                                its length span exceeds what the launch expects */
-  LW_DEV_BAD_STRIPS = 6     /* a strip-list entry is outside the matrix or not
+  LW_DEV_BAD_STRIPS = 6,    /* a strip-list entry is outside the matrix or not
                                above the entry before it (its tiles skipped) */
+  LW_DEV_BAD_SLOT = 7,      /* a cache slot past the last page (token skipped) */
+  LW_DEV_BAD_PAGE = 8,      /* a page-table entry outside the cache under keys
+                               the call needs (those keys are left out) */
+  LW_DEV_BAD_SEQ = 9        /* q_start not ascending within [0, q_tokens] (the
+                               sequence is skipped), or kv_len negative or past
+                               the page table (clamped) */
 };
 
 typedef enum {
@@ -530,6 +536,133 @@ lw_status lw_test_stall_next(int32_t wait_us);
    tables built by lw_table_from_lengths. */
 int32_t lw_table_lut_entries(const lw_table* t);
 
+/*
+ * Key/value cache in 4 bits: the tokens a generator has seen, next to its
+ * coded weights.  Each key and value head of a token is quantised as it is
+ * written, in groups of LW_KV_GROUP consecutive values: with x the values in
+ * fp32, clamped to +-LW_KV_LIMIT,
+ *   min = fp16(lowest x), scale = fp16((highest x - lowest x) * (1/15)),
+ *   code = clamp(rint((x - min) * (1/scale)), 0, 15)   (0 where scale is 0)
+ * in fp32 with round-to-nearest-even throughout; the cached value is
+ * scale * code + min.  A group that holds a NaN or an infinity is stored with
+ * a NaN scale and min (codes 0): it reads back as NaN.  5 bits a value.
+ *
+ * Layout.  `pages` is device memory of the caller: [n_pages][kv_heads]
+ * [page_tokens / 16] tiles of lw_kv_tile_bytes(head_dim) bytes.  A tile holds
+ * one key/value head of 16 consecutive slots, t = 0..15; with G = head_dim/32
+ * and GP = G rounded up to even, its parts follow one another:
+ *   key codes       uint32 [t][q = 0..3][g]: nibble i (bits 4i..4i+3) is the
+ *                   code of d = 32 g + 8 q + i
+ *   key scales      fp16 [t / 2][g][t % 2]
+ *   key minimums    fp16 [t][GP] (entries g >= G are not read)
+ *   value codes     uint32 [t / 2][n = 0..7][g]: nibble i (i = 0..3) of half
+ *                   t % 2 (bits 16 (t % 2) + 4 i ..) is the code of
+ *                   d = 32 g + 4 n + i
+ *   value scales    fp16 [t / 2][g][t % 2]
+ *   value minimums  fp16 [t / 2][g][t % 2]
+ * (the order in which a warp's matrix-instruction operands take them: a lane
+ * reads its codes of all groups as one vector).  Every byte of a tile belongs
+ * to one token, so tokens of one tile may be written by different calls.
+ * Slot s is token s % page_tokens of page s / page_tokens.
+ * Memory that was never written may hold any bits: keys past a sequence's
+ * length are not used, whatever they hold.
+ *
+ * head_dim is 64, 96 or 128 (else LW_ERR_UNSUPPORTED), page_tokens a positive
+ * multiple of 16, pages 16-byte aligned.
+ */
+#define LW_KV_GROUP 32
+#define LW_KV_TILE 16
+#define LW_KV_LIMIT 61440.0f
+
+typedef enum { LW_F32 = 0, LW_F16 = 1, LW_BF16 = 2 } lw_dtype;
+
+typedef struct {
+  void* pages;
+  int64_t n_pages;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page_tokens;
+  int32_t reserved;
+} lw_kv_cache;
+
+/* Rows of heads in device memory: element (token, head, d) is
+   ptr[token * token_stride + head * head_stride + d], strides in elements
+   (any value for reads; rows written must not overlap). */
+typedef struct {
+  void* ptr;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t dtype;     /* lw_dtype */
+  int32_t reserved;
+} lw_kv_rows;
+
+/* Bytes of one tile (0 for an unsupported head_dim) and of one page (0 for an
+   unsupported shape). */
+size_t lw_kv_tile_bytes(int32_t head_dim);
+size_t lw_kv_page_bytes(int32_t kv_heads, int32_t head_dim, int32_t page_tokens);
+
+/*
+ * Quantise the keys and values of n tokens into their slots.  k, v: rows
+ * [n][kv_heads][head_dim] of one type each.  slots: device int64 [n]; a
+ * negative slot's token is not stored, a slot past the last page is reported
+ * (LW_DEV_BAD_SLOT) and not stored.  No two tokens of a call may name the same
+ * slot.  n = 0 launches nothing.
+ */
+lw_status lw_kv_write(const lw_kv_cache* c, const lw_kv_rows* k, const lw_kv_rows* v,
+                      const int64_t* slots, int64_t n, int32_t* d_status, void* stream);
+
+/*
+ * Read n slots back: scale * code + min in fp32, rounded to the rows' type.
+ * A negative slot reads as zeros, and so does one past the last page (which
+ * is reported).
+ */
+lw_status lw_kv_read(const lw_kv_cache* c, const int64_t* slots, int64_t n, const lw_kv_rows* k,
+                     const lw_kv_rows* v, int32_t* d_status, void* stream);
+
+/*
+ * Attention over the cache.  Sequence b has the query tokens q_start[b] ..
+ * q_start[b + 1] - 1 (packed rows of q) and kv_len[b] cached keys, in the
+ * pages page_table[b][0], [1], ...; its T query tokens stand at the key
+ * positions kv_len[b] - T .. kv_len[b] - 1 (write them first).  Query head h
+ * reads key/value head h / (q_heads / kv_heads).  A query at position p sees
+ * key j if j < kv_len[b], j <= p (causal) and j > p - window (window > 0).
+ *   s_j = scale q.k_j;  out = sum_j softmax(s)_j v_j;  lse = log sum_j exp s_j
+ * with the cached values of k and v.  A query that sees no key gets out = 0,
+ * lse = -inf.  Page-table entries beyond a sequence's length, and pages no
+ * query sees, are not read.  The answer does not depend on max_q, on the page
+ * size or on where the pages lie; it is deterministic on a given device.
+ */
+typedef struct {
+  const void* q;               /* [q_tokens][q_heads][head_dim], strided */
+  int64_t q_token_stride, q_head_stride;
+  void* out;                   /* the same shape and type as q */
+  int64_t out_token_stride, out_head_stride;
+  float* lse;                  /* [q_tokens][q_heads], or NULL */
+  const int32_t* q_start;      /* device [batch + 1] */
+  const int32_t* kv_len;       /* device [batch] */
+  const int32_t* page_table;   /* device [batch][table_stride], table_width used */
+  int64_t table_stride;
+  int64_t q_tokens;
+  int32_t table_width;
+  int32_t dtype;               /* lw_dtype of q and out */
+  int32_t batch;
+  int32_t q_heads;             /* a multiple of kv_heads */
+  int32_t max_q;               /* the most query tokens a sequence has (chooses
+                                  the kernel, nothing else) */
+  int32_t causal;              /* 0 or 1 */
+  int32_t window;              /* 0: unlimited */
+  float scale;
+} lw_kv_attn;
+
+/* Bytes of device workspace an lw_kv_attention call needs (zeroed by the
+   caller before first use; every call that completes leaves its counters at
+   zero).  0 for an unsupported shape. */
+size_t lw_kv_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens,
+                             int32_t batch);
+
+lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, void* ws, size_t ws_bytes,
+                          int32_t* d_status, void* stream);
+
 /* The status's name ("LW_OK", "LW_ERR_SHAPE", ...; "unknown lw_status" for
    other values): a static string, never NULL, not to be freed. */
 const char* lw_status_string(lw_status s);
@@ -561,7 +694,8 @@ void lw_graph_free(lw_graph* g);
 /* ABI revision of this header: 4 (3 + lw_sections.lut_entries and
    lw_dev_bundle.lut_entries, which selects the table-driven product
    kernel; 3 added grouped launches, strip lists, the load-time
-   transcode, bundle files, step graphs, LW_ERR_IO, LW_DEV_BAD_STRIPS).  The
+   transcode, bundle files, step graphs, LW_ERR_IO, LW_DEV_BAD_STRIPS; the
+   lw_kv_* calls came later and changed nothing before them).  The
    bundle file format carries its own version. */
 int32_t lw_version(void);
 
