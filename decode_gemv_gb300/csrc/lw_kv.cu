@@ -228,7 +228,7 @@ extern "C" size_t lw_kv_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, i
   if (!c || !lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens) || q_heads < 1 ||
       q_heads % c->kv_heads || q_tokens < 0 || batch < 1)
     return 0;
-  return 256;
+  return kv_attention_workspace(c);
 }
 
 extern "C" lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, void* ws,
@@ -243,6 +243,8 @@ extern "C" lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, 
   if (a->batch < 1 || a->batch > 65535) return fail(LW_ERR_SHAPE, "batch %d (1..65535)", a->batch);
   if (a->q_tokens < 0 || a->q_tokens > (1ll << 31) - 1)
     return fail(LW_ERR_SHAPE, "%lld query tokens", (long long)a->q_tokens);
+  if (a->q_tokens * a->q_heads > (1ll << 31) - 1 || (int64_t)a->max_q * a->q_heads > (1ll << 31) - 1)
+    return fail(LW_ERR_SHAPE, "%lld query tokens of %d heads", (long long)a->q_tokens, a->q_heads);
   if (a->max_q < 0) return fail(LW_ERR_INVALID_ARG, "max_q %d", a->max_q);
   if (a->window < 0) return fail(LW_ERR_INVALID_ARG, "window %d", a->window);
   if (a->causal != 0 && a->causal != 1) return fail(LW_ERR_INVALID_ARG, "causal %d", a->causal);

@@ -8,6 +8,7 @@
 namespace lw {
 
 int device_sm_count();
+int resident_blocks(const void* kernel, int threads, size_t smem);
 
 // Views of the cache and of rows of heads, checked by every call.
 lw_status check_kv_cache(const lw_kv_cache* c);
@@ -19,6 +20,8 @@ inline bool kv_rows_aligned(const void* p, int64_t token_stride, int64_t head_st
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && token_stride % n == 0 && head_stride % n == 0;
 }
 
+// Bytes of workspace of any attention call on a cache.
+size_t kv_attention_workspace(const lw_kv_cache* c);
 lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, void* ws, int32_t* status,
                               cudaStream_t st);
 

@@ -1,0 +1,147 @@
+// What the cache attention kernels share: their arguments, the search for a
+// CTA's first unit, and the join of an item's partial results.
+#pragma once
+
+#include "lw_kv.cuh"
+#include "lw_kvplan.h"
+
+namespace lw {
+
+struct AttnArgs {
+  lw_kv_attn p;
+  const uint8_t* pages;
+  int64_t n_pages, page_bytes;
+  uint32_t* counters;   // [grid], zero between calls
+  float* partials;      // [grid][2] partial results of RT rows
+  int32_t page_tokens, heads, group;
+  int32_t vec;          // q and out rows are 16-byte aligned
+  int32_t* status;
+};
+
+namespace dev {
+
+// T and n of sequence b; T = 0 if its query range is not one (LOUD: reported)
+template <bool LOUD>
+__device__ __forceinline__ void kv_seq(const AttnArgs& a, int b, int& q0, int& T, int& n) {
+  q0 = __ldg(a.p.q_start + b);
+  const int q1 = __ldg(a.p.q_start + b + 1);
+  n = __ldg(a.p.kv_len + b);
+  const int most = a.p.table_width * a.page_tokens;
+  const bool bad = q0 < 0 || q1 < q0 || q1 > a.p.q_tokens;
+  if (LOUD && (bad || n < 0 || n > most)) report(a.status, LW_DEV_BAD_SEQ);
+  T = bad ? 0 : q1 - q0;
+  n = n < 0 ? 0 : (n > most ? most : n);
+}
+
+// Sum over the CTA of one value per thread, and the exclusive sum before
+// each thread (s: NT / 32 + 1 places).
+template <int NT>
+__device__ __forceinline__ long long cta_scan(long long v, long long* s, long long& total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  long long inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 31) s[warp] = inc;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    before += w < warp ? s[w] : 0;
+    total += s[w];
+  }
+  return before + inc - v;
+}
+
+// The CTA's range of units, and the sequence its first unit is in.  Whole
+// CTA of NT threads; false if the CTA has no units.
+template <int NT, int RT, int PER>
+__device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int& q0) {
+  __shared__ long long s_scan[NT / 32 + 1], s_base;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, batch = a.p.batch;
+  long long sum = 0, first = 0;
+  for (int b = tid; b < batch; b += NT) {
+    int s, T, n;
+    if (blockIdx.x == 0) kv_seq<true>(a, b, s, T, n);
+    else kv_seq<false>(a, b, s, T, n);
+    const long long u = T ? a.heads * kv_head_units(T, n, a.group, RT, PER, a.p.causal, a.p.window) : 0;
+    if (b == tid) first = u;
+    sum += u;
+  }
+  long long before = cta_scan<NT>(sum, s_scan, U);
+  if (U == 0) return false;
+  G = (long long)gridDim.x < U ? (int)gridDim.x : (int)U;
+  if ((int)blockIdx.x >= G) return false;
+  w.x = kv_first(U, blockIdx.x, G);
+  w.xe = kv_first(U, blockIdx.x + 1, G);
+  if (batch <= NT) {   // the sums were one sequence each
+    if (w.x >= before && w.x < before + first) {
+      s_b = tid;
+      s_base = before;
+    }
+  } else {
+    long long carry = 0;
+    for (int cb = 0; cb < batch && carry <= w.x; cb += NT) {
+      const int b = cb + tid;
+      long long u = 0, total;
+      if (b < batch) {
+        int s, T, n;
+        kv_seq<false>(a, b, s, T, n);
+        u = T ? a.heads * kv_head_units(T, n, a.group, RT, PER, a.p.causal, a.p.window) : 0;
+      }
+      before = carry + cta_scan<NT>(u, s_scan, total);
+      if (w.x >= before && w.x < before + u) {
+        s_b = b;
+        s_base = before;
+      }
+      carry += total;
+    }
+  }
+  __syncthreads();
+  w.b = s_b;
+  w.base = s_base;
+  kv_seq<false>(a, w.b, q0, w.T, w.n);
+  kv_seek(w, a.group, RT, PER, a.p.causal, a.p.window);
+  return true;
+}
+
+// On to the next item; false at the end of the range.
+template <int RT, int PER>
+__device__ __forceinline__ bool kv_advance(const AttnArgs& a, KvWalk& w, int& q0) {
+  const bool same = kv_next(w, a.heads);
+  if (w.x >= w.xe) return false;
+  if (!same) {
+    w.base = w.x;
+    do {
+      ++w.b;
+      kv_seq<false>(a, w.b, q0, w.T, w.n);
+    } while (w.T == 0);
+  }
+  kv_start(w, a.group, RT, PER, a.p.causal, a.p.window);
+  return true;
+}
+
+__device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, const float (&f)[4]) {
+  if (a.p.dtype == LW_F32) {
+    float* o = static_cast<float*>(a.p.out) + at;
+    if (a.vec) *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+    else
+      for (int i = 0; i < 4; ++i) o[i] = f[i];
+  } else {
+    uint16_t h[4];
+    for (int i = 0; i < 4; ++i)
+      h[i] = a.p.dtype == LW_F16 ? __half_as_ushort(__float2half_rn(f[i]))
+                                 : __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+    uint16_t* o = static_cast<uint16_t*>(a.p.out) + at;
+    if (a.vec) *reinterpret_cast<uint2*>(o) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+    else
+      for (int i = 0; i < 4; ++i) o[i] = h[i];
+  }
+}
+
+}  // namespace dev
+}  // namespace lw
