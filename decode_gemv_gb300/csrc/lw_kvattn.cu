@@ -19,7 +19,6 @@ FewVariant few_variant(int mode) {
 }
 
 // The most resident CTAs of a launch, and the workspace places they have.
-constexpr int kFewPerSm = 1;
 inline int attn_ctas() { return kFewPerSm * device_sm_count(); }
 
 }  // namespace

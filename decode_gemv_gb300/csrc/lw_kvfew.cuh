@@ -10,54 +10,67 @@
 // So the codes themselves are the matrix operands (exact: a 4-bit integer is
 // a subnormal fp16, c 2^-24, by masking alone; MODE 0 makes it normal first,
 // because the instruction aligns a subnormal's products by its least exponent
-// and drops what falls below: 1e-5 of the result), the scales enter in fp32 after
-// the key product and in p before the value product, and the minimums take one
-// further matrix instruction each.  The values' codes are centred because both
-// sums would otherwise be some 2 sqrt(n) times their difference: the matrix
-// instruction's accumulation truncates, and 9000 keys lost 1.3e-4 to that.  The
-// middles, not fp16 any more, take two columns each (hi, lo).  The other
-// operands (q', its group sums, p sc, p) are fp16: in MODE 0 (fp32 and fp16
-// calls) as two parts x = hi + lo 2^-11 of 11 bits each, hi in rows 0..7 and
-// lo in rows 8..15 of the same instruction, which the rows of a single token
-// leave free; in MODE 1 (16 rows) and MODE 2 (8 rows) hi alone, for bf16
-// calls: q is exact there, and p rounded to 11 bits is 8 times finer than the
-// output's 8.  Products accumulate in fp32, in MODE 0 for kFewFlush tiles
-// before they are added to shared memory rounded to nearest (the truncation
-// of many steps is a drift, not a scatter).
+// and drops what falls below: 1e-5 of the result), the scales enter in fp32
+// after the key product and in p before the value product, and the minimums
+// take one further matrix instruction each.  The values' codes are centred
+// because both sums would otherwise be some 2 sqrt(n) times their difference:
+// the matrix instruction's accumulation truncates, and 9000 keys lost 1.3e-4 to
+// that.  The middles, not fp16 any more, take two rows each in MODE 0 (hi, lo).
 //
-// Structure.  A CTA walks its range of units (lw_kvplan.h); a producer warp
-// fills a ring of shared-memory stages with a unit's 16-key tiles by bulk
-// copies, tile w for consumer warp w, which keeps its own running maximum,
-// sum and accumulators (one pass over the data) until the item ends; then the
-// warps' states are joined in shared memory.  An item cut between CTAs leaves
-// partial states in the workspace, and the CTA that brings the item's count
-// to its end joins them, in CTA order (the answer does not depend on the
-// order of arrival).
+// The key product has the rows as its first dimension (16 places), the value
+// product as its second (8 columns a step): the first one's accumulator
+// fragment is then the second one's operand fragment, and the accumulators of
+// 8 rows of 128 values take 32 registers.  The operands q', its group sums,
+// p sc and p are fp16: in MODE 0 (fp32 and fp16 calls, 8 rows) as two parts of
+// 11 bits each -- q' = hi + lo 2^-11 in rows 0..7 and 8..15 of one instruction,
+// p as hi + lo in two, p sc brought near 1 by a power of two first -- in MODE 1
+// (16 rows) and MODE 2 (8 rows) one part, for bf16 calls: q is exact there, and
+// p and p sc rounded to 11 bits are 8 times finer than the output's 8.  Products
+// accumulate in fp32, in MODE 0 for kFewFlush tiles before they are added to
+// shared memory rounded to nearest (the truncation of many steps is a drift,
+// not a scatter).
+//
+// Structure.  A CTA walks its range of units (lw_kvplan.h).  Warp w takes
+// every kFewWarps-th pair of 16-key tiles, fetched by bulk copies into a ring of its
+// own, and keeps its own running maximum, sum and accumulators (one pass over
+// the data) until the item ends; then the next item's first tiles are sent
+// for, and the warps' states are joined in shared memory.  An item cut between
+// CTAs leaves partial states in the workspace, and the CTA that brings the
+// item's count to its end joins them, in CTA order (the answer does not depend
+// on the order of arrival).
 #pragma once
 
 #include "lw_kvattn.cuh"
 
 namespace lw {
 
-constexpr int kFewWarps = 8;                        // consumer warps = tiles of a unit
-constexpr int kFewThreads = 32 * (kFewWarps + 1);
-constexpr int kFewStages = 4;
+constexpr int kFewWarps = 8;                        // warps of a CTA
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kFewPerSm = 2;                        // resident CTAs
+constexpr int kFewStages = 2;                       // places of a warp's ring, two tiles each
+constexpr int kFewUnit = 2 * kFewWarps;             // tiles of a unit
 constexpr int kFewFlush = 32;                       // tiles between two additions (MODE 0)
 
 template <int D, int MODE>
 struct Few {
   using L = KvTile<D>;
   static constexpr int kRows = MODE == 1 ? 16 : 8;   // rows of an item
-  static constexpr int kStage = kFewWarps * L::kBytes;
-  static constexpr int kPitch = D + 4;               // floats: conflict-free row writes
-  static constexpr int kRing = 256;
-  static constexpr int kJoin = kRing + kFewStages * kStage;
-  static constexpr int kState = kJoin + kFewWarps * 8 * kPitch * 4;   // m, l [warps][8]
-  static constexpr int kSmem = kState + 2 * kFewWarps * 8 * 4;
+  static constexpr int kRing = 256;                  // after the barriers and the flag
+  static constexpr int kJoin = kRing + kFewWarps * kFewStages * 2 * L::kBytes;
+  static constexpr int kState = kJoin + kFewWarps * 8 * D * 4;   // m, l [warps][8]
+  static constexpr int kNeed = kState + 2 * kFewWarps * 8 * 4;
+  // above the limit that holds without an attribute (static shared memory counts towards it)
+  static constexpr int kSmem = kNeed > 49168 ? kNeed : 49168;
   static constexpr int kPartial = kRows * (D + 2);   // floats: m, l, then the rows
 };
 
 namespace dev {
+
+// Place of element d (a multiple of 4) of row r among a warp's 8 rows in shared
+// memory: the four rows that a quarter of a warp stores at once fall on
+// different banks.
+template <int D>
+__device__ __forceinline__ int few_place(int r, int d) { return r * D + (d ^ ((r & 6) * 4)); }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -66,6 +79,30 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same with a zero accumulator
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// two products at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -73,15 +110,13 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ float2 h2f(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
-// x = hi + lo 2^-11: the fp16 pairs of two values
+// x = hi + lo / up: the fp16 pairs of two values
+template <int UP>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x, y);
   const float2 f = __half22float2(h);
   hi = h2bits(h);
-  lo = h2bits(__floats2half2_rn((x - f.x) * 2048.f, (y - f.y) * 2048.f));
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+  lo = h2bits(__floats2half2_rn((x - f.x) * UP, (y - f.y) * UP));
 }
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
@@ -96,10 +131,12 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
     for (int i = 0; i < N; ++i) w[i] = lds_u32(at + 4 * i);
   }
 }
-__device__ __forceinline__ void few_bar() {   // the consumer warps
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");
+__device__ __forceinline__ uint32_t max_h2(uint32_t x, uint32_t y) {
+  return h2bits(__hmax2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y)));
 }
-
+__device__ __forceinline__ uint32_t mul_h2(uint32_t x, uint32_t y) {
+  return h2bits(__hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y)));
+}
 // x[i] * m + b in fp16 pairs; the operands are exact here
 __device__ __forceinline__ uint32_t fma_h2(uint32_t x, uint32_t m, uint32_t b) {
   uint32_t y;
@@ -148,7 +185,12 @@ struct FewWarp {
   uint32_t aq[G][2][MODE == 2 ? 2 : 4];   // query operands: step, (a0, a2) or a0..a3
   uint32_t am[MODE == 2 ? 1 : 2];         // group sums
   FewRow row[NR];
-  float o[G][4][4], om[4];
+  // value sums: [g][s]: elements 32 g + 4 (lane / 4) + 2 s, + 1 (registers 0, 1
+  // and 2, 3) of rows 2 q, 2 q + 1 (and 8 more for the second NR); om: sums of
+  // the middles of group lane / 4 (hi parts; lane / 4 - 4: lo parts)
+  float o[NR][G][2][4], om[NR][4];
+  float unit;       // 2^E: p sc 2^-E is the operand (E <= 0 in MODE 1, 2, where om has the factor too)
+  uint32_t most;    // the largest scale it allows, twice
   float fm;         // row[0].m when the sums last went to shared memory (MODE 0)
 
   // Row r of the row tile (lane / 4, and lane / 4 + 8 in MODE 1)
@@ -200,8 +242,8 @@ struct FewWarp {
         const float u0 = x[g][2 * st], u1 = x[g][2 * st + 4];
         const float v0 = x[g][2 * st + 1] * kOdd, v1 = x[g][2 * st + 5] * kOdd;
         if constexpr (MODE == 0) {
-          split2(u0, u1, aq[g][st][0], aq[g][st][1]);
-          split2(v0, v1, aq[g][st][2], aq[g][st][3]);
+          split2<2048>(u0, u1, aq[g][st][0], aq[g][st][1]);
+          split2<2048>(v0, v1, aq[g][st][2], aq[g][st][3]);
         } else if constexpr (MODE == 1) {
           aq[g][st][which] = h2bits(__floats2half2_rn(u0, u1));
           aq[g][st][2 + which] = h2bits(__floats2half2_rn(v0, v1));
@@ -217,22 +259,28 @@ struct FewWarp {
       if (g == 2 * q) s0 = sum[g];
       if (g == 2 * q + 1) s1 = sum[g];
     }
-    if constexpr (MODE == 0) split2(s0, s1, am[0], am[1]);
+    if constexpr (MODE == 0) split2<2048>(s0, s1, am[0], am[1]);
     else am[which] = h2bits(__floats2half2_rn(s0, s1));
   }
 
   __device__ void start(const AttnArgs& a, const KvWalk& w, int q0, int rt_rows, int lane) {
 #pragma unroll
     for (int i = 0; i < NR; ++i) load_row(a, w, q0, rt_rows, i, lane);
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[g][i][j] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) om[j] = 0.f;
+    clear();
+    unit = 6.103515625e-5f;   // 2^-14
+    most = 0;
     fm = -INFINITY;
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][g][0][j] = o[i][g][1][j] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) om[i][j] = 0.f;
+    }
   }
 
   // One tile of 16 keys, keys kb..kb+15.  EDGE: some row does not see some of
@@ -244,37 +292,38 @@ struct FewWarp {
     uint32_t see[NR];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {   // 8 keys each
-      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      float c[4];
       uint32_t mn = 0;
       if (2 * q < L::GP) mn = lds_u32(s + L::kKeyMin + (uint32_t)((8 * h + r) * L::GP + 2 * q) * 2);
       if (G % 2 && q == G / 2) mn &= 0xFFFFu;
-      mma_f16(c, am[0], MODE == 2 ? 0u : am[MODE == 2 ? 0 : 1], 0u, 0u, mn, 0u);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] *= MODE == 0 ? 9.765625e-4f : 5.9604644775390625e-8f;   // as the codes' products
+      mma_f16_zero(c, am[0], MODE == 2 ? 0u : am[MODE == 2 ? 0 : 1], 0u, 0u, mn, 0u);
+      constexpr float kUnit = MODE == 0 ? 9.765625e-4f : 5.9604644775390625e-8f;   // as the codes' products
+      float2 x = mul2(make_float2(c[0], c[1]), make_float2(kUnit, kUnit));
+      float2 y = mul2(make_float2(c[2], c[3]), make_float2(kUnit, kUnit));
       uint32_t kw[G], sw[G];
       lds_words<G>(s + L::kKeyCodes + (uint32_t)(((8 * h + r) * 4 + q) * G) * 4, kw);
       lds_words<G>(s + L::kKeyScale + (uint32_t)((4 * h + q) * G) * 4, sw);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          const uint32_t w = kw[g] >> (8 * st);
-          if constexpr (MODE == 2) mma_f16(d, aq[g][st][0], 0u, aq[g][st][1], 0u, code_even<MODE>(w), code_odd<MODE>(w));
-          else mma_f16(d, aq[g][st][0], aq[g][st][1], aq[g][st][2], aq[g][st][3], code_even<MODE>(w), code_odd<MODE>(w));
+        float d[4];
+        const uint32_t w = kw[g] >> 8;
+        if constexpr (MODE == 2) {
+          mma_f16_zero(d, aq[g][0][0], 0u, aq[g][0][1], 0u, code_even<MODE>(kw[g]), code_odd<MODE>(kw[g]));
+          mma_f16(d, aq[g][1][0], 0u, aq[g][1][1], 0u, code_even<MODE>(w), code_odd<MODE>(w));
+        } else {
+          mma_f16_zero(d, aq[g][0][0], aq[g][0][1], aq[g][0][2], aq[g][0][3], code_even<MODE>(kw[g]),
+                       code_odd<MODE>(kw[g]));
+          mma_f16(d, aq[g][1][0], aq[g][1][1], aq[g][1][2], aq[g][1][3], code_even<MODE>(w), code_odd<MODE>(w));
         }
         const float2 sc = h2f(sw[g]);
-        c[0] = fmaf(sc.x, d[0], c[0]);
-        c[1] = fmaf(sc.y, d[1], c[1]);
-        if constexpr (MODE != 2) {
-          c[2] = fmaf(sc.x, d[2], c[2]);
-          c[3] = fmaf(sc.y, d[3], c[3]);
-        }
+        x = fma2(sc, make_float2(d[0], d[1]), x);
+        if constexpr (MODE != 2) y = fma2(sc, make_float2(d[2], d[3]), y);
       }
-      if constexpr (MODE == 0) {
-        c[0] = fmaf(c[2], 4.8828125e-4f, c[0]);   // 2^-11
-        c[1] = fmaf(c[3], 4.8828125e-4f, c[1]);
-      }
+      if constexpr (MODE == 0) x = fma2(y, make_float2(4.8828125e-4f, 4.8828125e-4f), x);   // 2^-11
+      c[0] = x.x;
+      c[1] = x.y;
+      c[2] = y.x;
+      c[3] = y.y;
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         t[i][2 * h] = c[2 * i] * row[i].f;
@@ -295,8 +344,26 @@ struct FewWarp {
       }
       up |= fmaxf(fmaxf(t[i][0], t[i][1]), fmaxf(t[i][2], t[i][3])) > row[i].m;
     }
-    if (__any_sync(0xFFFFFFFFu, up)) {   // some row has a new maximum: rescale
-      float al[2];
+    uint32_t v0[G], v1[G], s0[G], s1[G];
+    lds_words<G>(s + L::kValScale + (uint32_t)(q * G) * 4, s0);
+    lds_words<G>(s + L::kValScale + (uint32_t)((q + 4) * G) * 4, s1);
+    if constexpr (EDGE) {   // what lies past the end may be anything
+      const auto cut = [&](uint32_t w, int key) {
+        return (key < n ? w & 0xFFFFu : 0u) | (key + 1 < n ? w & 0xFFFF0000u : 0u);
+      };
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        s0[g] = cut(s0[g], kb + 2 * q);
+        s1[g] = cut(s1[g], kb + 8 + 2 * q);
+      }
+    }
+    // the operands' unit covers the largest scale so far
+    uint32_t big = max_h2(s0[0], s1[0]);
+#pragma unroll
+    for (int g = 1; g < G; ++g) big = max_h2(big, max_h2(s0[g], s1[g]));
+    up |= max_h2(big, most) != most;
+    if (__any_sync(0xFFFFFFFFu, up)) {   // a new maximum: rescale
+      float al[NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         float x = fmaxf(fmaxf(t[i][0], t[i][1]), fmaxf(t[i][2], t[i][3]));
@@ -308,16 +375,45 @@ struct FewWarp {
         row[i].m = x;
         row[i].l *= al[i];
       }
-      if (NR == 1) al[1] = al[0];
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int i = 0; i < NR; ++i) {   // to the lanes that hold the rows' sums
+        const float a0 = __shfl_sync(0xFFFFFFFFu, al[i], 8 * q), a1 = __shfl_sync(0xFFFFFFFFu, al[i], 8 * q + 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+          const float x = j % 2 ? a1 : a0;
+          om[i][j] *= x;
 #pragma unroll
-          for (int j = 0; j < (MODE == 2 ? 2 : 4); ++j) o[g][i][j] *= al[j / 2];
+          for (int g = 0; g < G; ++g) {
+            o[i][g][0][j] *= x;
+            o[i][g][1][j] *= x;
+          }
+        }
+      }
 #pragma unroll
-      for (int j = 0; j < (MODE == 2 ? 2 : 4); ++j) om[j] *= al[j / 2];
+      for (int d = 1; d < 4; d <<= 1) big = max_h2(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
+      big = max_h2(big, most);
+      uint32_t top = big & 0xFFFFu, t2 = big >> 16;   // scales are positive, or NaN
+      top = top > 0x7C00u ? 0u : top;
+      if (t2 <= 0x7C00u && t2 > top) top = t2;
+      const float before = unit;
+      most = ((top >> 10) << 10 | 0x3FFu) * 0x10001u;
+      int e = (int)(top >> 10) < 1 ? 1 : (int)(top >> 10);
+      if (MODE != 0 && e > 15) e = 15;
+      unit = __uint_as_float((uint32_t)(e + 112) << 23);
+      const float down = before * __uint_as_float(0x7F000000u - __float_as_uint(unit));
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (MODE != 0) om[i][j] *= down;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            o[i][g][0][j] *= down;
+            o[i][g][1][j] *= down;
+          }
+        }
     }
+    const float inv = __uint_as_float(0x7F000000u - __float_as_uint(unit));   // 2^-E
     float p[NR][4];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
@@ -325,11 +421,19 @@ struct FewWarp {
       for (int j = 0; j < 4; ++j) p[i][j] = ex2(t[i][j] - row[i].mu);
       row[i].l += (p[i][0] + p[i][1]) + (p[i][2] + p[i][3]);
     }
-    // middles: columns of this instruction are groups, their hi parts, then their lo parts
-    {
-      uint32_t b0 = 0, b1 = 0, a0, a1 = 0, a2, a3 = 0;
-      if (r % 4 < G) {
-        auto middle = [&](int pair, int key) {
+    float2 pe[NR][2];       // p 2^-E
+    uint32_t ph[NR][2];     // the same in fp16 (MODE 1, 2)
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        pe[i][j] = mul2(make_float2(p[i][2 * j], p[i][2 * j + 1]), make_float2(inv, inv));
+        ph[i][j] = h2bits(__floats2half2_rn(pe[i][j].x, pe[i][j].y));
+      }
+    {   // middles: rows of this instruction are groups, their hi parts, then their lo parts
+      uint32_t a0 = 0, a2 = 0;
+      if (MODE == 0 ? r % 4 < G : r < G) {
+        const auto middle = [&](int pair, int key) {
           const float2 mn = h2f(lds_u32(s + L::kValMin + (uint32_t)(pair * G + r % 4) * 4));
           const float2 sc = h2f(lds_u32(s + L::kValScale + (uint32_t)(pair * G + r % 4) * 4));
           float x = fmaf(8.f, sc.x, mn.x), y = fmaf(8.f, sc.y, mn.y);
@@ -337,122 +441,103 @@ struct FewWarp {
             if (key >= n || isnan(x)) x = 0.f;
             if (key + 1 >= n || isnan(y)) y = 0.f;
           }
+          if constexpr (MODE != 0) return h2bits(__floats2half2_rn(x, y));
           uint32_t hi, lo;
-          split2(x, y, hi, lo);
+          split2<2048>(x, y, hi, lo);
           return r < 4 ? hi : lo;
         };
-        b0 = middle(q, kb + 2 * q);
-        b1 = middle(q + 4, kb + 8 + 2 * q);
+        a0 = middle(q, kb + 2 * q);
+        a2 = middle(q + 4, kb + 8 + 2 * q);
       }
-      if constexpr (MODE == 0) {
-        split2(p[0][0], p[0][1], a0, a1);
-        split2(p[0][2], p[0][3], a2, a3);
-      } else {
-        a0 = h2bits(__floats2half2_rn(p[0][0], p[0][1]));
-        a2 = h2bits(__floats2half2_rn(p[0][2], p[0][3]));
-        if constexpr (MODE == 1) {
-          a1 = h2bits(__floats2half2_rn(p[NR - 1][0], p[NR - 1][1]));
-          a3 = h2bits(__floats2half2_rn(p[NR - 1][2], p[NR - 1][3]));
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        if constexpr (MODE == 0) {
+          uint32_t b0, b1, c0, c1;
+          split2<1>(p[i][0], p[i][1], b0, c0);
+          split2<1>(p[i][2], p[i][3], b1, c1);
+          mma_f16(om[i], a0, 0u, a2, 0u, c0, c1);
+          mma_f16(om[i], a0, 0u, a2, 0u, b0, b1);
+        } else {
+          mma_f16(om[i], a0, 0u, a2, 0u, ph[i][0], ph[i][1]);
         }
       }
-      mma_f16(om, a0, a1, a2, a3, b0, b1);
     }
-    uint32_t v0[G], v1[G], s0[G], s1[G];
     lds_words<G>(s + L::kValCodes + (uint32_t)((q * 8 + r) * G) * 4, v0);
     lds_words<G>(s + L::kValCodes + (uint32_t)(((q + 4) * 8 + r) * G) * 4, v1);
-    lds_words<G>(s + L::kValScale + (uint32_t)(q * G) * 4, s0);
-    lds_words<G>(s + L::kValScale + (uint32_t)((q + 4) * G) * 4, s1);
-#pragma unroll
-    for (int i = 0; i < NR; ++i)   // p sc 4 stays below 2^16: scales are at most 8192
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[i][j] *= 4.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const float2 x = h2f(s0[g]), y = h2f(s1[g]);
-      const float sc[4] = {x.x, x.y, y.x, y.y};
-      float u[NR][4];
+      uint32_t b0[NR], b1[NR], c0[NR], c1[NR];
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
+      for (int i = 0; i < NR; ++i) {
+        if constexpr (MODE == 0) {
+          const float2 ux = mul2(pe[i][0], h2f(s0[g])), uy = mul2(pe[i][1], h2f(s1[g]));
+          float u[4] = {ux.x, ux.y, uy.x, uy.y};
+          if constexpr (EDGE) {   // a NaN that this row does not see
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          u[i][j] = p[i][j] * sc[j];
-          if constexpr (EDGE)
-            if (!(see[i] >> j & 1u)) u[i][j] = 0.f;
-        }
-      uint32_t a0, a1 = 0, a2, a3 = 0;
-      if constexpr (MODE == 0) {
-        split2(u[0][0], u[0][1], a0, a1);
-        split2(u[0][2], u[0][3], a2, a3);
-      } else {
-        a0 = h2bits(__floats2half2_rn(u[0][0], u[0][1]));
-        a2 = h2bits(__floats2half2_rn(u[0][2], u[0][3]));
-        if constexpr (MODE == 1) {
-          a1 = h2bits(__floats2half2_rn(u[NR - 1][0], u[NR - 1][1]));
-          a3 = h2bits(__floats2half2_rn(u[NR - 1][2], u[NR - 1][3]));
+            for (int j = 0; j < 4; ++j)
+              if (!(see[i] >> j & 1u)) u[j] = 0.f;
+          }
+          split2<1>(u[0], u[1], b0[i], c0[i]);
+          split2<1>(u[2], u[3], b1[i], c1[i]);
+        } else {
+          b0[i] = mul_h2(ph[i][0], s0[g]);
+          b1[i] = mul_h2(ph[i][1], s1[g]);
+          if constexpr (EDGE) {
+            b0[i] &= (see[i] & 1u ? 0xFFFFu : 0u) | (see[i] & 2u ? 0xFFFF0000u : 0u);
+            b1[i] &= (see[i] & 4u ? 0xFFFFu : 0u) | (see[i] & 8u ? 0xFFFF0000u : 0u);
+          }
         }
       }
-      mma_f16(o[g][0], a0, a1, a2, a3, centre_even(v0[g]), centre_even(v1[g]));
-      mma_f16(o[g][1], a0, a1, a2, a3, centre_odd(v0[g]), centre_odd(v1[g]));
-      mma_f16(o[g][2], a0, a1, a2, a3, centre_even(v0[g] >> 8), centre_even(v1[g] >> 8));
-      mma_f16(o[g][3], a0, a1, a2, a3, centre_odd(v0[g] >> 8), centre_odd(v1[g] >> 8));
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const uint32_t w0 = v0[g] >> (8 * st), w1 = v1[g] >> (8 * st);
+        const uint32_t a0 = centre_even(w0), a1 = centre_odd(w0), a2 = centre_even(w1), a3 = centre_odd(w1);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          if constexpr (MODE == 0) mma_f16(o[i][g][st], a0, a1, a2, a3, c0[i], c1[i]);
+          mma_f16(o[i][g][st], a0, a1, a2, a3, b0[i], b1[i]);
+        }
+      }
     }
   }
 
-  // This lane's 8 elements (32 g + 8 q + 0..7) of row `which`, in true units
-  __device__ __forceinline__ void finish(int which, int g, int lane, float (&x)[8]) const {
-    float m0 = om[2 * which], m1 = om[2 * which + 1];
-    if constexpr (MODE == 0) {
-      m0 = fmaf(om[2], 4.8828125e-4f, m0);
-      m1 = fmaf(om[3], 4.8828125e-4f, m1);
-    }
-    const int src = (lane & ~3) + g / 2;   // the lane with columns g & ~1, g | 1; their lo parts two on
-    const float mx = g % 2 ? m1 : m0;
-    const float mn = fmaf(__shfl_sync(0xFFFFFFFFu, mx, src + 2), 4.8828125e-4f,
-                          __shfl_sync(0xFFFFFFFFu, mx, src));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y0 = o[g][i][2 * which], y1 = o[g][i][2 * which + 1];
-      if constexpr (MODE == 0) {
-        y0 = fmaf(o[g][i][2], 4.8828125e-4f, y0);
-        y1 = fmaf(o[g][i][3], 4.8828125e-4f, y1);
-      }
-      constexpr float up = 256.f;   // 2^10 / 4
-      x[i] = fmaf(y0, up, mn);
-      x[4 + i] = fmaf(y1, up, mn);
-    }
+  // This lane's elements 32 g + 4 (lane / 4) + 0..3 of row 2 q + e (and 8 which),
+  // in true units
+  __device__ __forceinline__ float4 finish(int which, int g, int e, int lane) const {
+    // the lanes with this group's hi and lo parts for rows 2 q, 2 q + 1
+    float mn = __shfl_sync(0xFFFFFFFFu, om[which][e], 4 * g + lane % 4);
+    if constexpr (MODE == 0)
+      mn = fmaf(__shfl_sync(0xFFFFFFFFu, om[which][e], 16 + 4 * g + lane % 4), 4.8828125e-4f, mn);
+    if constexpr (MODE != 0) mn *= unit;
+    const float up = 1024.f * unit;
+    return make_float4(fmaf(o[which][g][0][e], up, mn), fmaf(o[which][g][0][2 + e], up, mn),
+                       fmaf(o[which][g][1][e], up, mn), fmaf(o[which][g][1][2 + e], up, mn));
   }
 
-  // The same with what went to shared memory before (at: this lane's 8
-  // elements of group 0 there)
-  __device__ __forceinline__ void gather(int which, int g, int lane, const float* at, float (&x)[8]) const {
-    finish(which, g, lane, x);
-    if (MODE == 0 && __any_sync(0xFFFFFFFFu, fm != -INFINITY)) {
-      const float e = ex2(fm - row[0].mu);
-      const float4 u = *reinterpret_cast<const float4*>(at + 32 * g);
-      const float4 v = *reinterpret_cast<const float4*>(at + 32 * g + 4);
-      const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  // Add the sums of rows 8 which .. 8 which + 7 to what shared memory holds of
+  // them (MODE 0; nothing before the first time) or put them there.  at: the
+  // warp's 8 rows.
+  __device__ __forceinline__ void put(int which, int lane, float* at) const {
+    const int q = lane % 4;
+    const float held = MODE == 0 ? (fm == -INFINITY ? 0.f : ex2(fm - row[0].mu)) : 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (fm != -INFINITY) x[i] = fmaf(y[i], e, x[i]);
+    for (int e = 0; e < 2; ++e) {
+      const float h = MODE == 0 ? __shfl_sync(0xFFFFFFFFu, held, 8 * q + 4 * e) : 0.f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float4* to = reinterpret_cast<float4*>(at + few_place<D>(2 * q + e, 32 * g + 4 * (lane / 4)));
+        float4 x = finish(which, g, e, lane);
+        if (MODE == 0 && h != 0.f) {
+          const float4 y = *to;
+          x = make_float4(fmaf(y.x, h, x.x), fmaf(y.y, h, x.y), fmaf(y.z, h, x.z), fmaf(y.w, h, x.w));
+        }
+        *to = x;
+      }
     }
-  }
-  __device__ __forceinline__ void put(int which, int g, int lane, float* at) const {
-    float x[8];
-    gather(which, g, lane, at, x);
-    *reinterpret_cast<float4*>(at + 32 * g) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(at + 32 * g + 4) = make_float4(x[4], x[5], x[6], x[7]);
   }
   __device__ __forceinline__ void flush(int lane, float* at) {
-#pragma unroll
-    for (int g = 0; g < G; ++g) put(0, g, lane, at);
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[g][i][j] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) om[j] = 0.f;
+    put(0, lane, at);
+    clear();
     fm = row[0].m;
   }
 };
@@ -472,88 +557,98 @@ __device__ __forceinline__ void few_out(const AttnArgs& a, const KvWalk& w, int 
     a.p.lse[(int64_t)(q0 + t) * a.p.q_heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// A warp's pairs of tiles: sent for in order, kFewStages ahead.  The table is
+// read 32 tiles at a time, lane i holding where the i-th lies and sending for it.
+template <int D>
+struct FewFetch {
+  static constexpr int kTile = KvTile<D>::kBytes;
+  uint8_t* ring;
+  uint64_t* bars;
+  const int32_t* table;    // the sequence's pages
+  const uint8_t* src;      // this lane's tile, of the 32
+  int64_t head;            // first byte of the head in a page
+  int first, last;         // the item's tiles of this warp: first, first + 1, then kFewUnit on, below last
+  int next, at;            // tile to send for; its place among the 32
+  uint32_t there;          // which of the 32 have a page
+  int in, out;             // ring places to fill and to use
+  uint32_t have, parity;   // tiles sent for (two bits a place); phase per place
+
+  __device__ __forceinline__ void lookup(const AttnArgs& a, int lane) {
+    const int tile = next + (lane >> 1) * kFewUnit + (lane & 1), tpp = a.page_tokens / LW_KV_TILE;
+    const bool mine = tile < last;
+    const int page = mine ? __ldg(table + tile / tpp) : -1;
+    const bool ok = page >= 0 && page < a.n_pages;
+    if (mine && !ok) report(a.status, LW_DEV_BAD_PAGE);
+    there = __ballot_sync(0xFFFFFFFFu, ok);
+    src = a.pages + (int64_t)page * a.page_bytes + head + (tile % tpp) * kTile;
+    at = 0;
+  }
+  __device__ __forceinline__ void begin(const AttnArgs& a, const KvWalk& w, int warp, int lane) {
+    table = a.p.page_table + (int64_t)w.b * a.p.table_stride;
+    head = (int64_t)w.h * (a.page_tokens / LW_KV_TILE) * kTile;
+    next = first = w.span.lo + w.k0 * kFewUnit + 2 * warp;
+    last = w.span.lo + w.k1 * kFewUnit;
+    if (last > w.span.hi) last = w.span.hi;
+    in = out = 0;
+    have = 0;
+    at = 32;
+#pragma unroll
+    for (int i = 0; i < kFewStages; ++i) send(a, lane);
+  }
+  __device__ __forceinline__ void send(const AttnArgs& a, int lane) {
+    if (next >= last) return;
+    if (at == 32) lookup(a, lane);
+    const uint32_t two = there >> at & 3u;
+    if (two) {
+      if (lane == at) mbar_arrive_expect_tx(&bars[in], (uint32_t)__popc(two) * kTile);
+      __syncwarp();
+      if ((lane ^ at) < 2 && (there >> lane & 1u))
+        bulk_g2s(ring + (2 * in + (lane & 1)) * kTile, src, kTile, &bars[in]);
+      have |= two << (2 * in);
+    }
+    at += 2;
+    next += kFewUnit;
+    in = in + 1 == kFewStages ? 0 : in + 1;
+  }
+  // The tiles at `out` have come (false: the wait ran out)
+  __device__ __forceinline__ bool wait() {
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars[out], parity >> out & 1u));
+    parity ^= 1u << out;
+    have &= ~(3u << (2 * out));
+    return ok;
+  }
+};
+
 template <int D, int MODE>
-__global__ void __launch_bounds__(kFewThreads, 1) kv_few_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const AttnArgs a) {
   using F = Few<D, MODE>;
   using L = KvTile<D>;
-  constexpr int RT = F::kRows, G = L::G, W = kFewWarps;
+  constexpr int RT = F::kRows, W = kFewWarps;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
-  uint64_t* empty = full + kFewStages;
-  volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + 128);   // tiles copied, per stage
-  volatile uint32_t* flag = mask + kFewStages;   // [0] a wait ran out, [1] last part of an item
+  volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(smem + F::kRing - 16);   // last part of an item
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kFewStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], W);
-    }
-    flag[0] = 0;
+  FewFetch<D> t;
+  t.bars = reinterpret_cast<uint64_t*>(smem) + warp * kFewStages;
+  t.ring = smem + F::kRing + warp * kFewStages * 2 * L::kBytes;
+  t.parity = t.have = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kFewStages; ++i) mbar_init(&t.bars[i], 1);
     fence_barrier_init();
   }
+  __syncwarp();
   pdl_wait();
   KvWalk w;
-  int G_, q0;
+  int G, q0;
   long long U;
-  if (!kv_range<kFewThreads, RT, W>(a, w, G_, U, q0)) return;   // (its barriers order the set-up above)
-
-  if (warp == W) {   // producer
-    const int tpp = a.page_tokens / LW_KV_TILE;
-    auto entry = [&](const KvWalk& v, int k) {   // this lane's page of unit k
-      const int tile = v.span.lo + k * W + lane;
-      if (lane >= W || tile >= v.span.hi) return -2;
-      return __ldg(a.p.page_table + (int64_t)v.b * a.p.table_stride + tile / tpp);
-    };
-    uint32_t it = 0;
-    bool dead = false;
-    int page = entry(w, w.k0), k = w.k0;
-    KvWalk nx = w;
-    int nq0;
-    for (bool more = true; more;) {
-      const KvWalk cur = nx;
-      const int ck = k, cpage = page;
-      if (++k == nx.k1) {
-        more = kv_advance<RT, W>(a, nx, nq0);
-        k = nx.k0;
-      }
-      if (more) page = entry(nx, k);   // one unit ahead
-      const int s = it % kFewStages;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], (it / kFewStages & 1u) ^ 1u))) {
-        dead = true;
-        break;
-      }
-      const bool use = cpage >= 0 && cpage < a.n_pages;
-      if (!use && cpage != -2) report(a.status, LW_DEV_BAD_PAGE);
-      else if (cpage == -2 && lane < W && cur.span.lo + ck * W + lane < cur.span.hi) report(a.status, LW_DEV_BAD_PAGE);
-      const uint32_t got = __ballot_sync(0xFFFFFFFFu, use);
-      if (lane == 0) {
-        mask[s] = got;
-        mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(got) * L::kBytes);
-      }
-      __syncwarp();
-      if (use) {
-        const int tile = cur.span.lo + ck * W + lane;
-        bulk_g2s(smem + F::kRing + s * F::kStage + lane * L::kBytes,
-                 a.pages + cpage * a.page_bytes + ((int64_t)cur.h * tpp + tile % tpp) * L::kBytes, L::kBytes,
-                 &full[s]);
-      }
-      ++it;
-    }
-    if (dead) {   // no copy may be in flight when the CTA ends
-      flag[0] = 1;
-      report(a.status, LW_DEV_TIMEOUT);
-      for (uint32_t i = it > kFewStages ? it - kFewStages : 0; i < it; ++i)
-        mbar_wait(&full[i % kFewStages], i / kFewStages & 1u);
-    }
-    return;
-  }
+  if (!kv_range<kFewThreads, RT, kFewUnit>(a, w, G, U, q0)) return;
 
   FewWarp<D, MODE> f;
-  uint32_t it = 0;
-  bool dead = false;
+  bool dead = false;   // a wait ran out: reported, and only the barriers are kept up
   float* s_o = reinterpret_cast<float*>(smem + F::kJoin);
   float* s_m = reinterpret_cast<float*>(smem + F::kState);
   float* s_l = s_m + W * 8;
+  float* mine = s_o + warp * 8 * D;
+  t.begin(a, w, warp, lane);
   for (bool more = true; more;) {
     f.start(a, w, q0, RT, lane);
     // keys that every row of the item sees
@@ -564,33 +659,45 @@ __global__ void __launch_bounds__(kFewThreads, 1) kv_few_kernel(const AttnArgs a
       kv_token_keys(w.T, w.n, w.rt * RT / a.group, a.p.causal, a.p.window, x, all_hi);
       kv_token_keys(w.T, w.n, t1, a.p.causal, a.p.window, all_lo, x);
     }
-    float* mine = s_o + (warp * 8 + lane / 4) * F::kPitch + 8 * (lane % 4);
     int held = 0;
-    for (int k = w.k0; k < w.k1; ++k, ++it) {
-      if (MODE == 0 && held == kFewFlush) {
-        f.flush(lane, mine);
-        held = 0;
+    for (int tile = t.first; tile < t.last && !dead; tile += kFewUnit) {
+      const uint32_t two = t.have >> (2 * t.out) & 3u;
+      if (two) {   // else their pages are missing
+        if (!t.wait()) {
+          dead = true;
+          if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
+          mbar_wait(&t.bars[t.out], (t.parity >> t.out & 1u) ^ 1u);
+          break;
+        }
+        if (MODE == 0 && held >= kFewFlush) {
+          f.flush(lane, mine);
+          held = 0;
+        }
+        uint32_t at = smem_addr(t.ring) + 2 * t.out * L::kBytes;
+        int kb = tile * LW_KV_TILE;
+        if (two == 3u && kb >= all_lo && kb + 2 * LW_KV_TILE <= all_hi) {
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i, at += L::kBytes, kb += LW_KV_TILE) f.template tile<false>(at, kb, w.n, lane);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i, at += L::kBytes, kb += LW_KV_TILE)
+            if (two >> i & 1u) f.template tile<true>(at, kb, w.n, lane);
+        }
+        held += 2;
+        __syncwarp();
       }
-      const int s = it % kFewStages;
-      if (!dead && (flag[0] || !__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], it / kFewStages & 1u)))) {
-        dead = true;
-        flag[0] = 1;
-        report(a.status, LW_DEV_TIMEOUT);
-      }
-      dead = __any_sync(0xFFFFFFFFu, dead);
-      if (!dead && (mask[s] >> warp & 1u)) {
-        const uint32_t at = smem_addr(smem + F::kRing) + s * F::kStage + warp * L::kBytes;
-        const int kb = (w.span.lo + k * W + warp) * LW_KV_TILE;
-        if (kb >= all_lo && kb + LW_KV_TILE <= all_hi) f.template tile<false>(at, kb, w.n, lane);
-        else f.template tile<true>(at, kb, w.n, lane);
-        ++held;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
+      t.out = t.out + 1 == kFewStages ? 0 : t.out + 1;
+      t.send(a, lane);
     }
+    // the next item's first tiles, before this one's join
+    const KvWalk v = w;
+    const int vq0 = q0;
+    more = kv_advance<RT, kFewUnit>(a, w, q0);
+    if (more && !dead) t.begin(a, w, warp, lane);
+
     // join the warps, 8 rows at a time
-    const bool whole = w.k0 == 0 && w.k1 == w.units;
-    float* part = a.partials + ((size_t)blockIdx.x * 2 + (w.k0 == 0)) * F::kPartial;
+    const bool whole = v.k0 == 0 && v.k1 == v.units;
+    float* part = a.partials + ((size_t)blockIdx.x * 2 + (v.k0 == 0)) * F::kPartial;
 #pragma unroll
     for (int i = 0; i < FewWarp<D, MODE>::NR; ++i) {
       float l = f.row[i].l;
@@ -600,27 +707,26 @@ __global__ void __launch_bounds__(kFewThreads, 1) kv_few_kernel(const AttnArgs a
         s_m[warp * 8 + lane / 4] = f.row[i].m;
         s_l[warp * 8 + lane / 4] = l;
       }
-#pragma unroll
-      for (int g = 0; g < G; ++g) f.put(i, g, lane, mine);
-      few_bar();
-      for (int j = threadIdx.x; j < 8 * (D / 4); j += 32 * W) {
+      f.put(i, lane, mine);
+      __syncthreads();
+      for (int j = threadIdx.x; j < 8 * (D / 4); j += kFewThreads) {
         const int r = j / (D / 4), d = 4 * (j % (D / 4));
         float m = -INFINITY, sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int v = 0; v < W; ++v) m = fmaxf(m, s_m[v * 8 + r]);
+        for (int u = 0; u < W; ++u) m = fmaxf(m, s_m[u * 8 + r]);
         const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int v = 0; v < W; ++v) {
-          const float e = ex2(s_m[v * 8 + r] - mu);
-          sum = fmaf(s_l[v * 8 + r], e, sum);
-          const float4 z = *reinterpret_cast<const float4*>(s_o + (v * 8 + r) * F::kPitch + d);
+        for (int u = 0; u < W; ++u) {
+          const float e = ex2(s_m[u * 8 + r] - mu);
+          sum = fmaf(s_l[u * 8 + r], e, sum);
+          const float4 z = *reinterpret_cast<const float4*>(s_o + u * 8 * D + few_place<D>(r, d));
           y[0] = fmaf(z.x, e, y[0]);
           y[1] = fmaf(z.y, e, y[1]);
           y[2] = fmaf(z.z, e, y[2]);
           y[3] = fmaf(z.w, e, y[3]);
         }
         if (whole) {
-          few_out<RT>(a, w, q0, 8 * i + r, d, m, sum, y);
+          few_out<RT>(a, v, vq0, 8 * i + r, d, m, sum, y);
         } else {
           if (d == 0) {
             part[8 * i + r] = m;
@@ -629,22 +735,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) kv_few_kernel(const AttnArgs a
           *reinterpret_cast<float4*>(part + 2 * RT + (8 * i + r) * D + d) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
-      few_bar();
+      __syncthreads();
     }
     if (!whole) {
-      const long long x0 = w.x - w.k0;
-      const int c0 = tc_owner(x0, U, G_), parts = tc_owner(x0 + w.units - 1, U, G_) - c0 + 1;
+      const long long x0 = v.x - v.k0;
+      const int c0 = tc_owner(x0, U, G), parts = tc_owner(x0 + v.units - 1, U, G) - c0 + 1;
       __threadfence();
-      few_bar();
+      __syncthreads();
       if (threadIdx.x == 0) {
         const bool last = atomicAdd(a.counters + c0, 1u) == (uint32_t)parts - 1u;
         if (last) a.counters[c0] = 0;
-        flag[1] = last;
+        *flag = last;
       }
-      few_bar();
-      if (flag[1]) {
+      __syncthreads();
+      if (*flag) {
         __threadfence();
-        for (int j = threadIdx.x; j < RT * (D / 4); j += 32 * W) {
+        for (int j = threadIdx.x; j < RT * (D / 4); j += kFewThreads) {
           const int r = j / (D / 4), d = 4 * (j % (D / 4));
           float m = -INFINITY, sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
           const float* p0 = a.partials + ((size_t)c0 * 2 + 1) * F::kPartial;
@@ -662,13 +768,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) kv_few_kernel(const AttnArgs a
             y[2] = fmaf(z.z, e, y[2]);
             y[3] = fmaf(z.w, e, y[3]);
           }
-          few_out<RT>(a, w, q0, r, d, m, sum, y);
+          few_out<RT>(a, v, vq0, r, d, m, sum, y);
         }
       }
-      few_bar();
+      __syncthreads();
     }
-    more = kv_advance<RT, W>(a, w, q0);
   }
+  if (dead)   // no copy may be in flight when the CTA ends
+    for (int i = 0; i < kFewStages; ++i)
+      if (t.have >> (2 * i) & 3u) mbar_wait(&t.bars[i], t.parity >> i & 1u);
 }
 
 }  // namespace dev

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -90,23 +91,8 @@ class LwKvCache(ctypes.Structure):
                 ("page_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-class LwKvRows(ctypes.Structure):
-    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
-                ("reserved", ctypes.c_int32)]
-
-
-class LwKvAttn(ctypes.Structure):
-    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
-                ("q_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
-                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
-                ("lse", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
-                ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
-                ("table_stride", ctypes.c_int64), ("q_tokens", ctypes.c_int64),
-                ("table_width", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32),
-                ("max_q", ctypes.c_int32), ("causal", ctypes.c_int32),
-                ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+_KV_ROWS = struct.Struct("@Pqqii")                    # lw_kv_rows
+_KV_ATTN = struct.Struct("@PqqPqqPPPPqqiiiiiiif")      # lw_kv_attn
 
 
 _lib = None
@@ -743,13 +729,19 @@ def lw_noalloc_scratch_bytes() -> int:
 # the 4-bit key/value cache
 # ----------------------------------------------------------------------------
 
+# These calls run once a layer and step, so their checks are written twice: one
+# expression that a right call passes (a few microseconds), and, where it does
+# not hold, the checks one by one, which say what is wrong.
+
 class KvCache:
     """Pages of the 4-bit key/value cache (the layout of lw_kv_cache in
     include/lw.h) in a caller-owned tensor: any dtype and shape, contiguous,
     a whole number of pages."""
 
     def __init__(self, pages, kv_heads: int, head_dim: int, page_tokens: int):
+        import torch
         fn = "KvCache"
+        _kv_torch(torch)
         self.kv_heads, self.head_dim, self.page_tokens = int(kv_heads), int(head_dim), int(page_tokens)
         size = lw_kv_page_bytes(self.kv_heads, self.head_dim, self.page_tokens)
         if not size:
@@ -760,6 +752,7 @@ class KvCache:
         if have % size:
             _refuse(fn, f"pages: {have} bytes, not a multiple of the page size {size}")
         self.pages, self.device, self.n_pages = pages, pages.device, have // size
+        self.index = pages.get_device()   # -1: not on a CUDA device, which the calls refuse
         self.view = LwKvCache(ptr, self.n_pages, self.kv_heads, self.head_dim, self.page_tokens, 0)
         self.ref = ctypes.byref(self.view)
 
@@ -785,37 +778,49 @@ def lw_kv_workspace_bytes(cache: KvCache, q_heads: int, q_tokens: int, batch: in
     return int(load().lw_kv_workspace_bytes(cache.ref, q_heads, q_tokens, batch))
 
 
-_KV_TYPES = {}
+_KV_TYPES = {}          # torch dtype -> lw_dtype
+_I32 = _I64 = _F32 = None
+_raw_stream = None      # device index -> its current stream's handle
 
 
-def _kv_type(fn: str, name: str, t):
+def _kv_torch(torch):
+    global _I32, _I64, _F32, _raw_stream
+    if _KV_TYPES:
+        return
+    _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _KV_TYPES.update({torch.float32: LW_F32, torch.float16: LW_F16, torch.bfloat16: LW_BF16})
+
+
+def _kv_distinct(t) -> bool:
+    """Whether the rows [tokens][heads][dim] of `t` share no element."""
+    (n, h, d), (st, sh, _) = t.shape, t.stride()
+    if h == 1 or n <= 1:
+        return (n <= 1 or st >= d) and (h == 1 or sh >= d)
+    return (sh >= d and st >= (h - 1) * sh + d) or (st >= d and sh >= (n - 1) * st + d)
+
+
+def _kv_heads(fn: str, name: str, t, tokens, heads, dim, written=False):
+    """Refuse anything but rows of heads [tokens][heads][dim]."""
     import torch
-    if not _KV_TYPES:
-        _KV_TYPES.update({torch.float32: LW_F32, torch.float16: LW_F16, torch.bfloat16: LW_BF16})
     if not isinstance(t, torch.Tensor):
         _refuse(fn, f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    code = _KV_TYPES.get(t.dtype)
-    if code is None:
+    if t.dtype not in _KV_TYPES:
         _refuse(fn, f"{name}: dtype {str(t.dtype).replace('torch.', '')}, expected float32, float16 "
                     "or bfloat16")
-    return code
-
-
-def _kv_heads(fn: str, name: str, t, tokens, heads, dim):
-    """Type code and strides of rows of heads [tokens][heads][dim]."""
-    code = _kv_type(fn, name, t)
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or \
             (tokens is not None and t.shape[0] != tokens):
         want = f"[{'tokens' if tokens is None else tokens}, {heads}, {dim}]"
         _refuse(fn, f"{name}: shape {list(t.shape)}, expected {want}")
-    st, sh, sd = t.stride()
-    if sd != 1 and t.shape[0]:
+    if t.numel() and t.stride(2) != 1:
         _refuse(fn, f"{name}: the last dimension is strided")
-    return code, st, sh
+    if written and not _kv_distinct(t):
+        _refuse(fn, f"{name}: rows that are written overlap")
 
 
 def _kv_index(fn: str, name: str, t, dtype, n):
-    """Address of a contiguous index vector of n entries."""
+    """Refuse anything but a contiguous index vector of n entries."""
     import torch
     if not isinstance(t, torch.Tensor):
         _refuse(fn, f"{name}: expected a torch.Tensor, got {type(t).__name__}")
@@ -824,55 +829,95 @@ def _kv_index(fn: str, name: str, t, dtype, n):
                     f"{str(dtype).replace('torch.', '')}")
     if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
         _refuse(fn, f"{name}: expected a contiguous vector" + ("" if n is None else f" of {n} entries"))
-    return t.data_ptr()
 
 
-def _kv_on(fn: str, cache: KvCache, named):
-    dev = cache.device
-    if dev.type != "cuda":
-        _refuse(fn, f"cache: pages on {dev}, expected a CUDA device")
+def _kv_on(fn: str, cache: KvCache, *named):
+    if cache.index < 0:
+        _refuse(fn, f"cache: pages on {cache.device}, expected a CUDA device")
     for name, t in named:
-        if t.device != dev:
-            _refuse(fn, f"{name}: on {t.device}, the cache is on {dev}")
+        if t.device != cache.device:
+            _refuse(fn, f"{name}: on {t.device}, the cache is on {cache.device}")
 
 
-def _kv_rows(fn: str, cache: KvCache, slots, k, v, d_status, stream, written: bool):
-    import torch
-    sp = _kv_index(fn, "slots", slots, torch.int64, None)
-    n = slots.shape[0]
-    rows = []
+def _kv_rows_refuse(fn, cache, slots, k, v, d_status, written):
+    _kv_index(fn, "slots", slots, _I64, None)
     for name, t in (("k", k), ("v", v)):
-        code, st, sh = _kv_heads(fn, name, t, n, cache.kv_heads, cache.head_dim)
-        if written and n and not _kv_distinct(t):
-            _refuse(fn, f"{name}: rows that are written overlap")
-        rows.append(LwKvRows(t.data_ptr(), st, sh, code, 0))
-    stp = _status_ptr(fn, d_status)
-    _kv_on(fn, cache, (("slots", slots), ("k", k), ("v", v), ("d_status", d_status)))
-    return sp, n, ctypes.byref(rows[0]), ctypes.byref(rows[1]), stp, _stream_ptr(stream), rows
+        _kv_heads(fn, name, t, slots.shape[0], cache.kv_heads, cache.head_dim, written)
+    if k.dtype != v.dtype:
+        _refuse(fn, f"v: dtype {v.dtype}, k has {k.dtype}")
+    _status_ptr(fn, d_status)
+    _kv_on(fn, cache, ("slots", slots), ("k", k), ("v", v), ("d_status", d_status))
 
 
-def _kv_distinct(t) -> bool:
-    """Whether the rows [tokens][heads][dim] of `t` share no element."""
-    (n, h, d), (st, sh, _) = t.shape, t.stride()
-    if h == 1 or n == 1:
-        return (n == 1 or st >= d) and (h == 1 or sh >= d)
-    return (sh >= d and st >= (h - 1) * sh + d) or (st >= d and sh >= (n - 1) * st + d)
+def _kv_rows(fn, cache, slots, k, v, d_status, written):
+    """The checked calls' arguments: slots, count, rows of k and v, status."""
+    dev = cache.index
+    try:
+        n = slots.shape[0]
+        shape = (n, cache.kv_heads, cache.head_dim)
+        code, (kt, kh, kd), (vt, vh, vd) = _KV_TYPES.get(k.dtype), k.stride(), v.stride()
+        ok = (code is not None and v.dtype is k.dtype and k.shape == shape and v.shape == shape
+              and kd == 1 and vd == 1 and slots.dtype is _I64 and slots.dim() == 1
+              and slots.is_contiguous() and d_status.dtype is _I32 and d_status.numel() >= 1
+              and d_status.is_contiguous() and dev >= 0 and k.get_device() == dev
+              and v.get_device() == dev and slots.get_device() == dev and d_status.get_device() == dev
+              and (not written or (_kv_distinct(k) and _kv_distinct(v))))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _kv_rows_refuse(fn, cache, slots, k, v, d_status, written)
+        code, (kt, kh, kd), (vt, vh, vd) = _KV_TYPES[k.dtype], k.stride(), v.stride()
+    return (slots.data_ptr(), n, _KV_ROWS.pack(k.data_ptr(), kt, kh, code, 0),
+            _KV_ROWS.pack(v.data_ptr(), vt, vh, code, 0), d_status.data_ptr())
 
 
 def lw_kv_write(cache: KvCache, k, v, slots, d_status, stream=None) -> None:
     """Quantise k, v [n, kv_heads, head_dim] (one dtype; the last dimension
     contiguous) into the slots int64 [n]; a negative slot is not stored."""
-    fn = "lw_kv_write"
-    sp, n, kr, vr, stp, st, keep = _kv_rows(fn, cache, slots, k, v, d_status, stream, False)
-    _check(load().lw_kv_write(cache.ref, kr, vr, sp, n, stp, st), fn)
+    sp, n, kr, vr, st = _kv_rows("lw_kv_write", cache, slots, k, v, d_status, False)
+    r = _lib.lw_kv_write(cache.ref, kr, vr, sp, n, st,
+                         _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    if r:
+        raise LwError(r, "lw_kv_write")
 
 
 def lw_kv_read(cache: KvCache, slots, k, v, d_status, stream=None) -> None:
     """Read the slots back into k, v [n, kv_heads, head_dim]; a negative slot
     reads as zeros."""
-    fn = "lw_kv_read"
-    sp, n, kr, vr, stp, st, keep = _kv_rows(fn, cache, slots, k, v, d_status, stream, True)
-    _check(load().lw_kv_read(cache.ref, sp, n, kr, vr, stp, st), fn)
+    sp, n, kr, vr, st = _kv_rows("lw_kv_read", cache, slots, k, v, d_status, True)
+    r = _lib.lw_kv_read(cache.ref, sp, n, kr, vr, st,
+                        _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    if r:
+        raise LwError(r, "lw_kv_read")
+
+
+def _kv_attention_refuse(cache, q, q_start, kv_len, page_table, out, ws, d_status, lse):
+    import torch
+    fn = "lw_kv_attention"
+    heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    if isinstance(q, torch.Tensor) and (heads < 1 or heads % cache.kv_heads):
+        _refuse(fn, f"q: shape {list(q.shape)}, expected [tokens, a multiple of {cache.kv_heads}, "
+                    f"{cache.head_dim}]")
+    _kv_heads(fn, "q", q, None, heads, cache.head_dim)
+    _kv_heads(fn, "out", out, q.shape[0], heads, cache.head_dim, True)
+    if out.dtype != q.dtype:
+        _refuse(fn, f"out: dtype {out.dtype}, q has {q.dtype}")
+    _kv_index(fn, "kv_len", kv_len, _I32, None)
+    batch = kv_len.shape[0]
+    _kv_index(fn, "q_start", q_start, _I32, batch + 1)
+    if not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32:
+        _refuse(fn, "page_table: expected an int32 tensor")
+    if page_table.dim() != 2 or page_table.shape[0] != batch or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        _refuse(fn, f"page_table: expected [{batch}, pages] with contiguous rows")
+    named = (("q", q), ("out", out), ("q_start", q_start), ("kv_len", kv_len),
+             ("page_table", page_table), ("ws", ws), ("d_status", d_status))
+    if lse is not None:
+        _buf(fn, "lse", lse, 4 * q.shape[0] * heads, (torch.float32,))
+        named += (("lse", lse),)
+    _ws_ptr(fn, ws)
+    _status_ptr(fn, d_status)
+    _kv_on(fn, cache, *named)
 
 
 def lw_kv_attention(cache: KvCache, q, q_start, kv_len, page_table, out, ws, d_status, *,
@@ -882,39 +927,39 @@ def lw_kv_attention(cache: KvCache, q, q_start, kv_len, page_table, out, ws, d_s
     the cache: sequence b owns tokens q_start[b]..q_start[b+1]-1 and kv_len[b]
     keys in the pages page_table[b]; out as q, lse float32 [tokens, q_heads].
     scale: 1 / sqrt(head_dim) by default."""
-    import torch
-    fn = "lw_kv_attention"
-    code = _kv_type(fn, "q", q)
-    heads = q.shape[1] if q.dim() == 3 else 0
-    if heads < 1 or heads % cache.kv_heads:
-        _refuse(fn, f"q: shape {list(q.shape)}, expected [tokens, a multiple of {cache.kv_heads}, "
-                    f"{cache.head_dim}]")
-    tokens = q.shape[0]
-    _, qt, qh = _kv_heads(fn, "q", q, None, heads, cache.head_dim)
-    ocode, ot, oh = _kv_heads(fn, "out", out, tokens, heads, cache.head_dim)
-    if ocode != code:
-        _refuse(fn, f"out: dtype {out.dtype}, q has {q.dtype}")
-    if tokens and not _kv_distinct(out):
-        _refuse(fn, "out: rows that are written overlap")
-    lens = _kv_index(fn, "kv_len", kv_len, torch.int32, None)
-    batch = kv_len.shape[0]
-    starts = _kv_index(fn, "q_start", q_start, torch.int32, batch + 1)
-    if not isinstance(page_table, torch.Tensor) or page_table.dtype != torch.int32:
-        _refuse(fn, "page_table: expected an int32 tensor")
-    if page_table.dim() != 2 or page_table.shape[0] != batch or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        _refuse(fn, f"page_table: expected [{batch}, pages] with contiguous rows")
-    lsep = None
-    if lse is not None:
-        lsep = _buf(fn, "lse", lse, 4 * tokens * heads, (torch.float32,))
-    wp, wb = _ws_ptr(fn, ws)
-    sp = _status_ptr(fn, d_status)
-    named = (("q", q), ("out", out), ("q_start", q_start), ("kv_len", kv_len),
-             ("page_table", page_table), ("ws", ws), ("d_status", d_status))
-    _kv_on(fn, cache, named if lse is None else named + (("lse", lse),))
-    if scale is None:
-        scale = cache.head_dim ** -0.5
-    a = LwKvAttn(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, lsep, starts, lens,
-                 page_table.data_ptr(), page_table.stride(0), tokens, page_table.shape[1], code,
-                 batch, heads, int(max_q), int(bool(causal)), int(window), float(scale))
-    _check(load().lw_kv_attention(cache.ref, ctypes.byref(a), wp, wb, sp, _stream_ptr(stream)), fn)
+    dev = cache.index
+    try:
+        tokens, heads, dim = shape = q.shape
+        code, (qt, qh, qd), (ot, oh, od) = _KV_TYPES.get(q.dtype), q.stride(), out.stride()
+        batch, width = page_table.shape
+        ts, td = page_table.stride()
+        ok = (code is not None and out.dtype is q.dtype and out.shape == shape
+              and dim == cache.head_dim and heads % cache.kv_heads == 0 and qd == 1 and od == 1
+              and heads > 0 and (out.is_contiguous() or _kv_distinct(out))
+              and q_start.dtype is _I32 and q_start.shape == (batch + 1,) and q_start.is_contiguous()
+              and kv_len.dtype is _I32 and kv_len.shape == (batch,) and kv_len.is_contiguous()
+              and page_table.dtype is _I32 and (td == 1 or width <= 1)
+              and ws.is_contiguous() and d_status.dtype is _I32 and d_status.numel() >= 1
+              and d_status.is_contiguous() and dev >= 0 and q.get_device() == dev
+              and out.get_device() == dev and q_start.get_device() == dev
+              and kv_len.get_device() == dev and page_table.get_device() == dev
+              and ws.get_device() == dev and d_status.get_device() == dev
+              and (lse is None or (lse.dtype is _F32 and lse.is_contiguous()
+                                   and lse.numel() >= tokens * heads and lse.get_device() == dev)))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _kv_attention_refuse(cache, q, q_start, kv_len, page_table, out, ws, d_status, lse)
+        tokens, heads, dim = q.shape
+        code, (qt, qh, qd), (ot, oh, od) = _KV_TYPES[q.dtype], q.stride(), out.stride()
+        batch, width = page_table.shape
+        ts, td = page_table.stride()
+    a = _KV_ATTN.pack(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
+                      0 if lse is None else lse.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                      page_table.data_ptr(), ts, tokens, width, code, batch, heads, max_q,
+                      1 if causal else 0, window, dim ** -0.5 if scale is None else scale)
+    r = _lib.lw_kv_attention(cache.ref, a, ws.data_ptr(), ws.numel() * ws.element_size(),
+                             d_status.data_ptr(),
+                             _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    if r:
+        raise LwError(r, "lw_kv_attention")
