@@ -1,5 +1,6 @@
 // Attention over the 4-bit key/value cache: the launches.
 #include "lw_kvfew.cuh"
+#include "lw_kvmany.cuh"
 #include "lw_kv.h"
 
 namespace lw {
@@ -7,25 +8,27 @@ namespace {
 
 using AttnKernel = void (*)(const AttnArgs);
 
-struct FewVariant {
+struct Variant {
   AttnKernel kernel;
-  int smem, partial;
+  int threads, per_sm, smem;
 };
 template <int D>
-FewVariant few_variant(int mode) {
-  if (mode == 0) return {dev::kv_few_kernel<D, 0>, Few<D, 0>::kSmem, Few<D, 0>::kPartial};
-  if (mode == 1) return {dev::kv_few_kernel<D, 1>, Few<D, 1>::kSmem, Few<D, 1>::kPartial};
-  return {dev::kv_few_kernel<D, 2>, Few<D, 2>::kSmem, Few<D, 2>::kPartial};
+Variant variant(int mode) {
+  if (mode == 0) return {dev::kv_few_kernel<D, 0>, kFewThreads, kFewPerSm, Few<D, 0>::kSmem};
+  if (mode == 1) return {dev::kv_few_kernel<D, 1>, kFewThreads, kFewPerSm, Few<D, 1>::kSmem};
+  if (mode == 2) return {dev::kv_few_kernel<D, 2>, kFewThreads, kFewPerSm, Few<D, 2>::kSmem};
+  return {dev::kv_many_kernel<D>, kManyThreads, kManyPerSm, Many<D>::kSmem};
 }
 
-// The most resident CTAs of a launch, and the workspace places they have.
-inline int attn_ctas() { return kFewPerSm * device_sm_count(); }
+// The most resident CTAs of a launch: the workspace's places.
+inline int attn_ctas() { return 2 * device_sm_count(); }
+static_assert(kFewPerSm <= 2 && kManyPerSm <= 2, "workspace places");
 
 }  // namespace
 
 size_t kv_attention_workspace(const lw_kv_cache* c) {
   const size_t counters = ((size_t)attn_ctas() * 4 + 255) / 256 * 256;
-  return counters + (size_t)attn_ctas() * 2 * 16 * (size_t)(c->head_dim + 2) * 4;
+  return counters + (size_t)attn_ctas() * 2 * kManyRows * (size_t)(c->head_dim + 2) * 4;
 }
 
 lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* ws, int32_t* status,
@@ -44,15 +47,13 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* w
           kv_rows_aligned(p->out, p->out_token_stride, p->out_head_stride, p->dtype);
   a.status = status;
   const long long rows = (long long)p->max_q * a.group;
-  const int mode = p->dtype != LW_BF16 ? 0 : (rows > 8 ? 1 : 2);
-  const FewVariant v = c->head_dim == 64   ? few_variant<64>(mode)
-                       : c->head_dim == 96 ? few_variant<96>(mode)
-                                           : few_variant<128>(mode);
-  if (resident_blocks(reinterpret_cast<const void*>(v.kernel), kFewThreads, v.smem) < 1)
+  const int mode = p->dtype != LW_BF16 ? 0 : (rows > 16 ? 3 : rows > 8 ? 1 : 2);
+  const Variant v = c->head_dim == 64 ? variant<64>(mode) : c->head_dim == 96 ? variant<96>(mode) : variant<128>(mode);
+  if (resident_blocks(reinterpret_cast<const void*>(v.kernel), v.threads, v.smem) < 1)
     return fail(LW_ERR_CUDA, "lw_kv_attention: the kernel does not fit this device");
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)attn_ctas());
-  cfg.blockDim = dim3(kFewThreads);
+  cfg.gridDim = dim3((unsigned)(v.per_sm * device_sm_count()));
+  cfg.blockDim = dim3(v.threads);
   cfg.dynamicSmemBytes = v.smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];

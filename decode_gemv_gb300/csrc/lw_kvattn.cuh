@@ -125,23 +125,37 @@ __device__ __forceinline__ bool kv_advance(const AttnArgs& a, KvWalk& w, int& q0
   return true;
 }
 
-__device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, const float (&f)[4]) {
+// 4 or 8 consecutive elements of an output row, rounded to its type
+template <int N>
+__device__ __forceinline__ void store_n(const AttnArgs& a, int64_t at, const float (&f)[N]) {
   if (a.p.dtype == LW_F32) {
     float* o = static_cast<float*>(a.p.out) + at;
-    if (a.vec) *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
-    else
-      for (int i = 0; i < 4; ++i) o[i] = f[i];
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      if (a.vec) *reinterpret_cast<float4*>(o + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+      else
+        for (int j = 0; j < 4; ++j) o[i + j] = f[i + j];
+    }
   } else {
-    uint16_t h[4];
-    for (int i = 0; i < 4; ++i)
-      h[i] = a.p.dtype == LW_F16 ? __half_as_ushort(__float2half_rn(f[i]))
-                                 : __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
+    uint32_t h[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      h[i] = a.p.dtype == LW_F16
+                 ? __half_as_ushort(__float2half_rn(f[2 * i])) | (uint32_t)__half_as_ushort(__float2half_rn(f[2 * i + 1])) << 16
+                 : __bfloat16_as_ushort(__float2bfloat16_rn(f[2 * i])) |
+                       (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f[2 * i + 1])) << 16;
     uint16_t* o = static_cast<uint16_t*>(a.p.out) + at;
-    if (a.vec) *reinterpret_cast<uint2*>(o) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
-    else
-      for (int i = 0; i < 4; ++i) o[i] = h[i];
+    if (a.vec) {
+      if constexpr (N == 8) *reinterpret_cast<uint4*>(o) = make_uint4(h[0], h[1], h[2], h[3]);
+      else *reinterpret_cast<uint2*>(o) = make_uint2(h[0], h[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = (uint16_t)(h[i / 2] >> (16 * (i % 2)));
+    }
   }
 }
+__device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, const float (&f)[4]) { store_n<4>(a, at, f); }
+__device__ __forceinline__ void store8(const AttnArgs& a, int64_t at, const float (&f)[8]) { store_n<8>(a, at, f); }
 
 }  // namespace dev
 }  // namespace lw

@@ -557,24 +557,26 @@ __device__ __forceinline__ void few_out(const AttnArgs& a, const KvWalk& w, int 
     a.p.lse[(int64_t)(q0 + t) * a.p.q_heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// A warp's pairs of tiles: sent for in order, kFewStages ahead.  The table is
-// read 32 tiles at a time, lane i holding where the i-th lies and sending for it.
-template <int D>
+// A warp's tiles, N (1 or 2) neighbours at a time: sent for in order, STAGES
+// ahead.  The table is read 32 tiles at a time, lane i holding where the i-th
+// lies and sending for it.  UNIT: tiles of a unit (the step to the warp's next).
+template <int D, int UNIT, int N, int STAGES>
 struct FewFetch {
   static constexpr int kTile = KvTile<D>::kBytes;
+  static constexpr uint32_t kAll = (1u << N) - 1;
   uint8_t* ring;
   uint64_t* bars;
   const int32_t* table;    // the sequence's pages
   const uint8_t* src;      // this lane's tile, of the 32
   int64_t head;            // first byte of the head in a page
-  int first, last;         // the item's tiles of this warp: first, first + 1, then kFewUnit on, below last
+  int first, last;         // the item's tiles of this warp: first .. first + N - 1, then UNIT on, below last
   int next, at;            // tile to send for; its place among the 32
   uint32_t there;          // which of the 32 have a page
   int in, out;             // ring places to fill and to use
-  uint32_t have, parity;   // tiles sent for (two bits a place); phase per place
+  uint32_t have, parity;   // tiles sent for (N bits a place); phase per place
 
   __device__ __forceinline__ void lookup(const AttnArgs& a, int lane) {
-    const int tile = next + (lane >> 1) * kFewUnit + (lane & 1), tpp = a.page_tokens / LW_KV_TILE;
+    const int tile = next + lane / N * UNIT + lane % N, tpp = a.page_tokens / LW_KV_TILE;
     const bool mine = tile < last;
     const int page = mine ? __ldg(table + tile / tpp) : -1;
     const bool ok = page >= 0 && page < a.n_pages;
@@ -586,35 +588,35 @@ struct FewFetch {
   __device__ __forceinline__ void begin(const AttnArgs& a, const KvWalk& w, int warp, int lane) {
     table = a.p.page_table + (int64_t)w.b * a.p.table_stride;
     head = (int64_t)w.h * (a.page_tokens / LW_KV_TILE) * kTile;
-    next = first = w.span.lo + w.k0 * kFewUnit + 2 * warp;
-    last = w.span.lo + w.k1 * kFewUnit;
+    next = first = w.span.lo + w.k0 * UNIT + N * warp;
+    last = w.span.lo + w.k1 * UNIT;
     if (last > w.span.hi) last = w.span.hi;
     in = out = 0;
     have = 0;
     at = 32;
 #pragma unroll
-    for (int i = 0; i < kFewStages; ++i) send(a, lane);
+    for (int i = 0; i < STAGES; ++i) send(a, lane);
   }
   __device__ __forceinline__ void send(const AttnArgs& a, int lane) {
     if (next >= last) return;
     if (at == 32) lookup(a, lane);
-    const uint32_t two = there >> at & 3u;
-    if (two) {
-      if (lane == at) mbar_arrive_expect_tx(&bars[in], (uint32_t)__popc(two) * kTile);
+    const uint32_t some = there >> at & kAll;
+    if (some) {
+      if (lane == at) mbar_arrive_expect_tx(&bars[in], (uint32_t)__popc(some) * kTile);
       __syncwarp();
-      if ((lane ^ at) < 2 && (there >> lane & 1u))
-        bulk_g2s(ring + (2 * in + (lane & 1)) * kTile, src, kTile, &bars[in]);
-      have |= two << (2 * in);
+      if ((lane ^ at) < N && (there >> lane & 1u))
+        bulk_g2s(ring + (N * in + lane % N) * kTile, src, kTile, &bars[in]);
+      have |= some << (N * in);
     }
-    at += 2;
-    next += kFewUnit;
-    in = in + 1 == kFewStages ? 0 : in + 1;
+    at += N;
+    next += UNIT;
+    in = in + 1 == STAGES ? 0 : in + 1;
   }
   // The tiles at `out` have come (false: the wait ran out)
   __device__ __forceinline__ bool wait() {
     const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars[out], parity >> out & 1u));
     parity ^= 1u << out;
-    have &= ~(3u << (2 * out));
+    have &= ~(kAll << (N * out));
     return ok;
   }
 };
@@ -627,7 +629,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
   extern __shared__ __align__(128) uint8_t smem[];
   volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(smem + F::kRing - 16);   // last part of an item
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  FewFetch<D> t;
+  FewFetch<D, kFewUnit, 2, kFewStages> t;
   t.bars = reinterpret_cast<uint64_t*>(smem) + warp * kFewStages;
   t.ring = smem + F::kRing + warp * kFewStages * 2 * L::kBytes;
   t.parity = t.have = 0;

@@ -796,8 +796,10 @@ def _kv_torch(torch):
 def _kv_distinct(t) -> bool:
     """Whether the rows [tokens][heads][dim] of `t` share no element."""
     (n, h, d), (st, sh, _) = t.shape, t.stride()
-    if h == 1 or n <= 1:
-        return (n <= 1 or st >= d) and (h == 1 or sh >= d)
+    if n == 0:
+        return True
+    if h == 1 or n == 1:
+        return (n == 1 or st >= d) and (h == 1 or sh >= d)
     return (sh >= d and st >= (h - 1) * sh + d) or (st >= d and sh >= (n - 1) * st + d)
 
 
