@@ -20,15 +20,17 @@ Variant variant(int mode) {
   return {dev::kv_many_kernel<D>, kManyThreads, kManyPerSm, Many<D>::kSmem};
 }
 
-// The most resident CTAs of a launch: the workspace's places.
-inline int attn_ctas() { return 2 * device_sm_count(); }
-static_assert(kFewPerSm <= 2 && kManyPerSm <= 2, "workspace places");
+// The workspace: counters and partial results of the most resident CTAs of a
+// launch (counts of either kernel: a counter, and two parts of an item, a CTA;
+// twice that for the two row tiles of kv_many_kernel).
+inline size_t attn_counter_bytes() { return ((size_t)2 * device_sm_count() * 4 + 255) / 256 * 256; }
+static_assert(kFewPerSm <= 2 && kManyPerSm == 1, "workspace places");
 
 }  // namespace
 
 size_t kv_attention_workspace(const lw_kv_cache* c) {
-  const size_t counters = ((size_t)attn_ctas() * 4 + 255) / 256 * 256;
-  return counters + (size_t)attn_ctas() * 2 * kManyRows * (size_t)(c->head_dim + 2) * 4;
+  const size_t few = (size_t)kFewPerSm * 2 * 16, many = (size_t)2 * 2 * kManyTile;   // rows an SM
+  return attn_counter_bytes() + (size_t)device_sm_count() * (few > many ? few : many) * (size_t)(c->head_dim + 2) * 4;
 }
 
 lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* ws, int32_t* status,
@@ -39,7 +41,7 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* w
   a.n_pages = c->n_pages;
   a.page_bytes = (int64_t)lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens);
   a.counters = static_cast<uint32_t*>(ws);
-  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)attn_ctas() * 4 + 255) / 256 * 256);
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attn_counter_bytes());
   a.page_tokens = c->page_tokens;
   a.heads = c->kv_heads;
   a.group = p->q_heads / c->kv_heads;

@@ -103,6 +103,13 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
   return *reinterpret_cast<float2*>(&d);
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -128,7 +135,7 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
     w[0] = u.x; w[1] = u.y;
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = lds_u32(at + 4 * i);
+    for (int i = 0; i < N; ++i) w[i] = lds_u32(at + 4 * i);   // 3 words, or one
   }
 }
 __device__ __forceinline__ uint32_t max_h2(uint32_t x, uint32_t y) {

@@ -1,22 +1,22 @@
 // Cache attention for many rows: chunks of prompts, on the 5th-generation
 // tensor cores.
 //
-// An item is 128 rows (token, head) of one key/value head; keys come 64 at a
-// time.  S = Q K^T and O += P V are tcgen05.mma with the first operand (Q, P)
-// and the accumulators in tensor memory, the second (K, V, restored to fp16
-// from their codes) in shared memory:
+// An item is up to 256 rows (token, head) of one key/value head, two tiles of
+// 128; keys come 64 at a time.  S = Q K^T and O += P V are tcgen05.mma: Q, K
+// and V (fp16, restored from the codes) are operand tiles in shared memory, P
+// and the accumulators lie in tensor memory.
 //  * 4 loader warps, one per 16-key tile of the 64: fetch their tile by bulk
 //    copies (a ring of their own), restore k = sc c + mn and v = sc c + mn by
-//    one rounded fp16 fma each, and store them as operand tiles (two buffers);
-//  * 4 row warps, one thread per row: put the row of Q into tensor memory
-//    (scaled by a power of two: the fp16 range), then for every 64 keys read
-//    the row of S, take p = 2^(s - m), store it as fp16 over S, and add the
-//    row's sum.  m is raised, and O rescaled, only where a score passes it by
-//    2^8 (p stays below 2^8, in fp16 range and precision).  One of their
-//    threads issues the products (a ninth warp would take the registers of
-//    three).
-// Two CTAs share an SM: one's products run while the other's rows are at
-// work.  Operands of 11 bits (fp16) under outputs of 8 (bf16).
+//    one rounded fp16 fma each, and store them as operand tiles (two buffers),
+//    once for both row tiles;
+//  * 8 row warps, one thread per row: put Q into shared memory (each row scaled
+//    by a power of two: the fp16 range), then for every 64 keys read the row of
+//    S, take p = 2^(s - m), store it as fp16 over S, and add the row's sum.  m
+//    is raised, and O rescaled, only where a score passes it by 2^8 (p stays
+//    below 2^8, in fp16 range and precision);
+//  * one thread issues the products.  S has two buffers a tile: the next S is
+//    computed while the rows work on this one.
+// Operands of 11 bits (fp16) under outputs of 8 (bf16).
 //
 // The operand tiles are K-major core matrices of 8 x 16 bytes.  A key code
 // word holds 8 elements of one key: its fp16 pairs are elements (0,4), (1,5),
@@ -31,28 +31,30 @@
 
 namespace lw {
 
-constexpr int kManyRows = 128, kManyKeys = 64;
+constexpr int kManyTile = 128, kManyRows = 2 * kManyTile, kManyKeys = 64;
 constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit = loader warps
-constexpr int kManyThreads = 32 * 8;                // 4 row warps, 4 loader warps
-constexpr int kManyPerSm = 2;
+constexpr int kManyThreads = 32 * 13;               // 8 row warps, 4 loader warps, 1 to issue
+constexpr int kManyPerSm = 1;
 constexpr int kManyStages = 4;                      // tiles of a loader's ring
 
 template <int D>
 struct Many {
   using L = KvTile<D>;
-  static constexpr int kKLbo = kManyKeys * 16 + 32;   // bytes between 8-element columns (32: bank offset)
+  static constexpr int kQLbo = kManyTile * 16 + 16;   // bytes between 8-element columns (16, 32: bank offset)
+  static constexpr int kQBytes = D / 8 * kQLbo;
+  static constexpr int kKLbo = kManyKeys * 16 + 32;
   static constexpr int kKBytes = D / 8 * kKLbo;
   static constexpr int kVLbo = D * 16;                // bytes between 8-key columns
   static constexpr int kVBytes = kManyKeys / 8 * kVLbo;
   static constexpr int kHead = 1024;                  // barriers and flags
-  static constexpr int kK = kHead, kV = kK + 2 * kKBytes;
+  static constexpr int kQ = kHead, kK = kQ + 2 * kQBytes, kV = kK + 2 * kKBytes;
   static constexpr int kRing = kV + 2 * kVBytes;
   static constexpr int kSmem = kRing + kManyUnit * kManyStages * L::kBytes;
-  static constexpr int kPartial = kManyRows * (D + 2);   // floats: m, l, then [D / 4][rows][4]
-  // tensor-memory columns: S (and P over it), O, Q
-  static constexpr uint32_t kS = 0, kO = kManyKeys, kQ = kO + D;
-  static constexpr uint32_t kCols = 256;
-  static_assert(kQ + D / 2 <= kCols, "tensor memory");
+  static constexpr int kPartial = kManyTile * (D + 2);   // of a tile, floats: m, l, then [D / 4][rows][4]
+  // tensor-memory columns: S of tile x, buffer i (and P over it); O of tile x
+  __host__ __device__ static constexpr uint32_t s_col(int x, int i) { return 128 * x + 64 * i; }
+  __host__ __device__ static constexpr uint32_t o_col(int x) { return 256 + D * x; }
+  static constexpr uint32_t kCols = 512;
 };
 
 namespace dev {
@@ -100,31 +102,92 @@ __device__ __forceinline__ uint32_t whole_odd(uint32_t w) {   // 1024 + 16 c
 
 // A wait that gives up when another role has
 __device__ __forceinline__ bool many_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+  const auto passed = [&] {   // sleeps up to 2 us in the barrier
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(2000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (passed()) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (passed()) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > kWaitCycles) return false;
   }
 }
 
-// The row warps' barrier: whether `ok` holds in all of them
-__device__ __forceinline__ bool rows_agree(bool ok) {
+// The barrier of a tile's row warps: whether `ok` holds in all of them
+__device__ __forceinline__ bool rows_agree(int tile, bool ok) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)ok)
+      : "r"((uint32_t)ok), "r"(1 + tile)
       : "memory");
   return r != 0;
 }
 
-// Barriers of a CTA
+// 32 rows of Q (a warp's; row r of them in tile row 32 quarter + r) into the
+// operand tile, each scaled by 2^-e and given the sign of `scale` (so that the
+// largest product is the largest score); returns 2^e of row `lane`.  Row r
+// starts at element row_at of lane r, or is 0 (row_at < 0).
+template <int D, bool VEC>
+__device__ __forceinline__ float many_query(const __nv_bfloat16* q, int64_t row_at, float scale, uint32_t to,
+                                            int quarter, int lane) {
+  using F = Many<D>;
+  const uint32_t sign = __float_as_uint(scale) & 0x80000000u;
+  float mine = 1.f;
+  to += (uint32_t)((lane / 2) * F::kQLbo + (lane & 1) * 8 + quarter * 4 * 128);
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 16) {
+    uint2 w[16];   // this lane's elements 4 lane .. 4 lane + 3
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t at = __shfl_sync(0xFFFFFFFFu, row_at, r0 + i);
+      w[i] = make_uint2(0u, 0u);
+      if (at >= 0 && lane < D / 4) {
+        const __nv_bfloat16* p = q + at + 4 * lane;
+        if constexpr (VEC) w[i] = *reinterpret_cast<const uint2*>(p);
+        else
+          w[i] = make_uint2(__bfloat16_as_ushort(p[0]) | (uint32_t)__bfloat16_as_ushort(p[1]) << 16,
+                            __bfloat16_as_ushort(p[2]) | (uint32_t)__bfloat16_as_ushort(p[3]) << 16);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      // magnitudes are in order as integers (a NaN comes last, and stays NaN below)
+      const uint32_t a = max(max(w[i].x << 16 & 0x7FFF0000u, w[i].x & 0x7FFF0000u),
+                             max(w[i].y << 16 & 0x7FFF0000u, w[i].y & 0x7FFF0000u));
+      int e = (int)(__reduce_max_sync(0xFFFFFFFFu, a) >> 23) - 127;
+      e = e < -100 ? -100 : (e > 126 ? 126 : e);
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23 | sign);
+      if (lane == r0 + i) mine = __uint_as_float((uint32_t)(127 + e) << 23);
+      const uint32_t h0 = h2bits(__floats2half2_rn(__uint_as_float(w[i].x << 16) * down, __uint_as_float(w[i].x & 0xFFFF0000u) * down));
+      const uint32_t h1 = h2bits(__floats2half2_rn(__uint_as_float(w[i].y << 16) * down, __uint_as_float(w[i].y & 0xFFFF0000u) * down));
+      // an even lane has elements 0..3 of the eight and stores (0,4), (1,5); an odd one 4..7, (2,6), (3,7)
+      const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? h0 : h1, 1);
+      const uint32_t low = lane & 1 ? other : h0, high = lane & 1 ? h1 : other;
+      const int r = r0 + i;
+      if (lane < D / 4)
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + (uint32_t)((r / 8) * 128 + (r % 8) * 16)),
+                     "r"(__byte_perm(low, high, 0x5410)), "r"(__byte_perm(low, high, 0x7632))
+                     : "memory");
+    }
+  }
+  return mine;
+}
+
+// Barriers of a CTA.  Those of a row tile are one per S buffer, so that the use
+// before the one waited for is always complete (a parity names one of two).
 struct ManyBars {
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // per operand buffer
-  uint64_t s_full, o_full;                               // a product is complete
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];   // per row tile (and S buffer)
   uint64_t last;                                         // everything issued has completed
   uint64_t ring[kManyUnit][kManyStages];
 };
@@ -137,8 +200,8 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   extern __shared__ __align__(128) uint8_t smem[];
   ManyBars& bar = *reinterpret_cast<ManyBars*>(smem);
   static_assert(sizeof(ManyBars) <= 512, "barriers");
-  volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + 512);   // [0] abort, [1] last part,
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + 528);                     // tensor memory
+  volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + 512);   // [0] abort, [1], [2] last part of a tile's item
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + 528);   // tensor memory
   // [unit % 4][tile]: the tile's keys are there (written before k_full, read
   // after s_full; four units on, the rows have long answered)
   volatile uint8_t* present = smem + 544;
@@ -150,15 +213,22 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       mbar_init(&bar.k_free[i], 1);
       mbar_init(&bar.v_free[i], 1);
     }
-    mbar_init(&bar.s_full, 1);
-    mbar_init(&bar.o_full, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bar.q_full[x], 4);
+      mbar_init(&bar.s_full[x][0], 1);
+      mbar_init(&bar.s_full[x][1], 1);
+      mbar_init(&bar.p_full[x][0], 4);
+      mbar_init(&bar.p_full[x][1], 4);
+      mbar_init(&bar.o_done[x][0], 1);
+      mbar_init(&bar.o_done[x][1], 1);
+    }
     mbar_init(&bar.last, 1);
     for (int i = 0; i < kManyUnit; ++i)
       for (int j = 0; j < kManyStages; ++j) mbar_init(&bar.ring[i][j], 1);
     flags[0] = 0;
     fence_barrier_init();
   }
-  if (warp == 0) {
+  if (warp == 12) {
     tmem_alloc(smem_addr(tslot), F::kCols);
     tmem_relinquish();
   }
@@ -173,8 +243,8 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   const bool any = kv_range<kManyThreads, kManyRows, kManyUnit>(a, w, Gc, U, q0);
   bool ok = true;   // no wait ran out
 
-  if (any && warp >= 4 && warp < 8) {   // ---- loaders
-    const int lw = warp - 4;
+  if (any && warp >= 8 && warp < 12) {   // ---- loaders
+    const int lw = warp - 8;
     FewFetch<D, kManyUnit, 1, kManyStages> t;
     t.bars = bar.ring[lw];
     t.ring = smem + F::kRing + lw * kManyStages * L::kBytes;
@@ -204,24 +274,25 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
 #pragma unroll
           for (int h = 0; h < 2; ++h) {   // key 8 h + lane / 4, elements 32 g + 8 q + 0..7
             const int tk = 8 * h + lane / 4;
-            uint32_t cw[G], sw[G];
+            uint32_t cw[G], sw[G], mw[L::GP / 2];
             lds_words<G>(s + L::kKeyCodes + (uint32_t)((tk * 4 + q) * G) * 4, cw);
             lds_words<G>(s + L::kKeyScale + (uint32_t)(tk / 2 * G) * 4, sw);
-            bool nan = false;
+            lds_words<L::GP / 2>(s + L::kKeyMin + (uint32_t)(tk * L::GP) * 2, mw);
             if (edge) {   // rows that do not see a key must not get its NaN through V (0 x NaN): let it come by S
+              bool nan = false;
 #pragma unroll
               for (int g = 0; g < G; ++g) {
                 const uint32_t z = lds_u16(s + L::kValScale + (uint32_t)((tk / 2 * G + g) * 2 + tk % 2) * 2);
                 nan |= (z & 0x7FFFu) > 0x7C00u;
               }
+              if (nan) sw[0] = 0x7FFF7FFFu;
             }
             const uint32_t to = smem_addr(smem) + F::kK + buf * F::kKBytes + (uint32_t)((lw * 2 + h) * 128 + (lane / 4) * 16);
+            const uint32_t half = lane & 4 ? 0x3232u : 0x1010u;   // key 2 j or 2 j + 1
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              uint32_t sc = tk & 1 ? pair_hi(sw[g]) : pair_lo(sw[g]);
-              const uint32_t m1 = lds_u16(s + L::kKeyMin + (uint32_t)(tk * L::GP + g) * 2);
-              const uint32_t mn = pair_lo(m1);
-              if (nan) sc = 0x7FFF7FFFu;
+              const uint32_t sc = __byte_perm(sw[g], 0, half);
+              const uint32_t mn = __byte_perm(mw[g / 2], 0, g % 2 ? 0x3232u : 0x1010u);
               const uint32_t w0 = cw[g], w1 = cw[g] >> 8;
               sts_u4(to + (uint32_t)((4 * g + q) * F::kKLbo), fma_h2(whole_even(w0), sc, mn),
                      fma_h2(whole_odd(w0), sc, mn), fma_h2(whole_even(w1), sc, mn), fma_h2(whole_odd(w1), sc, mn));
@@ -234,38 +305,56 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         if (lane == 0) mbar_arrive(&bar.k_full[buf]);
         if (!__all_sync(0xFFFFFFFFu, many_wait(&bar.v_free[buf], par, flags))) { ok = false; break; }
         {
-          const int n = lane & 7, gh = lane >> 3 & 1, h = lane >> 4;   // 8 keys 8 h.., groups gh, gh + 2
+          constexpr int GW = (G + 1) / 2;   // groups of a lane: GW gh ..
+          const int n = lane & 7, gh = lane >> 3 & 1, h = lane >> 4;   // keys 8 h .. 8 h + 7
+          const int g0 = GW * gh;
           const uint32_t to = smem_addr(smem) + F::kV + buf * F::kVBytes + (uint32_t)((lw * 2 + h) * F::kVLbo + n * 16);
+          uint32_t cw[4][GW], sc[4][GW], mn[4][GW];
 #pragma unroll
-          for (int gg = 0; gg < (G + 1) / 2; ++gg) {
-            const int g = 2 * gg + gh;
-            if (g >= G) continue;
-            uint32_t e[4], o[4], e2[4], o2[4];
+          for (int j = 0; j < 4; ++j) {
+            const int p = 4 * h + j;   // pair of keys
+            if (there && G % 2 == 0) {
+              lds_words<GW>(s + L::kValCodes + (uint32_t)((p * 8 + n) * G + g0) * 4, cw[j]);
+              lds_words<GW>(s + L::kValScale + (uint32_t)(p * G + g0) * 4, sc[j]);
+              lds_words<GW>(s + L::kValMin + (uint32_t)(p * G + g0) * 4, mn[j]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int p = 4 * h + j;   // pair of keys
-              uint32_t cw = 0, sc = 0, mn = 0;
-              if (there) {
-                cw = lds_u32(s + L::kValCodes + (uint32_t)((p * 8 + n) * G + g) * 4);
-                sc = lds_u32(s + L::kValScale + (uint32_t)(p * G + g) * 4);
-                mn = lds_u32(s + L::kValMin + (uint32_t)(p * G + g) * 4);
-                if (edge) {
-                  const int key = kb + 2 * p;
-                  const uint32_t keep = (key < w.n && (sc & 0x7FFFu) <= 0x7C00u ? 0xFFFFu : 0u) |
-                                        (key + 1 < w.n && (sc & 0x7FFF0000u) <= 0x7C000000u ? 0xFFFF0000u : 0u);
-                  sc &= keep;
-                  mn &= keep;
+              for (int i = 0; i < GW; ++i) {
+                cw[j][i] = sc[j][i] = mn[j][i] = 0;
+                if (there && g0 + i < G) {
+                  cw[j][i] = lds_u32(s + L::kValCodes + (uint32_t)((p * 8 + n) * G + g0 + i) * 4);
+                  sc[j][i] = lds_u32(s + L::kValScale + (uint32_t)(p * G + g0 + i) * 4);
+                  mn[j][i] = lds_u32(s + L::kValMin + (uint32_t)(p * G + g0 + i) * 4);
                 }
               }
-              e[j] = fma_h2(whole_even(cw), sc, mn);
-              o[j] = fma_h2(whole_odd(cw), sc, mn);
-              e2[j] = fma_h2(whole_even(cw >> 8), sc, mn);
-              o2[j] = fma_h2(whole_odd(cw >> 8), sc, mn);
             }
-            sts_u4(to + (4 * g + 0) * 128, e[0], e[1], e[2], e[3]);
-            sts_u4(to + (4 * g + 1) * 128, o[0], o[1], o[2], o[3]);
-            sts_u4(to + (4 * g + 2) * 128, e2[0], e2[1], e2[2], e2[3]);
-            sts_u4(to + (4 * g + 3) * 128, o2[0], o2[1], o2[2], o2[3]);
+            if (edge) {
+              const int key = kb + 2 * p;
+#pragma unroll
+              for (int i = 0; i < GW; ++i) {
+                const uint32_t z = sc[j][i];
+                const uint32_t keep = (key < w.n && (z & 0x7FFFu) <= 0x7C00u ? 0xFFFFu : 0u) |
+                                      (key + 1 < w.n && (z & 0x7FFF0000u) <= 0x7C000000u ? 0xFFFF0000u : 0u);
+                sc[j][i] &= keep;
+                mn[j][i] &= keep;
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < GW; ++i) {
+            if (G % 2 && g0 + i >= G) continue;
+            const uint32_t row = to + (uint32_t)(4 * (g0 + i)) * 128;
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              uint32_t e[4], o[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                e[j] = fma_h2(whole_even(cw[j][i] >> (8 * st)), sc[j][i], mn[j][i]);
+                o[j] = fma_h2(whole_odd(cw[j][i] >> (8 * st)), sc[j][i], mn[j][i]);
+              }
+              sts_u4(row + (2 * st) * 128, e[0], e[1], e[2], e[3]);
+              sts_u4(row + (2 * st + 1) * 128, o[0], o[1], o[2], o[3]);
+            }
           }
         }
         fence_proxy_async();
@@ -284,163 +373,199 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       for (int i = 0; i < kManyStages; ++i)   // no copy may be in flight when the CTA ends
         if (t.have >> i & 1u) mbar_wait(&t.bars[i], t.parity >> i & 1u);
     }
-  } else if (any && warp < 4) {   // ---- rows
-    const uint32_t mine = tmem + ((uint32_t)(32 * warp) << 16);   // this warp's quarter
-    const int row = threadIdx.x;
-    const uint32_t kbase = smem_addr(smem) + F::kK, vbase = smem_addr(smem) + F::kV;
-    // the issuing thread's: S of unit u, once its keys are there; O of unit u
-    const auto issue_s = [&](uint32_t u) {
-      const uint32_t at = kbase + (u & 1) * F::kKBytes;
-      if (!many_wait(&bar.k_full[u & 1], u >> 1 & 1u, flags)) return false;
-      tc_fence_after();
+  } else if (any && warp == 12) {   // ---- issuer
+    if (lane == 0) {
+      const uint32_t base = smem_addr(smem);
+      uint32_t it = 0, items[2] = {0, 0}, done[2] = {0, 0};   // units; per tile: items, units before this item
+      // S of tile x from the keys of unit `u` (its c-th unit); O += P V
+      const auto issue_s = [&](int x, uint32_t u, uint32_t c) {
+        const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
+        const uint64_t kd = sdesc(base + F::kK + (u & 1) * F::kKBytes, F::kKLbo, 128);
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        umma_bf16_ta(tmem + F::kS, tmem + F::kQ + 8 * s, sdesc(at + 2 * s * F::kKLbo, F::kKLbo, 128),
-                     idesc_f16(kManyKeys), s > 0);
-      umma_commit(&bar.s_full);
-      umma_commit(&bar.k_free[u & 1]);
-      return true;
-    };
-    const auto issue_o = [&](uint32_t u, bool first) {
-      const uint32_t at = vbase + (u & 1) * F::kVBytes;
-      if (!many_wait(&bar.v_full[u & 1], u >> 1 & 1u, flags)) return false;
-      tc_fence_after();
+        for (int s = 0; s < D / 16; ++s)
+          umma_bf16(tmem + F::s_col(x, c & 1), qd + (2 * s * F::kQLbo >> 4), kd + (2 * s * F::kKLbo >> 4),
+                    idesc_f16(kManyKeys), s > 0);
+        umma_commit(&bar.s_full[x][c & 1]);
+      };
+      const auto issue_o = [&](int x, uint32_t u, uint32_t c, bool first) {
+        const uint64_t vd = sdesc(base + F::kV + (u & 1) * F::kVBytes, F::kVLbo, 128);
 #pragma unroll
-      for (int s = 0; s < kManyKeys / 16; ++s)
-        umma_bf16_ta(tmem + F::kO, tmem + F::kS + 8 * s, sdesc(at + 2 * s * F::kVLbo, F::kVLbo, 128),
-                     idesc_f16(D), !first || s > 0);
-      umma_commit(&bar.o_full);
-      umma_commit(&bar.v_free[u & 1]);
-      return true;
-    };
-    uint32_t it = 0;
-    bool stop = false;   // rows_agree said no
-    for (bool more = true; more && ok;) {
-      const int r = w.rt * kManyRows + row;
-      const bool live = r < w.T * a.group;
-      const int tok = live ? r / a.group : w.T - 1, hq = w.h * a.group + (live ? r - tok * a.group : 0);
-      int lo, hi, all_lo, all_hi, x;
-      kv_token_keys(w.T, w.n, tok, a.p.causal, a.p.window, lo, hi);
-      {
-        int t1 = (w.rt * kManyRows + kManyRows - 1) / a.group;
-        if (t1 > w.T - 1) t1 = w.T - 1;
-        kv_token_keys(w.T, w.n, w.rt * kManyRows / a.group, a.p.causal, a.p.window, x, all_hi);
-        kv_token_keys(w.T, w.n, t1, a.p.causal, a.p.window, all_lo, x);
-      }
-      // the row of Q, scaled by 2^-e
-      float f;
-      {
-        const int64_t at = (int64_t)(q0 + tok) * a.p.q_token_stride + (int64_t)hq * a.p.q_head_stride;
-        float top = 0.f, y[8];
-        for (int o = 0; o < D / 8; ++o) {
-          load_q8(a, at + 8 * o, y);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
-        }
-        int e = (int)(__float_as_uint(top) >> 23) - 127;
-        e = e < -100 ? -100 : (e > 126 ? 126 : e);
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        f = a.p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll 1
-        for (int o = 0; o < D / 16; ++o) {
-          uint32_t z[8];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            load_q8(a, at + 16 * o + 8 * j, y);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[4 * j + i] = h2bits(__floats2half2_rn(y[i] * down, y[i + 4] * down));
+        for (int s = 0; s < kManyKeys / 16; ++s)
+          umma_bf16_ta(tmem + F::o_col(x), tmem + F::s_col(x, c & 1) + 8 * s, vd + (2 * s * F::kVLbo >> 4),
+                       idesc_f16(D), !first || s > 0);
+        umma_commit(&bar.o_done[x][c & 1]);
+      };
+      for (bool more = true; more && ok;) {
+        const int tiles = (w.T * a.group - w.rt * kManyRows) > kManyTile ? 2 : 1;
+        const int n = w.k1 - w.k0;
+        // S of the i-th unit lies where P of the (i - 2)-th was
+        const auto next_s = [&](int i) {
+          if (!many_wait(&bar.k_full[(it + i) & 1], (it + i) >> 1 & 1u, flags)) return false;
+          for (int x = 0; x < tiles; ++x) {
+            const uint32_t c = done[x] + i;
+            if (i == 0 && !many_wait(&bar.q_full[x], items[x] & 1u, flags)) return false;
+            if (c >= 2 && !many_wait(&bar.o_done[x][c & 1], (c - 2) >> 1 & 1u, flags)) return false;
+            tc_fence_after();
+            issue_s(x, it + i, c);
           }
-          tmem_st8(mine + F::kQ + 8 * o, z);
+          umma_commit(&bar.k_free[(it + i) & 1]);
+          return true;
+        };
+        ok = next_s(0);
+        for (int i = 0; ok && i < n; ++i) {
+          if (i + 1 < n && !next_s(i + 1)) { ok = false; break; }
+          if (!many_wait(&bar.v_full[(it + i) & 1], (it + i) >> 1 & 1u, flags)) { ok = false; break; }
+          for (int x = 0; x < tiles; ++x) {
+            const uint32_t c = done[x] + i;
+            if (!many_wait(&bar.p_full[x][c & 1], c >> 1 & 1u, flags)) { ok = false; break; }
+            tc_fence_after();
+            issue_o(x, it + i, c, i == 0);
+          }
+          umma_commit(&bar.v_free[(it + i) & 1]);
         }
-        tmem_st_wait();
-        tc_fence_before();
+        it += n;
+        for (int x = 0; x < tiles; ++x) {
+          done[x] += n;
+          ++items[x];
+        }
+        if (ok) more = kv_advance<kManyRows, kManyUnit>(a, w, q0);
       }
-      ok = rows_agree(ok);   // (every Q row is in place; all four warps go on, or none)
-      if (!ok) break;
-      if (row == 0) ok = issue_s(it);
+      if (!ok) {
+        flags[0] = 1;
+        report(a.status, LW_DEV_TIMEOUT);
+      }
+      umma_commit(&bar.last);   // no product may be in flight when the tensor memory goes
+      mbar_wait(&bar.last, 0);
+    }
+  } else if (any && warp < 8) {   // ---- rows
+    const int x = warp / 4, row = threadIdx.x % kManyTile;   // tile, its row
+    const uint32_t mine = tmem + ((uint32_t)(32 * (warp % 4)) << 16);   // this warp's quarter
+    uint32_t it = 0, c = 0;   // units of the CTA; of this tile
+    struct Row { int tok, hq, lo, hi; bool live; };
+    const auto find = [&](const KvWalk& v) {
+      const int r = v.rt * kManyRows + x * kManyTile + row;
+      Row y;
+      y.live = r < v.T * a.group;
+      y.tok = y.live ? r / a.group : v.T - 1;
+      y.hq = v.h * a.group + (y.live ? r - y.tok * a.group : 0);
+      kv_token_keys(v.T, v.n, y.tok, a.p.causal, a.p.window, y.lo, y.hi);
+      return y;
+    };
+    const auto tile_there = [&](const KvWalk& v) { return v.rt * kManyRows + x * kManyTile < v.T * a.group; };
+    float f = 0.f;   // log2 units per unit of S
+    const auto load_q = [&](const Row& y, int s0) {
+      const int64_t at = y.live ? (int64_t)(s0 + y.tok) * a.p.q_token_stride + (int64_t)y.hq * a.p.q_head_stride : -1;
+      const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.p.q);
+      const uint32_t to = smem_addr(smem) + F::kQ + x * F::kQBytes;
+      const float e2 = a.vec ? many_query<D, true>(qp, at, a.p.scale, to, warp % 4, lane)
+                             : many_query<D, false>(qp, at, a.p.scale, to, warp % 4, lane);
+      // (never 0: a masked score times it stays -inf)
+      f = fmaxf(fabsf(a.p.scale) * 1.4426950408889634f * e2, 1e-37f);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.q_full[x]);
+    };
+    Row y = find(w);
+    if (tile_there(w)) load_q(y, q0);
+    for (bool more = true; more;) {
+      const KvWalk v = w;
+      const int vq0 = q0;
+      more = kv_advance<kManyRows, kManyUnit>(a, w, q0);
+      if (!tile_there(v)) {   // a short row tile: the other warps' alone
+        it += v.k1 - v.k0;
+        if (more) {
+          y = find(w);
+          if (tile_there(w)) load_q(y, q0);
+        }
+        continue;
+      }
+      // keys that every row of the tile sees
+      int all_lo, all_hi, u0;
+      {
+        const int r0 = v.rt * kManyRows + x * kManyTile;
+        int t1 = (r0 + kManyTile - 1) / a.group;
+        if (t1 > v.T - 1) t1 = v.T - 1;
+        kv_token_keys(v.T, v.n, r0 / a.group, a.p.causal, a.p.window, u0, all_hi);
+        kv_token_keys(v.T, v.n, t1, a.p.causal, a.p.window, all_lo, u0);
+      }
       float m = -INFINITY, mu = 0.f, l = 0.f;
-      for (int k = w.k0; k < w.k1; ++k, ++it) {
-        const int kb = (w.span.lo + k * kManyUnit) * LW_KV_TILE;
-        __syncwarp();
-        if (ok) ok = many_wait(&bar.s_full, it & 1u, flags);
+      for (int k = v.k0; k < v.k1; ++k, ++it, ++c) {
+        const int kb = (v.span.lo + k * kManyUnit) * LW_KV_TILE;
+        const uint32_t sc = mine + F::s_col(x, c & 1);
+        if (ok) ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.s_full[x][c & 1], c >> 1 & 1u, flags));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t there = *reinterpret_cast<const volatile uint32_t*>(present + it % 4 * kManyUnit);
         uint32_t s0[32], s1[32];
-        tmem_ld32(mine + F::kS, s0);
-        tmem_ld32(mine + F::kS + 32, s1);
+        tmem_ld32(sc, s0);
+        tmem_ld32(sc + 32, s1);
         tmem_ld_wait();
-        float2 t[32];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          t[j] = mul2(make_float2(__uint_as_float(s0[2 * j]), __uint_as_float(s0[2 * j + 1])), make_float2(f, f));
-          t[16 + j] = mul2(make_float2(__uint_as_float(s1[2 * j]), __uint_as_float(s1[2 * j + 1])), make_float2(f, f));
-        }
         if (kb < all_lo || kb + kManyKeys > all_hi || there != 0x01010101u) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const bool in = there >> (8 * (j / 8)) & 1u;
-            const int key = kb + 2 * j;
-            if (!(in && key >= lo && key < hi)) t[j].x = -INFINITY;
-            if (!(in && key + 1 >= lo && key + 1 < hi)) t[j].y = -INFINITY;
+          for (int j = 0; j < 64; ++j) {
+            const bool in = there >> (8 * (j / 16)) & 1u;
+            if (!(in && kb + j >= y.lo && kb + j < y.hi)) (j < 32 ? s0[j % 32] : s1[j % 32]) = 0xFF800000u;
           }
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(t[j].x, t[j].y));
+        for (int j = 0; j < 32; ++j) top = fmaxf(fmaxf(top, __uint_as_float(s0[j])), __uint_as_float(s1[j]));
+        top *= f;
         if (__any_sync(0xFFFFFFFFu, top > m + 8.f)) {
           const float mx = fmaxf(m, top);
           mu = mx == -INFINITY ? 0.f : mx;
           const float al = ex2(m - mu);
           m = mx;
           l *= al;
-          if (k > w.k0) {   // (the product of the keys before is complete: S came after it)
+          if (k > v.k0) {   // once the sum over the keys before is complete
+            ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.o_done[x][(c - 1) & 1], (c - 1) >> 1 & 1u, flags));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int d = 0; d < D; d += 32) {
               uint32_t z[32];
-              tmem_ld32(mine + F::kO + c, z);
+              tmem_ld32(mine + F::o_col(x) + d, z);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 32; ++j) z[j] = __float_as_uint(__uint_as_float(z[j]) * al);
-              tmem_st32(mine + F::kO + c, z);
+              tmem_st32(mine + F::o_col(x) + d, z);
             }
           }
         }
-        float2 sum = make_float2(0.f, 0.f);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 f2 = make_float2(f, f), mu2 = make_float2(-mu, -mu);
         uint32_t p[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float2 y = make_float2(ex2(t[j].x - mu), ex2(t[j].y - mu));
-          sum.x += y.x;
-          sum.y += y.y;
-          p[j] = h2bits(__floats2half2_rn(y.x, y.y));
+          const uint32_t* s = j < 16 ? s0 + 2 * j : s1 + 2 * (j - 16);
+          const float2 t = fma2(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), f2, mu2);
+          const float2 z = make_float2(ex2(t.x), ex2(t.y));
+          sum[j % 2] = add2(sum[j % 2], z);
+          p[j] = h2bits(__floats2half2_rn(z.x, z.y));
         }
-        l += sum.x + sum.y;
-        tmem_st32(mine + F::kS, p);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_st32(sc, p);
         tmem_st_wait();
         tc_fence_before();
-        ok = rows_agree(ok);
-        if (!ok) { stop = true; break; }
-        if (row == 0) {
-          ok = issue_o(it, k == w.k0);
-          // S lies over P: the next S once the sum over P is complete
-          if (ok && k + 1 < w.k1) ok = many_wait(&bar.o_full, it & 1u, flags) && issue_s(it + 1);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[x][c & 1]);
       }
-      if (stop) break;
-      const KvWalk v = w;
-      const int vq0 = q0;
-      more = kv_advance<kManyRows, kManyUnit>(a, w, q0);
-      __syncwarp();
-      if (ok) ok = many_wait(&bar.o_full, (it - 1) & 1u, flags);
-      ok = rows_agree(ok);
+      // (every S of this item is complete: Q's place is free)
+      const Row o = y;
+      if (more) {
+        y = find(w);
+        if (ok && tile_there(w)) load_q(y, q0);
+      }
+      if (ok) ok = many_wait(&bar.o_done[x][(c - 1) & 1], (c - 1) >> 1 & 1u, flags);
+      ok = rows_agree(x, ok);   // all four warps go on to the barriers below, or none
       if (!ok) break;
       tc_fence_after();
       const bool whole = v.k0 == 0 && v.k1 == v.units;
-      float* part = a.partials + ((size_t)blockIdx.x * 2 + (v.k0 == 0)) * F::kPartial;
+      float* part = a.partials + (((size_t)blockIdx.x * 2 + (v.k0 == 0)) * 2 + x) * F::kPartial;
       const auto give = [&](int g, float l, const float (&z)[32]) {   // 32 elements of the row, [i][n]
-        if (!live) return;
+        if (!o.live) return;
         const float inv = 1.f / l;
-        const int64_t at = (int64_t)(vq0 + tok) * a.p.out_token_stride + (int64_t)hq * a.p.out_head_stride + 32 * g;
+        const int64_t at = (int64_t)(vq0 + o.tok) * a.p.out_token_stride + (int64_t)o.hq * a.p.out_head_stride + 32 * g;
 #pragma unroll
         for (int n = 0; n < 8; n += 2) {
           float y[8];
@@ -450,14 +575,14 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         }
       };
       const auto give_lse = [&](float m, float l) {
-        if (live && a.p.lse)
-          a.p.lse[(int64_t)(vq0 + tok) * a.p.q_heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        if (o.live && a.p.lse)
+          a.p.lse[(int64_t)(vq0 + o.tok) * a.p.q_heads + o.hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       };
 #pragma unroll 1
       for (int g = 0; g < G; ++g) {
         uint32_t u[32];
         float z[32];
-        tmem_ld32(mine + F::kO + 32 * g, u);
+        tmem_ld32(mine + F::o_col(x) + 32 * g, u);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(u[j]);
@@ -466,7 +591,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         } else {
 #pragma unroll
           for (int n = 0; n < 8; ++n)
-            *reinterpret_cast<float4*>(part + 2 * kManyRows + ((8 * g + n) * kManyRows + row) * 4) =
+            *reinterpret_cast<float4*>(part + 2 * kManyTile + ((8 * g + n) * kManyTile + row) * 4) =
                 make_float4(z[n], z[8 + n], z[16 + n], z[24 + n]);
         }
       }
@@ -475,26 +600,26 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         give_lse(m, l);
       } else {
         part[row] = m;
-        part[kManyRows + row] = l;
+        part[kManyTile + row] = l;
         const long long x0 = v.x - v.k0;
         const int c0 = tc_owner(x0, U, Gc), parts = tc_owner(x0 + v.units - 1, U, Gc) - c0 + 1;
         __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (threadIdx.x == 0) {
-          const bool last = atomicAdd(a.counters + c0, 1u) == (uint32_t)parts - 1u;
-          if (last) a.counters[c0] = 0;
-          flags[1] = last;
+        rows_agree(x, true);
+        if (row == 0) {
+          const bool last = atomicAdd(a.counters + 2 * c0 + x, 1u) == (uint32_t)parts - 1u;
+          if (last) a.counters[2 * c0 + x] = 0;
+          flags[1 + x] = last;
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (flags[1]) {
+        rows_agree(x, true);
+        if (flags[1 + x]) {
           __threadfence();
           const auto from = [&](int i) {
-            return a.partials + (i ? (size_t)(c0 + i) * 2 : (size_t)c0 * 2 + 1) * F::kPartial;
+            return a.partials + ((i ? (size_t)(c0 + i) * 2 : (size_t)c0 * 2 + 1) * 2 + x) * F::kPartial;
           };
           float M = -INFINITY, S = 0.f;
           for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(from(i) + row));
           const float Mu = M == -INFINITY ? 0.f : M;
-          for (int i = 0; i < parts; ++i) S = fmaf(__ldcg(from(i) + kManyRows + row), ex2(__ldcg(from(i) + row) - Mu), S);
+          for (int i = 0; i < parts; ++i) S = fmaf(__ldcg(from(i) + kManyTile + row), ex2(__ldcg(from(i) + row) - Mu), S);
 #pragma unroll 1
           for (int g = 0; g < G; ++g) {
             float z[32];
@@ -506,7 +631,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
               const float e = ex2(__ldcg(p + row) - Mu);
 #pragma unroll
               for (int n = 0; n < 8; ++n) {
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 2 * kManyRows + ((8 * g + n) * kManyRows + row) * 4));
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 2 * kManyTile + ((8 * g + n) * kManyTile + row) * 4));
                 z[n] = fmaf(y.x, e, z[n]);
                 z[8 + n] = fmaf(y.y, e, z[8 + n]);
                 z[16 + n] = fmaf(y.z, e, z[16 + n]);
@@ -517,22 +642,18 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           }
           give_lse(M, S);
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        rows_agree(x, true);
       }
     }
     if (!ok) {
       flags[0] = 1;
       if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
     }
-    if (row == 0) {   // no product may be in flight when the tensor memory goes
-      umma_commit(&bar.last);
-      mbar_wait(&bar.last, 0);
-    }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, F::kCols);
+  if (warp == 12) tmem_dealloc(tmem, F::kCols);
 }
 
 }  // namespace dev
