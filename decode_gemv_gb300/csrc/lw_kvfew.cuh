@@ -566,8 +566,8 @@ __device__ __forceinline__ void few_out(const AttnArgs& a, const KvWalk& w, int 
 
 // A warp's tiles, N (1 or 2) neighbours at a time: sent for in order, STAGES
 // ahead.  The table is read 32 tiles at a time, lane i holding where the i-th
-// lies and sending for it.  UNIT: tiles of a unit (the step to the warp's next).
-template <int D, int UNIT, int N, int STAGES>
+// lies and sending for it.  STEP: tiles to the warp's next.
+template <int D, int STEP, int N, int STAGES>
 struct FewFetch {
   static constexpr int kTile = KvTile<D>::kBytes;
   static constexpr uint32_t kAll = (1u << N) - 1;
@@ -576,14 +576,14 @@ struct FewFetch {
   const int32_t* table;    // the sequence's pages
   const uint8_t* src;      // this lane's tile, of the 32
   int64_t head;            // first byte of the head in a page
-  int first, last;         // the item's tiles of this warp: first .. first + N - 1, then UNIT on, below last
+  int first, last;         // the item's tiles of this warp: first .. first + N - 1, then STEP on, below last
   int next, at;            // tile to send for; its place among the 32
   uint32_t there;          // which of the 32 have a page
   int in, out;             // ring places to fill and to use
   uint32_t have, parity;   // tiles sent for (N bits a place); phase per place
 
   __device__ __forceinline__ void lookup(const AttnArgs& a, int lane) {
-    const int tile = next + lane / N * UNIT + lane % N, tpp = a.page_tokens / LW_KV_TILE;
+    const int tile = next + lane / N * STEP + lane % N, tpp = a.page_tokens / LW_KV_TILE;
     const bool mine = tile < last;
     const int page = mine ? __ldg(table + tile / tpp) : -1;
     const bool ok = page >= 0 && page < a.n_pages;
@@ -592,12 +592,12 @@ struct FewFetch {
     src = a.pages + (int64_t)page * a.page_bytes + head + (tile % tpp) * kTile;
     at = 0;
   }
-  __device__ __forceinline__ void begin(const AttnArgs& a, const KvWalk& w, int warp, int lane) {
+  // The warp's tiles of an item: from, from + STEP, ... below `to`
+  __device__ __forceinline__ void begin(const AttnArgs& a, const KvWalk& w, int from, int to, int lane) {
     table = a.p.page_table + (int64_t)w.b * a.p.table_stride;
     head = (int64_t)w.h * (a.page_tokens / LW_KV_TILE) * kTile;
-    next = first = w.span.lo + w.k0 * UNIT + N * warp;
-    last = w.span.lo + w.k1 * UNIT;
-    if (last > w.span.hi) last = w.span.hi;
+    next = first = from;
+    last = to < w.span.hi ? to : w.span.hi;
     in = out = 0;
     have = 0;
     at = 32;
@@ -616,7 +616,7 @@ struct FewFetch {
       have |= some << (N * in);
     }
     at += N;
-    next += UNIT;
+    next += STEP;
     in = in + 1 == STAGES ? 0 : in + 1;
   }
   // The tiles at `out` have come (false: the wait ran out)
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
   float* s_m = reinterpret_cast<float*>(smem + F::kState);
   float* s_l = s_m + W * 8;
   float* mine = s_o + warp * 8 * D;
-  t.begin(a, w, warp, lane);
+  t.begin(a, w, w.span.lo + w.k0 * kFewUnit + 2 * warp, w.span.lo + w.k1 * kFewUnit, lane);
   for (bool more = true; more;) {
     f.start(a, w, q0, RT, lane);
     // keys that every row of the item sees
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
     const KvWalk v = w;
     const int vq0 = q0;
     more = kv_advance<RT, kFewUnit>(a, w, q0);
-    if (more && !dead) t.begin(a, w, warp, lane);
+    if (more && !dead) t.begin(a, w, w.span.lo + w.k0 * kFewUnit + 2 * warp, w.span.lo + w.k1 * kFewUnit, lane);
 
     // join the warps, 8 rows at a time
     const bool whole = v.k0 == 0 && v.k1 == v.units;

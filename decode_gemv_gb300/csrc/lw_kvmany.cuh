@@ -5,17 +5,19 @@
 // 128; keys come 64 at a time.  S = Q K^T and O += P V are tcgen05.mma: Q, K
 // and V (fp16, restored from the codes) are operand tiles in shared memory, P
 // and the accumulators lie in tensor memory.
-//  * 4 loader warps, one per 16-key tile of the 64: fetch their tile by bulk
+//  * 7 loader warps take the 16-key tiles in turn: fetch theirs by bulk
 //    copies (a ring of their own), restore k = sc c + mn and v = sc c + mn by
-//    one rounded fp16 fma each, and store them as operand tiles (two buffers),
-//    once for both row tiles;
+//    one rounded fp16 fma each, and store them as operand tiles (three
+//    buffers), once for both row tiles;
 //  * 8 row warps, one thread per row: put Q into shared memory (each row scaled
 //    by a power of two: the fp16 range), then for every 64 keys read the row of
 //    S, take p = 2^(s - m), store it as fp16 over S, and add the row's sum.  m
 //    is raised, and O rescaled, only where a score passes it by 2^8 (p stays
 //    below 2^8, in fp16 range and precision);
-//  * one thread issues the products.  S has two buffers a tile: the next S is
-//    computed while the rows work on this one.
+//  * one warp issues the products (all of its lanes walk along, so that the
+//    descriptors are warp-uniform: an issue from divergent code took 80 cycles
+//    and bounded the kernel).  S has two buffers a tile: the next S is computed
+//    while the rows work on this one.
 // Operands of 11 bits (fp16) under outputs of 8 (bf16).
 //
 // The operand tiles are K-major core matrices of 8 x 16 bytes.  A key code
@@ -32,10 +34,12 @@
 namespace lw {
 
 constexpr int kManyTile = 128, kManyRows = 2 * kManyTile, kManyKeys = 64;
-constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit = loader warps
-constexpr int kManyThreads = 32 * 13;               // 8 row warps, 4 loader warps, 1 to issue
+constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit
+constexpr int kManyLoaders = 7;
+constexpr int kManyThreads = 32 * (8 + kManyLoaders + 1);   // row warps, loader warps, one to issue
 constexpr int kManyPerSm = 1;
-constexpr int kManyStages = 4;                      // tiles of a loader's ring
+constexpr int kManyStages = 3;                      // tiles of a loader's ring
+constexpr int kManyBufs = 3;                        // restored units
 
 template <int D>
 struct Many {
@@ -47,9 +51,10 @@ struct Many {
   static constexpr int kVLbo = D * 16;                // bytes between 8-key columns
   static constexpr int kVBytes = kManyKeys / 8 * kVLbo;
   static constexpr int kHead = 1024;                  // barriers and flags
-  static constexpr int kQ = kHead, kK = kQ + 2 * kQBytes, kV = kK + 2 * kKBytes;
-  static constexpr int kRing = kV + 2 * kVBytes;
-  static constexpr int kSmem = kRing + kManyUnit * kManyStages * L::kBytes;
+  static constexpr int kQ = kHead, kKv = kQ + 2 * kQBytes;   // a buffer: K, then V
+  static constexpr int kKvBytes = kKBytes + kVBytes;
+  static constexpr int kRing = kKv + kManyBufs * kKvBytes;
+  static constexpr int kSmem = kRing + kManyLoaders * kManyStages * L::kBytes;
   static constexpr int kPartial = kManyTile * (D + 2);   // of a tile, floats: m, l, then [D / 4][rows][4]
   // tensor-memory columns: S of tile x, buffer i (and P over it); O of tile x
   __host__ __device__ static constexpr uint32_t s_col(int x, int i) { return 128 * x + 64 * i; }
@@ -133,63 +138,65 @@ __device__ __forceinline__ bool rows_agree(int tile, bool ok) {
   return r != 0;
 }
 
-// 32 rows of Q (a warp's; row r of them in tile row 32 quarter + r) into the
-// operand tile, each scaled by 2^-e and given the sign of `scale` (so that the
-// largest product is the largest score); returns 2^e of row `lane`.  Row r
-// starts at element row_at of lane r, or is 0 (row_at < 0).
+// This thread's row of Q (all of it 0 where p is NULL) into row `row` of the
+// operand tile, scaled by 2^-e and with the sign of `scale` (so that the largest
+// product is the largest score); returns 2^e.
 template <int D, bool VEC>
-__device__ __forceinline__ float many_query(const __nv_bfloat16* q, int64_t row_at, float scale, uint32_t to,
-                                            int quarter, int lane) {
-  using F = Many<D>;
-  const uint32_t sign = __float_as_uint(scale) & 0x80000000u;
-  float mine = 1.f;
-  to += (uint32_t)((lane / 2) * F::kQLbo + (lane & 1) * 8 + quarter * 4 * 128);
-#pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += 16) {
-    uint2 w[16];   // this lane's elements 4 lane .. 4 lane + 3
+__device__ __forceinline__ float many_query(const __nv_bfloat16* p, float scale, uint32_t to, int row) {
+  uint32_t w[D / 2];   // the row's pairs
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t at = __shfl_sync(0xFFFFFFFFu, row_at, r0 + i);
-      w[i] = make_uint2(0u, 0u);
-      if (at >= 0 && lane < D / 4) {
-        const __nv_bfloat16* p = q + at + 4 * lane;
-        if constexpr (VEC) w[i] = *reinterpret_cast<const uint2*>(p);
-        else
-          w[i] = make_uint2(__bfloat16_as_ushort(p[0]) | (uint32_t)__bfloat16_as_ushort(p[1]) << 16,
-                            __bfloat16_as_ushort(p[2]) | (uint32_t)__bfloat16_as_ushort(p[3]) << 16);
+  for (int i = 0; i < D / 8; ++i) {
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (p) {
+      if constexpr (VEC) {
+        u = __ldg(reinterpret_cast<const uint4*>(p + 8 * i));
+      } else {
+        uint32_t* v = &u.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[j] = __bfloat16_as_ushort(p[8 * i + 2 * j]) | (uint32_t)__bfloat16_as_ushort(p[8 * i + 2 * j + 1]) << 16;
       }
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      // magnitudes are in order as integers (a NaN comes last, and stays NaN below)
-      const uint32_t a = max(max(w[i].x << 16 & 0x7FFF0000u, w[i].x & 0x7FFF0000u),
-                             max(w[i].y << 16 & 0x7FFF0000u, w[i].y & 0x7FFF0000u));
-      int e = (int)(__reduce_max_sync(0xFFFFFFFFu, a) >> 23) - 127;
-      e = e < -100 ? -100 : (e > 126 ? 126 : e);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23 | sign);
-      if (lane == r0 + i) mine = __uint_as_float((uint32_t)(127 + e) << 23);
-      const uint32_t h0 = h2bits(__floats2half2_rn(__uint_as_float(w[i].x << 16) * down, __uint_as_float(w[i].x & 0xFFFF0000u) * down));
-      const uint32_t h1 = h2bits(__floats2half2_rn(__uint_as_float(w[i].y << 16) * down, __uint_as_float(w[i].y & 0xFFFF0000u) * down));
-      // an even lane has elements 0..3 of the eight and stores (0,4), (1,5); an odd one 4..7, (2,6), (3,7)
-      const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? h0 : h1, 1);
-      const uint32_t low = lane & 1 ? other : h0, high = lane & 1 ? h1 : other;
-      const int r = r0 + i;
-      if (lane < D / 4)
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + (uint32_t)((r / 8) * 128 + (r % 8) * 16)),
-                     "r"(__byte_perm(low, high, 0x5410)), "r"(__byte_perm(low, high, 0x7632))
-                     : "memory");
-    }
+    w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
   }
-  return mine;
+  uint32_t lo = 0, hi = 0;   // magnitudes are in order as integers (a NaN comes last, and stays NaN below)
+#pragma unroll
+  for (int i = 0; i < D / 2; ++i) {
+    lo = max(lo, w[i] & 0x7FFFu);
+    hi = max(hi, w[i] & 0x7FFF0000u);
+  }
+  int e = (int)(max(lo << 16, hi) >> 23) - 127;
+  e = e < -100 ? -100 : (e > 126 ? 126 : e);
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23 | (__float_as_uint(scale) & 0x80000000u));
+  to += (uint32_t)((row / 8) * 128 + (row % 8) * 16);
+#pragma unroll
+  for (int o = 0; o < D / 8; ++o) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] = __uint_as_float(w[4 * o + i] << 16) * down;
+      y[2 * i + 1] = __uint_as_float(w[4 * o + i] & 0xFFFF0000u) * down;
+    }
+    sts_u4(to + o * Many<D>::kQLbo, h2bits(__floats2half2_rn(y[0], y[4])), h2bits(__floats2half2_rn(y[1], y[5])),
+           h2bits(__floats2half2_rn(y[2], y[6])), h2bits(__floats2half2_rn(y[3], y[7])));
+  }
+  return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// One lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // Barriers of a CTA.  Those of a row tile are one per S buffer, so that the use
 // before the one waited for is always complete (a parity names one of two).
 struct ManyBars {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];   // per operand buffer
+  uint64_t kv_full[kManyBufs], kv_free[kManyBufs];       // per operand buffer
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];   // per row tile (and S buffer)
   uint64_t last;                                         // everything issued has completed
-  uint64_t ring[kManyUnit][kManyStages];
+  uint64_t ring[kManyLoaders][kManyStages];
 };
 
 template <int D>
@@ -202,16 +209,14 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   static_assert(sizeof(ManyBars) <= 512, "barriers");
   volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + 512);   // [0] abort, [1], [2] last part of a tile's item
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + 528);   // tensor memory
-  // [unit % 4][tile]: the tile's keys are there (written before k_full, read
-  // after s_full; four units on, the rows have long answered)
+  // [unit % 4][tile]: the tile's keys are there (written before kv_full, read
+  // after s_full; four units on, the rows have answered)
   volatile uint8_t* present = smem + 544;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.k_full[i], kManyUnit);
-      mbar_init(&bar.v_full[i], kManyUnit);
-      mbar_init(&bar.k_free[i], 1);
-      mbar_init(&bar.v_free[i], 1);
+    for (int i = 0; i < kManyBufs; ++i) {
+      mbar_init(&bar.kv_full[i], kManyUnit);
+      mbar_init(&bar.kv_free[i], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar.q_full[x], 4);
@@ -223,12 +228,12 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       mbar_init(&bar.o_done[x][1], 1);
     }
     mbar_init(&bar.last, 1);
-    for (int i = 0; i < kManyUnit; ++i)
+    for (int i = 0; i < kManyLoaders; ++i)
       for (int j = 0; j < kManyStages; ++j) mbar_init(&bar.ring[i][j], 1);
     flags[0] = 0;
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 8 + kManyLoaders) {
     tmem_alloc(smem_addr(tslot), F::kCols);
     tmem_relinquish();
   }
@@ -243,15 +248,16 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   const bool any = kv_range<kManyThreads, kManyRows, kManyUnit>(a, w, Gc, U, q0);
   bool ok = true;   // no wait ran out
 
-  if (any && warp >= 8 && warp < 12) {   // ---- loaders
+  if (any && warp >= 8 && warp < 8 + kManyLoaders) {   // ---- loaders
     const int lw = warp - 8;
-    FewFetch<D, kManyUnit, 1, kManyStages> t;
+    FewFetch<D, kManyLoaders, 1, kManyStages> t;
     t.bars = bar.ring[lw];
     t.ring = smem + F::kRing + lw * kManyStages * L::kBytes;
     t.parity = t.have = 0;
-    uint32_t it = 0;
+    constexpr int GW = (G + 1) / 2;   // groups of a lane
+    uint32_t it0 = 0;                 // units before this item
     for (bool more = true; more && ok;) {
-      t.begin(a, w, lw, lane);
+      t.begin(a, w, w.span.lo + w.k0 * kManyUnit + lw, w.span.lo + w.k1 * kManyUnit, lane);
       // rows of the item all see the keys [all_lo, all_hi)
       int all_lo, all_hi, x;
       {
@@ -260,111 +266,118 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         kv_token_keys(w.T, w.n, w.rt * kManyRows / a.group, a.p.causal, a.p.window, x, all_hi);
         kv_token_keys(w.T, w.n, t1, a.p.causal, a.p.window, all_lo, x);
       }
-      for (int k = w.k0; k < w.k1; ++k, ++it) {
-        const int tile = w.span.lo + k * kManyUnit + lw, buf = it & 1;
-        const uint32_t par = (it >> 1 & 1u) ^ 1u;
+      const int count = (w.k1 - w.k0) * kManyUnit;   // (the last unit's tiles may lie past the end)
+      for (int o = lw; o < count; o += kManyLoaders) {
+        const int tile = w.span.lo + w.k0 * kManyUnit + o, sub = o % kManyUnit;
+        const uint32_t it = it0 + o / kManyUnit, buf = it % kManyBufs, phase = it / kManyBufs & 1u;
         const bool there = tile < w.span.hi && (t.have >> t.out & 1u);
         if (there && !t.wait()) { ok = false; mbar_wait(&t.bars[t.out], (t.parity >> t.out & 1u) ^ 1u); break; }
         const uint32_t s = smem_addr(t.ring) + t.out * L::kBytes;
         const int kb = tile * LW_KV_TILE;
         const bool edge = kb < all_lo || kb + LW_KV_TILE > all_hi;
-        if (!__all_sync(0xFFFFFFFFu, many_wait(&bar.k_free[buf], par, flags))) { ok = false; break; }
+        // the codes, scales and minimums of this lane: keys lane / 4 and 8 more, elements
+        // 32 g + 8 q + 0..7; values of keys 8 h .. 8 h + 7, groups g0 .. g0 + GW - 1
+        const int q = lane & 3, n = lane & 7, h = lane >> 4, g0 = GW * (lane >> 3 & 1);
+        uint32_t kc[2][G], ks[2][G], km[2][L::GP / 2], vc[4][GW], vs[4][GW], vm[4][GW];
         if (there) {
-          const int q = lane & 3;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {   // key 8 h + lane / 4, elements 32 g + 8 q + 0..7
-            const int tk = 8 * h + lane / 4;
-            uint32_t cw[G], sw[G], mw[L::GP / 2];
-            lds_words<G>(s + L::kKeyCodes + (uint32_t)((tk * 4 + q) * G) * 4, cw);
-            lds_words<G>(s + L::kKeyScale + (uint32_t)(tk / 2 * G) * 4, sw);
-            lds_words<L::GP / 2>(s + L::kKeyMin + (uint32_t)(tk * L::GP) * 2, mw);
-            if (edge) {   // rows that do not see a key must not get its NaN through V (0 x NaN): let it come by S
+          for (int i = 0; i < 2; ++i) {
+            const int tk = 8 * i + lane / 4;
+            lds_words<G>(s + L::kKeyCodes + (uint32_t)((tk * 4 + q) * G) * 4, kc[i]);
+            lds_words<G>(s + L::kKeyScale + (uint32_t)(tk / 2 * G) * 4, ks[i]);
+            lds_words<L::GP / 2>(s + L::kKeyMin + (uint32_t)(tk * L::GP) * 2, km[i]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int p = 4 * h + j;   // pair of keys
+            if constexpr (G % 2 == 0) {
+              lds_words<GW>(s + L::kValCodes + (uint32_t)((p * 8 + n) * G + g0) * 4, vc[j]);
+              lds_words<GW>(s + L::kValScale + (uint32_t)(p * G + g0) * 4, vs[j]);
+              lds_words<GW>(s + L::kValMin + (uint32_t)(p * G + g0) * 4, vm[j]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < GW; ++i) {
+                const int g = g0 + i < G ? g0 + i : G - 1;   // (the group past the last is not stored)
+                vc[j][i] = lds_u32(s + L::kValCodes + (uint32_t)((p * 8 + n) * G + g) * 4);
+                vs[j][i] = lds_u32(s + L::kValScale + (uint32_t)(p * G + g) * 4);
+                vm[j][i] = lds_u32(s + L::kValMin + (uint32_t)(p * G + g) * 4);
+              }
+            }
+          }
+          if (edge) {
+            // rows that do not see a key must not get its NaN through V (0 x NaN): let it come by S
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int tk = 8 * i + lane / 4;
               bool nan = false;
 #pragma unroll
               for (int g = 0; g < G; ++g) {
                 const uint32_t z = lds_u16(s + L::kValScale + (uint32_t)((tk / 2 * G + g) * 2 + tk % 2) * 2);
                 nan |= (z & 0x7FFFu) > 0x7C00u;
               }
-              if (nan) sw[0] = 0x7FFF7FFFu;
+              if (nan) ks[i][0] = 0x7FFF7FFFu;
             }
-            const uint32_t to = smem_addr(smem) + F::kK + buf * F::kKBytes + (uint32_t)((lw * 2 + h) * 128 + (lane / 4) * 16);
-            const uint32_t half = lane & 4 ? 0x3232u : 0x1010u;   // key 2 j or 2 j + 1
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-              const uint32_t sc = __byte_perm(sw[g], 0, half);
-              const uint32_t mn = __byte_perm(mw[g / 2], 0, g % 2 ? 0x3232u : 0x1010u);
-              const uint32_t w0 = cw[g], w1 = cw[g] >> 8;
-              sts_u4(to + (uint32_t)((4 * g + q) * F::kKLbo), fma_h2(whole_even(w0), sc, mn),
-                     fma_h2(whole_odd(w0), sc, mn), fma_h2(whole_even(w1), sc, mn), fma_h2(whole_odd(w1), sc, mn));
-            }
-          }
-        }
-        if (lane == 0) present[it % 4 * kManyUnit + lw] = there;
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.k_full[buf]);
-        if (!__all_sync(0xFFFFFFFFu, many_wait(&bar.v_free[buf], par, flags))) { ok = false; break; }
-        {
-          constexpr int GW = (G + 1) / 2;   // groups of a lane: GW gh ..
-          const int n = lane & 7, gh = lane >> 3 & 1, h = lane >> 4;   // keys 8 h .. 8 h + 7
-          const int g0 = GW * gh;
-          const uint32_t to = smem_addr(smem) + F::kV + buf * F::kVBytes + (uint32_t)((lw * 2 + h) * F::kVLbo + n * 16);
-          uint32_t cw[4][GW], sc[4][GW], mn[4][GW];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int p = 4 * h + j;   // pair of keys
-            if (there && G % 2 == 0) {
-              lds_words<GW>(s + L::kValCodes + (uint32_t)((p * 8 + n) * G + g0) * 4, cw[j]);
-              lds_words<GW>(s + L::kValScale + (uint32_t)(p * G + g0) * 4, sc[j]);
-              lds_words<GW>(s + L::kValMin + (uint32_t)(p * G + g0) * 4, mn[j]);
-            } else {
+            for (int j = 0; j < 4; ++j) {
+              const int key = kb + 2 * (4 * h + j);
 #pragma unroll
               for (int i = 0; i < GW; ++i) {
-                cw[j][i] = sc[j][i] = mn[j][i] = 0;
-                if (there && g0 + i < G) {
-                  cw[j][i] = lds_u32(s + L::kValCodes + (uint32_t)((p * 8 + n) * G + g0 + i) * 4);
-                  sc[j][i] = lds_u32(s + L::kValScale + (uint32_t)(p * G + g0 + i) * 4);
-                  mn[j][i] = lds_u32(s + L::kValMin + (uint32_t)(p * G + g0 + i) * 4);
-                }
-              }
-            }
-            if (edge) {
-              const int key = kb + 2 * p;
-#pragma unroll
-              for (int i = 0; i < GW; ++i) {
-                const uint32_t z = sc[j][i];
+                const uint32_t z = vs[j][i];
                 const uint32_t keep = (key < w.n && (z & 0x7FFFu) <= 0x7C00u ? 0xFFFFu : 0u) |
                                       (key + 1 < w.n && (z & 0x7FFF0000u) <= 0x7C000000u ? 0xFFFF0000u : 0u);
-                sc[j][i] &= keep;
-                mn[j][i] &= keep;
+                vs[j][i] &= keep;
+                vm[j][i] &= keep;
               }
             }
           }
+        } else {   // no keys: S is masked, and V has to be finite
 #pragma unroll
-          for (int i = 0; i < GW; ++i) {
-            if (G % 2 && g0 + i >= G) continue;
-            const uint32_t row = to + (uint32_t)(4 * (g0 + i)) * 128;
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int st = 0; st < 2; ++st) {
-              uint32_t e[4], o[4];
+            for (int i = 0; i < GW; ++i) vc[j][i] = vs[j][i] = vm[j][i] = 0;
+        }
+        if (!__all_sync(0xFFFFFFFFu, many_wait(&bar.kv_free[buf], phase ^ 1u, flags))) { ok = false; break; }
+        const uint32_t kto = smem_addr(smem) + F::kKv + buf * F::kKvBytes + (uint32_t)(sub * 256 + (lane / 4) * 16 + q * F::kKLbo);
+        const uint32_t vto = smem_addr(smem) + F::kKv + buf * F::kKvBytes + F::kKBytes +
+                             (uint32_t)((sub * 2 + h) * F::kVLbo + n * 16 + g0 * 512);
+        if (there) {
+          const uint32_t half = lane & 4 ? 0x3232u : 0x1010u;   // key 2 j or 2 j + 1
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                e[j] = fma_h2(whole_even(cw[j][i] >> (8 * st)), sc[j][i], mn[j][i]);
-                o[j] = fma_h2(whole_odd(cw[j][i] >> (8 * st)), sc[j][i], mn[j][i]);
-              }
-              sts_u4(row + (2 * st) * 128, e[0], e[1], e[2], e[3]);
-              sts_u4(row + (2 * st + 1) * 128, o[0], o[1], o[2], o[3]);
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const uint32_t sc = __byte_perm(ks[i][g], 0, half);
+              const uint32_t mn = __byte_perm(km[i][g / 2], 0, g % 2 ? 0x3232u : 0x1010u);
+              const uint32_t w0 = kc[i][g], w1 = kc[i][g] >> 8;
+              sts_u4(kto + (uint32_t)(i * 128 + 4 * g * F::kKLbo), fma_h2(whole_even(w0), sc, mn),
+                     fma_h2(whole_odd(w0), sc, mn), fma_h2(whole_even(w1), sc, mn), fma_h2(whole_odd(w1), sc, mn));
             }
+        }
+#pragma unroll
+        for (int i = 0; i < GW; ++i) {
+          if (G % 2 && g0 + i >= G) continue;
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            uint32_t e[4], o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              e[j] = fma_h2(whole_even(vc[j][i] >> (8 * st)), vs[j][i], vm[j][i]);
+              o[j] = fma_h2(whole_odd(vc[j][i] >> (8 * st)), vs[j][i], vm[j][i]);
+            }
+            sts_u4(vto + (uint32_t)(i * 512 + (2 * st) * 128), e[0], e[1], e[2], e[3]);
+            sts_u4(vto + (uint32_t)(i * 512 + (2 * st + 1) * 128), o[0], o[1], o[2], o[3]);
           }
         }
+        if (lane == 0) present[it % 4 * kManyUnit + sub] = there;
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v_full[buf]);
+        if (lane == 0) mbar_arrive(&bar.kv_full[buf]);
         if (tile < w.span.hi) {
           t.out = t.out + 1 == kManyStages ? 0 : t.out + 1;
           t.send(a, lane);
         }
       }
+      it0 += w.k1 - w.k0;
       if (ok) more = kv_advance<kManyRows, kManyUnit>(a, w, q0);
     }
     if (!ok) {
@@ -373,74 +386,92 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       for (int i = 0; i < kManyStages; ++i)   // no copy may be in flight when the CTA ends
         if (t.have >> i & 1u) mbar_wait(&t.bars[i], t.parity >> i & 1u);
     }
-  } else if (any && warp == 12) {   // ---- issuer
-    if (lane == 0) {
-      const uint32_t base = smem_addr(smem);
-      uint32_t it = 0, items[2] = {0, 0}, done[2] = {0, 0};   // units; per tile: items, units before this item
-      // S of tile x from the keys of unit `u` (its c-th unit); O += P V
-      const auto issue_s = [&](int x, uint32_t u, uint32_t c) {
-        const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
-        const uint64_t kd = sdesc(base + F::kK + (u & 1) * F::kKBytes, F::kKLbo, 128);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          umma_bf16(tmem + F::s_col(x, c & 1), qd + (2 * s * F::kQLbo >> 4), kd + (2 * s * F::kKLbo >> 4),
-                    idesc_f16(kManyKeys), s > 0);
-        umma_commit(&bar.s_full[x][c & 1]);
-      };
-      const auto issue_o = [&](int x, uint32_t u, uint32_t c, bool first) {
-        const uint64_t vd = sdesc(base + F::kV + (u & 1) * F::kVBytes, F::kVLbo, 128);
-#pragma unroll
-        for (int s = 0; s < kManyKeys / 16; ++s)
-          umma_bf16_ta(tmem + F::o_col(x), tmem + F::s_col(x, c & 1) + 8 * s, vd + (2 * s * F::kVLbo >> 4),
-                       idesc_f16(D), !first || s > 0);
-        umma_commit(&bar.o_done[x][c & 1]);
-      };
-      for (bool more = true; more && ok;) {
-        const int tiles = (w.T * a.group - w.rt * kManyRows) > kManyTile ? 2 : 1;
-        const int n = w.k1 - w.k0;
-        // S of the i-th unit lies where P of the (i - 2)-th was
-        const auto next_s = [&](int i) {
-          if (!many_wait(&bar.k_full[(it + i) & 1], (it + i) >> 1 & 1u, flags)) return false;
-          for (int x = 0; x < tiles; ++x) {
-            const uint32_t c = done[x] + i;
-            if (i == 0 && !many_wait(&bar.q_full[x], items[x] & 1u, flags)) return false;
-            if (c >= 2 && !many_wait(&bar.o_done[x][c & 1], (c - 2) >> 1 & 1u, flags)) return false;
-            tc_fence_after();
-            issue_s(x, it + i, c);
-          }
-          umma_commit(&bar.k_free[(it + i) & 1]);
-          return true;
-        };
-        ok = next_s(0);
-        for (int i = 0; ok && i < n; ++i) {
-          if (i + 1 < n && !next_s(i + 1)) { ok = false; break; }
-          if (!many_wait(&bar.v_full[(it + i) & 1], (it + i) >> 1 & 1u, flags)) { ok = false; break; }
-          for (int x = 0; x < tiles; ++x) {
-            const uint32_t c = done[x] + i;
-            if (!many_wait(&bar.p_full[x][c & 1], c >> 1 & 1u, flags)) { ok = false; break; }
-            tc_fence_after();
-            issue_o(x, it + i, c, i == 0);
-          }
-          umma_commit(&bar.v_free[(it + i) & 1]);
-        }
-        it += n;
+  } else if (any && warp == 8 + kManyLoaders) {   // ---- issuer
+    const uint32_t base = smem_addr(smem);
+    const auto wait = [&](uint64_t* b, uint32_t parity, volatile uint32_t* f) {
+      return __all_sync(0xFFFFFFFFu, many_wait(b, parity, f)) != 0;
+    };
+    const auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+    const uint32_t tm = uniform(tmem);
+    // this unit and the one whose S is next: operand buffers and their phases; S buffers
+    int buf = 0, nbuf = 0, sbuf = 0, nsbuf = 0;
+    uint32_t nphase = 0;
+    uint32_t qph = 0, pph[2] = {0, 0}, oph[2] = {0, 0};   // phases of q_full (bit a tile), p_full and o_done (bit an S buffer)
+    uint32_t used[2] = {0, 0};                            // S buffers that have held a P
+    for (bool more = true; more && ok;) {
+      const int tiles = uniform((w.T * a.group - w.rt * kManyRows) > kManyTile ? 2 : 1);
+      const int n = uniform(w.k1 - w.k0);
+      const auto next_s = [&](bool first) {   // S of the next unit, over the P of two units before
+        if (!wait(&bar.kv_full[nbuf], nphase, flags)) return false;
+        const uint64_t kd = sdesc(base + F::kKv + nbuf * F::kKvBytes, F::kKLbo, 128);
+#pragma unroll 1
         for (int x = 0; x < tiles; ++x) {
-          done[x] += n;
-          ++items[x];
+          if (first) {
+            if (!wait(&bar.q_full[x], qph >> x & 1u, flags)) return false;
+            qph ^= 1u << x;
+          }
+          if (used[x] >> nsbuf & 1u) {
+            if (!wait(&bar.o_done[x][nsbuf], oph[x] >> nsbuf & 1u, flags)) return false;
+            oph[x] ^= 1u << nsbuf;
+          }
+          used[x] |= 1u << nsbuf;
+          tc_fence_after();
+          const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
+          const uint32_t d = tm + F::s_col(x, nsbuf);
+          if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              umma_bf16(d, qd + (2 * s * F::kQLbo >> 4), kd + (2 * s * F::kKLbo >> 4), idesc_f16(kManyKeys), s > 0);
+            umma_commit(&bar.s_full[x][nsbuf]);
+          }
+          __syncwarp();
         }
-        if (ok) more = kv_advance<kManyRows, kManyUnit>(a, w, q0);
+        nsbuf ^= 1;
+        if (++nbuf == kManyBufs) {
+          nbuf = 0;
+          nphase ^= 1u;
+        }
+        return true;
+      };
+      ok = next_s(true);
+#pragma unroll 1
+      for (int i = 0; ok && i < n; ++i) {
+        if (i + 1 < n && !next_s(false)) { ok = false; break; }
+        const uint64_t vd = sdesc(base + F::kKv + buf * F::kKvBytes + F::kKBytes, F::kVLbo, 128);
+#pragma unroll 1
+        for (int x = 0; x < tiles; ++x) {
+          if (!wait(&bar.p_full[x][sbuf], pph[x] >> sbuf & 1u, flags)) { ok = false; break; }
+          pph[x] ^= 1u << sbuf;
+          tc_fence_after();
+          const uint32_t d = tm + F::o_col(x), p = tm + F::s_col(x, sbuf);
+          if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < kManyKeys / 16; ++s)
+              umma_bf16_ta(d, p + 8 * s, vd + (2 * s * F::kVLbo >> 4), idesc_f16(D), i > 0 || s > 0);
+            umma_commit(&bar.o_done[x][sbuf]);
+            if (x == tiles - 1) umma_commit(&bar.kv_free[buf]);
+          }
+          __syncwarp();
+        }
+        sbuf ^= 1;
+        if (++buf == kManyBufs) buf = 0;
       }
-      if (!ok) {
-        flags[0] = 1;
-        report(a.status, LW_DEV_TIMEOUT);
-      }
-      umma_commit(&bar.last);   // no product may be in flight when the tensor memory goes
-      mbar_wait(&bar.last, 0);
+      if (ok) more = uniform(kv_advance<kManyRows, kManyUnit>(a, w, q0));
     }
+    if (!ok) {
+      flags[0] = 1;
+      if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
+    }
+    __syncwarp();
+    if (elect_one()) umma_commit(&bar.last);   // no product may be in flight when the tensor memory goes
+    __syncwarp();
+    mbar_wait(&bar.last, 0);
   } else if (any && warp < 8) {   // ---- rows
     const int x = warp / 4, row = threadIdx.x % kManyTile;   // tile, its row
     const uint32_t mine = tmem + ((uint32_t)(32 * (warp % 4)) << 16);   // this warp's quarter
-    uint32_t it = 0, c = 0;   // units of the CTA; of this tile
+    uint32_t it = 0;     // units of the CTA; S lies in buffer it % 2
+    uint32_t used = 0;   // a bit an S buffer: how often this tile has used it, mod 2 (the phase of its
+                         // next s_full; its last o_done has the other)
     struct Row { int tok, hq, lo, hi; bool live; };
     const auto find = [&](const KvWalk& v) {
       const int r = v.rt * kManyRows + x * kManyTile + row;
@@ -454,11 +485,11 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     const auto tile_there = [&](const KvWalk& v) { return v.rt * kManyRows + x * kManyTile < v.T * a.group; };
     float f = 0.f;   // log2 units per unit of S
     const auto load_q = [&](const Row& y, int s0) {
-      const int64_t at = y.live ? (int64_t)(s0 + y.tok) * a.p.q_token_stride + (int64_t)y.hq * a.p.q_head_stride : -1;
+      const int64_t at = (int64_t)(s0 + y.tok) * a.p.q_token_stride + (int64_t)y.hq * a.p.q_head_stride;
       const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.p.q);
       const uint32_t to = smem_addr(smem) + F::kQ + x * F::kQBytes;
-      const float e2 = a.vec ? many_query<D, true>(qp, at, a.p.scale, to, warp % 4, lane)
-                             : many_query<D, false>(qp, at, a.p.scale, to, warp % 4, lane);
+      qp = y.live ? qp + at : nullptr;
+      const float e2 = a.vec ? many_query<D, true>(qp, a.p.scale, to, row) : many_query<D, false>(qp, a.p.scale, to, row);
       // (never 0: a masked score times it stays -inf)
       f = fmaxf(fabsf(a.p.scale) * 1.4426950408889634f * e2, 1e-37f);
       fence_proxy_async();
@@ -489,10 +520,11 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         kv_token_keys(v.T, v.n, t1, a.p.causal, a.p.window, all_lo, u0);
       }
       float m = -INFINITY, mu = 0.f, l = 0.f;
-      for (int k = v.k0; k < v.k1; ++k, ++it, ++c) {
+      for (int k = v.k0; k < v.k1; ++k, ++it) {
         const int kb = (v.span.lo + k * kManyUnit) * LW_KV_TILE;
-        const uint32_t sc = mine + F::s_col(x, c & 1);
-        if (ok) ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.s_full[x][c & 1], c >> 1 & 1u, flags));
+        const int b = it & 1;
+        const uint32_t sc = mine + F::s_col(x, b);
+        if (ok) ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.s_full[x][b], used >> b & 1u, flags));
         if (!ok) break;
         tc_fence_after();
         const uint32_t there = *reinterpret_cast<const volatile uint32_t*>(present + it % 4 * kManyUnit);
@@ -518,7 +550,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           m = mx;
           l *= al;
           if (k > v.k0) {   // once the sum over the keys before is complete
-            ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.o_done[x][(c - 1) & 1], (c - 1) >> 1 & 1u, flags));
+            ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.o_done[x][b ^ 1], (used >> (b ^ 1) & 1u) ^ 1u, flags));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -548,7 +580,8 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[x][c & 1]);
+        if (lane == 0) mbar_arrive(&bar.p_full[x][b]);
+        used ^= 1u << b;
       }
       // (every S of this item is complete: Q's place is free)
       const Row o = y;
@@ -556,7 +589,10 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         y = find(w);
         if (ok && tile_there(w)) load_q(y, q0);
       }
-      if (ok) ok = many_wait(&bar.o_done[x][(c - 1) & 1], (c - 1) >> 1 & 1u, flags);
+      {
+        const int b = (it - 1) & 1;
+        if (ok) ok = many_wait(&bar.o_done[x][b], (used >> b & 1u) ^ 1u, flags);
+      }
       ok = rows_agree(x, ok);   // all four warps go on to the barriers below, or none
       if (!ok) break;
       tc_fence_after();
@@ -653,7 +689,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tmem, F::kCols);
+  if (warp == 8 + kManyLoaders) tmem_dealloc(tmem, F::kCols);
 }
 
 }  // namespace dev
