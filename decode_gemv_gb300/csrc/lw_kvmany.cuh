@@ -5,9 +5,9 @@
 // 128; keys come 64 at a time.  S = Q K^T and O += P V are tcgen05.mma: Q, K
 // and V (fp16, restored from the codes) are operand tiles in shared memory, P
 // and the accumulators lie in tensor memory.
-//  * 7 loader warps take the 16-key tiles in turn: fetch theirs by bulk
-//    copies (a ring of their own), restore k = sc c + mn and v = sc c + mn by
-//    one rounded fp16 fma each, and store them as operand tiles (three
+//  * 7 loader warps take the 16-key tiles in turn: a bulk copy brings the next
+//    one while the last, in registers, is restored -- k = sc c + mn and v = sc c +
+//    mn by one rounded fp16 fma each -- and stored as operand tiles (four
 //    buffers), once for both row tiles;
 //  * 8 row warps, one thread per row: put Q into shared memory (each row scaled
 //    by a power of two: the fp16 range), then for every 64 keys read the row of
@@ -17,7 +17,8 @@
 //  * one warp issues the products (all of its lanes walk along, so that the
 //    descriptors are warp-uniform: an issue from divergent code took 80 cycles
 //    and bounded the kernel).  S has two buffers a tile: the next S is computed
-//    while the rows work on this one.
+//    while the rows work on this one, and the two tiles' products alternate so
+//    that none waits for the one right before it.
 // Operands of 11 bits (fp16) under outputs of 8 (bf16).
 //
 // The operand tiles are K-major core matrices of 8 x 16 bytes.  A key code
@@ -38,8 +39,7 @@ constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit
 constexpr int kManyLoaders = 7;
 constexpr int kManyThreads = 32 * (8 + kManyLoaders + 1);   // row warps, loader warps, one to issue
 constexpr int kManyPerSm = 1;
-constexpr int kManyStages = 3;                      // tiles of a loader's ring
-constexpr int kManyBufs = 3;                        // restored units
+constexpr int kManyBufs = 4;                        // restored units
 
 template <int D>
 struct Many {
@@ -53,8 +53,8 @@ struct Many {
   static constexpr int kHead = 1024;                  // barriers and flags
   static constexpr int kQ = kHead, kKv = kQ + 2 * kQBytes;   // a buffer: K, then V
   static constexpr int kKvBytes = kKBytes + kVBytes;
-  static constexpr int kRing = kKv + kManyBufs * kKvBytes;
-  static constexpr int kSmem = kRing + kManyLoaders * kManyStages * L::kBytes;
+  static constexpr int kRing = kKv + kManyBufs * kKvBytes;   // a tile as it is stored, per loader
+  static constexpr int kSmem = kRing + kManyLoaders * L::kBytes;
   static constexpr int kPartial = kManyTile * (D + 2);   // of a tile, floats: m, l, then [D / 4][rows][4]
   // tensor-memory columns: S of tile x, buffer i (and P over it); O of tile x
   __host__ __device__ static constexpr uint32_t s_col(int x, int i) { return 128 * x + 64 * i; }
@@ -190,13 +190,51 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// A loader lane's share of a 16-key tile as it is stored: keys lane / 4 and 8
+// more, elements 32 g + 8 (lane % 4) + 0..7; values of keys 8 h .. 8 h + 7
+// (h = lane / 16), groups g0 .. g0 + GW - 1, elements 32 g + 4 (lane % 8) + 0..3.
+template <int D>
+struct ManyRaw {
+  using L = KvTile<D>;
+  static constexpr int G = L::G, GW = (G + 1) / 2;
+  uint32_t kc[2][G], ks[2][G], km[2][L::GP / 2], vc[4][GW], vs[4][GW], vm[4][GW];
+
+  __device__ __forceinline__ void read(uint32_t s, int lane) {
+    const int q = lane & 3, n = lane & 7, h = lane >> 4, g0 = GW * (lane >> 3 & 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int tk = 8 * i + lane / 4;
+      lds_words<G>(s + L::kKeyCodes + ((tk * 4 + q) * G) * 4, kc[i]);
+      lds_words<G>(s + L::kKeyScale + (tk / 2 * G) * 4, ks[i]);
+      lds_words<L::GP / 2>(s + L::kKeyMin + (tk * L::GP) * 2, km[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int p = 4 * h + j;   // pair of keys
+      if constexpr (G % 2 == 0) {
+        lds_words<GW>(s + L::kValCodes + ((p * 8 + n) * G + g0) * 4, vc[j]);
+        lds_words<GW>(s + L::kValScale + (p * G + g0) * 4, vs[j]);
+        lds_words<GW>(s + L::kValMin + (p * G + g0) * 4, vm[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < GW; ++i) {
+          const int g = g0 + i < G ? g0 + i : G - 1;   // (the group past the last is not stored)
+          vc[j][i] = lds_u32(s + L::kValCodes + ((p * 8 + n) * G + g) * 4);
+          vs[j][i] = lds_u32(s + L::kValScale + (p * G + g) * 4);
+          vm[j][i] = lds_u32(s + L::kValMin + (p * G + g) * 4);
+        }
+      }
+    }
+  }
+};
+
 // Barriers of a CTA.  Those of a row tile are one per S buffer, so that the use
 // before the one waited for is always complete (a parity names one of two).
 struct ManyBars {
   uint64_t kv_full[kManyBufs], kv_free[kManyBufs];       // per operand buffer
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];   // per row tile (and S buffer)
   uint64_t last;                                         // everything issued has completed
-  uint64_t ring[kManyLoaders][kManyStages];
+  uint64_t ring[kManyLoaders];
 };
 
 template <int D>
@@ -228,8 +266,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       mbar_init(&bar.o_done[x][1], 1);
     }
     mbar_init(&bar.last, 1);
-    for (int i = 0; i < kManyLoaders; ++i)
-      for (int j = 0; j < kManyStages; ++j) mbar_init(&bar.ring[i][j], 1);
+    for (int i = 0; i < kManyLoaders; ++i) mbar_init(&bar.ring[i], 1);
     flags[0] = 0;
     fence_barrier_init();
   }
@@ -250,14 +287,15 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
 
   if (any && warp >= 8 && warp < 8 + kManyLoaders) {   // ---- loaders
     const int lw = warp - 8;
-    FewFetch<D, kManyLoaders, 1, kManyStages> t;
-    t.bars = bar.ring[lw];
-    t.ring = smem + F::kRing + lw * kManyStages * L::kBytes;
-    t.parity = t.have = 0;
-    constexpr int GW = (G + 1) / 2;   // groups of a lane
+    constexpr int GW = ManyRaw<D>::GW;
     uint32_t it0 = 0;                 // units before this item
+    FewFetch<D, kManyLoaders, 1, 1> t;
+    t.bars = &bar.ring[lw];
+    t.ring = smem + F::kRing + lw * L::kBytes;
+    t.parity = t.have = 0;
     for (bool more = true; more && ok;) {
-      t.begin(a, w, w.span.lo + w.k0 * kManyUnit + lw, w.span.lo + w.k1 * kManyUnit, lane);
+      const int base = w.span.lo + w.k0 * kManyUnit, count = (w.k1 - w.k0) * kManyUnit;
+      t.begin(a, w, base + lw, base + count, lane);
       // rows of the item all see the keys [all_lo, all_hi)
       int all_lo, all_hi, x;
       {
@@ -266,67 +304,51 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         kv_token_keys(w.T, w.n, w.rt * kManyRows / a.group, a.p.causal, a.p.window, x, all_hi);
         kv_token_keys(w.T, w.n, t1, a.p.causal, a.p.window, all_lo, x);
       }
-      const int count = (w.k1 - w.k0) * kManyUnit;   // (the last unit's tiles may lie past the end)
-      for (int o = lw; o < count; o += kManyLoaders) {
-        const int tile = w.span.lo + w.k0 * kManyUnit + o, sub = o % kManyUnit;
+      for (int o = lw; o < count; o += kManyLoaders) {   // (the last unit may run past the span)
+        const int sub = o % kManyUnit;
         const uint32_t it = it0 + o / kManyUnit, buf = it % kManyBufs, phase = it / kManyBufs & 1u;
-        const bool there = tile < w.span.hi && (t.have >> t.out & 1u);
-        if (there && !t.wait()) { ok = false; mbar_wait(&t.bars[t.out], (t.parity >> t.out & 1u) ^ 1u); break; }
-        const uint32_t s = smem_addr(t.ring) + t.out * L::kBytes;
-        const int kb = tile * LW_KV_TILE;
+        const bool there = t.have & 1u;
+        const int kb = (base + o) * LW_KV_TILE;
         const bool edge = kb < all_lo || kb + LW_KV_TILE > all_hi;
-        // the codes, scales and minimums of this lane: keys lane / 4 and 8 more, elements
-        // 32 g + 8 q + 0..7; values of keys 8 h .. 8 h + 7, groups g0 .. g0 + GW - 1
         const int q = lane & 3, n = lane & 7, h = lane >> 4, g0 = GW * (lane >> 3 & 1);
-        uint32_t kc[2][G], ks[2][G], km[2][L::GP / 2], vc[4][GW], vs[4][GW], vm[4][GW];
+        ManyRaw<D> r;
         if (there) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int tk = 8 * i + lane / 4;
-            lds_words<G>(s + L::kKeyCodes + (uint32_t)((tk * 4 + q) * G) * 4, kc[i]);
-            lds_words<G>(s + L::kKeyScale + (uint32_t)(tk / 2 * G) * 4, ks[i]);
-            lds_words<L::GP / 2>(s + L::kKeyMin + (uint32_t)(tk * L::GP) * 2, km[i]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int p = 4 * h + j;   // pair of keys
-            if constexpr (G % 2 == 0) {
-              lds_words<GW>(s + L::kValCodes + (uint32_t)((p * 8 + n) * G + g0) * 4, vc[j]);
-              lds_words<GW>(s + L::kValScale + (uint32_t)(p * G + g0) * 4, vs[j]);
-              lds_words<GW>(s + L::kValMin + (uint32_t)(p * G + g0) * 4, vm[j]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < GW; ++i) {
-                const int g = g0 + i < G ? g0 + i : G - 1;   // (the group past the last is not stored)
-                vc[j][i] = lds_u32(s + L::kValCodes + (uint32_t)((p * 8 + n) * G + g) * 4);
-                vs[j][i] = lds_u32(s + L::kValScale + (uint32_t)(p * G + g) * 4);
-                vm[j][i] = lds_u32(s + L::kValMin + (uint32_t)(p * G + g) * 4);
-              }
-            }
-          }
+          if (!t.wait()) { ok = false; mbar_wait(t.bars, (t.parity & 1u) ^ 1u); break; }
+          r.read(smem_addr(t.ring), lane);
+          fence_proxy_async();   // (these reads before the copy that follows)
+          __syncwarp();
+        }
+        if (base + o < w.span.hi) t.send(a, lane);
+        if (there) {
           if (edge) {
             // rows that do not see a key must not get its NaN through V (0 x NaN): let it come by S
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int tk = 8 * i + lane / 4;
+              // (a lane with the value scales of the key's pair: half tk / 8 of the warp, either group half)
               bool nan = false;
+              const uint32_t odd = tk & 1 ? 16 : 0;
 #pragma unroll
-              for (int g = 0; g < G; ++g) {
-                const uint32_t z = lds_u16(s + L::kValScale + (uint32_t)((tk / 2 * G + g) * 2 + tk % 2) * 2);
-                nan |= (z & 0x7FFFu) > 0x7C00u;
-              }
-              if (nan) ks[i][0] = 0x7FFF7FFFu;
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int g = 0; g < GW; ++g)
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    const uint32_t z = __shfl_sync(0xFFFFFFFFu, r.vs[j][g], 16 * i + 8 * u);
+                    nan |= tk / 2 % 4 == j && (z >> odd & 0x7FFFu) > 0x7C00u;
+                  }
+              if (nan) r.ks[i][0] = 0x7FFF7FFFu;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int key = kb + 2 * (4 * h + j);
 #pragma unroll
               for (int i = 0; i < GW; ++i) {
-                const uint32_t z = vs[j][i];
+                const uint32_t z = r.vs[j][i];
                 const uint32_t keep = (key < w.n && (z & 0x7FFFu) <= 0x7C00u ? 0xFFFFu : 0u) |
                                       (key + 1 < w.n && (z & 0x7FFF0000u) <= 0x7C000000u ? 0xFFFF0000u : 0u);
-                vs[j][i] &= keep;
-                vm[j][i] &= keep;
+                r.vs[j][i] &= keep;
+                r.vm[j][i] &= keep;
               }
             }
           }
@@ -334,7 +356,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < GW; ++i) vc[j][i] = vs[j][i] = vm[j][i] = 0;
+            for (int i = 0; i < GW; ++i) r.vc[j][i] = r.vs[j][i] = r.vm[j][i] = 0;
         }
         if (!__all_sync(0xFFFFFFFFu, many_wait(&bar.kv_free[buf], phase ^ 1u, flags))) { ok = false; break; }
         const uint32_t kto = smem_addr(smem) + F::kKv + buf * F::kKvBytes + (uint32_t)(sub * 256 + (lane / 4) * 16 + q * F::kKLbo);
@@ -346,9 +368,9 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              const uint32_t sc = __byte_perm(ks[i][g], 0, half);
-              const uint32_t mn = __byte_perm(km[i][g / 2], 0, g % 2 ? 0x3232u : 0x1010u);
-              const uint32_t w0 = kc[i][g], w1 = kc[i][g] >> 8;
+              const uint32_t sc = __byte_perm(r.ks[i][g], 0, half);
+              const uint32_t mn = __byte_perm(r.km[i][g / 2], 0, g % 2 ? 0x3232u : 0x1010u);
+              const uint32_t w0 = r.kc[i][g], w1 = r.kc[i][g] >> 8;
               sts_u4(kto + (uint32_t)(i * 128 + 4 * g * F::kKLbo), fma_h2(whole_even(w0), sc, mn),
                      fma_h2(whole_odd(w0), sc, mn), fma_h2(whole_even(w1), sc, mn), fma_h2(whole_odd(w1), sc, mn));
             }
@@ -361,8 +383,8 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
             uint32_t e[4], o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              e[j] = fma_h2(whole_even(vc[j][i] >> (8 * st)), vs[j][i], vm[j][i]);
-              o[j] = fma_h2(whole_odd(vc[j][i] >> (8 * st)), vs[j][i], vm[j][i]);
+              e[j] = fma_h2(whole_even(r.vc[j][i] >> (8 * st)), r.vs[j][i], r.vm[j][i]);
+              o[j] = fma_h2(whole_odd(r.vc[j][i] >> (8 * st)), r.vs[j][i], r.vm[j][i]);
             }
             sts_u4(vto + (uint32_t)(i * 512 + (2 * st) * 128), e[0], e[1], e[2], e[3]);
             sts_u4(vto + (uint32_t)(i * 512 + (2 * st + 1) * 128), o[0], o[1], o[2], o[3]);
@@ -372,10 +394,6 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.kv_full[buf]);
-        if (tile < w.span.hi) {
-          t.out = t.out + 1 == kManyStages ? 0 : t.out + 1;
-          t.send(a, lane);
-        }
       }
       it0 += w.k1 - w.k0;
       if (ok) more = kv_advance<kManyRows, kManyUnit>(a, w, q0);
@@ -383,8 +401,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     if (!ok) {
       flags[0] = 1;
       if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
-      for (int i = 0; i < kManyStages; ++i)   // no copy may be in flight when the CTA ends
-        if (t.have >> i & 1u) mbar_wait(&t.bars[i], t.parity >> i & 1u);
+      if (t.have & 1u) mbar_wait(t.bars, t.parity & 1u);   // no copy may be in flight when the CTA ends
     }
   } else if (any && warp == 8 + kManyLoaders) {   // ---- issuer
     const uint32_t base = smem_addr(smem);
@@ -393,69 +410,70 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     };
     const auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
     const uint32_t tm = uniform(tmem);
-    // this unit and the one whose S is next: operand buffers and their phases; S buffers
-    int buf = 0, nbuf = 0, sbuf = 0, nsbuf = 0;
-    uint32_t nphase = 0;
-    uint32_t qph = 0, pph[2] = {0, 0}, oph[2] = {0, 0};   // phases of q_full (bit a tile), p_full and o_done (bit an S buffer)
-    uint32_t used[2] = {0, 0};                            // S buffers that have held a P
+    int buf = 0, sbuf = 0;   // operand and S buffer of the item's first unit
+    uint32_t kvph = 0, qph = 0;             // phases of kv_full (a bit a buffer) and q_full (a bit a tile)
+    uint32_t pph = 0, oph = 0, used = 0;    // of p_full and o_done, and whether the place has held a P (bit 2 x + buffer)
     for (bool more = true; more && ok;) {
       const int tiles = uniform((w.T * a.group - w.rt * kManyRows) > kManyTile ? 2 : 1);
       const int n = uniform(w.k1 - w.k0);
-      const auto next_s = [&](bool first) {   // S of the next unit, over the P of two units before
-        if (!wait(&bar.kv_full[nbuf], nphase, flags)) return false;
-        const uint64_t kd = sdesc(base + F::kKv + nbuf * F::kKvBytes, F::kKLbo, 128);
-#pragma unroll 1
-        for (int x = 0; x < tiles; ++x) {
-          if (first) {
-            if (!wait(&bar.q_full[x], qph >> x & 1u, flags)) return false;
-            qph ^= 1u << x;
-          }
-          if (used[x] >> nsbuf & 1u) {
-            if (!wait(&bar.o_done[x][nsbuf], oph[x] >> nsbuf & 1u, flags)) return false;
-            oph[x] ^= 1u << nsbuf;
-          }
-          used[x] |= 1u << nsbuf;
-          tc_fence_after();
-          const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
-          const uint32_t d = tm + F::s_col(x, nsbuf);
-          if (elect_one()) {
+      // S of tile x for the item's i-th unit, over the P of two units before
+      const auto issue_s = [&](int x, int i) {
+        const int kv = (buf + i) % kManyBufs, sb = (sbuf + i) & 1;
+        if (x == 0) {
+          if (!wait(&bar.kv_full[kv], kvph >> kv & 1u, flags)) return false;
+          kvph ^= 1u << kv;
+        }
+        if (i == 0) {
+          if (!wait(&bar.q_full[x], qph >> x & 1u, flags)) return false;
+          qph ^= 1u << x;
+        }
+        const uint32_t bit = 1u << (2 * x + sb);
+        if (used & bit) {
+          if (!wait(&bar.o_done[x][sb], (oph & bit) != 0, flags)) return false;
+          oph ^= bit;
+        }
+        used |= bit;
+        tc_fence_after();
+        const uint64_t kd = sdesc(base + F::kKv + kv * F::kKvBytes, F::kKLbo, 128);
+        const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
+        const uint32_t d = tm + F::s_col(x, sb);
+        if (elect_one()) {
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              umma_bf16(d, qd + (2 * s * F::kQLbo >> 4), kd + (2 * s * F::kKLbo >> 4), idesc_f16(kManyKeys), s > 0);
-            umma_commit(&bar.s_full[x][nsbuf]);
-          }
-          __syncwarp();
+          for (int s = 0; s < D / 16; ++s)
+            umma_bf16(d, qd + (2 * s * F::kQLbo >> 4), kd + (2 * s * F::kKLbo >> 4), idesc_f16(kManyKeys), s > 0);
+          umma_commit(&bar.s_full[x][sb]);
         }
-        nsbuf ^= 1;
-        if (++nbuf == kManyBufs) {
-          nbuf = 0;
-          nphase ^= 1u;
-        }
+        __syncwarp();
         return true;
       };
-      ok = next_s(true);
+      const auto issue_o = [&](int x, int i) {   // O += P V
+        const int kv = (buf + i) % kManyBufs, sb = (sbuf + i) & 1;
+        const uint32_t bit = 1u << (2 * x + sb);
+        if (!wait(&bar.p_full[x][sb], (pph & bit) != 0, flags)) return false;
+        pph ^= bit;
+        tc_fence_after();
+        const uint64_t vd = sdesc(base + F::kKv + kv * F::kKvBytes + F::kKBytes, F::kVLbo, 128);
+        const uint32_t d = tm + F::o_col(x), p = tm + F::s_col(x, sb);
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < kManyKeys / 16; ++s)
+            umma_bf16_ta(d, p + 8 * s, vd + (2 * s * F::kVLbo >> 4), idesc_f16(D), i > 0 || s > 0);
+          umma_commit(&bar.o_done[x][sb]);
+          if (x == tiles - 1) umma_commit(&bar.kv_free[kv]);
+        }
+        __syncwarp();
+        return true;
+      };
+      // tile 0 is one S ahead of tile 1
+      const bool two = tiles == 2;
+      ok = issue_s(0, 0) && (!two || issue_s(1, 0)) && (n == 1 || issue_s(0, 1));
 #pragma unroll 1
       for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n && !next_s(false)) { ok = false; break; }
-        const uint64_t vd = sdesc(base + F::kKv + buf * F::kKvBytes + F::kKBytes, F::kVLbo, 128);
-#pragma unroll 1
-        for (int x = 0; x < tiles; ++x) {
-          if (!wait(&bar.p_full[x][sbuf], pph[x] >> sbuf & 1u, flags)) { ok = false; break; }
-          pph[x] ^= 1u << sbuf;
-          tc_fence_after();
-          const uint32_t d = tm + F::o_col(x), p = tm + F::s_col(x, sbuf);
-          if (elect_one()) {
-#pragma unroll
-            for (int s = 0; s < kManyKeys / 16; ++s)
-              umma_bf16_ta(d, p + 8 * s, vd + (2 * s * F::kVLbo >> 4), idesc_f16(D), i > 0 || s > 0);
-            umma_commit(&bar.o_done[x][sbuf]);
-            if (x == tiles - 1) umma_commit(&bar.kv_free[buf]);
-          }
-          __syncwarp();
-        }
-        sbuf ^= 1;
-        if (++buf == kManyBufs) buf = 0;
+        ok = issue_o(0, i) && (!two || ((i + 1 == n || issue_s(1, i + 1)) && issue_o(1, i))) &&
+             (i + 2 >= n || issue_s(0, i + 2));
       }
+      buf = (buf + n) % kManyBufs;
+      sbuf = (sbuf + n) & 1;
       if (ok) more = uniform(kv_advance<kManyRows, kManyUnit>(a, w, q0));
     }
     if (!ok) {
