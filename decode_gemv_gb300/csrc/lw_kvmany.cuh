@@ -5,8 +5,8 @@
 // 128; keys come 64 at a time.  S = Q K^T and O += P V are tcgen05.mma: Q, K
 // and V (fp16, restored from the codes) are operand tiles in shared memory, P
 // and the accumulators lie in tensor memory.
-//  * 7 loader warps take the 16-key tiles in turn: a bulk copy brings the next
-//    one while the last, in registers, is restored -- k = sc c + mn and v = sc c +
+//  * 6 loader warps take the 16-key tiles in turn: bulk copies bring the next
+//    ones while the last, in registers, is restored -- k = sc c + mn and v = sc c +
 //    mn by one rounded fp16 fma each -- and stored as operand tiles (four
 //    buffers), once for both row tiles;
 //  * 8 row warps, one thread per row: put Q into shared memory (each row scaled
@@ -14,11 +14,12 @@
 //    S, take p = 2^(s - m), store it as fp16 over S, and add the row's sum.  m
 //    is raised, and O rescaled, only where a score passes it by 2^8 (p stays
 //    below 2^8, in fp16 range and precision);
-//  * one warp issues the products (all of its lanes walk along, so that the
-//    descriptors are warp-uniform: an issue from divergent code took 80 cycles
-//    and bounded the kernel).  S has two buffers a tile: the next S is computed
-//    while the rows work on this one, and the two tiles' products alternate so
-//    that none waits for the one right before it.
+//  * 2 warps issue the products, one per row tile: the queue of products is
+//    short (an issue takes as long as the product before it), so that while one
+//    waits for its rows the other keeps the tensor cores at work.  All lanes
+//    walk along and one is elected to issue (descriptors are warp-uniform then:
+//    from divergent code an issue took 80 cycles, more than its product).  S has
+//    two buffers a tile: the next S is computed while the rows work on this one.
 // Operands of 11 bits (fp16) under outputs of 8 (bf16).
 //
 // The operand tiles are K-major core matrices of 8 x 16 bytes.  A key code
@@ -36,8 +37,9 @@ namespace lw {
 
 constexpr int kManyTile = 128, kManyRows = 2 * kManyTile, kManyKeys = 64;
 constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit
-constexpr int kManyLoaders = 7;
-constexpr int kManyThreads = 32 * (8 + kManyLoaders + 1);   // row warps, loader warps, one to issue
+constexpr int kManyLoaders = 6;
+constexpr int kManyStages = 2;                      // places of a loader's ring
+constexpr int kManyThreads = 32 * (8 + kManyLoaders + 2);   // row warps, loader warps, issuers
 constexpr int kManyPerSm = 1;
 constexpr int kManyBufs = 4;                        // restored units
 
@@ -53,8 +55,8 @@ struct Many {
   static constexpr int kHead = 1024;                  // barriers and flags
   static constexpr int kQ = kHead, kKv = kQ + 2 * kQBytes;   // a buffer: K, then V
   static constexpr int kKvBytes = kKBytes + kVBytes;
-  static constexpr int kRing = kKv + kManyBufs * kKvBytes;   // a tile as it is stored, per loader
-  static constexpr int kSmem = kRing + kManyLoaders * L::kBytes;
+  static constexpr int kRing = kKv + kManyBufs * kKvBytes;   // tiles as they are stored
+  static constexpr int kSmem = kRing + kManyLoaders * kManyStages * L::kBytes;
   static constexpr int kPartial = kManyTile * (D + 2);   // of a tile, floats: m, l, then [D / 4][rows][4]
   // tensor-memory columns: S of tile x, buffer i (and P over it); O of tile x
   __host__ __device__ static constexpr uint32_t s_col(int x, int i) { return 128 * x + 64 * i; }
@@ -117,7 +119,7 @@ __device__ __forceinline__ bool many_wait(uint64_t* bar, uint32_t parity, volati
         : "memory");
     return ok != 0;
   };
-  if (passed()) return true;
+  if (mbar_try_wait(bar, parity)) return true;   // (the form without a time is the faster)
   const long long t0 = clock64();
   for (;;) {
     if (passed()) return true;
@@ -233,8 +235,8 @@ struct ManyRaw {
 struct ManyBars {
   uint64_t kv_full[kManyBufs], kv_free[kManyBufs];       // per operand buffer
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];   // per row tile (and S buffer)
-  uint64_t last;                                         // everything issued has completed
-  uint64_t ring[kManyLoaders];
+  uint64_t last[2];                                      // everything issued has completed
+  uint64_t ring[kManyLoaders][kManyStages];
 };
 
 template <int D>
@@ -254,9 +256,10 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   if (threadIdx.x == 0) {
     for (int i = 0; i < kManyBufs; ++i) {
       mbar_init(&bar.kv_full[i], kManyUnit);
-      mbar_init(&bar.kv_free[i], 1);
+      mbar_init(&bar.kv_free[i], 2);   // both tiles' products
     }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&bar.last[x], 1);
       mbar_init(&bar.q_full[x], 4);
       mbar_init(&bar.s_full[x][0], 1);
       mbar_init(&bar.s_full[x][1], 1);
@@ -265,8 +268,8 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       mbar_init(&bar.o_done[x][0], 1);
       mbar_init(&bar.o_done[x][1], 1);
     }
-    mbar_init(&bar.last, 1);
-    for (int i = 0; i < kManyLoaders; ++i) mbar_init(&bar.ring[i], 1);
+    for (int i = 0; i < kManyLoaders; ++i)
+      for (int j = 0; j < kManyStages; ++j) mbar_init(&bar.ring[i][j], 1);
     flags[0] = 0;
     fence_barrier_init();
   }
@@ -289,9 +292,9 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     const int lw = warp - 8;
     constexpr int GW = ManyRaw<D>::GW;
     uint32_t it0 = 0;                 // units before this item
-    FewFetch<D, kManyLoaders, 1, 1> t;
-    t.bars = &bar.ring[lw];
-    t.ring = smem + F::kRing + lw * L::kBytes;
+    FewFetch<D, kManyLoaders, 1, kManyStages> t;
+    t.bars = bar.ring[lw];
+    t.ring = smem + F::kRing + lw * kManyStages * L::kBytes;
     t.parity = t.have = 0;
     for (bool more = true; more && ok;) {
       const int base = w.span.lo + w.k0 * kManyUnit, count = (w.k1 - w.k0) * kManyUnit;
@@ -307,18 +310,21 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       for (int o = lw; o < count; o += kManyLoaders) {   // (the last unit may run past the span)
         const int sub = o % kManyUnit;
         const uint32_t it = it0 + o / kManyUnit, buf = it % kManyBufs, phase = it / kManyBufs & 1u;
-        const bool there = t.have & 1u;
+        const bool there = t.have >> t.out & 1u;
         const int kb = (base + o) * LW_KV_TILE;
         const bool edge = kb < all_lo || kb + LW_KV_TILE > all_hi;
         const int q = lane & 3, n = lane & 7, h = lane >> 4, g0 = GW * (lane >> 3 & 1);
         ManyRaw<D> r;
         if (there) {
-          if (!t.wait()) { ok = false; mbar_wait(t.bars, (t.parity & 1u) ^ 1u); break; }
-          r.read(smem_addr(t.ring), lane);
+          if (!t.wait()) { ok = false; mbar_wait(&t.bars[t.out], (t.parity >> t.out & 1u) ^ 1u); break; }
+          r.read(smem_addr(t.ring) + t.out * L::kBytes, lane);
           fence_proxy_async();   // (these reads before the copy that follows)
           __syncwarp();
         }
-        if (base + o < w.span.hi) t.send(a, lane);
+        if (base + o < w.span.hi) {
+          t.out = t.out + 1 == kManyStages ? 0 : t.out + 1;
+          t.send(a, lane);
+        }
         if (there) {
           if (edge) {
             // rows that do not see a key must not get its NaN through V (0 x NaN): let it come by S
@@ -401,41 +407,37 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     if (!ok) {
       flags[0] = 1;
       if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
-      if (t.have & 1u) mbar_wait(t.bars, t.parity & 1u);   // no copy may be in flight when the CTA ends
+      for (int i = 0; i < kManyStages; ++i)   // no copy may be in flight when the CTA ends
+        if (t.have >> i & 1u) mbar_wait(&t.bars[i], t.parity >> i & 1u);
     }
-  } else if (any && warp == 8 + kManyLoaders) {   // ---- issuer
-    const uint32_t base = smem_addr(smem);
-    const auto wait = [&](uint64_t* b, uint32_t parity, volatile uint32_t* f) {
-      return __all_sync(0xFFFFFFFFu, many_wait(b, parity, f)) != 0;
-    };
+  } else if (any && warp >= 8 + kManyLoaders) {   // ---- issuers
     const auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-    const uint32_t tm = uniform(tmem);
+    const auto wait = [&](uint64_t* b, bool parity) { return __all_sync(0xFFFFFFFFu, many_wait(b, parity, flags)) != 0; };
+    const int x = uniform(warp - 8 - kManyLoaders);   // row tile
+    const uint32_t tm = uniform(tmem), base = smem_addr(smem);
+    const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
     int buf = 0, sbuf = 0;   // operand and S buffer of the item's first unit
-    uint32_t kvph = 0, qph = 0;             // phases of kv_full (a bit a buffer) and q_full (a bit a tile)
-    uint32_t pph = 0, oph = 0, used = 0;    // of p_full and o_done, and whether the place has held a P (bit 2 x + buffer)
+    uint32_t kvph = 0, qph = 0;             // phases of kv_full (a bit a buffer) and q_full
+    uint32_t pph = 0, oph = 0, used = 0;    // of p_full and o_done, and whether the place has held a P (a bit an S buffer)
     for (bool more = true; more && ok;) {
-      const int tiles = uniform((w.T * a.group - w.rt * kManyRows) > kManyTile ? 2 : 1);
+      const bool mine = uniform(w.T * a.group - w.rt * kManyRows > x * kManyTile);
       const int n = uniform(w.k1 - w.k0);
-      // S of tile x for the item's i-th unit, over the P of two units before
-      const auto issue_s = [&](int x, int i) {
+      // S for the item's i-th unit, over the P of two units before
+      const auto issue_s = [&](int i) {
         const int kv = (buf + i) % kManyBufs, sb = (sbuf + i) & 1;
-        if (x == 0) {
-          if (!wait(&bar.kv_full[kv], kvph >> kv & 1u, flags)) return false;
-          kvph ^= 1u << kv;
-        }
+        if (!wait(&bar.kv_full[kv], kvph >> kv & 1u)) return false;
+        kvph ^= 1u << kv;
         if (i == 0) {
-          if (!wait(&bar.q_full[x], qph >> x & 1u, flags)) return false;
-          qph ^= 1u << x;
+          if (!wait(&bar.q_full[x], qph)) return false;
+          qph ^= 1u;
         }
-        const uint32_t bit = 1u << (2 * x + sb);
-        if (used & bit) {
-          if (!wait(&bar.o_done[x][sb], (oph & bit) != 0, flags)) return false;
-          oph ^= bit;
+        if (used >> sb & 1u) {
+          if (!wait(&bar.o_done[x][sb], oph >> sb & 1u)) return false;
+          oph ^= 1u << sb;
         }
-        used |= bit;
+        used |= 1u << sb;
         tc_fence_after();
         const uint64_t kd = sdesc(base + F::kKv + kv * F::kKvBytes, F::kKLbo, 128);
-        const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
         const uint32_t d = tm + F::s_col(x, sb);
         if (elect_one()) {
 #pragma unroll
@@ -446,11 +448,10 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         __syncwarp();
         return true;
       };
-      const auto issue_o = [&](int x, int i) {   // O += P V
+      const auto issue_o = [&](int i) {   // O += P V
         const int kv = (buf + i) % kManyBufs, sb = (sbuf + i) & 1;
-        const uint32_t bit = 1u << (2 * x + sb);
-        if (!wait(&bar.p_full[x][sb], (pph & bit) != 0, flags)) return false;
-        pph ^= bit;
+        if (!wait(&bar.p_full[x][sb], pph >> sb & 1u)) return false;
+        pph ^= 1u << sb;
         tc_fence_after();
         const uint64_t vd = sdesc(base + F::kKv + kv * F::kKvBytes + F::kKBytes, F::kVLbo, 128);
         const uint32_t d = tm + F::o_col(x), p = tm + F::s_col(x, sb);
@@ -459,18 +460,24 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           for (int s = 0; s < kManyKeys / 16; ++s)
             umma_bf16_ta(d, p + 8 * s, vd + (2 * s * F::kVLbo >> 4), idesc_f16(D), i > 0 || s > 0);
           umma_commit(&bar.o_done[x][sb]);
-          if (x == tiles - 1) umma_commit(&bar.kv_free[kv]);
+          umma_commit(&bar.kv_free[kv]);
         }
         __syncwarp();
         return true;
       };
-      // tile 0 is one S ahead of tile 1
-      const bool two = tiles == 2;
-      ok = issue_s(0, 0) && (!two || issue_s(1, 0)) && (n == 1 || issue_s(0, 1));
+      if (mine) {
+        ok = issue_s(0) && (n == 1 || issue_s(1));
 #pragma unroll 1
-      for (int i = 0; ok && i < n; ++i) {
-        ok = issue_o(0, i) && (!two || ((i + 1 == n || issue_s(1, i + 1)) && issue_o(1, i))) &&
-             (i + 2 >= n || issue_s(0, i + 2));
+        for (int i = 0; ok && i < n; ++i) ok = issue_o(i) && (i + 2 >= n || issue_s(i + 2));
+      } else {   // no rows here: only let the buffers go
+#pragma unroll 1
+        for (int i = 0; ok && i < n; ++i) {
+          const int kv = (buf + i) % kManyBufs;
+          ok = wait(&bar.kv_full[kv], kvph >> kv & 1u);
+          kvph ^= 1u << kv;
+          if (lane == 0) mbar_arrive(&bar.kv_free[kv]);
+          __syncwarp();
+        }
       }
       buf = (buf + n) % kManyBufs;
       sbuf = (sbuf + n) & 1;
@@ -481,9 +488,9 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
     }
     __syncwarp();
-    if (elect_one()) umma_commit(&bar.last);   // no product may be in flight when the tensor memory goes
+    if (elect_one()) umma_commit(&bar.last[x]);   // no product may be in flight when the tensor memory goes
     __syncwarp();
-    mbar_wait(&bar.last, 0);
+    mbar_wait(&bar.last[x], 0);
   } else if (any && warp < 8) {   // ---- rows
     const int x = warp / 4, row = threadIdx.x % kManyTile;   // tile, its row
     const uint32_t mine = tmem + ((uint32_t)(32 * (warp % 4)) << 16);   // this warp's quarter
