@@ -17,7 +17,8 @@ Variant variant(int mode) {
   if (mode == 0) return {dev::kv_few_kernel<D, 0>, kFewThreads, kFewPerSm, Few<D, 0>::kSmem};
   if (mode == 1) return {dev::kv_few_kernel<D, 1>, kFewThreads, kFewPerSm, Few<D, 1>::kSmem};
   if (mode == 2) return {dev::kv_few_kernel<D, 2>, kFewThreads, kFewPerSm, Few<D, 2>::kSmem};
-  return {dev::kv_many_kernel<D>, kManyThreads, kManyPerSm, Many<D>::kSmem};
+  if (mode == 3) return {dev::kv_many_kernel<D, false>, kManyThreads, kManyPerSm, Many<D, false>::kSmem};
+  return {dev::kv_many_kernel<D, true>, kManyThreads, kManyPerSm, Many<D, true>::kSmem};
 }
 
 // The workspace: counters and partial results of the most resident CTAs of a
@@ -49,7 +50,7 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* w
           kv_rows_aligned(p->out, p->out_token_stride, p->out_head_stride, p->dtype);
   a.status = status;
   const long long rows = (long long)p->max_q * a.group;
-  const int mode = p->dtype != LW_BF16 ? 0 : (rows > 16 ? 3 : rows > 8 ? 1 : 2);
+  const int mode = p->dtype != LW_BF16 ? (rows > 16 ? 4 : 0) : (rows > 16 ? 3 : rows > 8 ? 1 : 2);
   const Variant v = c->head_dim == 64 ? variant<64>(mode) : c->head_dim == 96 ? variant<96>(mode) : variant<128>(mode);
   if (resident_blocks(reinterpret_cast<const void*>(v.kernel), v.threads, v.smem) < 1)
     return fail(LW_ERR_CUDA, "lw_kv_attention: the kernel does not fit this device");

@@ -20,7 +20,12 @@
 //    walk along and one is elected to issue (descriptors are warp-uniform then:
 //    from divergent code an issue took 80 cycles, more than its product).  S has
 //    two buffers a tile: the next S is computed while the rows work on this one.
-// Operands of 11 bits (fp16) under outputs of 8 (bf16).
+// That is for bf16 calls: operands of 11 bits (fp16) under outputs of 8.
+//
+// WIDE (fp16 and fp32 calls): every operand is two fp16 parts, x = hi + lo 2^-11,
+// an item is one tile of 128 rows, and what the second tile had holds the lo
+// parts: S = Qh Kh + 2^-11 (Qh Kl + Ql Kh), O likewise from P and V, the two sums
+// in accumulators of their own (issuer 0 the first, issuer 1 the second).
 //
 // The operand tiles are K-major core matrices of 8 x 16 bytes.  A key code
 // word holds 8 elements of one key: its fp16 pairs are elements (0,4), (1,5),
@@ -30,22 +35,25 @@
 // then store 128 consecutive bytes).
 #pragma once
 
+#include <type_traits>
+
 #include "lw_btc.cuh"
 #include "lw_kvfew.cuh"
 
 namespace lw {
 
-constexpr int kManyTile = 128, kManyRows = 2 * kManyTile, kManyKeys = 64;
+constexpr int kManyTile = 128, kManyKeys = 64;
 constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit
 constexpr int kManyLoaders = 6;
 constexpr int kManyStages = 2;                      // places of a loader's ring
 constexpr int kManyThreads = 32 * (8 + kManyLoaders + 2);   // row warps, loader warps, issuers
 constexpr int kManyPerSm = 1;
-constexpr int kManyBufs = 4;                        // restored units
 
-template <int D>
+template <int D, bool WIDE>
 struct Many {
   using L = KvTile<D>;
+  static constexpr int kRows = WIDE ? kManyTile : 2 * kManyTile;   // of an item
+  static constexpr int kBufs = WIDE ? 2 : 4;                       // restored units
   static constexpr int kQLbo = kManyTile * 16 + 16;   // bytes between 8-element columns (16, 32: bank offset)
   static constexpr int kQBytes = D / 8 * kQLbo;
   static constexpr int kKLbo = kManyKeys * 16 + 32;
@@ -53,12 +61,14 @@ struct Many {
   static constexpr int kVLbo = D * 16;                // bytes between 8-key columns
   static constexpr int kVBytes = kManyKeys / 8 * kVLbo;
   static constexpr int kHead = 1024;                  // barriers and flags
-  static constexpr int kQ = kHead, kKv = kQ + 2 * kQBytes;   // a buffer: K, then V
+  static constexpr int kQ = kHead, kKv = kQ + 2 * kQBytes;   // a buffer: K, V (WIDE: and their lo parts)
   static constexpr int kKvBytes = kKBytes + kVBytes;
-  static constexpr int kRing = kKv + kManyBufs * kKvBytes;   // tiles as they are stored
+  static constexpr int kBufBytes = WIDE ? 2 * kKvBytes : kKvBytes;
+  static constexpr int kRing = kKv + kBufs * kBufBytes;   // tiles as they are stored
   static constexpr int kSmem = kRing + kManyLoaders * kManyStages * L::kBytes;
   static constexpr int kPartial = kManyTile * (D + 2);   // of a tile, floats: m, l, then [D / 4][rows][4]
-  // tensor-memory columns: S of tile x, buffer i (and P over it); O of tile x
+  // tensor-memory columns: S of tile x, buffer i (and P over it); O of tile x (WIDE: of part x; both parts
+  // of P over the first S)
   __host__ __device__ static constexpr uint32_t s_col(int x, int i) { return 128 * x + 64 * i; }
   __host__ __device__ static constexpr uint32_t o_col(int x) { return 256 + D * x; }
   static constexpr uint32_t kCols = 512;
@@ -179,10 +189,52 @@ __device__ __forceinline__ float many_query(const __nv_bfloat16* p, float scale,
       y[2 * i] = __uint_as_float(w[4 * o + i] << 16) * down;
       y[2 * i + 1] = __uint_as_float(w[4 * o + i] & 0xFFFF0000u) * down;
     }
-    sts_u4(to + o * Many<D>::kQLbo, h2bits(__floats2half2_rn(y[0], y[4])), h2bits(__floats2half2_rn(y[1], y[5])),
+    sts_u4(to + o * Many<D, false>::kQLbo, h2bits(__floats2half2_rn(y[0], y[4])), h2bits(__floats2half2_rn(y[1], y[5])),
            h2bits(__floats2half2_rn(y[2], y[6])), h2bits(__floats2half2_rn(y[3], y[7])));
   }
   return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// The same in two parts: lo 2^11 goes to the tile at `to_lo`.  The row is read
+// twice, the second time from the cache.
+template <int D, class T, bool VEC>
+__device__ __forceinline__ float many_query_wide(const T* p, float scale, uint32_t to, uint32_t to_lo, int row) {
+  float top = 0.f;
+  float y[8];
+#pragma unroll 4
+  for (int o = 0; o < D / 8; ++o)
+    if (p) {
+      kv_load8<T, VEC>(p + 8 * o, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
+    }
+  int e = (int)(__float_as_uint(top) >> 23) - 127;
+  e = e < -100 ? -100 : (e > 126 ? 126 : e);
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23 | (__float_as_uint(scale) & 0x80000000u));
+  const uint32_t at = (uint32_t)((row / 8) * 128 + (row % 8) * 16);
+#pragma unroll 4
+  for (int o = 0; o < D / 8; ++o) {
+    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+    if (p) {
+      kv_load8<T, VEC>(p + 8 * o, y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) split2<2048>(y[i] * down, y[i + 4] * down, hi[i], lo[i]);
+    }
+    sts_u4(to + at + o * Many<D, true>::kQLbo, hi[0], hi[1], hi[2], hi[3]);
+    sts_u4(to_lo + at + o * Many<D, true>::kQLbo, lo[0], lo[1], lo[2], lo[3]);
+  }
+  return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
+// sc c + mn of a pair of codes, as one rounded fp16 pair or as two parts
+template <bool WIDE>
+__device__ __forceinline__ void restore(uint32_t c, uint32_t sc, uint32_t mn, uint32_t& hi, uint32_t& lo) {
+  if constexpr (WIDE) {
+    const float2 x = fma2(h2f(c), h2f(sc), h2f(mn));
+    split2<2048>(x.x, x.y, hi, lo);
+  } else {
+    hi = fma_h2(c, sc, mn);
+  }
 }
 
 // One lane of a converged warp
@@ -233,15 +285,16 @@ struct ManyRaw {
 // Barriers of a CTA.  Those of a row tile are one per S buffer, so that the use
 // before the one waited for is always complete (a parity names one of two).
 struct ManyBars {
-  uint64_t kv_full[kManyBufs], kv_free[kManyBufs];       // per operand buffer
+  uint64_t kv_full[4], kv_free[4];                       // per operand buffer
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];   // per row tile (and S buffer)
   uint64_t last[2];                                      // everything issued has completed
   uint64_t ring[kManyLoaders][kManyStages];
 };
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const AttnArgs a) {
-  using F = Many<D>;
+  using F = Many<D, WIDE>;
+  constexpr int kRows = F::kRows, kBufs = F::kBufs;
   using L = KvTile<D>;
   constexpr int G = L::G;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -254,8 +307,8 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   volatile uint8_t* present = smem + 544;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kManyBufs; ++i) {
-      mbar_init(&bar.kv_full[i], kManyUnit);
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&bar.kv_full[i], kManyLoaders);
       mbar_init(&bar.kv_free[i], 2);   // both tiles' products
     }
     for (int x = 0; x < 2; ++x) {
@@ -285,7 +338,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   KvWalk w;
   int Gc, q0;
   long long U;
-  const bool any = kv_range<kManyThreads, kManyRows, kManyUnit>(a, w, Gc, U, q0);
+  const bool any = kv_range<kManyThreads, kRows, kManyUnit>(a, w, Gc, U, q0);
   bool ok = true;   // no wait ran out
 
   if (any && warp >= 8 && warp < 8 + kManyLoaders) {   // ---- loaders
@@ -302,14 +355,23 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       // rows of the item all see the keys [all_lo, all_hi)
       int all_lo, all_hi, x;
       {
-        int t1 = (w.rt * kManyRows + kManyRows - 1) / a.group;
+        int t1 = (w.rt * kRows + kRows - 1) / a.group;
         if (t1 > w.T - 1) t1 = w.T - 1;
-        kv_token_keys(w.T, w.n, w.rt * kManyRows / a.group, a.p.causal, a.p.window, x, all_hi);
+        kv_token_keys(w.T, w.n, w.rt * kRows / a.group, a.p.causal, a.p.window, x, all_hi);
         kv_token_keys(w.T, w.n, t1, a.p.causal, a.p.window, all_lo, x);
       }
-      for (int o = lw; o < count; o += kManyLoaders) {   // (the last unit may run past the span)
-        const int sub = o % kManyUnit;
-        const uint32_t it = it0 + o / kManyUnit, buf = it % kManyBufs, phase = it / kManyBufs & 1u;
+      // Every loader takes its turn in every unit, also in one without a tile of its own: the unit
+      // is full when all have, so that none is ever a phase of a barrier ahead or behind.
+      int o = lw;   // this warp's next tile (the last unit may run past the span)
+      for (int i = 0; ok && i < count / kManyUnit; ++i) {
+        const uint32_t it = it0 + i, buf = it % kBufs;
+        const uint32_t turn = (it / kBufs & 1u) ^ 1u;   // the buffer is free
+        if (o >= (i + 1) * kManyUnit) {
+          ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.kv_free[buf], turn, flags));
+          if (lane == 0) mbar_arrive(&bar.kv_full[buf]);
+          continue;
+        }
+        const int sub = o - i * kManyUnit;
         const bool there = t.have >> t.out & 1u;
         const int kb = (base + o) * LW_KV_TILE;
         const bool edge = kb < all_lo || kb + LW_KV_TILE > all_hi;
@@ -364,9 +426,10 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
 #pragma unroll
             for (int i = 0; i < GW; ++i) r.vc[j][i] = r.vs[j][i] = r.vm[j][i] = 0;
         }
-        if (!__all_sync(0xFFFFFFFFu, many_wait(&bar.kv_free[buf], phase ^ 1u, flags))) { ok = false; break; }
-        const uint32_t kto = smem_addr(smem) + F::kKv + buf * F::kKvBytes + (uint32_t)(sub * 256 + (lane / 4) * 16 + q * F::kKLbo);
-        const uint32_t vto = smem_addr(smem) + F::kKv + buf * F::kKvBytes + F::kKBytes +
+        ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.kv_free[buf], turn, flags));
+        if (!ok) break;
+        const uint32_t kto = smem_addr(smem) + F::kKv + buf * F::kBufBytes + (uint32_t)(sub * 256 + (lane / 4) * 16 + q * F::kKLbo);
+        const uint32_t vto = smem_addr(smem) + F::kKv + buf * F::kBufBytes + F::kKBytes +
                              (uint32_t)((sub * 2 + h) * F::kVLbo + n * 16 + g0 * 512);
         if (there) {
           const uint32_t half = lane & 4 ? 0x3232u : 0x1010u;   // key 2 j or 2 j + 1
@@ -376,9 +439,14 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
             for (int g = 0; g < G; ++g) {
               const uint32_t sc = __byte_perm(r.ks[i][g], 0, half);
               const uint32_t mn = __byte_perm(r.km[i][g / 2], 0, g % 2 ? 0x3232u : 0x1010u);
-              const uint32_t w0 = r.kc[i][g], w1 = r.kc[i][g] >> 8;
-              sts_u4(kto + (uint32_t)(i * 128 + 4 * g * F::kKLbo), fma_h2(whole_even(w0), sc, mn),
-                     fma_h2(whole_odd(w0), sc, mn), fma_h2(whole_even(w1), sc, mn), fma_h2(whole_odd(w1), sc, mn));
+              const uint32_t w0 = r.kc[i][g], w1 = r.kc[i][g] >> 8, to = kto + (uint32_t)(i * 128 + 4 * g * F::kKLbo);
+              uint32_t hi[4], lo[4];
+              restore<WIDE>(whole_even(w0), sc, mn, hi[0], lo[0]);
+              restore<WIDE>(whole_odd(w0), sc, mn, hi[1], lo[1]);
+              restore<WIDE>(whole_even(w1), sc, mn, hi[2], lo[2]);
+              restore<WIDE>(whole_odd(w1), sc, mn, hi[3], lo[3]);
+              sts_u4(to, hi[0], hi[1], hi[2], hi[3]);
+              if (WIDE) sts_u4(to + F::kKvBytes, lo[0], lo[1], lo[2], lo[3]);
             }
         }
 #pragma unroll
@@ -386,23 +454,29 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           if (G % 2 && g0 + i >= G) continue;
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
-            uint32_t e[4], o[4];
+            uint32_t e[4], o[4], el[4], ol[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              e[j] = fma_h2(whole_even(r.vc[j][i] >> (8 * st)), r.vs[j][i], r.vm[j][i]);
-              o[j] = fma_h2(whole_odd(r.vc[j][i] >> (8 * st)), r.vs[j][i], r.vm[j][i]);
+              restore<WIDE>(whole_even(r.vc[j][i] >> (8 * st)), r.vs[j][i], r.vm[j][i], e[j], el[j]);
+              restore<WIDE>(whole_odd(r.vc[j][i] >> (8 * st)), r.vs[j][i], r.vm[j][i], o[j], ol[j]);
             }
-            sts_u4(vto + (uint32_t)(i * 512 + (2 * st) * 128), e[0], e[1], e[2], e[3]);
-            sts_u4(vto + (uint32_t)(i * 512 + (2 * st + 1) * 128), o[0], o[1], o[2], o[3]);
+            const uint32_t to = vto + (uint32_t)(i * 512 + (2 * st) * 128);
+            sts_u4(to, e[0], e[1], e[2], e[3]);
+            sts_u4(to + 128, o[0], o[1], o[2], o[3]);
+            if (WIDE) {
+              sts_u4(to + F::kKvBytes, el[0], el[1], el[2], el[3]);
+              sts_u4(to + F::kKvBytes + 128, ol[0], ol[1], ol[2], ol[3]);
+            }
           }
         }
         if (lane == 0) present[it % 4 * kManyUnit + sub] = there;
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.kv_full[buf]);
+        o += kManyLoaders;
       }
       it0 += w.k1 - w.k0;
-      if (ok) more = kv_advance<kManyRows, kManyUnit>(a, w, q0);
+      if (ok) more = kv_advance<kRows, kManyUnit>(a, w, q0);
     }
     if (!ok) {
       flags[0] = 1;
@@ -413,52 +487,73 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   } else if (any && warp >= 8 + kManyLoaders) {   // ---- issuers
     const auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
     const auto wait = [&](uint64_t* b, bool parity) { return __all_sync(0xFFFFFFFFu, many_wait(b, parity, flags)) != 0; };
-    const int x = uniform(warp - 8 - kManyLoaders);   // row tile
+    const int x = uniform(warp - 8 - kManyLoaders);   // row tile (WIDE: 0 the hi products, 1 the lo ones)
+    const int xr = WIDE ? 0 : x;                      // whose rows
     const uint32_t tm = uniform(tmem), base = smem_addr(smem);
     const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
     int buf = 0, sbuf = 0;   // operand and S buffer of the item's first unit
     uint32_t kvph = 0, qph = 0;             // phases of kv_full (a bit a buffer) and q_full
     uint32_t pph = 0, oph = 0, used = 0;    // of p_full and o_done, and whether the place has held a P (a bit an S buffer)
+    const bool q_lo = WIDE && a.p.dtype == LW_F32;   // (fp16 queries are their hi parts)
     for (bool more = true; more && ok;) {
-      const bool mine = uniform(w.T * a.group - w.rt * kManyRows > x * kManyTile);
+      const bool mine = WIDE || uniform(w.T * a.group - w.rt * kRows > x * kManyTile);
       const int n = uniform(w.k1 - w.k0);
       // S for the item's i-th unit, over the P of two units before
       const auto issue_s = [&](int i) {
-        const int kv = (buf + i) % kManyBufs, sb = (sbuf + i) & 1;
+        const int kv = (buf + i) % kBufs, sb = (sbuf + i) & 1;
         if (!wait(&bar.kv_full[kv], kvph >> kv & 1u)) return false;
         kvph ^= 1u << kv;
         if (i == 0) {
-          if (!wait(&bar.q_full[x], qph)) return false;
+          if (!wait(&bar.q_full[xr], qph)) return false;
           qph ^= 1u;
         }
         if (used >> sb & 1u) {
           if (!wait(&bar.o_done[x][sb], oph >> sb & 1u)) return false;
+          if (WIDE && x == 0 && !wait(&bar.o_done[1][sb], oph >> sb & 1u)) return false;   // (reads P too)
           oph ^= 1u << sb;
         }
         used |= 1u << sb;
         tc_fence_after();
-        const uint64_t kd = sdesc(base + F::kKv + kv * F::kKvBytes, F::kKLbo, 128);
+        const uint64_t kd = sdesc(base + F::kKv + kv * F::kBufBytes, F::kKLbo, 128);
         const uint32_t d = tm + F::s_col(x, sb);
         if (elect_one()) {
+          if (!WIDE || x == 0) {
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            umma_bf16(d, qd + (2 * s * F::kQLbo >> 4), kd + (2 * s * F::kKLbo >> 4), idesc_f16(kManyKeys), s > 0);
+            for (int s = 0; s < D / 16; ++s)
+              umma_bf16(d, qd + (2 * s * F::kQLbo >> 4), kd + (2 * s * F::kKLbo >> 4), idesc_f16(kManyKeys), s > 0);
+          } else {
+            const uint64_t qh = qd - (F::kQBytes >> 4), kl = kd + (F::kKvBytes >> 4);
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              umma_bf16(d, qh + (2 * s * F::kQLbo >> 4), kl + (2 * s * F::kKLbo >> 4), idesc_f16(kManyKeys), s > 0);
+            if (q_lo) {
+#pragma unroll
+              for (int s = 0; s < D / 16; ++s)
+                umma_bf16(d, qd + (2 * s * F::kQLbo >> 4), kd + (2 * s * F::kKLbo >> 4), idesc_f16(kManyKeys), 1);
+            }
+          }
           umma_commit(&bar.s_full[x][sb]);
         }
         __syncwarp();
         return true;
       };
       const auto issue_o = [&](int i) {   // O += P V
-        const int kv = (buf + i) % kManyBufs, sb = (sbuf + i) & 1;
-        if (!wait(&bar.p_full[x][sb], pph >> sb & 1u)) return false;
+        const int kv = (buf + i) % kBufs, sb = (sbuf + i) & 1;
+        if (!wait(&bar.p_full[xr][sb], pph >> sb & 1u)) return false;
         pph ^= 1u << sb;
         tc_fence_after();
-        const uint64_t vd = sdesc(base + F::kKv + kv * F::kKvBytes + F::kKBytes, F::kVLbo, 128);
-        const uint32_t d = tm + F::o_col(x), p = tm + F::s_col(x, sb);
+        const uint64_t vd = sdesc(base + F::kKv + kv * F::kBufBytes + F::kKBytes, F::kVLbo, 128);
+        const uint32_t d = tm + F::o_col(x), p = tm + F::s_col(xr, sb);
         if (elect_one()) {
+          const uint64_t v = vd + (WIDE && x ? F::kKvBytes >> 4 : 0);
 #pragma unroll
           for (int s = 0; s < kManyKeys / 16; ++s)
-            umma_bf16_ta(d, p + 8 * s, vd + (2 * s * F::kVLbo >> 4), idesc_f16(D), i > 0 || s > 0);
+            umma_bf16_ta(d, p + 8 * s, v + (2 * s * F::kVLbo >> 4), idesc_f16(D), i > 0 || s > 0);
+          if (WIDE && x) {
+#pragma unroll
+            for (int s = 0; s < kManyKeys / 16; ++s)
+              umma_bf16_ta(d, p + 32 + 8 * s, vd + (2 * s * F::kVLbo >> 4), idesc_f16(D), 1);
+          }
           umma_commit(&bar.o_done[x][sb]);
           umma_commit(&bar.kv_free[kv]);
         }
@@ -472,16 +567,16 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       } else {   // no rows here: only let the buffers go
 #pragma unroll 1
         for (int i = 0; ok && i < n; ++i) {
-          const int kv = (buf + i) % kManyBufs;
+          const int kv = (buf + i) % kBufs;
           ok = wait(&bar.kv_full[kv], kvph >> kv & 1u);
           kvph ^= 1u << kv;
           if (lane == 0) mbar_arrive(&bar.kv_free[kv]);
           __syncwarp();
         }
       }
-      buf = (buf + n) % kManyBufs;
+      buf = (buf + n) % kBufs;
       sbuf = (sbuf + n) & 1;
-      if (ok) more = uniform(kv_advance<kManyRows, kManyUnit>(a, w, q0));
+      if (ok) more = uniform(kv_advance<kRows, kManyUnit>(a, w, q0));
     }
     if (!ok) {
       flags[0] = 1;
@@ -491,7 +586,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     if (elect_one()) umma_commit(&bar.last[x]);   // no product may be in flight when the tensor memory goes
     __syncwarp();
     mbar_wait(&bar.last[x], 0);
-  } else if (any && warp < 8) {   // ---- rows
+  } else if (any && warp < (WIDE ? 4 : 8)) {   // ---- rows
     const int x = warp / 4, row = threadIdx.x % kManyTile;   // tile, its row
     const uint32_t mine = tmem + ((uint32_t)(32 * (warp % 4)) << 16);   // this warp's quarter
     uint32_t it = 0;     // units of the CTA; S lies in buffer it % 2
@@ -499,7 +594,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
                          // next s_full; its last o_done has the other)
     struct Row { int tok, hq, lo, hi; bool live; };
     const auto find = [&](const KvWalk& v) {
-      const int r = v.rt * kManyRows + x * kManyTile + row;
+      const int r = v.rt * kRows + x * kManyTile + row;
       Row y;
       y.live = r < v.T * a.group;
       y.tok = y.live ? r / a.group : v.T - 1;
@@ -507,14 +602,21 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       kv_token_keys(v.T, v.n, y.tok, a.p.causal, a.p.window, y.lo, y.hi);
       return y;
     };
-    const auto tile_there = [&](const KvWalk& v) { return v.rt * kManyRows + x * kManyTile < v.T * a.group; };
+    const auto tile_there = [&](const KvWalk& v) { return v.rt * kRows + x * kManyTile < v.T * a.group; };
     float f = 0.f;   // log2 units per unit of S
     const auto load_q = [&](const Row& y, int s0) {
       const int64_t at = (int64_t)(s0 + y.tok) * a.p.q_token_stride + (int64_t)y.hq * a.p.q_head_stride;
-      const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.p.q);
       const uint32_t to = smem_addr(smem) + F::kQ + x * F::kQBytes;
-      qp = y.live ? qp + at : nullptr;
-      const float e2 = a.vec ? many_query<D, true>(qp, a.p.scale, to, row) : many_query<D, false>(qp, a.p.scale, to, row);
+      const auto read = [&](auto* q) {   // the row, by its type
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(q)>>;
+        q = y.live ? q + at : nullptr;
+        if constexpr (!WIDE) return a.vec ? many_query<D, true>(q, a.p.scale, to, row) : many_query<D, false>(q, a.p.scale, to, row);
+        else return a.vec ? many_query_wide<D, T, true>(q, a.p.scale, to, to + F::kQBytes, row)
+                          : many_query_wide<D, T, false>(q, a.p.scale, to, to + F::kQBytes, row);
+      };
+      float e2;
+      if constexpr (!WIDE) e2 = read(static_cast<const __nv_bfloat16*>(a.p.q));
+      else e2 = a.p.dtype == LW_F16 ? read(static_cast<const __half*>(a.p.q)) : read(static_cast<const float*>(a.p.q));
       // (never 0: a masked score times it stays -inf)
       f = fmaxf(fabsf(a.p.scale) * 1.4426950408889634f * e2, 1e-37f);
       fence_proxy_async();
@@ -526,7 +628,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     for (bool more = true; more;) {
       const KvWalk v = w;
       const int vq0 = q0;
-      more = kv_advance<kManyRows, kManyUnit>(a, w, q0);
+      more = kv_advance<kRows, kManyUnit>(a, w, q0);
       if (!tile_there(v)) {   // a short row tile: the other warps' alone
         it += v.k1 - v.k0;
         if (more) {
@@ -538,7 +640,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       // keys that every row of the tile sees
       int all_lo, all_hi, u0;
       {
-        const int r0 = v.rt * kManyRows + x * kManyTile;
+        const int r0 = v.rt * kRows + x * kManyTile;
         int t1 = (r0 + kManyTile - 1) / a.group;
         if (t1 > v.T - 1) t1 = v.T - 1;
         kv_token_keys(v.T, v.n, r0 / a.group, a.p.causal, a.p.window, u0, all_hi);
@@ -549,7 +651,9 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         const int kb = (v.span.lo + k * kManyUnit) * LW_KV_TILE;
         const int b = it & 1;
         const uint32_t sc = mine + F::s_col(x, b);
-        if (ok) ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.s_full[x][b], used >> b & 1u, flags));
+        if (ok) ok = many_wait(&bar.s_full[x][b], used >> b & 1u, flags);
+        if (WIDE && ok) ok = many_wait(&bar.s_full[1][b], used >> b & 1u, flags);
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t there = *reinterpret_cast<const volatile uint32_t*>(present + it % 4 * kManyUnit);
@@ -557,6 +661,23 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         tmem_ld32(sc, s0);
         tmem_ld32(sc + 32, s1);
         tmem_ld_wait();
+        if constexpr (WIDE) {   // and the lo parts' sum
+          const float2 down = make_float2(4.8828125e-4f, 4.8828125e-4f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t z[32];
+            uint32_t* s = h ? s1 : s0;
+            tmem_ld32(mine + F::s_col(1, b) + 32 * h, z);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 t = fma2(make_float2(__uint_as_float(z[j]), __uint_as_float(z[j + 1])), down,
+                                    make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+              s[j] = __float_as_uint(t.x);
+              s[j + 1] = __float_as_uint(t.y);
+            }
+          }
+        }
         if (kb < all_lo || kb + kManyKeys > all_hi || there != 0x01010101u) {
 #pragma unroll
           for (int j = 0; j < 64; ++j) {
@@ -575,11 +696,13 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           m = mx;
           l *= al;
           if (k > v.k0) {   // once the sum over the keys before is complete
-            ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.o_done[x][b ^ 1], (used >> (b ^ 1) & 1u) ^ 1u, flags));
+            const bool ph = (used >> (b ^ 1) & 1u) ^ 1u;
+            ok = many_wait(&bar.o_done[x][b ^ 1], ph, flags) && (!WIDE || many_wait(&bar.o_done[1][b ^ 1], ph, flags));
+            ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
+            for (int d = 0; d < (WIDE ? 2 * D : D); d += 32) {
               uint32_t z[32];
               tmem_ld32(mine + F::o_col(x) + d, z);
               tmem_ld_wait();
@@ -591,17 +714,26 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         }
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 f2 = make_float2(f, f), mu2 = make_float2(-mu, -mu);
-        uint32_t p[32];
+        // (the parts of p go where the scores were)
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const uint32_t* s = j < 16 ? s0 + 2 * j : s1 + 2 * (j - 16);
+          uint32_t* s = j < 16 ? s0 + 2 * j : s1 + 2 * (j - 16);
           const float2 t = fma2(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), f2, mu2);
           const float2 z = make_float2(ex2(t.x), ex2(t.y));
           sum[j % 2] = add2(sum[j % 2], z);
-          p[j] = h2bits(__floats2half2_rn(z.x, z.y));
+          if constexpr (WIDE) split2<2048>(z.x, z.y, s[0], s[1]);
+          else s[0] = h2bits(__floats2half2_rn(z.x, z.y));
         }
+        uint32_t p[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) p[j] = j < 16 ? s0[2 * j] : s1[2 * (j - 16)];
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st32(sc, p);
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) p[j] = j < 16 ? s0[2 * j + 1] : s1[2 * (j - 16) + 1];
+          tmem_st32(sc + 32, p);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -617,6 +749,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       {
         const int b = (it - 1) & 1;
         if (ok) ok = many_wait(&bar.o_done[x][b], (used >> b & 1u) ^ 1u, flags);
+        if (WIDE && ok) ok = many_wait(&bar.o_done[1][b], (used >> b & 1u) ^ 1u, flags);
       }
       ok = rows_agree(x, ok);   // all four warps go on to the barriers below, or none
       if (!ok) break;
@@ -647,6 +780,12 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(u[j]);
+        if constexpr (WIDE) {
+          tmem_ld32(mine + F::o_col(1) + 32 * g, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = fmaf(__uint_as_float(u[j]), 4.8828125e-4f, z[j]);
+        }
         if (whole) {
           give(g, l, z);
         } else {

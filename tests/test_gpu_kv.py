@@ -564,6 +564,20 @@ def test_many_sequences():
     Setup(17, [1] * 700, lens, 2, 1, 64, 16, "bf16").check()
 
 
+@pytest.mark.parametrize("typ", ["fp16", "bf16"])
+def test_short_and_long_chunks_together(typ):
+    """Many items of one key tile between long ones: parts of the kernel that have no work in the
+    short ones keep their place."""
+    kv_len = [20, 33, 900, 17, 40, 18, 64, 1300, 50, 19] * 6
+    Setup(19, [17] * 60, kv_len, 8, 4, 64, 16, typ).check()
+
+
+@pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
+def test_long_window(typ):
+    """Prompts under a sliding window: rows that see nothing of an item's first keys."""
+    Setup(20, [700, 900], [700, 1100], 8, 1, 64, 32, typ).check(window=200)
+
+
 def test_offsets_past_32_bits():
     """A cache of over 4 GiB: pages at its far end are written, read and attended."""
     heads, dim, page = 8, 128, 256
