@@ -121,9 +121,10 @@ __device__ __forceinline__ float2 h2f(uint32_t w) { return __half22float2(*reint
 template <int UP>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(h);
+  const float2 up = make_float2(UP, UP), f = mul2(__half22float2(h), make_float2(-UP, -UP));
+  const float2 d = fma2(make_float2(x, y), up, f);   // exact
   hi = h2bits(h);
-  lo = h2bits(__floats2half2_rn((x - f.x) * UP, (y - f.y) * UP));
+  lo = h2bits(__floats2half2_rn(d.x, d.y));
 }
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {

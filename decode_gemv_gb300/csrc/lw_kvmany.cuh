@@ -5,7 +5,7 @@
 // 128; keys come 64 at a time.  S = Q K^T and O += P V are tcgen05.mma: Q, K
 // and V (fp16, restored from the codes) are operand tiles in shared memory, P
 // and the accumulators lie in tensor memory.
-//  * 6 loader warps take the 16-key tiles in turn: bulk copies bring the next
+//  * 6 loader warps (WIDE: 10) take the 16-key tiles in turn: bulk copies bring the next
 //    ones while the last, in registers, is restored -- k = sc c + mn and v = sc c +
 //    mn by one rounded fp16 fma each -- and stored as operand tiles (four
 //    buffers), once for both row tiles;
@@ -44,9 +44,7 @@ namespace lw {
 
 constexpr int kManyTile = 128, kManyKeys = 64;
 constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit
-constexpr int kManyLoaders = 6;
-constexpr int kManyStages = 2;                      // places of a loader's ring
-constexpr int kManyThreads = 32 * (8 + kManyLoaders + 2);   // row warps, loader warps, issuers
+constexpr int kManyThreads = 32 * 16;               // warps: 8 of rows (WIDE: 4, 4 of loaders), 6 loaders, 2 issuers
 constexpr int kManyPerSm = 1;
 
 template <int D, bool WIDE>
@@ -54,6 +52,7 @@ struct Many {
   using L = KvTile<D>;
   static constexpr int kRows = WIDE ? kManyTile : 2 * kManyTile;   // of an item
   static constexpr int kBufs = WIDE ? 2 : 4;                       // restored units
+  static constexpr int kLoaders = WIDE ? 10 : 6, kStages = WIDE ? 1 : 2;   // loader warps, places of a loader's ring
   static constexpr int kQLbo = kManyTile * 16 + 16;   // bytes between 8-element columns (16, 32: bank offset)
   static constexpr int kQBytes = D / 8 * kQLbo;
   static constexpr int kKLbo = kManyKeys * 16 + 32;
@@ -65,7 +64,7 @@ struct Many {
   static constexpr int kKvBytes = kKBytes + kVBytes;
   static constexpr int kBufBytes = WIDE ? 2 * kKvBytes : kKvBytes;
   static constexpr int kRing = kKv + kBufs * kBufBytes;   // tiles as they are stored
-  static constexpr int kSmem = kRing + kManyLoaders * kManyStages * L::kBytes;
+  static constexpr int kSmem = kRing + kLoaders * kStages * L::kBytes;
   static constexpr int kPartial = kManyTile * (D + 2);   // of a tile, floats: m, l, then [D / 4][rows][4]
   // tensor-memory columns: S of tile x, buffer i (and P over it); O of tile x (WIDE: of part x; both parts
   // of P over the first S)
@@ -150,80 +149,58 @@ __device__ __forceinline__ bool rows_agree(int tile, bool ok) {
   return r != 0;
 }
 
-// This thread's row of Q (all of it 0 where p is NULL) into row `row` of the
-// operand tile, scaled by 2^-e and with the sign of `scale` (so that the largest
-// product is the largest score); returns 2^e.
-template <int D, bool VEC>
-__device__ __forceinline__ float many_query(const __nv_bfloat16* p, float scale, uint32_t to, int row) {
-  uint32_t w[D / 2];   // the row's pairs
+// A warp's 32 rows of Q into rows 32 quarter .. of the operand tile, each scaled
+// by 2^-e and given the sign of `scale` (so that the largest product is the
+// largest score); WIDE: lo 2^11 goes to the tile at `to_lo`.  Two rows at a time,
+// a lane eight elements (whole lines: a lane per row took 16 times the tag
+// lookups and bounded an item's start).  q + row_at is this lane's row, 0 where
+// row_at < 0.  Returns 2^e of this lane's row.
+template <int D, class T, bool VEC, bool WIDE>
+__device__ __forceinline__ float many_query(const T* q, int64_t row_at, float scale, uint32_t to, uint32_t to_lo,
+                                            int quarter, int lane) {
+  const int half = lane >> 4, o = lane & 15;
+  const uint32_t sign = __float_as_uint(scale) & 0x80000000u;
+  float mine = 1.f;
+  constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 16; i0 += kBatch) {
+    float y[kBatch][8];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (p) {
-      if constexpr (VEC) {
-        u = __ldg(reinterpret_cast<const uint4*>(p + 8 * i));
-      } else {
-        uint32_t* v = &u.x;
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t at = __shfl_sync(0xFFFFFFFFu, row_at, 2 * (i0 + i) + half);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[j] = __bfloat16_as_ushort(p[8 * i + 2 * j]) | (uint32_t)__bfloat16_as_ushort(p[8 * i + 2 * j + 1]) << 16;
+      for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
+      if (at >= 0 && o < D / 8) kv_load8<T, VEC>(q + at + 8 * o, y[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      float top = 0.f;   // (a NaN is not the largest, and stays NaN below)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[i][j]));
+#pragma unroll
+      for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      int e = (int)(__float_as_uint(top) >> 23) - 127;
+      e = e < -100 ? -100 : (e > 126 ? 126 : e);
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23 | sign);
+      const int r = 2 * (i0 + i);
+      const int e0 = __shfl_sync(0xFFFFFFFFu, e, 0), e1 = __shfl_sync(0xFFFFFFFFu, e, 16);
+      if (lane == r) mine = __uint_as_float((uint32_t)(127 + e0) << 23);
+      if (lane == r + 1) mine = __uint_as_float((uint32_t)(127 + e1) << 23);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (WIDE) split2<2048>(y[i][j] * down, y[i][j + 4] * down, hi[j], lo[j]);
+        else hi[j] = h2bits(__floats2half2_rn(y[i][j] * down, y[i][j + 4] * down));
+      }
+      const int row = r + half;
+      const uint32_t at = (uint32_t)(o * Many<D, WIDE>::kQLbo + (4 * quarter + row / 8) * 128 + (row % 8) * 16);
+      if (o < D / 8) {
+        sts_u4(to + at, hi[0], hi[1], hi[2], hi[3]);
+        if constexpr (WIDE) sts_u4(to_lo + at, lo[0], lo[1], lo[2], lo[3]);
       }
     }
-    w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
   }
-  uint32_t lo = 0, hi = 0;   // magnitudes are in order as integers (a NaN comes last, and stays NaN below)
-#pragma unroll
-  for (int i = 0; i < D / 2; ++i) {
-    lo = max(lo, w[i] & 0x7FFFu);
-    hi = max(hi, w[i] & 0x7FFF0000u);
-  }
-  int e = (int)(max(lo << 16, hi) >> 23) - 127;
-  e = e < -100 ? -100 : (e > 126 ? 126 : e);
-  const float down = __uint_as_float((uint32_t)(127 - e) << 23 | (__float_as_uint(scale) & 0x80000000u));
-  to += (uint32_t)((row / 8) * 128 + (row % 8) * 16);
-#pragma unroll
-  for (int o = 0; o < D / 8; ++o) {
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[2 * i] = __uint_as_float(w[4 * o + i] << 16) * down;
-      y[2 * i + 1] = __uint_as_float(w[4 * o + i] & 0xFFFF0000u) * down;
-    }
-    sts_u4(to + o * Many<D, false>::kQLbo, h2bits(__floats2half2_rn(y[0], y[4])), h2bits(__floats2half2_rn(y[1], y[5])),
-           h2bits(__floats2half2_rn(y[2], y[6])), h2bits(__floats2half2_rn(y[3], y[7])));
-  }
-  return __uint_as_float((uint32_t)(127 + e) << 23);
-}
-
-// The same in two parts: lo 2^11 goes to the tile at `to_lo`.  The row is read
-// twice, the second time from the cache.
-template <int D, class T, bool VEC>
-__device__ __forceinline__ float many_query_wide(const T* p, float scale, uint32_t to, uint32_t to_lo, int row) {
-  float top = 0.f;
-  float y[8];
-#pragma unroll 4
-  for (int o = 0; o < D / 8; ++o)
-    if (p) {
-      kv_load8<T, VEC>(p + 8 * o, y);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
-    }
-  int e = (int)(__float_as_uint(top) >> 23) - 127;
-  e = e < -100 ? -100 : (e > 126 ? 126 : e);
-  const float down = __uint_as_float((uint32_t)(127 - e) << 23 | (__float_as_uint(scale) & 0x80000000u));
-  const uint32_t at = (uint32_t)((row / 8) * 128 + (row % 8) * 16);
-#pragma unroll 4
-  for (int o = 0; o < D / 8; ++o) {
-    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-    if (p) {
-      kv_load8<T, VEC>(p + 8 * o, y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) split2<2048>(y[i] * down, y[i + 4] * down, hi[i], lo[i]);
-    }
-    sts_u4(to + at + o * Many<D, true>::kQLbo, hi[0], hi[1], hi[2], hi[3]);
-    sts_u4(to_lo + at + o * Many<D, true>::kQLbo, lo[0], lo[1], lo[2], lo[3]);
-  }
-  return __uint_as_float((uint32_t)(127 + e) << 23);
+  return mine;
 }
 
 // sc c + mn of a pair of codes, as one rounded fp16 pair or as two parts
@@ -288,13 +265,14 @@ struct ManyBars {
   uint64_t kv_full[4], kv_free[4];                       // per operand buffer
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];   // per row tile (and S buffer)
   uint64_t last[2];                                      // everything issued has completed
-  uint64_t ring[kManyLoaders][kManyStages];
+  uint64_t ring[12];                                     // [loader][place]
 };
 
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const AttnArgs a) {
   using F = Many<D, WIDE>;
-  constexpr int kRows = F::kRows, kBufs = F::kBufs;
+  constexpr int kRows = F::kRows, kBufs = F::kBufs, kLoaders = F::kLoaders, kStages = F::kStages;
+  static_assert(kLoaders * kStages <= 12, "ring barriers");
   using L = KvTile<D>;
   constexpr int G = L::G;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -308,7 +286,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBufs; ++i) {
-      mbar_init(&bar.kv_full[i], kManyLoaders);
+      mbar_init(&bar.kv_full[i], kLoaders);
       mbar_init(&bar.kv_free[i], 2);   // both tiles' products
     }
     for (int x = 0; x < 2; ++x) {
@@ -321,12 +299,11 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       mbar_init(&bar.o_done[x][0], 1);
       mbar_init(&bar.o_done[x][1], 1);
     }
-    for (int i = 0; i < kManyLoaders; ++i)
-      for (int j = 0; j < kManyStages; ++j) mbar_init(&bar.ring[i][j], 1);
+    for (int i = 0; i < 12; ++i) mbar_init(&bar.ring[i], 1);
     flags[0] = 0;
     fence_barrier_init();
   }
-  if (warp == 8 + kManyLoaders) {
+  if (warp == 14) {
     tmem_alloc(smem_addr(tslot), F::kCols);
     tmem_relinquish();
   }
@@ -341,13 +318,13 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   const bool any = kv_range<kManyThreads, kRows, kManyUnit>(a, w, Gc, U, q0);
   bool ok = true;   // no wait ran out
 
-  if (any && warp >= 8 && warp < 8 + kManyLoaders) {   // ---- loaders
-    const int lw = warp - 8;
+  if (any && warp >= (WIDE ? 4 : 8) && warp < 14) {   // ---- loaders
+    const int lw = warp - (WIDE ? 4 : 8);
     constexpr int GW = ManyRaw<D>::GW;
     uint32_t it0 = 0;                 // units before this item
-    FewFetch<D, kManyLoaders, 1, kManyStages> t;
-    t.bars = bar.ring[lw];
-    t.ring = smem + F::kRing + lw * kManyStages * L::kBytes;
+    FewFetch<D, kLoaders, 1, kStages> t;
+    t.bars = bar.ring + lw * kStages;
+    t.ring = smem + F::kRing + lw * kStages * L::kBytes;
     t.parity = t.have = 0;
     for (bool more = true; more && ok;) {
       const int base = w.span.lo + w.k0 * kManyUnit, count = (w.k1 - w.k0) * kManyUnit;
@@ -384,7 +361,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           __syncwarp();
         }
         if (base + o < w.span.hi) {
-          t.out = t.out + 1 == kManyStages ? 0 : t.out + 1;
+          t.out = t.out + 1 == kStages ? 0 : t.out + 1;
           t.send(a, lane);
         }
         if (there) {
@@ -473,7 +450,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.kv_full[buf]);
-        o += kManyLoaders;
+        o += kLoaders;
       }
       it0 += w.k1 - w.k0;
       if (ok) more = kv_advance<kRows, kManyUnit>(a, w, q0);
@@ -481,13 +458,13 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     if (!ok) {
       flags[0] = 1;
       if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
-      for (int i = 0; i < kManyStages; ++i)   // no copy may be in flight when the CTA ends
+      for (int i = 0; i < kStages; ++i)   // no copy may be in flight when the CTA ends
         if (t.have >> i & 1u) mbar_wait(&t.bars[i], t.parity >> i & 1u);
     }
-  } else if (any && warp >= 8 + kManyLoaders) {   // ---- issuers
+  } else if (any && warp >= 14) {   // ---- issuers
     const auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
     const auto wait = [&](uint64_t* b, bool parity) { return __all_sync(0xFFFFFFFFu, many_wait(b, parity, flags)) != 0; };
-    const int x = uniform(warp - 8 - kManyLoaders);   // row tile (WIDE: 0 the hi products, 1 the lo ones)
+    const int x = uniform(warp - 14);   // row tile (WIDE: 0 the hi products, 1 the lo ones)
     const int xr = WIDE ? 0 : x;                      // whose rows
     const uint32_t tm = uniform(tmem), base = smem_addr(smem);
     const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
@@ -605,14 +582,12 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     const auto tile_there = [&](const KvWalk& v) { return v.rt * kRows + x * kManyTile < v.T * a.group; };
     float f = 0.f;   // log2 units per unit of S
     const auto load_q = [&](const Row& y, int s0) {
-      const int64_t at = (int64_t)(s0 + y.tok) * a.p.q_token_stride + (int64_t)y.hq * a.p.q_head_stride;
+      const int64_t at = y.live ? (int64_t)(s0 + y.tok) * a.p.q_token_stride + (int64_t)y.hq * a.p.q_head_stride : -1;
       const uint32_t to = smem_addr(smem) + F::kQ + x * F::kQBytes;
-      const auto read = [&](auto* q) {   // the row, by its type
+      const auto read = [&](auto* q) {   // the rows, by their type
         using T = std::remove_const_t<std::remove_pointer_t<decltype(q)>>;
-        q = y.live ? q + at : nullptr;
-        if constexpr (!WIDE) return a.vec ? many_query<D, true>(q, a.p.scale, to, row) : many_query<D, false>(q, a.p.scale, to, row);
-        else return a.vec ? many_query_wide<D, T, true>(q, a.p.scale, to, to + F::kQBytes, row)
-                          : many_query_wide<D, T, false>(q, a.p.scale, to, to + F::kQBytes, row);
+        return a.vec ? many_query<D, T, true, WIDE>(q, at, a.p.scale, to, to + F::kQBytes, warp % 4, lane)
+                     : many_query<D, T, false, WIDE>(q, at, a.p.scale, to, to + F::kQBytes, warp % 4, lane);
       };
       float e2;
       if constexpr (!WIDE) e2 = read(static_cast<const __nv_bfloat16*>(a.p.q));
@@ -853,7 +828,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 8 + kManyLoaders) tmem_dealloc(tmem, F::kCols);
+  if (warp == 14) tmem_dealloc(tmem, F::kCols);
 }
 
 }  // namespace dev
