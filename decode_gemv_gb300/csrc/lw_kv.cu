@@ -12,8 +12,8 @@ lw_status check_kv_cache(const lw_kv_cache* c) {
   if (!lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens))
     return fail(LW_ERR_SHAPE, "kv_heads %d, page_tokens %d (a positive multiple of %d)", c->kv_heads,
                 c->page_tokens, LW_KV_TILE);
-  if (c->n_pages < 1 || c->n_pages > (1ll << 31) - 1)
-    return fail(LW_ERR_SHAPE, "%lld pages", (long long)c->n_pages);
+  if (c->n_pages < 1 || c->n_pages > ((1ll << 32) - 1) / c->page_tokens)
+    return fail(LW_ERR_SHAPE, "%lld pages of %d tokens", (long long)c->n_pages, c->page_tokens);
   if (!c->pages || (reinterpret_cast<uintptr_t>(c->pages) & 15u))
     return fail(LW_ERR_INVALID_ARG, "pages missing or not 16-byte aligned");
   return LW_OK;
@@ -30,125 +30,125 @@ struct CacheArgs {
   uint8_t* pages;
   const int64_t* slots;
   int64_t n, n_slots, page_bytes;
-  int32_t page_tokens, heads;
+  int32_t page_tiles, heads;
   int32_t* status;
 };
 
-// Where token t of a slot's tile starts: the tile's address (head 0), -1 if
-// the slot is not stored.  A slot past the pages is reported by lane `first`.
-__device__ __forceinline__ int64_t slot_tile(const CacheArgs& a, int64_t slot, int tile_bytes,
-                                             bool first) {
-  if (slot < 0) return -1;
-  if (slot >= a.n_slots) {
-    if (first) dev::report(a.status, LW_DEV_BAD_SLOT);
+// The tile of a slot (head 0: its place in the pages; -1 if the slot is not
+// stored).  A slot past the pages is reported where `first`.
+__device__ __forceinline__ int64_t slot_tile(const CacheArgs& a, int64_t slot, int tile_bytes, bool first) {
+  if (slot < 0 || slot >= a.n_slots) {
+    if (slot >= 0 && first) dev::report(a.status, LW_DEV_BAD_SLOT);
     return -1;
   }
-  const int64_t page = slot / a.page_tokens;
-  const int in = (int)(slot - page * a.page_tokens);
-  return page * a.page_bytes + (int64_t)(in / LW_KV_TILE) * tile_bytes;
+  const uint32_t tile = (uint32_t)(slot / LW_KV_TILE);   // (slots are below 2^32)
+  const uint32_t page = tile / (uint32_t)a.page_tiles;
+  return page * a.page_bytes + (int64_t)(tile - page * (uint32_t)a.page_tiles) * tile_bytes;
 }
 
-constexpr int kCacheThreads = 256;
+// Both kernels: a block takes 16 tokens of one head, a thread 8 consecutive
+// keys and the same 8 values of one of them (4 neighbouring lanes a group).
+// Bound by HBM: 2 bytes in or out a bf16 element, 0.625 for the cache.
+constexpr int kTokens = 16;
 
-// One thread quantises 8 consecutive values of one head of one token (4
-// neighbouring lanes a group); blockIdx.y = 0 for keys, 1 for values.
 template <class T, int D, bool VEC>
-__global__ void __launch_bounds__(kCacheThreads) kv_write_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kTokens * D / 8) kv_write_kernel(const CacheArgs a) {
   using L = KvTile<D>;
   constexpr int kChunks = D / 8;
-  const int64_t i = (int64_t)blockIdx.x * kCacheThreads + threadIdx.x;
-  const int64_t row = i / kChunks;
-  const int ch = (int)(i - row * kChunks);
-  const int64_t tok = row / a.heads;
-  const int h = (int)(row - tok * a.heads);
-  const bool val = blockIdx.y == 1;
-  const RowsArgs& r = val ? a.v : a.k;
+  const int64_t tok = (int64_t)blockIdx.x * kTokens + threadIdx.x / kChunks;
+  const int ch = threadIdx.x % kChunks, h = blockIdx.y;
+  dev::pdl_wait();
   int64_t at = -1, slot = -1;
-  float x[8] = {};
+  float k[8] = {}, v[8] = {};
   if (tok < a.n) {
     slot = a.slots[tok];
-    at = slot_tile(a, slot, L::kBytes, !val && h == 0 && ch == 0);
-    if (at >= 0)
-      dev::kv_load8<T, VEC>(static_cast<const T*>(r.ptr) + tok * r.token_stride + h * r.head_stride + 8 * ch, x);
+    dev::kv_load8<T, VEC>(static_cast<const T*>(a.k.ptr) + tok * a.k.token_stride + h * a.k.head_stride + 8 * ch, k);
+    dev::kv_load8<T, VEC>(static_cast<const T*>(a.v.ptr) + tok * a.v.token_stride + h * a.v.head_stride + 8 * ch, v);
+    at = slot_tile(a, slot, L::kBytes, h == 0 && ch == 0);
   }
-  __half scale, low;
-  const uint32_t w = dev::kv_quantise8(x, scale, low);
+  __half ks, km, vs, vm;
+  const uint32_t kw = dev::kv_quantise8(k, ks, km), vw = dev::kv_quantise8(v, vs, vm);
   if (at < 0) return;
   const int t = (int)(slot % LW_KV_TILE), g = ch >> 2, q = ch & 3;
-  uint8_t* tile = a.pages + at + (int64_t)h * (a.page_tokens / LW_KV_TILE) * L::kBytes;
-  if (!val) {
-    *reinterpret_cast<uint32_t*>(tile + L::kKeyCodes + 4 * ((t * 4 + q) * L::G + g)) = w;
-    if (q == 0) {
-      *reinterpret_cast<__half*>(tile + L::kKeyScale + 2 * ((t / 2 * L::G + g) * 2 + t % 2)) = scale;
-      *reinterpret_cast<__half*>(tile + L::kKeyMin + 2 * (t * L::GP + g)) = low;
-    }
-  } else {
-    uint8_t* u = tile + L::kValCodes + 4 * ((t / 2 * 8 + 2 * q) * L::G + g) + 2 * (t % 2);
-    *reinterpret_cast<uint16_t*>(u) = (uint16_t)w;
-    *reinterpret_cast<uint16_t*>(u + 4 * L::G) = (uint16_t)(w >> 16);
-    if (q == 0) {
-      *reinterpret_cast<__half*>(tile + L::kValScale + 2 * ((t / 2 * L::G + g) * 2 + t % 2)) = scale;
-      *reinterpret_cast<__half*>(tile + L::kValMin + 2 * ((t / 2 * L::G + g) * 2 + t % 2)) = low;
-    }
+  uint8_t* tile = a.pages + at + (int64_t)h * a.page_tiles * L::kBytes;
+  const int par = 2 * ((t / 2 * L::G + g) * 2 + t % 2);
+  *reinterpret_cast<uint32_t*>(tile + L::kKeyCodes + 4 * ((t * 4 + q) * L::G + g)) = kw;
+  uint8_t* u = tile + L::kValCodes + 4 * ((t / 2 * 8 + 2 * q) * L::G + g) + 2 * (t % 2);
+  *reinterpret_cast<uint16_t*>(u) = (uint16_t)vw;
+  *reinterpret_cast<uint16_t*>(u + 4 * L::G) = (uint16_t)(vw >> 16);
+  // a lane of the group each
+  if (q == 0) *reinterpret_cast<__half*>(tile + L::kKeyScale + par) = ks;
+  if (q == 1) *reinterpret_cast<__half*>(tile + L::kKeyMin + 2 * (t * L::GP + g)) = km;
+  if (q == 2) *reinterpret_cast<__half*>(tile + L::kValScale + par) = vs;
+  if (q == 3) *reinterpret_cast<__half*>(tile + L::kValMin + par) = vm;
+}
+
+// scale * code + min of 8 codes
+__device__ __forceinline__ void restore8(uint32_t w, __half scale, __half low, float (&x)[8]) {
+  const float s = __half2float(scale), m = __half2float(low);
+  const float2 s2 = make_float2(s, s), m2 = make_float2(m, m);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = i % 2 ? dev::whole_odd(w >> (8 * (i / 2))) : dev::whole_even(w >> (8 * (i / 2)));
+    const float2 y = dev::fma2(dev::h2f(c), s2, m2);
+    x[i] = y.x;
+    x[i + 4] = y.y;
   }
 }
 
 template <class T, int D, bool VEC>
-__global__ void __launch_bounds__(kCacheThreads) kv_read_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kTokens * D / 8) kv_read_kernel(const CacheArgs a) {
   using L = KvTile<D>;
   constexpr int kChunks = D / 8;
-  const int64_t i = (int64_t)blockIdx.x * kCacheThreads + threadIdx.x;
-  const int64_t row = i / kChunks;
-  const int ch = (int)(i - row * kChunks);
-  const int64_t tok = row / a.heads;
+  const int64_t tok = (int64_t)blockIdx.x * kTokens + threadIdx.x / kChunks;
+  const int ch = threadIdx.x % kChunks, h = blockIdx.y;
+  dev::pdl_wait();
   if (tok >= a.n) return;
-  const int h = (int)(row - tok * a.heads);
-  const bool val = blockIdx.y == 1;
-  const RowsArgs& r = val ? a.v : a.k;
   const int64_t slot = a.slots[tok];
-  const int64_t at = slot_tile(a, slot, L::kBytes, !val && h == 0 && ch == 0);
-  float x[8] = {};
+  const int64_t at = slot_tile(a, slot, L::kBytes, h == 0 && ch == 0);
+  float k[8] = {}, v[8] = {};
   if (at >= 0) {
     const int t = (int)(slot % LW_KV_TILE), g = ch >> 2, q = ch & 3;
-    const uint8_t* tile = a.pages + at + (int64_t)h * (a.page_tokens / LW_KV_TILE) * L::kBytes;
-    uint32_t w;
-    __half scale, low;
-    if (!val) {
-      w = *reinterpret_cast<const uint32_t*>(tile + L::kKeyCodes + 4 * ((t * 4 + q) * L::G + g));
-      scale = *reinterpret_cast<const __half*>(tile + L::kKeyScale + 2 * ((t / 2 * L::G + g) * 2 + t % 2));
-      low = *reinterpret_cast<const __half*>(tile + L::kKeyMin + 2 * (t * L::GP + g));
-    } else {
-      const uint8_t* u = tile + L::kValCodes + 4 * ((t / 2 * 8 + 2 * q) * L::G + g) + 2 * (t % 2);
-      w = *reinterpret_cast<const uint16_t*>(u) |
-          (uint32_t) * reinterpret_cast<const uint16_t*>(u + 4 * L::G) << 16;
-      scale = *reinterpret_cast<const __half*>(tile + L::kValScale + 2 * ((t / 2 * L::G + g) * 2 + t % 2));
-      low = *reinterpret_cast<const __half*>(tile + L::kValMin + 2 * ((t / 2 * L::G + g) * 2 + t % 2));
-    }
-    const float s = __half2float(scale), m = __half2float(low);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = fmaf(s, (float)((w >> (4 * j)) & 15u), m);
+    const uint8_t* tile = a.pages + at + (int64_t)h * a.page_tiles * L::kBytes;
+    const int par = 2 * ((t / 2 * L::G + g) * 2 + t % 2);
+    const uint32_t kw = *reinterpret_cast<const uint32_t*>(tile + L::kKeyCodes + 4 * ((t * 4 + q) * L::G + g));
+    const __half ks = *reinterpret_cast<const __half*>(tile + L::kKeyScale + par);
+    const __half km = *reinterpret_cast<const __half*>(tile + L::kKeyMin + 2 * (t * L::GP + g));
+    const uint8_t* u = tile + L::kValCodes + 4 * ((t / 2 * 8 + 2 * q) * L::G + g) + 2 * (t % 2);
+    const uint32_t vw = *reinterpret_cast<const uint16_t*>(u) |
+                        (uint32_t) * reinterpret_cast<const uint16_t*>(u + 4 * L::G) << 16;
+    const __half vs = *reinterpret_cast<const __half*>(tile + L::kValScale + par);
+    const __half vm = *reinterpret_cast<const __half*>(tile + L::kValMin + par);
+    restore8(kw, ks, km, k);
+    restore8(vw, vs, vm, v);
   }
-  dev::kv_store8<T, VEC>(static_cast<T*>(r.ptr) + tok * r.token_stride + h * r.head_stride + 8 * ch, x);
+  dev::kv_store8<T, VEC>(static_cast<T*>(a.k.ptr) + tok * a.k.token_stride + h * a.k.head_stride + 8 * ch, k);
+  dev::kv_store8<T, VEC>(static_cast<T*>(a.v.ptr) + tok * a.v.token_stride + h * a.v.head_stride + 8 * ch, v);
 }
 
 template <class T, int D>
-void launch_rows(const CacheArgs& a, bool write, bool vec, cudaStream_t st) {
-  const int64_t threads = a.n * a.heads * (D / 8);
-  const dim3 grid((unsigned)((threads + kCacheThreads - 1) / kCacheThreads), 2);
-  if (write) {
-    if (vec) kv_write_kernel<T, D, true><<<grid, kCacheThreads, 0, st>>>(a);
-    else kv_write_kernel<T, D, false><<<grid, kCacheThreads, 0, st>>>(a);
-  } else {
-    if (vec) kv_read_kernel<T, D, true><<<grid, kCacheThreads, 0, st>>>(a);
-    else kv_read_kernel<T, D, false><<<grid, kCacheThreads, 0, st>>>(a);
-  }
+cudaError_t launch_rows(const CacheArgs& a, bool write, bool vec, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((a.n + kTokens - 1) / kTokens), (unsigned)a.heads);
+  cfg.blockDim = dim3(kTokens * D / 8);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (write)
+    return vec ? cudaLaunchKernelEx(&cfg, kv_write_kernel<T, D, true>, a)
+               : cudaLaunchKernelEx(&cfg, kv_write_kernel<T, D, false>, a);
+  return vec ? cudaLaunchKernelEx(&cfg, kv_read_kernel<T, D, true>, a)
+             : cudaLaunchKernelEx(&cfg, kv_read_kernel<T, D, false>, a);
 }
 
 template <class T>
-void launch_rows_d(const CacheArgs& a, int dim, bool write, bool vec, cudaStream_t st) {
-  if (dim == 64) launch_rows<T, 64>(a, write, vec, st);
-  else if (dim == 96) launch_rows<T, 96>(a, write, vec, st);
-  else launch_rows<T, 128>(a, write, vec, st);
+cudaError_t launch_rows_d(const CacheArgs& a, int dim, bool write, bool vec, cudaStream_t st) {
+  if (dim == 64) return launch_rows<T, 64>(a, write, vec, st);
+  if (dim == 96) return launch_rows<T, 96>(a, write, vec, st);
+  return launch_rows<T, 128>(a, write, vec, st);
 }
 
 lw_status kv_rows_call(const char* fn, const lw_kv_cache* c, const int64_t* slots, int64_t n,
@@ -169,7 +169,7 @@ lw_status kv_rows_call(const char* fn, const lw_kv_cache* c, const int64_t* slot
   if (reinterpret_cast<uintptr_t>(k->ptr) % es || reinterpret_cast<uintptr_t>(v->ptr) % es ||
       reinterpret_cast<uintptr_t>(slots) % 8)
     return fail(LW_ERR_INVALID_ARG, "%s: an address is not aligned to its type", fn);
-  if (n > (1ll << 40) / ((int64_t)c->kv_heads * c->head_dim))
+  if ((n + kTokens - 1) / kTokens > (1ll << 31) - 1)
     return fail(LW_ERR_SHAPE, "%s: %lld tokens", fn, (long long)n);
   CacheArgs a{};
   a.k = {k->ptr, k->token_stride, k->head_stride};
@@ -179,17 +179,19 @@ lw_status kv_rows_call(const char* fn, const lw_kv_cache* c, const int64_t* slot
   a.n = n;
   a.n_slots = c->n_pages * c->page_tokens;
   a.page_bytes = (int64_t)lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens);
-  a.page_tokens = c->page_tokens;
+  a.page_tiles = c->page_tokens / LW_KV_TILE;
   a.heads = c->kv_heads;
   a.status = d_status;
   const bool vec = kv_rows_aligned(k->ptr, k->token_stride, k->head_stride, k->dtype) &&
                    kv_rows_aligned(v->ptr, v->token_stride, v->head_stride, v->dtype);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (k->dtype == LW_F32) launch_rows_d<float>(a, c->head_dim, write, vec, st);
-  else if (k->dtype == LW_F16) launch_rows_d<__half>(a, c->head_dim, write, vec, st);
-  else launch_rows_d<__nv_bfloat16>(a, c->head_dim, write, vec, st);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(LW_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  const cudaError_t e = k->dtype == LW_F32   ? launch_rows_d<float>(a, c->head_dim, write, vec, st)
+                        : k->dtype == LW_F16 ? launch_rows_d<__half>(a, c->head_dim, write, vec, st)
+                                             : launch_rows_d<__nv_bfloat16>(a, c->head_dim, write, vec, st);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(LW_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  }
   return LW_OK;
 }
 

@@ -105,17 +105,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ void sts_u4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ uint32_t pair_lo(uint32_t w) { return __byte_perm(w, w, 0x1010); }
-__device__ __forceinline__ uint32_t pair_hi(uint32_t w) { return __byte_perm(w, w, 0x3232); }
-// the codes of nibbles 0, 4 and 1, 5 as fp16 integers: 1024 + c less 1024
-__device__ __forceinline__ uint32_t whole_even(uint32_t w) {
-  const uint32_t x = (w & 0x000F000Fu) | 0x64006400u, b = 0xE400E400u;
-  return h2bits(__hadd2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&b)));
-}
-__device__ __forceinline__ uint32_t whole_odd(uint32_t w) {   // 1024 + 16 c
-  return fma_h2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
-}
-
 // A wait that gives up when another role has
 __device__ __forceinline__ bool many_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
   const auto passed = [&] {   // sleeps up to 2 us in the barrier
