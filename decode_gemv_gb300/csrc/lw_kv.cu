@@ -30,7 +30,7 @@ struct CacheArgs {
   uint8_t* pages;
   const int64_t* slots;
   int64_t n, n_slots, page_bytes;
-  int32_t page_tiles, heads;
+  int32_t page_tiles, page_shift, heads;   // page_tiles = 2^page_shift, or page_shift < 0
   int32_t* status;
 };
 
@@ -42,7 +42,7 @@ __device__ __forceinline__ int64_t slot_tile(const CacheArgs& a, int64_t slot, i
     return -1;
   }
   const uint32_t tile = (uint32_t)(slot / LW_KV_TILE);   // (slots are below 2^32)
-  const uint32_t page = tile / (uint32_t)a.page_tiles;
+  const uint32_t page = a.page_shift >= 0 ? tile >> a.page_shift : tile / (uint32_t)a.page_tiles;
   return page * a.page_bytes + (int64_t)(tile - page * (uint32_t)a.page_tiles) * tile_bytes;
 }
 
@@ -59,15 +59,17 @@ __global__ void __launch_bounds__(kTokens * D / 8) kv_write_kernel(const CacheAr
   const int ch = threadIdx.x % kChunks, h = blockIdx.y;
   dev::pdl_wait();
   int64_t at = -1, slot = -1;
-  float k[8] = {}, v[8] = {};
+  float k[8] = {}, v[8] = {}, lo[2] = {}, hi[2] = {};
   if (tok < a.n) {
     slot = a.slots[tok];
-    dev::kv_load8<T, VEC>(static_cast<const T*>(a.k.ptr) + tok * a.k.token_stride + h * a.k.head_stride + 8 * ch, k);
-    dev::kv_load8<T, VEC>(static_cast<const T*>(a.v.ptr) + tok * a.v.token_stride + h * a.v.head_stride + 8 * ch, v);
+    dev::kv_load8_range<T, VEC>(static_cast<const T*>(a.k.ptr) + tok * a.k.token_stride + h * a.k.head_stride + 8 * ch,
+                                k, lo[0], hi[0]);
+    dev::kv_load8_range<T, VEC>(static_cast<const T*>(a.v.ptr) + tok * a.v.token_stride + h * a.v.head_stride + 8 * ch,
+                                v, lo[1], hi[1]);
     at = slot_tile(a, slot, L::kBytes, h == 0 && ch == 0);
   }
   __half ks, km, vs, vm;
-  const uint32_t kw = dev::kv_quantise8(k, ks, km), vw = dev::kv_quantise8(v, vs, vm);
+  const uint32_t kw = dev::kv_quantise8(k, lo[0], hi[0], ks, km), vw = dev::kv_quantise8(v, lo[1], hi[1], vs, vm);
   if (at < 0) return;
   const int t = (int)(slot % LW_KV_TILE), g = ch >> 2, q = ch & 3;
   uint8_t* tile = a.pages + at + (int64_t)h * a.page_tiles * L::kBytes;
@@ -180,6 +182,9 @@ lw_status kv_rows_call(const char* fn, const lw_kv_cache* c, const int64_t* slot
   a.n_slots = c->n_pages * c->page_tokens;
   a.page_bytes = (int64_t)lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens);
   a.page_tiles = c->page_tokens / LW_KV_TILE;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_tiles == 1 << i) a.page_shift = i;
   a.heads = c->kv_heads;
   a.status = d_status;
   const bool vec = kv_rows_aligned(k->ptr, k->token_stride, k->head_stride, k->dtype) &&

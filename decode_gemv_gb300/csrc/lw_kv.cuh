@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "lw_dev.cuh"
 
@@ -131,37 +132,60 @@ __device__ __forceinline__ uint32_t whole_odd(uint32_t w) {
   return fma_h2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
 }
 
+// Smallest and largest of three, a NaN if there is one
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 8 consecutive values and their smallest and largest (NaN if one is; 16-bit
+// types compared in pairs)
+template <class T, bool VEC>
+__device__ __forceinline__ void kv_load8_range(const T* p, float (&x)[8], float& lo, float& hi) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const T2* w = reinterpret_cast<const T2*>(&u);
+    const T2 a = __hmin2_nan(__hmin2_nan(w[0], w[1]), __hmin2_nan(w[2], w[3]));
+    const T2 b = __hmax2_nan(__hmax2_nan(w[0], w[1]), __hmax2_nan(w[2], w[3]));
+    lo = kv_float<T>(__hmin_nan(a.x, a.y));
+    hi = kv_float<T>(__hmax_nan(b.x, b.y));
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = kv_float<T>(e[j]);
+  } else {
+    kv_load8<T, VEC>(p, x);
+    lo = min3(min3(min3(x[0], x[1], x[2]), x[3], x[4]), min3(x[5], x[6], x[7]), x[0]);
+    hi = max3(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]), x[0]);
+  }
+}
+
 // Scale and minimum of a group of 32 values, 8 of them in each of 4
-// neighbouring lanes, and this lane's codes (nibble i = value i).  Every step
-// is the definition's, in fp32 and rounded to nearest even (no contraction:
-// the written cache is the same whatever compiled this); what the definition
-// clamps is clamped where a group of the warp needs it, which is rare.
-__device__ __forceinline__ uint32_t kv_quantise8(float (&x)[8], __half& scale, __half& low) {
-  float lo = x[0], hi = x[0];
-  uint32_t top = 0;   // the largest magnitude: in order as an integer, infinities and NaN last
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  }
-  if (__any_sync(0xFFFFFFFFu, top > __float_as_uint(LW_KV_LIMIT))) {
-    lo = LW_KV_LIMIT;
-    hi = -LW_KV_LIMIT;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = fminf(fmaxf(x[i], -LW_KV_LIMIT), LW_KV_LIMIT);
-      lo = fminf(lo, x[i]);
-      hi = fmaxf(hi, x[i]);
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  }
-  const bool bad = top >= 0x7F800000u;
+// neighbouring lanes (lo, hi: the lane's smallest and largest), and this lane's
+// codes (nibble i = value i).  Every step is the definition's, in fp32 and
+// rounded to nearest even (no contraction: the written cache is the same
+// whatever compiled this); what the definition clamps is clamped where a group
+// of the warp needs it, which is rare.
+__device__ __forceinline__ uint32_t kv_quantise8(float (&x)[8], float lo, float hi, __half& scale, __half& low) {
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    const float a = __shfl_xor_sync(0xFFFFFFFFu, lo, o), b = __shfl_xor_sync(0xFFFFFFFFu, hi, o);
+    lo = min3(lo, a, a);
+    hi = max3(hi, b, b);
+  }
+  bool bad = false;
+  if (__any_sync(0xFFFFFFFFu, !(lo >= -LW_KV_LIMIT && hi <= LW_KV_LIMIT))) {
+    bad = !(lo >= -3.402823466e38f && hi <= 3.402823466e38f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -LW_KV_LIMIT), LW_KV_LIMIT);
+    lo = fminf(fmaxf(lo, -LW_KV_LIMIT), LW_KV_LIMIT);
+    hi = fminf(fmaxf(hi, -LW_KV_LIMIT), LW_KV_LIMIT);
   }
   scale = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), (float)(1.0 / 15.0)));
   low = __float2half_rn(lo);
