@@ -56,19 +56,46 @@ __device__ __forceinline__ long long cta_scan(long long v, long long* s, long lo
   return before + inc - v;
 }
 
-// The CTA's range of units, and the sequence its first unit is in.  Whole
-// CTA of NT threads; false if the CTA has no units.
-template <int NT, int RT, int PER>
+template <int RT, int PER, int EXTRA>
+__device__ __forceinline__ KvShape kv_shape(const AttnArgs& a) {
+  return KvShape{a.group, RT, PER, EXTRA, a.p.causal, a.p.window};
+}
+
+// On to the next item that has units of this CTA's; false at the end of the
+// range.
+template <int RT, int PER, int EXTRA>
+__device__ __forceinline__ bool kv_advance(const AttnArgs& a, KvWalk& w, int& q0) {
+  const KvShape c = kv_shape<RT, PER, EXTRA>(a);
+  do {
+    const bool same = kv_next(w, a.heads);
+    if (w.x >= w.xe) return false;
+    if (!same) {
+      w.base = w.x;
+      w.h = w.rt = 0;
+      do {
+        ++w.b;
+        kv_seq<false>(a, w.b, q0, w.T, w.n);
+      } while (w.T == 0);
+    }
+    kv_enter(c, w);
+  } while (w.k0 >= w.k1);
+  return true;
+}
+
+// The CTA's range, and its first item.  Whole CTA of NT threads; false if the
+// CTA has no units.
+template <int NT, int RT, int PER, int EXTRA>
 __device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int& q0) {
   __shared__ long long s_scan[NT / 32 + 1], s_base;
   __shared__ int s_b;
+  const KvShape c = kv_shape<RT, PER, EXTRA>(a);
   const int tid = threadIdx.x, batch = a.p.batch;
   long long sum = 0, first = 0;
   for (int b = tid; b < batch; b += NT) {
     int s, T, n;
     if (blockIdx.x == 0) kv_seq<true>(a, b, s, T, n);
     else kv_seq<false>(a, b, s, T, n);
-    const long long u = T ? a.heads * kv_head_units(T, n, a.group, RT, PER, a.p.causal, a.p.window) : 0;
+    const long long u = T ? a.heads * kv_head_weight(c, T, n) : 0;
     if (b == tid) first = u;
     sum += u;
   }
@@ -91,7 +118,7 @@ __device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int
       if (b < batch) {
         int s, T, n;
         kv_seq<false>(a, b, s, T, n);
-        u = T ? a.heads * kv_head_units(T, n, a.group, RT, PER, a.p.causal, a.p.window) : 0;
+        u = T ? a.heads * kv_head_weight(c, T, n) : 0;
       }
       before = carry + cta_scan<NT>(u, s_scan, total);
       if (w.x >= before && w.x < before + u) {
@@ -105,24 +132,8 @@ __device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int
   w.b = s_b;
   w.base = s_base;
   kv_seq<false>(a, w.b, q0, w.T, w.n);
-  kv_seek(w, a.group, RT, PER, a.p.causal, a.p.window);
-  return true;
-}
-
-// On to the next item; false at the end of the range.
-template <int RT, int PER>
-__device__ __forceinline__ bool kv_advance(const AttnArgs& a, KvWalk& w, int& q0) {
-  const bool same = kv_next(w, a.heads);
-  if (w.x >= w.xe) return false;
-  if (!same) {
-    w.base = w.x;
-    do {
-      ++w.b;
-      kv_seq<false>(a, w.b, q0, w.T, w.n);
-    } while (w.T == 0);
-  }
-  kv_start(w, a.group, RT, PER, a.p.causal, a.p.window);
-  return true;
+  kv_seek(c, w);
+  return w.k0 < w.k1 || kv_advance<RT, PER, EXTRA>(a, w, q0);
 }
 
 // 4 or 8 consecutive elements of an output row, rounded to its type

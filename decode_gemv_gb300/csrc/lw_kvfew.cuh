@@ -49,6 +49,7 @@ constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewPerSm = 2;                        // resident CTAs
 constexpr int kFewStages = 2;                       // places of a warp's ring, two tiles each
 constexpr int kFewUnit = 2 * kFewWarps;             // tiles of a unit
+constexpr int kFewExtra = 3;                        // an item's start and end: 3 units' time
 constexpr int kFewFlush = 32;                       // tiles between two additions (MODE 0)
 
 template <int D, int MODE>
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
   KvWalk w;
   int G, q0;
   long long U;
-  if (!kv_range<kFewThreads, RT, kFewUnit>(a, w, G, U, q0)) return;
+  if (!kv_range<kFewThreads, RT, kFewUnit, kFewExtra>(a, w, G, U, q0)) return;
 
   FewWarp<D, MODE> f;
   bool dead = false;   // a wait ran out: reported, and only the barriers are kept up
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
     // the next item's first tiles, before this one's join
     const KvWalk v = w;
     const int vq0 = q0;
-    more = kv_advance<RT, kFewUnit>(a, w, q0);
+    more = kv_advance<RT, kFewUnit, kFewExtra>(a, w, q0);
     if (more && !dead) t.begin(a, w, w.span.lo + w.k0 * kFewUnit + 2 * warp, w.span.lo + w.k1 * kFewUnit, lane);
 
     // join the warps, 8 rows at a time
@@ -711,8 +712,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
       __syncthreads();
     }
     if (!whole) {
-      const long long x0 = v.x - v.k0;
-      const int c0 = tc_owner(x0, U, G), parts = tc_owner(x0 + v.units - 1, U, G) - c0 + 1;
+      const int c0 = kv_owner(v.first, U, G), parts = kv_owner(v.first + v.units - 1, U, G) - c0 + 1;
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {

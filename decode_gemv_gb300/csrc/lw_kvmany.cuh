@@ -46,6 +46,7 @@ constexpr int kManyTile = 128, kManyKeys = 64;
 constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit
 constexpr int kManyThreads = 32 * 16;               // warps: 8 of rows (WIDE: 4, 4 of loaders), 6 loaders, 2 issuers
 constexpr int kManyPerSm = 1;
+constexpr int kManyExtra = 8;                       // an item's start and end: 8 units' time (measured 18000 cycles)
 
 template <int D, bool WIDE>
 struct Many {
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   KvWalk w;
   int Gc, q0;
   long long U;
-  const bool any = kv_range<kManyThreads, kRows, kManyUnit>(a, w, Gc, U, q0);
+  const bool any = kv_range<kManyThreads, kRows, kManyUnit, kManyExtra>(a, w, Gc, U, q0);
   bool ok = true;   // no wait ran out
 
   if (any && warp >= (WIDE ? 4 : 8) && warp < 14) {   // ---- loaders
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         o += kLoaders;
       }
       it0 += w.k1 - w.k0;
-      if (ok) more = kv_advance<kRows, kManyUnit>(a, w, q0);
+      if (ok) more = kv_advance<kRows, kManyUnit, kManyExtra>(a, w, q0);
     }
     if (!ok) {
       flags[0] = 1;
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       }
       buf = (buf + n) % kBufs;
       sbuf = (sbuf + n) & 1;
-      if (ok) more = uniform(kv_advance<kRows, kManyUnit>(a, w, q0));
+      if (ok) more = uniform(kv_advance<kRows, kManyUnit, kManyExtra>(a, w, q0));
     }
     if (!ok) {
       flags[0] = 1;
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     for (bool more = true; more;) {
       const KvWalk v = w;
       const int vq0 = q0;
-      more = kv_advance<kRows, kManyUnit>(a, w, q0);
+      more = kv_advance<kRows, kManyUnit, kManyExtra>(a, w, q0);
       if (!tile_there(v)) {   // a short row tile: the other warps' alone
         it += v.k1 - v.k0;
         if (more) {
@@ -765,8 +766,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       } else {
         part[row] = m;
         part[kManyTile + row] = l;
-        const long long x0 = v.x - v.k0;
-        const int c0 = tc_owner(x0, U, Gc), parts = tc_owner(x0 + v.units - 1, U, Gc) - c0 + 1;
+        const int c0 = kv_owner(v.first, U, Gc), parts = kv_owner(v.first + v.units - 1, U, Gc) - c0 + 1;
         __threadfence();
         rows_agree(x, true);
         if (row == 0) {
