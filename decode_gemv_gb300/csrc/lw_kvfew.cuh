@@ -147,7 +147,7 @@ __device__ __forceinline__ void load_q8(const AttnArgs& a, int64_t at, float (&x
 struct FewRow {
   float f;          // log2 units per unit of the scaled product
   int lo, hi;       // keys it sees
-  float m, mu, l;   // running maximum (log2 units), the same or 0, sum
+  float m, mu, l;   // running maximum (log2 units), the same (or 0) plus E, sum
 };
 
 template <int D, int MODE>
@@ -161,8 +161,8 @@ struct FewWarp {
   // and 2, 3) of rows 2 q, 2 q + 1 (and 8 more for the second NR); om: sums of
   // the middles of group lane / 4 (hi parts; lane / 4 - 4: lo parts)
   float o[NR][G][2][4], om[NR][4];
-  float unit;       // 2^E: p sc 2^-E is the operand (E <= 0 in MODE 1, 2, where om has the factor too)
-  uint32_t most;    // the largest scale it allows, twice
+  float unit;       // 2^E, E <= 0: the operands and all sums are of p 2^-E
+  uint32_t seen;    // exponent bits of the scales so far, of even and of odd keys
   float fm;         // row[0].m when the sums last went to shared memory (MODE 0)
 
   // Row r of the row tile (lane / 4, and lane / 4 + 8 in MODE 1)
@@ -190,13 +190,17 @@ struct FewWarp {
     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
     int e = (int)(__float_as_uint(top) >> 23) - 127;
     e = e < -100 ? -100 : (e > 126 ? 126 : e);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e
+    // 2^-e, with the sign of the scale: the largest product is the largest score
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23 | (__float_as_uint(a.p.scale) & 0x80000000u));
     FewRow& s = row[which];
     // products carry the codes' power of two and 2^-e
-    s.f = a.p.scale * 1.4426950408889634f * (MODE == 0 ? 1024.f : 16777216.f) * __uint_as_float((uint32_t)(127 + e) << 23);
+    // (never 0: a masked score times it stays -inf)
+    s.f = fmaxf(fabsf(a.p.scale) * 1.4426950408889634f * (MODE == 0 ? 1024.f : 16777216.f) *
+                    __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
     kv_token_keys(w.T, w.n, t, a.p.causal, a.p.window, s.lo, s.hi);
     s.m = -INFINITY;
-    s.mu = s.l = 0.f;
+    s.mu = -14.f;   // (E of the first unit)
+    s.l = 0.f;
     float sum[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -240,7 +244,7 @@ struct FewWarp {
     for (int i = 0; i < NR; ++i) load_row(a, w, q0, rt_rows, i, lane);
     clear();
     unit = 6.103515625e-5f;   // 2^-14
-    most = 0;
+    seen = 0;
     fm = -INFINITY;
   }
   __device__ __forceinline__ void clear() {
@@ -255,232 +259,272 @@ struct FewWarp {
     }
   }
 
-  // One tile of 16 keys, keys kb..kb+15.  EDGE: some row does not see some of
-  // them (those may hold any bits).
-  template <bool EDGE>
-  __device__ __forceinline__ void tile(uint32_t s, int kb, int n, int lane) {
+  // NT tiles of 16 keys, keys kb .. kb + 16 NT - 1.  EDGE: some row does not see
+  // some of them (those may hold any bits).
+  template <bool EDGE, int NT>
+  __device__ __forceinline__ void tiles(uint32_t s, int kb, int n, int lane) {
     const int q = lane % 4, r = lane / 4;
-    float t[NR][4];
-    uint32_t see[NR];
+    float2 t[NT][NR][2];   // scores: keys 2 q, 2 q + 1 of the tile, and 8 more
+    uint32_t see[NT][NR];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {   // 8 keys each
-      float c[4];
-      uint32_t mn = 0;
-      if (2 * q < L::GP) mn = lds_u32(s + L::kKeyMin + (uint32_t)((8 * h + r) * L::GP + 2 * q) * 2);
-      if (G % 2 && q == G / 2) mn &= 0xFFFFu;
-      mma_f16_zero(c, am[0], MODE == 2 ? 0u : am[MODE == 2 ? 0 : 1], 0u, 0u, mn, 0u);
-      constexpr float kUnit = MODE == 0 ? 9.765625e-4f : 5.9604644775390625e-8f;   // as the codes' products
-      float2 x = mul2(make_float2(c[0], c[1]), make_float2(kUnit, kUnit));
-      float2 y = mul2(make_float2(c[2], c[3]), make_float2(kUnit, kUnit));
-      uint32_t kw[G], sw[G];
-      lds_words<G>(s + L::kKeyCodes + (uint32_t)(((8 * h + r) * 4 + q) * G) * 4, kw);
-      lds_words<G>(s + L::kKeyScale + (uint32_t)((4 * h + q) * G) * 4, sw);
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        float d[4];
-        const uint32_t w = kw[g] >> 8;
-        if constexpr (MODE == 2) {
-          mma_f16_zero(d, aq[g][0][0], 0u, aq[g][0][1], 0u, code_even<MODE>(kw[g]), code_odd<MODE>(kw[g]));
-          mma_f16(d, aq[g][1][0], 0u, aq[g][1][1], 0u, code_even<MODE>(w), code_odd<MODE>(w));
-        } else {
-          mma_f16_zero(d, aq[g][0][0], aq[g][0][1], aq[g][0][2], aq[g][0][3], code_even<MODE>(kw[g]),
-                       code_odd<MODE>(kw[g]));
-          mma_f16(d, aq[g][1][0], aq[g][1][1], aq[g][1][2], aq[g][1][3], code_even<MODE>(w), code_odd<MODE>(w));
+      for (int h = 0; h < 2; ++h) {   // 8 keys each
+        const uint32_t at = s + (uint32_t)(i * L::kBytes);
+        float c[4];
+        uint32_t mn = 0;
+        if (2 * q < L::GP) mn = lds_u32(at + L::kKeyMin + (uint32_t)((8 * h + r) * L::GP + 2 * q) * 2);
+        if (G % 2 && q == G / 2) mn &= 0xFFFFu;
+        mma_f16_zero(c, am[0], MODE == 2 ? 0u : am[MODE == 2 ? 0 : 1], 0u, 0u, mn, 0u);
+        constexpr float kUnit = MODE == 0 ? 9.765625e-4f : 5.9604644775390625e-8f;   // as the codes' products
+        float2 x = mul2(make_float2(c[0], c[1]), make_float2(kUnit, kUnit));
+        float2 y = mul2(make_float2(c[2], c[3]), make_float2(kUnit, kUnit));
+        uint32_t kw[G], sw[G];
+        lds_words<G>(at + L::kKeyCodes + (uint32_t)(((8 * h + r) * 4 + q) * G) * 4, kw);
+        lds_words<G>(at + L::kKeyScale + (uint32_t)((4 * h + q) * G) * 4, sw);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float d[4];
+          const uint32_t w = kw[g] >> 8;
+          if constexpr (MODE == 2) {
+            mma_f16_zero(d, aq[g][0][0], 0u, aq[g][0][1], 0u, code_even<MODE>(kw[g]), code_odd<MODE>(kw[g]));
+            mma_f16(d, aq[g][1][0], 0u, aq[g][1][1], 0u, code_even<MODE>(w), code_odd<MODE>(w));
+          } else {
+            mma_f16_zero(d, aq[g][0][0], aq[g][0][1], aq[g][0][2], aq[g][0][3], code_even<MODE>(kw[g]),
+                         code_odd<MODE>(kw[g]));
+            mma_f16(d, aq[g][1][0], aq[g][1][1], aq[g][1][2], aq[g][1][3], code_even<MODE>(w), code_odd<MODE>(w));
+          }
+          const float2 sc = h2f(sw[g]);
+          x = fma2(sc, make_float2(d[0], d[1]), x);
+          if constexpr (MODE != 2) y = fma2(sc, make_float2(d[2], d[3]), y);
         }
-        const float2 sc = h2f(sw[g]);
-        x = fma2(sc, make_float2(d[0], d[1]), x);
-        if constexpr (MODE != 2) y = fma2(sc, make_float2(d[2], d[3]), y);
+        if constexpr (MODE == 0) x = fma2(y, make_float2(4.8828125e-4f, 4.8828125e-4f), x);   // 2^-11
+        t[i][0][h] = x;
+        if constexpr (NR == 2) t[i][NR - 1][h] = y;
       }
-      if constexpr (MODE == 0) x = fma2(y, make_float2(4.8828125e-4f, 4.8828125e-4f), x);   // 2^-11
-      c[0] = x.x;
-      c[1] = x.y;
-      c[2] = y.x;
-      c[3] = y.y;
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        t[i][2 * h] = c[2 * i] * row[i].f;
-        t[i][2 * h + 1] = c[2 * i + 1] * row[i].f;
-      }
-    }
     bool up = false;
+    float top[NR];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      if constexpr (EDGE) {
-        see[i] = 0;
+    for (int j = 0; j < NR; ++j) {
+      top[j] = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int key = kb + 8 * (j / 2) + 2 * q + j % 2;
-          if (key >= row[i].lo && key < row[i].hi) see[i] |= 1u << j;
-          else t[i][j] = -INFINITY;
+      for (int i = 0; i < NT; ++i) {
+        if constexpr (EDGE) {
+          see[i][j] = 0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int key = kb + 16 * i + 8 * (u / 2) + 2 * q + u % 2;
+            float& z = u % 2 ? t[i][j][u / 2].y : t[i][j][u / 2].x;
+            if (key >= row[j].lo && key < row[j].hi) see[i][j] |= 1u << u;
+            else z = -INFINITY;
+          }
         }
+        top[j] = fmaxf(fmaxf(top[j], t[i][j][0].x), t[i][j][0].y);
+        top[j] = fmaxf(fmaxf(top[j], t[i][j][1].x), t[i][j][1].y);
       }
-      up |= fmaxf(fmaxf(t[i][0], t[i][1]), fmaxf(t[i][2], t[i][3])) > row[i].m;
+      top[j] *= row[j].f;
+      up |= top[j] > row[j].m;
     }
-    uint32_t v0[G], v1[G], s0[G], s1[G];
-    lds_words<G>(s + L::kValScale + (uint32_t)(q * G) * 4, s0);
-    lds_words<G>(s + L::kValScale + (uint32_t)((q + 4) * G) * 4, s1);
-    if constexpr (EDGE) {   // what lies past the end may be anything
-      const auto cut = [&](uint32_t w, int key) {
-        return (key < n ? w & 0xFFFFu : 0u) | (key + 1 < n ? w & 0xFFFF0000u : 0u);
-      };
+    // the value operands' unit covers the largest scale so far: new exponent bits are looked at (a
+    // scale of bits seen before is at most 2^15 times the largest, and 2^15 stays in range)
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint32_t at = s + (uint32_t)(i * L::kBytes + L::kValScale);
+      uint32_t s0[G], s1[G];
+      lds_words<G>(at + (uint32_t)(q * G) * 4, s0);
+      lds_words<G>(at + (uint32_t)((q + 4) * G) * 4, s1);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        s0[g] = cut(s0[g], kb + 2 * q);
-        s1[g] = cut(s1[g], kb + 8 + 2 * q);
+        if constexpr (EDGE) {
+          s0[g] = cut(s0[g], kb + 16 * i + 2 * q, n);
+          s1[g] = cut(s1[g], kb + 16 * i + 8 + 2 * q, n);
+        }
+        bits |= s0[g] | s1[g];
       }
     }
-    // the operands' unit covers the largest scale so far
-    uint32_t big = max_h2(s0[0], s1[0]);
-#pragma unroll
-    for (int g = 1; g < G; ++g) big = max_h2(big, max_h2(s0[g], s1[g]));
-    up |= max_h2(big, most) != most;
+    up |= (bits & 0x7C007C00u & ~seen) != 0;
     if (__any_sync(0xFFFFFFFFu, up)) {   // a new maximum: rescale
       float al[NR];
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        float x = fmaxf(fmaxf(t[i][0], t[i][1]), fmaxf(t[i][2], t[i][3]));
+      for (int j = 0; j < NR; ++j) {
+        float x = top[j];
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-        x = fmaxf(x, row[i].m);
-        row[i].mu = x == -INFINITY ? 0.f : x;
-        al[i] = ex2(row[i].m - row[i].mu);
-        row[i].m = x;
-        row[i].l *= al[i];
+        x = fmaxf(x, row[j].m);
+        const float mu = x == -INFINITY ? 0.f : x;
+        al[j] = ex2(row[j].m - mu);
+        row[j].m = x;
       }
+      // the largest scale of the tiles (a NaN is none)
+      uint32_t big = 0;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {   // to the lanes that hold the rows' sums
-        const float a0 = __shfl_sync(0xFFFFFFFFu, al[i], 8 * q), a1 = __shfl_sync(0xFFFFFFFFu, al[i], 8 * q + 4);
+      for (int i = 0; i < NT; ++i) {
+        const uint32_t at = s + (uint32_t)(i * L::kBytes + L::kValScale);
+        uint32_t s0[G], s1[G];
+        lds_words<G>(at + (uint32_t)(q * G) * 4, s0);
+        lds_words<G>(at + (uint32_t)((q + 4) * G) * 4, s1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float x = j % 2 ? a1 : a0;
-          om[i][j] *= x;
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            o[i][g][0][j] *= x;
-            o[i][g][1][j] *= x;
+        for (int g = 0; g < G; ++g) {
+          if constexpr (EDGE) {
+            s0[g] = cut(s0[g], kb + 16 * i + 2 * q, n);
+            s1[g] = cut(s1[g], kb + 16 * i + 8 + 2 * q, n);
           }
+          big = max_h2(big, max_h2(s0[g], s1[g]));
         }
       }
 #pragma unroll
-      for (int d = 1; d < 4; d <<= 1) big = max_h2(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
-      big = max_h2(big, most);
-      uint32_t top = big & 0xFFFFu, t2 = big >> 16;   // scales are positive, or NaN
-      top = top > 0x7C00u ? 0u : top;
-      if (t2 <= 0x7C00u && t2 > top) top = t2;
+      for (int d = 1; d < 4; d <<= 1) {
+        big = max_h2(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
+        bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, d);
+      }
+      seen |= bits;
+      uint32_t e = max(big & 0x7FFFu, big >> 16 & 0x7FFFu) >> 10;
+      e = e < 1 ? 1 : (e > 15 ? 15 : e);
       const float before = unit;
-      most = ((top >> 10) << 10 | 0x3FFu) * 0x10001u;
-      int e = (int)(top >> 10) < 1 ? 1 : (int)(top >> 10);
-      if (MODE != 0 && e > 15) e = 15;
-      unit = __uint_as_float((uint32_t)(e + 112) << 23);
+      unit = fmaxf(unit, __uint_as_float((e + 112) << 23));
       const float down = before * __uint_as_float(0x7F000000u - __float_as_uint(unit));
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
+      for (int j = 0; j < NR; ++j) {
+        al[j] *= down;
+        row[j].l *= al[j];
+        // (E log2 units more: p 2^-E comes out of the exponential)
+        row[j].mu = (row[j].m == -INFINITY ? 0.f : row[j].m) + (float)((int)(__float_as_uint(unit) >> 23) - 127);
+        // to the lanes that hold the rows' sums
+        const float a0 = __shfl_sync(0xFFFFFFFFu, al[j], 8 * q), a1 = __shfl_sync(0xFFFFFFFFu, al[j], 8 * q + 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (MODE != 0) om[i][j] *= down;
+        for (int u = 0; u < 4; ++u) {
+          const float x = u % 2 ? a1 : a0;
+          om[j][u] *= x;
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            o[i][g][0][j] *= down;
-            o[i][g][1][j] *= down;
+            o[j][g][0][u] *= x;
+            o[j][g][1][u] *= x;
           }
         }
-    }
-    const float inv = __uint_as_float(0x7F000000u - __float_as_uint(unit));   // 2^-E
-    float p[NR][4];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[i][j] = ex2(t[i][j] - row[i].mu);
-      row[i].l += (p[i][0] + p[i][1]) + (p[i][2] + p[i][3]);
-    }
-    float2 pe[NR][2];       // p 2^-E
-    uint32_t ph[NR][2];     // the same in fp16 (MODE 1, 2)
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        pe[i][j] = mul2(make_float2(p[i][2 * j], p[i][2 * j + 1]), make_float2(inv, inv));
-        ph[i][j] = h2bits(__floats2half2_rn(pe[i][j].x, pe[i][j].y));
       }
-    {   // middles: rows of this instruction are groups, their hi parts, then their lo parts
-      uint32_t a0 = 0, a2 = 0;
-      if (MODE == 0 ? r % 4 < G : r < G) {
-        const auto middle = [&](int pair, int key) {
-          const float2 mn = h2f(lds_u32(s + L::kValMin + (uint32_t)(pair * G + r % 4) * 4));
-          const float2 sc = h2f(lds_u32(s + L::kValScale + (uint32_t)(pair * G + r % 4) * 4));
-          float x = fmaf(8.f, sc.x, mn.x), y = fmaf(8.f, sc.y, mn.y);
-          if constexpr (EDGE) {   // 0 x a masked key's bits has to be 0; a NaN group's scale shows it
-            if (key >= n || isnan(x)) x = 0.f;
-            if (key + 1 >= n || isnan(y)) y = 0.f;
-          }
-          if constexpr (MODE != 0) return h2bits(__floats2half2_rn(x, y));
-          uint32_t hi, lo;
-          split2<2048>(x, y, hi, lo);
-          return r < 4 ? hi : lo;
-        };
-        a0 = middle(q, kb + 2 * q);
-        a2 = middle(q + 4, kb + 8 + 2 * q);
-      }
+    }
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        if constexpr (MODE == 0) {
-          uint32_t b0, b1, c0, c1;
-          split2<1>(p[i][0], p[i][1], b0, c0);
-          split2<1>(p[i][2], p[i][3], b1, c1);
-          mma_f16(om[i], a0, 0u, a2, 0u, c0, c1);
-          mma_f16(om[i], a0, 0u, a2, 0u, b0, b1);
-        } else {
-          mma_f16(om[i], a0, 0u, a2, 0u, ph[i][0], ph[i][1]);
+    for (int i = 0; i < NT; ++i) {
+      const uint32_t at = s + (uint32_t)(i * L::kBytes);
+      float2 p[NR][2];        // p 2^-E
+      uint32_t ph[NR][2];     // the same in fp16
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        const float2 f2 = make_float2(row[j].f, row[j].f), mu2 = make_float2(-row[j].mu, -row[j].mu);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 z = fma2(t[i][j][h], f2, mu2);
+          p[j][h] = make_float2(ex2(z.x), ex2(z.y));
+          ph[j][h] = h2bits(__floats2half2_rn(p[j][h].x, p[j][h].y));
         }
+        row[j].l += (p[j][0].x + p[j][0].y) + (p[j][1].x + p[j][1].y);
       }
-    }
-    lds_words<G>(s + L::kValCodes + (uint32_t)((q * 8 + r) * G) * 4, v0);
-    lds_words<G>(s + L::kValCodes + (uint32_t)(((q + 4) * 8 + r) * G) * 4, v1);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      uint32_t b0[NR], b1[NR], c0[NR], c1[NR];
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        if constexpr (MODE == 0) {
-          const float2 ux = mul2(pe[i][0], h2f(s0[g])), uy = mul2(pe[i][1], h2f(s1[g]));
-          float u[4] = {ux.x, ux.y, uy.x, uy.y};
-          if constexpr (EDGE) {   // a NaN that this row does not see
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (!(see[i] >> j & 1u)) u[j] = 0.f;
-          }
-          split2<1>(u[0], u[1], b0[i], c0[i]);
-          split2<1>(u[2], u[3], b1[i], c1[i]);
-        } else {
-          b0[i] = mul_h2(ph[i][0], s0[g]);
-          b1[i] = mul_h2(ph[i][1], s1[g]);
+      if constexpr (MODE == 0) {   // middles: rows of this instruction are groups, hi parts, then lo parts
+        uint32_t a0 = 0, a2 = 0;
+        if (r % 4 < G) {
+          const auto middle = [&](int pair, int key) {
+            const float2 mn = h2f(lds_u32(at + L::kValMin + (uint32_t)(pair * G + r % 4) * 4));
+            const float2 sc = h2f(lds_u32(at + L::kValScale + (uint32_t)(pair * G + r % 4) * 4));
+            float x = fmaf(8.f, sc.x, mn.x), y = fmaf(8.f, sc.y, mn.y);
+            if constexpr (EDGE) {   // 0 x a masked key's bits has to be 0; a NaN group's scale shows it
+              if (key >= n || isnan(x)) x = 0.f;
+              if (key + 1 >= n || isnan(y)) y = 0.f;
+            }
+            uint32_t hi, lo;
+            split2<2048>(x, y, hi, lo);
+            return r < 4 ? hi : lo;
+          };
+          a0 = middle(q, kb + 16 * i + 2 * q);
+          a2 = middle(q + 4, kb + 16 * i + 8 + 2 * q);
+        }
+        uint32_t b0, b1, c0, c1;
+        split2<1>(p[0][0].x, p[0][0].y, b0, c0);
+        split2<1>(p[0][1].x, p[0][1].y, b1, c1);
+        mma_f16(om[0], a0, 0u, a2, 0u, c0, c1);
+        mma_f16(om[0], a0, 0u, a2, 0u, b0, b1);
+      } else {   // minimums and scales: rows 0..3 and 4..7; joined in fp32 tile by tile (their sums cancel)
+        uint32_t a0 = 0, a2 = 0;
+        if (r % 4 < G) {
+          const uint32_t from = at + (r < 4 ? L::kValMin : L::kValScale) + (uint32_t)(r % 4) * 4;
+          a0 = lds_u32(from + (uint32_t)(q * G) * 4);
+          a2 = lds_u32(from + (uint32_t)((q + 4) * G) * 4);
           if constexpr (EDGE) {
-            b0[i] &= (see[i] & 1u ? 0xFFFFu : 0u) | (see[i] & 2u ? 0xFFFF0000u : 0u);
-            b1[i] &= (see[i] & 4u ? 0xFFFFu : 0u) | (see[i] & 8u ? 0xFFFF0000u : 0u);
+            a0 = clean(cut(a0, kb + 16 * i + 2 * q, n));
+            a2 = clean(cut(a2, kb + 16 * i + 8 + 2 * q, n));
           }
         }
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+          float c[4];
+          mma_f16_zero(c, a0, 0u, a2, 0u, ph[j][0], ph[j][1]);
+          om[j][0] += fmaf(8.f, __shfl_down_sync(0xFFFFFFFFu, c[0], 16), c[0]);
+          om[j][1] += fmaf(8.f, __shfl_down_sync(0xFFFFFFFFu, c[1], 16), c[1]);
+        }
       }
+      uint32_t v0[G], v1[G], s0[G], s1[G];
+      lds_words<G>(at + L::kValScale + (uint32_t)(q * G) * 4, s0);
+      lds_words<G>(at + L::kValScale + (uint32_t)((q + 4) * G) * 4, s1);
+      lds_words<G>(at + L::kValCodes + (uint32_t)((q * 8 + r) * G) * 4, v0);
+      lds_words<G>(at + L::kValCodes + (uint32_t)(((q + 4) * 8 + r) * G) * 4, v1);
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const uint32_t w0 = v0[g] >> (8 * st), w1 = v1[g] >> (8 * st);
-        const uint32_t a0 = centre_even(w0), a1 = centre_odd(w0), a2 = centre_even(w1), a3 = centre_odd(w1);
+      for (int g = 0; g < G; ++g) {
+        if constexpr (EDGE) {   // what lies past the end may be anything
+          s0[g] = cut(s0[g], kb + 16 * i + 2 * q, n);
+          s1[g] = cut(s1[g], kb + 16 * i + 8 + 2 * q, n);
+        }
+        uint32_t b0[NR], b1[NR], c0[NR], c1[NR];
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          if constexpr (MODE == 0) mma_f16(o[i][g][st], a0, a1, a2, a3, c0[i], c1[i]);
-          mma_f16(o[i][g][st], a0, a1, a2, a3, b0[i], b1[i]);
+        for (int j = 0; j < NR; ++j) {
+          if constexpr (MODE == 0) {
+            const float2 ux = mul2(p[j][0], h2f(s0[g])), uy = mul2(p[j][1], h2f(s1[g]));
+            float u[4] = {ux.x, ux.y, uy.x, uy.y};
+            if constexpr (EDGE) {   // a NaN that this row does not see
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (!(see[i][j] >> k & 1u)) u[k] = 0.f;
+            }
+            split2<1>(u[0], u[1], b0[j], c0[j]);
+            split2<1>(u[2], u[3], b1[j], c1[j]);
+          } else {
+            b0[j] = mul_h2(ph[j][0], s0[g]);
+            b1[j] = mul_h2(ph[j][1], s1[g]);
+            if constexpr (EDGE) {
+              b0[j] &= (see[i][j] & 1u ? 0xFFFFu : 0u) | (see[i][j] & 2u ? 0xFFFF0000u : 0u);
+              b1[j] &= (see[i][j] & 4u ? 0xFFFFu : 0u) | (see[i][j] & 8u ? 0xFFFF0000u : 0u);
+            }
+          }
+        }
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const uint32_t w0 = v0[g] >> (8 * st), w1 = v1[g] >> (8 * st);
+          const uint32_t a0 = centre_even(w0), a1 = centre_odd(w0), a2 = centre_even(w1), a3 = centre_odd(w1);
+#pragma unroll
+          for (int j = 0; j < NR; ++j) {
+            if constexpr (MODE == 0) mma_f16(o[j][g][st], a0, a1, a2, a3, c0[j], c1[j]);
+            mma_f16(o[j][g][st], a0, a1, a2, a3, b0[j], b1[j]);
+          }
         }
       }
     }
   }
 
+  // A pair of keys' halves, 0 past the end; the same without NaN
+  static __device__ __forceinline__ uint32_t cut(uint32_t w, int key, int n) {
+    return (key < n ? w & 0xFFFFu : 0u) | (key + 1 < n ? w & 0xFFFF0000u : 0u);
+  }
+  static __device__ __forceinline__ uint32_t clean(uint32_t w) {
+    return ((w & 0x7FFFu) > 0x7C00u ? 0u : w & 0xFFFFu) | ((w & 0x7FFF0000u) > 0x7C000000u ? 0u : w & 0xFFFF0000u);
+  }
+
   // This lane's elements 32 g + 4 (lane / 4) + 0..3 of row 2 q + e (and 8 which),
   // in true units
   __device__ __forceinline__ float4 finish(int which, int g, int e, int lane) const {
-    // the lanes with this group's hi and lo parts for rows 2 q, 2 q + 1
+    // the lanes with this group's sums (MODE 0: and their lo parts) for rows 2 q, 2 q + 1
     float mn = __shfl_sync(0xFFFFFFFFu, om[which][e], 4 * g + lane % 4);
     if constexpr (MODE == 0)
       mn = fmaf(__shfl_sync(0xFFFFFFFFu, om[which][e], 16 + 4 * g + lane % 4), 4.8828125e-4f, mn);
-    if constexpr (MODE != 0) mn *= unit;
+    mn *= unit;
     const float up = 1024.f * unit;
     return make_float4(fmaf(o[which][g][0][e], up, mn), fmaf(o[which][g][0][2 + e], up, mn),
                        fmaf(o[which][g][1][e], up, mn), fmaf(o[which][g][1][2 + e], up, mn));
@@ -491,7 +535,7 @@ struct FewWarp {
   // warp's 8 rows.
   __device__ __forceinline__ void put(int which, int lane, float* at) const {
     const int q = lane % 4;
-    const float held = MODE == 0 ? (fm == -INFINITY ? 0.f : ex2(fm - row[0].mu)) : 0.f;
+    const float held = MODE == 0 ? (fm == -INFINITY ? 0.f : ex2(fm - (row[0].m == -INFINITY ? 0.f : row[0].m))) : 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float h = MODE == 0 ? __shfl_sync(0xFFFFFFFFu, held, 8 * q + 4 * e) : 0.f;
@@ -647,15 +691,18 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
           f.flush(lane, mine);
           held = 0;
         }
-        uint32_t at = smem_addr(t.ring) + 2 * t.out * L::kBytes;
-        int kb = tile * LW_KV_TILE;
+        const uint32_t at = smem_addr(t.ring) + 2 * t.out * L::kBytes;
+        const int kb = tile * LW_KV_TILE;
         if (two == 3u && kb >= all_lo && kb + 2 * LW_KV_TILE <= all_hi) {
+          // (both at once where their operands fit the registers)
+          constexpr int kAtOnce = D == 64 ? 2 : 1;
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i, at += L::kBytes, kb += LW_KV_TILE) f.template tile<false>(at, kb, w.n, lane);
+          for (int i = 0; i < 2; i += kAtOnce)
+            f.template tiles<false, kAtOnce>(at + i * L::kBytes, kb + i * LW_KV_TILE, w.n, lane);
         } else {
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i, at += L::kBytes, kb += LW_KV_TILE)
-            if (two >> i & 1u) f.template tile<true>(at, kb, w.n, lane);
+          for (int i = 0; i < 2; ++i)
+            if (two >> i & 1u) f.template tiles<true, 1>(at + i * L::kBytes, kb + i * LW_KV_TILE, w.n, lane);
         }
         held += 2;
         __syncwarp();
@@ -674,7 +721,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
     float* part = a.partials + ((size_t)blockIdx.x * 2 + (v.k0 == 0)) * F::kPartial;
 #pragma unroll
     for (int i = 0; i < FewWarp<D, MODE>::NR; ++i) {
-      float l = f.row[i].l;
+      float l = f.row[i].l * f.unit;
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
       if (lane % 4 == 0) {
