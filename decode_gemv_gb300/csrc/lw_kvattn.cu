@@ -14,9 +14,9 @@ struct Variant {
 };
 template <int D>
 Variant variant(int mode) {
-  if (mode == 0) return {dev::kv_few_kernel<D, 0>, kFewThreads, kFewPerSm, Few<D, 0>::kSmem};
-  if (mode == 1) return {dev::kv_few_kernel<D, 1>, kFewThreads, kFewPerSm, Few<D, 1>::kSmem};
-  if (mode == 2) return {dev::kv_few_kernel<D, 2>, kFewThreads, kFewPerSm, Few<D, 2>::kSmem};
+  if (mode == 0) return {dev::kv_few_kernel<D, 0>, Few<D, 0>::kThreads, Few<D, 0>::kPerSm, Few<D, 0>::kSmem};
+  if (mode == 1) return {dev::kv_few_kernel<D, 1>, Few<D, 1>::kThreads, Few<D, 1>::kPerSm, Few<D, 1>::kSmem};
+  if (mode == 2) return {dev::kv_few_kernel<D, 2>, Few<D, 2>::kThreads, Few<D, 2>::kPerSm, Few<D, 2>::kSmem};
   if (mode == 3) return {dev::kv_many_kernel<D, false>, kManyThreads, kManyPerSm, Many<D, false>::kSmem};
   return {dev::kv_many_kernel<D, true>, kManyThreads, kManyPerSm, Many<D, true>::kSmem};
 }
@@ -24,13 +24,16 @@ Variant variant(int mode) {
 // The workspace: counters and partial results of the most resident CTAs of a
 // launch (counts of either kernel: a counter, and two parts of an item, a CTA;
 // twice that for the two row tiles of kv_many_kernel).
-inline size_t attn_counter_bytes() { return ((size_t)2 * device_sm_count() * 4 + 255) / 256 * 256; }
-static_assert(kFewPerSm <= 2 && kManyPerSm == 1, "workspace places");
+constexpr int kMostPerSm = 2;
+inline size_t attn_counter_bytes() { return ((size_t)kMostPerSm * device_sm_count() * 4 + 255) / 256 * 256; }
+static_assert(Few<64, 0>::kPerSm <= kMostPerSm && Few<64, 1>::kPerSm <= kMostPerSm && Few<64, 2>::kPerSm <= kMostPerSm &&
+                  2 * kManyPerSm <= kMostPerSm,
+              "workspace places");
 
 }  // namespace
 
 size_t kv_attention_workspace(const lw_kv_cache* c) {
-  const size_t few = (size_t)kFewPerSm * 2 * 16, many = (size_t)2 * 2 * kManyTile;   // rows an SM
+  const size_t few = (size_t)kMostPerSm * 2 * 16, many = (size_t)2 * 2 * kManyTile;   // rows an SM
   return attn_counter_bytes() + (size_t)device_sm_count() * (few > many ? few : many) * (size_t)(c->head_dim + 2) * 4;
 }
 

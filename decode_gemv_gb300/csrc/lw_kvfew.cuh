@@ -30,36 +30,42 @@
 // shared memory rounded to nearest (the truncation of many steps is a drift,
 // not a scatter).
 //
-// Structure.  A CTA walks its range of units (lw_kvplan.h).  Warp w takes
-// every kFewWarps-th pair of 16-key tiles, fetched by bulk copies into a ring of its
-// own, and keeps its own running maximum, sum and accumulators (one pass over
-// the data) until the item ends; then the next item's first tiles are sent
-// for, and the warps' states are joined in shared memory.  An item cut between
-// CTAs leaves partial states in the workspace, and the CTA that brings the
-// item's count to its end joins them, in CTA order (the answer does not depend
-// on the order of arrival).
+// Structure.  A CTA walks its range of units (lw_kvplan.h).  Its warps take the
+// 16-key tiles in turn, fetched by bulk copies into a ring of their own, and each
+// keeps its own running maximum, sum and accumulators (one pass over the data)
+// until the item ends; then the next item's first tiles are sent for, and the
+// warps' states are joined in shared memory.  An item cut between CTAs leaves
+// partial states in the workspace, and the CTA that brings the item's count to
+// its end joins them, in CTA order (the answer does not depend on the order of
+// arrival).
 #pragma once
 
 #include "lw_kvattn.cuh"
 
 namespace lw {
 
-constexpr int kFewWarps = 8;                        // warps of a CTA
-constexpr int kFewThreads = 32 * kFewWarps;
-constexpr int kFewPerSm = 2;                        // resident CTAs
-constexpr int kFewStages = 2;                       // places of a warp's ring, two tiles each
-constexpr int kFewUnit = 2 * kFewWarps;             // tiles of a unit
-constexpr int kFewExtra = 3;                        // an item's start and end: 3 units' time
 constexpr int kFewFlush = 32;                       // tiles between two additions (MODE 0)
+constexpr int kFewExtra = 6;                        // an item's start and end: 6 units' time
 
 template <int D, int MODE>
 struct Few {
   using L = KvTile<D>;
+  // 16 warps an SM, as the registers allow.  Four CTAs of 4 warps instead of two
+  // of 8: 256 sequences of 100 keys 43 -> 36 us, but 38 of 8192 94 -> 104 us and
+  // one of 4097 15 -> 18 us (more items cut, more parts to join); 20 warps of 96
+  // registers: 8 of 65536 159 -> 264 us (spills).
+  static constexpr int kWarps = 8, kPerSm = 2, kThreads = 32 * kWarps;
+  // tiles a warp takes at once: two where their operands fit the registers
+  // (8 sequences of 65536 keys, 64 wide: 104 -> 89 us; 128 wide 157 -> 173 us)
+  static constexpr int kPair = D == 64 ? 2 : 1;
+  static constexpr int kStages = D == 64 ? 2 : 3;    // places of a warp's ring
+  static constexpr int kUnit = kWarps * kPair;       // tiles of a unit
   static constexpr int kRows = MODE == 1 ? 16 : 8;   // rows of an item
+  static constexpr int kJoin = MODE == 0 ? 8 : 4;    // of them joined at a time
   static constexpr int kRing = 256;                  // after the barriers and the flag
-  static constexpr int kJoin = kRing + kFewWarps * kFewStages * 2 * L::kBytes;
-  static constexpr int kState = kJoin + kFewWarps * 8 * D * 4;   // m, l [warps][8]
-  static constexpr int kNeed = kState + 2 * kFewWarps * 8 * 4;
+  static constexpr int kSums = kRing + kWarps * kStages * kPair * L::kBytes;   // [warps][kJoin][D]
+  static constexpr int kState = kSums + kWarps * kJoin * D * 4;           // m, l [warps][8]
+  static constexpr int kNeed = kState + 2 * kWarps * 8 * 4;
   // above the limit that holds without an attribute (static shared memory counts towards it)
   static constexpr int kSmem = kNeed > 49168 ? kNeed : 49168;
   static constexpr int kPartial = kRows * (D + 2);   // floats: m, l, then the rows
@@ -530,10 +536,10 @@ struct FewWarp {
                        fmaf(o[which][g][1][e], up, mn), fmaf(o[which][g][1][2 + e], up, mn));
   }
 
-  // Add the sums of rows 8 which .. 8 which + 7 to what shared memory holds of
-  // them (MODE 0; nothing before the first time) or put them there.  at: the
-  // warp's 8 rows.
-  __device__ __forceinline__ void put(int which, int lane, float* at) const {
+  // Put the sums of the 8 rows (8 `which` ..) into shared memory, or add them to
+  // what it holds of them (MODE 0, after a flush); outside MODE 0 rows 4 part ..
+  // 4 part + 3 alone.  at: the warp's rows there.
+  __device__ __forceinline__ void put(int which, int part, int lane, float* at) const {
     const int q = lane % 4;
     const float held = MODE == 0 ? (fm == -INFINITY ? 0.f : ex2(fm - (row[0].m == -INFINITY ? 0.f : row[0].m))) : 0.f;
 #pragma unroll
@@ -541,18 +547,19 @@ struct FewWarp {
       const float h = MODE == 0 ? __shfl_sync(0xFFFFFFFFu, held, 8 * q + 4 * e) : 0.f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        float4* to = reinterpret_cast<float4*>(at + few_place<D>(2 * q + e, 32 * g + 4 * (lane / 4)));
+        const int r = MODE == 0 ? 2 * q + e : 2 * (q & 1) + e;
+        float4* to = reinterpret_cast<float4*>(at + few_place<D>(r, 32 * g + 4 * (lane / 4)));
         float4 x = finish(which, g, e, lane);
         if (MODE == 0 && h != 0.f) {
           const float4 y = *to;
           x = make_float4(fmaf(y.x, h, x.x), fmaf(y.y, h, x.y), fmaf(y.z, h, x.z), fmaf(y.w, h, x.w));
         }
-        *to = x;
+        if (MODE == 0 || q / 2 == part) *to = x;
       }
     }
   }
   __device__ __forceinline__ void flush(int lane, float* at) {
-    put(0, lane, at);
+    put(0, 0, lane, at);
     clear();
     fm = row[0].m;
   }
@@ -638,37 +645,61 @@ struct FewFetch {
 };
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(Few<D, MODE>::kThreads, Few<D, MODE>::kPerSm) kv_few_kernel(const AttnArgs a) {
   using F = Few<D, MODE>;
   using L = KvTile<D>;
-  constexpr int RT = F::kRows, W = kFewWarps;
+  constexpr int RT = F::kRows, W = F::kWarps, NT = F::kThreads, J = F::kJoin;
   extern __shared__ __align__(128) uint8_t smem[];
-  volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(smem + F::kRing - 16);   // last part of an item
+  // the current item and the next: one thread walks (registers are short)
+  __shared__ KvWalk s_walk[2];
+  __shared__ long long s_U;
+  __shared__ int s_q0[2], s_more, s_G, s_last;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  FewFetch<D, kFewUnit, 2, kFewStages> t;
-  t.bars = reinterpret_cast<uint64_t*>(smem) + warp * kFewStages;
-  t.ring = smem + F::kRing + warp * kFewStages * 2 * L::kBytes;
+  FewFetch<D, F::kUnit, F::kPair, F::kStages> t;
+  t.bars = reinterpret_cast<uint64_t*>(smem) + warp * F::kStages;
+  t.ring = smem + F::kRing + warp * F::kStages * F::kPair * L::kBytes;
   t.parity = t.have = 0;
   if (lane == 0) {
-    for (int i = 0; i < kFewStages; ++i) mbar_init(&t.bars[i], 1);
+    for (int i = 0; i < F::kStages; ++i) mbar_init(&t.bars[i], 1);
     fence_barrier_init();
   }
   __syncwarp();
   pdl_wait();
-  KvWalk w;
-  int G, q0;
-  long long U;
-  if (!kv_range<kFewThreads, RT, kFewUnit, kFewExtra>(a, w, G, U, q0)) return;
+  {
+    KvWalk w;
+    int G, q0;
+    long long U;
+    if (!kv_range<NT, RT, F::kUnit, kFewExtra>(a, w, G, U, q0)) return;
+    if (threadIdx.x == 0) {
+      s_walk[0] = w;
+      s_q0[0] = q0;
+      s_G = G;
+      s_U = U;
+    }
+    __syncthreads();
+  }
+  const auto begin = [&](const KvWalk& w) {
+    t.begin(a, w, w.span.lo + w.k0 * F::kUnit + F::kPair * warp, w.span.lo + w.k1 * F::kUnit, lane);
+  };
 
   FewWarp<D, MODE> f;
   bool dead = false;   // a wait ran out: reported, and only the barriers are kept up
-  float* s_o = reinterpret_cast<float*>(smem + F::kJoin);
+  float* s_o = reinterpret_cast<float*>(smem + F::kSums);
   float* s_m = reinterpret_cast<float*>(smem + F::kState);
   float* s_l = s_m + W * 8;
-  float* mine = s_o + warp * 8 * D;
-  t.begin(a, w, w.span.lo + w.k0 * kFewUnit + 2 * warp, w.span.lo + w.k1 * kFewUnit, lane);
-  for (bool more = true; more;) {
-    f.start(a, w, q0, RT, lane);
+  float* mine = s_o + warp * J * D;
+  begin(s_walk[0]);
+  for (int cur = 0;; cur ^= 1) {
+    const KvWalk& w = s_walk[cur];
+    if (threadIdx.x == NT - 32) {   // the item after, while this one's first tiles come
+      KvWalk x = w;
+      int q0 = s_q0[cur];
+      s_more = kv_advance<RT, F::kUnit, kFewExtra>(a, x, q0);
+      s_walk[cur ^ 1] = x;
+      s_q0[cur ^ 1] = q0;
+    }
+    __syncwarp();
+    f.start(a, w, s_q0[cur], RT, lane);
     // keys that every row of the item sees
     int all_lo, all_hi, x;
     {
@@ -678,9 +709,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
       kv_token_keys(w.T, w.n, t1, a.p.causal, a.p.window, all_lo, x);
     }
     int held = 0;
-    for (int tile = t.first; tile < t.last && !dead; tile += kFewUnit) {
-      const uint32_t two = t.have >> (2 * t.out) & 3u;
-      if (two) {   // else their pages are missing
+    for (int tile = t.first; tile < t.last && !dead; tile += F::kUnit) {
+      const uint32_t some = t.have >> (F::kPair * t.out) & ((1u << F::kPair) - 1);
+      if (some) {   // else their pages are missing
         if (!t.wait()) {
           dead = true;
           if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
@@ -691,112 +722,117 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm) kv_few_kernel(const At
           f.flush(lane, mine);
           held = 0;
         }
-        const uint32_t at = smem_addr(t.ring) + 2 * t.out * L::kBytes;
+        const uint32_t at = smem_addr(t.ring) + F::kPair * t.out * L::kBytes;
         const int kb = tile * LW_KV_TILE;
-        if (two == 3u && kb >= all_lo && kb + 2 * LW_KV_TILE <= all_hi) {
-          // (both at once where their operands fit the registers)
-          constexpr int kAtOnce = D == 64 ? 2 : 1;
-#pragma unroll 1
-          for (int i = 0; i < 2; i += kAtOnce)
-            f.template tiles<false, kAtOnce>(at + i * L::kBytes, kb + i * LW_KV_TILE, w.n, lane);
+        if (some == (1u << F::kPair) - 1 && kb >= all_lo && kb + F::kPair * LW_KV_TILE <= all_hi) {
+          f.template tiles<false, F::kPair>(at, kb, w.n, lane);
         } else {
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i)
-            if (two >> i & 1u) f.template tiles<true, 1>(at + i * L::kBytes, kb + i * LW_KV_TILE, w.n, lane);
+          for (int i = 0; i < F::kPair; ++i)
+            if (some >> i & 1u) f.template tiles<true, 1>(at + i * L::kBytes, kb + i * LW_KV_TILE, w.n, lane);
         }
-        held += 2;
+        held += F::kPair;
         __syncwarp();
       }
-      t.out = t.out + 1 == kFewStages ? 0 : t.out + 1;
+      t.out = t.out + 1 == F::kStages ? 0 : t.out + 1;
       t.send(a, lane);
     }
-    // the next item's first tiles, before this one's join
-    const KvWalk v = w;
-    const int vq0 = q0;
-    more = kv_advance<RT, kFewUnit, kFewExtra>(a, w, q0);
-    if (more && !dead) t.begin(a, w, w.span.lo + w.k0 * kFewUnit + 2 * warp, w.span.lo + w.k1 * kFewUnit, lane);
 
-    // join the warps, 8 rows at a time
-    const bool whole = v.k0 == 0 && v.k1 == v.units;
-    float* part = a.partials + ((size_t)blockIdx.x * 2 + (v.k0 == 0)) * F::kPartial;
+    // join the warps, J rows at a time
+    const bool whole = w.k0 == 0 && w.k1 == w.units;
+    float* part = a.partials + ((size_t)blockIdx.x * 2 + (w.k0 == 0)) * F::kPartial;
 #pragma unroll
-    for (int i = 0; i < FewWarp<D, MODE>::NR; ++i) {
-      float l = f.row[i].l * f.unit;
-      l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-      l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-      if (lane % 4 == 0) {
-        s_m[warp * 8 + lane / 4] = f.row[i].m;
-        s_l[warp * 8 + lane / 4] = l;
+    for (int i = 0; i < RT / J; ++i) {
+      const int which = i * J / 8;
+      if (i * J % 8 == 0) {
+        float l = f.row[which].l * f.unit;
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+        if (lane % 4 == 0) {
+          s_m[warp * 8 + lane / 4] = f.row[which].m;
+          s_l[warp * 8 + lane / 4] = l;
+        }
       }
-      f.put(i, lane, mine);
+      f.put(which, i * J % 8 / 4, lane, mine);
       __syncthreads();
-      for (int j = threadIdx.x; j < 8 * (D / 4); j += kFewThreads) {
-        const int r = j / (D / 4), d = 4 * (j % (D / 4));
+      // the next item's first tiles, before this one's join
+      if (i == 0 && s_more && !dead) begin(s_walk[cur ^ 1]);
+      for (int j = threadIdx.x; j < J * (D / 4); j += NT) {
+        const int r = j / (D / 4), d = 4 * (j % (D / 4)), r8 = i * J % 8 + r;
         float m = -INFINITY, sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int u = 0; u < W; ++u) m = fmaxf(m, s_m[u * 8 + r]);
+        for (int u = 0; u < W; ++u) m = fmaxf(m, s_m[u * 8 + r8]);
         const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
         for (int u = 0; u < W; ++u) {
-          const float e = ex2(s_m[u * 8 + r] - mu);
-          sum = fmaf(s_l[u * 8 + r], e, sum);
-          const float4 z = *reinterpret_cast<const float4*>(s_o + u * 8 * D + few_place<D>(r, d));
+          const float e = ex2(s_m[u * 8 + r8] - mu);
+          sum = fmaf(s_l[u * 8 + r8], e, sum);
+          const float4 z = *reinterpret_cast<const float4*>(s_o + u * J * D + few_place<D>(r, d));
           y[0] = fmaf(z.x, e, y[0]);
           y[1] = fmaf(z.y, e, y[1]);
           y[2] = fmaf(z.z, e, y[2]);
           y[3] = fmaf(z.w, e, y[3]);
         }
+        const int rr = i * J + r;
         if (whole) {
-          few_out<RT>(a, v, vq0, 8 * i + r, d, m, sum, y);
+          few_out<RT>(a, w, s_q0[cur], rr, d, m, sum, y);
         } else {
           if (d == 0) {
-            part[8 * i + r] = m;
-            part[RT + 8 * i + r] = sum;
+            part[rr] = m;
+            part[RT + rr] = sum;
           }
-          *reinterpret_cast<float4*>(part + 2 * RT + (8 * i + r) * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<float4*>(part + 2 * RT + rr * D + d) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
       __syncthreads();
     }
     if (!whole) {
-      const int c0 = kv_owner(v.first, U, G), parts = kv_owner(v.first + v.units - 1, U, G) - c0 + 1;
+      const int c0 = kv_owner(w.first, s_U, s_G), parts = kv_owner(w.first + w.units - 1, s_U, s_G) - c0 + 1;
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
         const bool last = atomicAdd(a.counters + c0, 1u) == (uint32_t)parts - 1u;
         if (last) a.counters[c0] = 0;
-        *flag = last;
+        s_last = last;
       }
       __syncthreads();
-      if (*flag) {
+      if (s_last) {
         __threadfence();
-        for (int j = threadIdx.x; j < RT * (D / 4); j += kFewThreads) {
+        const auto from = [&](int i) { return a.partials + (i ? (size_t)(c0 + i) * 2 : (size_t)c0 * 2 + 1) * F::kPartial; };
+        // the parts' maxima and sums by way of shared memory, as far as they fit
+        constexpr int kFit = W * J * D / (2 * RT);
+        const bool fit = parts <= kFit;
+        if (fit)
+          for (int j = threadIdx.x; j < parts * 2 * RT; j += NT) s_o[j] = __ldcg(from(j / (2 * RT)) + j % (2 * RT));
+        __syncthreads();
+        for (int j = threadIdx.x; j < RT * (D / 4); j += NT) {
           const int r = j / (D / 4), d = 4 * (j % (D / 4));
+          if (w.rt * RT + r >= w.T * a.group) continue;
+          const auto state = [&](int i, int k) { return fit ? s_o[i * 2 * RT + k] : __ldcg(from(i) + k); };
           float m = -INFINITY, sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-          const float* p0 = a.partials + ((size_t)c0 * 2 + 1) * F::kPartial;
-          auto at = [&](int i) { return i ? a.partials + (size_t)(c0 + i) * 2 * F::kPartial : p0; };
-          for (int i = 0; i < parts; ++i) m = fmaxf(m, __ldcg(at(i) + r));
+          for (int i = 0; i < parts; ++i) m = fmaxf(m, state(i, r));
           const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
+#pragma unroll 8
           for (int i = 0; i < parts; ++i) {
-            const float* p = at(i);
-            const float e = ex2(__ldcg(p + r) - mu);
-            sum = fmaf(__ldcg(p + RT + r), e, sum);
-            const float4 z = __ldcg(reinterpret_cast<const float4*>(p + 2 * RT + r * D + d));
+            const float4 z = __ldcg(reinterpret_cast<const float4*>(from(i) + 2 * RT + r * D + d));
+            const float e = ex2(state(i, r) - mu);
+            sum = fmaf(state(i, RT + r), e, sum);
             y[0] = fmaf(z.x, e, y[0]);
             y[1] = fmaf(z.y, e, y[1]);
             y[2] = fmaf(z.z, e, y[2]);
             y[3] = fmaf(z.w, e, y[3]);
           }
-          few_out<RT>(a, v, vq0, r, d, m, sum, y);
+          few_out<RT>(a, w, s_q0[cur], r, d, m, sum, y);
         }
       }
       __syncthreads();
     }
+    if (!s_more) break;
+    __syncthreads();   // (all have read s_more and the item)
   }
   if (dead)   // no copy may be in flight when the CTA ends
-    for (int i = 0; i < kFewStages; ++i)
-      if (t.have >> (2 * i) & 3u) mbar_wait(&t.bars[i], t.parity >> i & 1u);
+    for (int i = 0; i < F::kStages; ++i)
+      if (t.have >> (F::kPair * i) & ((1u << F::kPair) - 1)) mbar_wait(&t.bars[i], t.parity >> i & 1u);
 }
 
 }  // namespace dev

@@ -46,12 +46,13 @@ constexpr int kManyTile = 128, kManyKeys = 64;
 constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit
 constexpr int kManyThreads = 32 * 16;               // warps: 8 of rows (WIDE: 4, 4 of loaders), 6 loaders, 2 issuers
 constexpr int kManyPerSm = 1;
-constexpr int kManyExtra = 8;                       // an item's start and end: 8 units' time (measured 18000 cycles)
 
 template <int D, bool WIDE>
 struct Many {
   using L = KvTile<D>;
   static constexpr int kRows = WIDE ? kManyTile : 2 * kManyTile;   // of an item
+  // an item's start and end, in units' time: 18000 cycles of 2300 (WIDE: 5500) a unit
+  static constexpr int kExtra = WIDE ? 4 : 8;
   static constexpr int kBufs = WIDE ? 2 : 4;                       // restored units
   static constexpr int kLoaders = WIDE ? 10 : 6, kStages = WIDE ? 1 : 2;   // loader warps, places of a loader's ring
   static constexpr int kQLbo = kManyTile * 16 + 16;   // bytes between 8-element columns (16, 32: bank offset)
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   KvWalk w;
   int Gc, q0;
   long long U;
-  const bool any = kv_range<kManyThreads, kRows, kManyUnit, kManyExtra>(a, w, Gc, U, q0);
+  const bool any = kv_range<kManyThreads, kRows, kManyUnit, F::kExtra>(a, w, Gc, U, q0);
   bool ok = true;   // no wait ran out
 
   if (any && warp >= (WIDE ? 4 : 8) && warp < 14) {   // ---- loaders
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         o += kLoaders;
       }
       it0 += w.k1 - w.k0;
-      if (ok) more = kv_advance<kRows, kManyUnit, kManyExtra>(a, w, q0);
+      if (ok) more = kv_advance<kRows, kManyUnit, F::kExtra>(a, w, q0);
     }
     if (!ok) {
       flags[0] = 1;
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       }
       buf = (buf + n) % kBufs;
       sbuf = (sbuf + n) & 1;
-      if (ok) more = uniform(kv_advance<kRows, kManyUnit, kManyExtra>(a, w, q0));
+      if (ok) more = uniform(kv_advance<kRows, kManyUnit, F::kExtra>(a, w, q0));
     }
     if (!ok) {
       flags[0] = 1;
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     for (bool more = true; more;) {
       const KvWalk v = w;
       const int vq0 = q0;
-      more = kv_advance<kRows, kManyUnit, kManyExtra>(a, w, q0);
+      more = kv_advance<kRows, kManyUnit, F::kExtra>(a, w, q0);
       if (!tile_there(v)) {   // a short row tile: the other warps' alone
         it += v.k1 - v.k0;
         if (more) {
