@@ -893,9 +893,14 @@ def lw_kv_read(cache: KvCache, slots, k, v, d_status, stream=None) -> None:
         raise LwError(r, "lw_kv_read")
 
 
-def _kv_attention_refuse(cache, q, q_start, kv_len, page_table, out, ws, d_status, lse):
+def _kv_attention_refuse(cache, q, q_start, kv_len, page_table, out, ws, d_status, lse, max_q):
+    import operator
     import torch
     fn = "lw_kv_attention"
+    try:
+        operator.index(max_q)
+    except TypeError:
+        _refuse(fn, f"max_q: expected a whole number, got {max_q!r}")
     heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
     if isinstance(q, torch.Tensor) and (heads < 1 or heads % cache.kv_heads):
         _refuse(fn, f"q: shape {list(q.shape)}, expected [tokens, a multiple of {cache.kv_heads}, "
@@ -942,7 +947,7 @@ def lw_kv_attention(cache: KvCache, q, q_start, kv_len, page_table, out, ws, d_s
               and kv_len.dtype is _I32 and kv_len.shape == (batch,) and kv_len.is_contiguous()
               and page_table.dtype is _I32 and (td == 1 or width <= 1)
               and ws.is_contiguous() and d_status.dtype is _I32 and d_status.numel() >= 1
-              and d_status.is_contiguous() and dev >= 0 and q.get_device() == dev
+              and d_status.is_contiguous() and type(max_q) is int and dev >= 0 and q.get_device() == dev
               and out.get_device() == dev and q_start.get_device() == dev
               and kv_len.get_device() == dev and page_table.get_device() == dev
               and ws.get_device() == dev and d_status.get_device() == dev
@@ -951,15 +956,18 @@ def lw_kv_attention(cache: KvCache, q, q_start, kv_len, page_table, out, ws, d_s
     except (AttributeError, TypeError, ValueError, IndexError):
         ok = False
     if not ok:
-        _kv_attention_refuse(cache, q, q_start, kv_len, page_table, out, ws, d_status, lse)
+        _kv_attention_refuse(cache, q, q_start, kv_len, page_table, out, ws, d_status, lse, max_q)
         tokens, heads, dim = q.shape
         code, (qt, qh, qd), (ot, oh, od) = _KV_TYPES[q.dtype], q.stride(), out.stride()
         batch, width = page_table.shape
         ts, td = page_table.stride()
-    a = _KV_ATTN.pack(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
-                      0 if lse is None else lse.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
-                      page_table.data_ptr(), ts, tokens, width, code, batch, heads, max_q,
-                      1 if causal else 0, window, dim ** -0.5 if scale is None else scale)
+    try:
+        a = _KV_ATTN.pack(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
+                          0 if lse is None else lse.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                          page_table.data_ptr(), ts, tokens, width, code, batch, heads, max_q,
+                          1 if causal else 0, window, dim ** -0.5 if scale is None else scale)
+    except struct.error as e:
+        _refuse("lw_kv_attention", f"max_q {max_q!r}, window {window!r}, scale {scale!r}: {e}")
     r = _lib.lw_kv_attention(cache.ref, a, ws.data_ptr(), ws.numel() * ws.element_size(),
                              d_status.data_ptr(),
                              _raw_stream(cache.index) if stream is None else stream.cuda_stream)
