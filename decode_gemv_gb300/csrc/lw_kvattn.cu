@@ -52,8 +52,15 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* w
   a.vec = kv_rows_aligned(p->q, p->q_token_stride, p->q_head_stride, p->dtype) &&
           kv_rows_aligned(p->out, p->out_token_stride, p->out_head_stride, p->dtype);
   a.status = status;
+  // The variant, by the rows of a sequence on a key/value head.  us, kv_few_kernel (items of 8 rows, or
+  // of 16) against kv_many_kernel, at 8 sequences of 32768 keys | 64 of 512, 8 heads of 128:
+  //   bf16  8 rows    89, 140 : 219 |  27,  40 : 75      fp32  16 rows  212 : 673 |  53 : 143
+  //        12 rows   159, 145 : 218 |  48,  41 : 75            32 rows  404 : 674 |  90 : 145
+  //        16 rows   160, 147 : 218 |  49,  42 : 75            48 rows  596 : 675 | 136 : 146
+  //        24 rows   230, 258 : 219 |  68,  80 : 75
+  //        32 rows   301, 263 : 219 |  82,  82 : 75
   const long long rows = (long long)p->max_q * a.group;
-  const int mode = p->dtype != LW_BF16 ? (rows > 16 ? 4 : 0) : (rows > 16 ? 3 : rows > 8 ? 1 : 2);
+  const int mode = p->dtype != LW_BF16 ? (rows > 48 ? 4 : 0) : (rows > 24 ? 3 : rows > 8 && rows <= 16 ? 1 : 2);
   const Variant v = c->head_dim == 64 ? variant<64>(mode) : c->head_dim == 96 ? variant<96>(mode) : variant<128>(mode);
   if (resident_blocks(reinterpret_cast<const void*>(v.kernel), v.threads, v.smem) < 1)
     return fail(LW_ERR_CUDA, "lw_kv_attention: the kernel does not fit this device");

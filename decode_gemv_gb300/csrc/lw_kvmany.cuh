@@ -53,7 +53,11 @@ struct Many {
   static constexpr int kRows = WIDE ? kManyTile : 2 * kManyTile;   // of an item
   // an item's start and end, in units' time: 18000 cycles of 2300 (WIDE: 5500) a unit
   static constexpr int kExtra = WIDE ? 4 : 8;
-  static constexpr int kBufs = WIDE ? 2 : 4;                       // restored units
+  static constexpr int kBufs = !WIDE || D == 64 ? 4 : D == 96 ? 3 : 2;   // restored units
+  // With two buffers a key tile is free after its S, not after its O: the keys two units on are
+  // restored while the rows work (with the pair as one, O(i) - restore - S(i + 2) - O(i + 1) were
+  // a chain of 5000 cycles a unit).
+  static constexpr bool kSplit = kBufs == 2;
   static constexpr int kLoaders = WIDE ? 10 : 6, kStages = WIDE ? 1 : 2;   // loader warps, places of a loader's ring
   static constexpr int kQLbo = kManyTile * 16 + 16;   // bytes between 8-element columns (16, 32: bank offset)
   static constexpr int kQBytes = D / 8 * kQLbo;
@@ -163,20 +167,25 @@ __device__ __forceinline__ float many_query(const T* q, int64_t row_at, float sc
       for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
       if (at >= 0 && o < D / 8) kv_load8<T, VEC>(q + at + 8 * o, y[i]);
     }
+    float top[kBatch];   // the rows' maxima side by side (a NaN is not the largest, and stays NaN below)
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      float top = 0.f;   // (a NaN is not the largest, and stays NaN below)
+      top[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[i][j]));
+      for (int j = 0; j < 8; ++j) top[i] = fmaxf(top[i], fabsf(y[i][j]));
+    }
 #pragma unroll
-      for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-      int e = (int)(__float_as_uint(top) >> 23) - 127;
+    for (int d = 8; d; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], d));
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      int e = (int)(__float_as_uint(top[i]) >> 23) - 127;
       e = e < -100 ? -100 : (e > 126 ? 126 : e);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23 | sign);
       const int r = 2 * (i0 + i);
-      const int e0 = __shfl_sync(0xFFFFFFFFu, e, 0), e1 = __shfl_sync(0xFFFFFFFFu, e, 16);
-      if (lane == r) mine = __uint_as_float((uint32_t)(127 + e0) << 23);
-      if (lane == r + 1) mine = __uint_as_float((uint32_t)(127 + e1) << 23);
+      const float up = __shfl_sync(0xFFFFFFFFu, __uint_as_float((uint32_t)(127 + e) << 23), (lane & 1) << 4);
+      if (lane >> 1 == i0 + i) mine = up;
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -253,7 +262,8 @@ struct ManyRaw {
 // Barriers of a CTA.  Those of a row tile are one per S buffer, so that the use
 // before the one waited for is always complete (a parity names one of two).
 struct ManyBars {
-  uint64_t kv_full[4], kv_free[4];                       // per operand buffer
+  uint64_t kv_full[4], kv_free[4];                       // per operand buffer (kSplit: k full, v free)
+  uint64_t v_full[2], k_free[2];                         // kSplit
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];   // per row tile (and S buffer)
   uint64_t last[2];                                      // everything issued has completed
   uint64_t ring[12];                                     // [loader][place]
@@ -263,6 +273,8 @@ template <int D, bool WIDE>
 __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const AttnArgs a) {
   using F = Many<D, WIDE>;
   constexpr int kRows = F::kRows, kBufs = F::kBufs, kLoaders = F::kLoaders, kStages = F::kStages;
+  constexpr bool kSplit = F::kSplit;
+  static_assert(!kSplit || WIDE, "a tile without rows lets its buffers go as pairs");
   static_assert(kLoaders * kStages <= 12, "ring barriers");
   using L = KvTile<D>;
   constexpr int G = L::G;
@@ -279,6 +291,10 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&bar.kv_full[i], kLoaders);
       mbar_init(&bar.kv_free[i], 2);   // both tiles' products
+      if (kSplit) {
+        mbar_init(&bar.v_full[i], kLoaders);
+        mbar_init(&bar.k_free[i], 2);
+      }
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar.last[x], 1);
@@ -335,8 +351,13 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         const uint32_t it = it0 + i, buf = it % kBufs;
         const uint32_t turn = (it / kBufs & 1u) ^ 1u;   // the buffer is free
         if (o >= (i + 1) * kManyUnit) {
+          if (kSplit) {
+            ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.k_free[buf], turn, flags));
+            if (lane == 0) mbar_arrive(&bar.kv_full[buf]);
+            if (!ok) break;
+          }
           ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.kv_free[buf], turn, flags));
-          if (lane == 0) mbar_arrive(&bar.kv_full[buf]);
+          if (lane == 0) mbar_arrive(kSplit ? &bar.v_full[buf] : &bar.kv_full[buf]);
           continue;
         }
         const int sub = o - i * kManyUnit;
@@ -394,7 +415,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
 #pragma unroll
             for (int i = 0; i < GW; ++i) r.vc[j][i] = r.vs[j][i] = r.vm[j][i] = 0;
         }
-        ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.kv_free[buf], turn, flags));
+        ok = __all_sync(0xFFFFFFFFu, many_wait(kSplit ? &bar.k_free[buf] : &bar.kv_free[buf], turn, flags));
         if (!ok) break;
         const uint32_t kto = smem_addr(smem) + F::kKv + buf * F::kBufBytes + (uint32_t)(sub * 256 + (lane / 4) * 16 + q * F::kKLbo);
         const uint32_t vto = smem_addr(smem) + F::kKv + buf * F::kBufBytes + F::kKBytes +
@@ -417,6 +438,14 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
               if (WIDE) sts_u4(to + F::kKvBytes, lo[0], lo[1], lo[2], lo[3]);
             }
         }
+        if (lane == 0) present[it % 4 * kManyUnit + sub] = there;
+        if (kSplit) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.kv_full[buf]);
+          ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.kv_free[buf], turn, flags));
+          if (!ok) break;
+        }
 #pragma unroll
         for (int i = 0; i < GW; ++i) {
           if (G % 2 && g0 + i >= G) continue;
@@ -437,10 +466,9 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
             }
           }
         }
-        if (lane == 0) present[it % 4 * kManyUnit + sub] = there;
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.kv_full[buf]);
+        if (lane == 0) mbar_arrive(kSplit ? &bar.v_full[buf] : &bar.kv_full[buf]);
         o += kLoaders;
       }
       it0 += w.k1 - w.k0;
@@ -460,7 +488,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     const uint32_t tm = uniform(tmem), base = smem_addr(smem);
     const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
     int buf = 0, sbuf = 0;   // operand and S buffer of the item's first unit
-    uint32_t kvph = 0, qph = 0;             // phases of kv_full (a bit a buffer) and q_full
+    uint32_t kvph = 0, vph = 0, qph = 0;    // phases of kv_full and v_full (a bit a buffer) and q_full
     uint32_t pph = 0, oph = 0, used = 0;    // of p_full and o_done, and whether the place has held a P (a bit an S buffer)
     const bool q_lo = WIDE && a.p.dtype == LW_F32;   // (fp16 queries are their hi parts)
     for (bool more = true; more && ok;) {
@@ -501,12 +529,17 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
             }
           }
           umma_commit(&bar.s_full[x][sb]);
+          if (kSplit) umma_commit(&bar.k_free[kv]);
         }
         __syncwarp();
         return true;
       };
       const auto issue_o = [&](int i) {   // O += P V
         const int kv = (buf + i) % kBufs, sb = (sbuf + i) & 1;
+        if (kSplit) {
+          if (!wait(&bar.v_full[kv], vph >> kv & 1u)) return false;
+          vph ^= 1u << kv;
+        }
         if (!wait(&bar.p_full[xr][sb], pph >> sb & 1u)) return false;
         pph ^= 1u << sb;
         tc_fence_after();
