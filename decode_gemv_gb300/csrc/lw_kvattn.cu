@@ -17,8 +17,8 @@ Variant variant(int mode) {
   if (mode == 0) return {dev::kv_few_kernel<D, 0>, Few<D, 0>::kThreads, Few<D, 0>::kPerSm, Few<D, 0>::kSmem};
   if (mode == 1) return {dev::kv_few_kernel<D, 1>, Few<D, 1>::kThreads, Few<D, 1>::kPerSm, Few<D, 1>::kSmem};
   if (mode == 2) return {dev::kv_few_kernel<D, 2>, Few<D, 2>::kThreads, Few<D, 2>::kPerSm, Few<D, 2>::kSmem};
-  if (mode == 3) return {dev::kv_many_kernel<D, false>, kManyThreads, kManyPerSm, Many<D, false>::kSmem};
-  return {dev::kv_many_kernel<D, true>, kManyThreads, kManyPerSm, Many<D, true>::kSmem};
+  if (mode == 3) return {dev::kv_many_kernel<D, false>, Many<D, false>::kThreads, kManyPerSm, Many<D, false>::kSmem};
+  return {dev::kv_many_kernel<D, true>, Many<D, true>::kThreads, kManyPerSm, Many<D, true>::kSmem};
 }
 
 // The workspace: counters and partial results of the most resident CTAs of a

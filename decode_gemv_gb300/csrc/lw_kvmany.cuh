@@ -44,7 +44,6 @@ namespace lw {
 
 constexpr int kManyTile = 128, kManyKeys = 64;
 constexpr int kManyUnit = kManyKeys / LW_KV_TILE;   // 16-key tiles of a unit
-constexpr int kManyThreads = 32 * 16;               // warps: 8 of rows (WIDE: 4, 4 of loaders), 6 loaders, 2 issuers
 constexpr int kManyPerSm = 1;
 
 template <int D, bool WIDE>
@@ -52,20 +51,22 @@ struct Many {
   using L = KvTile<D>;
   static constexpr int kRows = WIDE ? kManyTile : 2 * kManyTile;   // of an item
   // an item's start and end, in units' time: 18000 cycles of 2300 (WIDE: 5500) a unit
-  static constexpr int kExtra = WIDE ? 4 : 8;
+  static constexpr int kExtra = WIDE ? (D == 64 ? 7 : 4) : 8;
   static constexpr int kBufs = !WIDE || D == 64 ? 4 : D == 96 ? 3 : 2;   // restored units
   // With two buffers a key tile is free after its S, not after its O: the keys two units on are
   // restored while the rows work (with the pair as one, O(i) - restore - S(i + 2) - O(i + 1) were
   // a chain of 5000 cycles a unit).
   static constexpr bool kSplit = kBufs == 2;
-  static constexpr int kLoaders = WIDE ? 10 : 6, kStages = WIDE ? 1 : 2;   // loader warps, places of a loader's ring
+  static constexpr int kLoaders = WIDE && D > 64 ? 8 : 6, kStages = WIDE && D > 64 ? 1 : 2;   // loader warps, places of a loader's ring
+  static constexpr int kRowWarps = 8, kWarps = kRowWarps + kLoaders + 2, kThreads = 32 * kWarps;
+  static constexpr int kTileWarps = WIDE ? 8 : 4;     // row warps of a row tile
   static constexpr int kQLbo = kManyTile * 16 + 16;   // bytes between 8-element columns (16, 32: bank offset)
   static constexpr int kQBytes = D / 8 * kQLbo;
   static constexpr int kKLbo = kManyKeys * 16 + 32;
   static constexpr int kKBytes = D / 8 * kKLbo;
   static constexpr int kVLbo = D * 16;                // bytes between 8-key columns
   static constexpr int kVBytes = kManyKeys / 8 * kVLbo;
-  static constexpr int kHead = 1024;                  // barriers and flags
+  static constexpr int kHead = WIDE ? 3584 : 1024;    // barriers, flags, what the halves of a row exchange
   static constexpr int kQ = kHead, kKv = kQ + 2 * kQBytes;   // a buffer: K, V (WIDE: and their lo parts)
   static constexpr int kKvBytes = kKBytes + kVBytes;
   static constexpr int kBufBytes = WIDE ? 2 * kKvBytes : kKvBytes;
@@ -105,6 +106,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) 
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -133,70 +142,119 @@ __device__ __forceinline__ bool many_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // The barrier of a tile's row warps: whether `ok` holds in all of them
+template <int THREADS>
 __device__ __forceinline__ bool rows_agree(int tile, bool ok) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)ok), "r"(1 + tile)
+      : "r"((uint32_t)ok), "r"(1 + tile), "n"(THREADS)
       : "memory");
   return r != 0;
 }
+// The barrier of the two warps that share 32 rows: how many of their lanes say yes
+__device__ __forceinline__ uint32_t pair_count(int quarter, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.popc.u32 %0, %2, 64, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)yes), "r"(3 + quarter)
+      : "memory");
+  return r;
+}
 
-// A warp's 32 rows of Q into rows 32 quarter .. of the operand tile, each scaled
-// by 2^-e and given the sign of `scale` (so that the largest product is the
-// largest score); WIDE: lo 2^11 goes to the tile at `to_lo`.  Two rows at a time,
-// a lane eight elements (whole lines: a lane per row took 16 times the tag
-// lookups and bounded an item's start).  q + row_at is this lane's row, 0 where
-// row_at < 0.  Returns 2^e of this lane's row.
+// Rows 2 p0 .. 2 p1 - 1 of a warp's 32 rows of Q into rows 32 quarter .. of the
+// operand tile, each scaled by 2^-e and given the sign of `scale` (so that the
+// largest product is the largest score); WIDE: lo 2^11 goes to the tile at
+// `to_lo` (fp16 queries are their hi parts, and e = 0).  Two rows at a time, a
+// lane eight elements (whole lines: a lane per row took 16 times the tag lookups
+// and bounded an item's start).  q + row_at is this lane's row, 0 where row_at
+// < 0.  Returns 2^e of this lane's row, if it is one of these.
 template <int D, class T, bool VEC, bool WIDE>
 __device__ __forceinline__ float many_query(const T* q, int64_t row_at, float scale, uint32_t to, uint32_t to_lo,
-                                            int quarter, int lane) {
+                                            int quarter, int lane, int p0, int p1) {
+  constexpr bool kHalf = std::is_same_v<T, __half>;
+  constexpr int kW = sizeof(T) * 2;                                          // words of 8 elements
+  constexpr int kBatch = sizeof(T) == 4 ? 4 : 8;   // rows on their way at once
   const int half = lane >> 4, o = lane & 15;
   const uint32_t sign = __float_as_uint(scale) & 0x80000000u;
   float mine = 1.f;
-  constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;
 #pragma unroll 1
-  for (int i0 = 0; i0 < 16; i0 += kBatch) {
-    float y[kBatch][8];
+  for (int i0 = p0; i0 < p1; i0 += kBatch) {
+    uint32_t y[kBatch][kW];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int64_t at = __shfl_sync(0xFFFFFFFFu, row_at, 2 * (i0 + i) + half);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
-      if (at >= 0 && o < D / 8) kv_load8<T, VEC>(q + at + 8 * o, y[i]);
-    }
-    float top[kBatch];   // the rows' maxima side by side (a NaN is not the largest, and stays NaN below)
+      for (int j = 0; j < kW; ++j) y[i][j] = 0u;
+      if (at >= 0 && o < D / 8) {
+        const T* p = q + at + 8 * o;
+        if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      top[i] = 0.f;
+          for (int j = 0; j < kW; j += 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p + j * (4 / sizeof(T)));
+            y[i][j] = u.x; y[i][j + 1] = u.y; y[i][j + 2] = u.z; y[i][j + 3] = u.w;
+          }
+        } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top[i] = fmaxf(top[i], fabsf(y[i][j]));
-    }
+          for (int j = 0; j < 8; ++j) y[i][j] = __float_as_uint(p[j]);
+        } else {
+          const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int d = 8; d; d >>= 1)
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], d));
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      int e = (int)(__float_as_uint(top[i]) >> 23) - 127;
-      e = e < -100 ? -100 : (e > 126 ? 126 : e);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23 | sign);
-      const int r = 2 * (i0 + i);
-      const float up = __shfl_sync(0xFFFFFFFFu, __uint_as_float((uint32_t)(127 + e) << 23), (lane & 1) << 4);
-      if (lane >> 1 == i0 + i) mine = up;
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (WIDE) split2<2048>(y[i][j] * down, y[i][j + 4] * down, hi[j], lo[j]);
-        else hi[j] = h2bits(__floats2half2_rn(y[i][j] * down, y[i][j + 4] * down));
+          for (int j = 0; j < 4; ++j) y[i][j] = e[2 * j] | (uint32_t)e[2 * j + 1] << 16;
+        }
       }
-      const int row = r + half;
+    }
+    // the rows' largest magnitudes, by their bits, side by side (bf16: two at once)
+    uint32_t top[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      top[i] = 0;
+#pragma unroll
+      for (int j = 0; j < kW && !kHalf; ++j)
+        top[i] = sizeof(T) == 4 ? max(top[i], y[i][j] & 0x7FFFFFFFu) : __vmaxu2(top[i], y[i][j] & 0x7FFF7FFFu);
+    }
+#pragma unroll
+    for (int d = 8; d && !kHalf; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t z = __shfl_xor_sync(0xFFFFFFFFu, top[i], d);
+        top[i] = sizeof(T) == 4 ? max(top[i], z) : __vmaxu2(top[i], z);
+      }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      // pair j: elements j and j + 4
+      uint32_t hi[4], lo[4];
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) hi[j] = __byte_perm(y[i][j / 2], y[i][2 + j / 2], j % 2 ? 0x7632 : 0x5410);
+      }
+      if constexpr (kHalf) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) hi[j] ^= sign | sign >> 16;
+      } else {
+        const uint32_t m = sizeof(T) == 4 ? top[i] : max(top[i] << 16, top[i] & 0xFFFF0000u);
+        int e = (int)(m >> 23) - 127;
+        e = e < -100 ? -100 : (e > 126 ? 126 : e);
+        const float up = __shfl_sync(0xFFFFFFFFu, __uint_as_float((uint32_t)(127 + e) << 23), (lane & 1) << 4);
+        if (lane >> 1 == i0 + i) mine = up;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23 | sign);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 z;
+          if constexpr (sizeof(T) == 4) z = make_float2(__uint_as_float(y[i][j]), __uint_as_float(y[i][j + 4]));
+          else z = make_float2(__uint_as_float(hi[j] << 16), __uint_as_float(hi[j] & 0xFFFF0000u));
+          z = mul2(z, make_float2(down, down));
+          if constexpr (WIDE) split2<2048>(z.x, z.y, hi[j], lo[j]);
+          else hi[j] = h2bits(__floats2half2_rn(z.x, z.y));
+        }
+      }
+      const int row = 2 * (i0 + i) + half;
       const uint32_t at = (uint32_t)(o * Many<D, WIDE>::kQLbo + (4 * quarter + row / 8) * 128 + (row % 8) * 16);
       if (o < D / 8) {
         sts_u4(to + at, hi[0], hi[1], hi[2], hi[3]);
-        if constexpr (WIDE) sts_u4(to_lo + at, lo[0], lo[1], lo[2], lo[3]);
+        if constexpr (WIDE && !kHalf) sts_u4(to_lo + at, lo[0], lo[1], lo[2], lo[3]);
       }
     }
   }
@@ -270,7 +328,7 @@ struct ManyBars {
 };
 
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_kernel(const AttnArgs a) {
   using F = Many<D, WIDE>;
   constexpr int kRows = F::kRows, kBufs = F::kBufs, kLoaders = F::kLoaders, kStages = F::kStages;
   constexpr bool kSplit = F::kSplit;
@@ -286,6 +344,8 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   // [unit % 4][tile]: the tile's keys are there (written before kv_full, read
   // after s_full; four units on, the rows have answered)
   volatile uint8_t* present = smem + 544;
+  float* xch = reinterpret_cast<float*>(smem + 1024);   // WIDE: [2][rows], [rows] 2^e of Q, [2][rows] sums
+  constexpr int kIssuer = F::kRowWarps + kLoaders;      // the first of the two
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBufs; ++i) {
@@ -298,11 +358,11 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar.last[x], 1);
-      mbar_init(&bar.q_full[x], 4);
+      mbar_init(&bar.q_full[x], F::kTileWarps);
       mbar_init(&bar.s_full[x][0], 1);
       mbar_init(&bar.s_full[x][1], 1);
-      mbar_init(&bar.p_full[x][0], 4);
-      mbar_init(&bar.p_full[x][1], 4);
+      mbar_init(&bar.p_full[x][0], F::kTileWarps);
+      mbar_init(&bar.p_full[x][1], F::kTileWarps);
       mbar_init(&bar.o_done[x][0], 1);
       mbar_init(&bar.o_done[x][1], 1);
     }
@@ -310,7 +370,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     flags[0] = 0;
     fence_barrier_init();
   }
-  if (warp == 14) {
+  if (warp == kIssuer) {
     tmem_alloc(smem_addr(tslot), F::kCols);
     tmem_relinquish();
   }
@@ -322,11 +382,11 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   KvWalk w;
   int Gc, q0;
   long long U;
-  const bool any = kv_range<kManyThreads, kRows, kManyUnit, F::kExtra>(a, w, Gc, U, q0);
+  const bool any = kv_range<F::kThreads, kRows, kManyUnit, F::kExtra>(a, w, Gc, U, q0);
   bool ok = true;   // no wait ran out
 
-  if (any && warp >= (WIDE ? 4 : 8) && warp < 14) {   // ---- loaders
-    const int lw = warp - (WIDE ? 4 : 8);
+  if (any && warp >= F::kRowWarps && warp < kIssuer) {   // ---- loaders
+    const int lw = warp - F::kRowWarps;
     constexpr int GW = ManyRaw<D>::GW;
     uint32_t it0 = 0;                 // units before this item
     FewFetch<D, kLoaders, 1, kStages> t;
@@ -480,10 +540,10 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       for (int i = 0; i < kStages; ++i)   // no copy may be in flight when the CTA ends
         if (t.have >> i & 1u) mbar_wait(&t.bars[i], t.parity >> i & 1u);
     }
-  } else if (any && warp >= 14) {   // ---- issuers
+  } else if (any && warp >= kIssuer) {   // ---- issuers
     const auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
     const auto wait = [&](uint64_t* b, bool parity) { return __all_sync(0xFFFFFFFFu, many_wait(b, parity, flags)) != 0; };
-    const int x = uniform(warp - 14);   // row tile (WIDE: 0 the hi products, 1 the lo ones)
+    const int x = uniform(warp - kIssuer);   // row tile (WIDE: 0 the hi products, 1 the lo ones)
     const int xr = WIDE ? 0 : x;                      // whose rows
     const uint32_t tm = uniform(tmem), base = smem_addr(smem);
     const uint64_t qd = sdesc(base + F::kQ + x * F::kQBytes, F::kQLbo, 128);
@@ -587,9 +647,12 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
     if (elect_one()) umma_commit(&bar.last[x]);   // no product may be in flight when the tensor memory goes
     __syncwarp();
     mbar_wait(&bar.last[x], 0);
-  } else if (any && warp < (WIDE ? 4 : 8)) {   // ---- rows
-    const int x = warp / 4, row = threadIdx.x % kManyTile;   // tile, its row
-    const uint32_t mine = tmem + ((uint32_t)(32 * (warp % 4)) << 16);   // this warp's quarter
+  } else if (any) {   // ---- rows
+    // Tile and row of this thread.  WIDE: two threads a row, this one has keys 32 hf .. 32 hf + 31 of a unit.
+    const int x = WIDE ? 0 : warp / 4, hf = WIDE ? warp / 4 : 0, quarter = warp % 4, row = threadIdx.x % kManyTile;
+    constexpr int kMine = WIDE ? 32 : 64;   // keys of a unit
+    constexpr int kTileThreads = 32 * F::kTileWarps;
+    const uint32_t mine = tmem + ((uint32_t)(32 * quarter) << 16);   // this warp's quarter
     uint32_t it = 0;     // units of the CTA; S lies in buffer it % 2
     uint32_t used = 0;   // a bit an S buffer: how often this tile has used it, mod 2 (the phase of its
                          // next s_full; its last o_done has the other)
@@ -610,12 +673,18 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       const uint32_t to = smem_addr(smem) + F::kQ + x * F::kQBytes;
       const auto read = [&](auto* q) {   // the rows, by their type
         using T = std::remove_const_t<std::remove_pointer_t<decltype(q)>>;
-        return a.vec ? many_query<D, T, true, WIDE>(q, at, a.p.scale, to, to + F::kQBytes, warp % 4, lane)
-                     : many_query<D, T, false, WIDE>(q, at, a.p.scale, to, to + F::kQBytes, warp % 4, lane);
+        const int p0 = WIDE ? 8 * hf : 0, p1 = WIDE ? p0 + 8 : 16;
+        return a.vec ? many_query<D, T, true, WIDE>(q, at, a.p.scale, to, to + F::kQBytes, quarter, lane, p0, p1)
+                     : many_query<D, T, false, WIDE>(q, at, a.p.scale, to, to + F::kQBytes, quarter, lane, p0, p1);
       };
       float e2;
       if constexpr (!WIDE) e2 = read(static_cast<const __nv_bfloat16*>(a.p.q));
       else e2 = a.p.dtype == LW_F16 ? read(static_cast<const __half*>(a.p.q)) : read(static_cast<const float*>(a.p.q));
+      if constexpr (WIDE) {   // the other half's rows
+        if (lane / 16 == hf) xch[2 * kManyTile + row] = e2;
+        pair_count(quarter, true);
+        e2 = xch[2 * kManyTile + row];
+      }
       // (never 0: a masked score times it stays -inf)
       f = fmaxf(fabsf(a.p.scale) * 1.4426950408889634f * e2, 1e-37f);
       fence_proxy_async();
@@ -649,46 +718,59 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       for (int k = v.k0; k < v.k1; ++k, ++it) {
         const int kb = (v.span.lo + k * kManyUnit) * LW_KV_TILE;
         const int b = it & 1;
-        const uint32_t sc = mine + F::s_col(x, b);
+        const uint32_t sc = mine + F::s_col(x, b) + 32 * hf;
         if (ok) ok = many_wait(&bar.s_full[x][b], used >> b & 1u, flags);
         if (WIDE && ok) ok = many_wait(&bar.s_full[1][b], used >> b & 1u, flags);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+        if (!WIDE && !ok) break;
         tc_fence_after();
-        const uint32_t there = *reinterpret_cast<const volatile uint32_t*>(present + it % 4 * kManyUnit);
-        uint32_t s0[32], s1[32];
+        const uint32_t there = *reinterpret_cast<const volatile uint32_t*>(present + it % 4 * kManyUnit) >> (16 * hf) & (WIDE ? 0xFFFFu : 0xFFFFFFFFu);
+        uint32_t s0[32], s1[32];   // WIDE: s0 alone
         tmem_ld32(sc, s0);
-        tmem_ld32(sc + 32, s1);
+        if constexpr (!WIDE) tmem_ld32(sc + 32, s1);
+        else tmem_ld32(mine + F::s_col(1, b) + 32 * hf, s1);
         tmem_ld_wait();
         if constexpr (WIDE) {   // and the lo parts' sum
           const float2 down = make_float2(4.8828125e-4f, 4.8828125e-4f);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t z[32];
-            uint32_t* s = h ? s1 : s0;
-            tmem_ld32(mine + F::s_col(1, b) + 32 * h, z);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float2 t = fma2(make_float2(__uint_as_float(z[j]), __uint_as_float(z[j + 1])), down,
-                                    make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
-              s[j] = __float_as_uint(t.x);
-              s[j + 1] = __float_as_uint(t.y);
-            }
+          for (int j = 0; j < 32; j += 2) {
+            const float2 t = fma2(make_float2(__uint_as_float(s1[j]), __uint_as_float(s1[j + 1])), down,
+                                  make_float2(__uint_as_float(s0[j]), __uint_as_float(s0[j + 1])));
+            s0[j] = __float_as_uint(t.x);
+            s0[j + 1] = __float_as_uint(t.y);
           }
         }
-        if (kb < all_lo || kb + kManyKeys > all_hi || there != 0x01010101u) {
+        const int ka = kb + 32 * hf;   // this thread's first key
+        if (ka < all_lo || ka + kMine > all_hi || there != (WIDE ? 0x0101u : 0x01010101u)) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {
+          for (int j = 0; j < kMine; ++j) {
             const bool in = there >> (8 * (j / 16)) & 1u;
-            if (!(in && kb + j >= y.lo && kb + j < y.hi)) (j < 32 ? s0[j % 32] : s1[j % 32]) = 0xFF800000u;
+            if (!(in && ka + j >= y.lo && ka + j < y.hi)) (j < 32 ? s0[j % 32] : s1[j % 32]) = 0xFF800000u;
           }
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) top = fmaxf(fmaxf(top, __uint_as_float(s0[j])), __uint_as_float(s1[j]));
+        for (int j = 0; j < 32; ++j) {
+          top = fmaxf(top, __uint_as_float(s0[j]));
+          if (!WIDE) top = fmaxf(top, __uint_as_float(s1[j]));
+        }
         top *= f;
-        if (__any_sync(0xFFFFFFFFu, top > m + 8.f)) {
+        bool raise = __any_sync(0xFFFFFFFFu, top > m + 8.f);
+        if constexpr (WIDE) {   // Both halves or none, also of an end: a wait that ran out counts 32, a raise 1.
+          // (And both have read S, so that P may go over it.)
+          const uint32_t say = pair_count(quarter, !ok || (raise && lane == 0));
+          if (say >= 32) {
+            ok = false;
+            break;
+          }
+          raise = say != 0;
+          if (raise) {
+            xch[hf * kManyTile + row] = top;
+            pair_count(quarter, true);
+            top = fmaxf(top, xch[(hf ^ 1) * kManyTile + row]);
+          }
+        }
+        if (raise) {
           const float mx = fmaxf(m, top);
           mu = mx == -INFINITY ? 0.f : mx;
           const float al = ex2(m - mu);
@@ -698,16 +780,16 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
             const bool ph = (used >> (b ^ 1) & 1u) ^ 1u;
             ok = many_wait(&bar.o_done[x][b ^ 1], ph, flags) && (!WIDE || many_wait(&bar.o_done[1][b ^ 1], ph, flags));
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
+            if (!WIDE && !ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int d = 0; d < (WIDE ? 2 * D : D); d += 32) {
+            for (int d = 0; ok && d < D; d += 32) {   // (WIDE: the hi parts' sum one half, the lo parts' the other)
               uint32_t z[32];
-              tmem_ld32(mine + F::o_col(x) + d, z);
+              tmem_ld32(mine + F::o_col(x + hf) + d, z);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 32; ++j) z[j] = __float_as_uint(__uint_as_float(z[j]) * al);
-              tmem_st32(mine + F::o_col(x) + d, z);
+              tmem_st32(mine + F::o_col(x + hf) + d, z);
             }
           }
         }
@@ -715,7 +797,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         const float2 f2 = make_float2(f, f), mu2 = make_float2(-mu, -mu);
         // (the parts of p go where the scores were)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < kMine / 2; ++j) {
           uint32_t* s = j < 16 ? s0 + 2 * j : s1 + 2 * (j - 16);
           const float2 t = fma2(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), f2, mu2);
           const float2 z = make_float2(ex2(t.x), ex2(t.y));
@@ -723,15 +805,20 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           if constexpr (WIDE) split2<2048>(z.x, z.y, s[0], s[1]);
           else s[0] = h2bits(__floats2half2_rn(z.x, z.y));
         }
-        uint32_t p[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) p[j] = j < 16 ? s0[2 * j] : s1[2 * (j - 16)];
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_st32(sc, p);
-        if constexpr (WIDE) {
+        if constexpr (!WIDE) {
+          uint32_t p[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) p[j] = j < 16 ? s0[2 * j + 1] : s1[2 * (j - 16) + 1];
-          tmem_st32(sc + 32, p);
+          for (int j = 0; j < 32; ++j) p[j] = j < 16 ? s0[2 * j] : s1[2 * (j - 16)];
+          tmem_st32(sc, p);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {   // hi parts, lo parts
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = s0[2 * j + h];
+            tmem_st16(mine + F::s_col(x, b) + 32 * h + 16 * hf, p);
+          }
         }
         tmem_st_wait();
         tc_fence_before();
@@ -741,6 +828,12 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       }
       // (every S of this item is complete: Q's place is free)
       const Row o = y;
+      if constexpr (WIDE) {   // (the halves stay together; and their sums)
+        float* sums = xch + 3 * kManyTile;
+        sums[hf * kManyTile + row] = l;
+        ok = pair_count(quarter, ok) == 64;
+        l = sums[row] + sums[kManyTile + row];
+      }
       if (more) {
         y = find(w);
         if (ok && tile_there(w)) load_q(y, q0);
@@ -750,7 +843,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         if (ok) ok = many_wait(&bar.o_done[x][b], (used >> b & 1u) ^ 1u, flags);
         if (WIDE && ok) ok = many_wait(&bar.o_done[1][b], (used >> b & 1u) ^ 1u, flags);
       }
-      ok = rows_agree(x, ok);   // all four warps go on to the barriers below, or none
+      ok = rows_agree<kTileThreads>(x, ok);   // all warps of the tile go on to the barriers below, or none
       if (!ok) break;
       tc_fence_after();
       const bool whole = v.k0 == 0 && v.k1 == v.units;
@@ -768,11 +861,11 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
         }
       };
       const auto give_lse = [&](float m, float l) {
-        if (o.live && a.p.lse)
+        if (hf == 0 && o.live && a.p.lse)
           a.p.lse[(int64_t)(vq0 + o.tok) * a.p.q_heads + o.hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       };
 #pragma unroll 1
-      for (int g = 0; g < G; ++g) {
+      for (int g = hf; g < G; g += F::kTileWarps / 4) {
         uint32_t u[32];
         float z[32];
         tmem_ld32(mine + F::o_col(x) + 32 * g, u);
@@ -798,17 +891,19 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
       if (whole) {
         give_lse(m, l);
       } else {
-        part[row] = m;
-        part[kManyTile + row] = l;
+        if (hf == 0) {
+          part[row] = m;
+          part[kManyTile + row] = l;
+        }
         const int c0 = kv_owner(v.first, U, Gc), parts = kv_owner(v.first + v.units - 1, U, Gc) - c0 + 1;
         __threadfence();
-        rows_agree(x, true);
-        if (row == 0) {
+        rows_agree<kTileThreads>(x, true);
+        if (row == 0 && hf == 0) {
           const bool last = atomicAdd(a.counters + 2 * c0 + x, 1u) == (uint32_t)parts - 1u;
           if (last) a.counters[2 * c0 + x] = 0;
           flags[1 + x] = last;
         }
-        rows_agree(x, true);
+        rows_agree<kTileThreads>(x, true);
         if (flags[1 + x]) {
           __threadfence();
           const auto from = [&](int i) {
@@ -819,7 +914,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           const float Mu = M == -INFINITY ? 0.f : M;
           for (int i = 0; i < parts; ++i) S = fmaf(__ldcg(from(i) + kManyTile + row), ex2(__ldcg(from(i) + row) - Mu), S);
 #pragma unroll 1
-          for (int g = 0; g < G; ++g) {
+          for (int g = hf; g < G; g += F::kTileWarps / 4) {
             float z[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) z[j] = 0.f;
@@ -840,7 +935,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
           }
           give_lse(M, S);
         }
-        rows_agree(x, true);
+        rows_agree<kTileThreads>(x, true);
       }
     }
     if (!ok) {
@@ -851,7 +946,7 @@ __global__ void __launch_bounds__(kManyThreads, kManyPerSm) kv_many_kernel(const
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 14) tmem_dealloc(tmem, F::kCols);
+  if (warp == kIssuer) tmem_dealloc(tmem, F::kCols);
 }
 
 }  // namespace dev
