@@ -82,22 +82,78 @@ __device__ __forceinline__ bool kv_advance(const AttnArgs& a, KvWalk& w, int& q0
   return true;
 }
 
+// Row tiles of a sequence up to which one thread counts its weight, and every
+// thread walks them; the tiles of longer ones are shared by a warp's lanes (5
+// prompts of 2048 tokens, 128 tiles a head: a CTA's start was 90000 to 160000
+// cycles of 500000).
+constexpr int kKvAlone = 4;
+
+// kv_head_weight of each lane's sequence (0 if T is 0).  Whole warp.
+__device__ __forceinline__ long long kv_weight_warp(const KvShape& c, int T, int n) {
+  const int lane = threadIdx.x % 32, nrt = T ? kv_row_tiles(T, c.group, c.RT) : 0;
+  long long u = nrt && nrt <= kKvAlone ? kv_head_weight(c, T, n) : 0;
+  for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, nrt > kKvAlone); rest; rest &= rest - 1) {
+    const int l = __ffs(rest) - 1;
+    const int t = __shfl_sync(0xFFFFFFFFu, T, l), k = __shfl_sync(0xFFFFFFFFu, n, l);
+    const int tiles = __shfl_sync(0xFFFFFFFFu, nrt, l);
+    long long s = 0;
+    for (int rt = lane; rt < tiles; rt += 32) s += kv_item_weight(c, t, k, rt);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == l) u = s;
+  }
+  return u;
+}
+
+// kv_seek, per_head being the weight of a head.  Whole warp, the same in all lanes.
+__device__ __forceinline__ void kv_seek_warp(const KvShape& c, KvWalk& w, long long per_head) {
+  w.nrt = kv_row_tiles(w.T, c.group, c.RT);
+  if (w.nrt <= kKvAlone) {
+    kv_seek(c, w);
+    return;
+  }
+  w.h = (int)((w.x - w.base) / per_head);
+  long long begin = w.base + per_head * w.h;
+  const int lane = threadIdx.x % 32;
+  for (int r0 = 0; r0 < w.nrt; r0 += 32) {
+    const long long mine = r0 + lane < w.nrt ? kv_item_weight(c, w.T, w.n, r0 + lane) : 0;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, w.x < begin + inc);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      w.rt = r0 + l;
+      begin += __shfl_sync(0xFFFFFFFFu, inc - mine, l);
+      break;
+    }
+    begin += __shfl_sync(0xFFFFFFFFu, inc, 31);
+  }
+  kv_item(c, w, begin);
+}
+
 // The CTA's range, and its first item.  Whole CTA of NT threads; false if the
 // CTA has no units.
 template <int NT, int RT, int PER, int EXTRA>
 __device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int& q0) {
-  __shared__ long long s_scan[NT / 32 + 1], s_base;
-  __shared__ int s_b;
+  __shared__ long long s_scan[NT / 32 + 1], s_base, s_head;
+  __shared__ int s_b, s_q0, s_T, s_n;
   const KvShape c = kv_shape<RT, PER, EXTRA>(a);
   const int tid = threadIdx.x, batch = a.p.batch;
-  long long sum = 0, first = 0;
-  for (int b = tid; b < batch; b += NT) {
-    int s, T, n;
-    if (blockIdx.x == 0) kv_seq<true>(a, b, s, T, n);
-    else kv_seq<false>(a, b, s, T, n);
-    const long long u = T ? a.heads * kv_head_weight(c, T, n) : 0;
-    if (b == tid) first = u;
-    sum += u;
+  long long sum = 0, head = 0;
+  int T = 0, n = 0;
+  for (int cb = 0; cb < batch; cb += NT) {
+    const int b = cb + tid;
+    T = n = 0;
+    if (b < batch) {
+      if (blockIdx.x == 0) kv_seq<true>(a, b, q0, T, n);
+      else kv_seq<false>(a, b, q0, T, n);
+    }
+    head = kv_weight_warp(c, T, n);
+    sum += a.heads * head;
   }
   long long before = cta_scan<NT>(sum, s_scan, U);
   if (U == 0) return false;
@@ -105,34 +161,37 @@ __device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int
   if ((int)blockIdx.x >= G) return false;
   w.x = kv_first(U, blockIdx.x, G);
   w.xe = kv_first(U, blockIdx.x + 1, G);
+  const auto take = [&](int b) {   // the sequence at w.x is this thread's
+    if (w.x < before || w.x >= before + a.heads * head) return;
+    s_b = b;
+    s_base = before;
+    s_head = head;
+    s_q0 = q0;
+    s_T = T;
+    s_n = n;
+  };
   if (batch <= NT) {   // the sums were one sequence each
-    if (w.x >= before && w.x < before + first) {
-      s_b = tid;
-      s_base = before;
-    }
+    take(tid);
   } else {
     long long carry = 0;
     for (int cb = 0; cb < batch && carry <= w.x; cb += NT) {
       const int b = cb + tid;
-      long long u = 0, total;
-      if (b < batch) {
-        int s, T, n;
-        kv_seq<false>(a, b, s, T, n);
-        u = T ? a.heads * kv_head_weight(c, T, n) : 0;
-      }
-      before = carry + cta_scan<NT>(u, s_scan, total);
-      if (w.x >= before && w.x < before + u) {
-        s_b = b;
-        s_base = before;
-      }
+      long long total;
+      T = n = 0;
+      if (b < batch) kv_seq<false>(a, b, q0, T, n);
+      head = kv_weight_warp(c, T, n);
+      before = carry + cta_scan<NT>(a.heads * head, s_scan, total);
+      take(b);
       carry += total;
     }
   }
   __syncthreads();
   w.b = s_b;
   w.base = s_base;
-  kv_seq<false>(a, w.b, q0, w.T, w.n);
-  kv_seek(c, w);
+  q0 = s_q0;
+  w.T = s_T;
+  w.n = s_n;
+  kv_seek_warp(c, w, s_head);
   return w.k0 < w.k1 || kv_advance<RT, PER, EXTRA>(a, w, q0);
 }
 

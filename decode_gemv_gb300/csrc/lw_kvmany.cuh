@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
         }
         if (whole) {
           give(g, l, z);
-        } else {
+        } else if (o.live) {
 #pragma unroll
           for (int n = 0; n < 8; ++n)
             *reinterpret_cast<float4*>(part + 2 * kManyTile + ((8 * g + n) * kManyTile + row) * 4) =
@@ -914,7 +914,7 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
           const float Mu = M == -INFINITY ? 0.f : M;
           for (int i = 0; i < parts; ++i) S = fmaf(__ldcg(from(i) + kManyTile + row), ex2(__ldcg(from(i) + row) - Mu), S);
 #pragma unroll 1
-          for (int g = hf; g < G; g += F::kTileWarps / 4) {
+          for (int g = hf; o.live && g < G; g += F::kTileWarps / 4) {
             float z[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) z[j] = 0.f;

@@ -61,12 +61,14 @@ struct KvShape {
   int group, RT, per, extra, causal, window;
 };
 
-// Weight of one key/value head of a sequence.
+// Weight of an item, and of one key/value head of a sequence.
+LW_TC_HD int kv_item_weight(const KvShape& c, int T, int n, int rt) {
+  return c.extra + kv_units(kv_tile_span(T, n, c.group, c.RT, rt, c.causal, c.window), c.per);
+}
 LW_TC_HD long long kv_head_weight(const KvShape& c, int T, int n) {
   const int nrt = kv_row_tiles(T, c.group, c.RT);
   long long s = 0;
-  for (int rt = 0; rt < nrt; ++rt)
-    s += c.extra + kv_units(kv_tile_span(T, n, c.group, c.RT, rt, c.causal, c.window), c.per);
+  for (int rt = 0; rt < nrt; ++rt) s += kv_item_weight(c, T, n, rt);
   return s;
 }
 
