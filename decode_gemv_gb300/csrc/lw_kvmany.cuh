@@ -51,7 +51,7 @@ struct Many {
   using L = KvTile<D>;
   static constexpr int kRows = WIDE ? kManyTile : 2 * kManyTile;   // of an item
   // an item's start and end, in units' time: 18000 cycles of 2300 (WIDE: 5500) a unit
-  static constexpr int kExtra = WIDE ? (D == 64 ? 7 : 4) : 8;
+  static constexpr int kExtra = WIDE ? (D == 64 ? 8 : 4) : 10;
   static constexpr int kBufs = !WIDE || D == 64 ? 4 : D == 96 ? 3 : 2;   // restored units
   // With two buffers a key tile is free after its S, not after its O: the keys two units on are
   // restored while the rows work (with the pair as one, O(i) - restore - S(i + 2) - O(i + 1) were
