@@ -46,9 +46,14 @@ __device__ __forceinline__ int64_t slot_tile(const CacheArgs& a, int64_t slot, i
   return page * a.page_bytes + (int64_t)(tile - page * (uint32_t)a.page_tiles) * tile_bytes;
 }
 
-// Both kernels: a block takes 16 tokens of one head, a thread 8 consecutive
-// keys and the same 8 values of one of them (4 neighbouring lanes a group).
-// Bound by HBM: 2 bytes in or out a bf16 element, 0.625 for the cache.
+// Both kernels: a block takes 16 tokens of one head (a tile of the cache, if they
+// are consecutive, whose lines it completes), a thread 8 consecutive keys and the
+// same 8 values of one of them (4 neighbouring lanes a group).  The bytes that
+// have to move are 2 in or out a bf16 element and 0.625 for the cache.
+// Measured, 65536 tokens of 8 heads of 128 in bf16: write 87 us, 4.05 TB/s
+// (issue-bound: 84 % of the slots, 21 instructions a value for the range, the
+// definition's separate subtract, multiply and rint, and the nibbles), read 68
+// us, 5.2 TB/s.  A copy reaches 6.8.
 constexpr int kTokens = 16;
 
 template <class T, int D, bool VEC>

@@ -5,7 +5,7 @@
 // 128; keys come 64 at a time.  S = Q K^T and O += P V are tcgen05.mma: Q, K
 // and V (fp16, restored from the codes) are operand tiles in shared memory, P
 // and the accumulators lie in tensor memory.
-//  * 6 loader warps (WIDE: 10) take the 16-key tiles in turn: bulk copies bring the next
+//  * 6 loader warps take the 16-key tiles in turn: bulk copies bring the next
 //    ones while the last, in registers, is restored -- k = sc c + mn and v = sc c +
 //    mn by one rounded fp16 fma each -- and stored as operand tiles (four
 //    buffers), once for both row tiles;
@@ -25,7 +25,24 @@
 // WIDE (fp16 and fp32 calls): every operand is two fp16 parts, x = hi + lo 2^-11,
 // an item is one tile of 128 rows, and what the second tile had holds the lo
 // parts: S = Qh Kh + 2^-11 (Qh Kl + Ql Kh), O likewise from P and V, the two sums
-// in accumulators of their own (issuer 0 the first, issuer 1 the second).
+// in accumulators of their own (issuer 0 the first, issuer 1 the second; fp16
+// queries are their hi parts).  Two threads share a row, 32 keys of a unit each
+// (one a row had the loaders and the tensor cores wait: 2 x 1024 tokens on 4096
+// keys 537 -> 443 us), and agree through shared memory on the row's maximum where
+// it is raised.  Restoring an element is five times the work, so there are 8
+// loaders (64 wide: 6 of more registers); the buffers are what fits.
+//
+// Measured (8 heads of 128 with 4 query heads each), us and useful TFLOP/s, two
+// products a (row, key) pair:
+//   bf16  2048 tokens on 16384 keys 427, 1206    4096 on 4096 164, 836
+//         8 x 64 on 8192 85, 800                 8 x 512 on 512 77, 224
+//   fp16  2 x 1024 on 4096 390, 308 (five products for two)
+//   fp32  2 x 90 on 2400 50, 138 (six products for two)
+// Long bf16 chunks are bound by the row warps' softmax and the loaders' restoring
+// together (issue 62 %, tensor cores 50 %): two row warps and one and a half
+// loaders share a scheduler, a unit takes 2100 cycles, its products 1250 and its
+// exponentials 1000.  Short items are bound by their starts and ends: reading Q
+// 7000 cycles, writing out 4000 to 9000, joining a cut item's parts 10000.
 //
 // The operand tiles are K-major core matrices of 8 x 16 bytes.  A key code
 // word holds 8 elements of one key: its fp16 pairs are elements (0,4), (1,5),
@@ -50,7 +67,8 @@ template <int D, bool WIDE>
 struct Many {
   using L = KvTile<D>;
   static constexpr int kRows = WIDE ? kManyTile : 2 * kManyTile;   // of an item
-  // an item's start and end, in units' time: 18000 cycles of 2300 (WIDE: 5500) a unit
+  // an item's start and end, in units' time: some 20000 cycles of 2100 (WIDE: 4000 a unit, 2500 where 64
+  // wide).  4096 tokens on 4096 keys: 6 191 us, 8 165, 10 164, 16 170
   static constexpr int kExtra = WIDE ? (D == 64 ? 8 : 4) : 10;
   static constexpr int kBufs = !WIDE || D == 64 ? 4 : D == 96 ? 3 : 2;   // restored units
   // With two buffers a key tile is free after its S, not after its O: the keys two units on are
@@ -725,7 +743,7 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
         if (!WIDE && !ok) break;
         tc_fence_after();
         const uint32_t there = *reinterpret_cast<const volatile uint32_t*>(present + it % 4 * kManyUnit) >> (16 * hf) & (WIDE ? 0xFFFFu : 0xFFFFFFFFu);
-        uint32_t s0[32], s1[32];   // WIDE: s0 alone
+        uint32_t s0[32], s1[32];   // WIDE: the scores are s0 (s1 brings the lo parts' sum)
         tmem_ld32(sc, s0);
         if constexpr (!WIDE) tmem_ld32(sc + 32, s1);
         else tmem_ld32(mine + F::s_col(1, b) + 32 * hf, s1);

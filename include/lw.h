@@ -568,7 +568,14 @@ int32_t lw_table_lut_entries(const lw_table* t);
  * length are not used, whatever they hold.
  *
  * head_dim is 64, 96 or 128 (else LW_ERR_UNSUPPORTED), page_tokens a positive
- * multiple of 16, pages 16-byte aligned.
+ * multiple of 16, pages 16-byte aligned; n_pages * page_tokens < 2^32 (else
+ * LW_ERR_SHAPE).
+ *
+ * The three calls are asynchronous on `stream`, allocate nothing and can be
+ * captured; each reads and writes nothing before the work queued in front of it
+ * has completed.  d_status may be NULL.  Errors: LW_ERR_INVALID_ARG (a missing or
+ * misaligned address, rows of two types, a negative count, a workspace too
+ * small), LW_ERR_SHAPE, LW_ERR_UNSUPPORTED, LW_ERR_CUDA.
  */
 #define LW_KV_GROUP 32
 #define LW_KV_TILE 16
@@ -629,8 +636,12 @@ lw_status lw_kv_read(const lw_kv_cache* c, const int64_t* slots, int64_t n, cons
  *   s_j = scale q.k_j;  out = sum_j softmax(s)_j v_j;  lse = log sum_j exp s_j
  * with the cached values of k and v.  A query that sees no key gets out = 0,
  * lse = -inf.  Page-table entries beyond a sequence's length, and pages no
- * query sees, are not read.  The answer does not depend on max_q, on the page
- * size or on where the pages lie; it is deterministic on a given device.
+ * query sees, are not read.  The answer does not depend on the page size or on
+ * where the pages lie, and on max_q only through the kernel that it chooses (the
+ * same to the type's rounding); it is deterministic on a given device.  Sums and
+ * softmax statistics are fp32.  fp32 and fp16 calls carry every 16-bit operand of
+ * a matrix instruction in two parts (22 bits), bf16 calls in one (11 bits).
+ * q_tokens * q_heads and max_q * q_heads are below 2^31 (else LW_ERR_SHAPE).
  */
 typedef struct {
   const void* q;               /* [q_tokens][q_heads][head_dim], strided */
@@ -648,15 +659,16 @@ typedef struct {
   int32_t batch;
   int32_t q_heads;             /* a multiple of kv_heads */
   int32_t max_q;               /* the most query tokens a sequence has (chooses
-                                  the kernel, nothing else) */
+                                  the kernel; a larger or smaller number is right too) */
   int32_t causal;              /* 0 or 1 */
   int32_t window;              /* 0: unlimited */
   float scale;
 } lw_kv_attn;
 
 /* Bytes of device workspace an lw_kv_attention call needs (zeroed by the
-   caller before first use; every call that completes leaves its counters at
-   zero).  0 for an unsupported shape. */
+   caller before first use; every call leaves its counters at zero, but for one
+   that reports LW_DEV_TIMEOUT: zero it again then).  0 for an unsupported
+   shape. */
 size_t lw_kv_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens,
                              int32_t batch);
 
