@@ -578,6 +578,36 @@ def test_long_window(typ):
     Setup(20, [700, 900], [700, 1100], 8, 1, 64, 32, typ).check(window=200)
 
 
+@pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
+def test_many_row_tiles(typ):
+    """Prompts of over a hundred row tiles a head between short ones: the search for a CTA's range
+    shares them among lanes."""
+    Setup(21, [2100, 3, 0, 900], [2100, 50, 9, 1000], 8, 1, 64, 32, typ).check(window=100)
+
+
+@pytest.mark.parametrize("typ", ["fp16", "bf16"])
+def test_long_prompts_among_many_sequences(typ):
+    """More sequences than a CTA has threads, two of them of many row tiles."""
+    q_len, kv_len = [i % 3 for i in range(700)], [(37 * i) % 90 for i in range(700)]
+    for b, t in ((3, 400), (690, 300)):
+        q_len[b] = kv_len[b] = t
+    Setup(22, q_len, kv_len, 8, 2, 64, 16, typ).check()
+
+
+@pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("tokens", [2, 4, 5, 6, 7, 12, 13])
+def test_rows_around_the_variants(typ, tokens):
+    """8 query heads on 2: 8, 16, 20, 24, 28, 48 and 52 rows of a sequence."""
+    Setup(23, [tokens, 1, tokens], [700, 40, tokens], 8, 2, 96, 16, typ).check()
+
+
+@pytest.mark.parametrize("typ", ["fp32", "bf16"])
+@pytest.mark.parametrize("hint", [1, 3, 1000])
+def test_any_hint_is_right(typ, hint):
+    """max_q below and above the longest sequence's tokens."""
+    Setup(24, [1, 77, 30], [300, 500, 30], 8, 2, 128, 32, typ).check(max_q=hint)
+
+
 def test_offsets_past_32_bits():
     """A cache of over 4 GiB: pages at its far end are written, read and attended."""
     heads, dim, page = 8, 128, 256
