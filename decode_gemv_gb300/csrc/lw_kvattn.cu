@@ -59,6 +59,9 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* w
   //        16 rows   160, 147 : 218 |  49,  42 : 75            48 rows  596 : 675 | 136 : 146
   //        24 rows   230, 258 : 219 |  68,  80 : 75
   //        32 rows   301, 263 : 219 |  82,  82 : 75
+  // One sequence of 8192 keys alone, bf16: 16 rows 20, 26 : 53, 32 rows 26, 29 : 53, 48 rows 33, 34 : 53
+  // (kv_many_kernel's items start and end slowly); the lengths are not known here, so the rule is the
+  // full device's.
   const long long rows = (long long)p->max_q * a.group;
   const int mode = p->dtype != LW_BF16 ? (rows > 48 ? 4 : 0) : (rows > 24 ? 3 : rows > 8 && rows <= 16 ? 1 : 2);
   const Variant v = c->head_dim == 64 ? variant<64>(mode) : c->head_dim == 96 ? variant<96>(mode) : variant<128>(mode);
