@@ -740,6 +740,7 @@ __global__ void __launch_bounds__(Few<D, MODE>::kThreads, Few<D, MODE>::kPerSm) 
             if (some >> i & 1u) f.template tiles<true, 1>(at + i * L::kBytes, kb + i * LW_KV_TILE, w.n, lane);
         }
         held += F::kPair;
+        fence_proxy_async();   // (this lane's reads before the copy that takes the place next, also the next item's)
         __syncwarp();
       }
       t.out = t.out + 1 == F::kStages ? 0 : t.out + 1;
