@@ -20,12 +20,15 @@ struct AttnArgs {
 
 namespace dev {
 
-// T and n of sequence b; T = 0 if its query range is not one (LOUD: reported)
+// T and n of sequence b; T = 0 if its query range is not one (LOUD: reported).
+// Ordinary loads, here and of the page table: what the work in front writes may
+// not be read by way of the read-only path, which the wait for that work does not
+// order.
 template <bool LOUD>
 __device__ __forceinline__ void kv_seq(const AttnArgs& a, int b, int& q0, int& T, int& n) {
-  q0 = __ldg(a.p.q_start + b);
-  const int q1 = __ldg(a.p.q_start + b + 1);
-  n = __ldg(a.p.kv_len + b);
+  q0 = a.p.q_start[b];
+  const int q1 = a.p.q_start[b + 1];
+  n = a.p.kv_len[b];
   const int most = a.p.table_width * a.page_tokens;
   const bool bad = q0 < 0 || q1 < q0 || q1 > a.p.q_tokens;
   if (LOUD && (bad || n < 0 || n > most)) report(a.status, LW_DEV_BAD_SEQ);

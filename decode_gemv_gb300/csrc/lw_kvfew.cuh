@@ -609,7 +609,7 @@ struct FewFetch {
   __device__ __forceinline__ void lookup(const AttnArgs& a, int lane) {
     const int tile = next + lane / N * STEP + lane % N, tpp = a.page_tokens / LW_KV_TILE;
     const bool mine = tile < last;
-    const int page = mine ? __ldg(table + tile / tpp) : -1;
+    const int page = mine ? table[tile / tpp] : -1;
     const bool ok = page >= 0 && page < a.n_pages;
     if (mine && !ok) report(a.status, LW_DEV_BAD_PAGE);
     there = __ballot_sync(0xFFFFFFFFu, ok);

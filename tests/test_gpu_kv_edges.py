@@ -28,3 +28,31 @@ def test_ring_places_are_reused(typ, tokens, dim):
     for _ in range(20):
         again, _ = s.run()
         assert torch.equal(again, first)
+
+
+@pytest.mark.parametrize("typ,q_len", [("bf16", [1, 1, 1]), ("fp32", [40, 33, 64])])
+def test_arguments_written_just_before_the_call(typ, q_len):
+    """Lengths, query ranges and the page table come from the work in front of the call, step after
+    step of one captured graph."""
+    s = Setup(32, q_len, [130, 64, 70], 8, 2, 128, 16, typ)
+    want, _ = s.run(lse=False)
+    fresh = [t.clone() for t in (s.lens, s.start, s.table)]
+    out = torch.zeros_like(want)
+    ws = torch.zeros(lw.lw_kv_workspace_bytes(s.cache, 8, sum(q_len), 3), dtype=torch.uint8, device=DEV)
+    token = torch.zeros(1, 2, 128, device=DEV)
+    none = torch.full((1,), -1, dtype=torch.int64, device=DEV)
+    g = lw.StepGraph(torch.cuda.Stream())
+    with g.capture():
+        for t, f in zip((s.lens, s.start, s.table), fresh):
+            t.copy_(f)
+        lw.lw_kv_write(s.cache, token, token, none, s.st)   # (a call that lets the next one start early)
+        s.run(lse=False, out=out, ws=ws)
+        s.lens.fill_(1)          # what a stale read would find
+        s.start.fill_(0)
+        s.table.fill_(-1)
+    for _ in range(5):
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        g.launch()
+        torch.cuda.synchronize()
+        assert int(s.st) == 0 and torch.equal(out, want)
