@@ -255,7 +255,8 @@ extern "C" lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, 
   if (a->batch < 1 || a->batch > 65535) return fail(LW_ERR_SHAPE, "batch %d (1..65535)", a->batch);
   if (a->q_tokens < 0 || a->q_tokens > (1ll << 31) - 1)
     return fail(LW_ERR_SHAPE, "%lld query tokens", (long long)a->q_tokens);
-  if (a->q_tokens * a->q_heads > (1ll << 31) - 1 || (int64_t)a->max_q * a->q_heads > (1ll << 31) - 1)
+  // (rows and keys are counted in 32 bits, to the end of the last item or unit)
+  if (a->q_tokens * a->q_heads > kKvMost || (int64_t)a->max_q * a->q_heads > kKvMost)
     return fail(LW_ERR_SHAPE, "%lld query tokens of %d heads", (long long)a->q_tokens, a->q_heads);
   if (a->max_q < 0) return fail(LW_ERR_INVALID_ARG, "max_q %d", a->max_q);
   if (a->window < 0) return fail(LW_ERR_INVALID_ARG, "window %d", a->window);
@@ -263,7 +264,7 @@ extern "C" lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, 
   if (!(a->scale >= -3.402823466e38f && a->scale <= 3.402823466e38f))
     return fail(LW_ERR_INVALID_ARG, "scale is not finite");
   if (a->table_width < 0 || a->table_stride < 0 ||
-      (int64_t)a->table_width * c->page_tokens > (1ll << 31) - 1)
+      (int64_t)a->table_width * c->page_tokens > kKvMost)
     return fail(LW_ERR_SHAPE, "page table of %d pages of %d tokens", a->table_width, c->page_tokens);
   if (a->q_tokens == 0) return LW_OK;
   if (!a->q || !a->out || !a->q_start || !a->kv_len || (a->table_width && !a->page_table))

@@ -10,6 +10,11 @@ namespace lw {
 int device_sm_count();
 int resident_blocks(const void* kernel, int threads, size_t smem);
 
+// The most rows (query tokens times heads) of an attention call, and keys of its
+// page table: 32-bit numbers with room for the rows and keys that the last row
+// tile (256 rows) and unit (256 keys) run past the end.
+constexpr int64_t kKvMost = (1ll << 31) - 1024;
+
 // Views of the cache and of rows of heads, checked by every call.
 lw_status check_kv_cache(const lw_kv_cache* c);
 inline bool kv_type_ok(int32_t t) { return t == LW_F32 || t == LW_F16 || t == LW_BF16; }

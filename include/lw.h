@@ -568,8 +568,8 @@ int32_t lw_table_lut_entries(const lw_table* t);
  * length are not used, whatever they hold.
  *
  * head_dim is 64, 96 or 128 (else LW_ERR_UNSUPPORTED), page_tokens a positive
- * multiple of 16, pages 16-byte aligned; n_pages * page_tokens < 2^32 (else
- * LW_ERR_SHAPE).
+ * multiple of 16 up to 2^20, kv_heads at most 65535, pages 16-byte aligned;
+ * n_pages * page_tokens < 2^32 (else LW_ERR_SHAPE).
  *
  * The three calls are asynchronous on `stream`, allocate nothing and can be
  * captured; each reads and writes nothing before the work queued in front of it
@@ -641,7 +641,8 @@ lw_status lw_kv_read(const lw_kv_cache* c, const int64_t* slots, int64_t n, cons
  * same to the type's rounding); it is deterministic on a given device.  Sums and
  * softmax statistics are fp32.  fp32 and fp16 calls carry every 16-bit operand of
  * a matrix instruction in two parts (22 bits), bf16 calls in one (11 bits).
- * q_tokens * q_heads and max_q * q_heads are below 2^31 (else LW_ERR_SHAPE).
+ * q_tokens * q_heads, max_q * q_heads and table_width * page_tokens are at most
+ * 2^31 - 1024, batch and q_heads at most 65535 (else LW_ERR_SHAPE).
  */
 typedef struct {
   const void* q;               /* [q_tokens][q_heads][head_dim], strided */
