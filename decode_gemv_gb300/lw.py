@@ -775,21 +775,25 @@ def lw_kv_page_bytes(kv_heads: int, head_dim: int, page_tokens: int) -> int:
 
 
 def lw_kv_workspace_bytes(cache: KvCache, q_heads: int, q_tokens: int, batch: int) -> int:
+    if cache.index >= 0 and _current_device() != cache.index:   # (sized by the current device)
+        _kv_on("lw_kv_workspace_bytes", cache)
     return int(load().lw_kv_workspace_bytes(cache.ref, q_heads, q_tokens, batch))
 
 
 _KV_TYPES = {}          # torch dtype -> lw_dtype
 _I32 = _I64 = _F32 = None
 _raw_stream = None      # device index -> its current stream's handle
+_current_device = None  # () -> index of the current device, which the library launches on
 
 
 def _kv_torch(torch):
-    global _I32, _I64, _F32, _raw_stream
+    global _I32, _I64, _F32, _raw_stream, _current_device
     if _KV_TYPES:
         return
     _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _KV_TYPES.update({torch.float32: LW_F32, torch.float16: LW_F16, torch.bfloat16: LW_BF16})
 
 
@@ -836,6 +840,8 @@ def _kv_index(fn: str, name: str, t, dtype, n):
 def _kv_on(fn: str, cache: KvCache, *named):
     if cache.index < 0:
         _refuse(fn, f"cache: pages on {cache.device}, expected a CUDA device")
+    if _current_device() != cache.index:
+        _refuse(fn, f"cache: pages on {cache.device}, the current device is cuda:{_current_device()}")
     for name, t in named:
         if t.device != cache.device:
             _refuse(fn, f"{name}: on {t.device}, the cache is on {cache.device}")
@@ -861,7 +867,7 @@ def _kv_rows(fn, cache, slots, k, v, d_status, written):
         ok = (code is not None and v.dtype is k.dtype and k.shape == shape and v.shape == shape
               and kd == 1 and vd == 1 and slots.dtype is _I64 and slots.dim() == 1
               and slots.is_contiguous() and d_status.dtype is _I32 and d_status.numel() >= 1
-              and d_status.is_contiguous() and dev >= 0 and k.get_device() == dev
+              and d_status.is_contiguous() and dev >= 0 and _current_device() == dev and k.get_device() == dev
               and v.get_device() == dev and slots.get_device() == dev and d_status.get_device() == dev
               and (not written or (_kv_distinct(k) and _kv_distinct(v))))
     except (AttributeError, TypeError, ValueError, IndexError):
@@ -947,7 +953,8 @@ def lw_kv_attention(cache: KvCache, q, q_start, kv_len, page_table, out, ws, d_s
               and kv_len.dtype is _I32 and kv_len.shape == (batch,) and kv_len.is_contiguous()
               and page_table.dtype is _I32 and (td == 1 or width <= 1)
               and ws.is_contiguous() and d_status.dtype is _I32 and d_status.numel() >= 1
-              and d_status.is_contiguous() and type(max_q) is int and dev >= 0 and q.get_device() == dev
+              and d_status.is_contiguous() and type(max_q) is int and dev >= 0 and _current_device() == dev
+              and q.get_device() == dev
               and out.get_device() == dev and q_start.get_device() == dev
               and kv_len.get_device() == dev and page_table.get_device() == dev
               and ws.get_device() == dev and d_status.get_device() == dev

@@ -573,7 +573,8 @@ int32_t lw_table_lut_entries(const lw_table* t);
  *
  * The three calls are asynchronous on `stream`, allocate nothing and can be
  * captured; each reads and writes nothing before the work queued in front of it
- * has completed.  d_status may be NULL.  Errors: LW_ERR_INVALID_ARG (a missing or
+ * has completed.  They launch on the current device, which has to be the one of
+ * the stream and of every address.  d_status may be NULL.  Errors: LW_ERR_INVALID_ARG (a missing or
  * misaligned address, rows of two types, a negative count, a workspace too
  * small), LW_ERR_SHAPE, LW_ERR_UNSUPPORTED, LW_ERR_CUDA.
  */

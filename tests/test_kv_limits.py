@@ -36,3 +36,68 @@ def test_the_largest_sizes_are_taken():
     for kw in (dict(q_tokens=2 ** 31 - 1024), dict(max_q=2 ** 31 - 1024), dict(table_width=2 ** 27 - 64)):
         assert c_attention(**kw) == lw.LW_ERR_INVALID_ARG
         assert b"workspace" in lw.load().lw_last_error()
+
+
+# ---- the binding ------------------------------------------------------------
+
+class OnDevice1(torch.Tensor):
+    """A tensor that says it is on cuda:1."""
+    device = property(lambda self: torch.device("cuda:1"))
+
+    def get_device(self):
+        return 1
+
+
+def on1(t):
+    return t.as_subclass(OnDevice1)
+
+
+class Calls:
+    """Stands in for the library: counts the device calls and does nothing."""
+
+    def __init__(self, real):
+        self.real, self.made = real, []
+
+    def __getattr__(self, name):
+        if name in ("lw_kv_write", "lw_kv_read", "lw_kv_attention", "lw_kv_workspace_bytes"):
+            return lambda *a: self.made.append(name) or 0
+        return getattr(self.real, name)
+
+
+@pytest.fixture
+def device1(monkeypatch):
+    """A cache that says it is on cuda:1; its calls, by name; and which device is current."""
+    cache = lw.KvCache.empty(3, 2, 64, 16, device="cpu")
+    cache.index, cache.device = 1, torch.device("cuda:1")
+    lib, now = Calls(lw.load()), [1]
+    monkeypatch.setattr(lw, "_lib", lib)
+    monkeypatch.setattr(lw, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(lw, "_current_device", lambda: now[0], raising=False)
+    i32, st = dict(dtype=torch.int32), on1(torch.zeros(1, dtype=torch.int32))
+    k, v, slots = on1(torch.zeros(4, 2, 64)), on1(torch.zeros(4, 2, 64)), on1(torch.zeros(4, dtype=torch.int64))
+    q, out = on1(torch.zeros(3, 4, 64)), on1(torch.zeros(3, 4, 64))
+    start, lens, table = (on1(t) for t in (torch.tensor([0, 1, 3], **i32), torch.zeros(2, **i32),
+                                           torch.zeros(2, 5, **i32)))
+    ws = on1(torch.zeros(1000, dtype=torch.uint8))
+    calls = {"lw_kv_write": lambda k=k, v=v: lw.lw_kv_write(cache, k, v, slots, st),
+             "lw_kv_read": lambda k=k, v=v: lw.lw_kv_read(cache, slots, k, v, st),
+             "lw_kv_attention": lambda **kw: lw.lw_kv_attention(cache, q, start, lens, table, out, ws, st,
+                                                               **{"max_q": 2, **kw}),
+             "lw_kv_workspace_bytes": lambda: lw.lw_kv_workspace_bytes(cache, 4, 3, 2)}
+    return lib, now, calls
+
+
+def test_the_current_device_has_to_be_the_caches(device1):
+    """The library launches on, and sizes by, the current device: with another one current the calls
+    would hand its kernels addresses of the cache's device."""
+    lib, now, calls = device1
+    for name, call in calls.items():
+        call()
+        assert lib.made == [name]
+        lib.made.clear()
+        now[0] = 0
+        with pytest.raises(lw.LwError) as e:
+            call()
+        assert e.value.status == lw.LW_ERR_INVALID_ARG and "current device" in str(e.value)
+        assert not lib.made
+        now[0] = 1
