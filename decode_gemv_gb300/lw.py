@@ -807,6 +807,28 @@ def _kv_distinct(t) -> bool:
     return (sh >= d and st >= (h - 1) * sh + d) or (st >= d and sh >= (n - 1) * st + d)
 
 
+def _kv_apart(k, v) -> bool:
+    """Whether the rows [tokens][heads][dim] of `k` and `v` (one shape and type, the last
+    dimension contiguous) share no byte."""
+    n, h, d = k.shape
+    if n == 0 or h == 0:
+        return True
+    size, at, bt = k.element_size(), k.data_ptr(), v.data_ptr()
+    (kt, kh, _), (vt, vh, _) = k.stride(), v.stride()
+    row = d * size
+    kspan, vspan = (n - 1) * kt + (h - 1) * kh, (n - 1) * vt + (h - 1) * vh
+    if at + kspan * size + row <= bt or bt + vspan * size + row <= at:
+        return True
+    if kt == vt and kh == vh:   # interleaved in one buffer: a token's heads, then the other's, or head by head
+        apart, heads = abs(bt - at), (h - 1) * kh * size + row
+        if heads <= apart <= kt * size - heads or (row <= apart <= kh * size - row and apart + heads <= kt * size):
+            return True
+    starts = np.sort(np.concatenate([
+        (p + size * (np.arange(n)[:, None] * t + np.arange(h) * s)).ravel()
+        for p, t, s in ((at, kt, kh), (bt, vt, vh))]))
+    return bool((np.diff(starts) >= row).all())
+
+
 def _kv_heads(fn: str, name: str, t, tokens, heads, dim, written=False):
     """Refuse anything but rows of heads [tokens][heads][dim]."""
     import torch
@@ -853,6 +875,8 @@ def _kv_rows_refuse(fn, cache, slots, k, v, d_status, written):
         _kv_heads(fn, name, t, slots.shape[0], cache.kv_heads, cache.head_dim, written)
     if k.dtype != v.dtype:
         _refuse(fn, f"v: dtype {v.dtype}, k has {k.dtype}")
+    if written and not _kv_apart(k, v):
+        _refuse(fn, "v: rows that are written overlap k's")
     _status_ptr(fn, d_status)
     _kv_on(fn, cache, ("slots", slots), ("k", k), ("v", v), ("d_status", d_status))
 
@@ -869,7 +893,7 @@ def _kv_rows(fn, cache, slots, k, v, d_status, written):
               and slots.is_contiguous() and d_status.dtype is _I32 and d_status.numel() >= 1
               and d_status.is_contiguous() and dev >= 0 and _current_device() == dev and k.get_device() == dev
               and v.get_device() == dev and slots.get_device() == dev and d_status.get_device() == dev
-              and (not written or (_kv_distinct(k) and _kv_distinct(v))))
+              and (not written or (_kv_distinct(k) and _kv_distinct(v) and _kv_apart(k, v))))
     except (AttributeError, TypeError, ValueError, IndexError):
         ok = False
     if not ok:

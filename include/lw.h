@@ -623,6 +623,7 @@ lw_status lw_kv_write(const lw_kv_cache* c, const lw_kv_rows* k, const lw_kv_row
  * Read n slots back: scale * code + min in fp32, rounded to the rows' type.
  * A negative slot reads as zeros, and so does one past the last page (which
  * is reported).
+ * k's and v's rows must not overlap.
  */
 lw_status lw_kv_read(const lw_kv_cache* c, const int64_t* slots, int64_t n, const lw_kv_rows* k,
                      const lw_kv_rows* v, int32_t* d_status, void* stream);

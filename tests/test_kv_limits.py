@@ -101,3 +101,34 @@ def test_the_current_device_has_to_be_the_caches(device1):
         assert e.value.status == lw.LW_ERR_INVALID_ARG and "current device" in str(e.value)
         assert not lib.made
         now[0] = 1
+
+
+def test_read_refuses_keys_and_values_in_one_place(device1):
+    """Two writers on an element leave either's value: k and v that share memory are refused, rows
+    that only lie between one another are not."""
+    lib, _, calls = device1
+    both = torch.zeros(4, 2, 2, 64)                      # a token's keys, then its values
+    flat = torch.zeros(4 * 2 * 64 * 2 + 64)
+    fine = [(torch.zeros(4, 2, 64), torch.zeros(4, 2, 64)),
+            (both[:, 0], both[:, 1]), (both[:, 1], both[:, 0]),
+            (both[:, :, 0], both[:, :, 1]),              # head by head
+            (torch.zeros(2, 2, 4, 64)[:, 0].transpose(0, 1), torch.zeros(4, 2, 64)),
+            (flat[:512].view(4, 2, 64), flat[512:1024].view(4, 2, 64)),
+            # different strides in one buffer: k's tokens before v's heads
+            (flat[:512].view(4, 2, 64), flat[512:1024].view(2, 4, 64).transpose(0, 1))]
+    for k, v in fine:
+        calls["lw_kv_read"](on1(k), on1(v))
+        assert lib.made == ["lw_kv_read"]
+        lib.made.clear()
+    k = torch.zeros(4, 2, 64)
+    wrong = [(k, k), (k, k.view(2, 4, 64).transpose(0, 1)),
+             (flat[:512].view(4, 2, 64), flat[448:960].view(4, 2, 64)),          # the last head
+             (flat[:512].view(4, 2, 64), flat[511:1023].view(4, 2, 64)),         # one element
+             (both[:, 0], both.view(-1)[64:64 + 960].as_strided((4, 2, 64), (256, 64, 1)))]
+    for k, v in wrong:
+        with pytest.raises(lw.LwError) as e:
+            calls["lw_kv_read"](on1(k), on1(v))
+        assert e.value.status == lw.LW_ERR_INVALID_ARG and "overlap" in str(e.value)
+        assert not lib.made
+        calls["lw_kv_write"](on1(k), on1(v))             # (rows that are read may)
+        lib.made.clear()
