@@ -997,7 +997,7 @@ def lw_kv_attention(cache: KvCache, q, q_start, kv_len, page_table, out, ws, d_s
                           0 if lse is None else lse.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
                           page_table.data_ptr(), ts, tokens, width, code, batch, heads, max_q,
                           1 if causal else 0, window, dim ** -0.5 if scale is None else scale)
-    except (struct.error, OverflowError) as e:
+    except struct.error as e:
         _refuse("lw_kv_attention", f"max_q {max_q!r}, window {window!r}, scale {scale!r}: {e}")
     r = _lib.lw_kv_attention(cache.ref, a, ws.data_ptr(), ws.numel() * ws.element_size(),
                              d_status.data_ptr(),
