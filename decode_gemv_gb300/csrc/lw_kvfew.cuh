@@ -176,7 +176,7 @@ struct FewWarp {
   // the middles of group lane / 4 (hi parts; lane / 4 - 4: lo parts)
   float o[NR][G][2][4], om[NR][4];
   float unit;       // 2^E, E <= 0: the operands and all sums are of p 2^-E
-  uint32_t seen;    // exponent bits of the scales so far, of even and of odd keys
+  uint32_t limit;   // largest scale that the unit covers, twice (fp16)
   float fm;         // row[0].m when the sums last went to shared memory (MODE 0)
 
   // Row r of the row tile (lane / 4, and lane / 4 + 8 in MODE 1)
@@ -258,7 +258,7 @@ struct FewWarp {
     for (int i = 0; i < NR; ++i) load_row(a, w, q0, rt_rows, i, lane);
     clear();
     unit = 6.103515625e-5f;   // 2^-14
-    seen = 0;
+    limit = 0x07FF07FFu;
     fm = -INFINITY;
   }
   __device__ __forceinline__ void clear() {
@@ -339,9 +339,8 @@ struct FewWarp {
       top[j] *= row[j].f;
       up |= top[j] > row[j].m;
     }
-    // the value operands' unit covers the largest scale so far: new exponent bits are looked at (a
-    // scale of bits seen before is at most 2^15 times the largest, and 2^15 stays in range)
-    uint32_t bits = 0;
+    // the value operands' unit covers the largest scale so far (a NaN is none: the maximum leaves it out)
+    uint32_t big = 0;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const uint32_t at = s + (uint32_t)(i * L::kBytes + L::kValScale);
@@ -354,10 +353,10 @@ struct FewWarp {
           s0[g] = cut(s0[g], kb + 16 * i + 2 * q, n);
           s1[g] = cut(s1[g], kb + 16 * i + 8 + 2 * q, n);
         }
-        bits |= s0[g] | s1[g];
+        big = max_h2(big, max_h2(s0[g], s1[g]));
       }
     }
-    up |= (bits & 0x7C007C00u & ~seen) != 0;
+    up |= max_h2(big, limit) != limit;
     if (__any_sync(0xFFFFFFFFu, up)) {   // a new maximum: rescale
       float al[NR];
 #pragma unroll
@@ -370,31 +369,11 @@ struct FewWarp {
         al[j] = ex2(row[j].m - mu);
         row[j].m = x;
       }
-      // the largest scale of the tiles (a NaN is none)
-      uint32_t big = 0;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const uint32_t at = s + (uint32_t)(i * L::kBytes + L::kValScale);
-        uint32_t s0[G], s1[G];
-        lds_words<G>(at + (uint32_t)(q * G) * 4, s0);
-        lds_words<G>(at + (uint32_t)((q + 4) * G) * 4, s1);
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          if constexpr (EDGE) {
-            s0[g] = cut(s0[g], kb + 16 * i + 2 * q, n);
-            s1[g] = cut(s1[g], kb + 16 * i + 8 + 2 * q, n);
-          }
-          big = max_h2(big, max_h2(s0[g], s1[g]));
-        }
-      }
-#pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        big = max_h2(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
-        bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, d);
-      }
-      seen |= bits;
-      uint32_t e = max(big & 0x7FFFu, big >> 16 & 0x7FFFu) >> 10;
-      e = e < 1 ? 1 : (e > 15 ? 15 : e);
+      for (int d = 1; d < 4; d <<= 1) big = max_h2(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
+      big = max_h2(big, limit);
+      const uint32_t e = min(max(big & 0x7FFFu, big >> 16) >> 10, 15u);   // (beyond, p sc stays in range as it is)
+      limit = e == 15 ? 0x7BFF7BFFu : (e << 10 | 0x3FFu) * 0x10001u;
       const float before = unit;
       unit = fmaxf(unit, __uint_as_float((e + 112) << 23));
       const float down = before * __uint_as_float(0x7F000000u - __float_as_uint(unit));

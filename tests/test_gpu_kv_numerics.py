@@ -1,0 +1,136 @@
+"""Attention over the 4-bit cache on rows that are hard to add up, against a
+plain implementation in 64 bits on the cached values: value scales that rise
+after a NaN, rows that one key dominates, value groups of very different
+scales, and where a NaN goes, element by element.
+
+Tolerances, normwise (u = half a unit of the output type), S = the largest
+|score| of a test's inputs (natural units):
+* fp32 and fp16 calls: scores and probabilities in 22 bits, 4 S 2^-21 as the
+  rest of the tests have it (test_gpu_kv.py), plus u;
+* bf16 calls: p and p sc (few rows), p and v (many rows) each rounded to 11
+  bits, 2 2^-12; a key of many rows is rounded to 11 bits as well, which where
+  its elements err alike moves a score by S 2^-12; plus u = 2^-9.
+"""
+import numpy as np
+import pytest
+
+from decode_gemv_gb300 import lw
+from test_gpu_kv import DEV, TYPES, Setup, dequantise, quantise, status
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+U = {"fp32": 2.0 ** -24, "fp16": 2.0 ** -11, "bf16": 2.0 ** -9}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    lw.load()
+
+
+def bound(typ, top, many):
+    if typ == "bf16":
+        return U[typ] + 2.0 ** -11 + (top * 2.0 ** -12 if many else 4 * top * 2.0 ** -21)
+    return U[typ] + 4 * top * 2.0 ** -21
+
+
+class Given(Setup):
+    """Sequences of the given keys and values [n, kv_heads, dim] and queries [tokens, q_heads, dim]."""
+
+    def __init__(self, k, v, q, page, typ, seed=0):
+        kv_heads, dim = k[0].shape[1:]
+        rng = np.random.default_rng(seed)
+        self.args = (q[0].shape[1], kv_heads, dim, page)
+        self.q_len, self.kv_len, self.typ = [len(x) for x in q], [len(x) for x in k], typ
+        used = [-(-n // page) for n in self.kv_len]
+        self.cache = lw.KvCache(torch.randint(0, 256, (sum(used) * lw.lw_kv_page_bytes(kv_heads, dim, page),),
+                                              dtype=torch.uint8, device=DEV), kv_heads, dim, page)
+        order, at = rng.permutation(sum(used)).astype(np.int32), 0
+        table = np.full((len(k), max(used)), -1, np.int32)
+        self.k, self.v, self.st = [], [], status()
+        for b, n in enumerate(self.kv_len):
+            table[b, :used[b]] = order[at:at + used[b]]
+            at += used[b]
+            pos = np.arange(n)
+            slots = table[b, pos // page].astype(np.int64) * page + pos % page
+            put = [torch.from_numpy(np.ascontiguousarray(x[b], dtype=np.float32)).to(DEV) for x in (k, v)]
+            lw.lw_kv_write(self.cache, *put, torch.from_numpy(slots).to(DEV), self.st)
+            self.k.append(dequantise(*quantise(np.float32(k[b]))))
+            self.v.append(dequantise(*quantise(np.float32(v[b]))))
+        self.table = torch.from_numpy(table).to(DEV)
+        self.q = torch.from_numpy(np.concatenate(q).astype(np.float32)).to(DEV).to(TYPES[typ])
+        self.start = torch.from_numpy(np.concatenate([[0], np.cumsum(self.q_len)]).astype(np.int32)).to(DEV)
+        self.lens = torch.tensor(self.kv_len, dtype=torch.int32, device=DEV)
+
+    def expect(self, causal=True, window=0):
+        """out (NaN where a NaN of a seen key's value or of its score goes), lse, the largest |score|."""
+        q_heads, kv_heads, dim, _ = self.args
+        q = self.q.double().cpu().numpy()
+        out, lse, at, top = np.zeros(q.shape), np.full(q.shape[:2], -np.inf), 0, 0.0
+        for b, (t, n) in enumerate(zip(self.q_len, self.kv_len)):
+            pos, j = np.arange(n - t, n)[:, None], np.arange(n)[None]
+            see = np.ones((t, n), bool)
+            if causal:
+                see &= j <= pos
+            if window:
+                see &= j > pos - window
+            for h in range(q_heads):
+                kh = h // (q_heads // kv_heads)
+                k, v = self.k[b][:, kh], self.v[b][:, kh]
+                s = np.where(see, dim ** -0.5 * (q[at:at + t, h] @ np.nan_to_num(k).T), -np.inf)
+                top = max(top, np.abs(s[see]).max(initial=0))
+                m = s.max(-1, keepdims=True)
+                p = np.exp(s - m)
+                l = p.sum(-1, keepdims=True)
+                o, e = p @ np.nan_to_num(v) / l, (m + np.log(l))[:, 0]
+                o[(see.astype(np.float64) @ np.isnan(v)) > 0] = np.nan
+                lost = see[:, np.isnan(k).any(-1)].any(-1)
+                o[lost], e[lost] = np.nan, np.nan
+                out[at:at + t, h], lse[at:at + t, h] = o, e
+            at += t
+        return out, lse, top
+
+    def check(self, causal=True, window=0, many=False, group=None, **kw):
+        got, lse = self.run(causal=causal, window=window, **kw)
+        torch.cuda.synchronize()
+        assert int(self.st) == 0
+        want, wl, top = self.expect(causal, window)
+        g, e = got.double().cpu().numpy(), lse.double().cpu().numpy()
+        wrong = int((np.isnan(g) != np.isnan(want)).sum()), int((np.isnan(e) != np.isnan(wl)).sum())
+        assert wrong == (0, 0), f"NaN, or none, in {wrong} places of out and lse"
+        wrong = int(np.isinf(g).sum())
+        assert wrong == 0, f"{wrong} infinities"
+        tol = bound(self.typ, top, many)
+        d = np.nan_to_num(g) - np.nan_to_num(want)
+        for i in range(0, want.shape[-1], group or want.shape[-1]):
+            part = np.s_[..., i:i + (group or want.shape[-1])]
+            norm = np.linalg.norm(np.nan_to_num(want[part]))
+            err = np.linalg.norm(d[part]) / norm if norm else 0.0
+            assert err <= tol, f"from element {i}: {err:.3e} > {tol:.3e}"
+        f = np.isfinite(wl)
+        assert np.abs(e[f] - wl[f]).max(initial=0) <= top * (2.0 ** -11 if self.typ == "bf16" else 2.0 ** -19) + 1e-6
+        return got
+
+
+# ---- the units that follow the value scales -----------------------------------
+
+@pytest.mark.parametrize("typ,tokens", [("fp32", 1), ("fp16", 1), ("bf16", 1), ("bf16", 4)])
+def test_scales_that_rise_after_a_nan(typ, tokens):
+    """A NaN group among values of scale 0, then scales above 4 under falling scores: a warp's unit
+    follows the scales that come, not the NaN's bits."""
+    rng = np.random.default_rng(41)
+    batch, heads, group, dim, n = 76, 8, 4, 128, 1024
+    unit = np.where(rng.standard_normal(dim) > 0, 1.0, -1.0)
+    k, v, q = [], [], []
+    for _ in range(batch):
+        k.append(np.where(np.arange(n) < 256, 1.0, 0.9)[:, None, None] * unit * np.ones((1, heads, 1)))
+        x = np.full((n, heads, dim), 0.5)
+        x[8:256:16, :, 40] = x[9:256:16, :, 40] = np.nan   # (an even and an odd key of every tile)
+        x[256:] = 100 * rng.standard_normal((n - 256, heads, dim))
+        v.append(x)
+        q.append(0.2 * unit + 0.01 * rng.standard_normal((tokens, heads * group, dim)))
+    s = Given(k, v, q, 64, typ)
+    got = s.check(group=32)
+    nan = torch.isnan(got)
+    assert bool(nan[..., 32:64].all()) and not bool(nan[..., :32].any()) and not bool(nan[..., 64:].any())
