@@ -23,9 +23,13 @@
 // 8 rows of 128 values take 32 registers.  The operands q', its group sums,
 // p sc and p are fp16: in MODE 0 (fp32 and fp16 calls, 8 rows) as two parts of
 // 11 bits each -- q' = hi + lo 2^-11 in rows 0..7 and 8..15 of one instruction,
-// p as hi + lo in two, p sc brought near 1 by a power of two first -- in MODE 1
-// (16 rows) and MODE 2 (8 rows) one part, for bf16 calls: q is exact there, and
-// p and p sc rounded to 11 bits are 8 times finer than the output's 8.  Products
+// p and p sc as hi + lo in two -- in MODE 1 (16 rows) and MODE 2 (8 rows) one part,
+// for bf16 calls: q is exact there (down to 2^-13 of the row's largest element),
+// and p and p sc rounded to 11 bits are 8 times finer than the output's 8.  p is
+// carried as p 2^15 and p sc as p sc 2^(15 + x) with x by the largest scale so
+// far, so that both end just below fp16's largest number: a p of 2^-29 of the
+// row's largest then still has 11 bits (in units of 1 all of the keys beside one
+// that dominates its row were lost: 1e-2 of the result).  Products
 // accumulate in fp32, in MODE 0 for kFewFlush tiles before they are added to
 // shared memory rounded to nearest (the truncation of many steps is a drift,
 // not a scatter).
@@ -161,13 +165,14 @@ __device__ __forceinline__ void load_q8(const AttnArgs& a, int64_t at, float (&x
 struct FewRow {
   float f;          // log2 units per unit of the scaled product
   int lo, hi;       // keys it sees
-  float m, mu, l;   // running maximum (log2 units), the same (or 0) plus E, sum
+  float m, mu, l;   // running maximum (log2 units), the same (or 0) less 15, sum of p 2^15
 };
 
 template <int D, int MODE>
 struct FewWarp {
   using L = KvTile<D>;
   static constexpr int G = L::G, NR = MODE == 1 ? 2 : 1;
+  static constexpr float kUp = 15.f, kDown = 3.0517578125e-5f;   // 2^-15
   uint32_t aq[G][2][MODE == 2 ? 2 : 4];   // query operands: step, (a0, a2) or a0..a3
   uint32_t am[MODE == 2 ? 1 : 2];         // group sums
   FewRow row[NR];
@@ -175,8 +180,8 @@ struct FewWarp {
   // and 2, 3) of rows 2 q, 2 q + 1 (and 8 more for the second NR); om: sums of
   // the middles of group lane / 4 (hi parts; lane / 4 - 4: lo parts)
   float o[NR][G][2][4], om[NR][4];
-  float unit;       // 2^E, E <= 0: the operands and all sums are of p 2^-E
-  uint32_t limit;   // largest scale that the unit covers, twice (fp16)
+  float unit;       // 2^(-15 - x): om and l are of p 2^15, o of p sc 2^(15 + x)
+  uint32_t limit;   // largest scale that x covers, twice (fp16)
   float fm;         // row[0].m when the sums last went to shared memory (MODE 0)
 
   // Row r of the row tile (lane / 4, and lane / 4 + 8 in MODE 1)
@@ -213,7 +218,7 @@ struct FewWarp {
                     __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
     kv_token_keys(w.T, w.n, t, a.p.causal, a.p.window, s.lo, s.hi);
     s.m = -INFINITY;
-    s.mu = -14.f;   // (E of the first unit)
+    s.mu = -kUp;
     s.l = 0.f;
     float sum[G];
 #pragma unroll
@@ -257,9 +262,28 @@ struct FewWarp {
 #pragma unroll
     for (int i = 0; i < NR; ++i) load_row(a, w, q0, rt_rows, i, lane);
     clear();
-    unit = 6.103515625e-5f;   // 2^-14
-    limit = 0x07FF07FFu;
+    unit = kDown;
+    limit = 0;
+    follow(0);
     fm = -INFINITY;
+  }
+  // x for scales up to `top` (fp16 bits): p sc 2^(15 + x) below 2^15, and above 2^14 for the largest.
+  // With one part x = 0 does where that is above 2^9 (scales from 2^-6 to 1, as a rule): the floor of
+  // fp16 then lies at 2^-34 of the row's largest p.
+  __device__ __forceinline__ void follow(uint32_t top) {
+    top = min(top, 0x7BFFu);
+    const int bit = 31 - __clz(top | 1u);
+    int e = top < 0x400u ? bit - 24 : (int)(top >> 10) - 15;   // top in [2^e, 2^(e + 1))
+    uint32_t most = top < 0x400u ? (2u << bit) - 1u : top | 0x3FFu;
+    if constexpr (MODE != 0) {
+      if (e >= -6 && e < 0) {
+        e = -1;
+        most = 0x3BFFu;
+      }
+      e = e < -16 ? -16 : e;   // (2^x is an fp16)
+    }
+    unit = __uint_as_float((uint32_t)(127 - 15 + 1 + e) << 23);   // x = -1 - e
+    limit = most * 0x10001u;
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -372,27 +396,25 @@ struct FewWarp {
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) big = max_h2(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
       big = max_h2(big, limit);
-      const uint32_t e = min(max(big & 0x7FFFu, big >> 16) >> 10, 15u);   // (beyond, p sc stays in range as it is)
-      limit = e == 15 ? 0x7BFF7BFFu : (e << 10 | 0x3FFu) * 0x10001u;
       const float before = unit;
-      unit = fmaxf(unit, __uint_as_float((e + 112) << 23));
+      follow(max(big & 0x7FFFu, big >> 16));
       const float down = before * __uint_as_float(0x7F000000u - __float_as_uint(unit));
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
-        al[j] *= down;
         row[j].l *= al[j];
-        // (E log2 units more: p 2^-E comes out of the exponential)
-        row[j].mu = (row[j].m == -INFINITY ? 0.f : row[j].m) + (float)((int)(__float_as_uint(unit) >> 23) - 127);
+        // (p 2^15 comes out of the exponential)
+        row[j].mu = (row[j].m == -INFINITY ? 0.f : row[j].m) - kUp;
         // to the lanes that hold the rows' sums
         const float a0 = __shfl_sync(0xFFFFFFFFu, al[j], 8 * q), a1 = __shfl_sync(0xFFFFFFFFu, al[j], 8 * q + 4);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float x = u % 2 ? a1 : a0;
           om[j][u] *= x;
+          const float y = x * down;
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            o[j][g][0][u] *= x;
-            o[j][g][1][u] *= x;
+            o[j][g][0][u] *= y;
+            o[j][g][1][u] *= y;
           }
         }
       }
@@ -400,7 +422,7 @@ struct FewWarp {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const uint32_t at = s + (uint32_t)(i * L::kBytes);
-      float2 p[NR][2];        // p 2^-E
+      float2 p[NR][2];        // p 2^15
       uint32_t ph[NR][2];     // the same in fp16
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
@@ -460,6 +482,28 @@ struct FewWarp {
       lds_words<G>(at + L::kValScale + (uint32_t)((q + 4) * G) * 4, s1);
       lds_words<G>(at + L::kValCodes + (uint32_t)((q * 8 + r) * G) * 4, v0);
       lds_words<G>(at + L::kValCodes + (uint32_t)(((q + 4) * 8 + r) * G) * 4, v1);
+      if (MODE == 0 || unit != kDown) {   // p 2^(15 + x)
+        const float by = __uint_as_float(0x77800000u - __float_as_uint(unit));   // 2^x
+        if constexpr (MODE == 0) {
+          p[0][0] = mul2(p[0][0], make_float2(by, by));
+          p[0][1] = mul2(p[0][1], make_float2(by, by));
+        } else {
+          const uint32_t by2 = h2bits(__float2half2_rn(by));
+          if (by < 1.f) {
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+              ph[j][0] = mul_h2(ph[j][0], by2);
+              ph[j][1] = mul_h2(ph[j][1], by2);
+            }
+          } else {   // (p has no room: the scales, exactly)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              s0[g] = mul_h2(s0[g], by2);
+              s1[g] = mul_h2(s1[g], by2);
+            }
+          }
+        }
+      }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         if constexpr (EDGE) {   // what lies past the end may be anything
@@ -517,7 +561,7 @@ struct FewWarp {
     float mn = __shfl_sync(0xFFFFFFFFu, om[which][e], 4 * g + lane % 4);
     if constexpr (MODE == 0)
       mn = fmaf(__shfl_sync(0xFFFFFFFFu, om[which][e], 16 + 4 * g + lane % 4), 4.8828125e-4f, mn);
-    mn *= unit;
+    mn *= kDown;
     const float up = 1024.f * unit;
     return make_float4(fmaf(o[which][g][0][e], up, mn), fmaf(o[which][g][0][2 + e], up, mn),
                        fmaf(o[which][g][1][e], up, mn), fmaf(o[which][g][1][2 + e], up, mn));
@@ -733,7 +777,7 @@ __global__ void __launch_bounds__(Few<D, MODE>::kThreads, Few<D, MODE>::kPerSm) 
     for (int i = 0; i < RT / J; ++i) {
       const int which = i * J / 8;
       if (i * J % 8 == 0) {
-        float l = f.row[which].l * f.unit;
+        float l = f.row[which].l * f.kDown;
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
         if (lane % 4 == 0) {

@@ -36,20 +36,27 @@ def bound(typ, top, many):
 
 
 class Given(Setup):
-    """Sequences of the given keys and values [n, kv_heads, dim] and queries [tokens, q_heads, dim]."""
+    """Sequences of the given keys and values [n, kv_heads, dim] and queries [tokens, q_heads, dim]; the
+    very array of the sequence before: the same pages."""
 
     def __init__(self, k, v, q, page, typ, seed=0):
         kv_heads, dim = k[0].shape[1:]
         rng = np.random.default_rng(seed)
         self.args = (q[0].shape[1], kv_heads, dim, page)
         self.q_len, self.kv_len, self.typ = [len(x) for x in q], [len(x) for x in k], typ
-        used = [-(-n // page) for n in self.kv_len]
+        same = [b > 0 and k[b] is k[b - 1] for b in range(len(k))]
+        used = [0 if same[b] else -(-n // page) for b, n in enumerate(self.kv_len)]
         self.cache = lw.KvCache(torch.randint(0, 256, (sum(used) * lw.lw_kv_page_bytes(kv_heads, dim, page),),
                                               dtype=torch.uint8, device=DEV), kv_heads, dim, page)
         order, at = rng.permutation(sum(used)).astype(np.int32), 0
         table = np.full((len(k), max(used)), -1, np.int32)
         self.k, self.v, self.st = [], [], status()
         for b, n in enumerate(self.kv_len):
+            if same[b]:
+                table[b] = table[b - 1]
+                self.k.append(self.k[-1])
+                self.v.append(self.v[-1])
+                continue
             table[b, :used[b]] = order[at:at + used[b]]
             at += used[b]
             pos = np.arange(n)
@@ -66,30 +73,30 @@ class Given(Setup):
     def expect(self, causal=True, window=0):
         """out (NaN where a NaN of a seen key's value or of its score goes), lse, the largest |score|."""
         q_heads, kv_heads, dim, _ = self.args
-        q = self.q.double().cpu().numpy()
-        out, lse, at, top = np.zeros(q.shape), np.full(q.shape[:2], -np.inf), 0, 0.0
+        q = self.q.double()
+        out, lse, at, top = torch.zeros_like(q), torch.zeros(q.shape[:2], dtype=torch.float64, device=DEV), 0, 0.0
         for b, (t, n) in enumerate(zip(self.q_len, self.kv_len)):
-            pos, j = np.arange(n - t, n)[:, None], np.arange(n)[None]
-            see = np.ones((t, n), bool)
+            if not b or self.k[b] is not self.k[b - 1]:
+                keys, values = torch.from_numpy(self.k[b]).to(DEV), torch.from_numpy(self.v[b]).to(DEV)
+            pos, j = torch.arange(n - t, n, device=DEV)[:, None], torch.arange(n, device=DEV)[None]
+            see = torch.ones(t, n, dtype=torch.bool, device=DEV)
             if causal:
                 see &= j <= pos
             if window:
                 see &= j > pos - window
             for h in range(q_heads):
-                kh = h // (q_heads // kv_heads)
-                k, v = self.k[b][:, kh], self.v[b][:, kh]
-                s = np.where(see, dim ** -0.5 * (q[at:at + t, h] @ np.nan_to_num(k).T), -np.inf)
-                top = max(top, np.abs(s[see]).max(initial=0))
-                m = s.max(-1, keepdims=True)
-                p = np.exp(s - m)
-                l = p.sum(-1, keepdims=True)
-                o, e = p @ np.nan_to_num(v) / l, (m + np.log(l))[:, 0]
-                o[(see.astype(np.float64) @ np.isnan(v)) > 0] = np.nan
-                lost = see[:, np.isnan(k).any(-1)].any(-1)
+                k, v = keys[:, h // (q_heads // kv_heads)], values[:, h // (q_heads // kv_heads)]
+                s = dim ** -0.5 * (q[at:at + t, h] @ k.nan_to_num(0.0).T)
+                top = max(top, float(s[see].abs().max()))
+                s = torch.where(see, s, -np.inf)
+                e = s.logsumexp(-1)
+                o = (s - e[:, None]).exp() @ v.nan_to_num(0.0)
+                o[(see.double() @ v.isnan().double()) > 0] = np.nan
+                lost = see[:, k.isnan().any(-1)].any(-1)
                 o[lost], e[lost] = np.nan, np.nan
                 out[at:at + t, h], lse[at:at + t, h] = o, e
             at += t
-        return out, lse, top
+        return out.cpu().numpy(), lse.cpu().numpy(), top
 
     def check(self, causal=True, window=0, many=False, group=None, **kw):
         got, lse = self.run(causal=causal, window=window, **kw)
@@ -134,3 +141,59 @@ def test_scales_that_rise_after_a_nan(typ, tokens):
     got = s.check(group=32)
     nan = torch.isnan(got)
     assert bool(nan[..., 32:64].all()) and not bool(nan[..., :32].any()) and not bool(nan[..., 64:].any())
+
+
+# ---- small probabilities --------------------------------------------------------
+
+def sinks(rng, n, heads, dim, at, score):
+    """Keys [n, heads, dim] of which those at `at` score `score` (natural units) for queries near
+    half the returned direction, and values, large ones, that are 0 at those keys."""
+    unit = np.where(rng.standard_normal(dim) > 0, 1.0, -1.0)
+    k = rng.standard_normal((n, heads, dim))
+    v = 1000 * rng.standard_normal((n, heads, dim))
+    k[at] = score / (dim ** -0.5 * 0.5 * dim) * unit
+    v[at] = 0
+    return k, v, unit
+
+
+def near(rng, unit, tokens, q_heads):
+    return 0.5 * unit + 0.02 * rng.standard_normal((tokens, q_heads, len(unit)))
+
+
+@pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("tokens,q_heads", [(1, 4), (3, 8)])
+def test_rows_that_a_few_keys_dominate(typ, dim, tokens, q_heads):
+    """A key of every 16 takes nearly all of a row and its value is 0: what the others bring is all of
+    the result, each at a millionth of the largest probability."""
+    rng = np.random.default_rng(42)
+    k, v, unit = sinks(rng, 4097, 2, dim, np.s_[3::16], 14.0)
+    s = Given([k], [v], [near(rng, unit, tokens, q_heads)], 64, typ)
+    s.check(many=tokens * q_heads // 2 > 24)
+
+
+@pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("weight", [0.9, 0.99])
+@pytest.mark.parametrize("tokens,batch,n", [(1, 38, 4097), (1, 38, 32768)])
+def test_rows_that_one_key_dominates(typ, weight, tokens, batch, n):
+    """The first keys (one for every warp that may share an item) have `weight` of each row between
+    them and values of 0, under enough sequences that an item is not cut; the sequences share pages."""
+    rng = np.random.default_rng(43)
+    score = np.log(n * weight / (1 - weight) / 8)
+    k, v, unit = sinks(rng, n, 8, 128, np.arange(8) * 16 + 5, score)
+    q = [near(rng, unit, tokens, 16) for _ in range(batch)]
+    s = Given([k] * batch, [v] * batch, q, 64, typ)
+    s.check(many=tokens > 1)
+
+
+@pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("tokens,q_heads", [(1, 4), (3, 8), (40, 4)])
+def test_value_groups_of_very_different_scales(typ, tokens, q_heads):
+    """Groups of a head at 3000, 1 and 0.02: each is as near as if it were alone."""
+    rng = np.random.default_rng(44)
+    n, dim = 1000, 128
+    k, v = rng.standard_normal((n, 2, dim)), rng.standard_normal((n, 2, dim))
+    v[..., :32] *= 3000
+    v[..., 64:96] *= 0.02
+    s = Given([k], [v], [0.3 * rng.standard_normal((tokens, q_heads, dim))], 16, typ)
+    s.check(many=tokens * q_heads // 2 > 24, group=32)
