@@ -25,6 +25,8 @@
 // 11 bits each -- q' = hi + lo 2^-11 in rows 0..7 and 8..15 of one instruction,
 // p and p sc as hi + lo in two -- in MODE 1 (16 rows) and MODE 2 (8 rows) one part,
 // for bf16 calls: q is exact there (down to 2^-13 of the row's largest element),
+// its group sums are in two parts (the lower ones in the instruction's other 8 places,
+// against the same minimums: one part moved a score by 2e-3 where minimums are large),
 // and p and p sc rounded to 11 bits are 8 times finer than the output's 8.  p is
 // carried as p 2^15 and p sc as p sc 2^(15 + x) with x by the largest scale so
 // far, so that both end just below fp16's largest number: a p of 2^-29 of the
@@ -174,7 +176,7 @@ struct FewWarp {
   static constexpr int G = L::G, NR = MODE == 1 ? 2 : 1;
   static constexpr float kUp = 15.f, kDown = 3.0517578125e-5f;   // 2^-15
   uint32_t aq[G][2][MODE == 2 ? 2 : 4];   // query operands: step, (a0, a2) or a0..a3
-  uint32_t am[MODE == 2 ? 1 : 2];         // group sums
+  uint32_t am[2];   // group sums, two parts (MODE 1: [part][row] in shared memory, registers are short)
   FewRow row[NR];
   // value sums: [g][s]: elements 32 g + 4 (lane / 4) + 2 s, + 1 (registers 0, 1
   // and 2, 3) of rows 2 q, 2 q + 1 (and 8 more for the second NR); om: sums of
@@ -185,7 +187,8 @@ struct FewWarp {
   float fm;         // row[0].m when the sums last went to shared memory (MODE 0)
 
   // Row r of the row tile (lane / 4, and lane / 4 + 8 in MODE 1)
-  __device__ void load_row(const AttnArgs& a, const KvWalk& w, int q0, int rt_rows, int which, int lane) {
+  __device__ void load_row(const AttnArgs& a, const KvWalk& w, int q0, int rt_rows, int which, int lane,
+                           uint32_t* sums) {
     const int q = lane % 4, r = w.rt * rt_rows + lane / 4 + 8 * which;
     float x[G][8], top = 0.f;
     const bool live = r < w.T * a.group;
@@ -255,12 +258,14 @@ struct FewWarp {
       if (g == 2 * q + 1) s1 = sum[g];
     }
     if constexpr (MODE == 0) split2<2048>(s0, s1, am[0], am[1]);
-    else am[which] = h2bits(__floats2half2_rn(s0, s1));
+    else if constexpr (MODE == 1) split2<1>(s0, s1, sums[4 * lane + which], sums[4 * lane + 2 + which]);
+    else split2<1>(s0, s1, am[0], am[1]);
   }
 
-  __device__ void start(const AttnArgs& a, const KvWalk& w, int q0, int rt_rows, int lane) {
+  // sums: MODE 1: 512 bytes of shared memory, the warp's until its first put
+  __device__ void start(const AttnArgs& a, const KvWalk& w, int q0, int rt_rows, int lane, uint32_t* sums) {
 #pragma unroll
-    for (int i = 0; i < NR; ++i) load_row(a, w, q0, rt_rows, i, lane);
+    for (int i = 0; i < NR; ++i) load_row(a, w, q0, rt_rows, i, lane, sums);
     clear();
     unit = kDown;
     limit = 0;
@@ -300,8 +305,10 @@ struct FewWarp {
   // NT tiles of 16 keys, keys kb .. kb + 16 NT - 1.  EDGE: some row does not see
   // some of them (those may hold any bits).
   template <bool EDGE, int NT>
-  __device__ __forceinline__ void tiles(uint32_t s, int kb, int n, int lane) {
+  __device__ __forceinline__ void tiles(uint32_t s, int kb, int n, int lane, uint32_t sums) {
     const int q = lane % 4, r = lane / 4;
+    uint4 m4;
+    if constexpr (MODE == 1) m4 = lds_u4(sums + 16 * lane);
     float2 t[NT][NR][2];   // scores: keys 2 q, 2 q + 1 of the tile, and 8 more
     uint32_t see[NT][NR];
 #pragma unroll
@@ -313,7 +320,9 @@ struct FewWarp {
         uint32_t mn = 0;
         if (2 * q < L::GP) mn = lds_u32(at + L::kKeyMin + (uint32_t)((8 * h + r) * L::GP + 2 * q) * 2);
         if (G % 2 && q == G / 2) mn &= 0xFFFFu;
-        mma_f16_zero(c, am[0], MODE == 2 ? 0u : am[MODE == 2 ? 0 : 1], 0u, 0u, mn, 0u);
+        if constexpr (MODE == 0) mma_f16_zero(c, am[0], am[1], 0u, 0u, mn, 0u);
+        else if constexpr (MODE == 1) mma_f16_zero(c, m4.x, m4.y, m4.z, m4.w, mn, mn);
+        else mma_f16_zero(c, am[0], 0u, am[1], 0u, mn, mn);
         constexpr float kUnit = MODE == 0 ? 9.765625e-4f : 5.9604644775390625e-8f;   // as the codes' products
         float2 x = mul2(make_float2(c[0], c[1]), make_float2(kUnit, kUnit));
         float2 y = mul2(make_float2(c[2], c[3]), make_float2(kUnit, kUnit));
@@ -730,7 +739,7 @@ __global__ void __launch_bounds__(Few<D, MODE>::kThreads, Few<D, MODE>::kPerSm) 
       s_q0[cur ^ 1] = q0;
     }
     __syncwarp();
-    f.start(a, w, s_q0[cur], RT, lane);
+    f.start(a, w, s_q0[cur], RT, lane, reinterpret_cast<uint32_t*>(mine));
     // keys that every row of the item sees
     int all_lo, all_hi, x;
     {
@@ -756,11 +765,11 @@ __global__ void __launch_bounds__(Few<D, MODE>::kThreads, Few<D, MODE>::kPerSm) 
         const uint32_t at = smem_addr(t.ring) + F::kPair * t.out * L::kBytes;
         const int kb = tile * LW_KV_TILE;
         if (some == (1u << F::kPair) - 1 && kb >= all_lo && kb + F::kPair * LW_KV_TILE <= all_hi) {
-          f.template tiles<false, F::kPair>(at, kb, w.n, lane);
+          f.template tiles<false, F::kPair>(at, kb, w.n, lane, smem_addr(mine));
         } else {
 #pragma unroll 1
           for (int i = 0; i < F::kPair; ++i)
-            if (some >> i & 1u) f.template tiles<true, 1>(at + i * L::kBytes, kb + i * LW_KV_TILE, w.n, lane);
+            if (some >> i & 1u) f.template tiles<true, 1>(at + i * L::kBytes, kb + i * LW_KV_TILE, w.n, lane, smem_addr(mine));
         }
         held += F::kPair;
         fence_proxy_async();   // (this lane's reads before the copy that takes the place next, also the next item's)
