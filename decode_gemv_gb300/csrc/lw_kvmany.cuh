@@ -11,9 +11,10 @@
 //    buffers), once for both row tiles;
 //  * 8 row warps, one thread per row: put Q into shared memory (each row scaled
 //    by a power of two: the fp16 range), then for every 64 keys read the row of
-//    S, take p = 2^(s - m), store it as fp16 over S, and add the row's sum.  m
-//    is raised, and O rescaled, only where a score passes it by 2^8 (p stays
-//    below 2^8, in fp16 range and precision);
+//    S, take p = 2^(s - m), store p 2^11 as fp16 over S, and add the row's sum.  m
+//    is raised, and O rescaled, only where a score passes it by 2^4: p 2^11 stays
+//    within 2^15, below fp16's largest number, and a p of 2^-25 still has 11 bits
+//    (in units of 1 all of the keys beside one that dominates its row were lost);
 //  * 2 warps issue the products, one per row tile: the queue of products is
 //    short (an issue takes as long as the product before it), so that while one
 //    waits for its rows the other keeps the tensor cores at work.  All lanes
@@ -96,6 +97,8 @@ struct Many {
   __host__ __device__ static constexpr uint32_t s_col(int x, int i) { return 128 * x + 64 * i; }
   __host__ __device__ static constexpr uint32_t o_col(int x) { return 256 + D * x; }
   static constexpr uint32_t kCols = 512;
+  // log2 units: p is carried as p 2^kUp, and m raised where a score passes it by kSlack
+  static constexpr float kUp = 11.f, kSlack = 4.f;
 };
 
 namespace dev {
@@ -732,7 +735,7 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
         kv_token_keys(v.T, v.n, r0 / a.group, a.p.causal, a.p.window, u0, all_hi);
         kv_token_keys(v.T, v.n, t1, a.p.causal, a.p.window, all_lo, u0);
       }
-      float m = -INFINITY, mu = 0.f, l = 0.f;
+      float m = -INFINITY, mu = -F::kUp, l = 0.f;   // the maximum, the same (or 0) less kUp, sum of p 2^kUp
       for (int k = v.k0; k < v.k1; ++k, ++it) {
         const int kb = (v.span.lo + k * kManyUnit) * LW_KV_TILE;
         const int b = it & 1;
@@ -773,7 +776,7 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
           if (!WIDE) top = fmaxf(top, __uint_as_float(s1[j]));
         }
         top *= f;
-        bool raise = __any_sync(0xFFFFFFFFu, top > m + 8.f);
+        bool raise = __any_sync(0xFFFFFFFFu, top > m + F::kSlack);
         if constexpr (WIDE) {   // Both halves or none, also of an end: a wait that ran out counts 32, a raise 1.
           // (And both have read S, so that P may go over it.)
           const uint32_t say = pair_count(quarter, !ok || (raise && lane == 0));
@@ -792,6 +795,7 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
           const float mx = fmaxf(m, top);
           mu = mx == -INFINITY ? 0.f : mx;
           const float al = ex2(m - mu);
+          mu -= F::kUp;
           m = mx;
           l *= al;
           if (k > v.k0) {   // once the sum over the keys before is complete
@@ -907,10 +911,10 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
       }
       tc_fence_before();
       if (whole) {
-        give_lse(m, l);
+        give_lse(m - F::kUp, l);
       } else {
         if (hf == 0) {
-          part[row] = m;
+          part[row] = m - F::kUp;   // (the parts' sums are relative to this)
           part[kManyTile + row] = l;
         }
         const int c0 = kv_owner(v.first, U, Gc), parts = kv_owner(v.first + v.units - 1, U, Gc) - c0 + 1;

@@ -164,7 +164,7 @@ def near(rng, unit, tokens, q_heads):
 
 @pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
 @pytest.mark.parametrize("dim", [64, 96, 128])
-@pytest.mark.parametrize("tokens,q_heads", [(1, 4), (3, 8)])
+@pytest.mark.parametrize("tokens,q_heads", [(1, 4), (3, 8), (40, 4)])
 def test_rows_that_a_few_keys_dominate(typ, dim, tokens, q_heads):
     """A key of every 16 takes nearly all of a row and its value is 0: what the others bring is all of
     the result, each at a millionth of the largest probability."""
@@ -176,7 +176,7 @@ def test_rows_that_a_few_keys_dominate(typ, dim, tokens, q_heads):
 
 @pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
 @pytest.mark.parametrize("weight", [0.9, 0.99])
-@pytest.mark.parametrize("tokens,batch,n", [(1, 38, 4097), (1, 38, 32768)])
+@pytest.mark.parametrize("tokens,batch,n", [(1, 38, 4097), (1, 38, 32768), (30, 19, 8192)])
 def test_rows_that_one_key_dominates(typ, weight, tokens, batch, n):
     """The first keys (one for every warp that may share an item) have `weight` of each row between
     them and values of 0, under enough sequences that an item is not cut; the sequences share pages."""
