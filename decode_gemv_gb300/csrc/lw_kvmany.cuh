@@ -338,6 +338,24 @@ struct ManyRaw {
   }
 };
 
+// Groups (a bit each) with a NaN under one of a unit's keys from kb on that a row of
+// keys [lo, hi) sees; keys: [tile][group], a bit a key.  Rare, and kept out of the
+// row warps' loop, whose registers are short.
+template <int G>
+__device__ __noinline__ uint8_t many_nan_groups(const volatile uint16_t* keys, uint32_t tiles, int kb, int lo, int hi) {
+  uint32_t groups = 0;
+#pragma unroll 1
+  for (int i = 0; i < 4 * kManyUnit; ++i) {
+    const int key = kb + i / 4 * LW_KV_TILE;
+    if (i % 4 >= G || !(tiles >> (8 * (i / 4)) & 2u)) continue;
+    uint32_t bits = keys[i];
+    bits &= lo <= key ? 0xFFFFu : lo >= key + 16 ? 0u : 0xFFFFu << (lo - key);
+    bits &= hi >= key + 16 ? 0xFFFFu : hi <= key ? 0u : (1u << (hi - key)) - 1u;
+    if (bits) groups |= 1u << (i % 4);
+  }
+  return (uint8_t)groups;
+}
+
 // Barriers of a CTA.  Those of a row tile are one per S buffer, so that the use
 // before the one waited for is always complete (a parity names one of two).
 struct ManyBars {
@@ -362,9 +380,14 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
   static_assert(sizeof(ManyBars) <= 512, "barriers");
   volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + 512);   // [0] abort, [1], [2] last part of a tile's item
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + 528);   // tensor memory
-  // [unit % 4][tile]: the tile's keys are there (written before kv_full, read
-  // after s_full; four units on, the rows have answered)
+  // [unit % 4][tile]: 1: the tile's keys are there, 2: some of them have a NaN in a value group that
+  // is masked here (written before kv_full, read after s_full; four units on, the rows have answered)
   volatile uint8_t* present = smem + 544;
+  // [unit % 4][tile][group]: those keys, a bit each.  A row that does not see such a key must not get
+  // its NaN by way of V (0 x NaN), so V has zeros there and the rows that do see it set the group's
+  // outputs at the end.
+  volatile uint16_t* nan_keys = reinterpret_cast<volatile uint16_t*>(smem + 576);
+  volatile uint8_t* nan_row = smem + 704 + threadIdx.x;   // a row thread's groups with a NaN under a key that it sees
   float* xch = reinterpret_cast<float*>(smem + 1024);   // WIDE: [2][rows], [rows] 2^e of Q, [2][rows] sums
   constexpr int kIssuer = F::kRowWarps + kLoaders;      // the first of the two
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -457,40 +480,7 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
           t.out = t.out + 1 == kStages ? 0 : t.out + 1;
           t.send(a, lane);
         }
-        if (there) {
-          if (edge) {
-            // rows that do not see a key must not get its NaN through V (0 x NaN): let it come by S
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int tk = 8 * i + lane / 4;
-              // (a lane with the value scales of the key's pair: half tk / 8 of the warp, either group half)
-              bool nan = false;
-              const uint32_t odd = tk & 1 ? 16 : 0;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int g = 0; g < GW; ++g)
-#pragma unroll
-                  for (int u = 0; u < 2; ++u) {
-                    const uint32_t z = __shfl_sync(0xFFFFFFFFu, r.vs[j][g], 16 * i + 8 * u);
-                    nan |= tk / 2 % 4 == j && (z >> odd & 0x7FFFu) > 0x7C00u;
-                  }
-              if (nan) r.ks[i][0] = 0x7FFF7FFFu;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int key = kb + 2 * (4 * h + j);
-#pragma unroll
-              for (int i = 0; i < GW; ++i) {
-                const uint32_t z = r.vs[j][i];
-                const uint32_t keep = (key < w.n && (z & 0x7FFFu) <= 0x7C00u ? 0xFFFFu : 0u) |
-                                      (key + 1 < w.n && (z & 0x7FFF0000u) <= 0x7C000000u ? 0xFFFF0000u : 0u);
-                r.vs[j][i] &= keep;
-                r.vm[j][i] &= keep;
-              }
-            }
-          }
-        } else {   // no keys: S is masked, and V has to be finite
+        if (!there) {   // no keys: S is masked, and V has to be finite
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -519,7 +509,35 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
               if (WIDE) sts_u4(to + F::kKvBytes, lo[0], lo[1], lo[2], lo[3]);
             }
         }
-        if (lane == 0) present[it % 4 * kManyUnit + sub] = there;
+        bool nans = false;
+        if (there && edge) {
+          uint32_t bad[GW] = {}, some = 0;   // keys with a NaN scale, as bits of the tile
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = kb + 2 * (4 * h + j);
+#pragma unroll
+            for (int i = 0; i < GW; ++i) {
+              const uint32_t z = r.vs[j][i];
+              const bool n0 = (z & 0x7FFFu) > 0x7C00u, n1 = (z & 0x7FFF0000u) > 0x7C000000u;
+              const uint32_t keep = (key < w.n && !n0 ? 0xFFFFu : 0u) | (key + 1 < w.n && !n1 ? 0xFFFF0000u : 0u);
+              r.vs[j][i] &= keep;
+              r.vm[j][i] &= keep;
+              bad[i] |= ((uint32_t)(key < w.n && n0) | (uint32_t)(key + 1 < w.n && n1) << 1) << (2 * (4 * h + j));
+              some |= bad[i];
+            }
+          }
+          nans = __any_sync(0xFFFFFFFFu, some != 0);
+          if (nans) {
+#pragma unroll
+            for (int i = 0; i < GW; ++i) {   // the two halves of the warp have 8 keys each of the same groups
+              bad[i] |= __shfl_xor_sync(0xFFFFFFFFu, bad[i], 16);
+              if (lane < 16 && lane % 8 == 0 && g0 + i < G)
+                nan_keys[(it % 4 * kManyUnit + sub) * 4 + g0 + i] = (uint16_t)bad[i];
+            }
+            __syncwarp();
+          }
+        }
+        if (lane == 0) present[it % 4 * kManyUnit + sub] = nans ? 3 : there;
         if (kSplit) {
           fence_proxy_async();
           __syncwarp();
@@ -736,6 +754,7 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
         kv_token_keys(v.T, v.n, t1, a.p.causal, a.p.window, all_lo, u0);
       }
       float m = -INFINITY, mu = -F::kUp, l = 0.f;   // the maximum, the same (or 0) less kUp, sum of p 2^kUp
+      *nan_row = 0;
       for (int k = v.k0; k < v.k1; ++k, ++it) {
         const int kb = (v.span.lo + k * kManyUnit) * LW_KV_TILE;
         const int b = it & 1;
@@ -745,7 +764,10 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!WIDE && !ok) break;
         tc_fence_after();
-        const uint32_t there = *reinterpret_cast<const volatile uint32_t*>(present + it % 4 * kManyUnit) >> (16 * hf) & (WIDE ? 0xFFFFu : 0xFFFFFFFFu);
+        const uint32_t tiles = *reinterpret_cast<const volatile uint32_t*>(present + it % 4 * kManyUnit);
+        const uint32_t there = tiles >> (16 * hf) & (WIDE ? 0xFFFFu : 0xFFFFFFFFu);
+        if (tiles & 0x02020202u)   // (both halves of a row look at all of its keys)
+          *nan_row |= many_nan_groups<G>(nan_keys + it % 4 * 4 * kManyUnit, tiles, kb, y.lo, y.hi);
         uint32_t s0[32], s1[32];   // WIDE: the scores are s0 (s1 brings the lo parts' sum)
         tmem_ld32(sc, s0);
         if constexpr (!WIDE) tmem_ld32(sc + 32, s1);
@@ -899,6 +921,10 @@ __global__ void __launch_bounds__(Many<D, WIDE>::kThreads, kManyPerSm) kv_many_k
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; ++j) z[j] = fmaf(__uint_as_float(u[j]), 4.8828125e-4f, z[j]);
+        }
+        if (*nan_row >> g & 1) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(0x7FFFFFFFu);
         }
         if (whole) {
           give(g, l, z);

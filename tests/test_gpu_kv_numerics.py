@@ -219,3 +219,34 @@ def test_scores_of_large_minimums_that_cancel(typ, dim, tokens, q_heads):
     q[..., 32:64] = q[..., 31::-1]
     a = float((np.abs(q).max((0, 1)) * np.abs(k).max((0, 1))).sum()) * dim ** -0.5
     Given([k], [v], [q], 16, typ).check(magnitude=a)
+
+
+# ---- where a NaN goes -------------------------------------------------------------
+
+@pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("dim,element", [(64, 40), (96, 70), (96, 5), (128, 127)])
+@pytest.mark.parametrize("tokens,q_heads,n", [(1, 4, 300), (5, 4, 300), (70, 4, 300), (90, 8, 200), (70, 2, 5000)])
+@pytest.mark.parametrize("window", [0, 37])
+def test_a_nan_in_a_value_reaches_its_group_alone(typ, dim, element, tokens, q_heads, n, window):
+    """A value's NaN is its group's (32 elements) for the rows that see the key, whichever tile holds
+    it; the other elements, and lse, have none of it."""
+    rng = np.random.default_rng(45)
+    k, v = rng.standard_normal((n, 2, dim)), rng.standard_normal((n, 2, dim))
+    q = rng.standard_normal((tokens, q_heads, dim))
+    for key in {20, n - tokens - 1, n - tokens // 2 - 1, n - 1}:
+        x = v.copy()
+        x[key, 1, element] = np.nan
+        s = Given([k, k[:60]], [x, v[:60]], [q, q[:1]], 16, typ)
+        s.check(window=window, many=tokens * q_heads // 2 > 24)
+
+
+@pytest.mark.parametrize("typ", ["fp32", "bf16"])
+@pytest.mark.parametrize("tokens", [2, 70])
+def test_nan_in_a_key_and_in_several_values(typ, tokens):
+    """A key's NaN is the whole row's and its lse's; several values' NaN are their groups'."""
+    rng = np.random.default_rng(46)
+    n, dim = 700, 128
+    k, v = rng.standard_normal((n, 1, dim)), rng.standard_normal((n, 1, dim))
+    v[n - 40, 0, 3] = v[n - 41, 0, 70] = v[n - 1, 0, 100] = v[5, 0, 40] = np.nan
+    k[n - 2, 0, 9] = np.nan
+    Given([k], [v], [rng.standard_normal((tokens, 4, dim))], 32, typ).check(many=tokens > 10)
