@@ -240,7 +240,7 @@ extern "C" size_t lw_kv_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, i
   if (!c || !lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens) || q_heads < 1 ||
       q_heads % c->kv_heads || q_tokens < 0 || batch < 1)
     return 0;
-  return kv_attention_workspace(c);
+  return kv_attention_workspace(c, q_heads, q_tokens);
 }
 
 extern "C" lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, void* ws,

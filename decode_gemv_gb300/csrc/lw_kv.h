@@ -25,8 +25,8 @@ inline bool kv_rows_aligned(const void* p, int64_t token_stride, int64_t head_st
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && token_stride % n == 0 && head_stride % n == 0;
 }
 
-// Bytes of workspace of any attention call on a cache.
-size_t kv_attention_workspace(const lw_kv_cache* c);
+// Bytes of workspace of an attention call of q_tokens tokens in all.
+size_t kv_attention_workspace(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens);
 lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, void* ws, int32_t* status,
                               cudaStream_t st);
 

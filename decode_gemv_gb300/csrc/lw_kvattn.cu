@@ -30,11 +30,16 @@ static_assert(Few<64, 0>::kPerSm <= kMostPerSm && Few<64, 1>::kPerSm <= kMostPer
                   2 * kManyPerSm <= kMostPerSm,
               "workspace places");
 
+// Rows of a sequence on a key/value head up to which kv_few_kernel takes a call (the crossings at the rule below)
+constexpr int kFewMostBf16 = 24, kFewMost = 48;
+
 }  // namespace
 
-size_t kv_attention_workspace(const lw_kv_cache* c) {
+// A call whose tokens, were they all one sequence's, are few rows is kv_few_kernel's in every type.
+size_t kv_attention_workspace(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens) {
   const size_t few = (size_t)kMostPerSm * 2 * 16, many = (size_t)2 * 2 * kManyTile;   // rows an SM
-  return attn_counter_bytes() + (size_t)device_sm_count() * (few > many ? few : many) * (size_t)(c->head_dim + 2) * 4;
+  const bool all_few = q_tokens * (q_heads / c->kv_heads) <= kFewMostBf16;
+  return attn_counter_bytes() + (size_t)device_sm_count() * (all_few ? few : many) * (size_t)(c->head_dim + 2) * 4;
 }
 
 lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* ws, int32_t* status,
@@ -62,8 +67,9 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* w
   // One sequence of 8192 keys alone, bf16: 16 rows 20, 26 : 53, 32 rows 26, 29 : 53, 48 rows 33, 34 : 53
   // (kv_many_kernel's items start and end slowly); the lengths are not known here, so the rule is the
   // full device's.
-  const long long rows = (long long)p->max_q * a.group;
-  const int mode = p->dtype != LW_BF16 ? (rows > 48 ? 4 : 0) : (rows > 24 ? 3 : rows > 8 && rows <= 16 ? 1 : 2);
+  const long long rows = (p->max_q < p->q_tokens ? p->max_q : p->q_tokens) * a.group;
+  const int mode = p->dtype != LW_BF16 ? (rows > kFewMost ? 4 : 0)
+                                       : (rows > kFewMostBf16 ? 3 : rows > 8 && rows <= 16 ? 1 : 2);
   const Variant v = c->head_dim == 64 ? variant<64>(mode) : c->head_dim == 96 ? variant<96>(mode) : variant<128>(mode);
   if (resident_blocks(reinterpret_cast<const void*>(v.kernel), v.threads, v.smem) < 1)
     return fail(LW_ERR_CUDA, "lw_kv_attention: the kernel does not fit this device");

@@ -668,10 +668,12 @@ typedef struct {
   float scale;
 } lw_kv_attn;
 
-/* Bytes of device workspace an lw_kv_attention call needs (zeroed by the
-   caller before first use; every call leaves its counters at zero, but for one
-   that reports LW_DEV_TIMEOUT: zero it again then).  0 for an unsupported
-   shape. */
+/* Bytes of device workspace an lw_kv_attention call needs: room for the partial
+   results of the CTAs that the current device holds at once, for few rows where
+   q_tokens * q_heads / kv_heads <= 24, and else for many.  What q_tokens asks for
+   is enough for fewer as well, whatever the batch.  Zeroed by the caller before
+   first use; every call leaves its counters at zero, but for one that reports
+   LW_DEV_TIMEOUT: zero it again then.  0 for an unsupported shape. */
 size_t lw_kv_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens,
                              int32_t batch);
 

@@ -56,3 +56,17 @@ def test_arguments_written_just_before_the_call(typ, q_len):
         g.launch()
         torch.cuda.synchronize()
         assert int(s.st) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("typ", ["fp32", "bf16"])
+@pytest.mark.parametrize("hint", [1, 3, 1000])
+def test_a_small_calls_workspace_is_enough(typ, hint):
+    """Few rows in all, whatever max_q says: right on the workspace asked for, and nothing behind it is
+    written."""
+    s = Setup(33, [2, 0, 3, 1], [3000, 5, 700, 0], 8, 2, 128, 16, typ)
+    need = lw.lw_kv_workspace_bytes(s.cache, 8, 6, 4)
+    assert need < lw.lw_kv_workspace_bytes(s.cache, 8, 7, 4)
+    room = torch.full((need + (1 << 20),), 0x5A, dtype=torch.uint8, device=DEV)
+    room[:need] = 0
+    s.check(max_q=hint, ws=room[:need])
+    assert bool((room[need:] == 0x5A).all())

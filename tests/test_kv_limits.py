@@ -38,6 +38,19 @@ def test_the_largest_sizes_are_taken():
         assert b"workspace" in lw.load().lw_last_error()
 
 
+@pytest.mark.parametrize("dim", [64, 96, 128])
+def test_the_workspace_is_the_calls(dim):
+    """A call of few rows in all asks for an eighth of what many rows do; more tokens, whatever the
+    batch, never ask for less."""
+    cache = lw.KvCache.empty(3, 2, dim, 16, device="cpu")
+    sizes = [lw.lw_kv_workspace_bytes(cache, 8, t, 1) for t in (0, 1, 6, 7, 100, 1 << 20)]
+    assert sizes == sorted(sizes) and sizes[2] * 7 < sizes[3]
+    assert [lw.lw_kv_workspace_bytes(cache, 8, t, 50) for t in (0, 1, 6, 7, 100, 1 << 20)] == sizes
+    # what it cuts off is read by no call: the C call asks for the same
+    need = lw.lw_kv_workspace_bytes(lw.KvCache.empty(10, 1, 64, 16, device="cpu"), 1, 3, 2)
+    assert c_attention(ws_bytes=need - 1) == lw.LW_ERR_INVALID_ARG
+
+
 # ---- the binding ------------------------------------------------------------
 
 class OnDevice1(torch.Tensor):
