@@ -50,8 +50,9 @@
 // instructions' results, 4 warps a scheduler).  8 sequences of 65536 keys, 8 heads
 // of 128 with 4 query heads each: bf16 156 us (0.67 GB of cache, 4.3 TB/s), fp32
 // 208 us.  Bound by latency where they are few: 37 keys 7.5 us, 4097 keys of one
-// sequence 15 us (a launch, the search of the range, some tiles a warp, the join of
-// 19 parts a head: each a chain of loads).
+// sequence 15 us (a launch, the search of the range, a tile a warp, the join of up to
+// 32 parts a head: each a chain of loads; 8 heads of weight 39 on 304 CTAs leave some
+// 50 CTAs an item's front alone, without a unit).
 #pragma once
 
 #include "lw_kvattn.cuh"
