@@ -250,3 +250,26 @@ def test_nan_in_a_key_and_in_several_values(typ, tokens):
     v[n - 40, 0, 3] = v[n - 41, 0, 70] = v[n - 1, 0, 100] = v[5, 0, 40] = np.nan
     k[n - 2, 0, 9] = np.nan
     Given([k], [v], [rng.standard_normal((tokens, 4, dim))], 32, typ).check(many=tokens > 10)
+
+
+# ---- how many bits bf16 calls have --------------------------------------------------
+
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("tokens,q_heads", [(1, 8), (2, 16), (3, 16), (40, 8)])
+def test_bf16_operands_hold_their_bits(dim, tokens, q_heads):
+    """Before the output's rounding a bf16 call is within 2^-11 (p and p sc to 11 bits each, 2^-12 at
+    most), with many rows 3 2^-12 and the scores' 2^-12 S_rms.  The rounding's own error r is known from
+    the exact result; independent errors add as squares (2 % for chance): two bits fewer in an operand
+    would show."""
+    rng = np.random.default_rng(48)
+    n, many = 3000, tokens * q_heads // 2 > 24
+    k, v = rng.standard_normal((n, 2, dim)), rng.standard_normal((n, 2, dim))
+    s = Given([k] * 4, [v] * 4, [rng.standard_normal((tokens, q_heads, dim)) for _ in range(4)], 64, "bf16")
+    got, _ = s.run()
+    torch.cuda.synchronize()
+    want = s.expect()[0]
+    norm = np.linalg.norm(want)
+    err = np.linalg.norm(got.double().cpu().numpy() - want) / norm
+    r = np.linalg.norm(torch.from_numpy(want).to(torch.bfloat16).double().numpy() - want) / norm
+    own = 4 * 2.0 ** -12 if many else 2.0 ** -11   # (S_rms is 1 here)
+    assert err <= 1.02 * np.hypot(r, own), f"{err:.3e}, rounding alone {r:.3e}"
