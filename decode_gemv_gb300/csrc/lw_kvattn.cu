@@ -31,7 +31,7 @@ static_assert(Few<64, 0>::kPerSm <= kMostPerSm && Few<64, 1>::kPerSm <= kMostPer
               "workspace places");
 
 // Rows of a sequence on a key/value head up to which kv_few_kernel takes a call (the crossings at the rule below)
-constexpr int kFewMostBf16 = 24, kFewMost = 48;
+constexpr int kFewMostBf16 = 24, kFewMost = 32;
 
 }  // namespace
 
@@ -59,14 +59,16 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* w
   a.status = status;
   // The variant, by the rows of a sequence on a key/value head.  us, kv_few_kernel (items of 8 rows, or
   // of 16) against kv_many_kernel, at 8 sequences of 32768 keys | 64 of 512, 8 heads of 128:
-  //   bf16  8 rows    89, 140 : 219 |  27,  40 : 75      fp32  16 rows  212 : 673 |  53 : 143
-  //        12 rows   159, 145 : 218 |  48,  41 : 75            32 rows  404 : 674 |  90 : 145
-  //        16 rows   160, 147 : 218 |  49,  42 : 75            48 rows  596 : 675 | 136 : 146
-  //        24 rows   230, 258 : 219 |  68,  80 : 75
-  //        32 rows   301, 263 : 219 |  82,  82 : 75
-  // One sequence of 8192 keys alone, bf16: 16 rows 20, 26 : 53, 32 rows 26, 29 : 53, 48 rows 33, 34 : 53
-  // (kv_many_kernel's items start and end slowly); the lengths are not known here, so the rule is the
-  // full device's.
+  //   bf16  8 rows    90, 138 : 197 |  26,  39 : 70      fp32  16 rows  210 : 422 |  53 : 123
+  //        12 rows   161, 143 : 198 |  46,  40 : 69            32 rows  399 : 423 |  90 : 124
+  //        16 rows   161, 146 : 198 |  47,  41 : 69            48 rows  590 : 423 | 144 : 126
+  //        24 rows   233, 251 : 199 |  67,  81 : 69            64 rows  779 : 425 | 182 : 129
+  //        32 rows   303, 256 : 199 |  80,  82 : 70
+  // One sequence of 8192 keys alone, bf16: 16 rows 19, 26 : 49, 32 rows 25, 28 : 50, 48 rows 30, 33 : 50;
+  // fp32: 32 rows 29 : 51, 64 rows 40 : 55 (kv_many_kernel's items start and end slowly); the lengths are
+  // not known here, so the rule is the full device's.  At 24 rows in bf16 each side wins one column, and
+  // one sequence alone decides.  (Items of 16 rows at 128 wide, 720 bytes a thread of which are spilled:
+  // they read the cache once where items of 8 read it twice.)
   const long long rows = (p->max_q < p->q_tokens ? p->max_q : p->q_tokens) * a.group;
   const int mode = p->dtype != LW_BF16 ? (rows > kFewMost ? 4 : 0)
                                        : (rows > kFewMostBf16 ? 3 : rows > 8 && rows <= 16 ? 1 : 2);
