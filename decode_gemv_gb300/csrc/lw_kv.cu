@@ -51,9 +51,10 @@ __device__ __forceinline__ int64_t slot_tile(const CacheArgs& a, int64_t slot, i
 // same 8 values of one of them (4 neighbouring lanes a group).  The bytes that
 // have to move are 2 in or out a bf16 element and 0.625 for the cache.
 // Measured, 65536 tokens of 8 heads of 128 in bf16: write 87 us, 4.05 TB/s
-// (issue-bound: 84 % of the slots, 21 instructions a value for the range, the
-// definition's separate subtract, multiply and rint, and the nibbles), read 68
-// us, 5.2 TB/s.  A copy reaches 6.8.
+// (issue-bound: 84 % of the slots, 21 instructions a value: a third of them the
+// definition's steps on each value, the rest a group's scale, minimum, reciprocal
+// and limits, done in all four lanes of the group, and a token's slot, tile and
+// addresses, for every 8 + 8 values), read 68 us, 5.2 TB/s.  A copy reaches 6.8.
 constexpr int kTokens = 16;
 
 template <class T, int D, bool VEC>

@@ -46,13 +46,15 @@
 // arrival).
 //
 // Bound by instruction issue where keys are many: a tile of 16 keys is 250
-// instructions, and they issue in 54 % of the slots (waits on the matrix
+// instructions, and they issue in 53 % of the slots (waits on the matrix
 // instructions' results, 4 warps a scheduler).  8 sequences of 65536 keys, 8 heads
-// of 128 with 4 query heads each: bf16 156 us (0.67 GB of cache, 4.3 TB/s), fp32
-// 208 us.  Bound by latency where they are few: 37 keys 7.5 us, 4097 keys of one
+// of 128 with 4 query heads each: bf16 157 us (0.67 GB of cache, 4.3 TB/s), fp32
+// 205 us.  At 128 registers a thread the 128-wide forms spill: 40 to 124 bytes with
+// items of 8 rows, 720 with 16 (253 us where 8 rows take 157; two items of 8 are no
+// faster).  Bound by latency where they are few: 37 keys 7.5 us, 4097 keys of one
 // sequence 15 us (a launch, the search of the range, a tile a warp, the join of up to
-// 32 parts a head: each a chain of loads; 8 heads of weight 39 on 304 CTAs leave some
-// 50 CTAs an item's front alone, without a unit).
+// 32 parts a head: each a chain of loads; 8 heads of weight 39 on 304 CTAs leave
+// 48 CTAs an item's front alone, without a unit).
 #pragma once
 
 #include "lw_kvattn.cuh"
@@ -71,7 +73,7 @@ struct Few {
   // registers: 8 of 65536 159 -> 264 us (spills).
   static constexpr int kWarps = 8, kPerSm = 2, kThreads = 32 * kWarps;
   // tiles a warp takes at once: two where their operands fit the registers
-  // (8 sequences of 65536 keys, 64 wide: 104 -> 89 us; 128 wide 157 -> 173 us)
+  // (8 sequences of 65536 keys, 64 wide: 104 -> 93 us; 128 wide 157 -> 196 us)
   static constexpr int kPair = D == 64 ? 2 : 1;
   static constexpr int kStages = D == 64 ? 2 : 3;    // places of a warp's ring
   static constexpr int kUnit = kWarps * kPair;       // tiles of a unit
@@ -268,8 +270,6 @@ struct FewWarp {
 #pragma unroll
     for (int i = 0; i < NR; ++i) load_row(a, w, q0, rt_rows, i, lane, sums);
     clear();
-    unit = kDown;
-    limit = 0;
     follow(0);
     fm = -INFINITY;
   }

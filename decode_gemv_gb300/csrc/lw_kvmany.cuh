@@ -29,20 +29,21 @@
 // in accumulators of their own (issuer 0 the first, issuer 1 the second; fp16
 // queries are their hi parts).  Two threads share a row, 32 keys of a unit each
 // (one a row had the loaders and the tensor cores wait: 2 x 1024 tokens on 4096
-// keys 537 -> 443 us), and agree through shared memory on the row's maximum where
+// keys 537 -> 443 us when it was changed), and agree through shared memory on the row's maximum where
 // it is raised.  Restoring an element is five times the work, so there are 8
 // loaders (64 wide: 6 of more registers); the buffers are what fits.
 //
 // Measured (8 heads of 128 with 4 query heads each), us and useful TFLOP/s, two
 // products a (row, key) pair:
-//   bf16  2048 tokens on 16384 keys 427, 1206    4096 on 4096 164, 836
-//         8 x 64 on 8192 85, 800                 8 x 512 on 512 77, 224
-//   fp16  2 x 1024 on 4096 390, 308 (five products for two)
-//   fp32  2 x 90 on 2400 50, 138 (six products for two)
+//   bf16  2048 tokens on 16384 keys 398, 1295    4096 on 4096 152, 906
+//         8 x 64 on 8192 82, 835                 8 x 512 on 512 73, 237
+//   fp16  2 x 1024 on 4096 405, 297 (five products for two)
+//   fp32  2 x 90 on 2400 51, 136; 2048 on 6000 559, 298 (six products for two)
 // Long bf16 chunks are bound by the row warps' softmax and the loaders' restoring
-// together (issue 62 %, tensor cores 50 %): two row warps and one and a half
-// loaders share a scheduler, a unit takes 2100 cycles, its products 1250 and its
-// exponentials 1000.  Short items are bound by their starts and ends: reading Q
+// together (issue 63 %, tensor cores 53 %): two row warps and one and a half
+// loaders share a scheduler, a unit takes 2000 cycles, its products 1250 and its
+// exponentials 1000.  The registers are short: a bf16 thread spills 94 to 142 bytes,
+// one of WIDE 96 and 128 wide (96 registers) 396 to 466.  Short items are bound by their starts and ends: reading Q
 // 7000 cycles, writing out 4000 to 9000, joining a cut item's parts 10000.
 //
 // The operand tiles are K-major core matrices of 8 x 16 bytes.  A key code
@@ -69,7 +70,7 @@ struct Many {
   using L = KvTile<D>;
   static constexpr int kRows = WIDE ? kManyTile : 2 * kManyTile;   // of an item
   // an item's start and end, in units' time: some 20000 cycles of 2100 (WIDE: 4000 a unit, 2500 where 64
-  // wide).  4096 tokens on 4096 keys: 6 191 us, 8 165, 10 164, 16 170
+  // wide).  4096 tokens on 4096 keys: 6 175 us, 8 156, 10 152, 12 155, 16 157
   static constexpr int kExtra = WIDE ? (D == 64 ? 8 : 4) : 10;
   static constexpr int kBufs = !WIDE || D == 64 ? 4 : D == 96 ? 3 : 2;   // restored units
   // With two buffers a key tile is free after its S, not after its O: the keys two units on are

@@ -637,12 +637,16 @@ lw_status lw_kv_read(const lw_kv_cache* c, const int64_t* slots, int64_t n, cons
  * key j if j < kv_len[b], j <= p (causal) and j > p - window (window > 0).
  *   s_j = scale q.k_j;  out = sum_j softmax(s)_j v_j;  lse = log sum_j exp s_j
  * with the cached values of k and v.  A query that sees no key gets out = 0,
- * lse = -inf.  Page-table entries beyond a sequence's length, and pages no
+ * lse = -inf.  Rows of q outside every sequence are not written.  A cached NaN is
+ * where the formula has it: in a key, all of the rows that see the key, lse too;
+ * in a value, its group's 32 elements of those rows.  Page-table entries beyond a sequence's length, and pages no
  * query sees, are not read.  The answer does not depend on the page size or on
  * where the pages lie, and on max_q only through the kernel that it chooses (the
  * same to the type's rounding); it is deterministic on a given device.  Sums and
  * softmax statistics are fp32.  fp32 and fp16 calls carry every 16-bit operand of
- * a matrix instruction in two parts (22 bits), bf16 calls in one (11 bits).
+ * a matrix instruction in two parts (22 bits), bf16 calls in one (11 bits), but for
+ * the queries' group sums; probabilities keep the 22 bits down to 2^-18, and 11
+ * down to 2^-23, of the largest among the keys summed together.
  * q_tokens * q_heads, max_q * q_heads and table_width * page_tokens are at most
  * 2^31 - 1024, batch and q_heads at most 65535 (else LW_ERR_SHAPE).
  */
