@@ -20,7 +20,8 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "liblw.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU = ["lw_api.cu", "lw_q.cu", "lw_qlut.cu", "lw_bf16.cu", "lw_noalloc.cu", "lw_trans.cu",
-      "lw_strips.cu", "lw_kv.cu", "lw_kvattn.cu"]
+      "lw_strips.cu", "lw_kv.cu", "lw_kvattn.cu", "lw_kvrotary.cu", "lw_kvweigh.cu",
+      "lw_kvevict.cu", "lw_kvblocks.cu"]
 CPP = ["lw_host.cpp", "lw_file.cpp"]
 
 

@@ -19,32 +19,26 @@ lw_status check_kv_cache(const lw_kv_cache* c) {
   return LW_OK;
 }
 
-namespace {
-
-struct RowsArgs {
-  void* ptr;
-  int64_t token_stride, head_stride;
-};
-struct CacheArgs {
-  RowsArgs k, v;
-  uint8_t* pages;
-  const int64_t* slots;
-  int64_t n, n_slots, page_bytes;
-  int32_t page_tiles, page_shift, heads;   // page_tiles = 2^page_shift, or page_shift < 0
-  int32_t* status;
-};
-
-// The tile of a slot (head 0: its place in the pages; -1 if the slot is not
-// stored).  A slot past the pages is reported where `first`.
-__device__ __forceinline__ int64_t slot_tile(const CacheArgs& a, int64_t slot, int tile_bytes, bool first) {
-  if (slot < 0 || slot >= a.n_slots) {
-    if (slot >= 0 && first) dev::report(a.status, LW_DEV_BAD_SLOT);
-    return -1;
-  }
-  const uint32_t tile = (uint32_t)(slot / LW_KV_TILE);   // (slots are below 2^32)
-  const uint32_t page = a.page_shift >= 0 ? tile >> a.page_shift : tile / (uint32_t)a.page_tiles;
-  return page * a.page_bytes + (int64_t)(tile - page * (uint32_t)a.page_tiles) * tile_bytes;
+CacheArgs kv_cache_args(const lw_kv_cache* c, const lw_kv_rows* k, const lw_kv_rows* v, const int64_t* slots,
+                        int64_t n, int32_t* d_status) {
+  CacheArgs a{};
+  a.k = {k->ptr, k->token_stride, k->head_stride};
+  a.v = {v->ptr, v->token_stride, v->head_stride};
+  a.pages = static_cast<uint8_t*>(c->pages);
+  a.slots = slots;
+  a.n = n;
+  a.n_slots = c->n_pages * c->page_tokens;
+  a.page_bytes = (int64_t)lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens);
+  a.page_tiles = c->page_tokens / LW_KV_TILE;
+  a.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_tiles == 1 << i) a.page_shift = i;
+  a.heads = c->kv_heads;
+  a.status = d_status;
+  return a;
 }
+
+namespace {
 
 // Both kernels: a block takes 16 tokens of one head (a tile of the cache, if they
 // are consecutive, whose lines it completes), a thread 8 consecutive keys and the
@@ -72,23 +66,13 @@ __global__ void __launch_bounds__(kTokens * D / 8) kv_write_kernel(const CacheAr
                                 k, lo[0], hi[0]);
     dev::kv_load8_range<T, VEC>(static_cast<const T*>(a.v.ptr) + tok * a.v.token_stride + h * a.v.head_stride + 8 * ch,
                                 v, lo[1], hi[1]);
-    at = slot_tile(a, slot, L::kBytes, h == 0 && ch == 0);
+    at = dev::slot_tile(a, slot, L::kBytes, h == 0 && ch == 0);
   }
   __half ks, km, vs, vm;
   const uint32_t kw = dev::kv_quantise8(k, lo[0], hi[0], ks, km), vw = dev::kv_quantise8(v, lo[1], hi[1], vs, vm);
   if (at < 0) return;
-  const int t = (int)(slot % LW_KV_TILE), g = ch >> 2, q = ch & 3;
-  uint8_t* tile = a.pages + at + (int64_t)h * a.page_tiles * L::kBytes;
-  const int par = 2 * ((t / 2 * L::G + g) * 2 + t % 2);
-  *reinterpret_cast<uint32_t*>(tile + L::kKeyCodes + 4 * ((t * 4 + q) * L::G + g)) = kw;
-  uint8_t* u = tile + L::kValCodes + 4 * ((t / 2 * 8 + 2 * q) * L::G + g) + 2 * (t % 2);
-  *reinterpret_cast<uint16_t*>(u) = (uint16_t)vw;
-  *reinterpret_cast<uint16_t*>(u + 4 * L::G) = (uint16_t)(vw >> 16);
-  // a lane of the group each
-  if (q == 0) *reinterpret_cast<__half*>(tile + L::kKeyScale + par) = ks;
-  if (q == 1) *reinterpret_cast<__half*>(tile + L::kKeyMin + 2 * (t * L::GP + g)) = km;
-  if (q == 2) *reinterpret_cast<__half*>(tile + L::kValScale + par) = vs;
-  if (q == 3) *reinterpret_cast<__half*>(tile + L::kValMin + par) = vm;
+  dev::kv_put8<D>(a.pages + at + (int64_t)h * a.page_tiles * L::kBytes, (int)(slot % LW_KV_TILE), ch, kw, ks, km, vw,
+                  vs, vm);
 }
 
 // scale * code + min of 8 codes
@@ -113,7 +97,7 @@ __global__ void __launch_bounds__(kTokens * D / 8) kv_read_kernel(const CacheArg
   dev::pdl_wait();
   if (tok >= a.n) return;
   const int64_t slot = a.slots[tok];
-  const int64_t at = slot_tile(a, slot, L::kBytes, h == 0 && ch == 0);
+  const int64_t at = dev::slot_tile(a, slot, L::kBytes, h == 0 && ch == 0);
   float k[8] = {}, v[8] = {};
   if (at >= 0) {
     const int t = (int)(slot % LW_KV_TILE), g = ch >> 2, q = ch & 3;
@@ -179,20 +163,7 @@ lw_status kv_rows_call(const char* fn, const lw_kv_cache* c, const int64_t* slot
     return fail(LW_ERR_INVALID_ARG, "%s: an address is not aligned to its type", fn);
   if ((n + kTokens - 1) / kTokens > (1ll << 31) - 1)
     return fail(LW_ERR_SHAPE, "%s: %lld tokens", fn, (long long)n);
-  CacheArgs a{};
-  a.k = {k->ptr, k->token_stride, k->head_stride};
-  a.v = {v->ptr, v->token_stride, v->head_stride};
-  a.pages = static_cast<uint8_t*>(c->pages);
-  a.slots = slots;
-  a.n = n;
-  a.n_slots = c->n_pages * c->page_tokens;
-  a.page_bytes = (int64_t)lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens);
-  a.page_tiles = c->page_tokens / LW_KV_TILE;
-  a.page_shift = -1;
-  for (int i = 0; i < 31; ++i)
-    if (a.page_tiles == 1 << i) a.page_shift = i;
-  a.heads = c->kv_heads;
-  a.status = d_status;
+  const CacheArgs a = kv_cache_args(c, k, v, slots, n, d_status);
   const bool vec = kv_rows_aligned(k->ptr, k->token_stride, k->head_stride, k->dtype) &&
                    kv_rows_aligned(v->ptr, v->token_stride, v->head_stride, v->dtype);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -244,9 +215,7 @@ extern "C" size_t lw_kv_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, i
   return kv_attention_workspace(c, q_heads, q_tokens);
 }
 
-extern "C" lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, void* ws,
-                                     size_t ws_bytes, int32_t* d_status, void* stream) {
-  clear_error();
+lw_status lw::check_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a) {
   lw_status s = check_kv_cache(c);
   if (s != LW_OK) return s;
   if (!a) return fail(LW_ERR_INVALID_ARG, "NULL arguments");
@@ -275,8 +244,16 @@ extern "C" lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, 
       reinterpret_cast<uintptr_t>(a->lse) % 4 || reinterpret_cast<uintptr_t>(a->q_start) % 4 ||
       reinterpret_cast<uintptr_t>(a->kv_len) % 4 || reinterpret_cast<uintptr_t>(a->page_table) % 4)
     return fail(LW_ERR_INVALID_ARG, "an address is not aligned to its type");
+  return LW_OK;
+}
+
+extern "C" lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, void* ws,
+                                     size_t ws_bytes, int32_t* d_status, void* stream) {
+  clear_error();
+  const lw_status s = check_kv_attention(c, a);
+  if (s != LW_OK || a->q_tokens == 0) return s;
   const size_t need = lw_kv_workspace_bytes(c, a->q_heads, a->q_tokens, a->batch);
   if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 15u))
     return fail(LW_ERR_INVALID_ARG, "workspace missing, misaligned or %zu bytes of %zu", ws_bytes, need);
-  return launch_kv_attention(c, a, ws, d_status, static_cast<cudaStream_t>(stream));
+  return launch_kv_attention(c, a, 0, ws, d_status, static_cast<cudaStream_t>(stream));
 }

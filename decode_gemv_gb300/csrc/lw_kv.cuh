@@ -28,7 +28,33 @@ static_assert(KvTile<64>::kBytes % 16 == 0 && KvTile<96>::kBytes % 16 == 0 &&
                   KvTile<128>::kBytes % 16 == 0,
               "tiles are copied in units of 16 bytes");
 
+// Rows of heads, and what the calls that write tokens or read them back take.
+struct RowsArgs {
+  void* ptr;
+  int64_t token_stride, head_stride;
+};
+struct CacheArgs {
+  RowsArgs k, v;
+  uint8_t* pages;
+  const int64_t* slots;
+  int64_t n, n_slots, page_bytes;
+  int32_t page_tiles, page_shift, heads;   // page_tiles = 2^page_shift, or page_shift < 0
+  int32_t* status;
+};
+
 namespace dev {
+
+// The tile of a slot (head 0: its place in the pages; -1 if the slot is not
+// stored).  A slot past the pages is reported where `first`.
+__device__ __forceinline__ int64_t slot_tile(const CacheArgs& a, int64_t slot, int tile_bytes, bool first) {
+  if (slot < 0 || slot >= a.n_slots) {
+    if (slot >= 0 && first) report(a.status, LW_DEV_BAD_SLOT);
+    return -1;
+  }
+  const uint32_t tile = (uint32_t)(slot / LW_KV_TILE);   // (slots are below 2^32)
+  const uint32_t page = a.page_shift >= 0 ? tile >> a.page_shift : tile / (uint32_t)a.page_tiles;
+  return page * a.page_bytes + (int64_t)(tile - page * (uint32_t)a.page_tiles) * tile_bytes;
+}
 
 template <class T>
 __device__ __forceinline__ float kv_float(T x);
@@ -81,6 +107,21 @@ __device__ __forceinline__ void kv_store8(T* p, const float (&x)[8]) {
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = kv_round<T>(x[i]);
+  }
+}
+
+// N consecutive words of a tile in global memory
+template <int N>
+__device__ __forceinline__ void ldg_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x; w[1] = u.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
   }
 }
 
@@ -219,6 +260,24 @@ __device__ __forceinline__ uint32_t kv_quantise8(float (&x)[8], float lo, float 
     w = 0;
   }
   return w;
+}
+
+// Chunk ch (8 values, in 4 neighbouring lanes a group) of one token's key and value codes into its
+// tile; the group's scales and minimums by a lane each.
+template <int D>
+__device__ __forceinline__ void kv_put8(uint8_t* tile, int t, int ch, uint32_t kw, __half ks, __half km, uint32_t vw,
+                                        __half vs, __half vm) {
+  using L = KvTile<D>;
+  const int g = ch >> 2, q = ch & 3;
+  const int par = 2 * ((t / 2 * L::G + g) * 2 + t % 2);
+  *reinterpret_cast<uint32_t*>(tile + L::kKeyCodes + 4 * ((t * 4 + q) * L::G + g)) = kw;
+  uint8_t* u = tile + L::kValCodes + 4 * ((t / 2 * 8 + 2 * q) * L::G + g) + 2 * (t % 2);
+  *reinterpret_cast<uint16_t*>(u) = (uint16_t)vw;
+  *reinterpret_cast<uint16_t*>(u + 4 * L::G) = (uint16_t)(vw >> 16);
+  if (q == 0) *reinterpret_cast<__half*>(tile + L::kKeyScale + par) = ks;
+  if (q == 1) *reinterpret_cast<__half*>(tile + L::kKeyMin + 2 * (t * L::GP + g)) = km;
+  if (q == 2) *reinterpret_cast<__half*>(tile + L::kValScale + par) = vs;
+  if (q == 3) *reinterpret_cast<__half*>(tile + L::kValMin + par) = vm;
 }
 
 }  // namespace dev

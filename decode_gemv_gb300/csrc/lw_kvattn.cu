@@ -42,7 +42,7 @@ size_t kv_attention_workspace(const lw_kv_cache* c, int32_t q_heads, int64_t q_t
   return attn_counter_bytes() + (size_t)device_sm_count() * (all_few ? few : many) * (size_t)(c->head_dim + 2) * 4;
 }
 
-lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* ws, int32_t* status,
+lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, int parts, void* ws, int32_t* status,
                               cudaStream_t st) {
   AttnArgs a{};
   a.p = *p;
@@ -56,6 +56,7 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* w
   a.group = p->q_heads / c->kv_heads;
   a.vec = kv_rows_aligned(p->q, p->q_token_stride, p->q_head_stride, p->dtype) &&
           kv_rows_aligned(p->out, p->out_token_stride, p->out_head_stride, p->dtype);
+  a.parts = parts;
   a.status = status;
   // The variant, by the rows of a sequence on a key/value head.  us, kv_few_kernel (items of 8 rows, or
   // of 16) against kv_many_kernel, at 8 sequences of 32768 keys | 64 of 512, 8 heads of 128:
@@ -70,8 +71,9 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, void* w
   // one sequence alone decides.  (Items of 16 rows at 128 wide, 720 bytes a thread of which are spilled:
   // they read the cache once where items of 8 read it twice.)
   const long long rows = (p->max_q < p->q_tokens ? p->max_q : p->q_tokens) * a.group;
-  const int mode = p->dtype != LW_BF16 ? (rows > kFewMost ? 4 : 0)
-                                       : (rows > kFewMostBf16 ? 3 : rows > 8 && rows <= 16 ? 1 : 2);
+  // (A token that reads pages of its own is the rows of one group: kv_few_kernel's.)
+  const int mode = p->dtype != LW_BF16 ? (rows > kFewMost && !parts ? 4 : 0)
+                                       : (rows > kFewMostBf16 && !parts ? 3 : rows > 8 && rows <= 16 ? 1 : 2);
   const Variant v = c->head_dim == 64 ? variant<64>(mode) : c->head_dim == 96 ? variant<96>(mode) : variant<128>(mode);
   if (resident_blocks(reinterpret_cast<const void*>(v.kernel), v.threads, v.smem) < 1)
     return fail(LW_ERR_CUDA, "lw_kv_attention: the kernel does not fit this device");

@@ -15,6 +15,7 @@ struct AttnArgs {
   float* partials;      // [grid][2] partial results of RT rows
   int32_t page_tokens, heads, group;
   int32_t vec;          // q and out rows are 16-byte aligned
+  int32_t parts;        // 0, or the heads of the cache that is seen head by head: see kv_seq
   int32_t* status;
 };
 
@@ -24,8 +25,17 @@ namespace dev {
 // Ordinary loads, here and of the page table: what the work in front writes may
 // not be read by way of the read-only path, which the wait for that work does not
 // order.
+// With `parts` every token and key/value head is a sequence of its own, of one token
+// (b = token * parts + head) on kv_len[b] keys, or of none where that is negative.
 template <bool LOUD>
 __device__ __forceinline__ void kv_seq(const AttnArgs& a, int b, int& q0, int& T, int& n) {
+  if (a.parts) {
+    q0 = b;
+    n = a.p.kv_len[b];
+    T = n >= 0;
+    n = max(n, 0);
+    return;
+  }
   q0 = a.p.q_start[b];
   const int q1 = a.p.q_start[b + 1];
   n = a.p.kv_len[b];
@@ -34,6 +44,13 @@ __device__ __forceinline__ void kv_seq(const AttnArgs& a, int b, int& q0, int& T
   if (LOUD && (bad || n < 0 || n > most)) report(a.status, LW_DEV_BAD_SEQ);
   T = bad ? 0 : q1 - q0;
   n = n < 0 ? 0 : (n > most ? most : n);
+}
+
+// Where the rows of packed token i begin
+__device__ __forceinline__ int64_t kv_token_at(const AttnArgs& a, int i, int64_t token_stride, int64_t head_stride) {
+  if (a.parts <= 1) return i * token_stride;
+  const int t = i / a.parts;
+  return t * token_stride + (int64_t)(i - t * a.parts) * a.group * head_stride;
 }
 
 // Sum over the CTA of one value per thread, and the exclusive sum before

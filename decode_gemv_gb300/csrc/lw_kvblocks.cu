@@ -1,0 +1,497 @@
+// Sparse attention over the 4-bit cache: summaries of pages, and the choice of
+// the pages that each query reads.
+#include "lw_kvfew.cuh"
+#include "lw_kv.h"
+#include "lw_kvselect.cuh"
+
+namespace lw {
+namespace {
+
+constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
+
+// A page's record of one head: int8 hi[D], lo[D], fp32 step, 12 bytes unused
+__host__ __device__ constexpr int record_bytes(int D) { return 2 * D + 16; }
+
+// ---- summaries -----------------------------------------------------------------
+struct SummaryArgs {
+  lw_kv_summaries p;
+  const uint8_t* pages;
+  int64_t n_pages, page_bytes;
+  int32_t page_tokens, heads;
+  int32_t* status;
+};
+constexpr int kSumWarps = 8;
+
+// A warp a page and head: lanes hold keys lane / 4 and 8 more of a tile, elements 32 g + 8 (lane % 4) + 0..7.
+template <int D>
+__global__ void __launch_bounds__(32 * kSumWarps) kv_summarise_kernel(const SummaryArgs a) {
+  using L = KvTile<D>;
+  constexpr int G = L::G, GX = G == 2 ? 2 : 4;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = lane / 4, q = lane % 4;
+  const int h = blockIdx.y, b = blockIdx.z, tpp = a.page_tokens / LW_KV_TILE;
+  dev::pdl_wait();
+  const int len = a.p.kv_len[b], most = a.p.table_width * a.page_tokens;
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0 && (len < 0 || len > most)) dev::report(a.status, LW_DEV_BAD_SEQ);
+  const int n = len < 0 ? 0 : (len > most ? most : len);
+  const int start = max(a.p.start[b], 0);
+  if (start >= n) return;
+  const int last = (n - 1) / a.page_tokens;
+  const int32_t* table = a.p.page_table + (int64_t)b * a.p.table_stride;
+  for (int blk = start / a.page_tokens + blockIdx.x * kSumWarps + warp; blk <= last; blk += gridDim.x * kSumWarps) {
+    const int page = table[blk];
+    if (page < 0 || page >= a.n_pages) {
+      if (lane == 0) dev::report(a.status, LW_DEV_BAD_PAGE);
+      continue;
+    }
+    const uint8_t* s = a.pages + page * a.page_bytes + (int64_t)h * tpp * L::kBytes;
+    const int keys = min(n - blk * a.page_tokens, a.page_tokens);
+    float lo[GX][8], hi[GX][8];
+#pragma unroll
+    for (int g = 0; g < GX; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo[g][i] = INFINITY;
+        hi[g][i] = -INFINITY;
+      }
+#pragma unroll 1
+    for (int tile = 0; 16 * tile < keys; ++tile, s += L::kBytes) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int tk = t + 8 * e;
+        if (16 * tile + tk >= keys) continue;
+        uint32_t kc[G], ks[G], km[L::GP / 2];
+        dev::ldg_words<G>(s + L::kKeyCodes + ((tk * 4 + q) * G) * 4, kc);
+        dev::ldg_words<G>(s + L::kKeyScale + (tk / 2 * G) * 4, ks);
+        dev::ldg_words<L::GP / 2>(s + L::kKeyMin + tk * L::GP * 2, km);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float2 s2 = dev::h2f(ks[g]), m2 = dev::h2f(km[g / 2]);
+          const float sc = t % 2 ? s2.y : s2.x, mn = g % 2 ? m2.y : m2.x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t c = i % 2 ? dev::whole_odd(kc[g] >> (8 * (i / 2))) : dev::whole_even(kc[g] >> (8 * (i / 2)));
+            const float2 y = dev::fma2(dev::h2f(c), make_float2(sc, sc), make_float2(mn, mn));
+            lo[g][i] = dev::min3(lo[g][i], y.x, y.x);
+            hi[g][i] = dev::max3(hi[g][i], y.x, y.x);
+            lo[g][i + 4] = dev::min3(lo[g][i + 4], y.y, y.y);
+            hi[g][i + 4] = dev::max3(hi[g][i + 4], y.y, y.y);
+          }
+        }
+      }
+    }
+    // over the keys: lane t of a channel's 8 ends up with the 4 channels of group t / 2, half t % 2 (64 wide:
+    // of group t / 2 % 2)
+    float l4[4], h4[4];
+    {
+      constexpr int kHalf = GX / 2;
+#pragma unroll
+      for (int x = 0; x < kHalf; ++x)   // a lane keeps half the groups
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool up = GX == 4 ? lane & 16 : lane & 8;
+          const int o = GX == 4 ? 16 : 8;
+          const float gl = __shfl_xor_sync(0xFFFFFFFFu, up ? lo[x][i] : lo[x + kHalf][i], o);
+          const float gh = __shfl_xor_sync(0xFFFFFFFFu, up ? hi[x][i] : hi[x + kHalf][i], o);
+          const float ol = up ? lo[x + kHalf][i] : lo[x][i], oh = up ? hi[x + kHalf][i] : hi[x][i];
+          lo[x][i] = dev::min3(ol, gl, gl);
+          hi[x][i] = dev::max3(oh, gh, gh);
+        }
+      if constexpr (GX == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool up = lane & 8;
+          const float gl = __shfl_xor_sync(0xFFFFFFFFu, up ? lo[0][i] : lo[1][i], 8);
+          const float gh = __shfl_xor_sync(0xFFFFFFFFu, up ? hi[0][i] : hi[1][i], 8);
+          const float ol = up ? lo[1][i] : lo[0][i], oh = up ? hi[1][i] : hi[0][i];
+          lo[0][i] = dev::min3(ol, gl, gl);
+          hi[0][i] = dev::max3(oh, gh, gh);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float gl = __shfl_xor_sync(0xFFFFFFFFu, lo[0][i], 16), gh = __shfl_xor_sync(0xFFFFFFFFu, hi[0][i], 16);
+          lo[0][i] = dev::min3(lo[0][i], gl, gl);
+          hi[0][i] = dev::max3(hi[0][i], gh, gh);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 4;
+        const float gl = __shfl_xor_sync(0xFFFFFFFFu, up ? lo[0][i] : lo[0][i + 4], 4);
+        const float gh = __shfl_xor_sync(0xFFFFFFFFu, up ? hi[0][i] : hi[0][i + 4], 4);
+        const float ol = up ? lo[0][i + 4] : lo[0][i], oh = up ? hi[0][i + 4] : hi[0][i];
+        l4[i] = dev::min3(ol, gl, gl);
+        h4[i] = dev::max3(oh, gh, gh);
+      }
+    }
+    const int g = GX == 4 ? t / 2 : t / 2 % 2;
+    const bool real = g < G;   // (96 wide: the fourth group is not there)
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (real) top = dev::max3(top, fabsf(l4[i]), fabsf(h4[i]));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float x = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+      top = dev::max3(top, x, x);
+    }
+    const bool zero = !(top > kTiny);   // (or a NaN)
+    const float inv = zero ? 0.f : __fmul_rn(127.f, __frcp_rn(top));
+    uint32_t wl = 0, wh = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int cl = zero ? 0 : __float2int_rn(__fmul_rn(l4[i], inv)), ch = zero ? 0 : __float2int_rn(__fmul_rn(h4[i], inv));
+      wl |= (uint32_t)(cl & 255) << (8 * i);
+      wh |= (uint32_t)(ch & 255) << (8 * i);
+    }
+    uint8_t* r = static_cast<uint8_t*>(a.p.summary) + ((int64_t)page * a.heads + h) * record_bytes(D);
+    if (real && (GX == 4 || lane < 16)) {
+      const int at = 32 * g + 8 * q + 4 * (t % 2);
+      *reinterpret_cast<uint32_t*>(r + at) = wh;
+      *reinterpret_cast<uint32_t*>(r + D + at) = wl;
+    }
+    if (lane == 0) *reinterpret_cast<float*>(r + 2 * D) = __fmul_rn(top, (float)(1.0 / 127.0));
+  }
+}
+
+// ---- scores and choice ---------------------------------------------------------
+struct BlockArgs {
+  lw_kv_attn p;
+  lw_kv_blocks s;
+  float* scores;         // [q_tokens * heads][table_width]
+  int32_t* pages;        // [q_tokens * heads][blocks]: pages of the cache seen head by head
+  int32_t* lens;         // [q_tokens * heads]: keys in them, -1 for a token of no sequence
+  int64_t n_pages;
+  int32_t page_tokens, heads, group, vec;
+  int32_t* status;
+};
+
+// The sequence that has query token `tok`, the token's key position in it, its row of the page table; false
+// if there is none.  Whole CTA.
+__device__ __forceinline__ bool token_seq(const BlockArgs& a, int tok, int* s_seq, int& b, int& pos) {
+  if (threadIdx.x == 0) *s_seq = 0x7FFFFFFF;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.p.batch; i += blockDim.x) {
+    const int q0 = a.p.q_start[i], q1 = a.p.q_start[i + 1];
+    if (q0 >= 0 && q1 <= a.p.q_tokens && q0 <= tok && tok < q1) atomicMin(s_seq, i);
+  }
+  __syncthreads();
+  b = *s_seq;
+  if (b == 0x7FFFFFFF) return false;
+  const int len = a.p.kv_len[b], most = a.p.table_width * a.page_tokens;
+  const int n = len < 0 ? 0 : (len > most ? most : len);
+  pos = (int)((int64_t)n - a.p.q_start[b + 1] + tok);
+  return true;
+}
+
+constexpr int kScoreWarps = 8, kScoreBlocks = 256;   // pages a CTA scores at most
+constexpr int kMostGroup = 256;
+
+// Codes of the group's query heads -- their positive and negative parts apart, so that the larger of c hi and
+// c lo is picked by a product: sum c+ hi + c- lo -- and the pages' scores.  8 lanes a record.
+template <int D, class T>
+__global__ void __launch_bounds__(32 * kScoreWarps) kv_score_kernel(const BlockArgs a) {
+  constexpr int W = D / 32;            // words a lane
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_seq;
+  uint32_t* codes = reinterpret_cast<uint32_t*>(smem);                  // [group][2][8][W]
+  float* units = reinterpret_cast<float*>(smem + (size_t)a.group * 2 * D);
+  const int h = blockIdx.y, tok = blockIdx.z, warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane % 8;
+  dev::pdl_wait();
+  int b, pos;
+  if (!token_seq(a, tok, &s_seq, b, pos) || pos < 0) return;
+  const int nb = pos / a.page_tokens + 1, x0 = blockIdx.x * kScoreBlocks;
+  if (x0 >= nb || nb <= a.s.blocks) return;   // all are read: no scores are needed
+  // four heads a warp at a time
+  for (int g0 = 4 * warp; g0 < a.group; g0 += 4 * kScoreWarps) {
+    const int g = g0 + lane / 8;
+    const T* q = static_cast<const T*>(a.p.q) + (int64_t)tok * a.p.q_token_stride +
+                 (int64_t)(h * a.group + (g < a.group ? g : 0)) * a.p.q_head_stride + r * (D / 8);
+    float x[D / 8], top = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      x[i] = dev::kv_float<T>(q[i]);
+      top = dev::max3(top, fabsf(x[i]), top);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const float y = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+      top = dev::max3(top, y, y);
+    }
+    const bool zero = !(top > kTiny && top <= 3.402823466e38f);
+    const float inv = zero ? 0.f : __fmul_rn(127.f, __frcp_rn(top));
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      uint32_t plus = 0, minus = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = zero ? 0 : __float2int_rn(__fmul_rn(x[4 * w + i], inv));
+        plus |= (uint32_t)(max(c, 0) & 255) << (8 * i);
+        minus |= (uint32_t)(min(c, 0) & 255) << (8 * i);
+      }
+      if (g < a.group) {
+        codes[((g * 2) * 8 + r) * W + w] = plus;
+        codes[((g * 2 + 1) * 8 + r) * W + w] = minus;
+      }
+    }
+    if (g < a.group && r == 0) units[g] = zero ? 0.f : __fmul_rn(top, (float)(1.0 / 127.0));
+  }
+  __syncthreads();
+  const int32_t* table = a.p.page_table + (int64_t)b * a.p.table_stride;
+  float* scores = a.scores + ((int64_t)tok * a.heads + h) * a.p.table_width;
+  const int end = min(nb, x0 + kScoreBlocks);
+  for (int x1 = x0 + 4 * warp; x1 < end; x1 += 4 * kScoreWarps) {
+    const int x = x1 + lane / 8;
+    const int page = x < end ? table[x] : -1;
+    const bool ok = page >= 0 && page < a.n_pages;
+    const uint8_t* rec = static_cast<const uint8_t*>(a.s.summary) + ((int64_t)(ok ? page : 0) * a.heads + h) * record_bytes(D);
+    uint32_t hi[W], lo[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      hi[w] = *reinterpret_cast<const uint32_t*>(rec + (r * W + w) * 4);
+      lo[w] = *reinterpret_cast<const uint32_t*>(rec + D + (r * W + w) * 4);
+    }
+    const float step = *reinterpret_cast<const float*>(rec + 2 * D);
+    float best = -INFINITY;
+    for (int g = 0; g < a.group; ++g) {
+      int dot = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        dot = __dp4a((int)codes[((g * 2) * 8 + r) * W + w], (int)hi[w], dot);
+        dot = __dp4a((int)codes[((g * 2 + 1) * 8 + r) * W + w], (int)lo[w], dot);
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+      best = fmaxf(best, __fmul_rn(units[g], (float)dot));
+    }
+    // (a page outside the cache is read by nobody: the attention leaves it out)
+    if (r == 0 && x < end) scores[x] = ok ? __fmul_rn(step, best) : -INFINITY;
+  }
+}
+
+constexpr int kChoose = 256;
+
+// The pages of one query token and key/value head, ascending.
+__global__ void __launch_bounds__(kChoose) kv_choose_kernel(const BlockArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
+  __shared__ uint32_t hist[256], s_scan[kChoose / 32], s_pick[2];
+  __shared__ int s_seq;
+  const int h = blockIdx.x, tok = blockIdx.y, tid = threadIdx.x;
+  dev::pdl_wait();
+  if (h == 0 && tok == 0)
+    for (int i = tid; i < a.p.batch; i += kChoose) {
+      const int q0 = a.p.q_start[i], q1 = a.p.q_start[i + 1], n = a.p.kv_len[i];
+      if (q0 < 0 || q1 < q0 || q1 > a.p.q_tokens || n < 0 || n > a.p.table_width * a.page_tokens)
+        dev::report(a.status, LW_DEV_BAD_SEQ);
+    }
+  const int64_t row = (int64_t)tok * a.heads + h;
+  int b, pos;
+  if (!token_seq(a, tok, &s_seq, b, pos)) {
+    if (tid == 0) a.lens[row] = -1;
+    return;
+  }
+  const int nb = pos < 0 ? 0 : pos / a.page_tokens + 1, count = nb < a.s.blocks ? nb : a.s.blocks;
+  const int32_t* table = a.p.page_table + (int64_t)b * a.p.table_stride;
+  int32_t* pages = a.pages + row * a.s.blocks;
+  int32_t* chosen = a.s.chosen ? a.s.chosen + row * a.s.blocks : nullptr;
+  const auto put = [&](int i, int blk) {
+    const int page = table[blk];
+    const bool ok = page >= 0 && page < a.n_pages;
+    pages[i] = ok ? page * a.heads + h : -1;
+    if (chosen) chosen[i] = blk;
+  };
+  if (chosen)
+    for (int i = count + tid; i < a.s.blocks; i += kChoose) chosen[i] = -1;
+  if (tid == 0) a.lens[row] = nb ? (count - 1) * a.page_tokens + pos - (nb - 1) * a.page_tokens + 1 : 0;
+  if (nb <= a.s.blocks) {
+    for (int i = tid; i < nb; i += kChoose) put(i, i);
+    return;
+  }
+  const int first = a.s.first, last = nb - a.s.recent;
+  for (int i = tid; i < first; i += kChoose) put(i, i);
+  for (int i = last + tid; i < nb; i += kChoose) put(count - nb + i, i);
+  uint32_t need = (uint32_t)(count - first - a.s.recent), limit = 0;
+  if (need == 0) return;
+  const float* scores = a.scores + row * a.p.table_width;
+  for (int i = first + tid; i < last; i += kChoose) keys[i - first] = dev::order_key(scores[i]);
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    hist[tid] = 0;
+    __syncthreads();
+    const uint32_t mask = shift == 24 ? 0 : ~0u << (shift + 8);
+    for (int i = tid; i < last - first; i += kChoose)
+      if ((keys[i] & mask) == limit) atomicAdd(&hist[keys[i] >> shift & 255], 1u);
+    __syncthreads();
+    limit |= dev::pick_digit<kChoose>(hist, need, s_scan, s_pick) << shift;
+  }
+  uint32_t above = 0, equal = 0;
+  for (int i0 = 0; i0 < last - first; i0 += kChoose) {
+    const int i = i0 + tid;
+    const uint32_t k = i < last - first ? keys[i] : 0;
+    const bool more = i < last - first && k > limit, same = i < last - first && k == limit;
+    uint32_t total;
+    const uint32_t at = dev::scan_cta<kChoose>((uint32_t)more | (uint32_t)same << 16, s_scan, total);
+    const uint32_t ab = above + (at & 0xFFFFu), eq = equal + (at >> 16);
+    if (more || (same && eq < need)) put(first + (int)(ab + (eq < need ? eq : need)), first + i);
+    above += total & 0xFFFFu;
+    equal += total >> 16;
+  }
+}
+
+constexpr int kMostWidth = 49152;
+
+template <int D, class T>
+lw_status launch_score(const BlockArgs& a, dim3 grid, cudaStream_t st) {
+  const size_t smem = (size_t)a.group * (2 * D + 4);
+  if (resident_blocks(reinterpret_cast<const void*>(kv_score_kernel<D, T>), 32 * kScoreWarps, smem) < 1)
+    return fail(LW_ERR_CUDA, "lw_kv_attention_blocks: the kernel does not fit this device");
+  return kv_launch("lw_kv_attention_blocks", kv_score_kernel<D, T>, grid, 32 * kScoreWarps, smem, 1, st, a);
+}
+template <int D>
+lw_status launch_score_t(const BlockArgs& a, dim3 grid, cudaStream_t st) {
+  return a.p.dtype == LW_F32   ? launch_score<D, float>(a, grid, st)
+         : a.p.dtype == LW_F16 ? launch_score<D, __half>(a, grid, st)
+                               : launch_score<D, __nv_bfloat16>(a, grid, st);
+}
+
+// The cache with a head's share of a page as a page: what a query that reads pages of its own attends to
+lw_kv_cache by_head(const lw_kv_cache* c) {
+  lw_kv_cache v = *c;
+  v.n_pages = c->n_pages * c->kv_heads;
+  v.kv_heads = 1;
+  return v;
+}
+
+// Workspace: attention's, then page numbers, lengths and scores of each token and head
+struct BlockSpace {
+  size_t pages, lens, scores, bytes;
+};
+BlockSpace block_space(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens, int32_t width, int32_t blocks) {
+  const lw_kv_cache v = by_head(c);
+  const size_t rows = (size_t)q_tokens * c->kv_heads;
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  BlockSpace s{};
+  s.pages = up(kv_attention_workspace(&v, q_heads / c->kv_heads, q_tokens * c->kv_heads));
+  s.lens = s.pages + up(rows * blocks * 4);
+  s.scores = s.lens + up(rows * 4);
+  s.bytes = s.scores + up(rows * width * 4);
+  return s;
+}
+
+}  // namespace
+}  // namespace lw
+
+using namespace lw;
+
+extern "C" size_t lw_kv_summary_bytes(const lw_kv_cache* c) {
+  if (!c || !lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens) || c->n_pages < 1) return 0;
+  return (size_t)c->n_pages * c->kv_heads * record_bytes(c->head_dim);
+}
+
+extern "C" lw_status lw_kv_summarise(const lw_kv_cache* c, const lw_kv_summaries* p, int32_t* d_status, void* stream) {
+  const char* fn = "lw_kv_summarise";
+  clear_error();
+  lw_status s = check_kv_cache(c);
+  if (s != LW_OK) return s;
+  if (!p) return fail(LW_ERR_INVALID_ARG, "NULL arguments");
+  if (p->batch < 1 || p->batch > 65535) return fail(LW_ERR_SHAPE, "%s: batch %d (1..65535)", fn, p->batch);
+  if (p->table_width < 0 || p->table_stride < 0 || (int64_t)p->table_width * c->page_tokens > kKvMost)
+    return fail(LW_ERR_SHAPE, "%s: page table of %d pages of %d tokens", fn, p->table_width, c->page_tokens);
+  const auto off = [](const void* x, uintptr_t n) { return reinterpret_cast<uintptr_t>(x) % n != 0; };
+  if (!p->summary || !p->start || !p->kv_len || (p->table_width && !p->page_table))
+    return fail(LW_ERR_INVALID_ARG, "%s: NULL summary, start, kv_len or page_table", fn);
+  if (off(p->summary, 16) || off(p->start, 4) || off(p->kv_len, 4) || off(p->page_table, 4))
+    return fail(LW_ERR_INVALID_ARG, "%s: an address is not aligned to its type", fn);
+  SummaryArgs a{};
+  a.p = *p;
+  a.pages = static_cast<const uint8_t*>(c->pages);
+  a.n_pages = c->n_pages;
+  a.page_bytes = (int64_t)lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens);
+  a.page_tokens = c->page_tokens;
+  a.heads = c->kv_heads;
+  a.status = d_status;
+  // CTAs of a sequence's head: what there may be to do, or what fills the device a few times over
+  const int64_t pairs = (int64_t)p->batch * c->kv_heads;
+  int64_t x = (p->table_width + kSumWarps - 1) / kSumWarps, most = 16ll * device_sm_count() / pairs;
+  if (x > most) x = most;
+  if (x < 1) x = 1;
+  const dim3 grid((unsigned)x, (unsigned)c->kv_heads, (unsigned)p->batch);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return c->head_dim == 64   ? kv_launch(fn, kv_summarise_kernel<64>, grid, 32 * kSumWarps, 0, 1, st, a)
+         : c->head_dim == 96 ? kv_launch(fn, kv_summarise_kernel<96>, grid, 32 * kSumWarps, 0, 1, st, a)
+                             : kv_launch(fn, kv_summarise_kernel<128>, grid, 32 * kSumWarps, 0, 1, st, a);
+}
+
+extern "C" size_t lw_kv_blocks_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens,
+                                               int32_t table_width, int32_t blocks) {
+  if (!c || !lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens) || q_heads < 1 || q_heads % c->kv_heads ||
+      q_tokens < 0 || q_tokens * c->kv_heads > 65535 || table_width < 0 || table_width > kMostWidth || blocks < 1 ||
+      blocks > kMostWidth)
+    return 0;
+  return block_space(c, q_heads, q_tokens, table_width, blocks).bytes;
+}
+
+extern "C" lw_status lw_kv_attention_blocks(const lw_kv_cache* c, const lw_kv_attn* p, const lw_kv_blocks* k, void* ws,
+                                            size_t ws_bytes, int32_t* d_status, void* stream) {
+  const char* fn = "lw_kv_attention_blocks";
+  clear_error();
+  lw_status s = check_kv_attention(c, p);
+  if (s != LW_OK) return s;
+  if (!k) return fail(LW_ERR_INVALID_ARG, "%s: NULL blocks", fn);
+  if (p->causal != 1 || p->window != 0) return fail(LW_ERR_UNSUPPORTED, "%s: causal attention without a window only", fn);
+  if (!(p->scale > 0.f)) return fail(LW_ERR_UNSUPPORTED, "%s: scale %g is not positive", fn, (double)p->scale);
+  if (k->blocks < 1 || k->blocks > kMostWidth || k->first < 0 || k->recent < 1 ||
+      (int64_t)k->first + k->recent > k->blocks)
+    return fail(LW_ERR_INVALID_ARG, "%s: blocks %d, first %d, recent %d", fn, k->blocks, k->first, k->recent);
+  if (p->table_width > kMostWidth) return fail(LW_ERR_SHAPE, "%s: page table of %d pages (at most %d)", fn, p->table_width, kMostWidth);
+  if (p->q_tokens * c->kv_heads > 65535)
+    return fail(LW_ERR_SHAPE, "%s: %lld query tokens of %d key/value heads", fn, (long long)p->q_tokens, c->kv_heads);
+  const int group = p->q_heads / c->kv_heads;
+  if (group > kMostGroup) return fail(LW_ERR_SHAPE, "%s: %d query heads a key/value head (at most %d)", fn, group, kMostGroup);
+  const lw_kv_cache v = by_head(c);
+  if (v.n_pages > ((1ll << 32) - 1) / c->page_tokens || v.n_pages > (1ll << 31) - 1)
+    return fail(LW_ERR_SHAPE, "%s: %lld pages of %d heads of %d tokens", fn, (long long)c->n_pages, c->kv_heads, c->page_tokens);
+  if ((int64_t)k->blocks * c->page_tokens > kKvMost)
+    return fail(LW_ERR_SHAPE, "%s: %d blocks of %d tokens", fn, k->blocks, c->page_tokens);
+  if (p->q_tokens == 0) return LW_OK;
+  if (!k->summary || (reinterpret_cast<uintptr_t>(k->summary) & 15u) || reinterpret_cast<uintptr_t>(k->chosen) % 4)
+    return fail(LW_ERR_INVALID_ARG, "%s: summary missing, or an address is not aligned to its type", fn);
+  const BlockSpace at = block_space(c, p->q_heads, p->q_tokens, p->table_width, k->blocks);
+  if (!ws || ws_bytes < at.bytes || (reinterpret_cast<uintptr_t>(ws) & 15u))
+    return fail(LW_ERR_INVALID_ARG, "%s: workspace missing, misaligned or %zu bytes of %zu", fn, ws_bytes, at.bytes);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  BlockArgs a{};
+  a.p = *p;
+  a.s = *k;
+  a.pages = reinterpret_cast<int32_t*>(w + at.pages);
+  a.lens = reinterpret_cast<int32_t*>(w + at.lens);
+  a.scores = reinterpret_cast<float*>(w + at.scores);
+  a.n_pages = c->n_pages;
+  a.page_tokens = c->page_tokens;
+  a.heads = c->kv_heads;
+  a.group = group;
+  a.status = d_status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p->table_width > k->blocks) {   // (else every page is read)
+    const dim3 grid((unsigned)((p->table_width + kScoreBlocks - 1) / kScoreBlocks), (unsigned)c->kv_heads, (unsigned)p->q_tokens);
+    s = c->head_dim == 64   ? launch_score_t<64>(a, grid, st)
+        : c->head_dim == 96 ? launch_score_t<96>(a, grid, st)
+                            : launch_score_t<128>(a, grid, st);
+    if (s != LW_OK) return s;
+  }
+  const size_t smem = (size_t)p->table_width * 4;
+  if (resident_blocks(reinterpret_cast<const void*>(kv_choose_kernel), kChoose, smem) < 1)
+    return fail(LW_ERR_CUDA, "%s: the kernel does not fit this device", fn);
+  s = kv_launch(fn, kv_choose_kernel, dim3((unsigned)c->kv_heads, (unsigned)p->q_tokens), kChoose, smem, 1, st, a);
+  if (s != LW_OK) return s;
+  lw_kv_attn one = *p;
+  one.q_start = nullptr;
+  one.kv_len = a.lens;
+  one.page_table = a.pages;
+  one.table_stride = one.table_width = k->blocks;
+  one.q_tokens = p->q_tokens * c->kv_heads;
+  one.batch = (int32_t)one.q_tokens;
+  one.q_heads = group;
+  one.max_q = 1;
+  return launch_kv_attention(&v, &one, c->kv_heads, ws, d_status, st);
+}

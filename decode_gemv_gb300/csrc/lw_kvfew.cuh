@@ -197,7 +197,7 @@ struct FewWarp {
     const bool live = r < w.T * a.group;
     const int t = live ? r / a.group : w.T - 1;
     if (live) {
-      const int64_t at = (int64_t)(q0 + t) * a.p.q_token_stride +
+      const int64_t at = kv_token_at(a, q0 + t, a.p.q_token_stride, a.p.q_head_stride) +
                          (int64_t)(w.h * a.group + r - t * a.group) * a.p.q_head_stride + 8 * q;
 #pragma unroll
       for (int g = 0; g < G; ++g) load_q8(a, at + 32 * g, x[g]);
@@ -616,7 +616,7 @@ __device__ __forceinline__ void few_out(const AttnArgs& a, const KvWalk& w, int 
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = l == 0.f ? 0.f : f[i] * inv;
-  store4(a, (int64_t)(q0 + t) * a.p.out_token_stride + (int64_t)hq * a.p.out_head_stride + d, f);
+  store4(a, kv_token_at(a, q0 + t, a.p.out_token_stride, a.p.out_head_stride) + (int64_t)hq * a.p.out_head_stride + d, f);
   if (d == 0 && a.p.lse)
     a.p.lse[(int64_t)(q0 + t) * a.p.q_heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }

@@ -23,7 +23,7 @@ LW_FMT_Q4_PAIR, LW_FMT_Q6, LW_FMT_BF16_EXP = 1, 2, 3
 # device status codes (*d_status), as in include/lw.h
 (LW_DEV_OK, LW_DEV_LANE_LENGTH, LW_DEV_BAD_CODE, LW_DEV_TILE_SIZE, LW_DEV_TIMEOUT,
  LW_DEV_BAD_TABLE, LW_DEV_BAD_STRIPS, LW_DEV_BAD_SLOT, LW_DEV_BAD_PAGE,
- LW_DEV_BAD_SEQ) = range(10)
+ LW_DEV_BAD_SEQ, LW_DEV_BAD_POSITION) = range(11)
 (LW_OK, LW_ERR_INVALID_ARG, LW_ERR_SHAPE, LW_ERR_UNSUPPORTED, LW_ERR_ALLOC, LW_ERR_CORRUPT,
  LW_ERR_CUDA, LW_ERR_IO) = range(8)
 SECTION_NAMES = ["words", "tile_off", "lane_bits", "table", "qparams", "signman",
@@ -31,7 +31,8 @@ SECTION_NAMES = ["words", "tile_off", "lane_bits", "table", "qparams", "signman"
 STATUS_NAMES = {0: "LW_OK", 1: "LW_ERR_INVALID_ARG", 2: "LW_ERR_SHAPE", 3: "LW_ERR_UNSUPPORTED",
                 4: "LW_ERR_ALLOC", 5: "LW_ERR_CORRUPT", 6: "LW_ERR_CUDA", 7: "LW_ERR_IO"}
 DEV_STATUS = {0: "ok", 1: "lane length", 2: "bad code", 3: "tile size", 4: "timeout",
-              5: "bad table", 6: "bad strips", 7: "bad slot", 8: "bad page", 9: "bad sequence"}
+              5: "bad table", 6: "bad strips", 7: "bad slot", 8: "bad page", 9: "bad sequence",
+              10: "bad position"}
 TABLE_BYTES = 1024
 EXPORTED = ["lw_encode_bundle", "lw_bundle_sections", "lw_bundle_free", "lw_table_from_lengths",
             "lw_validate_sections", "lw_workspace_bytes", "lw_decode", "lw_decode_gemv",
@@ -43,9 +44,13 @@ EXPORTED = ["lw_encode_bundle", "lw_bundle_sections", "lw_bundle_free", "lw_tabl
             "lw_twin_tile_rows", "lw_decode_gemm_strips", "lw_graph_begin", "lw_graph_end",
             "lw_graph_launch", "lw_graph_free", "lw_decode_gemm_group", "lw_twin_gemm_group",
             "lw_table_lut_entries", "lw_test_stall_next", "lw_kv_tile_bytes", "lw_kv_page_bytes",
-            "lw_kv_write", "lw_kv_read", "lw_kv_workspace_bytes", "lw_kv_attention"]
+            "lw_kv_write", "lw_kv_read", "lw_kv_workspace_bytes", "lw_kv_attention",
+            "lw_rotary_table", "lw_kv_write_rotary", "lw_kv_weigh_workspace_bytes", "lw_kv_weigh",
+            "lw_kv_evict", "lw_kv_summary_bytes", "lw_kv_summarise",
+            "lw_kv_blocks_workspace_bytes", "lw_kv_attention_blocks"]
 LW_F32, LW_F16, LW_BF16 = 0, 1, 2
 LW_KV_GROUP, LW_KV_TILE, LW_KV_LIMIT = 32, 16, 61440.0
+(LW_ROTARY_PLAIN, LW_ROTARY_LINEAR, LW_ROTARY_NTK, LW_ROTARY_BANDS, LW_ROTARY_YARN) = range(5)
 
 
 class LwError(RuntimeError):
@@ -93,6 +98,12 @@ class LwKvCache(ctypes.Structure):
 
 _KV_ROWS = struct.Struct("@Pqqii")                    # lw_kv_rows
 _KV_ATTN = struct.Struct("@PqqPqqPPPPqqiiiiiiif")      # lw_kv_attn
+_ROTARY = struct.Struct("@iidddddd")                  # lw_rotary
+_KV_ROTATED = struct.Struct("@PqqiiPqqiiPqqiiPqqiiPPPqqiiii")   # lw_kv_rotated
+_KV_WEIGHTS = struct.Struct("@PqqPPPPqqPqqPqqqiiiiiiif")        # lw_kv_weights
+_KV_EVICTION = struct.Struct("@PqqqPPqPqPPqqqPiiiiii")          # lw_kv_eviction
+_KV_SUMMARIES = struct.Struct("@PPPPqii")             # lw_kv_summaries
+_KV_BLOCKS = struct.Struct("@PPiiii")                 # lw_kv_blocks
 
 
 _lib = None
@@ -151,6 +162,15 @@ def load():
         "lw_kv_read": ([P, P, i64, P, P, P, P], i32),
         "lw_kv_workspace_bytes": ([P, i32, i64, i32], sz),
         "lw_kv_attention": ([P, P, P, sz, P, P], i32),
+        "lw_rotary_table": ([P, i64, i64, P, P], i32),
+        "lw_kv_write_rotary": ([P, P, P, P], i32),
+        "lw_kv_weigh_workspace_bytes": ([P, i32, i64], sz),
+        "lw_kv_weigh": ([P, P, P, sz, P, P], i32),
+        "lw_kv_evict": ([P, P, P, P], i32),
+        "lw_kv_summary_bytes": ([P], sz),
+        "lw_kv_summarise": ([P, P, P, P], i32),
+        "lw_kv_blocks_workspace_bytes": ([P, i32, i64, i32, i32], sz),
+        "lw_kv_attention_blocks": ([P, P, P, P, sz, P, P], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -1004,3 +1024,463 @@ def lw_kv_attention(cache: KvCache, q, q_start, kv_len, page_table, out, ws, d_s
                              _raw_stream(cache.index) if stream is None else stream.cuda_stream)
     if r:
         raise LwError(r, "lw_kv_attention")
+
+
+# ---- rotary positions --------------------------------------------------------
+
+def lw_rotary_table(table, *, first: int = 0, base: float = 10000.0, scaling: int = LW_ROTARY_PLAIN,
+                    factor: float = 1.0, old_length: float = 0.0, low: float = 0.0, high: float = 0.0,
+                    gain: float = 0.0, stream=None) -> None:
+    """Fill table float32 [positions, rot] with the cosines and sines of positions first,
+    first + 1, ...: what lw_kv_write_rotary rotates by."""
+    import torch
+    fn = "lw_rotary_table"
+    _kv_torch(torch)
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.float32 or table.dim() != 2 or \
+            not table.is_contiguous():
+        _refuse(fn, "table: expected a contiguous float32 tensor [positions, rot]")
+    if table.get_device() < 0 or table.get_device() != _current_device():
+        _refuse(fn, f"table: on {table.device}, expected the current CUDA device")
+    try:
+        a = _ROTARY.pack(table.shape[1], scaling, base, factor, old_length, low, high, gain)
+    except struct.error as e:
+        _refuse(fn, f"rot {table.shape[1]}, scaling {scaling!r}: {e}")
+    r = load().lw_rotary_table(a, first, table.shape[0], table.data_ptr(),
+                               _raw_stream(table.get_device()) if stream is None else stream.cuda_stream)
+    if r:
+        raise LwError(r, fn)
+
+
+def _kv_beside(a, b) -> bool:
+    """Whether the rows [tokens][heads][dim] of `a` and `b` (one type, the last dimension contiguous; as many
+    tokens, any heads) share no byte."""
+    (n, ha, d), (_, hb, e) = a.shape, b.shape
+    if n == 0 or ha == 0 or hb == 0:
+        return True
+    if ha == hb and d == e:
+        return _kv_apart(a, b)
+    size, at, bt = a.element_size(), a.data_ptr(), b.data_ptr()
+    (sa, ga, _), (sb, gb, _) = a.stride(), b.stride()
+    heads_a, heads_b = ((ha - 1) * ga + d) * size, ((hb - 1) * gb + e) * size   # of a token
+    if at + (n - 1) * sa * size + heads_a <= bt or bt + (n - 1) * sb * size + heads_b <= at:
+        return True
+    if sa == sb and sa > 0:   # interleaved in one buffer, token by token
+        apart = (bt - at) % (sa * size)
+        if heads_a <= apart and apart + heads_b <= sa * size:
+            return True
+    rows = [(p + size * (np.arange(n)[:, None] * t + np.arange(h) * g)).ravel()
+            for p, t, h, g in ((at, sa, ha, ga), (bt, sb, hb, gb))]
+    start = np.concatenate(rows)
+    end = start + np.repeat([d * size, e * size], [len(rows[0]), len(rows[1])])
+    order = np.argsort(start, kind="stable")
+    return bool((start[order][1:] >= end[order][:-1]).all())
+
+
+def _kv_same_rows(a, b) -> bool:
+    return a.data_ptr() == b.data_ptr() and a.stride() == b.stride()
+
+
+def _kv_rotary_refuse(fn, cache, k, v, slots, positions, table, d_status, q, q_out):
+    import torch
+    _kv_index(fn, "slots", slots, _I64, None)
+    n = slots.shape[0]
+    _kv_index(fn, "positions", positions, _I64, n)
+    for name, t in (("k", k), ("v", v)):
+        _kv_heads(fn, name, t, n, cache.kv_heads, cache.head_dim)
+    if k.dtype != v.dtype:
+        _refuse(fn, f"v: dtype {v.dtype}, k has {k.dtype}")
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.float32 or table.dim() != 2 or \
+            not table.is_contiguous():
+        _refuse(fn, "table: expected a contiguous float32 tensor [positions, rot]")
+    named = (("slots", slots), ("positions", positions), ("k", k), ("v", v), ("table", table),
+             ("d_status", d_status))
+    if (q is None) != (q_out is None):
+        _refuse(fn, "q and q_out come together")
+    if q is not None:
+        heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        if isinstance(q, torch.Tensor) and heads < 1:
+            _refuse(fn, f"q: shape {list(q.shape)}, expected [{n}, heads, {cache.head_dim}]")
+        _kv_heads(fn, "q", q, n, heads, cache.head_dim)
+        _kv_heads(fn, "q_out", q_out, n, heads, cache.head_dim, True)
+        if q.dtype != k.dtype or q_out.dtype != q.dtype:
+            _refuse(fn, f"q, q_out: dtypes {q.dtype}, {q_out.dtype}, k has {k.dtype}")
+        if not (_kv_same_rows(q, q_out) or _kv_apart(q, q_out)):
+            _refuse(fn, "q_out: rows that are written overlap q's (it may be q itself)")
+        for name, t in (("k", k), ("v", v)):
+            if not _kv_beside(q_out, t):
+                _refuse(fn, f"q_out: rows that are written overlap {name}'s")
+        named += (("q", q), ("q_out", q_out))
+    _status_ptr(fn, d_status)
+    _kv_on(fn, cache, *named)
+
+
+def lw_kv_write_rotary(cache: KvCache, k, v, slots, positions, table, d_status, *, q=None, q_out=None,
+                       interleaved: bool = False, stream=None) -> None:
+    """lw_kv_write of keys rotated by their tokens' positions int64 [n], and the queries
+    q [n, q_heads, head_dim] of the same tokens rotated into q_out (which may be q).  table float32
+    [positions, rot] (lw_rotary_table): the first rot elements of a head are rotated, in pairs of
+    neighbours (interleaved) or of elements rot / 2 apart."""
+    dev = cache.index
+    try:
+        n = slots.shape[0]
+        shape = (n, cache.kv_heads, cache.head_dim)
+        code, (kt, kh, kd), (vt, vh, vd) = _KV_TYPES.get(k.dtype), k.stride(), v.stride()
+        rows, rot = table.shape
+        ok = (code is not None and v.dtype is k.dtype and k.shape == shape and v.shape == shape
+              and kd == 1 and vd == 1 and slots.dtype is _I64 and slots.dim() == 1
+              and slots.is_contiguous() and positions.dtype is _I64 and positions.shape == (n,)
+              and positions.is_contiguous() and table.dtype is _F32 and table.is_contiguous()
+              and d_status.dtype is _I32 and d_status.numel() >= 1 and d_status.is_contiguous()
+              and dev >= 0 and _current_device() == dev and k.get_device() == dev
+              and v.get_device() == dev and slots.get_device() == dev
+              and positions.get_device() == dev and table.get_device() == dev
+              and d_status.get_device() == dev)
+        if q is None:
+            ok = ok and q_out is None
+            qp = op = heads = qt = qh = ot = oh = 0
+        else:
+            heads = q.shape[1]
+            qp, op, (qt, qh, qd), (ot, oh, od) = q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
+            ok = (ok and q.dtype is k.dtype and q_out.dtype is k.dtype and heads > 0
+                  and q.shape == (n, heads, cache.head_dim) and q_out.shape == q.shape and qd == 1
+                  and od == 1 and _kv_distinct(q_out) and q.get_device() == dev
+                  and q_out.get_device() == dev
+                  and ((qp == op and qt == ot and qh == oh) or _kv_apart(q, q_out))
+                  and _kv_beside(q_out, k) and _kv_beside(q_out, v))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _kv_rotary_refuse("lw_kv_write_rotary", cache, k, v, slots, positions, table, d_status, q, q_out)
+        n, (rows, rot) = slots.shape[0], table.shape
+        code, (kt, kh, kd), (vt, vh, vd) = _KV_TYPES[k.dtype], k.stride(), v.stride()
+        qp = op = heads = qt = qh = ot = oh = 0
+        if q is not None:
+            heads = q.shape[1]
+            qp, op, (qt, qh, qd), (ot, oh, od) = q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
+    a = _KV_ROTATED.pack(k.data_ptr(), kt, kh, code, 0, v.data_ptr(), vt, vh, code, 0, qp, qt, qh, code, 0,
+                         op, ot, oh, code, 0, slots.data_ptr(), positions.data_ptr(), table.data_ptr(),
+                         rows, n, heads, rot, 1 if interleaved else 0, 0)
+    r = _lib.lw_kv_write_rotary(cache.ref, a, d_status.data_ptr(),
+                                _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if r:
+        raise LwError(r, "lw_kv_write_rotary")
+
+
+# ---- eviction by accumulated attention weight ----------------------------------
+
+def _kv_weight_rows(fn, name, t, batch, heads, keys, written):
+    """Refuse anything but rows of weights float32 [batch, kv_heads, keys]."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+        _refuse(fn, f"{name}: expected a float32 tensor")
+    if t.dim() != 3 or t.shape[0] != batch or t.shape[1] != heads or (keys is not None and t.shape[2] != keys):
+        _refuse(fn, f"{name}: shape {list(t.shape)}, expected "
+                    f"[{batch}, {heads}, {'keys' if keys is None else keys}]")
+    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+        _refuse(fn, f"{name}: the last dimension is strided")
+    if written and not _kv_distinct(t):
+        _refuse(fn, f"{name}: rows that are written overlap")
+
+
+def _kv_table(fn, name, t, batch):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        _refuse(fn, f"{name}: expected an int32 tensor")
+    if t.dim() != 2 or t.shape[0] != batch or (t.shape[1] > 1 and t.stride(1) != 1):
+        _refuse(fn, f"{name}: expected [{batch}, pages] with contiguous rows")
+
+
+def _kv_clear(a, b) -> bool:
+    """Whether the weights `b`, written, are `a` itself, entry for entry, or share no byte with it."""
+    if a.data_ptr() == b.data_ptr() and a.stride()[:2] == b.stride()[:2]:
+        return True
+    def end(t):
+        return t.data_ptr() + 4 * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+    return a.numel() == 0 or b.numel() == 0 or end(a) <= b.data_ptr() or end(b) <= a.data_ptr()
+
+
+def lw_kv_weigh_workspace_bytes(cache: KvCache, q_heads: int, q_tokens: int) -> int:
+    return int(load().lw_kv_weigh_workspace_bytes(cache.ref, q_heads, q_tokens))
+
+
+def _kv_weigh_refuse(cache, q, lse, q_start, kv_len, page_table, weights, ws, d_status, max_q, add_to):
+    import operator
+    import torch
+    fn = "lw_kv_weigh"
+    try:
+        operator.index(max_q)
+    except TypeError:
+        _refuse(fn, f"max_q: expected a whole number, got {max_q!r}")
+    heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    if isinstance(q, torch.Tensor) and (heads < 1 or heads % cache.kv_heads):
+        _refuse(fn, f"q: shape {list(q.shape)}, expected [tokens, a multiple of {cache.kv_heads}, "
+                    f"{cache.head_dim}]")
+    _kv_heads(fn, "q", q, None, heads, cache.head_dim)
+    _kv_index(fn, "kv_len", kv_len, _I32, None)
+    batch = kv_len.shape[0]
+    _kv_index(fn, "q_start", q_start, _I32, batch + 1)
+    _kv_table(fn, "page_table", page_table, batch)
+    _buf(fn, "lse", lse, 4 * q.shape[0] * heads, (torch.float32,))
+    _kv_weight_rows(fn, "weights", weights, batch, cache.kv_heads, None, True)
+    named = (("q", q), ("lse", lse), ("q_start", q_start), ("kv_len", kv_len), ("page_table", page_table),
+             ("weights", weights), ("ws", ws), ("d_status", d_status))
+    if add_to is not None:
+        _kv_weight_rows(fn, "add_to", add_to, batch, cache.kv_heads, weights.shape[2], False)
+        if not _kv_clear(add_to, weights):
+            _refuse(fn, "add_to: overlaps weights (it may be weights itself)")
+        named += (("add_to", add_to),)
+    _ws_ptr(fn, ws)
+    _status_ptr(fn, d_status)
+    _kv_on(fn, cache, *named)
+
+
+def lw_kv_weigh(cache: KvCache, q, lse, q_start, kv_len, page_table, weights, ws, d_status, *, max_q: int,
+                add_to=None, scale=None, causal: bool = True, window: int = 0, stream=None) -> None:
+    """The softmax weight that each cached key was given, summed over the query tokens and the query
+    heads of its key/value head: weights float32 [batch, kv_heads, keys] = add_to (none, or weights
+    itself to go on summing) + those sums.  The other arguments as lw_kv_attention had them, lse
+    [tokens, q_heads] as it left it."""
+    dev = cache.index
+    try:
+        tokens, heads, dim = q.shape
+        code, (qt, qh, qd) = _KV_TYPES.get(q.dtype), q.stride()
+        batch, width = page_table.shape
+        ts, td = page_table.stride()
+        shape, (wb, wh, wd) = weights.shape, weights.stride()
+        keys = shape[2]
+        ap = ab = ah = 0
+        ok = (code is not None and dim == cache.head_dim and heads % cache.kv_heads == 0 and heads > 0
+              and qd == 1 and shape == (batch, cache.kv_heads, keys) and weights.dtype is _F32
+              and (wd == 1 or keys <= 1) and _kv_distinct(weights)
+              and lse.dtype is _F32 and lse.is_contiguous() and lse.numel() >= tokens * heads
+              and q_start.dtype is _I32 and q_start.shape == (batch + 1,) and q_start.is_contiguous()
+              and kv_len.dtype is _I32 and kv_len.shape == (batch,) and kv_len.is_contiguous()
+              and page_table.dtype is _I32 and (td == 1 or width <= 1)
+              and ws.is_contiguous() and d_status.dtype is _I32 and d_status.numel() >= 1
+              and d_status.is_contiguous() and type(max_q) is int and dev >= 0 and _current_device() == dev
+              and q.get_device() == dev and lse.get_device() == dev and q_start.get_device() == dev
+              and kv_len.get_device() == dev and page_table.get_device() == dev
+              and weights.get_device() == dev and ws.get_device() == dev and d_status.get_device() == dev)
+        if add_to is not None:
+            ap, (ab, ah, ad) = add_to.data_ptr(), add_to.stride()
+            ok = (ok and add_to.dtype is _F32 and add_to.shape == shape and (ad == 1 or keys <= 1)
+                  and add_to.get_device() == dev and _kv_clear(add_to, weights))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        _kv_weigh_refuse(cache, q, lse, q_start, kv_len, page_table, weights, ws, d_status, max_q, add_to)
+        tokens, heads, dim = q.shape
+        code, (qt, qh, qd) = _KV_TYPES[q.dtype], q.stride()
+        batch, width = page_table.shape
+        ts, td = page_table.stride()
+        keys, (wb, wh, wd) = weights.shape[2], weights.stride()
+        ap, (ab, ah, ad) = (0, (0, 0, 0)) if add_to is None else (add_to.data_ptr(), add_to.stride())
+    try:
+        a = _KV_WEIGHTS.pack(q.data_ptr(), qt, qh, lse.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                             page_table.data_ptr(), ts, tokens, ap, ab, ah, weights.data_ptr(), wb, wh, keys,
+                             width, code, batch, heads, max_q, 1 if causal else 0, window,
+                             dim ** -0.5 if scale is None else scale)
+    except struct.error as e:
+        _refuse("lw_kv_weigh", f"max_q {max_q!r}, window {window!r}, scale {scale!r}: {e}")
+    r = _lib.lw_kv_weigh(cache.ref, a, ws.data_ptr(), ws.numel() * ws.element_size(), d_status.data_ptr(),
+                         _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if r:
+        raise LwError(r, "lw_kv_weigh")
+
+
+def _kv_whole(fn, **named):
+    import operator
+    for name, x in named.items():
+        try:
+            operator.index(x)
+        except TypeError:
+            _refuse(fn, f"{name}: expected a whole number, got {x!r}")
+
+
+def lw_kv_evict(cache: KvCache, weights, kv_len, page_table, out_table, out_len, out_weights, kept, d_status, *,
+                keep: int, first: int = 0, recent: int = 0, stream=None) -> None:
+    """Keep at most `keep` keys of each head of a sequence: the first `first`, the last `recent`, and
+    of the others those of the largest weights float32 [batch, kv_heads, keys].  They move together to the
+    front of out_table's pages (page_table itself, or other pages); kept int32 [batch, kv_heads, keep]
+    lists them (-1: none), out_len int32 [batch] says how many there are, out_weights (None, weights
+    itself, or other rows of at least `keep`) gets their weights."""
+    import torch
+    fn = "lw_kv_evict"
+    _kv_whole(fn, keep=keep, first=first, recent=recent)
+    _kv_index(fn, "kv_len", kv_len, _I32, None)
+    batch, heads = kv_len.shape[0], cache.kv_heads
+    _kv_index(fn, "out_len", out_len, _I32, batch)
+    _kv_table(fn, "page_table", page_table, batch)
+    _kv_table(fn, "out_table", out_table, batch)
+    _kv_weight_rows(fn, "weights", weights, batch, heads, None, False)
+    named = (("weights", weights), ("kv_len", kv_len), ("page_table", page_table), ("out_table", out_table),
+             ("out_len", out_len), ("kept", kept), ("d_status", d_status))
+    if not isinstance(kept, torch.Tensor) or kept.dtype != torch.int32 or not kept.is_contiguous() or \
+            tuple(kept.shape) != (batch, heads, keep):
+        _refuse(fn, f"kept: expected a contiguous int32 tensor [{batch}, {heads}, {keep}]")
+    if batch and abs(out_len.data_ptr() - kv_len.data_ptr()) < 4 * batch:
+        _refuse(fn, "out_len: overlaps kv_len")
+    op = ob = oh = on = 0
+    if out_weights is not None:
+        _kv_weight_rows(fn, "out_weights", out_weights, batch, heads, None, True)
+        if not _kv_clear(weights, out_weights):
+            _refuse(fn, "out_weights: overlaps weights (it may be weights itself)")
+        op, (ob, oh, _), on = out_weights.data_ptr(), out_weights.stride(), out_weights.shape[2]
+        named += (("out_weights", out_weights),)
+    _status_ptr(fn, d_status)
+    _kv_on(fn, cache, *named)
+    wb, wh, _ = weights.stride()
+    try:
+        a = _KV_EVICTION.pack(weights.data_ptr(), wb, wh, weights.shape[2], kv_len.data_ptr(),
+                              page_table.data_ptr(), page_table.stride(0), out_table.data_ptr(),
+                              out_table.stride(0), out_len.data_ptr(), op, ob, oh, on, kept.data_ptr(),
+                              page_table.shape[1], out_table.shape[1], batch, keep, first, recent)
+    except struct.error as e:
+        _refuse(fn, f"keep {keep!r}, first {first!r}, recent {recent!r}: {e}")
+    r = load().lw_kv_evict(cache.ref, a, d_status.data_ptr(),
+                           _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    if r:
+        raise LwError(r, fn)
+
+
+# ---- sparse attention ----------------------------------------------------------
+
+def lw_kv_summary_bytes(cache: KvCache) -> int:
+    return int(load().lw_kv_summary_bytes(cache.ref))
+
+
+def _kv_summary(fn, cache, summary):
+    _buf(fn, "summary", summary, lw_kv_summary_bytes(cache))
+
+
+def lw_kv_summarise(cache: KvCache, summary, start, kv_len, page_table, d_status, stream=None) -> None:
+    """Bring the summaries of the pages that hold tokens start[b] .. kv_len[b] - 1 up to date: summary is
+    memory of lw_kv_summary_bytes(cache) bytes, start and kv_len int32 [batch]."""
+    dev = cache.index
+    try:
+        batch, width = page_table.shape
+        ts, td = page_table.stride()
+        ok = (start.dtype is _I32 and start.shape == (batch,) and start.is_contiguous()
+              and kv_len.dtype is _I32 and kv_len.shape == (batch,) and kv_len.is_contiguous()
+              and page_table.dtype is _I32 and (td == 1 or width <= 1) and summary.is_contiguous()
+              and summary.numel() * summary.element_size() >= lw_kv_summary_bytes(cache)
+              and d_status.dtype is _I32 and d_status.numel() >= 1 and d_status.is_contiguous()
+              and dev >= 0 and _current_device() == dev and summary.get_device() == dev
+              and start.get_device() == dev and kv_len.get_device() == dev
+              and page_table.get_device() == dev and d_status.get_device() == dev)
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    fn = "lw_kv_summarise"
+    if not ok:
+        _kv_index(fn, "kv_len", kv_len, _I32, None)
+        batch = kv_len.shape[0]
+        _kv_index(fn, "start", start, _I32, batch)
+        _kv_table(fn, "page_table", page_table, batch)
+        _kv_summary(fn, cache, summary)
+        _status_ptr(fn, d_status)
+        _kv_on(fn, cache, ("summary", summary), ("start", start), ("kv_len", kv_len),
+               ("page_table", page_table), ("d_status", d_status))
+        width, ts = page_table.shape[1], page_table.stride(0)
+    a = _KV_SUMMARIES.pack(summary.data_ptr(), start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), ts,
+                           width, batch)
+    r = _lib.lw_kv_summarise(cache.ref, a, d_status.data_ptr(),
+                             _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if r:
+        raise LwError(r, fn)
+
+
+def lw_kv_blocks_workspace_bytes(cache: KvCache, q_heads: int, q_tokens: int, table_width: int, blocks: int) -> int:
+    if cache.index >= 0 and _current_device() != cache.index:   # (sized by the current device)
+        _kv_on("lw_kv_blocks_workspace_bytes", cache)
+    return int(load().lw_kv_blocks_workspace_bytes(cache.ref, q_heads, q_tokens, table_width, blocks))
+
+
+def _kv_blocks_refuse(cache, summary, q, q_start, kv_len, page_table, out, ws, d_status, blocks, first, recent,
+                      lse, chosen):
+    import torch
+    fn = "lw_kv_attention_blocks"
+    _kv_whole(fn, blocks=blocks, first=first, recent=recent)
+    heads = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    if isinstance(q, torch.Tensor) and (heads < 1 or heads % cache.kv_heads):
+        _refuse(fn, f"q: shape {list(q.shape)}, expected [tokens, a multiple of {cache.kv_heads}, "
+                    f"{cache.head_dim}]")
+    _kv_heads(fn, "q", q, None, heads, cache.head_dim)
+    _kv_heads(fn, "out", out, q.shape[0], heads, cache.head_dim, True)
+    if out.dtype != q.dtype:
+        _refuse(fn, f"out: dtype {out.dtype}, q has {q.dtype}")
+    _kv_index(fn, "kv_len", kv_len, _I32, None)
+    batch = kv_len.shape[0]
+    _kv_index(fn, "q_start", q_start, _I32, batch + 1)
+    _kv_table(fn, "page_table", page_table, batch)
+    _kv_summary(fn, cache, summary)
+    named = (("summary", summary), ("q", q), ("out", out), ("q_start", q_start), ("kv_len", kv_len),
+             ("page_table", page_table), ("ws", ws), ("d_status", d_status))
+    if lse is not None:
+        _buf(fn, "lse", lse, 4 * q.shape[0] * heads, (torch.float32,))
+        named += (("lse", lse),)
+    if chosen is not None:
+        want = (q.shape[0], cache.kv_heads, blocks)
+        if not isinstance(chosen, torch.Tensor) or chosen.dtype != torch.int32 or \
+                not chosen.is_contiguous() or tuple(chosen.shape) != want:
+            _refuse(fn, f"chosen: expected a contiguous int32 tensor {list(want)}")
+        named += (("chosen", chosen),)
+    _ws_ptr(fn, ws)
+    _status_ptr(fn, d_status)
+    _kv_on(fn, cache, *named)
+
+
+def lw_kv_attention_blocks(cache: KvCache, summary, q, q_start, kv_len, page_table, out, ws, d_status, *,
+                           blocks: int, first: int = 1, recent: int = 1, scale=None, lse=None, chosen=None,
+                           stream=None) -> None:
+    """lw_kv_attention (causal) in which every query token and key/value head reads at most `blocks` pages:
+    the first `first`, the last `recent`, and those that score highest against `summary`
+    (lw_kv_summarise).  chosen int32 [tokens, kv_heads, blocks]: the pages' places in the page table, -1
+    where there are fewer.  ws: lw_kv_blocks_workspace_bytes, zeroed once."""
+    dev = cache.index
+    try:
+        tokens, heads, dim = shape = q.shape
+        code, (qt, qh, qd), (ot, oh, od) = _KV_TYPES.get(q.dtype), q.stride(), out.stride()
+        batch, width = page_table.shape
+        ts, td = page_table.stride()
+        ok = (code is not None and out.dtype is q.dtype and out.shape == shape
+              and dim == cache.head_dim and heads % cache.kv_heads == 0 and qd == 1 and od == 1
+              and heads > 0 and (out.is_contiguous() or _kv_distinct(out))
+              and q_start.dtype is _I32 and q_start.shape == (batch + 1,) and q_start.is_contiguous()
+              and kv_len.dtype is _I32 and kv_len.shape == (batch,) and kv_len.is_contiguous()
+              and page_table.dtype is _I32 and (td == 1 or width <= 1) and summary.is_contiguous()
+              and summary.numel() * summary.element_size() >= lw_kv_summary_bytes(cache)
+              and ws.is_contiguous() and d_status.dtype is _I32 and d_status.numel() >= 1
+              and d_status.is_contiguous() and type(blocks) is int and type(first) is int
+              and type(recent) is int and dev >= 0 and _current_device() == dev
+              and q.get_device() == dev and out.get_device() == dev and q_start.get_device() == dev
+              and kv_len.get_device() == dev and page_table.get_device() == dev
+              and summary.get_device() == dev and ws.get_device() == dev and d_status.get_device() == dev
+              and (lse is None or (lse.dtype is _F32 and lse.is_contiguous()
+                                   and lse.numel() >= tokens * heads and lse.get_device() == dev))
+              and (chosen is None or (chosen.dtype is _I32 and chosen.is_contiguous()
+                                      and chosen.shape == (tokens, cache.kv_heads, blocks)
+                                      and chosen.get_device() == dev)))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    fn = "lw_kv_attention_blocks"
+    if not ok:
+        _kv_blocks_refuse(cache, summary, q, q_start, kv_len, page_table, out, ws, d_status, blocks, first,
+                          recent, lse, chosen)
+        tokens, heads, dim = q.shape
+        code, (qt, qh, qd), (ot, oh, od) = _KV_TYPES[q.dtype], q.stride(), out.stride()
+        batch, width = page_table.shape
+        ts, td = page_table.stride()
+    try:
+        a = _KV_ATTN.pack(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
+                          0 if lse is None else lse.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                          page_table.data_ptr(), ts, tokens, width, code, batch, heads, 1, 1, 0,
+                          dim ** -0.5 if scale is None else scale)
+        b = _KV_BLOCKS.pack(summary.data_ptr(), 0 if chosen is None else chosen.data_ptr(), blocks, first,
+                            recent, 0)
+    except struct.error as e:
+        _refuse(fn, f"blocks {blocks!r}, first {first!r}, recent {recent!r}, scale {scale!r}: {e}")
+    r = _lib.lw_kv_attention_blocks(cache.ref, a, b, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                    d_status.data_ptr(),
+                                    _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if r:
+        raise LwError(r, fn)

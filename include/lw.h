@@ -88,9 +88,10 @@ enum {
   LW_DEV_BAD_SLOT = 7,      /* a cache slot past the last page (token skipped) */
   LW_DEV_BAD_PAGE = 8,      /* a page-table entry outside the cache under keys
                                the call needs (those keys are left out) */
-  LW_DEV_BAD_SEQ = 9        /* q_start not ascending within [0, q_tokens] (the
+  LW_DEV_BAD_SEQ = 9,       /* q_start not ascending within [0, q_tokens] (the
                                sequence is skipped), or kv_len negative or past
                                the page table (clamped) */
+  LW_DEV_BAD_POSITION = 10  /* a position past the rotary table (token skipped) */
 };
 
 typedef enum {
@@ -571,7 +572,7 @@ int32_t lw_table_lut_entries(const lw_table* t);
  * multiple of 16 up to 2^20, kv_heads at most 65535, pages 16-byte aligned;
  * n_pages * page_tokens < 2^32 (else LW_ERR_SHAPE).
  *
- * The three calls are asynchronous on `stream`, allocate nothing and can be
+ * The lw_kv_* calls are asynchronous on `stream`, allocate nothing and can be
  * captured; each reads and writes nothing before the work queued in front of it
  * has completed.  They launch on the current device, which has to be the one of
  * the stream and of every address.  d_status may be NULL.  Errors: LW_ERR_INVALID_ARG (a missing or
@@ -683,6 +684,207 @@ size_t lw_kv_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_to
 
 lw_status lw_kv_attention(const lw_kv_cache* c, const lw_kv_attn* a, void* ws, size_t ws_bytes,
                           int32_t* d_status, void* stream);
+
+/*
+ * Rotary positions.  A table row holds, for one position p, the cosines of the
+ * rot / 2 pairs' angles p f_i and then their sines, each times a gain, in fp32
+ * (computed in fp64).  With the plain frequencies f_i = base^(-2 i / rot):
+ *   LW_ROTARY_PLAIN    f_i
+ *   LW_ROTARY_LINEAR   f_i / factor (positions interpolated)
+ *   LW_ROTARY_NTK      the plain ones of base factor^(rot / (rot - 2)) (rot > 2)
+ *   LW_ROTARY_BANDS    f_i (k + (1 - k) / factor), k = clamp((t - low) / (high -
+ *                      low), 0, 1), t = old_length f_i / (2 pi) the turns in the
+ *                      old length: long waves stretched, short ones kept
+ *   LW_ROTARY_YARN     f_i (k + (1 - k) / factor), k = 1 - clamp((i - a) /
+ *                      max(b - a, 0.001), 0, 1), a and b the pairs (rounded down and
+ *                      up, within 0 .. rot - 1) that make `high` and `low` turns in
+ *                      the old length: rot log(old_length / (2 pi turns)) / (2 log base)
+ * low, high: 0 for 1 and 4 (bands), 1 and 32 (YaRN).  gain: 0 for 1, and for
+ * 0.1 log(factor) + 1 with YaRN.  rot is even, 2..128; base > 1, factor > 0
+ * (not read by LW_ROTARY_PLAIN), old_length > 0 and high > low for the last two.
+ */
+typedef enum {
+  LW_ROTARY_PLAIN = 0, LW_ROTARY_LINEAR = 1, LW_ROTARY_NTK = 2, LW_ROTARY_BANDS = 3, LW_ROTARY_YARN = 4
+} lw_rotary_scaling;
+
+typedef struct {
+  int32_t rot;
+  int32_t scaling;   /* lw_rotary_scaling */
+  double base, factor, old_length, low, high, gain;
+} lw_rotary;
+
+/* Rows `first` .. `first + n - 1` into device memory [n][rot]; positions are 0 ..
+   2^31 - 1.  Asynchronous on `stream`, allocates nothing. */
+lw_status lw_rotary_table(const lw_rotary* r, int64_t first, int64_t n, float* table, void* stream);
+
+/*
+ * lw_kv_write with rotary positions: the keys are rotated on their way into the
+ * cache, and the queries of the same tokens as they pass.  Token i stands at
+ * positions[i]; with c, s the table's row there, a pair (x, y) of a head becomes
+ *   (fl(fl(x c) - fl(y s)), fl(fl(y c) + fl(x s)))        in fp32,
+ * pair j being elements 2 j, 2 j + 1 (interleaved) or j, j + rot / 2 (not);
+ * elements from rot on stay as they are, and so do the values.  Keys go to the
+ * quantiser as they come, unrounded; queries are rounded to their type.  q_out may be q (the same
+ * address and strides); else they share no byte.  A token of a negative position
+ * is skipped: nothing stored, its queries not written; one past the table too, and reported
+ * (LW_DEV_BAD_POSITION).  A negative slot's token is not stored, its queries are
+ * rotated.  No two tokens of a call may name the same slot.
+ */
+typedef struct {
+  lw_kv_rows k, v;            /* [n][kv_heads][head_dim] */
+  lw_kv_rows q, q_out;        /* [n][q_heads][head_dim]; none if q.ptr is NULL; the type of k and v */
+  const int64_t* slots;       /* device [n] */
+  const int64_t* positions;   /* device [n] */
+  const float* table;         /* device [table_rows][rot] */
+  int64_t table_rows, n;
+  int32_t q_heads;
+  int32_t rot;                /* even, 2..head_dim */
+  int32_t interleaved;        /* 0 or 1 */
+  int32_t reserved;
+} lw_kv_rotated;
+
+lw_status lw_kv_write_rotary(const lw_kv_cache* c, const lw_kv_rotated* a, int32_t* d_status,
+                             void* stream);
+
+/*
+ * Accumulated attention weight: what softmax gave each cached key, summed over
+ * the query tokens and over the query heads that share the key's head,
+ *   weights[b][h][j] = add_to[b][h][j] + sum exp(scale q.k_j - lse)
+ * over the rows (token t of sequence b, query head of h's group) that see key j:
+ * q, lse, q_start, kv_len, page_table, scale, causal and window as they were in
+ * lw_kv_attention, after which lse is there.  add_to may be NULL (0) or weights
+ * itself.  Entries j < kv_len[b] are written, the others left.  Sums and
+ * exponentials are fp32, the order of the sum is fixed (deterministic on a given
+ * device); products carry 22 bits of fp32 queries, all of 16-bit ones (down to
+ * 2^-14 of a row's largest).  A NaN in a key or in lse is in the weights that
+ * the formula puts it in.  Keys in pages outside the cache weigh nothing.
+ * kv_len past w_keys is reported (LW_DEV_BAD_SEQ); those keys are not written.
+ * Limits as in lw_kv_attention.
+ */
+typedef struct {
+  const void* q;               /* [q_tokens][q_heads][head_dim], strided */
+  int64_t q_token_stride, q_head_stride;
+  const float* lse;            /* [q_tokens][q_heads] */
+  const int32_t* q_start;      /* device [batch + 1] */
+  const int32_t* kv_len;       /* device [batch] */
+  const int32_t* page_table;   /* device [batch][table_stride], table_width used */
+  int64_t table_stride;
+  int64_t q_tokens;
+  const float* add_to;         /* [batch][kv_heads][w_keys], strided, or NULL */
+  int64_t add_seq_stride, add_head_stride;
+  float* weights;              /* [batch][kv_heads][w_keys], strided */
+  int64_t w_seq_stride, w_head_stride;
+  int64_t w_keys;
+  int32_t table_width;
+  int32_t dtype;               /* lw_dtype of q */
+  int32_t batch;
+  int32_t q_heads;             /* a multiple of kv_heads */
+  int32_t max_q;               /* the most query tokens a sequence has (a hint, as in lw_kv_attention) */
+  int32_t causal;              /* 0 or 1 */
+  int32_t window;              /* 0: unlimited */
+  float scale;
+} lw_kv_weights;
+
+/* Bytes of device workspace an lw_kv_weigh call needs (0: none).  What it holds
+   is of no account before and after a call. */
+size_t lw_kv_weigh_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens);
+
+lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, void* ws, size_t ws_bytes,
+                      int32_t* d_status, void* stream);
+
+/*
+ * Eviction: every head of sequence b keeps m = min(kv_len[b], keep) of its keys
+ * -- the first `first`, the last `recent`, and of the others those of the
+ * largest weights (ties: the lower key; a NaN is larger than every number) -- with their values,
+ * moved in order to tokens 0 .. m - 1 of the pages out_table[b]; out_len[b] = m.
+ * kept[b][h] lists them, ascending, -1 from m on; out_weights[b][h][0 .. m - 1]
+ * are their weights, and entries m .. kv_len[b] - 1 (where there are) zeros.
+ * Keys that were rotated stay so: their positions are the original ones.
+ * out_table may be page_table's own pages in the same places (in place: the
+ * pages beyond token m are then free), or pages that no sequence of the call
+ * names; out_weights may be weights itself.  A page that is written must be one
+ * sequence's alone.  out_len must not be kv_len.  Tokens of pages outside the cache are not moved,
+ * and reported (LW_DEV_BAD_PAGE).  The places of tokens past m are left as they were.  kv_len past the page table or
+ * w_keys is clamped (LW_DEV_BAD_SEQ).  first, recent >= 0, 1 <= keep, first +
+ * recent <= keep <= out_width * page_tokens, and keep <= ow_keys where there are
+ * out_weights.
+ */
+typedef struct {
+  const float* weights;        /* [batch][kv_heads][w_keys], strided */
+  int64_t w_seq_stride, w_head_stride, w_keys;
+  const int32_t* kv_len;       /* device [batch] */
+  const int32_t* page_table;   /* device [batch][table_stride], table_width used */
+  int64_t table_stride;
+  const int32_t* out_table;    /* device [batch][out_stride], out_width used */
+  int64_t out_stride;
+  int32_t* out_len;            /* device [batch] */
+  float* out_weights;          /* [batch][kv_heads][ow_keys], strided, or NULL */
+  int64_t ow_seq_stride, ow_head_stride, ow_keys;
+  int32_t* kept;               /* device [batch][kv_heads][keep] */
+  int32_t table_width, out_width, batch, keep, first, recent;
+} lw_kv_eviction;
+
+lw_status lw_kv_evict(const lw_kv_cache* c, const lw_kv_eviction* a, int32_t* d_status, void* stream);
+
+/*
+ * Sparse attention.  A summary of each page and key/value head says within which
+ * range each channel of its cached keys lies, in 8 bits: with lo_d, hi_d the
+ * smallest and largest k_d among the page's keys and a the largest of their magnitudes,
+ *   step = fl(a (1/127)), codes rint(fl(lo_d i)), rint(fl(hi_d i)), i = fl(127 fl(1 / a))
+ * (codes 0 where a <= 2^-100) in fp32.  A NaN among the keys makes step a NaN, and the page's
+ * score larger than every number.  Record of page x, head h, at
+ * (x kv_heads + h) (2 head_dim + 16) bytes: int8 hi[head_dim], int8 lo[head_dim],
+ * fp32 step, 12 bytes unused.  `summary` is device memory of the caller, 16-byte aligned.
+ */
+size_t lw_kv_summary_bytes(const lw_kv_cache* c);   /* 0 for an unsupported shape */
+
+/* Summaries of the pages that hold tokens start[b] .. kv_len[b] - 1 of each
+   sequence, from all of their keys below kv_len[b] (a negative start counts as 0).
+   To be called when tokens were written, before the attention that reads them.  start, kv_len:
+   device [batch].  kv_len past the table: clamped, LW_DEV_BAD_SEQ; pages
+   outside the cache: left out, LW_DEV_BAD_PAGE. */
+typedef struct {
+  void* summary;
+  const int32_t* start;
+  const int32_t* kv_len;
+  const int32_t* page_table;   /* device [batch][table_stride], table_width used */
+  int64_t table_stride;
+  int32_t table_width;
+  int32_t batch;
+} lw_kv_summaries;
+
+lw_status lw_kv_summarise(const lw_kv_cache* c, const lw_kv_summaries* a, int32_t* d_status, void* stream);
+
+/*
+ * lw_kv_attention in which every query token and key/value head reads `blocks`
+ * pages of its own.  A query at position p has the nb = p / page_tokens + 1
+ * pages up to its own (causal must be 1, window 0, scale > 0): the first `first`, the
+ * last `recent`, and of the others those of the largest
+ *   score = fl(step max_heads fl(u sum_d max(c_d lo_d, c_d hi_d)))
+ * (ties: the lower page), at most `blocks` in all; c_d = rint(fl(q_d fl(127 fl(1 / a))))
+ * and u = fl(a (1/127)) of each query head of the group, a the largest |q_d|
+ * (c = 0 and u = 0 where a <= 2^-100 or is not finite).  The sums are whole numbers below 2^24: which
+ * pages are read depends on no order of summing.  The query then attends to those
+ * pages' keys up to p.  chosen (or NULL): device [q_tokens][kv_heads][blocks],
+ * the pages' places in the page table, ascending, -1 where there are fewer;
+ * rows of tokens outside every sequence are left.
+ * 1 <= recent, 0 <= first, first + recent <= blocks; table_width <= 49152;
+ * q_tokens * kv_heads <= 65535; n_pages * kv_heads * page_tokens < 2^32 (else LW_ERR_SHAPE).
+ * max_q is not used.  Everything else, lse too, as in lw_kv_attention.
+ */
+typedef struct {
+  const void* summary;
+  int32_t* chosen;
+  int32_t blocks, first, recent, reserved;
+} lw_kv_blocks;
+
+/* Bytes of device workspace: the first lw_kv_workspace_bytes(...) of it are zeroed before first
+   use as for lw_kv_attention (zeroing all is right too); 0 for an unsupported shape. */
+size_t lw_kv_blocks_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens,
+                                    int32_t table_width, int32_t blocks);
+
+lw_status lw_kv_attention_blocks(const lw_kv_cache* c, const lw_kv_attn* a, const lw_kv_blocks* s,
+                                 void* ws, size_t ws_bytes, int32_t* d_status, void* stream);
 
 /* The status's name ("LW_OK", "LW_ERR_SHAPE", ...; "unknown lw_status" for
    other values): a static string, never NULL, not to be freed. */
