@@ -45,7 +45,8 @@ struct RotaryArgs {
   const float* table;
   int64_t table_rows;
   int64_t write_blocks;      // blocks of the first role; the others rotate queries
-  int32_t rot, q_heads, splits, per_split;
+  int32_t rot, q_heads;
+  int32_t splits, per_split, kv_splits, kv_per_split;   // shares of the heads, and heads of a share
 };
 
 // The table's row of a token's position; NULL if the token is skipped (a position past the table is reported
@@ -64,52 +65,140 @@ __device__ __forceinline__ void load8f(const float* p, float (&x)[8]) {
   x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
 }
 
-// Elements 8 ch .. of a rotated key.  WIDE: rows, table and pairs are in step with 16-byte accesses.
+// 8 elements as they lie in memory, by 16-byte accesses
+template <class T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = dev::kv_float<T>(e[i]);
+  }
+};
+
+// ---- keys and values -----------------------------------------------------------
+// What a thread does to elements 8 ch .. 8 ch + 7 of every key head of its token.  WIDE (rot a multiple of 16,
+// rows and table on 16-byte boundaries): all of them are rotated, on one side of their pairs, or none is.
 template <class T, bool WIDE, bool NEAR>
-__device__ __forceinline__ void rotated_key(const RotaryArgs& a, const float* row, const T* key, int ch, float (&k)[8]) {
-  const int half = a.rot / 2, d0 = 8 * ch;
-  if constexpr (WIDE) {   // rot is a multiple of 16: a chunk is rotated or not, and on one side of the pairs
-    dev::kv_load8<T, true>(key + d0, k);
-    if (d0 >= a.rot) return;
-    if constexpr (NEAR) {
-      const float4 c = *reinterpret_cast<const float4*>(row + d0 / 2);
-      const float4 s = *reinterpret_cast<const float4*>(row + half + d0 / 2);
-      const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+struct KeyTurn {
+  float c[8], s[8];       // !NEAR: of elements 8 ch + i, the sine with the sign that its product enters with;
+                          // NEAR: of pairs 4 ch + i, i < 4
+  const float* row;
+  int d0, other, half, rot;
+  bool turned;
+
+  __device__ __forceinline__ void begin(const float* r, int ch, int rot_) {
+    row = r;
+    rot = rot_;
+    half = rot / 2;
+    d0 = 8 * ch;
+    turned = d0 < rot;
+    other = d0 < half ? d0 + half : d0 - half;
+    if constexpr (WIDE) {
+      if (!turned) return;
+      if constexpr (NEAR) {
+        const float4 u = *reinterpret_cast<const float4*>(row + d0 / 2), v = *reinterpret_cast<const float4*>(row + half + d0 / 2);
+        c[0] = u.x; c[1] = u.y; c[2] = u.z; c[3] = u.w;
+        s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
+      } else {
+        const bool low = d0 < half;
+        load8f(row + (low ? d0 : d0 - half), c);
+        load8f(row + half + (low ? d0 : d0 - half), s);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = k[2 * i], y = k[2 * i + 1];
-        k[2 * i] = __fsub_rn(__fmul_rn(x, cs[i]), __fmul_rn(y, sn[i]));
-        k[2 * i + 1] = __fadd_rn(__fmul_rn(y, cs[i]), __fmul_rn(x, sn[i]));
-      }
-    } else {
-      const bool low = d0 < half;
-      float y[8], c[8], s[8];
-      const int i0 = low ? d0 : d0 - half;
-      dev::kv_load8<T, true>(key + (low ? d0 + half : i0), y);
-      load8f(row + i0, c);
-      load8f(row + half + i0, s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float z = __fmul_rn(y[i], s[i]);
-        k[i] = __fadd_rn(__fmul_rn(k[i], c[i]), low ? -z : z);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int d = d0 + i;
-      k[i] = dev::kv_float<T>(key[d]);
-      if (d < a.rot) {
-        const bool low = NEAR ? d % 2 == 0 : d < half;
-        const int pair = NEAR ? d / 2 : (low ? d : d - half);
-        const float y = dev::kv_float<T>(key[NEAR ? d ^ 1 : (low ? d + half : d - half)]);
-        const float z = __fmul_rn(y, row[half + pair]);
-        k[i] = __fadd_rn(__fmul_rn(k[i], row[pair]), low ? -z : z);
+        for (int i = 0; i < 8; ++i) s[i] = low ? -s[i] : s[i];
       }
     }
   }
+  // k: the head's elements as they are; far: their partners' (WIDE, !NEAR)
+  __device__ __forceinline__ void turn(const T* key, const Raw8<T>& far, float (&k)[8]) const {
+    if constexpr (WIDE) {
+      if (!turned) return;
+      if constexpr (NEAR) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = k[2 * i], y = k[2 * i + 1];
+          k[2 * i] = __fsub_rn(__fmul_rn(x, c[i]), __fmul_rn(y, s[i]));
+          k[2 * i + 1] = __fadd_rn(__fmul_rn(y, c[i]), __fmul_rn(x, s[i]));
+        }
+      } else {
+        float y[8];
+        far.values(y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = __fadd_rn(__fmul_rn(k[i], c[i]), __fmul_rn(y[i], s[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d = d0 + i;
+        if (d < rot) {
+          const bool low = NEAR ? d % 2 == 0 : d < half;
+          const int pair = NEAR ? d / 2 : (low ? d : d - half);
+          const float z = __fmul_rn(dev::kv_float<T>(key[NEAR ? d ^ 1 : (low ? d + half : d - half)]), row[half + pair]);
+          k[i] = __fadd_rn(__fmul_rn(k[i], row[pair]), low ? -z : z);
+        }
+      }
+    }
+  }
+};
+
+// Key and value heads [h0, h1) of one token into its slot.  Whole warps: a group's four lanes agree on its range.
+template <class T, int D, bool WIDE, bool NEAR>
+__device__ __forceinline__ void write_heads(const RotaryArgs& a, int64_t tok, int ch, int h0, int h1) {
+  using L = KvTile<D>;
+  int64_t at = -1, slot = -1;
+  KeyTurn<T, WIDE, NEAR> turn;
+  const T *k = static_cast<const T*>(a.c.k.ptr), *v = static_cast<const T*>(a.c.v.ptr);
+  if (tok < a.c.n) {
+    slot = a.c.slots[tok];
+    const float* row = table_row(a, tok, h0 == 0 && ch == 0);
+    if (row) {
+      at = dev::slot_tile(a.c, slot, L::kBytes, h0 == 0 && ch == 0);
+      turn.begin(row, ch, a.rot);
+    }
+    k += tok * a.c.k.token_stride;
+    v += tok * a.c.v.token_stride;
+  }
+  const int t = (int)(slot % LW_KV_TILE);
+  Raw8<T> rk, rv, rf;
+  const auto load = [&](int h) {
+    if constexpr (WIDE) {
+      rk.load(k + h * a.c.k.head_stride + 8 * ch);
+      rv.load(v + h * a.c.v.head_stride + 8 * ch);
+      if (!NEAR && turn.turned) rf.load(k + h * a.c.k.head_stride + turn.other);
+    }
+  };
+  if (at >= 0) load(h0);
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    float x[8] = {}, y[8] = {}, lo[2] = {}, hi[2] = {};
+    if (at >= 0) {
+      if constexpr (WIDE) {
+        rk.values(x);
+        rv.values(y);
+        turn.turn(nullptr, rf, x);
+        if (h + 1 < h1) load(h + 1);
+      } else {
+        dev::kv_load8<T, false>(k + h * a.c.k.head_stride + 8 * ch, x);
+        dev::kv_load8<T, false>(v + h * a.c.v.head_stride + 8 * ch, y);
+        turn.turn(k + h * a.c.k.head_stride, rf, x);
+      }
+      lo[0] = dev::min3(dev::min3(dev::min3(x[0], x[1], x[2]), x[3], x[4]), dev::min3(x[5], x[6], x[7]), x[0]);
+      hi[0] = dev::max3(dev::max3(dev::max3(x[0], x[1], x[2]), x[3], x[4]), dev::max3(x[5], x[6], x[7]), x[0]);
+      lo[1] = dev::min3(dev::min3(dev::min3(y[0], y[1], y[2]), y[3], y[4]), dev::min3(y[5], y[6], y[7]), y[0]);
+      hi[1] = dev::max3(dev::max3(dev::max3(y[0], y[1], y[2]), y[3], y[4]), dev::max3(y[5], y[6], y[7]), y[0]);
+    }
+    __half ks, km, vs, vm;
+    const uint32_t kw = dev::kv_quantise8(x, lo[0], hi[0], ks, km), vw = dev::kv_quantise8(y, lo[1], hi[1], vs, vm);
+    if (at >= 0)
+      dev::kv_put8<D>(a.c.pages + at + (int64_t)h * a.c.page_tiles * L::kBytes, t, ch, kw, ks, km, vw, vs, vm);
+  }
 }
 
+// ---- queries -------------------------------------------------------------------
 // Query heads [h0, h1) of one token: thread `part` of D / 16 holds 8 pairs' cosines and sines and takes those
 // pairs of every head (it alone reads and writes them: q_out may be q), or 16 of the elements that stay.
 template <class T, int D, bool WIDE, bool NEAR>
@@ -131,29 +220,32 @@ __device__ __forceinline__ void rotate_queries(const RotaryArgs& a, const float*
     }
 #pragma unroll 1
     for (int h = h0; h < h1; h += kAhead) {
-      float x[kAhead][8], y[kAhead][8];
+      Raw8<T> rx[kAhead], ry[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
         if (h + i < h1) {
-          dev::kv_load8<T, true>(q + (h + i) * a.q.head_stride + x0, x[i]);
-          dev::kv_load8<T, true>(q + (h + i) * a.q.head_stride + y0, y[i]);
+          rx[i].load(q + (h + i) * a.q.head_stride + x0);
+          ry[i].load(q + (h + i) * a.q.head_stride + y0);
         }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
         if (h + i < h1) {
+          float x[8], y[8];
+          rx[i].values(x);
+          ry[i].values(y);
           if (turned) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               // (pair j: elements j of x and y, or neighbours, the first four pairs in x)
-              float& u = NEAR ? (j < 4 ? x[i][(2 * j) & 7] : y[i][(2 * j) & 7]) : x[i][j];
-              float& v = NEAR ? (j < 4 ? x[i][(2 * j + 1) & 7] : y[i][(2 * j + 1) & 7]) : y[i][j];
+              float& u = NEAR ? (j < 4 ? x[(2 * j) & 7] : y[(2 * j) & 7]) : x[j];
+              float& v = NEAR ? (j < 4 ? x[(2 * j + 1) & 7] : y[(2 * j + 1) & 7]) : y[j];
               const float nu = __fsub_rn(__fmul_rn(u, c[j]), __fmul_rn(v, s[j]));
               v = __fadd_rn(__fmul_rn(v, c[j]), __fmul_rn(u, s[j]));
               u = nu;
             }
           }
-          dev::kv_store8<T, true>(out + (h + i) * a.q_out.head_stride + x0, x[i]);
-          dev::kv_store8<T, true>(out + (h + i) * a.q_out.head_stride + y0, y[i]);
+          dev::kv_store8<T, true>(out + (h + i) * a.q_out.head_stride + x0, x);
+          dev::kv_store8<T, true>(out + (h + i) * a.q_out.head_stride + y0, y);
         }
     }
   } else {
@@ -177,46 +269,28 @@ __device__ __forceinline__ void rotate_queries(const RotaryArgs& a, const float*
 
 constexpr int kTokens = 16;   // of a writing block; twice as many of a rotating one
 
+// Measured, 65536 tokens of 32 query and 8 key/value heads of 128 in bf16: 254 us, 5.4 TB/s of the 1.37 GB that
+// have to move (a copy reaches 6.8).  A block a head, each with its tokens' angles and slots read anew, took 577 us:
+// a chain of three reads for 4 KB of keys and values.  One token: 3 us, the same chain.
 template <class T, int D, bool WIDE, bool NEAR>
-__global__ void __launch_bounds__(kTokens * D / 8) kv_write_rotary_kernel(const RotaryArgs a) {
-  using L = KvTile<D>;
+__global__ void __launch_bounds__(kTokens * D / 8, 3) kv_write_rotary_kernel(const RotaryArgs a) {
   dev::pdl_wait();
-  if (blockIdx.x >= a.write_blocks) {
+  if (blockIdx.x < a.write_blocks) {
+    constexpr int kChunks = D / 8;
+    const int64_t block = blockIdx.x / a.kv_splits;
+    const int h0 = (int)(blockIdx.x - block * a.kv_splits) * a.kv_per_split;
+    const int h1 = h0 + a.kv_per_split < a.c.heads ? h0 + a.kv_per_split : a.c.heads;
+    write_heads<T, D, WIDE, NEAR>(a, block * kTokens + threadIdx.x / kChunks, threadIdx.x % kChunks, h0, h1);
+  } else {
     constexpr int kParts = D / 16;
     const int64_t b = blockIdx.x - a.write_blocks, block = b / a.splits;
     const int h0 = (int)(b - block * a.splits) * a.per_split;
+    const int h1 = h0 + a.per_split < a.q_heads ? h0 + a.per_split : a.q_heads;
     const int64_t tok = block * (2 * kTokens) + threadIdx.x / kParts;
     if (tok >= a.c.n) return;
     const float* row = table_row(a, tok, false);
-    if (!row) return;
-    const int h1 = h0 + a.per_split < a.q_heads ? h0 + a.per_split : a.q_heads;
-    rotate_queries<T, D, WIDE, NEAR>(a, row, tok, threadIdx.x % kParts, h0, h1);
-    return;
+    if (row) rotate_queries<T, D, WIDE, NEAR>(a, row, tok, threadIdx.x % kParts, h0, h1);
   }
-  constexpr int kChunks = D / 8;
-  const int64_t block = blockIdx.x / a.c.heads;
-  const int h = (int)(blockIdx.x - block * a.c.heads), ch = threadIdx.x % kChunks;
-  const int64_t tok = block * kTokens + threadIdx.x / kChunks;
-  int64_t at = -1, slot = -1;
-  float k[8] = {}, v[8] = {}, lo[2] = {}, hi[2] = {};
-  if (tok < a.c.n) {
-    slot = a.c.slots[tok];
-    const float* row = table_row(a, tok, h == 0 && ch == 0);
-    if (row) at = dev::slot_tile(a.c, slot, L::kBytes, h == 0 && ch == 0);
-    if (at >= 0) {
-      rotated_key<T, WIDE, NEAR>(a, row, static_cast<const T*>(a.c.k.ptr) + tok * a.c.k.token_stride + h * a.c.k.head_stride,
-                                 ch, k);
-      dev::kv_load8_range<T, WIDE>(static_cast<const T*>(a.c.v.ptr) + tok * a.c.v.token_stride + h * a.c.v.head_stride + 8 * ch,
-                                   v, lo[1], hi[1]);
-      lo[0] = dev::min3(dev::min3(dev::min3(k[0], k[1], k[2]), k[3], k[4]), dev::min3(k[5], k[6], k[7]), k[0]);
-      hi[0] = dev::max3(dev::max3(dev::max3(k[0], k[1], k[2]), k[3], k[4]), dev::max3(k[5], k[6], k[7]), k[0]);
-    }
-  }
-  __half ks, km, vs, vm;
-  const uint32_t kw = dev::kv_quantise8(k, lo[0], hi[0], ks, km), vw = dev::kv_quantise8(v, lo[1], hi[1], vs, vm);
-  if (at < 0) return;
-  dev::kv_put8<D>(a.c.pages + at + (int64_t)h * a.c.page_tiles * L::kBytes, (int)(slot % LW_KV_TILE), ch, kw, ks, km,
-                  vw, vs, vm);
 }
 
 template <class T, int D>
@@ -330,14 +404,19 @@ extern "C" lw_status lw_kv_write_rotary(const lw_kv_cache* c, const lw_kv_rotate
   a.table_rows = p->table_rows;
   a.rot = p->rot;
   a.q_heads = queries ? p->q_heads : 0;
-  // A rotating block takes 32 tokens' heads, or a share of them where tokens are few
-  const int64_t groups = (p->n + 2 * kTokens - 1) / (2 * kTokens);
-  int64_t splits = (4ll * device_sm_count() + groups - 1) / groups;
-  if (splits > a.q_heads) splits = a.q_heads;
-  if (splits < 1) splits = 1;
-  a.per_split = (int32_t)((a.q_heads + splits - 1) / splits);
-  a.splits = a.per_split ? (a.q_heads + a.per_split - 1) / a.per_split : 1;
-  a.write_blocks = (p->n + kTokens - 1) / kTokens * c->kv_heads;
+  // A block takes all heads of its tokens (16 that are written, 32 that are rotated), or a share of them where
+  // tokens are few: some blocks an SM
+  const auto share = [](int64_t groups, int heads, int32_t& splits, int32_t& per) {
+    int64_t n = (6ll * device_sm_count() + groups - 1) / groups;
+    if (n > heads) n = heads;
+    if (n < 1) n = 1;
+    per = (int32_t)((heads + n - 1) / n);
+    splits = per ? (heads + per - 1) / per : 1;
+  };
+  const int64_t groups = (p->n + 2 * kTokens - 1) / (2 * kTokens), writes = (p->n + kTokens - 1) / kTokens;
+  share(groups, a.q_heads, a.splits, a.per_split);
+  share(writes, c->kv_heads, a.kv_splits, a.kv_per_split);
+  a.write_blocks = writes * a.kv_splits;
   const int64_t blocks = a.write_blocks + (queries ? groups * a.splits : 0);
   if (blocks > (1ll << 31) - 1) return fail(LW_ERR_SHAPE, "%s: %lld tokens", fn, (long long)p->n);
   const bool wide = p->rot % 16 == 0 && !off(p->table, 16) &&
