@@ -73,14 +73,14 @@ extern "C" lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, v
   w.group = a->q_heads / c->kv_heads;
   w.vec = kv_rows_aligned(a->q, a->q_token_stride, a->q_head_stride, a->dtype);
   w.status = d_status;
-  // CTAs of a sequence's head: as many as give each some tiles, in all not more than the device takes at once
-  // a few times over (they find out themselves how long their sequence is)
+  // CTAs of a sequence's head: some 32 tiles a warp (a CTA's start, its rows and first copies, is 2 us), but
+  // enough CTAs for the device to be full, if a warp has a tile to do
   const int64_t pairs = (int64_t)a->batch * c->kv_heads;
   const int64_t tiles = ((int64_t)a->table_width * c->page_tokens + 15) / 16;
-  int64_t x = (tiles + 31) / 32, most = 64ll * device_sm_count() / pairs;
-  if (x > most) x = most;
-  if (x < 1) x = 1;
-  w.parts = (int32_t)x;
+  const int64_t fill = (2 * device_sm_count() + pairs - 1) / pairs;
+  int64_t x = (tiles + 7) / 8 < fill ? (tiles + 7) / 8 : fill;
+  if (x < (tiles + 255) / 256) x = (tiles + 255) / 256;
+  if (x > 65535) x = 65535;
   const dim3 grid((unsigned)x, (unsigned)c->kv_heads, (unsigned)a->batch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return c->head_dim == 64   ? launch_few_t<64>(w, grid, st)

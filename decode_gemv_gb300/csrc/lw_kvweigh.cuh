@@ -19,7 +19,6 @@ struct WeighArgs {
   const uint8_t* pages;
   int64_t n_pages, page_bytes;
   int32_t page_tokens, heads, group, vec;
-  int32_t parts;   // CTAs of one sequence's head
   int32_t* status;
 };
 
@@ -32,7 +31,12 @@ struct WeighFew {
   static constexpr int kRow = kBlocks * kParts * kFrag;    // then the rows: f, lse, hi, lo, group sums
   static constexpr int kRowWords = 4 + D / 32;
   static constexpr int kRange = kRow + kBlocks * 8 * kRowWords * 4;   // keys that all, and any, rows of a block see
-  static constexpr int kSmem = kRange + kBlocks * 4 * 4;
+  static constexpr int kBars = kRange + kBlocks * 4 * 4;
+  static constexpr int kStages = 4;                        // tiles of a warp on their way
+  static constexpr int kRing = (kBars + kWarps * kStages * 8 + 127) / 128 * 128;
+  static constexpr int kKeys = KvTile<D>::kValCodes;       // the key half of a tile
+  static constexpr int kSmem = kRing + kWarps * kStages * kKeys;
+  static constexpr int kPerSm = 2;
 };
 
 namespace dev {
@@ -141,57 +145,143 @@ __device__ void weigh_row(const WeighArgs& a, uint8_t* smem, int blk, int r, int
   }
 }
 
+// A warp's tiles: first, first + step, ... below `end`, their key halves fetched by bulk copies into a ring of its
+// own, in order.  The page table is read 32 tiles at a time, lane i holding the i-th one's place.
 template <int D, class T>
-__global__ void __launch_bounds__(WeighFew<D, T>::kThreads) kv_weigh_few_kernel(const WeighArgs a) {
+struct WeighFetch {
+  using W = WeighFew<D, T>;
+  uint8_t* ring;
+  uint64_t* bars;
+  const int32_t* table;
+  int64_t head;
+  int next, end, step, at, in, out;
+  uint32_t there, have, parity;
+  const uint8_t* src;
+
+  __device__ __forceinline__ void lookup(const WeighArgs& a, int lane) {
+    const int64_t tile = next + (int64_t)lane * step;
+    const int tpp = a.page_tokens / LW_KV_TILE;
+    const bool mine = tile < end;
+    const int page = mine ? table[tile / tpp] : -1;
+    const bool ok = page >= 0 && page < a.n_pages;
+    if (mine && !ok) report(a.status, LW_DEV_BAD_PAGE);
+    there = __ballot_sync(0xFFFFFFFFu, ok);
+    src = a.pages + (int64_t)page * a.page_bytes + head + (tile % tpp) * KvTile<D>::kBytes;
+    at = 0;
+  }
+  __device__ __forceinline__ void send(const WeighArgs& a, int lane) {
+    if (next >= end) return;
+    if (at == 32) lookup(a, lane);
+    if (there >> at & 1u) {
+      if (lane == at) {
+        mbar_arrive_expect_tx(&bars[in], W::kKeys);
+        bulk_g2s(ring + in * W::kKeys, src, W::kKeys, &bars[in]);
+      }
+      have |= 1u << in;
+    }
+    ++at;
+    next += step;
+    in = in + 1 == W::kStages ? 0 : in + 1;
+  }
+  __device__ __forceinline__ void begin(const WeighArgs& a, int first, int lane) {
+    next = first;
+    in = out = 0;
+    have = 0;
+    at = 32;
+#pragma unroll
+    for (int i = 0; i < W::kStages; ++i) send(a, lane);
+  }
+  // The tile at `out` has come (false: the wait ran out)
+  __device__ __forceinline__ bool wait() {
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars[out], parity >> out & 1u));
+    if (!ok) return false;
+    parity ^= 1u << out;
+    have &= ~(1u << out);
+    return true;
+  }
+  // On to the next tile
+  __device__ __forceinline__ void pass() { out = out + 1 == W::kStages ? 0 : out + 1; }
+  // After a wait that ran out: what is still on its way
+  __device__ __forceinline__ void drain() {
+    for (int i = 0; i < W::kStages; ++i)
+      if (have >> i & 1u) mbar_wait(&bars[i], parity >> i & 1u);
+  }
+};
+
+template <int D, class T>
+__global__ void __launch_bounds__(WeighFew<D, T>::kThreads, WeighFew<D, T>::kPerSm) kv_weigh_few_kernel(const WeighArgs a) {
   using W = WeighFew<D, T>;
   using L = KvTile<D>;
   constexpr int G = L::G;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = lane / 4, q = lane % 4;
   const int b = blockIdx.z, h = blockIdx.y;
+  WeighFetch<D, T> f;
+  f.bars = reinterpret_cast<uint64_t*>(smem + W::kBars) + warp * W::kStages;
+  if (lane < W::kStages) mbar_init(&f.bars[lane], 1);
+  fence_barrier_init();
+  __syncwarp();
   pdl_wait();
   int q0, Tq, n;
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) weigh_seq<true>(a, b, q0, Tq, n);
   else weigh_seq<false>(a, b, q0, Tq, n);
   const int keys = n < a.p.w_keys ? n : (int)a.p.w_keys;
-  const int tiles = (keys + 15) / 16, tpp = a.page_tokens / LW_KV_TILE;
+  const int tiles = (keys + 15) / 16, first = blockIdx.x * W::kWarps + warp;
   if ((int)blockIdx.x * W::kWarps >= tiles) return;
   const int rows = Tq * a.group;
-  const int32_t* table = a.p.page_table + (int64_t)b * a.p.table_stride;
   const float* add = a.p.add_to ? a.p.add_to + b * a.p.add_seq_stride + h * a.p.add_head_stride : nullptr;
   float* out = a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride;
+  f.ring = smem + W::kRing + warp * W::kStages * W::kKeys;
+  f.table = a.p.page_table + (int64_t)b * a.p.table_stride;
+  f.head = (int64_t)h * (a.page_tokens / LW_KV_TILE) * L::kBytes;
+  f.end = tiles;
+  f.step = gridDim.x * W::kWarps;
+  f.parity = 0;
+  bool ok = true;
   int r0 = 0;
   do {
+    if (ok) f.begin(a, first, lane);
     const int blocks = (min(rows - r0, 8 * W::kBlocks) + 7) / 8;
     if (r0) __syncthreads();
     for (int i = warp; i < blocks; i += W::kWarps) weigh_row<D, T>(a, smem, i, r0 + 8 * i + t, q0, Tq, n, h, lane);
     __syncthreads();
-    for (int tile = blockIdx.x * W::kWarps + warp; tile < tiles; tile += gridDim.x * W::kWarps) {
-      const int page = table[tile / tpp];
-      const bool there = page >= 0 && page < a.n_pages;
-      if (!there && lane == 0) report(a.status, LW_DEV_BAD_PAGE);
+    // what the weights are added to, a tile ahead (what an earlier set of rows left is this thread's own)
+    const float* from = r0 ? out : add;
+    const auto before = [&](int tile) {
+      const int j = 16 * tile + t + 8 * q;
+      return q < 2 && from && tile < tiles && j < keys ? from[j] : 0.f;
+    };
+    float had = before(first);
+    for (int tile = first; tile < tiles && ok; tile += f.step) {
+      const float had_next = tile < tiles - f.step ? before(tile + f.step) : 0.f;
       const int j0 = 16 * tile + t;
       float sum[2] = {0.f, 0.f};
-      if (there && blocks) {
-        const uint8_t* s = a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
-        uint32_t kc[2][G], ks[2][G], km[2][L::GP / 2], c[2][G][4];
+      if (f.have >> f.out & 1u) {
+        ok = f.wait();
+        if (!ok) break;
+        const uint32_t s = smem_addr(f.ring + f.out * W::kKeys);
+        uint32_t c[2][G][4];
         float sc[2][G], mid[2][G];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int tk = t + 8 * i;
-          ldg_words<G>(s + L::kKeyCodes + ((tk * 4 + q) * G) * 4, kc[i]);
-          ldg_words<G>(s + L::kKeyScale + (tk / 2 * G) * 4, ks[i]);
-          ldg_words<L::GP / 2>(s + L::kKeyMin + tk * L::GP * 2, km[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
+          uint32_t kc[G], ks[G], km[L::GP / 2];
+          lds_words<G>(s + L::kKeyCodes + ((tk * 4 + q) * G) * 4, kc);
+          lds_words<G>(s + L::kKeyScale + (tk / 2 * G) * 4, ks);
+          lds_words<L::GP / 2>(s + L::kKeyMin + tk * L::GP * 2, km);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            centred(kc[i][g], c[i][g]);
-            const float2 s2 = h2f(ks[i][g]), m2 = h2f(km[i][g / 2]);
+            centred(kc[g], c[i][g]);
+            const float2 s2 = h2f(ks[g]), m2 = h2f(km[g / 2]);
             sc[i][g] = t % 2 ? s2.y : s2.x;
             mid[i][g] = fmaf(8.f, sc[i][g], g % 2 ? m2.y : m2.x);
           }
+        }
+        // all lanes have read the place: the next tile may come into it
+        fence_proxy_async();
+        __syncwarp();
+        f.pass();
+        f.send(a, lane);
 #pragma unroll 1
         for (int k = 0; k < blocks; ++k) {
           const int4 range = *(reinterpret_cast<const int4*>(smem + W::kRange) + k);
@@ -202,14 +292,14 @@ __global__ void __launch_bounds__(WeighFew<D, T>::kThreads) kv_weigh_few_kernel(
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             float acc[4];
-            const uint4 f = *reinterpret_cast<const uint4*>(frag + (g * 32 + lane) * 4);
-            mma_f16_zero(acc, c[0][g][0], c[1][g][0], c[0][g][1], c[1][g][1], f.x, f.y);
-            mma_f16(acc, c[0][g][2], c[1][g][2], c[0][g][3], c[1][g][3], f.z, f.w);
+            const uint4 u = *reinterpret_cast<const uint4*>(frag + (g * 32 + lane) * 4);
+            mma_f16_zero(acc, c[0][g][0], c[1][g][0], c[0][g][1], c[1][g][1], u.x, u.y);
+            mma_f16(acc, c[0][g][2], c[1][g][2], c[0][g][3], c[1][g][3], u.z, u.w);
             if constexpr (W::kParts == 2) {
               float low[4];
-              const uint4 f = *reinterpret_cast<const uint4*>(frag + W::kFrag / 4 + (g * 32 + lane) * 4);
-              mma_f16_zero(low, c[0][g][0], c[1][g][0], c[0][g][1], c[1][g][1], f.x, f.y);
-              mma_f16(low, c[0][g][2], c[1][g][2], c[0][g][3], c[1][g][3], f.z, f.w);
+              const uint4 v = *reinterpret_cast<const uint4*>(frag + W::kFrag / 4 + (g * 32 + lane) * 4);
+              mma_f16_zero(low, c[0][g][0], c[1][g][0], c[0][g][1], c[1][g][1], v.x, v.y);
+              mma_f16(low, c[0][g][2], c[1][g][2], c[0][g][3], c[1][g][3], v.z, v.w);
 #pragma unroll
               for (int i = 0; i < 4; ++i) acc[i] = fmaf(low[i], 1.f / 2048.f, acc[i]);
             }
@@ -238,16 +328,20 @@ __global__ void __launch_bounds__(WeighFew<D, T>::kThreads) kv_weigh_few_kernel(
           sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
           sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
         }
+      } else {
+        f.pass();
+        f.send(a, lane);
       }
-      // (what an earlier set of rows left is this thread's own)
-      if (q < 2) {
-        const int j = j0 + 8 * q;
-        const float s = q ? sum[1] : sum[0];
-        if (j < keys) out[j] = (r0 ? out[j] : add ? add[j] : 0.f) + s;
-      }
+      const int j = j0 + 8 * q;
+      if (q < 2 && j < keys) out[j] = had + (q ? sum[1] : sum[0]);
+      had = had_next;
     }
     r0 += 8 * W::kBlocks;
   } while (r0 < rows);
+  if (!ok) {
+    report(a.status, LW_DEV_TIMEOUT);
+    f.drain();
+  }
 }
 
 }  // namespace dev
