@@ -10,7 +10,7 @@ struct EvictArgs {
   lw_kv_eviction p;
   uint8_t* pages;
   int64_t n_pages, page_bytes;
-  int32_t page_tokens, heads;
+  int32_t page_tokens, heads, most_keys;
   int32_t* status;
 };
 
@@ -24,54 +24,142 @@ __device__ __forceinline__ int evict_keys(const EvictArgs& a, int b) {
 }
 
 // ---- the choice ----------------------------------------------------------------
-constexpr int kSelect = 1024;
+// A cluster a head.  Its CTAs share the competing keys in contiguous stretches; each reads its own once and keeps
+// the order keys in shared memory (a stretch that is too long is read again instead).  The limit is found in
+// three digits of 11, 11 and 10 bits; a digit's histograms lie in the CTAs' shared memory and every CTA adds them
+// up, so that all find the same digit with one barrier of the cluster a digit.  From the same histograms a CTA
+// knows how many keys above the limit, and at it, lie in the stretches before its own: the places follow without
+// another exchange.
+constexpr int kSelect = 512, kSelectWarps = kSelect / 32, kBins = 2048;
+constexpr int kMostSelect = 40960;   // order keys a CTA keeps
 
-// A CTA a head: kept[b][h], ascending.
 __global__ void __launch_bounds__(kSelect) kv_evict_select_kernel(const EvictArgs a) {
-  __shared__ uint32_t hist[256], s_scan[32], s_pick[2];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  extern __shared__ __align__(16) uint32_t smem[];
+  __shared__ uint32_t s_scan[kSelectWarps], s_pick[2], s_more[kSelectWarps], s_same[kSelectWarps];
+  uint32_t* hist = smem;                 // [3][kBins]
+  uint32_t* keys = smem + 3 * kBins;     // [a.most_keys]
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const uint32_t ranks = dev::cluster_size(), rank = dev::cluster_rank();
+  for (int i = tid; i < 3 * kBins; i += kSelect) hist[i] = 0;
   dev::pdl_wait();
-  const int n = h == 0 && tid == 0 ? evict_keys<true>(a, b) : evict_keys<false>(a, b);
+  const int n = h == 0 && rank == 0 && tid == 0 ? evict_keys<true>(a, b) : evict_keys<false>(a, b);
   const int m = n < a.p.keep ? n : a.p.keep;
-  if (h == 0 && tid == 0) a.p.out_len[b] = m;
+  if (h == 0 && rank == 0 && tid == 0) a.p.out_len[b] = m;
   int32_t* kept = a.p.kept + ((int64_t)b * a.heads + h) * a.p.keep;
-  for (int i = m + tid; i < a.p.keep; i += kSelect) kept[i] = -1;
-  if (n <= a.p.keep) {
-    for (int i = tid; i < n; i += kSelect) kept[i] = i;
+  const int self = (int)rank * kSelect + tid, all = (int)ranks * kSelect;
+  for (int64_t i = (int64_t)m + self; i < a.p.keep; i += all) kept[i] = -1;
+  if (n <= a.p.keep) {   // (the same in all of the cluster)
+    for (int64_t i = self; i < n; i += all) kept[i] = (int)i;
     return;
   }
   // keys [first, last) compete for `need` places
   const int first = a.p.first, last = n - a.p.recent;
-  const float* w = a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride;
-  uint32_t need = (uint32_t)(m - a.p.first - a.p.recent), limit = 0;
-  const bool some = need > 0;
-  if (some) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t mask = shift == 24 ? 0 : ~0u << (shift + 8);
-      for (int i = first + tid; i < last; i += kSelect) {
-        const uint32_t k = dev::order_key(w[i]);
-        if ((k & mask) == limit) atomicAdd(&hist[k >> shift & 255], 1u);
+  for (int64_t i = self; i < first; i += all) kept[i] = (int)i;
+  for (int64_t i = (int64_t)last + self; i < n; i += all) kept[m - n + i] = (int)i;
+  uint32_t need = (uint32_t)(m - first - a.p.recent), limit = 0;
+  if (need == 0) return;
+  const int stretch = (int)((((int64_t)last - first + ranks - 1) / ranks + 31) / 32 * 32);
+  const int64_t from = first + (int64_t)rank * stretch;
+  const int count = from < last ? (int)(last - from < stretch ? last - from : stretch) : 0;
+  const float* w = a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride + from;
+  const bool here = count <= a.most_keys;
+  __syncthreads();
+  uint32_t above = 0, equal = 0;   // of the stretches before
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
+    const uint32_t mask = pass == 0 ? 0 : pass == 1 ? ~0u << 21 : ~0u << 10;
+    uint32_t* mine = hist + pass * kBins;
+    const auto add = [&](uint32_t k) {
+      if ((k & mask) == limit) atomicAdd(&mine[k >> shift & (bins - 1)], 1u);
+    };
+    if (pass == 0 || !here) {
+      constexpr int kAhead = 8;
+      for (int i0 = tid; i0 < count; i0 += kAhead * kSelect) {
+        float x[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) x[e] = i0 + e * kSelect < count ? w[i0 + e * kSelect] : 0.f;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          if (i0 + e * kSelect < count) {
+            const uint32_t k = dev::order_key(x[e]);
+            if (here) keys[i0 + e * kSelect] = k;
+            add(k);
+          }
       }
-      __syncthreads();
-      limit |= dev::pick_digit<kSelect>(hist, need, s_scan, s_pick) << shift;
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < count; i += kSelect) add(keys[i]);
     }
-  }
-  for (int i = tid; i < first; i += kSelect) kept[i] = i;
-  for (int i = last + tid; i < n; i += kSelect) kept[m - n + i] = i;
-  if (!some) return;
-  uint32_t above = 0, equal = 0;   // before this stretch of keys
-  for (int i0 = first; i0 < last; i0 += kSelect) {
-    const int i = i0 + tid;
-    const uint32_t k = i < last ? dev::order_key(w[i]) : 0;
-    const bool more = i < last && k > limit, same = i < last && k == limit;
+    dev::cluster_sync();
+    // thread t has the four bins below bins - 4 t: in all, and in the stretches before
+    const int top = bins - 4 * (tid + 1);
+    uint32_t sum[4] = {}, before[4] = {};
+    if (top >= 0) {
+      for (uint32_t r = 0; r < ranks; ++r) {
+        const uint4 v = dev::cluster_load4(mine + top, r);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[i] += x[i];
+          before[i] += r < rank ? x[i] : 0;
+        }
+      }
+    }
     uint32_t total;
-    const uint32_t pos = dev::scan_cta<kSelect>((uint32_t)more | (uint32_t)same << 16, s_scan, total);
-    const uint32_t ab = above + (pos & 0xFFFFu), eq = equal + (pos >> 16);
-    if (more || (same && eq < need)) kept[first + ab + (eq < need ? eq : need)] = i;
-    above += total & 0xFFFFu;
-    equal += total >> 16;
+    uint32_t over = dev::scan_cta<kSelect>(sum[0] + sum[1] + sum[2] + sum[3], s_scan, total);
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      if (over < need && over + sum[i] >= need) {
+        s_pick[0] = (uint32_t)(top + i);
+        s_pick[1] = need - over;
+      }
+      over += sum[i];
+    }
+    __syncthreads();
+    const uint32_t digit = s_pick[0];
+    need = s_pick[1];
+    limit |= digit << shift;
+    uint32_t up = 0, at = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      up += top + i > (int)digit ? before[i] : 0;
+      at += top + i == (int)digit ? before[i] : 0;
+    }
+    (void)dev::scan_cta<kSelect>(up, s_scan, total);
+    above += total;
+    if (pass == 2) (void)dev::scan_cta<kSelect>(at, s_scan, equal);
+  }
+  dev::cluster_sync();   // (no CTA leaves while another reads its histograms)
+  // a warp takes a part of the stretch, counts it, and places it
+  const int part = ((count + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+  const int i0 = warp * part, i1 = i0 + part < count ? i0 + part : count;
+  uint32_t more = 0, same = 0;
+#pragma unroll 4
+  for (int i = i0 + lane; i < i0 + part; i += 32) {
+    const uint32_t k = i < i1 ? (here ? keys[i] : dev::order_key(w[i])) : 0u;
+    more += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && k > limit));
+    same += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && k == limit));
+  }
+  if (lane == 0) {
+    s_more[warp] = more;
+    s_same[warp] = same;
+  }
+  __syncthreads();
+  for (int v = 0; v < warp; ++v) {
+    above += s_more[v];
+    equal += s_same[v];
+  }
+  const uint32_t lower = (1u << lane) - 1;
+#pragma unroll 4
+  for (int i = i0 + lane; i < i0 + part; i += 32) {
+    const uint32_t k = i < i1 ? (here ? keys[i] : dev::order_key(w[i])) : 0u;
+    const bool is_more = i < i1 && k > limit, is_same = i < i1 && k == limit;
+    const uint32_t bm = __ballot_sync(0xFFFFFFFFu, is_more), bs = __ballot_sync(0xFFFFFFFFu, is_same);
+    const uint32_t am = above + __popc(bm & lower), as = equal + __popc(bs & lower);
+    if (is_more || (is_same && as < need)) kept[first + am + (as < need ? as : need)] = (int)(from + i);
+    above += __popc(bm);
+    equal += __popc(bs);
   }
 }
 
@@ -82,27 +170,12 @@ __global__ void __launch_bounds__(kSelect) kv_evict_select_kernel(const EvictArg
 // places may be the source's own.
 constexpr int kMoveWarps = 16, kMove = 32 * kMoveWarps;
 
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kMove, 2) kv_evict_move_kernel(const EvictArgs a) {
   using L = KvTile<D>;
   constexpr int G = L::G;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
+  const int ranks = (int)dev::cluster_size(), rank = (int)dev::cluster_rank();
   const int h = blockIdx.y, b = blockIdx.z, tpp = a.page_tokens / LW_KV_TILE;
   dev::pdl_wait();
   const int n = evict_keys<false>(a, b);
@@ -187,7 +260,7 @@ __global__ void __launch_bounds__(kMove, 2) kv_evict_move_kernel(const EvictArgs
         }
       }
     }
-    cluster_sync();
+    dev::cluster_sync();
     if (mine) {
       const int i = 16 * tile + lane;
       if (ow && lane < 16 && i < m) ow[i] = weight;
@@ -214,7 +287,7 @@ __global__ void __launch_bounds__(kMove, 2) kv_evict_move_kernel(const EvictArgs
     }
   }
   if (!ow) return;
-  cluster_sync();   // (weights behind the kept ones' places were read by then)
+  dev::cluster_sync();   // (weights behind the kept ones' places were read by then)
   const int64_t end = n < a.p.ow_keys ? n : a.p.ow_keys;
   for (int64_t i = m + rank * kMove + (int)threadIdx.x; i < end; i += ranks * kMove) ow[i] = 0.f;
 }
@@ -258,12 +331,25 @@ extern "C" lw_status lw_kv_evict(const lw_kv_cache* c, const lw_kv_eviction* p, 
   a.heads = c->kv_heads;
   a.status = d_status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  s = kv_launch(fn, kv_evict_select_kernel, dim3((unsigned)c->kv_heads, (unsigned)p->batch), kSelect, 0, 1, st, a);
-  if (s != LW_OK) return s;
-  // CTAs of a head, until the device is full twice over (two fit an SM)
-  const int64_t pairs = (int64_t)p->batch * c->kv_heads, rounds = (p->keep + 16 * kMoveWarps - 1) / (16 * kMoveWarps);
+  // CTAs of a head.  The choice: some 4096 keys each, as far as three an SM have room
+  const int64_t pairs = (int64_t)p->batch * c->kv_heads, sms = device_sm_count();
+  int64_t keys = (int64_t)p->table_width * c->page_tokens;
+  if (p->w_keys < keys) keys = p->w_keys;
   int ranks = 1;
-  while (ranks < 8 && ranks < rounds && 2 * ranks * pairs <= 2 * device_sm_count()) ranks *= 2;
+  while (ranks < 8 && 2 * ranks * pairs <= 3 * sms && keys > 4096ll * ranks) ranks *= 2;
+  int64_t most = (keys + ranks - 1) / ranks + 32;
+  if (most > kMostSelect) most = kMostSelect;
+  a.most_keys = (int32_t)most;
+  const size_t smem = (3 * kBins + (size_t)most) * 4;
+  if (resident_blocks(reinterpret_cast<const void*>(kv_evict_select_kernel), kSelect, smem) < 1)
+    return fail(LW_ERR_CUDA, "%s: the kernel does not fit this device", fn);
+  s = kv_launch(fn, kv_evict_select_kernel, dim3((unsigned)ranks, (unsigned)c->kv_heads, (unsigned)p->batch), kSelect,
+                smem, ranks, st, a);
+  if (s != LW_OK) return s;
+  // The move: until the device is full (two an SM)
+  const int64_t rounds = (p->keep + 16 * kMoveWarps - 1) / (16 * kMoveWarps);
+  ranks = 1;
+  while (ranks < 8 && ranks < rounds && 2 * ranks * pairs <= 2 * sms) ranks *= 2;
   const dim3 grid((unsigned)ranks, (unsigned)c->kv_heads, (unsigned)p->batch);
   return c->head_dim == 64   ? kv_launch(fn, kv_evict_move_kernel<64>, grid, kMove, 0, ranks, st, a)
          : c->head_dim == 96 ? kv_launch(fn, kv_evict_move_kernel<96>, grid, kMove, 0, ranks, st, a)

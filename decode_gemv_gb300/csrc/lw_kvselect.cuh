@@ -44,6 +44,35 @@ __device__ __forceinline__ uint32_t scan_cta(uint32_t v, uint32_t* s, uint32_t& 
   return before + inc - v;
 }
 
+// Clusters: the barrier of all threads (an acquire and a release), a CTA's rank, how many there are, and words of
+// another CTA's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint4 cluster_load4(const void* mine, uint32_t rank) {
+  uint4 v;
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mine))), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
 // The digit (of 256) in which the `need`-th largest key lies, by its histogram; need becomes what is left of it
 // within that digit.  Whole CTA of at least 256 threads.
 template <int NT>
