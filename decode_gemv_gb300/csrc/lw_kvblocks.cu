@@ -24,7 +24,7 @@ constexpr int kSumWarps = 8;
 
 // A warp a page and head: lanes hold keys lane / 4 and 8 more of a tile, elements 32 g + 8 (lane % 4) + 0..7.
 template <int D>
-__global__ void __launch_bounds__(32 * kSumWarps) kv_summarise_kernel(const SummaryArgs a) {
+__global__ void __launch_bounds__(32 * kSumWarps, 2) kv_summarise_kernel(const SummaryArgs a) {
   using L = KvTile<D>;
   constexpr int G = L::G, GX = G == 2 ? 2 : 4;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = lane / 4, q = lane % 4;
@@ -35,16 +35,37 @@ __global__ void __launch_bounds__(32 * kSumWarps) kv_summarise_kernel(const Summ
   const int n = len < 0 ? 0 : (len > most ? most : len);
   const int start = max(a.p.start[b], 0);
   if (start >= n) return;
-  const int last = (n - 1) / a.page_tokens;
+  const int last = (n - 1) / a.page_tokens, step = gridDim.x * kSumWarps;
   const int32_t* table = a.p.page_table + (int64_t)b * a.p.table_stride;
-  for (int blk = start / a.page_tokens + blockIdx.x * kSumWarps + warp; blk <= last; blk += gridDim.x * kSumWarps) {
-    const int page = table[blk];
-    if (page < 0 || page >= a.n_pages) {
+  int blk = start / a.page_tokens + blockIdx.x * kSumWarps + warp;
+  // what is read next: a tile ahead, over the ends of pages too
+  const auto page_of = [&](int x) { return x <= last ? table[x] : -1; };
+  const auto keys_of = [&](int x) { return min(n - x * a.page_tokens, a.page_tokens); };
+  const auto there = [&](int page) { return page >= 0 && page < a.n_pages; };
+  struct Raw {
+    uint32_t kc[2][G], ks[2][G], km[2][L::GP / 2];
+  };
+  const auto read = [&](Raw& r, int page, int tile, int keys) {
+    // (a key past the end: the lane's other one once more, or the first)
+    const uint8_t* s = a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile) * L::kBytes;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int left = keys - 16 * tile, tk = t + 8 * e < left ? t + 8 * e : (t < left ? t : 0);
+      dev::ldg_words<G>(s + L::kKeyCodes + ((tk * 4 + q) * G) * 4, r.kc[e]);
+      dev::ldg_words<G>(s + L::kKeyScale + (tk / 2 * G) * 4, r.ks[e]);
+      dev::ldg_words<L::GP / 2>(s + L::kKeyMin + tk * L::GP * 2, r.km[e]);
+    }
+  };
+  Raw now;
+  int page = page_of(blk), next_page = page_of(blk + step);
+  if (blk <= last && there(page)) read(now, page, 0, keys_of(blk));
+  for (; blk <= last; blk += step, page = next_page, next_page = page_of(blk + step)) {
+    if (!there(page)) {
       if (lane == 0) dev::report(a.status, LW_DEV_BAD_PAGE);
+      if (there(next_page)) read(now, next_page, 0, keys_of(blk + step));
       continue;
     }
-    const uint8_t* s = a.pages + page * a.page_bytes + (int64_t)h * tpp * L::kBytes;
-    const int keys = min(n - blk * a.page_tokens, a.page_tokens);
+    const int keys = keys_of(blk), tiles = (keys + 15) / 16;
     float lo[GX][8], hi[GX][8];
 #pragma unroll
     for (int g = 0; g < GX; ++g)
@@ -54,28 +75,31 @@ __global__ void __launch_bounds__(32 * kSumWarps) kv_summarise_kernel(const Summ
         hi[g][i] = -INFINITY;
       }
 #pragma unroll 1
-    for (int tile = 0; 16 * tile < keys; ++tile, s += L::kBytes) {
+    for (int tile = 0; tile < tiles; ++tile) {
+      const Raw r = now;
+      if (tile + 1 < tiles) read(now, page, tile + 1, keys);
+      else if (there(next_page)) read(now, next_page, 0, keys_of(blk + step));
+      // (which of a pair of scales: by the key that was read)
+      const bool odd = t < keys - 16 * tile && t % 2;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int tk = t + 8 * e;
-        if (16 * tile + tk >= keys) continue;
-        uint32_t kc[G], ks[G], km[L::GP / 2];
-        dev::ldg_words<G>(s + L::kKeyCodes + ((tk * 4 + q) * G) * 4, kc);
-        dev::ldg_words<G>(s + L::kKeyScale + (tk / 2 * G) * 4, ks);
-        dev::ldg_words<L::GP / 2>(s + L::kKeyMin + tk * L::GP * 2, km);
+      for (int g = 0; g < G; ++g) {
+        float2 y[2][4];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const float2 s2 = dev::h2f(ks[g]), m2 = dev::h2f(km[g / 2]);
-          const float sc = t % 2 ? s2.y : s2.x, mn = g % 2 ? m2.y : m2.x;
+        for (int e = 0; e < 2; ++e) {
+          const float2 s2 = dev::h2f(r.ks[e][g]), m2 = dev::h2f(r.km[e][g / 2]);
+          const float sc = odd ? s2.y : s2.x, mn = g % 2 ? m2.y : m2.x;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t c = i % 2 ? dev::whole_odd(kc[g] >> (8 * (i / 2))) : dev::whole_even(kc[g] >> (8 * (i / 2)));
-            const float2 y = dev::fma2(dev::h2f(c), make_float2(sc, sc), make_float2(mn, mn));
-            lo[g][i] = dev::min3(lo[g][i], y.x, y.x);
-            hi[g][i] = dev::max3(hi[g][i], y.x, y.x);
-            lo[g][i + 4] = dev::min3(lo[g][i + 4], y.y, y.y);
-            hi[g][i + 4] = dev::max3(hi[g][i + 4], y.y, y.y);
+            const uint32_t c = i % 2 ? dev::whole_odd(r.kc[e][g] >> (8 * (i / 2))) : dev::whole_even(r.kc[e][g] >> (8 * (i / 2)));
+            y[e][i] = dev::fma2(dev::h2f(c), make_float2(sc, sc), make_float2(mn, mn));
           }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lo[g][i] = dev::min3(lo[g][i], y[0][i].x, y[1][i].x);
+          hi[g][i] = dev::max3(hi[g][i], y[0][i].x, y[1][i].x);
+          lo[g][i + 4] = dev::min3(lo[g][i + 4], y[0][i].y, y[1][i].y);
+          hi[g][i + 4] = dev::max3(hi[g][i + 4], y[0][i].y, y[1][i].y);
         }
       }
     }
