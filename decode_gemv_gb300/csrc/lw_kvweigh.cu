@@ -1,5 +1,5 @@
 // Accumulated attention weight over the 4-bit cache.
-#include "lw_kvweigh.cuh"
+#include "lw_kvweighmany.cuh"
 #include "lw_kv.h"
 
 namespace lw {
@@ -19,16 +19,52 @@ lw_status launch_few_t(const WeighArgs& a, dim3 grid, cudaStream_t st) {
                                : launch_few<D, __nv_bfloat16>(a, grid, st);
 }
 
+
+// Rows of a sequence on a key/value head up to which kv_weigh_few_kernel takes a call
+constexpr int kFewMost = 64;
+
+inline int64_t row_tiles(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens) {
+  return (q_tokens * (q_heads / c->kv_heads) + 127) / 128;
+}
+inline size_t record_bytes(int D, int parts) { return (size_t)parts * D * 256 + 1024; }
+
+template <int D, class T>
+lw_status launch_many(const WeighArgs& a, void* ws, int64_t tiles, int64_t key_tiles, cudaStream_t st) {
+  constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
+  using W = WeighMany<D, kParts>;
+  const auto kernel = dev::kv_weigh_many_kernel<D, kParts>;
+  if (resident_blocks(reinterpret_cast<const void*>(kernel), W::kThreads, W::kSmem) < 1)
+    return fail(LW_ERR_CUDA, "lw_kv_weigh: the kernel does not fit this device");
+  const WeighRowsArgs r{a, static_cast<uint8_t*>(ws), (int32_t)tiles};
+  const lw_status s = kv_launch("lw_kv_weigh", dev::kv_weigh_rows_kernel<D, T>, dim3((unsigned)tiles, (unsigned)a.heads),
+                                512, 0, 1, st, r);
+  if (s != LW_OK) return s;
+  const WeighManyArgs w{a, static_cast<const uint8_t*>(ws), (int32_t)tiles};
+  // CTAs of a unit: until the device is full
+  int ranks = 1;
+  while (ranks < 8 && 2 * ranks * key_tiles * a.heads * a.p.batch <= device_sm_count()) ranks *= 2;
+  return kv_launch("lw_kv_weigh", kernel, dim3((unsigned)(key_tiles * ranks), (unsigned)a.heads, (unsigned)a.p.batch),
+                   W::kThreads, W::kSmem, ranks, st, w);
+}
+template <int D>
+lw_status launch_many_t(const WeighArgs& a, void* ws, int64_t tiles, int64_t key_tiles, cudaStream_t st) {
+  return a.p.dtype == LW_F32   ? launch_many<D, float>(a, ws, tiles, key_tiles, st)
+         : a.p.dtype == LW_F16 ? launch_many<D, __half>(a, ws, tiles, key_tiles, st)
+                               : launch_many<D, __nv_bfloat16>(a, ws, tiles, key_tiles, st);
+}
+
 }  // namespace
 }  // namespace lw
 
 using namespace lw;
 
 extern "C" size_t lw_kv_weigh_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens) {
-  (void)c;
-  (void)q_heads;
-  (void)q_tokens;
-  return 0;
+  if (!c || !lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens) || q_heads < 1 || q_heads % c->kv_heads ||
+      q_tokens < 0 || q_tokens > kKvMost / q_heads)
+    return 0;
+  // none for few rows in all: whatever sequences they are of, kv_weigh_few_kernel takes them
+  if (q_tokens * (q_heads / c->kv_heads) <= kFewMost) return 0;
+  return (size_t)c->kv_heads * row_tiles(c, q_heads, q_tokens) * record_bytes(c->head_dim, 2);
 }
 
 extern "C" lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, void* ws, size_t ws_bytes,
@@ -73,16 +109,25 @@ extern "C" lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, v
   w.group = a->q_heads / c->kv_heads;
   w.vec = kv_rows_aligned(a->q, a->q_token_stride, a->q_head_stride, a->dtype);
   w.status = d_status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int64_t keys = (int64_t)a->table_width * c->page_tokens;
+  if (a->w_keys < keys) keys = a->w_keys;
+  const int64_t rows = (a->max_q < a->q_tokens ? a->max_q : a->q_tokens) * w.group;
+  if (rows > kFewMost) {
+    const int64_t tiles = row_tiles(c, a->q_heads, a->q_tokens), key_tiles = (keys + 127) / 128;
+    return c->head_dim == 64   ? launch_many_t<64>(w, ws, tiles, key_tiles, st)
+           : c->head_dim == 96 ? launch_many_t<96>(w, ws, tiles, key_tiles, st)
+                               : launch_many_t<128>(w, ws, tiles, key_tiles, st);
+  }
   // CTAs of a sequence's head: some 32 tiles a warp (a CTA's start, its rows and first copies, is 2 us), but
   // enough CTAs for the device to be full, if a warp has a tile to do
   const int64_t pairs = (int64_t)a->batch * c->kv_heads;
-  const int64_t tiles = ((int64_t)a->table_width * c->page_tokens + 15) / 16;
+  const int64_t tiles = (keys + 15) / 16;
   const int64_t fill = (2 * device_sm_count() + pairs - 1) / pairs;
   int64_t x = (tiles + 7) / 8 < fill ? (tiles + 7) / 8 : fill;
   if (x < (tiles + 255) / 256) x = (tiles + 255) / 256;
   if (x > 65535) x = 65535;
   const dim3 grid((unsigned)x, (unsigned)c->kv_heads, (unsigned)a->batch);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   return c->head_dim == 64   ? launch_few_t<64>(w, grid, st)
          : c->head_dim == 96 ? launch_few_t<96>(w, grid, st)
                              : launch_few_t<128>(w, grid, st);

@@ -1,0 +1,388 @@
+// Accumulated attention weight for many rows (prompts), on the 5th-generation
+// tensor cores.
+//
+// S = K Q^T has the keys as its first dimension: a key is a lane of tensor
+// memory, the thread that owns it adds up its row of exponentials in registers,
+// and no reduction crosses threads.  A unit is 128 keys of one head; its rows --
+// the packed (token, head of the group) pairs of its sequence -- come 128 at a
+// time.  Operands are fp16: a key as two parts, hi + lo (22 bits; restored from
+// the codes once a unit), a 16-bit query as itself, an fp32 one as two parts.  So
+// S takes two products (three for fp32: hi hi, lo hi, hi lo) into one fp32
+// accumulator.  Queries are scaled by a power of two a row, their largest element
+// to 2^14; keys by one a unit where all of them are small.
+//
+// Two kernels.  kv_weigh_rows_kernel writes the rows as operand tiles, once for
+// all units (a unit would spend as many instructions on them as on its
+// exponentials), with each row's scale and lse in log2 units.  kv_weigh_many_kernel
+// is a CTA a unit:
+//  * warp 0 fetches row tiles by bulk copies (a tile is one contiguous image);
+//  * warp 1 issues the products, into four accumulators of 128 columns;
+//  * 8 warps restore the keys, then two groups of four take the tiles in turn:
+//    a thread reads its key's 128 scores and adds 2^(s f - lse) of those that it is
+//    seen by.  A key is seen by a contiguous range of rows (causal: from some row
+//    on, windowed: up to some row), so only tiles across an end of it are masked.
+// Units are few where keys are: then a cluster shares a unit's row tiles, and rank 0
+// adds the ranks' sums in order.
+#pragma once
+
+#include "lw_kvmany.cuh"
+#include "lw_kvselect.cuh"
+#include "lw_kvweigh.cuh"
+
+namespace lw {
+
+template <int D, int PARTS>   // parts of a query operand
+struct WeighMany {
+  using L = KvTile<D>;
+  static constexpr int kRows = 128, kKeys = 128;
+  static constexpr int kPart = D * kRows * 2;                  // bytes of one operand part of a row tile
+  static constexpr int kImage = PARTS * kPart;
+  static constexpr int kParam = kRows * 8;                     // [pair of rows] f, f, -lse, -lse
+  static constexpr int kRecord = kImage + kParam;              // of the workspace
+  static constexpr int kStages = PARTS == 1 ? 4 : 2;
+  static constexpr int kThreads = 320;
+  static constexpr int kLbo = kKeys * 16 + 32;                 // bytes between 8-element columns of the keys (32: bank offset)
+  static constexpr int kKeyPart = D / 8 * kLbo;
+  static constexpr int kHead = 1024 + 2 * kKeys * 4;           // barriers and flags, the groups' sums
+  static constexpr int kParams = kHead;                        // [4]
+  static constexpr int kA = kParams + 4 * kParam;
+  static constexpr int kB = kA + 2 * kKeyPart;
+  // over half an SM's: one CTA an SM, whose tensor memory is all of it
+  static constexpr int kNeed = kB + kStages * kImage, kSmem = kNeed > 118784 ? kNeed : 118784;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct WeighManyArgs {
+  WeighArgs a;
+  const uint8_t* rows;    // [heads][row_tiles] records
+  int32_t row_tiles;
+};
+struct WeighRowsArgs {
+  WeighArgs a;
+  uint8_t* rows;
+  int32_t row_tiles;
+};
+
+namespace dev {
+
+// One row tile of one head: 4 lanes a row, as weigh_row.
+template <int D, class T>
+__global__ void __launch_bounds__(512) kv_weigh_rows_kernel(const WeighRowsArgs w) {
+  constexpr int PARTS = sizeof(T) == 4 ? 2 : 1, G = D / 32;
+  using W = WeighMany<D, PARTS>;
+  const WeighArgs& a = w.a;
+  const int h = blockIdx.y, row = threadIdx.x / 4, q = threadIdx.x % 4;
+  pdl_wait();
+  const int64_t r = (int64_t)blockIdx.x * W::kRows + row;
+  const bool live = r < a.p.q_tokens * a.group;
+  const int64_t tok = live ? r / a.group : 0;
+  const int head = h * a.group + (int)(live ? r - tok * a.group : 0);
+  float x[G][8], top = 0.f;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    if (live)
+      weigh_load8<T>(a, tok * a.p.q_token_stride + (int64_t)head * a.p.q_head_stride + 32 * g + 8 * q, x[g]);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[g][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[g][i]));
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+  int e = (int)(__float_as_uint(top) >> 23) - 127;
+  e = e < -100 ? -100 : (e > 127 ? 127 : e);
+  const float down = __uint_as_float((uint32_t)(127 - e + 14) << 23);
+  uint8_t* rec = w.rows + ((int64_t)h * w.row_tiles + blockIdx.x) * W::kRecord;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u = x[g][i] * down, v = x[g][i + 4] * down;
+      if constexpr (PARTS == 2) split2<1>(u, v, hi[i], lo[i]);
+      else hi[i] = h2bits(__floats2half2_rn(u, v));
+    }
+    uint8_t* to = rec + (4 * g + q) * (W::kRows * 16) + row * 16;
+    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if constexpr (PARTS == 2) *reinterpret_cast<uint4*>(to + W::kPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  if (q == 0) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    float* p = reinterpret_cast<float*>(rec + W::kImage) + row / 2 * 4 + row % 2;
+    p[0] = live ? a.p.scale * __uint_as_float((uint32_t)(e - 14 + 127) << 23) * kLog2e : 0.f;
+    p[2] = live ? -a.p.lse[tok * a.p.q_heads + head] * kLog2e : -INFINITY;
+  }
+}
+
+struct WeighBars {
+  uint64_t b_full[4], b_free[4];                    // row tiles
+  uint64_t p_full[4], d_full[4], d_free[4];         // their scales and lse; accumulators
+  uint64_t last;
+};
+
+template <int D, int PARTS>
+__global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyArgs w) {
+  using W = WeighMany<D, PARTS>;
+  using L = KvTile<D>;
+  constexpr int G = L::G, S = W::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const WeighArgs& a = w.a;
+  WeighBars& bar = *reinterpret_cast<WeighBars*>(smem);
+  volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + 512);   // [0] abort
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + 516);
+  uint32_t* s_top = reinterpret_cast<uint32_t*>(smem + 520);                      // largest key magnitude, as bits
+  float* sums = reinterpret_cast<float*>(smem + 1024);                            // [2][keys]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
+  const int k0 = (int)(blockIdx.x / ranks) * W::kKeys, h = blockIdx.y, b = blockIdx.z;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.b_full[i], 1);
+      mbar_init(&bar.b_free[i], 1);
+      mbar_init(&bar.p_full[i], 1);
+      mbar_init(&bar.d_full[i], 1);
+      mbar_init(&bar.d_free[i], 4);
+    }
+    mbar_init(&bar.last, 1);
+    flags[0] = 0;
+    *s_top = 0;
+    fence_barrier_init();
+  }
+  pdl_wait();
+  int q0, T, n;
+  if (k0 == 0 && rank == 0 && h == 0 && threadIdx.x == 0) weigh_seq<true>(a, b, q0, T, n);
+  else weigh_seq<false>(a, b, q0, T, n);
+  const int keys = n < a.p.w_keys ? n : (int)a.p.w_keys;
+  if (k0 >= keys) return;   // (all of the cluster)
+  // rows that see key j of this sequence: [first_row(j), end_row(j)), packed
+  const int64_t R0 = (int64_t)q0 * a.group;
+  const int past = n - T;   // the first token's position
+  const auto first_row = [&](int j) {
+    const int64_t t = a.p.causal ? (int64_t)j - past : 0;
+    return R0 + (t < 0 ? 0 : t > T ? T : t) * a.group;
+  };
+  const auto end_row = [&](int j) {
+    const int64_t t = a.p.window ? (int64_t)j + a.p.window - past : T;
+    return R0 + (t < 0 ? 0 : t > T ? T : t) * a.group;
+  };
+  const int k1 = min(k0 + W::kKeys, keys);
+  const int64_t ra = first_row(k0), rb = end_row(k1 - 1);
+  // this rank's row tiles
+  int t0 = 0, nt = 0;
+  if (ra < rb) {
+    const int first = (int)(ra / W::kRows), all = (int)((rb - 1) / W::kRows) - first + 1;
+    t0 = first + (int)((int64_t)all * rank / ranks);
+    nt = first + (int)((int64_t)all * (rank + 1) / ranks) - t0;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tslot), 512);
+    tmem_relinquish();
+  }
+  const int kw = warp - 2;   // of the 8 key warps
+  // ---- the keys: 16 a warp, restored into two operand parts
+  uint32_t kc[2][G], ks[2][G], km[2][L::GP / 2];
+  bool there = false;
+  if (warp >= 2) {
+    const int tile = k0 / 16 + kw, tpp = a.page_tokens / LW_KV_TILE, t = lane / 4, q = lane % 4;
+    const int page = 16 * tile < keys ? a.p.page_table[(int64_t)b * a.p.table_stride + tile / tpp] : -1;
+    there = page >= 0 && page < a.n_pages;
+    if (!there && 16 * tile < keys && lane == 0) report(a.status, LW_DEV_BAD_PAGE);
+    float top = 0.f;
+    if (there) {
+      const uint8_t* s = a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tk = t + 8 * i;
+        ldg_words<G>(s + L::kKeyCodes + ((tk * 4 + q) * G) * 4, kc[i]);
+        ldg_words<G>(s + L::kKeyScale + (tk / 2 * G) * 4, ks[i]);
+        ldg_words<L::GP / 2>(s + L::kKeyMin + tk * L::GP * 2, km[i]);
+        if (16 * tile + tk < keys)
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float2 s2 = h2f(ks[i][g]), m2 = h2f(km[i][g / 2]);
+            const float sc = t % 2 ? s2.y : s2.x, mn = g % 2 ? m2.y : m2.x;
+            top = fmaxf(top, fmaxf(fabsf(mn), fabsf(fmaf(15.f, sc, mn))));
+          }
+      }
+    }
+    top = top <= 3.402823466e38f ? top : 65504.f;
+    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+    if (lane == 0) atomicMax(s_top, most);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  // all keys below 2^-4: brought up to there (lo parts would have too few bits as fp16); a power of two
+  const int ke = (int)(*s_top >> 23) - 127, lift = ke < -4 ? min(-4 - ke, 24) : 0;
+  const float up = __uint_as_float((uint32_t)(127 + lift) << 23);
+  if (warp >= 2) {
+    const int t = lane / 4, q = lane % 4;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        uint32_t hi[4] = {}, lo[4] = {};
+        if (there) {
+          const float2 s2 = h2f(ks[i][g]), m2 = h2f(km[i][g / 2]);
+          const float sc = t % 2 ? s2.y : s2.x, mn = g % 2 ? m2.y : m2.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t c = e % 2 ? whole_odd(kc[i][g] >> (8 * (e / 2))) : whole_even(kc[i][g] >> (8 * (e / 2)));
+            const float2 y = mul2(fma2(h2f(c), make_float2(sc, sc), make_float2(mn, mn)), make_float2(up, up));
+            split2<1>(y.x, y.y, hi[e], lo[e]);
+          }
+        }
+        const uint32_t to = smem_addr(smem) + W::kA + (uint32_t)((4 * g + q) * W::kLbo + (16 * kw + 8 * i + t) * 16);
+        sts_u4(to, hi[0], hi[1], hi[2], hi[3]);
+        sts_u4(to + W::kKeyPart, lo[0], lo[1], lo[2], lo[3]);
+      }
+    fence_proxy_async();
+  }
+  __syncthreads();
+  bool ok = true;
+  if (warp == 0) {   // ---- row tiles
+    if (lane == 0) {
+      const uint8_t* src = w.rows + ((int64_t)h * w.row_tiles + t0) * W::kRecord;
+      int i = 0;
+      for (; i < nt && ok; ++i, src += W::kRecord) {
+        const int s = i % S, d = i % 4;
+        ok = many_wait(&bar.b_free[s], (uint32_t)(i / S & 1) ^ 1u, flags) && many_wait(&bar.d_free[d], (uint32_t)(i / 4 & 1) ^ 1u, flags);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&bar.p_full[d], W::kParam);
+        bulk_g2s(smem + W::kParams + d * W::kParam, src + W::kImage, W::kParam, &bar.p_full[d]);
+        mbar_arrive_expect_tx(&bar.b_full[s], W::kImage);
+        bulk_g2s(smem + W::kB + s * W::kImage, src, W::kImage, &bar.b_full[s]);
+      }
+      if (!ok) {
+        flags[0] = 1;
+        report(a.status, LW_DEV_TIMEOUT);
+        for (int j = max(0, i - 4); j < i; ++j) {   // no copy may be in flight when the CTA ends
+          mbar_wait(&bar.p_full[j % 4], (uint32_t)(j / 4 & 1));
+          if (j >= i - S) mbar_wait(&bar.b_full[j % S], (uint32_t)(j / S & 1));
+        }
+      }
+    }
+  } else if (warp == 1) {   // ---- products
+    const auto wait = [&](uint64_t* x, uint32_t parity) { return __all_sync(0xFFFFFFFFu, many_wait(x, parity, flags)) != 0; };
+    const uint32_t base = smem_addr(smem), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const int count = __shfl_sync(0xFFFFFFFFu, nt, 0);
+    const uint64_t kd = sdesc(base + W::kA, W::kLbo, 128);
+    for (int i = 0; i < count && ok; ++i) {
+      const int s = i % S, d = i % 4;
+      ok = wait(&bar.d_free[d], (uint32_t)(i / 4 & 1) ^ 1u) && wait(&bar.b_full[s], (uint32_t)(i / S & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t qd = sdesc(base + W::kB + s * W::kImage, W::kRows * 16, 128);
+      const uint32_t to = tm + 128 * d;
+      if (elect_one()) {
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)   // lo hi
+          umma_bf16(to, kd + ((W::kKeyPart + 2 * x * W::kLbo) >> 4), qd + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), x > 0);
+        if constexpr (PARTS == 2) {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)   // hi lo
+            umma_bf16(to, kd + (2 * x * W::kLbo >> 4), qd + ((W::kPart + 2 * x * W::kRows * 16) >> 4), idesc_f16(W::kRows), 1);
+        }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)   // hi hi
+          umma_bf16(to, kd + (2 * x * W::kLbo >> 4), qd + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), 1);
+        umma_commit(&bar.b_free[s]);
+        umma_commit(&bar.d_full[d]);
+      }
+      __syncwarp();
+    }
+    if (!ok) {
+      flags[0] = 1;
+      if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
+    }
+    __syncwarp();
+    if (elect_one()) umma_commit(&bar.last);   // no product may be in flight when the tensor memory goes
+    __syncwarp();
+    mbar_wait(&bar.last, 0);
+  } else {   // ---- exponentials
+    const int group = kw / 4, quarter = warp % 4, key = 32 * quarter + lane, j = k0 + key;
+    const uint32_t mine = tmem + ((uint32_t)(32 * quarter) << 16);
+    // (a key past the end, or of a page that is not there, is seen by no row)
+    const int tile = k0 / 16 + key / 16;
+    bool real = j < keys;
+    if (real) {
+      const int page = a.p.page_table[(int64_t)b * a.p.table_stride + tile / (a.page_tokens / LW_KV_TILE)];
+      real = page >= 0 && page < a.n_pages;
+    }
+    const int64_t from = real ? first_row(j) : 0, to = real ? end_row(j) : 0;
+    // rows that every key of this warp sees
+    const float down = __uint_as_float((uint32_t)(127 - lift) << 23);
+    float2 total = make_float2(0.f, 0.f);
+    for (int i = group; i < nt && ok; i += 2) {
+      const int d = i % 4;
+      const int64_t r0 = (int64_t)(t0 + i) * W::kRows;
+      ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.p_full[d], (uint32_t)(i / 4 & 1), flags) &&
+                                       many_wait(&bar.d_full[d], (uint32_t)(i / 4 & 1), flags));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t params = smem_addr(smem) + W::kParams + d * W::kParam;
+      const bool whole = __all_sync(0xFFFFFFFFu, lift == 0 && from <= r0 && to >= r0 + W::kRows);
+      const int lo = (int)(from - r0 < 0 ? 0 : from - r0 > W::kRows ? W::kRows : from - r0);
+      const int hi = (int)(to - r0 < 0 ? 0 : to - r0 > W::kRows ? W::kRows : to - r0);
+      float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t z[2][32];
+      tmem_ld32(mine + 128 * d, z[0]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld_wait();
+        if (c < 3) tmem_ld32(mine + 128 * d + 32 * (c + 1), z[(c + 1) & 1]);
+        const uint32_t(&y)[32] = z[c & 1];
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float4 p = lds_f4(params + (16 * c + e) * 16);
+            const float2 x = fma2(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), make_float2(p.x, p.y),
+                                  make_float2(p.z, p.w));
+            part[e & 1] = add2(part[e & 1], make_float2(ex2(x.x), ex2(x.y)));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float4 p = lds_f4(params + (16 * c + e) * 16);
+            const float2 s = mul2(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), make_float2(down, down));
+            const float2 x = fma2(s, make_float2(p.x, p.y), make_float2(p.z, p.w));
+            const int col = 32 * c + 2 * e;
+            part[e & 1] = add2(part[e & 1], make_float2(col >= lo && col < hi ? ex2(x.x) : 0.f,
+                                                        col + 1 >= lo && col + 1 < hi ? ex2(x.y) : 0.f));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.d_free[d]);
+      total = add2(total, add2(part[0], part[1]));
+    }
+    if (!ok) {
+      flags[0] = 1;
+      if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
+    }
+    sums[group * W::kKeys + key] = total.x + total.y;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+  // the groups' sums, then the ranks', in order
+  if (threadIdx.x < W::kKeys) sums[threadIdx.x] += sums[W::kKeys + threadIdx.x];
+  if (ranks > 1) cluster_sync();
+  if (rank == 0 && threadIdx.x < W::kKeys) {
+    const int j = k0 + threadIdx.x;
+    float s = sums[threadIdx.x];
+    for (int r = 1; r < ranks; ++r) s += cluster_load(sums + threadIdx.x, (uint32_t)r);
+    if (j < keys) {
+      const float* add = a.p.add_to ? a.p.add_to + b * a.p.add_seq_stride + h * a.p.add_head_stride : nullptr;
+      (a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride)[j] = (add ? add[j] : 0.f) + s;
+    }
+  }
+  if (ranks > 1) cluster_sync();   // (a rank's sums stay until they are read)
+}
+
+}  // namespace dev
+}  // namespace lw
