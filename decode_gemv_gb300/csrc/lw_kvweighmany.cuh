@@ -16,11 +16,16 @@
 // exponentials), with each row's scale and lse in log2 units.  kv_weigh_many_kernel
 // is a CTA a unit:
 //  * warp 0 fetches row tiles by bulk copies (a tile is one contiguous image);
-//  * warp 1 issues the products, into four accumulators of 128 columns;
+//  * warp 1 issues the products, into three accumulators of 128 columns: the keys are the operand in tensor
+//    memory (both in shared memory are 8 KB for 64 cycles of products, all that it gives: 379 us where this takes
+//    350);
 //  * 8 warps restore the keys, then two groups of four take the tiles in turn:
 //    a thread reads its key's 128 scores and adds 2^(s f - lse) of those that it is
 //    seen by.  A key is seen by a contiguous range of rows (causal: from some row
 //    on, windowed: up to some row), so only tiles across an end of it are masked.
+// 2048 tokens on 14336 keys (8 heads of 128 with 4 query heads each, bf16): 350 us, 736 TFLOP/s of useful
+// products, of which two are carried out for one: 1470, three quarters of what the tensor cores give.  The rest is
+// the start of a unit (keys, tensor memory: 3 us of 46) and the last round of units.
 // Units are few where keys are: then a cluster shares a unit's row tiles, and rank 0
 // adds the ranks' sums in order.
 #pragma once
@@ -39,14 +44,13 @@ struct WeighMany {
   static constexpr int kImage = PARTS * kPart;
   static constexpr int kParam = kRows * 8;                     // [pair of rows] f, f, -lse, -lse
   static constexpr int kRecord = kImage + kParam;              // of the workspace
-  static constexpr int kStages = PARTS == 1 ? 4 : 2;
+  static constexpr int kStages = PARTS == 1 ? 4 : 3;
   static constexpr int kThreads = 320;
-  static constexpr int kLbo = kKeys * 16 + 32;                 // bytes between 8-element columns of the keys (32: bank offset)
-  static constexpr int kKeyPart = D / 8 * kLbo;
+  // tensor-memory columns: three accumulators, then the keys' parts
+  static constexpr int kBufs = 3, kKeyCol = kBufs * kRows, kKeyCols = D / 2;
   static constexpr int kHead = 1024 + 2 * kKeys * 4;           // barriers and flags, the groups' sums
-  static constexpr int kParams = kHead;                        // [4]
-  static constexpr int kA = kParams + 4 * kParam;
-  static constexpr int kB = kA + 2 * kKeyPart;
+  static constexpr int kParams = kHead;                        // [kBufs]
+  static constexpr int kB = kParams + kBufs * kParam;
   // over half an SM's: one CTA an SM, whose tensor memory is all of it
   static constexpr int kNeed = kB + kStages * kImage, kSmem = kNeed > 118784 ? kNeed : 118784;
   static_assert(kSmem <= 232448, "shared memory");
@@ -179,31 +183,27 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     tmem_alloc(smem_addr(tslot), 512);
     tmem_relinquish();
   }
-  const int kw = warp - 2;   // of the 8 key warps
-  // ---- the keys: 16 a warp, restored into two operand parts
-  uint32_t kc[2][G], ks[2][G], km[2][L::GP / 2];
-  bool there = false;
+  // ---- the keys: a lane of tensor memory each, half of their elements a group of four warps
+  const int kw = warp - 2, group = kw / 4, quarter = warp % 4, key = 32 * quarter + lane, j = k0 + key;
+  constexpr int kOct = D / 16;   // 8-element columns of a thread: words of codes
+  uint32_t kc[kOct];
+  float sc[kOct], mn[kOct];
+  bool real = false;             // (a key past the end, or of a page that is not there, is seen by no row)
   if (warp >= 2) {
-    const int tile = k0 / 16 + kw, tpp = a.page_tokens / LW_KV_TILE, t = lane / 4, q = lane % 4;
-    const int page = 16 * tile < keys ? a.p.page_table[(int64_t)b * a.p.table_stride + tile / tpp] : -1;
-    there = page >= 0 && page < a.n_pages;
-    if (!there && 16 * tile < keys && lane == 0) report(a.status, LW_DEV_BAD_PAGE);
+    const int tile = j / 16, tpp = a.page_tokens / LW_KV_TILE, tk = j % 16;
+    const int page = j < keys ? a.p.page_table[(int64_t)b * a.p.table_stride + tile / tpp] : -1;
+    real = page >= 0 && page < a.n_pages;
+    if (!real && j < keys) report(a.status, LW_DEV_BAD_PAGE);
     float top = 0.f;
-    if (there) {
+    if (real) {
       const uint8_t* s = a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int tk = t + 8 * i;
-        ldg_words<G>(s + L::kKeyCodes + ((tk * 4 + q) * G) * 4, kc[i]);
-        ldg_words<G>(s + L::kKeyScale + (tk / 2 * G) * 4, ks[i]);
-        ldg_words<L::GP / 2>(s + L::kKeyMin + tk * L::GP * 2, km[i]);
-        if (16 * tile + tk < keys)
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const float2 s2 = h2f(ks[i][g]), m2 = h2f(km[i][g / 2]);
-            const float sc = t % 2 ? s2.y : s2.x, mn = g % 2 ? m2.y : m2.x;
-            top = fmaxf(top, fmaxf(fabsf(mn), fabsf(fmaf(15.f, sc, mn))));
-          }
+      for (int i = 0; i < kOct; ++i) {
+        const int o = kOct * group + i, g = o / 4;   // column o: elements 32 g + 8 (o % 4) ..
+        kc[i] = *reinterpret_cast<const uint32_t*>(s + L::kKeyCodes + ((tk * 4 + o % 4) * G + g) * 4);
+        sc[i] = __half2float(*reinterpret_cast<const __half*>(s + L::kKeyScale + 2 * ((tk / 2 * G + g) * 2 + tk % 2)));
+        mn[i] = __half2float(*reinterpret_cast<const __half*>(s + L::kKeyMin + 2 * (tk * L::GP + g)));
+        top = fmaxf(top, fmaxf(fabsf(mn[i]), fabsf(fmaf(15.f, sc[i], mn[i]))));
       }
     }
     top = top <= 3.402823466e38f ? top : 65504.f;
@@ -218,37 +218,38 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
   const int ke = (int)(*s_top >> 23) - 127, lift = ke < -4 ? min(-4 - ke, 24) : 0;
   const float up = __uint_as_float((uint32_t)(127 + lift) << 23);
   if (warp >= 2) {
-    const int t = lane / 4, q = lane % 4;
+    const uint32_t to = tmem + ((uint32_t)(32 * quarter) << 16) + W::kKeyCol + 4 * kOct * group;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kOct; i += 2) {
+      uint32_t hi[8] = {}, lo[8] = {};
+      if (real) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        uint32_t hi[4] = {}, lo[4] = {};
-        if (there) {
-          const float2 s2 = h2f(ks[i][g]), m2 = h2f(km[i][g / 2]);
-          const float sc = t % 2 ? s2.y : s2.x, mn = g % 2 ? m2.y : m2.x;
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t c = e % 2 ? whole_odd(kc[i][g] >> (8 * (e / 2))) : whole_even(kc[i][g] >> (8 * (e / 2)));
-            const float2 y = mul2(fma2(h2f(c), make_float2(sc, sc), make_float2(mn, mn)), make_float2(up, up));
-            split2<1>(y.x, y.y, hi[e], lo[e]);
+            const uint32_t c = e % 2 ? whole_odd(kc[i + x] >> (8 * (e / 2))) : whole_even(kc[i + x] >> (8 * (e / 2)));
+            const float2 y = mul2(fma2(h2f(c), make_float2(sc[i + x], sc[i + x]), make_float2(mn[i + x], mn[i + x])), make_float2(up, up));
+            split2<1>(y.x, y.y, hi[4 * x + e], lo[4 * x + e]);
           }
-        }
-        const uint32_t to = smem_addr(smem) + W::kA + (uint32_t)((4 * g + q) * W::kLbo + (16 * kw + 8 * i + t) * 16);
-        sts_u4(to, hi[0], hi[1], hi[2], hi[3]);
-        sts_u4(to + W::kKeyPart, lo[0], lo[1], lo[2], lo[3]);
       }
-    fence_proxy_async();
+      __syncwarp();
+      tmem_st8(to + 4 * i, hi);
+      tmem_st8(to + W::kKeyCols + 4 * i, lo);
+    }
+    tmem_st_wait();
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   bool ok = true;
   if (warp == 0) {   // ---- row tiles
     if (lane == 0) {
       const uint8_t* src = w.rows + ((int64_t)h * w.row_tiles + t0) * W::kRecord;
       int i = 0;
       for (; i < nt && ok; ++i, src += W::kRecord) {
-        const int s = i % S, d = i % 4;
-        ok = many_wait(&bar.b_free[s], (uint32_t)(i / S & 1) ^ 1u, flags) && many_wait(&bar.d_free[d], (uint32_t)(i / 4 & 1) ^ 1u, flags);
+        const int s = i % S, d = i % W::kBufs;
+        ok = many_wait(&bar.b_free[s], (uint32_t)(i / S & 1) ^ 1u, flags) &&
+             many_wait(&bar.d_free[d], (uint32_t)(i / W::kBufs & 1) ^ 1u, flags);
         if (!ok) break;
         mbar_arrive_expect_tx(&bar.p_full[d], W::kParam);
         bulk_g2s(smem + W::kParams + d * W::kParam, src + W::kImage, W::kParam, &bar.p_full[d]);
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
         flags[0] = 1;
         report(a.status, LW_DEV_TIMEOUT);
         for (int j = max(0, i - 4); j < i; ++j) {   // no copy may be in flight when the CTA ends
-          mbar_wait(&bar.p_full[j % 4], (uint32_t)(j / 4 & 1));
+          if (j >= i - W::kBufs) mbar_wait(&bar.p_full[j % W::kBufs], (uint32_t)(j / W::kBufs & 1));
           if (j >= i - S) mbar_wait(&bar.b_full[j % S], (uint32_t)(j / S & 1));
         }
       }
@@ -268,26 +269,26 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     const auto wait = [&](uint64_t* x, uint32_t parity) { return __all_sync(0xFFFFFFFFu, many_wait(x, parity, flags)) != 0; };
     const uint32_t base = smem_addr(smem), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const int count = __shfl_sync(0xFFFFFFFFu, nt, 0);
-    const uint64_t kd = sdesc(base + W::kA, W::kLbo, 128);
+    const uint32_t kh = tm + W::kKeyCol, kl = kh + W::kKeyCols;
     for (int i = 0; i < count && ok; ++i) {
-      const int s = i % S, d = i % 4;
-      ok = wait(&bar.d_free[d], (uint32_t)(i / 4 & 1) ^ 1u) && wait(&bar.b_full[s], (uint32_t)(i / S & 1));
+      const int s = i % S, d = i % W::kBufs;
+      ok = wait(&bar.d_free[d], (uint32_t)(i / W::kBufs & 1) ^ 1u) && wait(&bar.b_full[s], (uint32_t)(i / S & 1));
       if (!ok) break;
       tc_fence_after();
-      const uint64_t qd = sdesc(base + W::kB + s * W::kImage, W::kRows * 16, 128);
-      const uint32_t to = tm + 128 * d;
+      const uint64_t qh = sdesc(base + W::kB + s * W::kImage, W::kRows * 16, 128), ql = qh + (W::kPart >> 4);
+      const uint32_t to = tm + W::kRows * d;
       if (elect_one()) {
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x)   // lo hi
-          umma_bf16(to, kd + ((W::kKeyPart + 2 * x * W::kLbo) >> 4), qd + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), x > 0);
+        for (int x = 0; x < D / 16; ++x)
+          umma_bf16_ta(to, kl + 8 * x, qh + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), x > 0);
         if constexpr (PARTS == 2) {
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x)   // hi lo
-            umma_bf16(to, kd + (2 * x * W::kLbo >> 4), qd + ((W::kPart + 2 * x * W::kRows * 16) >> 4), idesc_f16(W::kRows), 1);
+          for (int x = 0; x < D / 16; ++x)
+            umma_bf16_ta(to, kh + 8 * x, ql + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), 1);
         }
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x)   // hi hi
-          umma_bf16(to, kd + (2 * x * W::kLbo >> 4), qd + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), 1);
+        for (int x = 0; x < D / 16; ++x)
+          umma_bf16_ta(to, kh + 8 * x, qh + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), 1);
         umma_commit(&bar.b_free[s]);
         umma_commit(&bar.d_full[d]);
       }
@@ -302,24 +303,15 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     __syncwarp();
     mbar_wait(&bar.last, 0);
   } else {   // ---- exponentials
-    const int group = kw / 4, quarter = warp % 4, key = 32 * quarter + lane, j = k0 + key;
     const uint32_t mine = tmem + ((uint32_t)(32 * quarter) << 16);
-    // (a key past the end, or of a page that is not there, is seen by no row)
-    const int tile = k0 / 16 + key / 16;
-    bool real = j < keys;
-    if (real) {
-      const int page = a.p.page_table[(int64_t)b * a.p.table_stride + tile / (a.page_tokens / LW_KV_TILE)];
-      real = page >= 0 && page < a.n_pages;
-    }
     const int64_t from = real ? first_row(j) : 0, to = real ? end_row(j) : 0;
-    // rows that every key of this warp sees
     const float down = __uint_as_float((uint32_t)(127 - lift) << 23);
     float2 total = make_float2(0.f, 0.f);
     for (int i = group; i < nt && ok; i += 2) {
-      const int d = i % 4;
+      const int d = i % W::kBufs;
       const int64_t r0 = (int64_t)(t0 + i) * W::kRows;
-      ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.p_full[d], (uint32_t)(i / 4 & 1), flags) &&
-                                       many_wait(&bar.d_full[d], (uint32_t)(i / 4 & 1), flags));
+      ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.p_full[d], (uint32_t)(i / W::kBufs & 1), flags) &&
+                                       many_wait(&bar.d_full[d], (uint32_t)(i / W::kBufs & 1), flags));
       if (!ok) break;
       tc_fence_after();
       const uint32_t params = smem_addr(smem) + W::kParams + d * W::kParam;
@@ -328,11 +320,11 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
       const int hi = (int)(to - r0 < 0 ? 0 : to - r0 > W::kRows ? W::kRows : to - r0);
       float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       uint32_t z[2][32];
-      tmem_ld32(mine + 128 * d, z[0]);
+      tmem_ld32(mine + W::kRows * d, z[0]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         tmem_ld_wait();
-        if (c < 3) tmem_ld32(mine + 128 * d + 32 * (c + 1), z[(c + 1) & 1]);
+        if (c < 3) tmem_ld32(mine + W::kRows * d + 32 * (c + 1), z[(c + 1) & 1]);
         const uint32_t(&y)[32] = z[c & 1];
         if (whole) {
 #pragma unroll
