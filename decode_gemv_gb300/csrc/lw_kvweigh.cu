@@ -5,20 +5,24 @@
 namespace lw {
 namespace {
 
-template <int D, class T>
+template <int D, class T, bool ONE>
 lw_status launch_few(const WeighArgs& a, dim3 grid, cudaStream_t st) {
-  using W = WeighFew<D, T>;
-  if (resident_blocks(reinterpret_cast<const void*>(dev::kv_weigh_few_kernel<D, T>), W::kThreads, W::kSmem) < 1)
+  using W = WeighFew<D, T, ONE>;
+  const auto kernel = dev::kv_weigh_few_kernel<D, T, ONE>;
+  if (resident_blocks(reinterpret_cast<const void*>(kernel), W::kThreads, W::kSmem) < 1)
     return fail(LW_ERR_CUDA, "lw_kv_weigh: the kernel does not fit this device");
-  return kv_launch("lw_kv_weigh", dev::kv_weigh_few_kernel<D, T>, grid, W::kThreads, W::kSmem, 1, st, a);
+  return kv_launch("lw_kv_weigh", kernel, grid, W::kThreads, W::kSmem, 1, st, a);
+}
+template <int D, bool ONE>
+lw_status launch_few_t(const WeighArgs& a, dim3 grid, cudaStream_t st) {
+  return a.p.dtype == LW_F32   ? launch_few<D, float, ONE>(a, grid, st)
+         : a.p.dtype == LW_F16 ? launch_few<D, __half, ONE>(a, grid, st)
+                               : launch_few<D, __nv_bfloat16, ONE>(a, grid, st);
 }
 template <int D>
-lw_status launch_few_t(const WeighArgs& a, dim3 grid, cudaStream_t st) {
-  return a.p.dtype == LW_F32   ? launch_few<D, float>(a, grid, st)
-         : a.p.dtype == LW_F16 ? launch_few<D, __half>(a, grid, st)
-                               : launch_few<D, __nv_bfloat16>(a, grid, st);
+lw_status launch_few_d(const WeighArgs& a, bool one, dim3 grid, cudaStream_t st) {
+  return one ? launch_few_t<D, true>(a, grid, st) : launch_few_t<D, false>(a, grid, st);
 }
-
 
 // Rows of a sequence on a key/value head up to which kv_weigh_few_kernel takes a call
 constexpr int kFewMost = 64;
@@ -120,15 +124,14 @@ extern "C" lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, v
                                : launch_many_t<128>(w, ws, tiles, key_tiles, st);
   }
   // CTAs of a sequence's head: some 32 tiles a warp (a CTA's start, its rows and first copies, is 2 us), but
-  // enough CTAs for the device to be full, if a warp has a tile to do
+  // enough CTAs for the device to be full, if a warp has a pair of tiles to do
   const int64_t pairs = (int64_t)a->batch * c->kv_heads;
   const int64_t tiles = (keys + 15) / 16;
   const int64_t fill = (2 * device_sm_count() + pairs - 1) / pairs;
-  int64_t x = (tiles + 7) / 8 < fill ? (tiles + 7) / 8 : fill;
+  int64_t x = (tiles + 15) / 16 < fill ? (tiles + 15) / 16 : fill;
   if (x < (tiles + 255) / 256) x = (tiles + 255) / 256;
-  if (x > 65535) x = 65535;
   const dim3 grid((unsigned)x, (unsigned)c->kv_heads, (unsigned)a->batch);
-  return c->head_dim == 64   ? launch_few_t<64>(w, grid, st)
-         : c->head_dim == 96 ? launch_few_t<96>(w, grid, st)
-                             : launch_few_t<128>(w, grid, st);
+  return c->head_dim == 64   ? launch_few_d<64>(w, rows <= 8, grid, st)
+         : c->head_dim == 96 ? launch_few_d<96>(w, rows <= 8, grid, st)
+                             : launch_few_d<128>(w, rows <= 8, grid, st);
 }
