@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(WeighFew<D, T, ONE>::kThreads, WeighFew<D, T, 
         f.send(a, lane);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (!(some >> u & 1u)) continue;
+          // (ONE: without a branch, so that the two tiles' chains interleave; what is not there is dropped below)
+          if (!ONE && !(some >> u & 1u)) continue;
           const int j0 = 16 * (tile + u);
           // (ONE: the codes become operands group by group; else once for all blocks)
           uint32_t c[ONE ? 1 : G][2][4];
@@ -348,11 +349,11 @@ __global__ void __launch_bounds__(WeighFew<D, T, ONE>::kThreads, WeighFew<D, T, 
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = ex2(fmaf(z[i], row[i % 2].x, -row[i % 2].y) * 1.4426950408889634f);
-            if (j0 < range.x || j0 + 16 > range.y) {
+            if (j0 < range.x || j0 + 16 > range.y || (ONE && !(some >> u & 1u))) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int j = j0 + t + 8 * (i / 2);
-                if (j < __float_as_int(row[i % 2].z) || j >= __float_as_int(row[i % 2].w)) w[i] = 0.f;
+                if (j < __float_as_int(row[i % 2].z) || j >= __float_as_int(row[i % 2].w) || !(some >> u & 1u)) w[i] = 0.f;
               }
             }
             sum[2 * u] += w[0] + w[1];
