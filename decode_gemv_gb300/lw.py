@@ -775,6 +775,7 @@ class KvCache:
         self.index = pages.get_device()   # -1: not on a CUDA device, which the calls refuse
         self.view = LwKvCache(ptr, self.n_pages, self.kv_heads, self.head_dim, self.page_tokens, 0)
         self.ref = ctypes.byref(self.view)
+        self.summary_bytes = int(load().lw_kv_summary_bytes(self.ref))
 
     @classmethod
     def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page_tokens: int, device="cuda"):
@@ -1080,6 +1081,17 @@ def _kv_same_rows(a, b) -> bool:
     return a.data_ptr() == b.data_ptr() and a.stride() == b.stride()
 
 
+def _kv_written_beside(q_out, qp, k, v) -> bool:
+    """A quick yes to what the usual call needs: q_out's rows are distinct, are q's (at `qp`, of q_out's strides) or
+    share no byte with them, and share none with k's and v's."""
+    if q_out.is_contiguous() and k.is_contiguous() and v.is_contiguous():
+        at, n = q_out.data_ptr(), q_out.nbytes
+        kp, vp, kn = k.data_ptr(), v.data_ptr(), k.nbytes
+        return ((at == qp or at + n <= qp or qp + n <= at) and (at + n <= kp or kp + kn <= at)
+                and (at + n <= vp or vp + kn <= at))
+    return False
+
+
 def _kv_rotary_refuse(fn, cache, k, v, slots, positions, table, d_status, q, q_out):
     import torch
     _kv_index(fn, "slots", slots, _I64, None)
@@ -1143,10 +1155,10 @@ def lw_kv_write_rotary(cache: KvCache, k, v, slots, positions, table, d_status, 
             qp, op, (qt, qh, qd), (ot, oh, od) = q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
             ok = (ok and q.dtype is k.dtype and q_out.dtype is k.dtype and heads > 0
                   and q.shape == (n, heads, cache.head_dim) and q_out.shape == q.shape and qd == 1
-                  and od == 1 and _kv_distinct(q_out) and q.get_device() == dev
-                  and q_out.get_device() == dev
-                  and ((qp == op and qt == ot and qh == oh) or _kv_apart(q, q_out))
-                  and _kv_beside(q_out, k) and _kv_beside(q_out, v))
+                  and od == 1 and q.get_device() == dev and q_out.get_device() == dev
+                  and ((qt == ot and qh == oh and _kv_written_beside(q_out, qp, k, v))
+                       or (_kv_distinct(q_out) and ((qp == op and qt == ot and qh == oh) or _kv_apart(q, q_out))
+                           and _kv_beside(q_out, k) and _kv_beside(q_out, v))))
     except (AttributeError, TypeError, ValueError, IndexError):
         ok = False
     if not ok:
@@ -1346,7 +1358,7 @@ def lw_kv_evict(cache: KvCache, weights, kv_len, page_table, out_table, out_len,
 # ---- sparse attention ----------------------------------------------------------
 
 def lw_kv_summary_bytes(cache: KvCache) -> int:
-    return int(load().lw_kv_summary_bytes(cache.ref))
+    return cache.summary_bytes
 
 
 def _kv_summary(fn, cache, summary):
@@ -1363,7 +1375,7 @@ def lw_kv_summarise(cache: KvCache, summary, start, kv_len, page_table, d_status
         ok = (start.dtype is _I32 and start.shape == (batch,) and start.is_contiguous()
               and kv_len.dtype is _I32 and kv_len.shape == (batch,) and kv_len.is_contiguous()
               and page_table.dtype is _I32 and (td == 1 or width <= 1) and summary.is_contiguous()
-              and summary.numel() * summary.element_size() >= lw_kv_summary_bytes(cache)
+              and summary.nbytes >= cache.summary_bytes
               and d_status.dtype is _I32 and d_status.numel() >= 1 and d_status.is_contiguous()
               and dev >= 0 and _current_device() == dev and summary.get_device() == dev
               and start.get_device() == dev and kv_len.get_device() == dev
@@ -1448,7 +1460,7 @@ def lw_kv_attention_blocks(cache: KvCache, summary, q, q_start, kv_len, page_tab
               and q_start.dtype is _I32 and q_start.shape == (batch + 1,) and q_start.is_contiguous()
               and kv_len.dtype is _I32 and kv_len.shape == (batch,) and kv_len.is_contiguous()
               and page_table.dtype is _I32 and (td == 1 or width <= 1) and summary.is_contiguous()
-              and summary.numel() * summary.element_size() >= lw_kv_summary_bytes(cache)
+              and summary.nbytes >= cache.summary_bytes
               and ws.is_contiguous() and d_status.dtype is _I32 and d_status.numel() >= 1
               and d_status.is_contiguous() and type(blocks) is int and type(first) is int
               and type(recent) is int and dev >= 0 and _current_device() == dev
