@@ -44,7 +44,7 @@ def test_generation(typ):
 
     # ---- the prompts: one product's output, queries rotated in place
     qkv = torch.randn(total, HQ + 2 * H, D, device=DEV, generator=gen).to(typ)
-    before = qkv.float()
+    before = qkv.float().clone()     # (the rotation is in place)
     q, k, v = qkv[:, :HQ], qkv[:, HQ:HQ + H], qkv[:, HQ + H:]
     pos = torch.cat([torch.arange(n, device=DEV) for n in LENS])
     slots = torch.cat([slots_of(table[b], range(n), PAGE) for b, n in enumerate(LENS)])
