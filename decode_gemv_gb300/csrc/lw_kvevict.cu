@@ -164,16 +164,102 @@ __global__ void __launch_bounds__(kSelect) kv_evict_select_kernel(const EvictArg
 }
 
 // ---- the move ------------------------------------------------------------------
-// A cluster a head; every warp assembles one tile of 16 kept tokens a round.  A
-// round's tokens are all read before any is written (a barrier of the cluster
-// between), and later rounds' tokens lie behind its places (kept[i] >= i): the
-// places may be the source's own.
+// A cluster a head; every warp assembles one tile of 16 kept tokens a round,
+// while the next round's tokens are looked up.  In place a round's tokens are all
+// read before any is written (a barrier of the cluster between), and later
+// rounds' tokens lie behind its places (kept[i] >= i); into other pages, the
+// warps need not wait for one another.
+// 64 heads' 8192 of 65536 keys: 58 us into other pages, 66 in place; the choice 30.  The 84 MB that move are read as
+// some 235: a token of 160 bytes lies in ten sectors (its pair's value codes, scales and minimums beside its own),
+// and memory gives 64 bytes at a time: 47 us at a copy's rate.
 constexpr int kMoveWarps = 16, kMove = 32 * kMoveWarps;
+
+// The tokens of a tile: lane i (and i + 16) has the i-th.
+struct MoveTokens {
+  int64_t src;   // its tile, -1 if there is none
+  int j;         // its key, -1 if there is none
+  float weight;
+};
+
+template <int D>
+struct MoveTile {
+  using L = KvTile<D>;
+  static constexpr int G = L::G;
+  static constexpr int kCodes = 2 * D / 32;   // words of key codes a lane; of value codes as many
+  uint32_t kc[kCodes], vc[kCodes], km, ks, vs, vm;
+
+  // tile and place of the token in lane t (all lanes ask)
+  static __device__ __forceinline__ const uint8_t* token(const uint8_t* pages, const MoveTokens& x, int t, int& tt) {
+    const int64_t s = __shfl_sync(0xFFFFFFFFu, x.src, t);
+    tt = __shfl_sync(0xFFFFFFFFu, x.j, t) & 15;
+    return pages + (s < 0 ? 0 : s);   // (what is not there is read from the first tile, and not written)
+  }
+  __device__ __forceinline__ void read(const uint8_t* pages, const MoveTokens& x, int lane) {
+#pragma unroll
+    for (int i = 0; i < kCodes; ++i) {
+      const int at = lane + 32 * i;
+      int tt;
+      const uint8_t* s = token(pages, x, at / (D / 8), tt);
+      kc[i] = *reinterpret_cast<const uint32_t*>(s + L::kKeyCodes + 4 * (tt * (D / 8) + at % (D / 8)));
+    }
+    {
+      constexpr int kPer = L::GP / 2;
+      const int at = lane % (16 * kPer);
+      int tt;
+      const uint8_t* s = token(pages, x, at / kPer, tt);
+      km = *reinterpret_cast<const uint32_t*>(s + L::kKeyMin + 4 * (tt * kPer + at % kPer));
+    }
+    // words of two tokens
+#pragma unroll
+    for (int i = 0; i < kCodes; ++i) {
+      const int at = lane + 32 * i, p = at / (8 * G), r = at % (8 * G);
+      uint32_t v = 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        int tt;
+        const uint8_t* s = token(pages, x, 2 * p + e, tt);
+        v |= (uint32_t) * reinterpret_cast<const uint16_t*>(s + L::kValCodes + 4 * (tt / 2 * 8 * G + r) + 2 * (tt % 2)) << (16 * e);
+      }
+      vc[i] = v;
+    }
+    const int at = lane % (8 * G), p = at / G, g = at % G;
+    ks = vs = vm = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      int tt;
+      const uint8_t* s = token(pages, x, 2 * p + e, tt);
+      const int o = 4 * (tt / 2 * G + g) + 2 * (tt % 2);
+      ks |= (uint32_t) * reinterpret_cast<const uint16_t*>(s + L::kKeyScale + o) << (16 * e);
+      vs |= (uint32_t) * reinterpret_cast<const uint16_t*>(s + L::kValScale + o) << (16 * e);
+      vm |= (uint32_t) * reinterpret_cast<const uint16_t*>(s + L::kValMin + o) << (16 * e);
+    }
+  }
+  // `have`: which tokens there are
+  __device__ __forceinline__ void write(uint8_t* dst, uint32_t have, int lane) const {
+    const auto put = [&](uint8_t* at, uint32_t v, int t) {   // a word of tokens t and t + 1
+      if ((have >> t & 3u) == 3u) *reinterpret_cast<uint32_t*>(at) = v;
+      else if (have >> t & 1u) *reinterpret_cast<uint16_t*>(at) = (uint16_t)v;
+      else if (have >> (t + 1) & 1u) *reinterpret_cast<uint16_t*>(at + 2) = (uint16_t)(v >> 16);
+    };
+#pragma unroll
+    for (int i = 0; i < kCodes; ++i) {
+      const int at = lane + 32 * i;
+      if (have >> (at / (D / 8)) & 1u) *reinterpret_cast<uint32_t*>(dst + L::kKeyCodes + 4 * at) = kc[i];
+      put(dst + L::kValCodes + 4 * at, vc[i], 2 * (at / (8 * G)));
+    }
+    constexpr int kPer = L::GP / 2;
+    if (lane < 16 * kPer && (have >> (lane / kPer) & 1u)) *reinterpret_cast<uint32_t*>(dst + L::kKeyMin + 4 * lane) = km;
+    if (lane < 8 * G) {
+      put(dst + L::kKeyScale + 4 * lane, ks, 2 * (lane / G));
+      put(dst + L::kValScale + 4 * lane, vs, 2 * (lane / G));
+      put(dst + L::kValMin + 4 * lane, vm, 2 * (lane / G));
+    }
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kMove, 2) kv_evict_move_kernel(const EvictArgs a) {
   using L = KvTile<D>;
-  constexpr int G = L::G;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int ranks = (int)dev::cluster_size(), rank = (int)dev::cluster_rank();
   const int h = blockIdx.y, b = blockIdx.z, tpp = a.page_tokens / LW_KV_TILE;
@@ -185,109 +271,52 @@ __global__ void __launch_bounds__(kMove, 2) kv_evict_move_kernel(const EvictArgs
   const float* w = a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride;
   float* ow = a.p.out_weights ? a.p.out_weights + b * a.p.ow_seq_stride + h * a.p.ow_head_stride : nullptr;
   const int tiles = (m + 15) / 16, step = ranks * kMoveWarps;
-  for (int t0 = 0; t0 < tiles; t0 += step) {
-    const int tile = t0 + rank * kMoveWarps + warp;
-    const bool mine = tile < tiles;
-    uint8_t* dst = nullptr;
-    float weight = 0.f;
-    uint32_t have = 0;
-    bool stay = false;
-    constexpr int kCodes = 2 * D / 32;   // words of key codes a lane; of value codes as many
-    uint32_t kc[kCodes], vc[kCodes], km = 0, ks = 0, vs = 0, vm = 0;
-    if (mine) {
-      const int page_to = to[tile / tpp];
-      const bool dst_ok = page_to >= 0 && page_to < a.n_pages;
-      if (!dst_ok && lane == 0) dev::report(a.status, LW_DEV_BAD_PAGE);
-      if (dst_ok) dst = a.pages + page_to * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
-      // lanes 0..15: a token each
-      const int i = 16 * tile + lane % 16;
-      const int j = i < m ? kept[i] : -1;
-      int64_t src = -1;   // the token's tile
-      if (j >= 0) {
-        const int page = from[j / a.page_tokens];
-        if (page >= 0 && page < a.n_pages)
-          src = page * a.page_bytes + ((int64_t)h * tpp + (j / LW_KV_TILE) % tpp) * L::kBytes;
-        else dev::report(a.status, LW_DEV_BAD_PAGE);
-        if (ow) weight = w[j];
-      }
-      have = __ballot_sync(0xFFFFFFFFu, src >= 0) & 0xFFFFu;
-      // all in their places already
-      stay = __all_sync(0xFFFFFFFFu, src < 0 || (a.pages + src == dst && j % 16 == lane % 16));
-      const auto tok = [&](int t, int& tt) -> const uint8_t* {   // tile and place of the t-th token (all lanes)
-        const int64_t s = __shfl_sync(0xFFFFFFFFu, src, t);
-        tt = __shfl_sync(0xFFFFFFFFu, j, t) & 15;
-        return a.pages + (s < 0 ? 0 : s);
-      };
-      if (!stay) {
-#pragma unroll
-        for (int x = 0; x < kCodes; ++x) {
-          const int i = lane + 32 * x, t = i / (D / 8);
-          int tt;
-          const uint8_t* s = tok(t, tt);
-          kc[x] = *reinterpret_cast<const uint32_t*>(s + L::kKeyCodes + 4 * (tt * (D / 8) + i % (D / 8)));
-        }
-        {
-          constexpr int kPer = L::GP / 2;
-          const int i = lane % (16 * kPer), t = i / kPer;
-          int tt;
-          const uint8_t* s = tok(t, tt);
-          km = *reinterpret_cast<const uint32_t*>(s + L::kKeyMin + 4 * (tt * kPer + i % kPer));
-        }
-        // words of two tokens: halves of token 2 p and 2 p + 1
-#pragma unroll
-        for (int x = 0; x < kCodes; ++x) {
-          const int i = lane + 32 * x, p = i / (8 * G), r = i % (8 * G);
-          uint32_t v = 0;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            int tt;
-            const uint8_t* s = tok(2 * p + e, tt);
-            v |= (uint32_t) * reinterpret_cast<const uint16_t*>(s + L::kValCodes + 4 * (tt / 2 * 8 * G + r) + 2 * (tt % 2)) << (16 * e);
-          }
-          vc[x] = v;
-        }
-        {
-          const int i = lane % (8 * G), p = i / G, g = i % G;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            int tt;
-            const uint8_t* s = tok(2 * p + e, tt);
-            const int at = 4 * (tt / 2 * G + g) + 2 * (tt % 2);
-            ks |= (uint32_t) * reinterpret_cast<const uint16_t*>(s + L::kKeyScale + at) << (16 * e);
-            vs |= (uint32_t) * reinterpret_cast<const uint16_t*>(s + L::kValScale + at) << (16 * e);
-            vm |= (uint32_t) * reinterpret_cast<const uint16_t*>(s + L::kValMin + at) << (16 * e);
-          }
-        }
-      }
+  // places that are read as well (the same in all of the cluster)
+  const bool in_place = tiles > 0 && (from[0] == to[0] || w == ow);
+  const auto key_of = [&](int tile) {   // this lane's kept key
+    const int i = 16 * tile + lane % 16;
+    return tile < tiles && i < m ? kept[i] : -1;
+  };
+  const auto look = [&](int j) {
+    MoveTokens x{-1, j, 0.f};
+    if (j >= 0) {
+      const int page = from[j / a.page_tokens];
+      if (page >= 0 && page < a.n_pages)
+        x.src = page * a.page_bytes + ((int64_t)h * tpp + (j / LW_KV_TILE) % tpp) * L::kBytes;
+      else dev::report(a.status, LW_DEV_BAD_PAGE);
+      if (ow) x.weight = w[j];
     }
-    dev::cluster_sync();
-    if (mine) {
-      const int i = 16 * tile + lane;
-      if (ow && lane < 16 && i < m) ow[i] = weight;
-      if (dst && !stay) {
-        const auto put = [&](uint8_t* at, uint32_t v, int t) {   // a word of tokens t and t + 1
-          if ((have >> t & 3u) == 3u) *reinterpret_cast<uint32_t*>(at) = v;
-          else if (have >> t & 1u) *reinterpret_cast<uint16_t*>(at) = (uint16_t)v;
-          else if (have >> (t + 1) & 1u) *reinterpret_cast<uint16_t*>(at + 2) = (uint16_t)(v >> 16);
-        };
-#pragma unroll
-        for (int x = 0; x < kCodes; ++x) {
-          const int i = lane + 32 * x;
-          if (have >> (i / (D / 8)) & 1u) *reinterpret_cast<uint32_t*>(dst + L::kKeyCodes + 4 * i) = kc[x];
-          put(dst + L::kValCodes + 4 * i, vc[x], 2 * (i / (8 * G)));
-        }
-        constexpr int kPer = L::GP / 2;
-        if (lane < 16 * kPer && (have >> (lane / kPer) & 1u)) *reinterpret_cast<uint32_t*>(dst + L::kKeyMin + 4 * lane) = km;
-        if (lane < 8 * G) {
-          put(dst + L::kKeyScale + 4 * lane, ks, 2 * (lane / G));
-          put(dst + L::kValScale + 4 * lane, vs, 2 * (lane / G));
-          put(dst + L::kValMin + 4 * lane, vm, 2 * (lane / G));
-        }
-      }
+    return x;
+  };
+  const auto place = [&](int tile) -> uint8_t* {
+    if (tile >= tiles) return nullptr;
+    const int page = to[tile / tpp];
+    if (page < 0 || page >= a.n_pages) {
+      if (lane == 0) dev::report(a.status, LW_DEV_BAD_PAGE);
+      return nullptr;
     }
+    return a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
+  };
+  int tile = rank * kMoveWarps + warp;
+  MoveTokens x = look(key_of(tile));
+  int next_key = key_of(tile + step);
+  for (int t0 = 0; t0 < tiles; t0 += step, tile += step) {
+    uint8_t* const dst = place(tile);
+    // a tile whose tokens are all in their places already is left as it is
+    const bool stay = __all_sync(0xFFFFFFFFu, x.src < 0 || (a.pages + x.src == dst && x.j % 16 == lane % 16));
+    const uint32_t have = __ballot_sync(0xFFFFFFFFu, x.src >= 0) & 0xFFFFu;
+    const bool move = dst && !stay;
+    MoveTile<D> z;
+    if (move) z.read(a.pages, x, lane);
+    const MoveTokens y = look(next_key);   // (behind this round's places)
+    next_key = key_of(tile + 2 * step);
+    if (in_place) dev::cluster_sync();
+    if (ow && lane < 16 && x.j >= 0) ow[16 * tile + lane] = x.weight;
+    if (move) z.write(dst, have, lane);
+    x = y;
   }
   if (!ow) return;
-  dev::cluster_sync();   // (weights behind the kept ones' places were read by then)
+  if (in_place) dev::cluster_sync();   // (weights behind the kept ones' places have been read by then)
   const int64_t end = n < a.p.ow_keys ? n : a.p.ow_keys;
   for (int64_t i = m + rank * kMove + (int)threadIdx.x; i < end; i += ranks * kMove) ow[i] = 0.f;
 }
