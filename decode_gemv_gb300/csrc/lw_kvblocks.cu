@@ -182,52 +182,44 @@ __global__ void __launch_bounds__(32 * kSumWarps, 2) kv_summarise_kernel(const S
 struct BlockArgs {
   lw_kv_attn p;
   lw_kv_blocks s;
-  float* scores;         // [q_tokens * heads][table_width]
   int32_t* pages;        // [q_tokens * heads][blocks]: pages of the cache seen head by head
   int32_t* lens;         // [q_tokens * heads]: keys in them, -1 for a token of no sequence
   int64_t n_pages;
-  int32_t page_tokens, heads, group, vec;
+  int32_t page_tokens, heads, group, most_pages;   // most_pages: of a CTA's stretch
   int32_t* status;
 };
 
-// The sequence that has query token `tok`, the token's key position in it, its row of the page table; false
-// if there is none.  Whole CTA.
-__device__ __forceinline__ bool token_seq(const BlockArgs& a, int tok, int* s_seq, int& b, int& pos) {
-  if (threadIdx.x == 0) *s_seq = 0x7FFFFFFF;
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.p.batch; i += blockDim.x) {
-    const int q0 = a.p.q_start[i], q1 = a.p.q_start[i + 1];
-    if (q0 >= 0 && q1 <= a.p.q_tokens && q0 <= tok && tok < q1) atomicMin(s_seq, i);
-  }
-  __syncthreads();
-  b = *s_seq;
-  if (b == 0x7FFFFFFF) return false;
-  const int len = a.p.kv_len[b], most = a.p.table_width * a.page_tokens;
-  const int n = len < 0 ? 0 : (len > most ? most : len);
-  pos = (int)((int64_t)n - a.p.q_start[b + 1] + tok);
-  return true;
-}
+constexpr int kMostGroup = 128, kChoose = 256;
+using ChooseShared = dev::SelectShared<8>;
 
-constexpr int kScoreWarps = 8, kScoreBlocks = 256;   // pages a CTA scores at most
-constexpr int kMostGroup = 256;
-
-// Codes of the group's query heads -- their positive and negative parts apart, so that the larger of c hi and
-// c lo is picked by a product: sum c+ hi + c- lo -- and the pages' scores.  8 lanes a record.
+// The pages of one query token and key/value head, ascending.  A cluster a token and head: its CTAs score stretches of
+// the pages and choose together (lw_kvselect.cuh).
+// Scores.  The codes of the group's query heads have their positive and negative parts apart, so that the larger of
+// c hi and c lo is picked by a product: sum c+ hi + c- lo, in whole numbers (dp4a).  8 lanes take a record.
 template <int D, class T>
-__global__ void __launch_bounds__(32 * kScoreWarps) kv_score_kernel(const BlockArgs a) {
-  constexpr int W = D / 32;            // words a lane
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_seq;
-  uint32_t* codes = reinterpret_cast<uint32_t*>(smem);                  // [group][2][8][W]
-  float* units = reinterpret_cast<float*>(smem + (size_t)a.group * 2 * D);
-  const int h = blockIdx.y, tok = blockIdx.z, warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane % 8;
+__global__ void __launch_bounds__(kChoose) kv_choose_kernel(const BlockArgs a) {
+  constexpr int W = D / 32, NT = kChoose, kWarps = NT / 32;   // W: words of a part of a record a lane
+  extern __shared__ __align__(16) uint32_t smem[];
+  ChooseShared& s = *reinterpret_cast<ChooseShared*>(smem);
+  uint32_t* keys = smem + sizeof(ChooseShared) / 4;      // [a.most_pages]
+  uint32_t* codes = keys + a.most_pages;                      // [group][2][8][W]
+  float* units = reinterpret_cast<float*>(codes + a.group * (D / 2));
+  __shared__ int s_seq, s_pos;
+  const int h = blockIdx.y, tok = blockIdx.z, tid = threadIdx.x, warp = tid / 32, lane = tid % 32, r = lane % 8;
+  const int rank = (int)dev::cluster_rank(), self = rank * NT + tid, all = (int)dev::cluster_size() * NT;
+  for (int i = tid; i < ChooseShared::kPasses * ChooseShared::kBins; i += NT) s.hist[i] = 0;
+  if (tid == 0) s_seq = 0x7FFFFFFF;
   dev::pdl_wait();
-  int b, pos;
-  if (!token_seq(a, tok, &s_seq, b, pos) || pos < 0) return;
-  const int nb = pos / a.page_tokens + 1, x0 = blockIdx.x * kScoreBlocks;
-  if (x0 >= nb || nb <= a.s.blocks) return;   // all are read: no scores are needed
-  // four heads a warp at a time
-  for (int g0 = 4 * warp; g0 < a.group; g0 += 4 * kScoreWarps) {
+  // the sequences' ranges, a thread one: sent for before the queries are, so that their ways overlap
+  int q0 = -1, q1 = -1, len = 0;
+  const auto sequence = [&](int i) {
+    q0 = i < a.p.batch ? a.p.q_start[i] : -1;
+    q1 = i < a.p.batch ? a.p.q_start[i + 1] : -1;
+    len = i < a.p.batch ? a.p.kv_len[i] : 0;
+  };
+  sequence(tid);
+  // ---- the queries' codes, four heads a warp at a time
+  for (int g0 = 4 * warp; g0 < a.group; g0 += 4 * kWarps) {
     const int g = g0 + lane / 8;
     const T* q = static_cast<const T*>(a.p.q) + (int64_t)tok * a.p.q_token_stride +
                  (int64_t)(h * a.group + (g < a.group ? g : 0)) * a.p.q_head_stride + r * (D / 8);
@@ -261,58 +253,23 @@ __global__ void __launch_bounds__(32 * kScoreWarps) kv_score_kernel(const BlockA
     if (g < a.group && r == 0) units[g] = zero ? 0.f : __fmul_rn(top, (float)(1.0 / 127.0));
   }
   __syncthreads();
-  const int32_t* table = a.p.page_table + (int64_t)b * a.p.table_stride;
-  float* scores = a.scores + ((int64_t)tok * a.heads + h) * a.p.table_width;
-  const int end = min(nb, x0 + kScoreBlocks);
-  for (int x1 = x0 + 4 * warp; x1 < end; x1 += 4 * kScoreWarps) {
-    const int x = x1 + lane / 8;
-    const int page = x < end ? table[x] : -1;
-    const bool ok = page >= 0 && page < a.n_pages;
-    const uint8_t* rec = static_cast<const uint8_t*>(a.s.summary) + ((int64_t)(ok ? page : 0) * a.heads + h) * record_bytes(D);
-    uint32_t hi[W], lo[W];
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      hi[w] = *reinterpret_cast<const uint32_t*>(rec + (r * W + w) * 4);
-      lo[w] = *reinterpret_cast<const uint32_t*>(rec + D + (r * W + w) * 4);
-    }
-    const float step = *reinterpret_cast<const float*>(rec + 2 * D);
-    float best = -INFINITY;
-    for (int g = 0; g < a.group; ++g) {
-      int dot = 0;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        dot = __dp4a((int)codes[((g * 2) * 8 + r) * W + w], (int)hi[w], dot);
-        dot = __dp4a((int)codes[((g * 2 + 1) * 8 + r) * W + w], (int)lo[w], dot);
-      }
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-      best = fmaxf(best, __fmul_rn(units[g], (float)dot));
-    }
-    // (a page outside the cache is read by nobody: the attention leaves it out)
-    if (r == 0 && x < end) scores[x] = ok ? __fmul_rn(step, best) : -INFINITY;
+  // ---- the sequence that has the token, and the token's key position
+  const int most = a.p.table_width * a.page_tokens;
+  for (int i0 = 0; i0 < a.p.batch; i0 += NT) {
+    const int i = i0 + tid;
+    if (i0) sequence(i);
+    if (i < a.p.batch && h == 0 && tok == 0 && rank == 0 && (q0 < 0 || q1 < q0 || q1 > a.p.q_tokens || len < 0 || len > most))
+      dev::report(a.status, LW_DEV_BAD_SEQ);
+    const bool has = q0 >= 0 && q1 <= a.p.q_tokens && q0 <= tok && tok < q1;
+    if (has) atomicMin(&s_seq, i);   // (ranges that overlap: the first)
+    __syncthreads();
+    if (has && s_seq == i) s_pos = (int)((int64_t)min(max(len, 0), most) - q1 + tok);
   }
-}
-
-constexpr int kChoose = 256;
-
-// The pages of one query token and key/value head, ascending.
-__global__ void __launch_bounds__(kChoose) kv_choose_kernel(const BlockArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem);
-  __shared__ uint32_t hist[256], s_scan[kChoose / 32], s_pick[2];
-  __shared__ int s_seq;
-  const int h = blockIdx.x, tok = blockIdx.y, tid = threadIdx.x;
-  dev::pdl_wait();
-  if (h == 0 && tok == 0)
-    for (int i = tid; i < a.p.batch; i += kChoose) {
-      const int q0 = a.p.q_start[i], q1 = a.p.q_start[i + 1], n = a.p.kv_len[i];
-      if (q0 < 0 || q1 < q0 || q1 > a.p.q_tokens || n < 0 || n > a.p.table_width * a.page_tokens)
-        dev::report(a.status, LW_DEV_BAD_SEQ);
-    }
+  __syncthreads();
   const int64_t row = (int64_t)tok * a.heads + h;
-  int b, pos;
-  if (!token_seq(a, tok, &s_seq, b, pos)) {
-    if (tid == 0) a.lens[row] = -1;
+  const int b = s_seq, pos = s_pos;
+  if (b == 0x7FFFFFFF) {   // of none (the same in all of the cluster)
+    if (self == 0) a.lens[row] = -1;
     return;
   }
   const int nb = pos < 0 ? 0 : pos / a.page_tokens + 1, count = nb < a.s.blocks ? nb : a.s.blocks;
@@ -326,56 +283,77 @@ __global__ void __launch_bounds__(kChoose) kv_choose_kernel(const BlockArgs a) {
     if (chosen) chosen[i] = blk;
   };
   if (chosen)
-    for (int i = count + tid; i < a.s.blocks; i += kChoose) chosen[i] = -1;
-  if (tid == 0) a.lens[row] = nb ? (count - 1) * a.page_tokens + pos - (nb - 1) * a.page_tokens + 1 : 0;
+    for (int i = count + self; i < a.s.blocks; i += all) chosen[i] = -1;
+  if (self == 0) a.lens[row] = nb ? (count - 1) * a.page_tokens + pos - (nb - 1) * a.page_tokens + 1 : 0;
   if (nb <= a.s.blocks) {
-    for (int i = tid; i < nb; i += kChoose) put(i, i);
+    for (int i = self; i < nb; i += all) put(i, i);
     return;
   }
   const int first = a.s.first, last = nb - a.s.recent;
-  for (int i = tid; i < first; i += kChoose) put(i, i);
-  for (int i = last + tid; i < nb; i += kChoose) put(count - nb + i, i);
-  uint32_t need = (uint32_t)(count - first - a.s.recent), limit = 0;
+  for (int i = self; i < first; i += all) put(i, i);
+  for (int i = last + self; i < nb; i += all) put(count - nb + i, i);
+  const uint32_t need = (uint32_t)(count - first - a.s.recent);
   if (need == 0) return;
-  const float* scores = a.scores + row * a.p.table_width;
-  for (int i = first + tid; i < last; i += kChoose) keys[i - first] = dev::order_key(scores[i]);
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0 : ~0u << (shift + 8);
-    for (int i = tid; i < last - first; i += kChoose)
-      if ((keys[i] & mask) == limit) atomicAdd(&hist[keys[i] >> shift & 255], 1u);
-    __syncthreads();
-    limit |= dev::pick_digit<kChoose>(hist, need, s_scan, s_pick) << shift;
+  // ---- this CTA's stretch of the pages that compete
+  int mine;
+  const int from = (int)dev::select_stretch(first, last, mine);
+  for (int i0 = 0; i0 < mine; i0 += 8 * 4 * kWarps) {
+    // eight rounds of a page an eight lanes: lane r knows the r-th one's
+    const int ir = i0 + r * 4 * kWarps + 4 * warp + lane / 8;
+    const int page_r = ir < mine ? table[from + ir] : -1;
+#pragma unroll 4
+    for (int e = 0; e < 8; ++e) {
+      const int i = i0 + e * 4 * kWarps + 4 * warp + lane / 8;
+      if (i0 + e * 4 * kWarps + 4 * warp >= mine) break;   // (the same in all of the warp)
+      const int page = __shfl_sync(0xFFFFFFFFu, page_r, (lane & 24) + e);
+      const bool ok = page >= 0 && page < a.n_pages;
+      const uint8_t* rec = static_cast<const uint8_t*>(a.s.summary) + ((int64_t)(ok ? page : 0) * a.heads + h) * record_bytes(D);
+      uint32_t hi[W], lo[W];
+      dev::ldg_words<W>(rec + 4 * W * r, hi);
+      dev::ldg_words<W>(rec + D + 4 * W * r, lo);
+      const float step = *reinterpret_cast<const float*>(rec + 2 * D);
+      float best = -INFINITY;
+      for (int g = 0; g < a.group; ++g) {
+        int dot = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          dot = __dp4a((int)codes[((g * 2) * 8 + r) * W + w], (int)hi[w], dot);
+          dot = __dp4a((int)codes[((g * 2 + 1) * 8 + r) * W + w], (int)lo[w], dot);
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+        best = fmaxf(best, __fmul_rn(units[g], (float)dot));
+      }
+      // (a page outside the cache is read by nobody: the attention leaves it out)
+      if (r == 0 && i < mine) keys[i] = dev::order_key(ok ? __fmul_rn(step, best) : -INFINITY);
+    }
   }
-  uint32_t above = 0, equal = 0;
-  for (int i0 = 0; i0 < last - first; i0 += kChoose) {
-    const int i = i0 + tid;
-    const uint32_t k = i < last - first ? keys[i] : 0;
-    const bool more = i < last - first && k > limit, same = i < last - first && k == limit;
-    uint32_t total;
-    const uint32_t at = dev::scan_cta<kChoose>((uint32_t)more | (uint32_t)same << 16, s_scan, total);
-    const uint32_t ab = above + (at & 0xFFFFu), eq = equal + (at >> 16);
-    if (more || (same && eq < need)) put(first + (int)(ab + (eq < need ? eq : need)), first + i);
-    above += total & 0xFFFFu;
-    equal += total >> 16;
-  }
+  __syncthreads();
+  dev::select_places<NT, 8>(s, mine, need, [&](int i) { return keys[i]; }, [&](int place, int i) { put(first + place, from + i); });
 }
 
-constexpr int kMostWidth = 49152;
+constexpr int kMostWidth = 40960;   // order keys of a page table in one CTA's shared memory
 
 template <int D, class T>
-lw_status launch_score(const BlockArgs& a, dim3 grid, cudaStream_t st) {
-  const size_t smem = (size_t)a.group * (2 * D + 4);
-  if (resident_blocks(reinterpret_cast<const void*>(kv_score_kernel<D, T>), 32 * kScoreWarps, smem) < 1)
-    return fail(LW_ERR_CUDA, "lw_kv_attention_blocks: the kernel does not fit this device");
-  return kv_launch("lw_kv_attention_blocks", kv_score_kernel<D, T>, grid, 32 * kScoreWarps, smem, 1, st, a);
+lw_status launch_choose(BlockArgs a, cudaStream_t st) {
+  const char* fn = "lw_kv_attention_blocks";
+  // CTAs of a token and head: some 256 pages each, as far as six an SM have room
+  const int64_t pairs = a.p.q_tokens * a.heads;
+  int ranks = 1;
+  while (ranks < 8 && 2 * ranks * pairs <= 6 * device_sm_count() && a.p.table_width > 256 * ranks) ranks *= 2;
+  a.most_pages = (a.p.table_width + ranks - 1) / ranks + 32;
+  a.most_pages = (a.most_pages + 3) / 4 * 4;
+  const size_t smem = sizeof(ChooseShared) + (size_t)a.most_pages * 4 + (size_t)a.group * (2 * D + 4);
+  if (resident_blocks(reinterpret_cast<const void*>(kv_choose_kernel<D, T>), kChoose, smem) < 1)
+    return fail(LW_ERR_CUDA, "%s: the kernel does not fit this device", fn);
+  return kv_launch(fn, kv_choose_kernel<D, T>, dim3((unsigned)ranks, (unsigned)a.heads, (unsigned)a.p.q_tokens),
+                   kChoose, smem, ranks, st, a);
 }
 template <int D>
-lw_status launch_score_t(const BlockArgs& a, dim3 grid, cudaStream_t st) {
-  return a.p.dtype == LW_F32   ? launch_score<D, float>(a, grid, st)
-         : a.p.dtype == LW_F16 ? launch_score<D, __half>(a, grid, st)
-                               : launch_score<D, __nv_bfloat16>(a, grid, st);
+lw_status launch_choose_t(const BlockArgs& a, cudaStream_t st) {
+  return a.p.dtype == LW_F32   ? launch_choose<D, float>(a, st)
+         : a.p.dtype == LW_F16 ? launch_choose<D, __half>(a, st)
+                               : launch_choose<D, __nv_bfloat16>(a, st);
 }
 
 // The cache with a head's share of a page as a page: what a query that reads pages of its own attends to
@@ -386,19 +364,18 @@ lw_kv_cache by_head(const lw_kv_cache* c) {
   return v;
 }
 
-// Workspace: attention's, then page numbers, lengths and scores of each token and head
+// Workspace: attention's, then page numbers and lengths of each token and head
 struct BlockSpace {
-  size_t pages, lens, scores, bytes;
+  size_t pages, lens, bytes;
 };
-BlockSpace block_space(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens, int32_t width, int32_t blocks) {
+BlockSpace block_space(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens, int32_t blocks) {
   const lw_kv_cache v = by_head(c);
   const size_t rows = (size_t)q_tokens * c->kv_heads;
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   BlockSpace s{};
   s.pages = up(kv_attention_workspace(&v, q_heads / c->kv_heads, q_tokens * c->kv_heads));
   s.lens = s.pages + up(rows * blocks * 4);
-  s.scores = s.lens + up(rows * 4);
-  s.bytes = s.scores + up(rows * width * 4);
+  s.bytes = s.lens + up(rows * 4);
   return s;
 }
 
@@ -452,7 +429,7 @@ extern "C" size_t lw_kv_blocks_workspace_bytes(const lw_kv_cache* c, int32_t q_h
       q_tokens < 0 || q_tokens * c->kv_heads > 65535 || table_width < 0 || table_width > kMostWidth || blocks < 1 ||
       blocks > kMostWidth)
     return 0;
-  return block_space(c, q_heads, q_tokens, table_width, blocks).bytes;
+  return block_space(c, q_heads, q_tokens, blocks).bytes;
 }
 
 extern "C" lw_status lw_kv_attention_blocks(const lw_kv_cache* c, const lw_kv_attn* p, const lw_kv_blocks* k, void* ws,
@@ -480,7 +457,7 @@ extern "C" lw_status lw_kv_attention_blocks(const lw_kv_cache* c, const lw_kv_at
   if (p->q_tokens == 0) return LW_OK;
   if (!k->summary || (reinterpret_cast<uintptr_t>(k->summary) & 15u) || reinterpret_cast<uintptr_t>(k->chosen) % 4)
     return fail(LW_ERR_INVALID_ARG, "%s: summary missing, or an address is not aligned to its type", fn);
-  const BlockSpace at = block_space(c, p->q_heads, p->q_tokens, p->table_width, k->blocks);
+  const BlockSpace at = block_space(c, p->q_heads, p->q_tokens, k->blocks);
   if (!ws || ws_bytes < at.bytes || (reinterpret_cast<uintptr_t>(ws) & 15u))
     return fail(LW_ERR_INVALID_ARG, "%s: workspace missing, misaligned or %zu bytes of %zu", fn, ws_bytes, at.bytes);
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -489,24 +466,15 @@ extern "C" lw_status lw_kv_attention_blocks(const lw_kv_cache* c, const lw_kv_at
   a.s = *k;
   a.pages = reinterpret_cast<int32_t*>(w + at.pages);
   a.lens = reinterpret_cast<int32_t*>(w + at.lens);
-  a.scores = reinterpret_cast<float*>(w + at.scores);
   a.n_pages = c->n_pages;
   a.page_tokens = c->page_tokens;
   a.heads = c->kv_heads;
   a.group = group;
   a.status = d_status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (p->table_width > k->blocks) {   // (else every page is read)
-    const dim3 grid((unsigned)((p->table_width + kScoreBlocks - 1) / kScoreBlocks), (unsigned)c->kv_heads, (unsigned)p->q_tokens);
-    s = c->head_dim == 64   ? launch_score_t<64>(a, grid, st)
-        : c->head_dim == 96 ? launch_score_t<96>(a, grid, st)
-                            : launch_score_t<128>(a, grid, st);
-    if (s != LW_OK) return s;
-  }
-  const size_t smem = (size_t)p->table_width * 4;
-  if (resident_blocks(reinterpret_cast<const void*>(kv_choose_kernel), kChoose, smem) < 1)
-    return fail(LW_ERR_CUDA, "%s: the kernel does not fit this device", fn);
-  s = kv_launch(fn, kv_choose_kernel, dim3((unsigned)c->kv_heads, (unsigned)p->q_tokens), kChoose, smem, 1, st, a);
+  s = c->head_dim == 64   ? launch_choose_t<64>(a, st)
+      : c->head_dim == 96 ? launch_choose_t<96>(a, st)
+                          : launch_choose_t<128>(a, st);
   if (s != LW_OK) return s;
   lw_kv_attn one = *p;
   one.q_start = nullptr;

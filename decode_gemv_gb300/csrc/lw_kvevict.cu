@@ -24,29 +24,24 @@ __device__ __forceinline__ int evict_keys(const EvictArgs& a, int b) {
 }
 
 // ---- the choice ----------------------------------------------------------------
-// A cluster a head.  Its CTAs share the competing keys in contiguous stretches; each reads its own once and keeps
-// the order keys in shared memory (a stretch that is too long is read again instead).  The limit is found in
-// three digits of 11, 11 and 10 bits; a digit's histograms lie in the CTAs' shared memory and every CTA adds them
-// up, so that all find the same digit with one barrier of the cluster a digit.  From the same histograms a CTA
-// knows how many keys above the limit, and at it, lie in the stretches before its own: the places follow without
-// another exchange.
-constexpr int kSelect = 512, kSelectWarps = kSelect / 32, kBins = 2048;
+// A cluster a head (lw_kvselect.cuh); a stretch that is too long for shared memory is read again instead.
 constexpr int kMostSelect = 40960;   // order keys a CTA keeps
+constexpr int kSelect = 512;
+using EvictShared = dev::SelectShared<11>;
 
 __global__ void __launch_bounds__(kSelect) kv_evict_select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t smem[];
-  __shared__ uint32_t s_scan[kSelectWarps], s_pick[2], s_more[kSelectWarps], s_same[kSelectWarps];
-  uint32_t* hist = smem;                 // [3][kBins]
-  uint32_t* keys = smem + 3 * kBins;     // [a.most_keys]
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const uint32_t ranks = dev::cluster_size(), rank = dev::cluster_rank();
-  for (int i = tid; i < 3 * kBins; i += kSelect) hist[i] = 0;
+  EvictShared& s = *reinterpret_cast<EvictShared*>(smem);
+  uint32_t* keys = smem + sizeof(EvictShared) / 4;     // [a.most_keys]
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int rank = (int)dev::cluster_rank();
+  for (int i = tid; i < EvictShared::kPasses * EvictShared::kBins; i += kSelect) s.hist[i] = 0;
   dev::pdl_wait();
   const int n = h == 0 && rank == 0 && tid == 0 ? evict_keys<true>(a, b) : evict_keys<false>(a, b);
   const int m = n < a.p.keep ? n : a.p.keep;
   if (h == 0 && rank == 0 && tid == 0) a.p.out_len[b] = m;
   int32_t* kept = a.p.kept + ((int64_t)b * a.heads + h) * a.p.keep;
-  const int self = (int)rank * kSelect + tid, all = (int)ranks * kSelect;
+  const int self = rank * kSelect + tid, all = (int)dev::cluster_size() * kSelect;
   for (int64_t i = (int64_t)m + self; i < a.p.keep; i += all) kept[i] = -1;
   if (n <= a.p.keep) {   // (the same in all of the cluster)
     for (int64_t i = self; i < n; i += all) kept[i] = (int)i;
@@ -56,111 +51,26 @@ __global__ void __launch_bounds__(kSelect) kv_evict_select_kernel(const EvictArg
   const int first = a.p.first, last = n - a.p.recent;
   for (int64_t i = self; i < first; i += all) kept[i] = (int)i;
   for (int64_t i = (int64_t)last + self; i < n; i += all) kept[m - n + i] = (int)i;
-  uint32_t need = (uint32_t)(m - first - a.p.recent), limit = 0;
+  const uint32_t need = (uint32_t)(m - first - a.p.recent);
   if (need == 0) return;
-  const int stretch = (int)((((int64_t)last - first + ranks - 1) / ranks + 31) / 32 * 32);
-  const int64_t from = first + (int64_t)rank * stretch;
-  const int count = from < last ? (int)(last - from < stretch ? last - from : stretch) : 0;
+  int count;
+  const int64_t from = dev::select_stretch(first, last, count);
   const float* w = a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride + from;
   const bool here = count <= a.most_keys;
-  __syncthreads();
-  uint32_t above = 0, equal = 0;   // of the stretches before
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
-    const uint32_t mask = pass == 0 ? 0 : pass == 1 ? ~0u << 21 : ~0u << 10;
-    uint32_t* mine = hist + pass * kBins;
-    const auto add = [&](uint32_t k) {
-      if ((k & mask) == limit) atomicAdd(&mine[k >> shift & (bins - 1)], 1u);
-    };
-    if (pass == 0 || !here) {
-      constexpr int kAhead = 8;
-      for (int i0 = tid; i0 < count; i0 += kAhead * kSelect) {
-        float x[kAhead];
+  if (here) {
+    constexpr int kAhead = 8;
+    for (int i0 = tid; i0 < count; i0 += kAhead * kSelect) {
+      float x[kAhead];
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e) x[e] = i0 + e * kSelect < count ? w[i0 + e * kSelect] : 0.f;
+      for (int e = 0; e < kAhead; ++e) x[e] = i0 + e * kSelect < count ? w[i0 + e * kSelect] : 0.f;
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e)
-          if (i0 + e * kSelect < count) {
-            const uint32_t k = dev::order_key(x[e]);
-            if (here) keys[i0 + e * kSelect] = k;
-            add(k);
-          }
-      }
-    } else {
-#pragma unroll 4
-      for (int i = tid; i < count; i += kSelect) add(keys[i]);
+      for (int e = 0; e < kAhead; ++e)
+        if (i0 + e * kSelect < count) keys[i0 + e * kSelect] = dev::order_key(x[e]);
     }
-    dev::cluster_sync();
-    // thread t has the four bins below bins - 4 t: in all, and in the stretches before
-    const int top = bins - 4 * (tid + 1);
-    uint32_t sum[4] = {}, before[4] = {};
-    if (top >= 0) {
-      for (uint32_t r = 0; r < ranks; ++r) {
-        const uint4 v = dev::cluster_load4(mine + top, r);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[i] += x[i];
-          before[i] += r < rank ? x[i] : 0;
-        }
-      }
-    }
-    uint32_t total;
-    uint32_t over = dev::scan_cta<kSelect>(sum[0] + sum[1] + sum[2] + sum[3], s_scan, total);
-#pragma unroll
-    for (int i = 3; i >= 0; --i) {
-      if (over < need && over + sum[i] >= need) {
-        s_pick[0] = (uint32_t)(top + i);
-        s_pick[1] = need - over;
-      }
-      over += sum[i];
-    }
-    __syncthreads();
-    const uint32_t digit = s_pick[0];
-    need = s_pick[1];
-    limit |= digit << shift;
-    uint32_t up = 0, at = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      up += top + i > (int)digit ? before[i] : 0;
-      at += top + i == (int)digit ? before[i] : 0;
-    }
-    (void)dev::scan_cta<kSelect>(up, s_scan, total);
-    above += total;
-    if (pass == 2) (void)dev::scan_cta<kSelect>(at, s_scan, equal);
-  }
-  dev::cluster_sync();   // (no CTA leaves while another reads its histograms)
-  // a warp takes a part of the stretch, counts it, and places it
-  const int part = ((count + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-  const int i0 = warp * part, i1 = i0 + part < count ? i0 + part : count;
-  uint32_t more = 0, same = 0;
-#pragma unroll 4
-  for (int i = i0 + lane; i < i0 + part; i += 32) {
-    const uint32_t k = i < i1 ? (here ? keys[i] : dev::order_key(w[i])) : 0u;
-    more += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && k > limit));
-    same += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && k == limit));
-  }
-  if (lane == 0) {
-    s_more[warp] = more;
-    s_same[warp] = same;
   }
   __syncthreads();
-  for (int v = 0; v < warp; ++v) {
-    above += s_more[v];
-    equal += s_same[v];
-  }
-  const uint32_t lower = (1u << lane) - 1;
-#pragma unroll 4
-  for (int i = i0 + lane; i < i0 + part; i += 32) {
-    const uint32_t k = i < i1 ? (here ? keys[i] : dev::order_key(w[i])) : 0u;
-    const bool is_more = i < i1 && k > limit, is_same = i < i1 && k == limit;
-    const uint32_t bm = __ballot_sync(0xFFFFFFFFu, is_more), bs = __ballot_sync(0xFFFFFFFFu, is_same);
-    const uint32_t am = above + __popc(bm & lower), as = equal + __popc(bs & lower);
-    if (is_more || (is_same && as < need)) kept[first + am + (as < need ? as : need)] = (int)(from + i);
-    above += __popc(bm);
-    equal += __popc(bs);
-  }
+  dev::select_places<kSelect, 11>(s, count, need, [&](int i) { return here ? keys[i] : dev::order_key(w[i]); },
+                     [&](int place, int i) { kept[first + place] = (int)(from + i); });
 }
 
 // ---- the move ------------------------------------------------------------------
@@ -369,7 +279,7 @@ extern "C" lw_status lw_kv_evict(const lw_kv_cache* c, const lw_kv_eviction* p, 
   int64_t most = (keys + ranks - 1) / ranks + 32;
   if (most > kMostSelect) most = kMostSelect;
   a.most_keys = (int32_t)most;
-  const size_t smem = (3 * kBins + (size_t)most) * 4;
+  const size_t smem = sizeof(EvictShared) + (size_t)most * 4;
   if (resident_blocks(reinterpret_cast<const void*>(kv_evict_select_kernel), kSelect, smem) < 1)
     return fail(LW_ERR_CUDA, "%s: the kernel does not fit this device", fn);
   s = kv_launch(fn, kv_evict_select_kernel, dim3((unsigned)ranks, (unsigned)c->kv_heads, (unsigned)p->batch), kSelect,

@@ -868,8 +868,8 @@ lw_status lw_kv_summarise(const lw_kv_cache* c, const lw_kv_summaries* a, int32_
  * pages' keys up to p.  chosen (or NULL): device [q_tokens][kv_heads][blocks],
  * the pages' places in the page table, ascending, -1 where there are fewer;
  * rows of tokens outside every sequence are left.
- * 1 <= recent, 0 <= first, first + recent <= blocks; table_width <= 49152;
- * q_tokens * kv_heads <= 65535; n_pages * kv_heads * page_tokens < 2^32 (else LW_ERR_SHAPE).
+ * 1 <= recent, 0 <= first, first + recent <= blocks; table_width, blocks <= 40960;
+ * q_heads / kv_heads <= 128; q_tokens * kv_heads <= 65535; n_pages * kv_heads * page_tokens < 2^32 (else LW_ERR_SHAPE).
  * max_q is not used.  Everything else, lse too, as in lw_kv_attention.
  */
 typedef struct {
