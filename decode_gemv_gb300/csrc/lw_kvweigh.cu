@@ -24,8 +24,16 @@ lw_status launch_few_d(const WeighArgs& a, bool one, dim3 grid, cudaStream_t st)
   return one ? launch_few_t<D, true>(a, grid, st) : launch_few_t<D, false>(a, grid, st);
 }
 
-// Rows of a sequence on a key/value head up to which kv_weigh_few_kernel takes a call
-constexpr int kFewMost = 64;
+// The variant, by the rows of a sequence on a key/value head.  us, 8 sequences of 32768 keys | 64 of 512, 8 heads of
+// 128: a block of 8 rows in registers, 64 rows in shared memory, kv_weigh_many_kernel
+//   bf16   8 rows   57  71        |  12  13        fp32   8 rows   71  81        |  14  15
+//         16 rows  110  89  598   |  22  16  87         16 rows  138 107  645   |  25  19  94
+//        128 rows  855 397  534   | 157  59  87        128 rows 1076 542  582   | 185  79 102
+//        192 rows      594  635   |      87 101        160 rows      704  709   |     102 122
+//                                                      192 rows      812  708   |     117 125
+// One sequence of 8192 keys alone, 192 rows: 27 and 29, 35 and 33.  (kv_weigh_many_kernel takes rows 128 at a time,
+// and a unit of 128 keys starts slowly.)
+constexpr int kOneMost = 8, kFewMost16 = 192, kFewMost32 = 160;
 
 inline int64_t row_tiles(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens) {
   return (q_tokens * (q_heads / c->kv_heads) + 127) / 128;
@@ -44,10 +52,13 @@ lw_status launch_many(const WeighArgs& a, void* ws, int64_t tiles, int64_t key_t
                                 512, 0, 1, st, r);
   if (s != LW_OK) return s;
   const WeighManyArgs w{a, static_cast<const uint8_t*>(ws), (int32_t)tiles};
-  // CTAs of a unit: until the device is full
+  // CTAs of a unit, until the device is full; and units' CTAs of a sequence's head, all at once or as many as fill it
+  // eight times over (a table may be far wider than its sequences are long: a CTA without keys costs 2 us)
+  const int64_t pairs = (int64_t)a.heads * a.p.batch, most = (8 * device_sm_count() + pairs - 1) / pairs;
+  const int64_t x = key_tiles < most ? key_tiles : most;
   int ranks = 1;
-  while (ranks < 8 && 2 * ranks * key_tiles * a.heads * a.p.batch <= device_sm_count()) ranks *= 2;
-  return kv_launch("lw_kv_weigh", kernel, dim3((unsigned)(key_tiles * ranks), (unsigned)a.heads, (unsigned)a.p.batch),
+  while (ranks < 8 && 2 * ranks * key_tiles * pairs <= device_sm_count()) ranks *= 2;
+  return kv_launch("lw_kv_weigh", kernel, dim3((unsigned)(x * ranks), (unsigned)a.heads, (unsigned)a.p.batch),
                    W::kThreads, W::kSmem, ranks, st, w);
 }
 template <int D>
@@ -66,8 +77,8 @@ extern "C" size_t lw_kv_weigh_workspace_bytes(const lw_kv_cache* c, int32_t q_he
   if (!c || !lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens) || q_heads < 1 || q_heads % c->kv_heads ||
       q_tokens < 0 || q_tokens > kKvMost / q_heads)
     return 0;
-  // none for few rows in all: whatever sequences they are of, kv_weigh_few_kernel takes them
-  if (q_tokens * (q_heads / c->kv_heads) <= kFewMost) return 0;
+  // none for few rows in all: whatever sequences they are of, kv_weigh_few_kernel takes them, in every type
+  if (q_tokens * (q_heads / c->kv_heads) <= kFewMost32) return 0;
   return (size_t)c->kv_heads * row_tiles(c, q_heads, q_tokens) * record_bytes(c->head_dim, 2);
 }
 
@@ -117,7 +128,7 @@ extern "C" lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, v
   int64_t keys = (int64_t)a->table_width * c->page_tokens;
   if (a->w_keys < keys) keys = a->w_keys;
   const int64_t rows = (a->max_q < a->q_tokens ? a->max_q : a->q_tokens) * w.group;
-  if (rows > kFewMost) {
+  if (rows > (a->dtype == LW_F32 ? kFewMost32 : kFewMost16)) {
     const int64_t tiles = row_tiles(c, a->q_heads, a->q_tokens), key_tiles = (keys + 127) / 128;
     return c->head_dim == 64   ? launch_many_t<64>(w, ws, tiles, key_tiles, st)
            : c->head_dim == 96 ? launch_many_t<96>(w, ws, tiles, key_tiles, st)
@@ -130,8 +141,10 @@ extern "C" lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, v
   const int64_t fill = (2 * device_sm_count() + pairs - 1) / pairs;
   int64_t x = (tiles + 15) / 16 < fill ? (tiles + 15) / 16 : fill;
   if (x < (tiles + 255) / 256) x = (tiles + 255) / 256;
+  const int64_t most = (32 * device_sm_count() + pairs - 1) / pairs;   // (tables far wider than the sequences are long)
+  if (x > most) x = most;
   const dim3 grid((unsigned)x, (unsigned)c->kv_heads, (unsigned)a->batch);
-  return c->head_dim == 64   ? launch_few_d<64>(w, rows <= 8, grid, st)
-         : c->head_dim == 96 ? launch_few_d<96>(w, rows <= 8, grid, st)
-                             : launch_few_d<128>(w, rows <= 8, grid, st);
+  return c->head_dim == 64   ? launch_few_d<64>(w, rows <= kOneMost, grid, st)
+         : c->head_dim == 96 ? launch_few_d<96>(w, rows <= kOneMost, grid, st)
+                             : launch_few_d<128>(w, rows <= kOneMost, grid, st);
 }

@@ -48,9 +48,10 @@ struct WeighMany {
   static constexpr int kThreads = 320;
   // tensor-memory columns: three accumulators, then the keys' parts
   static constexpr int kBufs = 3, kKeyCol = kBufs * kRows, kKeyCols = D / 2;
+  static constexpr int kSlots = 4;   // of barriers and parameters: an even number, so that each is one group's
   static constexpr int kHead = 1024 + 2 * kKeys * 4;           // barriers and flags, the groups' sums
-  static constexpr int kParams = kHead;                        // [kBufs]
-  static constexpr int kB = kParams + kBufs * kParam;
+  static constexpr int kParams = kHead;                        // [kSlots]
+  static constexpr int kB = kParams + kSlots * kParam;
   // over half an SM's: one CTA an SM, whose tensor memory is all of it
   static constexpr int kNeed = kB + kStages * kImage, kSmem = kNeed > 118784 ? kNeed : 118784;
   static_assert(kSmem <= 232448, "shared memory");
@@ -139,7 +140,8 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
   float* sums = reinterpret_cast<float*>(smem + 1024);                            // [2][keys]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
-  const int k0 = (int)(blockIdx.x / ranks) * W::kKeys, h = blockIdx.y, b = blockIdx.z;
+  const int h = blockIdx.y, b = blockIdx.z;
+  int k0 = (int)(blockIdx.x / ranks) * W::kKeys;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar.b_full[i], 1);
@@ -170,210 +172,220 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     const int64_t t = a.p.window ? (int64_t)j + a.p.window - past : T;
     return R0 + (t < 0 ? 0 : t > T ? T : t) * a.group;
   };
-  const int k1 = min(k0 + W::kKeys, keys);
-  const int64_t ra = first_row(k0), rb = end_row(k1 - 1);
-  // this rank's row tiles
-  int t0 = 0, nt = 0;
-  if (ra < rb) {
-    const int first = (int)(ra / W::kRows), all = (int)((rb - 1) / W::kRows) - first + 1;
-    t0 = first + (int)((int64_t)all * rank / ranks);
-    nt = first + (int)((int64_t)all * (rank + 1) / ranks) - t0;
-  }
   if (warp == 1) {
     tmem_alloc(smem_addr(tslot), 512);
     tmem_relinquish();
   }
-  // ---- the keys: a lane of tensor memory each, half of their elements a group of four warps
-  const int kw = warp - 2, group = kw / 4, quarter = warp % 4, key = 32 * quarter + lane, j = k0 + key;
-  constexpr int kOct = D / 16;   // 8-element columns of a thread: words of codes
-  uint32_t kc[kOct];
-  float sc[kOct], mn[kOct];
-  bool real = false;             // (a key past the end, or of a page that is not there, is seen by no row)
-  if (warp >= 2) {
-    const int tile = j / 16, tpp = a.page_tokens / LW_KV_TILE, tk = j % 16;
-    const int page = j < keys ? a.p.page_table[(int64_t)b * a.p.table_stride + tile / tpp] : -1;
-    real = page >= 0 && page < a.n_pages;
-    if (!real && j < keys) report(a.status, LW_DEV_BAD_PAGE);
-    float top = 0.f;
-    if (real) {
-      const uint8_t* s = a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
-#pragma unroll
-      for (int i = 0; i < kOct; ++i) {
-        const int o = kOct * group + i, g = o / 4;   // column o: elements 32 g + 8 (o % 4) ..
-        kc[i] = *reinterpret_cast<const uint32_t*>(s + L::kKeyCodes + ((tk * 4 + o % 4) * G + g) * 4);
-        sc[i] = __half2float(*reinterpret_cast<const __half*>(s + L::kKeyScale + 2 * ((tk / 2 * G + g) * 2 + tk % 2)));
-        mn[i] = __half2float(*reinterpret_cast<const __half*>(s + L::kKeyMin + 2 * (tk * L::GP + g)));
-        top = fmaxf(top, fmaxf(fabsf(mn[i]), fabsf(fmaf(15.f, sc[i], mn[i]))));
-      }
-    }
-    top = top <= 3.402823466e38f ? top : 65504.f;
-    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
-    if (lane == 0) atomicMax(s_top, most);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
-  // all keys below 2^-4: brought up to there (lo parts would have too few bits as fp16); a power of two
-  const int ke = (int)(*s_top >> 23) - 127, lift = ke < -4 ? min(-4 - ke, 24) : 0;
-  const float up = __uint_as_float((uint32_t)(127 + lift) << 23);
-  if (warp >= 2) {
-    const uint32_t to = tmem + ((uint32_t)(32 * quarter) << 16) + W::kKeyCol + 4 * kOct * group;
-#pragma unroll
-    for (int i = 0; i < kOct; i += 2) {
-      uint32_t hi[8] = {}, lo[8] = {};
-      if (real) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t c = e % 2 ? whole_odd(kc[i + x] >> (8 * (e / 2))) : whole_even(kc[i + x] >> (8 * (e / 2)));
-            const float2 y = mul2(fma2(h2f(c), make_float2(sc[i + x], sc[i + x]), make_float2(mn[i + x], mn[i + x])), make_float2(up, up));
-            split2<1>(y.x, y.y, hi[4 * x + e], lo[4 * x + e]);
-          }
-      }
-      __syncwarp();
-      tmem_st8(to + 4 * i, hi);
-      tmem_st8(to + W::kKeyCols + 4 * i, lo);
-    }
-    tmem_st_wait();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   bool ok = true;
-  if (warp == 0) {   // ---- row tiles
-    if (lane == 0) {
-      const uint8_t* src = w.rows + ((int64_t)h * w.row_tiles + t0) * W::kRecord;
-      int i = 0;
-      for (; i < nt && ok; ++i, src += W::kRecord) {
-        const int s = i % S, d = i % W::kBufs;
-        ok = many_wait(&bar.b_free[s], (uint32_t)(i / S & 1) ^ 1u, flags) &&
-             many_wait(&bar.d_free[d], (uint32_t)(i / W::kBufs & 1) ^ 1u, flags);
+  int done = 0;           // row tiles of the units before: the barriers' phases go on
+  uint32_t unit = 0;
+  const int step = (int)(gridDim.x / ranks) * W::kKeys;
+  for (; k0 < keys; k0 = k0 < keys - step ? k0 + step : keys, ++unit) {
+    const int k1 = min(k0 + W::kKeys, keys);
+    const int64_t ra = first_row(k0), rb = end_row(k1 - 1);
+    // this rank's row tiles
+    int t0 = 0, nt = 0;
+    if (ra < rb) {
+      const int first = (int)(ra / W::kRows), all = (int)((rb - 1) / W::kRows) - first + 1;
+      t0 = first + (int)((int64_t)all * rank / ranks);
+      nt = first + (int)((int64_t)all * (rank + 1) / ranks) - t0;
+    }
+    // ---- the keys: a lane of tensor memory each, half of their elements a group of four warps
+    const int kw = warp - 2, group = kw / 4, quarter = warp % 4, key = 32 * quarter + lane, j = k0 + key;
+    constexpr int kOct = D / 16;   // 8-element columns of a thread: words of codes
+    uint32_t kc[kOct];
+    float sc[kOct], mn[kOct];
+    bool real = false;             // (a key past the end, or of a page that is not there, is seen by no row)
+    if (warp >= 2) {
+      const int tile = j / 16, tpp = a.page_tokens / LW_KV_TILE, tk = j % 16;
+      const int page = j < keys ? a.p.page_table[(int64_t)b * a.p.table_stride + tile / tpp] : -1;
+      real = page >= 0 && page < a.n_pages;
+      if (!real && j < keys) report(a.status, LW_DEV_BAD_PAGE);
+      float top = 0.f;
+      if (real) {
+        const uint8_t* s = a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
+#pragma unroll
+        for (int i = 0; i < kOct; ++i) {
+          const int o = kOct * group + i, g = o / 4;   // column o: elements 32 g + 8 (o % 4) ..
+          kc[i] = *reinterpret_cast<const uint32_t*>(s + L::kKeyCodes + ((tk * 4 + o % 4) * G + g) * 4);
+          sc[i] = __half2float(*reinterpret_cast<const __half*>(s + L::kKeyScale + 2 * ((tk / 2 * G + g) * 2 + tk % 2)));
+          mn[i] = __half2float(*reinterpret_cast<const __half*>(s + L::kKeyMin + 2 * (tk * L::GP + g)));
+          top = fmaxf(top, fmaxf(fabsf(mn[i]), fabsf(fmaf(15.f, sc[i], mn[i]))));
+        }
+      }
+      top = top <= 3.402823466e38f ? top : 65504.f;
+      const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+      if (lane == 0) atomicMax(s_top, most);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    // all keys below 2^-4: brought up to there (lo parts would have too few bits as fp16); a power of two
+    const int ke = (int)(*s_top >> 23) - 127, lift = ke < -4 ? min(-4 - ke, 24) : 0;
+    const float up = __uint_as_float((uint32_t)(127 + lift) << 23);
+    if (warp >= 2) {
+      const uint32_t to = tmem + ((uint32_t)(32 * quarter) << 16) + W::kKeyCol + 4 * kOct * group;
+#pragma unroll
+      for (int i = 0; i < kOct; i += 2) {
+        uint32_t hi[8] = {}, lo[8] = {};
+        if (real) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t c = e % 2 ? whole_odd(kc[i + x] >> (8 * (e / 2))) : whole_even(kc[i + x] >> (8 * (e / 2)));
+              const float2 y = mul2(fma2(h2f(c), make_float2(sc[i + x], sc[i + x]), make_float2(mn[i + x], mn[i + x])), make_float2(up, up));
+              split2<1>(y.x, y.y, hi[4 * x + e], lo[4 * x + e]);
+            }
+        }
+        __syncwarp();
+        tmem_st8(to + 4 * i, hi);
+        tmem_st8(to + W::kKeyCols + 4 * i, lo);
+      }
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0) *s_top = 0;   // (all have read it)
+    if (warp == 0) {   // ---- row tiles
+      if (lane == 0) {
+        const uint8_t* src = w.rows + ((int64_t)h * w.row_tiles + t0) * W::kRecord;
+        int i = done;
+        for (; i < done + nt && ok; ++i, src += W::kRecord) {
+          const int s = i % S, d = i % W::kSlots;
+          ok = many_wait(&bar.b_free[s], (uint32_t)(i / S & 1) ^ 1u, flags) &&
+               many_wait(&bar.d_free[d], (uint32_t)(i / W::kSlots & 1) ^ 1u, flags);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bar.p_full[d], W::kParam);
+          bulk_g2s(smem + W::kParams + d * W::kParam, src + W::kImage, W::kParam, &bar.p_full[d]);
+          mbar_arrive_expect_tx(&bar.b_full[s], W::kImage);
+          bulk_g2s(smem + W::kB + s * W::kImage, src, W::kImage, &bar.b_full[s]);
+        }
+        if (!ok) {
+          flags[0] = 1;
+          report(a.status, LW_DEV_TIMEOUT);
+          for (int x = max(0, i - 4); x < i; ++x) {   // no copy may be in flight when the CTA ends
+            mbar_wait(&bar.p_full[x % W::kSlots], (uint32_t)(x / W::kSlots & 1));
+            if (x >= i - S) mbar_wait(&bar.b_full[x % S], (uint32_t)(x / S & 1));
+          }
+        }
+      }
+    } else if (warp == 1) {   // ---- products
+      const auto wait = [&](uint64_t* x, uint32_t parity) { return __all_sync(0xFFFFFFFFu, many_wait(x, parity, flags)) != 0; };
+      const uint32_t base = smem_addr(smem), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const int count = __shfl_sync(0xFFFFFFFFu, nt, 0);
+      const uint32_t kh = tm + W::kKeyCol, kl = kh + W::kKeyCols;
+      const int first = __shfl_sync(0xFFFFFFFFu, done, 0);
+      for (int i = first; i < first + count && ok; ++i) {
+        const int s = i % S, d = i % W::kBufs, was = i - W::kBufs;   // (the tile that had the accumulators before)
+        ok = (was < 0 || wait(&bar.d_free[was % W::kSlots], (uint32_t)(was / W::kSlots & 1))) && wait(&bar.b_full[s], (uint32_t)(i / S & 1));
         if (!ok) break;
-        mbar_arrive_expect_tx(&bar.p_full[d], W::kParam);
-        bulk_g2s(smem + W::kParams + d * W::kParam, src + W::kImage, W::kParam, &bar.p_full[d]);
-        mbar_arrive_expect_tx(&bar.b_full[s], W::kImage);
-        bulk_g2s(smem + W::kB + s * W::kImage, src, W::kImage, &bar.b_full[s]);
+        tc_fence_after();
+        const uint64_t qh = sdesc(base + W::kB + s * W::kImage, W::kRows * 16, 128), ql = qh + (W::kPart >> 4);
+        const uint32_t to = tm + W::kRows * d;
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            umma_bf16_ta(to, kl + 8 * x, qh + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), x > 0);
+          if constexpr (PARTS == 2) {
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+              umma_bf16_ta(to, kh + 8 * x, ql + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), 1);
+          }
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            umma_bf16_ta(to, kh + 8 * x, qh + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), 1);
+          umma_commit(&bar.b_free[s]);
+          umma_commit(&bar.d_full[i % W::kSlots]);
+        }
+        __syncwarp();
       }
       if (!ok) {
         flags[0] = 1;
-        report(a.status, LW_DEV_TIMEOUT);
-        for (int j = max(0, i - 4); j < i; ++j) {   // no copy may be in flight when the CTA ends
-          if (j >= i - W::kBufs) mbar_wait(&bar.p_full[j % W::kBufs], (uint32_t)(j / W::kBufs & 1));
-          if (j >= i - S) mbar_wait(&bar.b_full[j % S], (uint32_t)(j / S & 1));
-        }
-      }
-    }
-  } else if (warp == 1) {   // ---- products
-    const auto wait = [&](uint64_t* x, uint32_t parity) { return __all_sync(0xFFFFFFFFu, many_wait(x, parity, flags)) != 0; };
-    const uint32_t base = smem_addr(smem), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    const int count = __shfl_sync(0xFFFFFFFFu, nt, 0);
-    const uint32_t kh = tm + W::kKeyCol, kl = kh + W::kKeyCols;
-    for (int i = 0; i < count && ok; ++i) {
-      const int s = i % S, d = i % W::kBufs;
-      ok = wait(&bar.d_free[d], (uint32_t)(i / W::kBufs & 1) ^ 1u) && wait(&bar.b_full[s], (uint32_t)(i / S & 1));
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t qh = sdesc(base + W::kB + s * W::kImage, W::kRows * 16, 128), ql = qh + (W::kPart >> 4);
-      const uint32_t to = tm + W::kRows * d;
-      if (elect_one()) {
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          umma_bf16_ta(to, kl + 8 * x, qh + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), x > 0);
-        if constexpr (PARTS == 2) {
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x)
-            umma_bf16_ta(to, kh + 8 * x, ql + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), 1);
-        }
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          umma_bf16_ta(to, kh + 8 * x, qh + (2 * x * W::kRows * 16 >> 4), idesc_f16(W::kRows), 1);
-        umma_commit(&bar.b_free[s]);
-        umma_commit(&bar.d_full[d]);
+        if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
       }
       __syncwarp();
-    }
-    if (!ok) {
-      flags[0] = 1;
-      if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
-    }
-    __syncwarp();
-    if (elect_one()) umma_commit(&bar.last);   // no product may be in flight when the tensor memory goes
-    __syncwarp();
-    mbar_wait(&bar.last, 0);
-  } else {   // ---- exponentials
-    const uint32_t mine = tmem + ((uint32_t)(32 * quarter) << 16);
-    const int64_t from = real ? first_row(j) : 0, to = real ? end_row(j) : 0;
-    const float down = __uint_as_float((uint32_t)(127 - lift) << 23);
-    float2 total = make_float2(0.f, 0.f);
-    for (int i = group; i < nt && ok; i += 2) {
-      const int d = i % W::kBufs;
-      const int64_t r0 = (int64_t)(t0 + i) * W::kRows;
-      ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.p_full[d], (uint32_t)(i / W::kBufs & 1), flags) &&
-                                       many_wait(&bar.d_full[d], (uint32_t)(i / W::kBufs & 1), flags));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t params = smem_addr(smem) + W::kParams + d * W::kParam;
-      const bool whole = __all_sync(0xFFFFFFFFu, lift == 0 && from <= r0 && to >= r0 + W::kRows);
-      const int lo = (int)(from - r0 < 0 ? 0 : from - r0 > W::kRows ? W::kRows : from - r0);
-      const int hi = (int)(to - r0 < 0 ? 0 : to - r0 > W::kRows ? W::kRows : to - r0);
-      float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      uint32_t z[2][32];
-      tmem_ld32(mine + W::kRows * d, z[0]);
+      if (elect_one()) umma_commit(&bar.last);   // no product may be in flight when the tensor memory goes
+      __syncwarp();
+      mbar_wait(&bar.last, unit & 1u);
+    } else {   // ---- exponentials
+      const uint32_t mine = tmem + ((uint32_t)(32 * quarter) << 16);
+      const int64_t from = real ? first_row(j) : 0, to = real ? end_row(j) : 0;
+      const float down = __uint_as_float((uint32_t)(127 - lift) << 23);
+      float2 total = make_float2(0.f, 0.f);
+      for (int i = done + ((group ^ done) & 1); i < done + nt && ok; i += 2) {   // (tile i is group i % 2's)
+        const int d = i % W::kBufs, slot = i % W::kSlots;
+        const int64_t r0 = (int64_t)(t0 + i - done) * W::kRows;
+        ok = __all_sync(0xFFFFFFFFu, many_wait(&bar.p_full[slot], (uint32_t)(i / W::kSlots & 1), flags) &&
+                                         many_wait(&bar.d_full[slot], (uint32_t)(i / W::kSlots & 1), flags));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t params = smem_addr(smem) + W::kParams + slot * W::kParam;
+        const bool whole = __all_sync(0xFFFFFFFFu, lift == 0 && from <= r0 && to >= r0 + W::kRows);
+        const int lo = (int)(from - r0 < 0 ? 0 : from - r0 > W::kRows ? W::kRows : from - r0);
+        const int hi = (int)(to - r0 < 0 ? 0 : to - r0 > W::kRows ? W::kRows : to - r0);
+        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t z[2][32];
+        tmem_ld32(mine + W::kRows * d, z[0]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld_wait();
-        if (c < 3) tmem_ld32(mine + W::kRows * d + 32 * (c + 1), z[(c + 1) & 1]);
-        const uint32_t(&y)[32] = z[c & 1];
-        if (whole) {
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait();
+          if (c < 3) tmem_ld32(mine + W::kRows * d + 32 * (c + 1), z[(c + 1) & 1]);
+          const uint32_t(&y)[32] = z[c & 1];
+          if (whole) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float4 p = lds_f4(params + (16 * c + e) * 16);
-            const float2 x = fma2(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), make_float2(p.x, p.y),
-                                  make_float2(p.z, p.w));
-            part[e & 1] = add2(part[e & 1], make_float2(ex2(x.x), ex2(x.y)));
-          }
-        } else {
+            for (int e = 0; e < 16; ++e) {
+              const float4 p = lds_f4(params + (16 * c + e) * 16);
+              const float2 x = fma2(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), make_float2(p.x, p.y),
+                                    make_float2(p.z, p.w));
+              part[e & 1] = add2(part[e & 1], make_float2(ex2(x.x), ex2(x.y)));
+            }
+          } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float4 p = lds_f4(params + (16 * c + e) * 16);
-            const float2 s = mul2(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), make_float2(down, down));
-            const float2 x = fma2(s, make_float2(p.x, p.y), make_float2(p.z, p.w));
-            const int col = 32 * c + 2 * e;
-            part[e & 1] = add2(part[e & 1], make_float2(col >= lo && col < hi ? ex2(x.x) : 0.f,
-                                                        col + 1 >= lo && col + 1 < hi ? ex2(x.y) : 0.f));
+            for (int e = 0; e < 16; ++e) {
+              const float4 p = lds_f4(params + (16 * c + e) * 16);
+              const float2 s = mul2(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), make_float2(down, down));
+              const float2 x = fma2(s, make_float2(p.x, p.y), make_float2(p.z, p.w));
+              const int col = 32 * c + 2 * e;
+              part[e & 1] = add2(part[e & 1], make_float2(col >= lo && col < hi ? ex2(x.x) : 0.f,
+                                                          col + 1 >= lo && col + 1 < hi ? ex2(x.y) : 0.f));
+            }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.d_free[slot]);
+        total = add2(total, add2(part[0], part[1]));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.d_free[d]);
-      total = add2(total, add2(part[0], part[1]));
+      if (!ok) {
+        flags[0] = 1;
+        if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
+      }
+      sums[group * W::kKeys + key] = total.x + total.y;
     }
-    if (!ok) {
-      flags[0] = 1;
-      if (lane == 0) report(a.status, LW_DEV_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    done += nt;
+    // the groups' sums, then the ranks', in order
+    if (threadIdx.x < W::kKeys) sums[threadIdx.x] += sums[W::kKeys + threadIdx.x];
+    if (ranks > 1) cluster_sync();
+    if (rank == 0 && threadIdx.x < W::kKeys) {
+      const int at = k0 + threadIdx.x;
+      float s = sums[threadIdx.x];
+      for (int r = 1; r < ranks; ++r) s += cluster_load(sums + threadIdx.x, (uint32_t)r);
+      if (at < keys) {
+        const float* add = a.p.add_to ? a.p.add_to + b * a.p.add_seq_stride + h * a.p.add_head_stride : nullptr;
+        (a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride)[at] = (add ? add[at] : 0.f) + s;
+      }
     }
-    sums[group * W::kKeys + key] = total.x + total.y;
+    if (ranks > 1) cluster_sync();   // (a rank's sums stay until they are read)
   }
-  __syncwarp();
-  tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
-  // the groups' sums, then the ranks', in order
-  if (threadIdx.x < W::kKeys) sums[threadIdx.x] += sums[W::kKeys + threadIdx.x];
-  if (ranks > 1) cluster_sync();
-  if (rank == 0 && threadIdx.x < W::kKeys) {
-    const int j = k0 + threadIdx.x;
-    float s = sums[threadIdx.x];
-    for (int r = 1; r < ranks; ++r) s += cluster_load(sums + threadIdx.x, (uint32_t)r);
-    if (j < keys) {
-      const float* add = a.p.add_to ? a.p.add_to + b * a.p.add_seq_stride + h * a.p.add_head_stride : nullptr;
-      (a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride)[j] = (add ? add[j] : 0.f) + s;
-    }
-  }
-  if (ranks > 1) cluster_sync();   // (a rank's sums stay until they are read)
+  if (warp == 1) tmem_dealloc(*tslot, 512);
 }
 
 }  // namespace dev

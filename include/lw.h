@@ -756,7 +756,7 @@ lw_status lw_kv_write_rotary(const lw_kv_cache* c, const lw_kv_rotated* a, int32
  * itself.  Entries j < kv_len[b] are written, the others left.  Sums and
  * exponentials are fp32, the order of the sum is fixed (deterministic on a given
  * device); products carry 22 bits of fp32 queries, all of 16-bit ones (down to
- * 2^-14 of a row's largest).  A NaN in a key or in lse is in the weights that
+ * 2^-23 of a row's largest).  A NaN in a key or in lse is in the weights that
  * the formula puts it in.  Keys in pages outside the cache weigh nothing.
  * kv_len past w_keys is reported (LW_DEV_BAD_SEQ); those keys are not written.
  * Limits as in lw_kv_attention.

@@ -233,3 +233,25 @@ def test_two_streams_and_replay():
     torch.cuda.synchronize()
     for _, w, want, st, _ in jobs:
         assert int(st) == 0 and relative(w, 3 * want) <= TOL
+
+
+def test_many_sequences_of_many_rows():
+    """More heads of sequences than CTAs: one takes several units of 128 keys, under a table far wider than most
+    sequences are long; and the same rows by way of the few-row kernel."""
+    gen, st = generator(14), status()
+    ts = [66 + i % 5 for i in range(80)]
+    lens = [t + (37 * i) % 500 for i, t in enumerate(ts)]
+    cache, table, free = filled(gen, lens, 16, 64, 32)
+    table = torch.cat([table, torch.full((80, 40), -1, dtype=torch.int32, device=DEV)], 1)
+    start = [sum(ts[:i]) for i in range(81)]
+    q = queries(gen, start[-1], 16, 64, "bf16")
+    lse = logsums(cache, table, q, start, lens, True, 0, 0.125)
+    want = expected(cache, table, q, start, lens, lse, None, True, 0, 0.125)
+    keys = table.shape[1] * 32
+    for hint in (70, 1):
+        w = torch.full((80, 16, keys), 9.0, device=DEV)
+        weigh(cache, table, q, lse, start, lens, w, st, scale=0.125, max_q=hint)
+        for b, n in enumerate(lens):
+            assert relative(w[b, :, :n], want[b, :, :n]) <= TOL, (hint, b)
+            assert bool((w[b, :, n:] == 9).all())
+    assert int(st) == 0
