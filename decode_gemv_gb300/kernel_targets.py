@@ -19,6 +19,11 @@ uploaded once; every call on the same device buffers):
   kv_decode          lw_kv_attention, 8 sequences of 16384 keys, 32 query heads on 8 of 128, bf16
   kv_chunk           lw_kv_attention, a chunk of 2048 tokens on 16384 keys, the same heads
   kv_window          lw_kv_attention, 5 prompts of 2048, fp16, 16 heads on 2 of 64, window 1024
+  kv_rotary          lw_kv_write_rotary, 32768 tokens of 32 query and 8 key/value heads of 128, bf16
+  kv_weigh           lw_kv_weigh, one token of 8 sequences of 16384 keys, the heads of kv_decode
+  kv_weigh_chunk     lw_kv_weigh, a chunk of 1024 tokens on 8192 keys, the same heads
+  kv_evict           lw_kv_evict, 8 sequences of 16384 keys cut to 4096, in place
+  kv_blocks          lw_kv_summarise of 8 sequences of 16384 keys, lw_kv_attention_blocks, 32 pages of 64
 
 Exits nonzero if a call reports a device status."""
 import argparse
@@ -30,11 +35,16 @@ from decode_gemv_gb300 import inputs, lw
 
 TARGETS = ("gate_q4", "gate_q4_twin", "gate_q4_b16", "gate_q4_b32", "gate_q4_decode",
            "llama_gate_bf16", "llama_gate_bf16_b16", "llama_gate_bf16_b64", "llama_gate_bf16_decode",
-           "kv_write", "kv_decode", "kv_chunk", "kv_window")
+           "kv_write", "kv_decode", "kv_chunk", "kv_window", "kv_rotary", "kv_weigh", "kv_weigh_chunk",
+           "kv_evict", "kv_blocks")
 # query tokens, keys, sequences, query heads, key/value heads, head_dim, page, type, window
 KV_CALLS = {"kv_decode": (1, 16384, 8, 32, 8, 128, 64, torch.bfloat16, 0),
             "kv_chunk": (2048, 16384, 1, 32, 8, 128, 64, torch.bfloat16, 0),
-            "kv_window": (2048, 2048, 5, 16, 2, 64, 32, torch.float16, 1024)}
+            "kv_window": (2048, 2048, 5, 16, 2, 64, 32, torch.float16, 1024),
+            "kv_weigh": (1, 16384, 8, 32, 8, 128, 64, torch.bfloat16, 0),
+            "kv_weigh_chunk": (1024, 8192, 1, 32, 8, 128, 64, torch.bfloat16, 0),
+            "kv_evict": (1, 16384, 8, 32, 8, 128, 64, torch.bfloat16, 0),
+            "kv_blocks": (1, 16384, 8, 32, 8, 128, 64, torch.bfloat16, 0)}
 
 
 def kv_target(t, reps, dev, st):
@@ -49,6 +59,14 @@ def kv_target(t, reps, dev, st):
         for _ in range(reps):
             lw.lw_kv_write(cache, k, v, slots, st)
         return
+    if t == "kv_rotary":
+        cache = lw.KvCache.empty(512, 8, 128, 64, dev)
+        q, k, v, slots = randn(32768, 32, 128), randn(32768, 8, 128), randn(32768, 8, 128), torch.arange(32768, device=dev)
+        table = torch.empty(32768, 128, device=dev)
+        lw.lw_rotary_table(table)
+        for _ in range(reps):
+            lw.lw_kv_write_rotary(cache, k, v, slots, slots, table, st, q=q, q_out=q)
+        return
     T, n, batch, hq, hk, dim, page, dtype, window = KV_CALLS[t]
     width = -(-n // page)
     cache = lw.KvCache.empty(batch * width, hk, dim, page, dev)
@@ -60,6 +78,24 @@ def kv_target(t, reps, dev, st):
     out = torch.empty_like(q)
     start = torch.arange(batch + 1, device=dev, dtype=torch.int32) * T
     lens = torch.full((batch,), n, dtype=torch.int32, device=dev)
+    if t.startswith("kv_weigh"):
+        lse, w = torch.full((batch * T, hq), 10.0, device=dev), torch.zeros(batch, hk, n, device=dev)
+        ws = torch.empty(max(lw.lw_kv_weigh_workspace_bytes(cache, hq, batch * T), 1), dtype=torch.uint8, device=dev)
+        for _ in range(reps):
+            lw.lw_kv_weigh(cache, q, lse, start, lens, table, w, ws, st, max_q=T, add_to=w)
+        return
+    if t == "kv_evict":
+        w, kept = torch.rand(batch, hk, n, device=dev, generator=gen) ** 8, torch.empty(batch, hk, 4096, dtype=torch.int32, device=dev)
+        for _ in range(reps):
+            lw.lw_kv_evict(cache, w, lens, table, table, torch.empty_like(lens), None, kept, st, keep=4096, first=4, recent=512)
+        return
+    if t == "kv_blocks":
+        summary = torch.empty(lw.lw_kv_summary_bytes(cache), dtype=torch.uint8, device=dev)
+        ws = torch.zeros(lw.lw_kv_blocks_workspace_bytes(cache, hq, batch, width, 32), dtype=torch.uint8, device=dev)
+        for _ in range(reps):
+            lw.lw_kv_summarise(cache, summary, torch.zeros_like(lens), lens, table, st)
+            lw.lw_kv_attention_blocks(cache, summary, q, start, lens, table, out, ws, st, blocks=32, first=1, recent=2)
+        return
     ws = torch.zeros(lw.lw_kv_workspace_bytes(cache, hq, batch * T, batch), dtype=torch.uint8, device=dev)
     for _ in range(reps):
         lw.lw_kv_attention(cache, q, start, lens, table, out, ws, st, max_q=T, window=window)

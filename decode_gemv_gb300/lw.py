@@ -1309,13 +1309,8 @@ def _kv_whole(fn, **named):
             _refuse(fn, f"{name}: expected a whole number, got {x!r}")
 
 
-def lw_kv_evict(cache: KvCache, weights, kv_len, page_table, out_table, out_len, out_weights, kept, d_status, *,
-                keep: int, first: int = 0, recent: int = 0, stream=None) -> None:
-    """Keep at most `keep` keys of each head of a sequence: the first `first`, the last `recent`, and
-    of the others those of the largest weights float32 [batch, kv_heads, keys].  They move together to the
-    front of out_table's pages (page_table itself, or other pages); kept int32 [batch, kv_heads, keep]
-    lists them (-1: none), out_len int32 [batch] says how many there are, out_weights (None, weights
-    itself, or other rows of at least `keep`) gets their weights."""
+def _kv_evict_refuse(cache, weights, kv_len, page_table, out_table, out_len, out_weights, kept, d_status, keep, first,
+                     recent):
     import torch
     fn = "lw_kv_evict"
     _kv_whole(fn, keep=keep, first=first, recent=recent)
@@ -1332,25 +1327,65 @@ def lw_kv_evict(cache: KvCache, weights, kv_len, page_table, out_table, out_len,
         _refuse(fn, f"kept: expected a contiguous int32 tensor [{batch}, {heads}, {keep}]")
     if batch and abs(out_len.data_ptr() - kv_len.data_ptr()) < 4 * batch:
         _refuse(fn, "out_len: overlaps kv_len")
-    op = ob = oh = on = 0
     if out_weights is not None:
         _kv_weight_rows(fn, "out_weights", out_weights, batch, heads, None, True)
         if not _kv_clear(weights, out_weights):
             _refuse(fn, "out_weights: overlaps weights (it may be weights itself)")
-        op, (ob, oh, _), on = out_weights.data_ptr(), out_weights.stride(), out_weights.shape[2]
         named += (("out_weights", out_weights),)
     _status_ptr(fn, d_status)
     _kv_on(fn, cache, *named)
-    wb, wh, _ = weights.stride()
+
+
+def lw_kv_evict(cache: KvCache, weights, kv_len, page_table, out_table, out_len, out_weights, kept, d_status, *,
+                keep: int, first: int = 0, recent: int = 0, stream=None) -> None:
+    """Keep at most `keep` keys of each head of a sequence: the first `first`, the last `recent`, and
+    of the others those of the largest weights float32 [batch, kv_heads, keys].  They move together to the
+    front of out_table's pages (page_table itself, or other pages); kept int32 [batch, kv_heads, keep]
+    lists them (-1: none), out_len int32 [batch] says how many there are, out_weights (None, weights
+    itself, or other rows of at least `keep`) gets their weights."""
+    dev = cache.index
     try:
-        a = _KV_EVICTION.pack(weights.data_ptr(), wb, wh, weights.shape[2], kv_len.data_ptr(),
-                              page_table.data_ptr(), page_table.stride(0), out_table.data_ptr(),
-                              out_table.stride(0), out_len.data_ptr(), op, ob, oh, on, kept.data_ptr(),
-                              page_table.shape[1], out_table.shape[1], batch, keep, first, recent)
+        batch, width = page_table.shape
+        out_batch, out_width = out_table.shape
+        ts, td = page_table.stride()
+        so, od = out_table.stride()
+        heads, (wb, wh, wd), keys = cache.kv_heads, weights.stride(), weights.shape[2]
+        kp, lp = kv_len.data_ptr(), out_len.data_ptr()
+        ok = (out_batch == batch and page_table.dtype is _I32 and out_table.dtype is _I32
+              and (td == 1 or width <= 1) and (od == 1 or out_width <= 1)
+              and weights.dtype is _F32 and weights.shape == (batch, heads, keys) and (wd == 1 or keys <= 1)
+              and kv_len.dtype is _I32 and kv_len.shape == (batch,) and kv_len.is_contiguous()
+              and out_len.dtype is _I32 and out_len.shape == (batch,) and out_len.is_contiguous()
+              and abs(kp - lp) >= 4 * batch and type(keep) is int and type(first) is int and type(recent) is int
+              and kept.dtype is _I32 and kept.shape == (batch, heads, keep) and kept.is_contiguous()
+              and d_status.dtype is _I32 and d_status.numel() >= 1 and d_status.is_contiguous()
+              and dev >= 0 and _current_device() == dev and weights.get_device() == dev
+              and kv_len.get_device() == dev and page_table.get_device() == dev and out_table.get_device() == dev
+              and out_len.get_device() == dev and kept.get_device() == dev and d_status.get_device() == dev)
+        op = ob = oh = on = 0
+        if out_weights is not None:
+            op, (ob, oh, od), on = out_weights.data_ptr(), out_weights.stride(), out_weights.shape[2]
+            ok = (ok and out_weights.dtype is _F32 and out_weights.shape == (batch, heads, on)
+                  and (od == 1 or on <= 1) and _kv_distinct(out_weights) and _kv_clear(weights, out_weights)
+                  and out_weights.get_device() == dev)
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    fn = "lw_kv_evict"
+    if not ok:
+        _kv_evict_refuse(cache, weights, kv_len, page_table, out_table, out_len, out_weights, kept, d_status, keep,
+                         first, recent)
+        (batch, width), out_width = page_table.shape, out_table.shape[1]
+        ts, so, (wb, wh, _), keys = page_table.stride(0), out_table.stride(0), weights.stride(), weights.shape[2]
+        kp, lp, op, ob, oh, on = kv_len.data_ptr(), out_len.data_ptr(), 0, 0, 0, 0
+        if out_weights is not None:
+            op, (ob, oh, _), on = out_weights.data_ptr(), out_weights.stride(), out_weights.shape[2]
+    try:
+        a = _KV_EVICTION.pack(weights.data_ptr(), wb, wh, keys, kp, page_table.data_ptr(), ts, out_table.data_ptr(),
+                              so, lp, op, ob, oh, on, kept.data_ptr(), width, out_width, batch, keep, first, recent)
     except struct.error as e:
         _refuse(fn, f"keep {keep!r}, first {first!r}, recent {recent!r}: {e}")
-    r = load().lw_kv_evict(cache.ref, a, d_status.data_ptr(),
-                           _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    r = _lib.lw_kv_evict(cache.ref, a, d_status.data_ptr(),
+                         _raw_stream(dev) if stream is None else stream.cuda_stream)
     if r:
         raise LwError(r, fn)
 

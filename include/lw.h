@@ -840,8 +840,8 @@ size_t lw_kv_summary_bytes(const lw_kv_cache* c);   /* 0 for an unsupported shap
 
 /* Summaries of the pages that hold tokens start[b] .. kv_len[b] - 1 of each
    sequence, from all of their keys below kv_len[b] (a negative start counts as 0).
-   To be called when tokens were written, before the attention that reads them.  start, kv_len:
-   device [batch].  kv_len past the table: clamped, LW_DEV_BAD_SEQ; pages
+   To be called when tokens were written or moved (from 0 on where lw_kv_evict moved a
+   sequence's), before the attention that reads them.  start, kv_len: device [batch].  kv_len past the table: clamped, LW_DEV_BAD_SEQ; pages
    outside the cache: left out, LW_DEV_BAD_PAGE. */
 typedef struct {
   void* summary;
@@ -878,8 +878,8 @@ typedef struct {
   int32_t blocks, first, recent, reserved;
 } lw_kv_blocks;
 
-/* Bytes of device workspace: the first lw_kv_workspace_bytes(...) of it are zeroed before first
-   use as for lw_kv_attention (zeroing all is right too); 0 for an unsupported shape. */
+/* Bytes of device workspace, zeroed by the caller before first use, and used, as lw_kv_attention's; 0 for an
+   unsupported shape. */
 size_t lw_kv_blocks_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens,
                                     int32_t table_width, int32_t blocks);
 

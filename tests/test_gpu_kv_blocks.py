@@ -10,7 +10,7 @@ from decode_gemv_gb300 import lw
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
-    from tests.kv_plain import DEV, TYPES, filled, generator, i32, keys_values, read, relative, slots_of, status
+    from kv_plain import DEV, TYPES, filled, generator, i32, keys_values, read, relative, slots_of, status
 TOL = {"fp32": 7.6e-5, "fp16": 7.6e-5 + 2.0 ** -11, "bf16": 1e-2 + 2.0 ** -8}
 
 

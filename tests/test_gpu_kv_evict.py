@@ -9,7 +9,7 @@ from decode_gemv_gb300 import lw
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
-    from tests.kv_plain import DEV, filled, generator, i32, read_all, slots_of, status
+    from kv_plain import DEV, filled, generator, i32, read_all, slots_of, status
 
 
 @pytest.fixture(scope="module", autouse=True)

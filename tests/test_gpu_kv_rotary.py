@@ -14,7 +14,7 @@ from decode_gemv_gb300 import lw
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
-    from tests.kv_plain import DEV, TYPES, generator, keys_values, pool, read_all, status
+    from kv_plain import DEV, TYPES, generator, keys_values, pool, read_all, status
 
 
 @pytest.fixture(scope="module", autouse=True)

@@ -11,7 +11,7 @@ from decode_gemv_gb300 import lw
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
-    from tests.kv_plain import DEV, generator, i32, pool, read, relative, scores, slots_of, spans, status
+    from kv_plain import DEV, generator, i32, pool, read, relative, scores, slots_of, spans, status
 HQ, H, D, PAGE, KEEP, FIRST, RECENT, BLOCKS = 8, 2, 128, 16, 128, 4, 32, 5
 LENS, STEPS = [300, 90], 40
 

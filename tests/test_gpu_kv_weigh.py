@@ -13,7 +13,7 @@ from decode_gemv_gb300 import lw
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
-    from tests.kv_plain import DEV, TYPES, filled, generator, i32, read, relative, scores, slots_of, spans, status
+    from kv_plain import DEV, TYPES, filled, generator, i32, read, relative, scores, slots_of, spans, status
 TOL = 8e-5
 
 
