@@ -26,10 +26,11 @@ namespace dev {
 // not be read by way of the read-only path, which the wait for that work does not
 // order.
 // With `parts` every token and key/value head is a sequence of its own, of one token
-// (b = token * parts + head) on kv_len[b] keys, or of none where that is negative.
-template <bool LOUD>
+// (b = token * parts + head) on kv_len[b] keys, or of none where that is negative.  PARTS: the kernel that takes
+// such calls (the other's registers are short: the question alone cost it 4 %).
+template <bool LOUD, bool PARTS>
 __device__ __forceinline__ void kv_seq(const AttnArgs& a, int b, int& q0, int& T, int& n) {
-  if (a.parts) {
+  if (PARTS && a.parts) {
     q0 = b;
     n = a.p.kv_len[b];
     T = n >= 0;
@@ -83,7 +84,7 @@ __device__ __forceinline__ KvShape kv_shape(const AttnArgs& a) {
 
 // On to the next item that has units of this CTA's; false at the end of the
 // range.
-template <int RT, int PER, int EXTRA>
+template <int RT, int PER, int EXTRA, bool PARTS = false>
 __device__ __forceinline__ bool kv_advance(const AttnArgs& a, KvWalk& w, int& q0) {
   const KvShape c = kv_shape<RT, PER, EXTRA>(a);
   do {
@@ -94,7 +95,7 @@ __device__ __forceinline__ bool kv_advance(const AttnArgs& a, KvWalk& w, int& q0
       w.h = w.rt = 0;
       do {
         ++w.b;
-        kv_seq<false>(a, w.b, q0, w.T, w.n);
+        kv_seq<false, PARTS>(a, w.b, q0, w.T, w.n);
       } while (w.T == 0);
     }
     kv_enter(c, w);
@@ -157,7 +158,7 @@ __device__ __forceinline__ void kv_seek_warp(const KvShape& c, KvWalk& w, long l
 
 // The CTA's range, and its first item.  Whole CTA of NT threads; false if the
 // CTA has no units.
-template <int NT, int RT, int PER, int EXTRA>
+template <int NT, int RT, int PER, int EXTRA, bool PARTS = false>
 __device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int& q0) {
   __shared__ long long s_scan[NT / 32 + 1], s_base, s_head;
   __shared__ int s_b, s_q0, s_T, s_n;
@@ -169,8 +170,8 @@ __device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int
     const int b = cb + tid;
     T = n = 0;
     if (b < batch) {
-      if (blockIdx.x == 0) kv_seq<true>(a, b, q0, T, n);
-      else kv_seq<false>(a, b, q0, T, n);
+      if (blockIdx.x == 0) kv_seq<true, PARTS>(a, b, q0, T, n);
+      else kv_seq<false, PARTS>(a, b, q0, T, n);
     }
     head = kv_weight_warp(c, T, n);
     sum += a.heads * head;
@@ -198,7 +199,7 @@ __device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int
       const int b = cb + tid;
       long long total;
       T = n = 0;
-      if (b < batch) kv_seq<false>(a, b, q0, T, n);
+      if (b < batch) kv_seq<false, PARTS>(a, b, q0, T, n);
       head = kv_weight_warp(c, T, n);
       before = carry + cta_scan<NT>(a.heads * head, s_scan, total);
       take(b);
@@ -212,7 +213,7 @@ __device__ bool kv_range(const AttnArgs& a, KvWalk& w, int& G, long long& U, int
   w.T = s_T;
   w.n = s_n;
   kv_seek_warp(c, w, s_head);
-  return w.k0 < w.k1 || kv_advance<RT, PER, EXTRA>(a, w, q0);
+  return w.k0 < w.k1 || kv_advance<RT, PER, EXTRA, PARTS>(a, w, q0);
 }
 
 // 4 or 8 consecutive elements of an output row, rounded to its type

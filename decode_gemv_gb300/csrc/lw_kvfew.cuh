@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(Few<D, MODE>::kThreads, Few<D, MODE>::kPerSm) 
     KvWalk w;
     int G, q0;
     long long U;
-    if (!kv_range<NT, RT, F::kUnit, kFewExtra>(a, w, G, U, q0)) return;
+    if (!kv_range<NT, RT, F::kUnit, kFewExtra, true>(a, w, G, U, q0)) return;
     if (threadIdx.x == 0) {
       s_walk[0] = w;
       s_q0[0] = q0;
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(Few<D, MODE>::kThreads, Few<D, MODE>::kPerSm) 
     if (threadIdx.x == NT - 32) {   // the item after, while this one's first tiles come
       KvWalk x = w;
       int q0 = s_q0[cur];
-      s_more = kv_advance<RT, F::kUnit, kFewExtra>(a, x, q0);
+      s_more = kv_advance<RT, F::kUnit, kFewExtra, true>(a, x, q0);
       s_walk[cur ^ 1] = x;
       s_q0[cur ^ 1] = q0;
     }

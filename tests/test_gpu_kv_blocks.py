@@ -268,3 +268,27 @@ def test_replayed():
         torch.cuda.synchronize()
         check(cache, q, start, now, table, 6, 1, 2, 1 / math.sqrt(128), (out, lse, chosen), TOL["bf16"])
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("batch", [1, 120])
+def test_thousands_of_pages(batch):
+    """6250 pages of 16 keys: shared by a cluster, or (many heads of sequences) one CTA's."""
+    gen, st, n, page = generator(7), status(), 100000, 16
+    cache, table, _ = filled(gen, [n], 2, 64, page)
+    summary = torch.zeros(lw.lw_kv_summary_bytes(cache), dtype=torch.uint8, device=DEV)
+    lw.lw_kv_summarise(cache, summary, i32([0]), i32([n]), table, st)
+    q = torch.randn(batch, 4, 64, device=DEV, generator=gen)
+    # sequences that share their pages: queries at any position
+    lens = [n - 800 * i for i in range(batch)]
+    got = attend(cache, summary, q, list(range(batch + 1)), lens, table.expand(batch, -1).contiguous(), st, 70, 2, 3)
+    assert int(st) == 0
+    chi, clo, step = summary_of(cache, table[0], n)
+    for b in range(0, batch, 17):
+        # (the last page of a shorter sequence is summed up whole, and always read)
+        nb = (lens[b] - 1) // page + 1
+        for h in range(2):
+            c, u = coded(q[b, 2 * h:2 * h + 2], q[b, 2 * h:2 * h + 2].abs().amax(-1, keepdim=True))
+            dot = torch.maximum(c[:, None] * chi[:nb, h], c[:, None] * clo[:nb, h]).double().sum(-1).float()
+            score = (dot * u).amax(0) * step[:nb, h]
+            assert got[2][b, h].tolist() == chosen_by(score.tolist(), nb, 70, 2, 3)
+    check(cache, q[:1], [0, 1], lens[:1], table, 70, 2, 3, 0.125, [x[:1] for x in got], TOL["fp32"])

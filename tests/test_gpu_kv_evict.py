@@ -9,7 +9,7 @@ from decode_gemv_gb300 import lw
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
-    from kv_plain import DEV, filled, generator, i32, read_all, slots_of, status
+    from kv_plain import DEV, filled, generator, i32, read, read_all, slots_of, status
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -150,3 +150,20 @@ def test_replayed():
                 assert torch.equal(w[b, h, :len(at)], host[b, h, at])
         kv_len.copy_(out_len)
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal"])
+def test_more_keys_than_shared_memory_holds(kind):
+    """400000 keys of one head: eight CTAs' stretches of 50000 are read again instead of kept."""
+    gen, st, n, keep = generator(3), status(), 400000, 1500
+    cache, table, free = filled(gen, [n], 1, 64, 256, 6)
+    w = weights(gen, 1, 1, n, kind)
+    kept, out_len = torch.empty(1, 1, keep, dtype=torch.int32, device=DEV), i32([0])
+    out, to = torch.empty(1, 1, keep, device=DEV), free[:6].view(1, 6).contiguous()
+    before = read(cache, slots_of(table[0], range(n), 256))
+    lw.lw_kv_evict(cache, w, i32([n]), table, to, out_len, out, kept, st, keep=keep, first=7, recent=100)
+    at = choose(w[0, 0].tolist(), n, keep, 7, 100)
+    assert int(st) == 0 and kept[0, 0].tolist() == at and int(out_len) == keep
+    assert torch.equal(out[0, 0], w[0, 0, at])
+    now = read(cache, slots_of(to[0], range(keep), 256))
+    assert all(torch.equal(x, y[at]) for x, y in zip(now, before))

@@ -255,3 +255,17 @@ def test_many_sequences_of_many_rows():
             assert relative(w[b, :, :n], want[b, :, :n]) <= TOL, (hint, b)
             assert bool((w[b, :, n:] == 9).all())
     assert int(st) == 0
+
+
+def test_no_queries():
+    """Sequences without query tokens: what was there, or zeros."""
+    gen, st = generator(15), status()
+    cache, table, _ = filled(gen, [70, 0], 2, 64, 16)
+    q, lse = queries(gen, 0, 4, 64, "fp32"), torch.empty(0, 4, device=DEV)
+    w = torch.rand(2, 2, 75, device=DEV, generator=gen)
+    had = w.clone()
+    weigh(cache, table, q, lse, [0, 0, 0], [70, 0], w, st, max_q=0, add_to=w)
+    assert torch.equal(w, had)
+    weigh(cache, table, q, lse, [0, 0, 0], [70, 0], w, st, max_q=0)
+    assert not bool(w[0, :, :70].any()) and torch.equal(w[0, :, 70:], had[0, :, 70:]) and torch.equal(w[1], had[1])
+    assert int(st) == 0
