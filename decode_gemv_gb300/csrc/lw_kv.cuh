@@ -41,6 +41,8 @@ struct CacheArgs {
   int32_t page_tiles, page_shift, heads;   // page_tiles = 2^page_shift, or page_shift < 0
   int32_t* status;
 };
+CacheArgs kv_cache_args(const lw_kv_cache* c, const lw_kv_rows* k, const lw_kv_rows* v, const int64_t* slots,
+                        int64_t n, int32_t* d_status);
 
 namespace dev {
 

@@ -1,6 +1,6 @@
 // Sparse attention over the 4-bit cache: summaries of pages, and the choice of
 // the pages that each query reads.
-#include "lw_kvfew.cuh"
+#include "lw_kv.cuh"
 #include "lw_kv.h"
 #include "lw_kvselect.cuh"
 

@@ -7,9 +7,6 @@
 
 namespace lw {
 
-CacheArgs kv_cache_args(const lw_kv_cache* c, const lw_kv_rows* k, const lw_kv_rows* v, const int64_t* slots,
-                        int64_t n, int32_t* d_status);
-
 namespace {
 
 // ---- the table ---------------------------------------------------------------

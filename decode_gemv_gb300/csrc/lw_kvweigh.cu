@@ -27,13 +27,14 @@ lw_status launch_few_d(const WeighArgs& a, bool one, dim3 grid, cudaStream_t st)
 // The variant, by the rows of a sequence on a key/value head.  us, 8 sequences of 32768 keys | 64 of 512, 8 heads of
 // 128: a block of 8 rows in registers, 64 rows in shared memory, kv_weigh_many_kernel
 //   bf16   8 rows   57  71        |  12  13        fp32   8 rows   71  81        |  14  15
-//         16 rows  110  89  598   |  22  16  87         16 rows  138 107  645   |  25  19  94
-//        128 rows  855 397  534   | 157  59  87        128 rows 1076 542  582   | 185  79 102
-//        192 rows      594  635   |      87 101        160 rows      704  709   |     102 122
-//                                                      192 rows      812  708   |     117 125
-// One sequence of 8192 keys alone, 192 rows: 27 and 29, 35 and 33.  (kv_weigh_many_kernel takes rows 128 at a time,
-// and a unit of 128 keys starts slowly.)
-constexpr int kOneMost = 8, kFewMost16 = 192, kFewMost32 = 160;
+//         16 rows  110  89        |  22  16              16 rows  138 107        |  25  19
+//        128 rows  855 397  455   | 157  59  73         128 rows 1076 542  464   | 185  79  83
+//        160 rows      519  554   |      77  87         160 rows      705  603   |     102 104
+//        192 rows      594  550   |      87  88
+// One sequence of 8192 keys alone: bf16 256 rows 35 and 24, fp32 192 rows 35 and 28.  (kv_weigh_many_kernel takes
+// rows 128 at a time, and a unit of 128 keys starts slowly.  Between 64 and 128 rows in fp32 the first 64 cost 271
+// and the next ones as much.)
+constexpr int kOneMost = 8, kFewMost16 = 160, kFewMost32 = 112;
 
 inline int64_t row_tiles(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens) {
   return (q_tokens * (q_heads / c->kv_heads) + 127) / 128;
@@ -52,10 +53,23 @@ lw_status launch_many(const WeighArgs& a, void* ws, int64_t tiles, int64_t key_t
                                 512, 0, 1, st, r);
   if (s != LW_OK) return s;
   const WeighManyArgs w{a, static_cast<const uint8_t*>(ws), (int32_t)tiles};
-  // CTAs of a unit, until the device is full; and units' CTAs of a sequence's head, all at once or as many as fill it
-  // eight times over (a table may be far wider than its sequences are long: a CTA without keys costs 2 us)
-  const int64_t pairs = (int64_t)a.heads * a.p.batch, most = (8 * device_sm_count() + pairs - 1) / pairs;
-  const int64_t x = key_tiles < most ? key_tiles : most;
+  // CTAs of a sequence's head: each takes every so many-th unit, and fetches the next one's keys meanwhile.  One
+  // sequence's units are alike: as many CTAs as the device takes at once, if that many fit its heads; several
+  // sequences may not be: some rounds of CTAs, of 4 to 8 the one that wastes least (a table may also be far wider
+  // than its sequences are long: a CTA without keys costs 2 us).
+  const int64_t pairs = (int64_t)a.heads * a.p.batch, sms = device_sm_count();
+  int64_t x = 1;
+  double best = 0.0;
+  for (int k = a.p.batch == 1 ? 1 : 4; k <= 8 && best < 0.95; ++k) {
+    const int64_t n = k * sms / pairs > 1 ? k * sms / pairs : 1;
+    const double use = (double)(n * pairs) / (double)((n * pairs + sms - 1) / sms * sms);
+    if (use > best) {
+      best = use;
+      x = n;
+    }
+  }
+  if (x > key_tiles) x = key_tiles;
+  // CTAs of a unit, until the device is full
   int ranks = 1;
   while (ranks < 8 && 2 * ranks * key_tiles * pairs <= device_sm_count()) ranks *= 2;
   return kv_launch("lw_kv_weigh", kernel, dim3((unsigned)(x * ranks), (unsigned)a.heads, (unsigned)a.p.batch),

@@ -23,9 +23,11 @@
 //    a thread reads its key's 128 scores and adds 2^(s f - lse) of those that it is
 //    seen by.  A key is seen by a contiguous range of rows (causal: from some row
 //    on, windowed: up to some row), so only tiles across an end of it are masked.
-// 2048 tokens on 14336 keys (8 heads of 128 with 4 query heads each, bf16): 350 us, 736 TFLOP/s of useful
-// products, of which two are carried out for one: 1470, three quarters of what the tensor cores give.  The rest is
-// the start of a unit (keys, tensor memory: 3 us of 46) and the last round of units.
+// 2048 tokens on 14336 keys (8 heads of 128 with 4 query heads each, bf16): 360 us, 716 TFLOP/s of useful
+// products, of which two are carried out for one: 1430, 84 % of what the tensor cores sustain; a tile's exponentials
+// take about as long as its products.  8 sequences of 32768 keys, 64 tokens each: 522 us, a unit 4.8 us, of which 1 is
+// products: its start (keys restored, tensor memory written) and its end.  The next unit's keys are fetched while this
+// one's rows run (603 -> 550 us at 48 tokens).
 // Units are few where keys are: then a cluster shares a unit's row tiles, and rank 0
 // adds the ranks' sums in order.
 #pragma once
@@ -176,10 +178,37 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     tmem_alloc(smem_addr(tslot), 512);
     tmem_relinquish();
   }
+  __syncthreads();   // (barriers)
   bool ok = true;
-  int done = 0;           // row tiles of the units before: the barriers' phases go on
+  int done = 0, sent = 0;   // row tiles of the units before (the barriers' phases go on), and (thread 0) sent for
   uint32_t unit = 0;
   const int step = (int)(gridDim.x / ranks) * W::kKeys;
+  const float* add = a.p.add_to ? a.p.add_to + b * a.p.add_seq_stride + h * a.p.add_head_stride : nullptr;
+  float* out = a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride;
+  // Keys: a lane of tensor memory each, half of their elements a group of four warps (2 ..)
+  const int kw = warp - 2, group = kw / 4, quarter = warp % 4, key = 32 * quarter + lane;
+  constexpr int kOct = D / 16;   // 8-element columns of a thread: words of codes
+  uint32_t kc[kOct];
+  __half sc[kOct], mn[kOct];
+  bool next_real = false;
+  const auto fetch = [&](int k0) {
+    next_real = false;
+    if (warp < 2 || k0 >= keys) return;
+    const int j = k0 + key, tile = j / 16, tpp = a.page_tokens / LW_KV_TILE, tk = j % 16;
+    const int page = j < keys ? a.p.page_table[(int64_t)b * a.p.table_stride + tile / tpp] : -1;
+    next_real = page >= 0 && page < a.n_pages;
+    if (!next_real && j < keys) report(a.status, LW_DEV_BAD_PAGE);
+    if (!next_real) return;
+    const uint8_t* s = a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
+#pragma unroll
+    for (int i = 0; i < kOct; ++i) {
+      const int o = kOct * group + i, g = o / 4;   // column o: elements 32 g + 8 (o % 4) ..
+      kc[i] = *reinterpret_cast<const uint32_t*>(s + L::kKeyCodes + ((tk * 4 + o % 4) * G + g) * 4);
+      sc[i] = *reinterpret_cast<const __half*>(s + L::kKeyScale + 2 * ((tk / 2 * G + g) * 2 + tk % 2));
+      mn[i] = *reinterpret_cast<const __half*>(s + L::kKeyMin + 2 * (tk * L::GP + g));
+    }
+  };
+  fetch(k0);
   for (; k0 < keys; k0 = k0 < keys - step ? k0 + step : keys, ++unit) {
     const int k1 = min(k0 + W::kKeys, keys);
     const int64_t ra = first_row(k0), rb = end_row(k1 - 1);
@@ -190,33 +219,40 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
       t0 = first + (int)((int64_t)all * rank / ranks);
       nt = first + (int)((int64_t)all * (rank + 1) / ranks) - t0;
     }
-    // ---- the keys: a lane of tensor memory each, half of their elements a group of four warps
-    const int kw = warp - 2, group = kw / 4, quarter = warp % 4, key = 32 * quarter + lane, j = k0 + key;
-    constexpr int kOct = D / 16;   // 8-element columns of a thread: words of codes
-    uint32_t kc[kOct];
-    float sc[kOct], mn[kOct];
-    bool real = false;             // (a key past the end, or of a page that is not there, is seen by no row)
+    // (thread 0) The next row tile, where its places are free: the first ones while the keys come
+    const auto send = [&] {
+      const int s = sent % S, d = sent % W::kSlots;
+      ok = many_wait(&bar.b_free[s], (uint32_t)(sent / S & 1) ^ 1u, flags) &&
+           many_wait(&bar.d_free[d], (uint32_t)(sent / W::kSlots & 1) ^ 1u, flags);
+      if (!ok) return;
+      const uint8_t* src = w.rows + ((int64_t)h * w.row_tiles + t0 + sent - done) * W::kRecord;
+      mbar_arrive_expect_tx(&bar.p_full[d], W::kParam);
+      bulk_g2s(smem + W::kParams + d * W::kParam, src + W::kImage, W::kParam, &bar.p_full[d]);
+      mbar_arrive_expect_tx(&bar.b_full[s], W::kImage);
+      bulk_g2s(smem + W::kB + s * W::kImage, src, W::kImage, &bar.b_full[s]);
+      ++sent;
+    };
+    if (threadIdx.x == 0)
+      for (int i = 0; i < S && i < nt && ok; ++i) send();
+    // ---- the keys, which have been sent for
+    const int j = k0 + key;
+    const bool real = next_real;   // (a key past the end, or of a page that is not there, is seen by no row)
     if (warp >= 2) {
-      const int tile = j / 16, tpp = a.page_tokens / LW_KV_TILE, tk = j % 16;
-      const int page = j < keys ? a.p.page_table[(int64_t)b * a.p.table_stride + tile / tpp] : -1;
-      real = page >= 0 && page < a.n_pages;
-      if (!real && j < keys) report(a.status, LW_DEV_BAD_PAGE);
       float top = 0.f;
-      if (real) {
-        const uint8_t* s = a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
+      if (real)
 #pragma unroll
         for (int i = 0; i < kOct; ++i) {
-          const int o = kOct * group + i, g = o / 4;   // column o: elements 32 g + 8 (o % 4) ..
-          kc[i] = *reinterpret_cast<const uint32_t*>(s + L::kKeyCodes + ((tk * 4 + o % 4) * G + g) * 4);
-          sc[i] = __half2float(*reinterpret_cast<const __half*>(s + L::kKeyScale + 2 * ((tk / 2 * G + g) * 2 + tk % 2)));
-          mn[i] = __half2float(*reinterpret_cast<const __half*>(s + L::kKeyMin + 2 * (tk * L::GP + g)));
-          top = fmaxf(top, fmaxf(fabsf(mn[i]), fabsf(fmaf(15.f, sc[i], mn[i]))));
+          const float m = __half2float(mn[i]);
+          top = fmaxf(top, fmaxf(fabsf(m), fabsf(fmaf(15.f, __half2float(sc[i]), m))));
         }
-      }
       top = top <= 3.402823466e38f ? top : 65504.f;
       const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
       if (lane == 0) atomicMax(s_top, most);
     }
+    // what the sums are added to
+    const int at = k0 + (int)threadIdx.x;
+    const bool last = rank == 0 && threadIdx.x < W::kKeys && at < keys;
+    const float had = last && add ? add[at] : 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -235,7 +271,8 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t c = e % 2 ? whole_odd(kc[i + x] >> (8 * (e / 2))) : whole_even(kc[i + x] >> (8 * (e / 2)));
-              const float2 y = mul2(fma2(h2f(c), make_float2(sc[i + x], sc[i + x]), make_float2(mn[i + x], mn[i + x])), make_float2(up, up));
+              const float s1 = __half2float(sc[i + x]), m1 = __half2float(mn[i + x]);
+              const float2 y = mul2(fma2(h2f(c), make_float2(s1, s1), make_float2(m1, m1)), make_float2(up, up));
               split2<1>(y.x, y.y, hi[4 * x + e], lo[4 * x + e]);
             }
         }
@@ -249,27 +286,18 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     __syncthreads();
     tc_fence_after();
     if (threadIdx.x == 0) *s_top = 0;   // (all have read it)
+    fetch(k0 < keys - step ? k0 + step : keys);   // the next unit's, while this one's rows run
     if (warp == 0) {   // ---- row tiles
       if (lane == 0) {
-        const uint8_t* src = w.rows + ((int64_t)h * w.row_tiles + t0) * W::kRecord;
-        int i = done;
-        for (; i < done + nt && ok; ++i, src += W::kRecord) {
-          const int s = i % S, d = i % W::kSlots;
-          ok = many_wait(&bar.b_free[s], (uint32_t)(i / S & 1) ^ 1u, flags) &&
-               many_wait(&bar.d_free[d], (uint32_t)(i / W::kSlots & 1) ^ 1u, flags);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&bar.p_full[d], W::kParam);
-          bulk_g2s(smem + W::kParams + d * W::kParam, src + W::kImage, W::kParam, &bar.p_full[d]);
-          mbar_arrive_expect_tx(&bar.b_full[s], W::kImage);
-          bulk_g2s(smem + W::kB + s * W::kImage, src, W::kImage, &bar.b_full[s]);
-        }
+        for (; sent < done + nt && ok;) send();
         if (!ok) {
           flags[0] = 1;
           report(a.status, LW_DEV_TIMEOUT);
-          for (int x = max(0, i - 4); x < i; ++x) {   // no copy may be in flight when the CTA ends
+          for (int x = max(0, sent - 4); x < sent; ++x) {   // no copy may be in flight when the CTA ends
             mbar_wait(&bar.p_full[x % W::kSlots], (uint32_t)(x / W::kSlots & 1));
-            if (x >= i - S) mbar_wait(&bar.b_full[x % S], (uint32_t)(x / S & 1));
+            if (x >= sent - S) mbar_wait(&bar.b_full[x % S], (uint32_t)(x / S & 1));
           }
+          sent = done + nt;
         }
       }
     } else if (warp == 1) {   // ---- products
@@ -373,14 +401,10 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     // the groups' sums, then the ranks', in order
     if (threadIdx.x < W::kKeys) sums[threadIdx.x] += sums[W::kKeys + threadIdx.x];
     if (ranks > 1) cluster_sync();
-    if (rank == 0 && threadIdx.x < W::kKeys) {
-      const int at = k0 + threadIdx.x;
-      float s = sums[threadIdx.x];
-      for (int r = 1; r < ranks; ++r) s += cluster_load(sums + threadIdx.x, (uint32_t)r);
-      if (at < keys) {
-        const float* add = a.p.add_to ? a.p.add_to + b * a.p.add_seq_stride + h * a.p.add_head_stride : nullptr;
-        (a.p.weights + b * a.p.w_seq_stride + h * a.p.w_head_stride)[at] = (add ? add[at] : 0.f) + s;
-      }
+    if (last) {
+      float sum = sums[threadIdx.x];
+      for (int r = 1; r < ranks; ++r) sum += cluster_load(sums + threadIdx.x, (uint32_t)r);
+      out[at] = had + sum;
     }
     if (ranks > 1) cluster_sync();   // (a rank's sums stay until they are read)
   }
