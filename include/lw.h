@@ -918,7 +918,7 @@ void lw_graph_free(lw_graph* g);
    lw_dev_bundle.lut_entries, which selects the table-driven product
    kernel; 3 added grouped launches, strip lists, the load-time
    transcode, bundle files, step graphs, LW_ERR_IO, LW_DEV_BAD_STRIPS; the
-   lw_kv_* calls came later and changed nothing before them).  The
+   lw_kv_* and lw_rotary_* calls came later and changed nothing before them).  The
    bundle file format carries its own version. */
 int32_t lw_version(void);
 
