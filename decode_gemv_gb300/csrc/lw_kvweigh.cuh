@@ -66,6 +66,12 @@ __device__ __forceinline__ void weigh_seq(const WeighArgs& a, int b, int& q0, in
   n = n < 0 ? 0 : (n > most ? most : n);
 }
 
+// The first key that a row of a sequence of T > 0 query tokens sees (the last one is the sequence's)
+__device__ __forceinline__ int weigh_first(const WeighArgs& a, int T, int n) {
+  const int64_t lo = a.p.window ? (int64_t)n - T - a.p.window + 1 : 0;
+  return lo > 0 ? (int)lo : 0;
+}
+
 // 8 consecutive elements of a query row
 template <class T>
 __device__ __forceinline__ void weigh_load8(const WeighArgs& a, int64_t at, float (&x)[8]) {
@@ -144,8 +150,8 @@ __device__ void weigh_row(const WeighArgs& a, uint8_t* smem, int blk, int r, int
 }
 
 // A warp's pairs of neighbouring tiles: first, first + step, ... below `end` (in tiles), their key halves fetched by
-// bulk copies into a ring of its own, in order.  The page table is read 32 tiles at a time: lanes 2 i and 2 i + 1
-// hold the i-th pair's places.
+// bulk copies into a ring of its own, in order.  Tiles below `seen` hold no key that a row sees: they need no page.
+// The page table is read 32 tiles at a time: lanes 2 i and 2 i + 1 hold the i-th pair's places.
 template <int D, class T, bool ONE>
 struct WeighFetch {
   using W = WeighFew<D, T, ONE>;
@@ -153,14 +159,14 @@ struct WeighFetch {
   uint64_t* bars;
   const int32_t* table;
   int64_t head;
-  int next, end, step, at, in, out;
+  int next, seen, end, step, at, in, out;
   uint32_t there, have, parity;   // tiles that have a page; tiles sent for (2 bits a place); phase per place
   const uint8_t* src;
 
   __device__ __forceinline__ void lookup(const WeighArgs& a, int lane) {
     const int64_t tile = next + (int64_t)(lane / 2) * step + lane % 2;
     const int tpp = a.page_tokens / LW_KV_TILE;
-    const bool mine = tile < end;
+    const bool mine = tile >= seen && tile < end;
     const int page = mine ? table[tile / tpp] : -1;
     const bool ok = page >= 0 && page < a.n_pages;
     if (mine && !ok) report(a.status, LW_DEV_BAD_PAGE);
@@ -264,6 +270,7 @@ __global__ void __launch_bounds__(WeighFew<D, T, ONE>::kThreads, WeighFew<D, T, 
   f.ring = smem + W::kRing + warp * W::kStages * 2 * W::kKeys;
   f.table = a.p.page_table + (int64_t)b * a.p.table_stride;
   f.head = (int64_t)h * (a.page_tokens / LW_KV_TILE) * L::kBytes;
+  f.seen = Tq ? weigh_first(a, Tq, n) / 16 : tiles;
   f.end = tiles;
   f.step = gridDim.x * W::kWarps * 2;
   f.parity = 0;

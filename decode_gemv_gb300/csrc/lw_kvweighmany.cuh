@@ -195,9 +195,10 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     next_real = false;
     if (warp < 2 || k0 >= keys) return;
     const int j = k0 + key, tile = j / 16, tpp = a.page_tokens / LW_KV_TILE, tk = j % 16;
-    const int page = j < keys ? a.p.page_table[(int64_t)b * a.p.table_stride + tile / tpp] : -1;
+    const bool seen = j < keys && first_row(j) < end_row(j);   // (else its page is not needed)
+    const int page = seen ? a.p.page_table[(int64_t)b * a.p.table_stride + tile / tpp] : -1;
     next_real = page >= 0 && page < a.n_pages;
-    if (!next_real && j < keys) report(a.status, LW_DEV_BAD_PAGE);
+    if (!next_real && seen) report(a.status, LW_DEV_BAD_PAGE);
     if (!next_real) return;
     const uint8_t* s = a.pages + page * a.page_bytes + ((int64_t)h * tpp + tile % tpp) * L::kBytes;
 #pragma unroll
@@ -209,16 +210,23 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     }
   };
   fetch(k0);
-  for (; k0 < keys; k0 = k0 < keys - step ? k0 + step : keys, ++unit) {
+  for (int next; k0 < keys; k0 = next) {
+    next = k0 < keys - step ? k0 + step : keys;
     const int k1 = min(k0 + W::kKeys, keys);
     const int64_t ra = first_row(k0), rb = end_row(k1 - 1);
-    // this rank's row tiles
-    int t0 = 0, nt = 0;
-    if (ra < rb) {
-      const int first = (int)(ra / W::kRows), all = (int)((rb - 1) / W::kRows) - first + 1;
-      t0 = first + (int)((int64_t)all * rank / ranks);
-      nt = first + (int)((int64_t)all * (rank + 1) / ranks) - t0;
+    // what the sums are added to
+    const int at = k0 + (int)threadIdx.x;
+    const bool last = rank == 0 && threadIdx.x < W::kKeys && at < keys;
+    const float had = last && add ? add[at] : 0.f;
+    if (ra >= rb) {   // no row sees these keys (the same in all of the cluster)
+      fetch(next);
+      if (last) out[at] = had;
+      continue;
     }
+    // this rank's row tiles
+    const int first_tile = (int)(ra / W::kRows), all = (int)((rb - 1) / W::kRows) - first_tile + 1;
+    const int t0 = first_tile + (int)((int64_t)all * rank / ranks);
+    const int nt = first_tile + (int)((int64_t)all * (rank + 1) / ranks) - t0;
     // (thread 0) The next row tile, where its places are free: the first ones while the keys come
     const auto send = [&] {
       const int s = sent % S, d = sent % W::kSlots;
@@ -249,10 +257,6 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
       const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
       if (lane == 0) atomicMax(s_top, most);
     }
-    // what the sums are added to
-    const int at = k0 + (int)threadIdx.x;
-    const bool last = rank == 0 && threadIdx.x < W::kKeys && at < keys;
-    const float had = last && add ? add[at] : 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
     __syncthreads();
     tc_fence_after();
     if (threadIdx.x == 0) *s_top = 0;   // (all have read it)
-    fetch(k0 < keys - step ? k0 + step : keys);   // the next unit's, while this one's rows run
+    fetch(next);   // the next unit's, while this one's rows run
     if (warp == 0) {   // ---- row tiles
       if (lane == 0) {
         for (; sent < done + nt && ok;) send();
@@ -407,6 +411,7 @@ __global__ void __launch_bounds__(320, 1) kv_weigh_many_kernel(const WeighManyAr
       out[at] = had + sum;
     }
     if (ranks > 1) cluster_sync();   // (a rank's sums stay until they are read)
+    ++unit;
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc(*tslot, 512);

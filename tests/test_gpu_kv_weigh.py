@@ -269,3 +269,41 @@ def test_no_queries():
     weigh(cache, table, q, lse, [0, 0, 0], [70, 0], w, st, max_q=0)
     assert not bool(w[0, :, :70].any()) and torch.equal(w[0, :, 70:], had[0, :, 70:]) and torch.equal(w[1], had[1])
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("typ", ["fp32", "bf16"])
+@pytest.mark.parametrize("ts", [[1, 0, 3], [60, 0, 700], [400, 0, 5]], ids=str)
+@pytest.mark.parametrize("causal", [True, False])
+def test_pages_that_no_row_sees_are_not_needed(ts, causal, typ):
+    """Pages behind the window, and those of a sequence without query tokens, are freed: attention with the same
+    arguments does not read them, and neither do its weights.  What was there stays, or is 0."""
+    gen, st, lens, page, window = generator(16 + sum(ts)), status(), [3000, 900, 2500], 16, 129
+    cache, table, _ = filled(gen, lens, 2, 64, page)
+    start = [sum(ts[:i]) for i in range(4)]
+    q = queries(gen, start[-1], 8, 64, typ)
+    freed = table.clone()
+    first = [max(0, n - t - window + 1) if t else n for n, t in zip(lens, ts)]      # the first key that a row sees
+    for b in range(3):
+        freed[b, :first[b] // page if ts[b] else None] = -1
+    kw = dict(max_q=max(ts), causal=causal, window=window, scale=0.125)
+    lse, out = torch.empty(start[-1], 8, device=DEV), torch.empty_like(q)
+    ws = torch.zeros(lw.lw_kv_workspace_bytes(cache, 8, start[-1], 3), dtype=torch.uint8, device=DEV)
+    lw.lw_kv_attention(cache, q, i32(start), i32(lens), freed, out, ws, st, lse=lse, **kw)
+    assert int(st) == 0
+    lse = logsums(cache, table, q, start, lens, causal, window, 0.125)
+    add = torch.rand(3, 2, 3000, device=DEV, generator=gen)
+    for given in (None, add):
+        want = expected(cache, table, q, start, lens, lse, given, causal, window, 0.125)
+        for hint in (max(ts), 1):
+            w = torch.full((3, 2, 3000), 7.0, device=DEV)
+            weigh(cache, freed, q, lse, start, lens, w, st, add_to=given, **{**kw, "max_q": hint})
+            assert int(st) == 0
+            for b, n in enumerate(lens):
+                assert relative(w[b, :, :n], want[b, :, :n]) <= TOL, (b, hint)
+                unseen = torch.zeros_like(w[b, :, :first[b]]) if given is None else given[b, :, :first[b]]
+                assert torch.equal(w[b, :, :first[b]], unseen) and bool((w[b, :, n:] == 7).all())
+    # the page of the first key that is seen is needed
+    gone = freed.clone()
+    gone[0, first[0] // page] = -1
+    weigh(cache, gone, q, lse, start, lens, w, st, **kw)
+    assert int(st) == lw.LW_DEV_BAD_PAGE
