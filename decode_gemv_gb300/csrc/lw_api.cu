@@ -26,16 +26,29 @@ int device_sm_count() {
 int resident_blocks(const void* kernel, int threads, size_t smem) {
   static std::mutex mu;
   static std::unordered_map<uint64_t, int> occ;           // (kernel, smem, device) -> blocks
-  static std::unordered_map<uint64_t, size_t> smem_set;   // (kernel, device) -> limit set
+  struct Limit {
+    size_t set, own;   // bytes of dynamic shared memory allowed so far; of the kernel's own, static, share
+  };
+  static std::unordered_map<uint64_t, Limit> limits;      // (kernel, device)
   int d = 0;
   cudaGetDevice(&d);
   const uint64_t kd = (reinterpret_cast<uint64_t>(kernel) << 7) ^ (uint64_t)d;
   const uint64_t key = kd * 1315423911ull ^ (uint64_t)smem;
   std::lock_guard<std::mutex> g(mu);
+  auto lim = limits.find(kd);
+  if (lim == limits.end()) {
+    cudaFuncAttributes fa{};
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    lim = limits.emplace(kd, Limit{0, fa.sharedSizeBytes}).first;
+  }
   // the dynamic shared-memory limit of a kernel only ever grows, so a cached
-  // occupancy answer stays valid for every size at or below it
-  size_t& cur = smem_set[kd];
-  if (smem > 48 * 1024 && smem > cur) {
+  // occupancy answer stays valid for every size at or below it (what needs no
+  // limit is counted with the static share)
+  size_t& cur = lim->second.set;
+  if (smem + lim->second.own > 48 * 1024 && smem > cur) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess) {
       cudaGetLastError();

@@ -292,3 +292,45 @@ def test_thousands_of_pages(batch):
             score = (dot * u).amax(0) * step[:nb, h]
             assert got[2][b, h].tolist() == chosen_by(score.tolist(), nb, 70, 2, 3)
     check(cache, q[:1], [0, 1], lens[:1], table, 70, 2, 3, 0.125, [x[:1] for x in got], TOL["fp32"])
+
+
+WIDTHS = """
+import sys
+import torch
+from decode_gemv_gb300 import lw
+
+def run(group, widths):
+    heads, dim, page, blocks = 8, 128, 16, 3
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tokens = 6 * sms // (2 * heads) + 2                 # too many tokens and heads for clusters: one CTA has a table
+    cache = lw.KvCache.empty(4, heads, dim, page, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache.pages.zero_()
+    st, start = torch.zeros(1, **i32), torch.arange(tokens + 1, **i32)
+    n, q = torch.full((tokens,), 64, **i32), torch.ones(tokens, heads * group, dim, device="cuda")
+    summary, out = torch.zeros(lw.lw_kv_summary_bytes(cache), dtype=torch.uint8, device="cuda"), torch.empty_like(q)
+    chosen = torch.empty(tokens, heads, blocks, **i32)
+    for width in widths:
+        table = torch.full((tokens, width), -1, **i32)
+        table[:, :4] = torch.arange(4, **i32)
+        ws = torch.zeros(lw.lw_kv_blocks_workspace_bytes(cache, heads * group, tokens, width, blocks), dtype=torch.uint8,
+                         device="cuda")
+        lw.lw_kv_attention_blocks(cache, summary, q, start, n, table, out, ws, st, blocks=blocks, chosen=chosen)
+        assert bool((chosen == torch.tensor([0, 1, 3], **i32)).all()) and int(st) == 0, (group, width)
+
+for group in (4, 1, 16):
+    # around 48 KB of order keys, heads' codes and the choice's own, and up to the widest
+    room = (49152 - 4300 - 260 * group) // 4 - 32
+    run(group, [*range(room - 24, room + 12, 4), 20000, 40960])
+print("done")
+"""
+
+
+def test_any_width_of_the_page_table():
+    """In a process of its own: what a kernel may take of shared memory is raised by wider tables and stays so."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    r = subprocess.run([sys.executable, "-c", WIDTHS], capture_output=True, text=True, timeout=300,
+                       cwd=Path(__file__).resolve().parent.parent)
+    assert r.returncode == 0 and r.stdout.split()[-1] == "done", r.stdout + r.stderr
