@@ -188,7 +188,7 @@ struct BlockArgs {
   int32_t* pages;        // [q_tokens * heads][blocks]: pages of the cache seen head by head
   int32_t* lens;         // [q_tokens * heads]: keys in them, -1 for a token of no sequence
   int64_t n_pages;
-  int32_t page_tokens, heads, group, most_pages;   // most_pages: of a CTA's stretch
+  int32_t page_tokens, heads, group, most_pages;   // most_pages: room for a CTA's stretch
   int32_t* status;
 };
 
@@ -346,8 +346,7 @@ lw_status launch_choose(BlockArgs a, cudaStream_t st) {
   const int64_t pairs = a.p.q_tokens * a.heads;
   int ranks = 1;
   while (ranks < 8 && 2 * ranks * pairs <= 6 * device_sm_count() && a.p.table_width > 256 * ranks) ranks *= 2;
-  a.most_pages = (a.p.table_width + ranks - 1) / ranks + 32;
-  a.most_pages = (a.most_pages + 3) / 4 * 4;
+  a.most_pages = (int32_t)kv_select_room(a.p.table_width, ranks);
   const size_t smem = sizeof(ChooseShared) + (size_t)a.most_pages * 4 + (size_t)a.group * (2 * D + 4);
   if (resident_blocks(reinterpret_cast<const void*>(kv_choose_kernel<D, T>), kChoose, smem) < 1)
     return fail(LW_ERR_CUDA, "%s: the kernel does not fit this device", fn);

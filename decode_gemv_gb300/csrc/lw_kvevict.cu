@@ -276,7 +276,7 @@ extern "C" lw_status lw_kv_evict(const lw_kv_cache* c, const lw_kv_eviction* p, 
   if (p->w_keys < keys) keys = p->w_keys;
   int ranks = 1;
   while (ranks < 8 && 2 * ranks * pairs <= 3 * sms && keys > 4096ll * ranks) ranks *= 2;
-  int64_t most = (keys + ranks - 1) / ranks + 32;
+  int64_t most = kv_select_room(keys, ranks);
   if (most > kMostSelect) most = kMostSelect;
   a.most_keys = (int32_t)most;
   const size_t smem = sizeof(EvictShared) + (size_t)most * 4;

@@ -16,6 +16,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "lw_kvroom.h"
+
 namespace lw {
 namespace dev {
 
@@ -193,7 +195,7 @@ __device__ __forceinline__ void select_places(SelectShared<BITS>& s, int count, 
 // This CTA's stretch of [first, last): where it begins, and how many there are
 __device__ __forceinline__ int64_t select_stretch(int first, int last, int& count) {
   const uint32_t ranks = cluster_size(), rank = cluster_rank();
-  const int stretch = (int)((((int64_t)last - first + ranks - 1) / ranks + 31) / 32 * 32);
+  const int stretch = kv_select_stretch((long long)last - first, (int)ranks);
   const int64_t from = first + (int64_t)rank * stretch;
   count = from < last ? (int)(last - from < stretch ? last - from : stretch) : 0;
   return from;
