@@ -51,6 +51,9 @@ lw_status kv_launch(const char* fn, void (*kernel)(Args...), dim3 grid, int thre
   return LW_OK;
 }
 
+// Bytes in front of a workspace that hold attention's counters (zero between calls); every call that uses a
+// workspace leaves its first bytes to them, so that one may serve all.
+size_t kv_counter_bytes();
 // Bytes of workspace of an attention call of q_tokens tokens in all.
 size_t kv_attention_workspace(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens);
 // The checks of an attention call but for its workspace.

@@ -25,7 +25,6 @@ Variant variant(int mode) {
 // launch (counts of either kernel: a counter, and two parts of an item, a CTA;
 // twice that for the two row tiles of kv_many_kernel).
 constexpr int kMostPerSm = 2;
-inline size_t attn_counter_bytes() { return ((size_t)kMostPerSm * device_sm_count() * 4 + 255) / 256 * 256; }
 static_assert(Few<64, 0>::kPerSm <= kMostPerSm && Few<64, 1>::kPerSm <= kMostPerSm && Few<64, 2>::kPerSm <= kMostPerSm &&
                   2 * kManyPerSm <= kMostPerSm,
               "workspace places");
@@ -35,11 +34,13 @@ constexpr int kFewMostBf16 = 24, kFewMost = 32;
 
 }  // namespace
 
+size_t kv_counter_bytes() { return ((size_t)kMostPerSm * device_sm_count() * 4 + 255) / 256 * 256; }
+
 // A call whose tokens, were they all one sequence's, are few rows is kv_few_kernel's in every type.
 size_t kv_attention_workspace(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens) {
   const size_t few = (size_t)kMostPerSm * 2 * 16, many = (size_t)2 * 2 * kManyTile;   // rows an SM
   const bool all_few = q_tokens * (q_heads / c->kv_heads) <= kFewMostBf16;
-  return attn_counter_bytes() + (size_t)device_sm_count() * (all_few ? few : many) * (size_t)(c->head_dim + 2) * 4;
+  return kv_counter_bytes() + (size_t)device_sm_count() * (all_few ? few : many) * (size_t)(c->head_dim + 2) * 4;
 }
 
 lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, int parts, void* ws, int32_t* status,
@@ -50,7 +51,7 @@ lw_status launch_kv_attention(const lw_kv_cache* c, const lw_kv_attn* p, int par
   a.n_pages = c->n_pages;
   a.page_bytes = (int64_t)lw_kv_page_bytes(c->kv_heads, c->head_dim, c->page_tokens);
   a.counters = static_cast<uint32_t*>(ws);
-  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attn_counter_bytes());
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kv_counter_bytes());
   a.page_tokens = c->page_tokens;
   a.heads = c->kv_heads;
   a.group = p->q_heads / c->kv_heads;

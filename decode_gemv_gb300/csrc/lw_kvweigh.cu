@@ -93,7 +93,7 @@ extern "C" size_t lw_kv_weigh_workspace_bytes(const lw_kv_cache* c, int32_t q_he
     return 0;
   // none for few rows in all: whatever sequences they are of, kv_weigh_few_kernel takes them, in every type
   if (q_tokens * (q_heads / c->kv_heads) <= kFewMost32) return 0;
-  return (size_t)c->kv_heads * row_tiles(c, q_heads, q_tokens) * record_bytes(c->head_dim, 2);
+  return kv_counter_bytes() + (size_t)c->kv_heads * row_tiles(c, q_heads, q_tokens) * record_bytes(c->head_dim, 2);
 }
 
 extern "C" lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, void* ws, size_t ws_bytes,
@@ -144,6 +144,7 @@ extern "C" lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, v
   const int64_t rows = (a->max_q < a->q_tokens ? a->max_q : a->q_tokens) * w.group;
   if (rows > (a->dtype == LW_F32 ? kFewMost32 : kFewMost16)) {
     const int64_t tiles = row_tiles(c, a->q_heads, a->q_tokens), key_tiles = (keys + 127) / 128;
+    ws = static_cast<uint8_t*>(ws) + kv_counter_bytes();   // (which may be attention's workspace)
     return c->head_dim == 64   ? launch_many_t<64>(w, ws, tiles, key_tiles, st)
            : c->head_dim == 96 ? launch_many_t<96>(w, ws, tiles, key_tiles, st)
                                : launch_many_t<128>(w, ws, tiles, key_tiles, st);

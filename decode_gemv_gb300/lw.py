@@ -1212,6 +1212,8 @@ def _kv_clear(a, b) -> bool:
 
 
 def lw_kv_weigh_workspace_bytes(cache: KvCache, q_heads: int, q_tokens: int) -> int:
+    if cache.index >= 0 and _current_device() != cache.index:   # (sized by the current device)
+        _kv_on("lw_kv_weigh_workspace_bytes", cache)
     return int(load().lw_kv_weigh_workspace_bytes(cache.ref, q_heads, q_tokens))
 
 

@@ -678,7 +678,10 @@ typedef struct {
    q_tokens * q_heads / kv_heads <= 24, and else for many.  What q_tokens asks for
    is enough for fewer as well, whatever the batch.  Zeroed by the caller before
    first use; every call leaves its counters at zero, but for one that reports
-   LW_DEV_TIMEOUT: zero it again then.  0 for an unsupported shape. */
+   LW_DEV_TIMEOUT: zero it again then.  0 for an unsupported shape.
+   One workspace, of the largest of their sizes and zeroed once, may serve all
+   lw_kv_attention, lw_kv_weigh and lw_kv_attention_blocks calls (and graphs of them) that
+   follow one another; calls that may run at the same time need one each. */
 size_t lw_kv_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens,
                              int32_t batch);
 
@@ -785,8 +788,9 @@ typedef struct {
   float scale;
 } lw_kv_weights;
 
-/* Bytes of device workspace an lw_kv_weigh call needs (0: none).  What it holds
-   is of no account before and after a call. */
+/* Bytes of device workspace an lw_kv_weigh call needs on the current device (0: none).  What it holds
+   is of no account before and after a call, but for attention's counters in front
+   where it is attention's too (lw_kv_workspace_bytes): those are left alone. */
 size_t lw_kv_weigh_workspace_bytes(const lw_kv_cache* c, int32_t q_heads, int64_t q_tokens);
 
 lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, void* ws, size_t ws_bytes,

@@ -130,3 +130,40 @@ def test_generation(typ):
                 heads = slice(h * (HQ // H), (h + 1) * (HQ // H))
                 assert relative(sparse[b, heads], s[heads][:, key].softmax(-1) @ vv[key, h]) <= tol
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("typ", [torch.float32, torch.bfloat16])
+def test_one_workspace_for_all_calls(typ):
+    """A workspace of the largest size, zeroed once, serves attention, its weights and sparse attention in turn: the
+    same bits as with workspaces of their own.  (Items are cut between CTAs here, which the counters in front join.)"""
+    gen, st, n = generator(78), status(), 5000
+    cache = pool(gen, 320, H, D, PAGE)
+    table = torch.randperm(320, device=DEV, generator=gen).to(torch.int32).view(1, 320)
+    kv = torch.randn(2, n, H, D, device=DEV, generator=gen)
+    lw.lw_kv_write(cache, kv[0], kv[1], slots_of(table[0], range(n), PAGE), st)
+    summary = torch.zeros(lw.lw_kv_summary_bytes(cache), dtype=torch.uint8, device=DEV)
+    lw.lw_kv_summarise(cache, summary, i32([0]), i32([n]), table, st)
+
+    def sizes(tokens):
+        return (lw.lw_kv_workspace_bytes(cache, HQ, tokens, 1), lw.lw_kv_weigh_workspace_bytes(cache, HQ, tokens),
+                lw.lw_kv_blocks_workspace_bytes(cache, HQ, tokens, 320, 200))
+
+    def zeros(size):
+        return torch.zeros(max(size, 16), dtype=torch.uint8, device=DEV)
+
+    def step(q, tokens, attn, weigh, blocks):
+        out, sparse, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(tokens, HQ, device=DEV)
+        w = torch.empty(1, H, n, device=DEV)
+        args = (i32([0, tokens]), i32([n]), table)
+        lw.lw_kv_attention(cache, q, *args, out, attn, st, max_q=tokens, lse=lse)
+        lw.lw_kv_weigh(cache, q, lse, *args, w, weigh, st, max_q=tokens)
+        lw.lw_kv_attention_blocks(cache, summary, q, *args, sparse, blocks, st, blocks=200)
+        return out, lse, w, sparse
+
+    ws = zeros(max(max(sizes(t)) for t in (1, 7, 300)))
+    for tokens in (300, 1, 7, 300, 1):
+        q = torch.randn(tokens, HQ, D, device=DEV, generator=gen).to(typ)
+        want = step(q, tokens, *(zeros(x) for x in sizes(tokens)))
+        got = step(q, tokens, ws, ws, ws)
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), tokens
+    assert int(st) == 0

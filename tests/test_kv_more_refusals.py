@@ -387,3 +387,16 @@ def test_c_blocks():
                   (dict(page_table=0), INV), (dict(start=FAKE + 2), INV), (dict(batch=0), SHP), (dict(width=-1), SHP),
                   (dict(width=1 << 30), SHP), (dict(stride=-1), SHP)])
     assert status("lw_kv_summarise", ctypes.byref(view()), None, None, None)[0] == INV
+
+
+def test_sizes_are_the_current_devices(monkeypatch):
+    """A workspace is sized by the current device: with another one current than the cache's it is refused."""
+    c = cache()
+    c.index, c.device = 1, torch.device("cuda:1")
+    now = [1]
+    monkeypatch.setattr(lw, "_current_device", lambda: now[0])
+    calls = (lambda: lw.lw_kv_weigh_workspace_bytes(c, 4, 300), lambda: lw.lw_kv_blocks_workspace_bytes(c, 4, 3, 5, 4))
+    assert all(call() > 0 for call in calls)
+    now[0] = 0
+    for call in calls:
+        refused(call, "current device")
