@@ -1208,7 +1208,8 @@ def _kv_clear(a, b) -> bool:
         return True
     def end(t):
         return t.data_ptr() + 4 * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
-    return a.numel() == 0 or b.numel() == 0 or end(a) <= b.data_ptr() or end(b) <= a.data_ptr()
+    return (a.numel() == 0 or b.numel() == 0 or end(a) <= b.data_ptr() or end(b) <= a.data_ptr()
+            or _kv_beside(a, b))   # (interleaved in one buffer)
 
 
 def lw_kv_weigh_workspace_bytes(cache: KvCache, q_heads: int, q_tokens: int) -> int:

@@ -400,3 +400,27 @@ def test_sizes_are_the_current_devices(monkeypatch):
     now[0] = 0
     for call in calls:
         refused(call, "current device")
+
+
+def test_weights_that_lie_between_one_another(guarded):
+    """Rows of one buffer that share no byte, as layers' weights beside one another: not refused (but for the device)."""
+    c = cache()
+    buf = torch.zeros(2, 3, 2, 80)                   # [batch][layer][kv_heads][keys]
+    heads = torch.zeros(2, 2, 2, 80)                 # [batch][kv_heads][which][keys]
+    wide = torch.zeros(2, 2, 120)
+    i32 = dict(page_table=torch.zeros(2, 5, **I32), out_table=torch.zeros(2, 2, **I32))
+
+    def weigh(weights, add_to):
+        lw.lw_kv_weigh(c, rows(3, 4), torch.zeros(3, 4), torch.tensor([0, 1, 3], **I32), torch.zeros(2, **I32),
+                       i32["page_table"], weights, torch.zeros(16, dtype=torch.uint8), st(), max_q=2, add_to=add_to)
+
+    def evict(weights, out):
+        lw.lw_kv_evict(c, weights, torch.zeros(2, **I32), i32["page_table"], i32["out_table"], torch.zeros(2, **I32), out,
+                       torch.zeros(2, 2, 20, **I32), st(), keep=20)
+
+    for call in (weigh, evict):
+        for a, b in ((buf[:, 0], buf[:, 1]), (buf[:, 2], buf[:, 0]), (heads[:, :, 0], heads[:, :, 1])):
+            refused(lambda: call(a, b), "pages on cpu")
+        refused(lambda: call(buf[:, 0], buf[:, :2].flatten(1, 2)[:, 1:3]), "overlaps")     # a head of both
+    refused(lambda: evict(wide[..., :80], wide[..., 80:]), "pages on cpu")                 # behind the weights, row by row
+    refused(lambda: evict(wide[..., :80], wide[..., 79:]), "overlaps")
