@@ -313,8 +313,8 @@ def run(group, widths):
     for width in widths:
         table = torch.full((tokens, width), -1, **i32)
         table[:, :4] = torch.arange(4, **i32)
-        ws = torch.zeros(lw.lw_kv_blocks_workspace_bytes(cache, heads * group, tokens, width, blocks), dtype=torch.uint8,
-                         device="cuda")
+        need = lw.lw_kv_blocks_workspace_bytes(cache, heads * group, tokens, width, blocks)
+        ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
         lw.lw_kv_attention_blocks(cache, summary, q, start, n, table, out, ws, st, blocks=blocks, chosen=chosen)
         assert bool((chosen == torch.tensor([0, 1, 3], **i32)).all()) and int(st) == 0, (group, width)
 
@@ -334,3 +334,66 @@ def test_any_width_of_the_page_table():
     r = subprocess.run([sys.executable, "-c", WIDTHS], capture_output=True, text=True, timeout=300,
                        cwd=Path(__file__).resolve().parent.parent)
     assert r.returncode == 0 and r.stdout.split()[-1] == "done", r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("case", [(8, 1, 128, 64), (16, 16, 64, 16), (6, 2, 96, 48)], ids=str)
+def test_bf16_operands_hold_their_bits(case):
+    """Before the output's rounding a bf16 call is within 2^-11, as lw_kv_attention's few rows are (probabilities, and
+    these times the values' scales, in 11 bits each: 2^-12 at most).  The rounding's own error is known from the exact
+    result; independent errors add as squares (2 % for chance).  So a call may differ from one that carries 32 bits
+    throughout by as many outputs as lie that near the middle between two bf16 numbers."""
+    hq, h, dim, page = case
+    gen, st, lens = generator(60), status(), [3000, 2500, 2000, 1000]
+    cache, table, _ = filled(gen, lens, h, dim, page)
+    summary = torch.zeros(lw.lw_kv_summary_bytes(cache), dtype=torch.uint8, device=DEV)
+    lw.lw_kv_summarise(cache, summary, i32([0] * 4), i32(lens), table, st)
+    q = torch.randn(8, hq, dim, device=DEV, generator=gen).to(torch.bfloat16)
+    out, _, chosen = attend(cache, summary, q, [0, 2, 4, 6, 8], lens, table, st, 640 // page, 1, 2)
+    want = torch.zeros(q.shape, dtype=torch.float64, device=DEV)
+    for i in range(8):
+        n = lens[i // 2]
+        k, v = (x.double() for x in read(cache, slots_of(table[i // 2], range(n), page)))
+        for g in range(h):
+            rows = slice(g * (hq // h), (g + 1) * (hq // h))
+            at = [x for x in chosen[i, g].tolist() if x >= 0]
+            pos = n - 2 + i % 2
+            key = torch.tensor([j for x in at for j in range(x * page, min(x * page + page, pos + 1))], device=DEV)
+            want[i, rows] = (q[i, rows].double() @ k[key, g].T / math.sqrt(dim)).softmax(-1) @ v[key, g]
+    r = relative(want.to(torch.bfloat16), want)
+    assert int(st) == 0 and relative(out, want) <= 1.02 * math.hypot(r, 2.0 ** -11)
+
+
+@pytest.mark.parametrize("case", [(4, 1, 128, 64), (2, 2, 64, 16), (8, 1, 96, 48)], ids=str)
+def test_scores_stand_for_unrounded_ranges(case):
+    """A page's score is its ranges' upper bound on q.k, sum max(q lo, q hi), but for 8-bit codes: each element is off
+    by at most half a step, so the sum by E = sum |q| step / 2 + |k| u / 2 + step u / 4 (1e-4 of it for fp32 steps: a
+    code's quotient is near 127 to 2^-22).  No page that was left out has an unrounded score above a chosen one's by
+    more than their two E."""
+    hq, h, dim, page = case
+    gen, st, n, blocks, first, recent = generator(61), status(), 6000, 20, 1, 2
+    cache, table, _ = filled(gen, [n], h, dim, page)
+    summary = torch.zeros(lw.lw_kv_summary_bytes(cache), dtype=torch.uint8, device=DEV)
+    lw.lw_kv_summarise(cache, summary, i32([0]), i32([n]), table, st)
+    q = torch.randn(6, hq, dim, device=DEV, generator=gen)
+    _, _, chosen = attend(cache, summary, q, [0, 6], [n], table, st, blocks, first, recent)
+    assert int(st) == 0
+    k, nb = read(cache, slots_of(table[0], range(n), page))[0].double(), -(-n // page)
+    k = torch.cat([k, k[-1:].expand(nb * page - n, h, dim)]).view(nb, page, h, dim)
+    lo, hi = k.amin(1), k.amax(1)
+    size = torch.maximum(lo.abs(), hi.abs())
+    step = size.amax(-1, keepdim=True) / 127
+    for i in range(6):
+        pages = (n - 6 + i) // page + 1
+        for g in range(h):
+            rows = q[i, g * (hq // h):(g + 1) * (hq // h)].double()[:, None]       # [group, 1, dim]
+            u = rows.abs().amax(-1, keepdim=True) / 127
+            true = torch.maximum(rows * lo[:pages, g], rows * hi[:pages, g]).sum(-1)
+            off = (rows.abs() * step[:pages, g] / 2 + size[:pages, g] * u / 2 + step[:pages, g] * u / 4).sum(-1)
+            score, off = true.amax(0), off.amax(0) * (1 + 1e-4) + 1e-5 * true.abs().amax(0)
+            took = torch.zeros(pages, dtype=torch.bool, device=DEV)
+            took[chosen[i, g].long()] = True
+            free = torch.ones_like(took)
+            free[:first], free[pages - recent:] = False, False
+            ins, outs = took & free, ~took & free
+            assert int(ins.sum()) == blocks - first - recent
+            assert float((score + off)[ins].min()) >= float((score - off)[outs].max())

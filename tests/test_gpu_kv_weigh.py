@@ -307,3 +307,56 @@ def test_pages_that_no_row_sees_are_not_needed(ts, causal, typ):
     gone[0, first[0] // page] = -1
     weigh(cache, gone, q, lse, start, lens, w, st, **kw)
     assert int(st) == lw.LW_DEV_BAD_PAGE
+
+
+@pytest.mark.parametrize("typ", ["fp32", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 30, 300])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+def test_keys_of_any_magnitude(typ, tokens, dim):
+    """Keys from the smallest that fp16 scales hold to the format's limit, with queries that bring the scores to unit
+    spread; in the last sequence large and small keys by turns of 100, each part's weights looked at alone.
+    A product's keys keep 2^-21 of the largest of a unit's, some 5 times the usual one: with terms of 12 in all at
+    most, 12 (16 2^-24 + 5 2^-21 + 2^-23) = 4e-5 beside the exponential's and the sums' 1.6e-5."""
+    gen, st, n, page = generator(17), status(), 700, 16
+    mags = (1e-5, 1e-3, 0.03, 1.0, 12000.0, None)
+    cache, table, _ = filled(gen, [n] * 6, 2, dim, page)
+    k = torch.randn(6, n, 2, dim, device=DEV, generator=gen)
+    q = torch.randn(6, tokens, 4, dim, device=DEV, generator=gen)
+    for b, mag in enumerate(mags):
+        if mag is None:
+            k[b] *= torch.where(torch.arange(n, device=DEV) // 100 % 2 == 0, 1.0, 1e-3)[:, None, None]
+        else:
+            k[b], q[b] = k[b].clamp(-5, 5) * mag, q[b] / mag
+        lw.lw_kv_write(cache, k[b], k[b], slots_of(table[b], range(n), page), st)
+    q, start, lens = q.flatten(0, 1).to(TYPES[typ]), [tokens * b for b in range(7)], [n] * 6
+    scale = 0.7 / math.sqrt(dim)
+    lse = logsums(cache, table, q, start, lens, True, 0, scale)
+    want = expected(cache, table, q, start, lens, lse, None, True, 0, scale)
+    w = torch.empty(6, 2, n, device=DEV)
+    for hint in (tokens, 1):
+        weigh(cache, table, q, lse, start, lens, w, st, scale=scale, max_q=hint)
+        for b in range(6):
+            for at in range(0, n, 100):
+                part = slice(at, at + 100)
+                assert relative(w[b, :, part], want[b, :, part]) <= TOL, (b, at, hint)
+    assert int(st) == 0
+
+
+@pytest.mark.parametrize("typ", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window", [0, 1000, 4000])
+def test_units_of_one_cta(typ, dim, window):
+    """A long sequence's units of 128 keys are more than the CTAs of its heads: each takes several, the first of them
+    without a row under a window."""
+    gen, st, n, heads, tokens = generator(18), status(), 9000, 8, 300
+    cache, table, _ = filled(gen, [n], heads, dim, 64)
+    q, scale = queries(gen, tokens, heads, dim, typ), 1 / math.sqrt(dim)
+    lse = logsums(cache, table, q, [0, tokens], [n], True, window, scale)
+    add = torch.rand(1, heads, n, device=DEV, generator=gen)
+    want = expected(cache, table, q, [0, tokens], [n], lse, add, True, window, scale)
+    w = torch.empty(1, heads, n, device=DEV)
+    for _ in range(2):
+        weigh(cache, table, q, lse, [0, tokens], [n], w, st, scale=scale, max_q=tokens, add_to=add, window=window)
+        for h in range(heads):
+            assert relative(w[0, h], want[0, h]) <= TOL
+    assert int(st) == 0
