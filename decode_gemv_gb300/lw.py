@@ -1045,7 +1045,11 @@ def lw_rotary_table(table, *, first: int = 0, base: float = 10000.0, scaling: in
     try:
         a = _ROTARY.pack(table.shape[1], scaling, base, factor, old_length, low, high, gain)
     except struct.error as e:
-        _refuse(fn, f"rot {table.shape[1]}, scaling {scaling!r}: {e}")
+        _refuse(fn, f"rot {table.shape[1]}, scaling {scaling!r}, base {base!r}, factor {factor!r}, old_length "
+                    f"{old_length!r}, low {low!r}, high {high!r}, gain {gain!r}: {e}")
+    _kv_whole(fn, first=first)
+    if not -1 << 63 <= first < 1 << 63:
+        _refuse(fn, f"first: {first} is out of range")
     r = load().lw_rotary_table(a, first, table.shape[0], table.data_ptr(),
                                _raw_stream(table.get_device()) if stream is None else stream.cuda_stream)
     if r:

@@ -424,3 +424,13 @@ def test_weights_that_lie_between_one_another(guarded):
         refused(lambda: call(buf[:, 0], buf[:, :2].flatten(1, 2)[:, 1:3]), "overlaps")     # a head of both
     refused(lambda: evict(wide[..., :80], wide[..., 80:]), "pages on cpu")                 # behind the weights, row by row
     refused(lambda: evict(wide[..., :80], wide[..., 79:]), "overlaps")
+
+
+def test_positions_out_of_range(guarded, monkeypatch):
+    """A first position that no 64-bit number holds is refused, not wrapped round to another one."""
+    from test_kv_limits import on1
+    monkeypatch.setattr(lw, "_current_device", lambda: 1)
+    for first in (1 << 64, (1 << 64) + 5, -(1 << 70), 1 << 63, 1.5, "3", None):
+        refused(lambda: lw.lw_rotary_table(on1(torch.zeros(4, 8)), first=first), "first")
+    refused(lambda: lw.lw_rotary_table(on1(torch.zeros(4, 8)), base=10 ** 400), "base")
+    refused(lambda: lw.lw_rotary_table(on1(torch.zeros(4, 8)), gain="x"), "gain")
