@@ -22,9 +22,9 @@ struct SummaryArgs {
 };
 constexpr int kSumWarps = 8;
 
-// Bound by instruction issue: some 370 instructions for 16 keys (restoring the codes 140, minimum and maximum 64,
-// the page's sums over the keys a quarter of 280), two CTAs an SM.  8 sequences of 20000 to 131072 tokens, 8 heads of
-// 128: 166 us, 0.38 GB of keys, 2.3 TB/s; one page of each of 16 sequences' 16 heads 8 us.
+// Bound by instruction issue: 519 instructions for 16 keys (measured with pages of 64: a sixth is the page's reduction
+// over lanes, the rest restores codes and compares) in 68 % of the slots, two CTAs an SM.  8 sequences of 20000 to
+// 131072 tokens, 8 heads of 128: 168 us, 0.38 GB of keys, 2.3 TB/s; one page of each of 16 sequences' 16 heads 7 us.
 // A warp a page and head: lanes hold keys lane / 4 and 8 more of a tile, elements 32 g + 8 (lane % 4) + 0..7.
 template <int D>
 __global__ void __launch_bounds__(32 * kSumWarps, 2) kv_summarise_kernel(const SummaryArgs a) {
@@ -199,8 +199,9 @@ using ChooseShared = dev::SelectShared<8>;
 // the pages and choose together (lw_kvselect.cuh).
 // Scores.  The codes of the group's query heads have their positive and negative parts apart, so that the larger of
 // c hi and c lo is picked by a product: sum c+ hi + c- lo, in whole numbers (dp4a).  8 lanes take a record.
-// 64 tokens and heads on up to 2048 pages 25 us (17 MB of records), 768 on up to 563 20 us: chains of reads (ranges,
-// page table, records, page table) and the choice's barriers; two kernels, the scores by way of memory, took 28 and 22.
+// 64 tokens and heads on up to 2048 pages 25 us (17 MB of records), 768 on up to 563 20 us (of calls of 51 and 61):
+// chains of reads (ranges, page table, records, page table) and the choice's barriers; two kernels, the scores by way
+// of memory, took 28 and 22.
 template <int D, class T>
 __global__ void __launch_bounds__(kChoose) kv_choose_kernel(const BlockArgs a) {
   constexpr int W = D / 32, NT = kChoose, kWarps = NT / 32;   // W: words of a part of a record a lane

@@ -24,7 +24,9 @@ __device__ __forceinline__ int evict_keys(const EvictArgs& a, int b) {
 }
 
 // ---- the choice ----------------------------------------------------------------
-// A cluster a head (lw_kvselect.cuh); a stretch that is too long for shared memory is read again instead.
+// A cluster a head (lw_kvselect.cuh); a stretch that is too long for shared memory is read again instead.  64 heads'
+// 65536 keys some 32 us, where 17 MB have to come: after the load a CTA walks its keys five times (three digits by
+// atomics in shared memory, the count, the places), with barriers between.
 constexpr int kMostSelect = 40960;   // order keys a CTA keeps
 constexpr int kSelect = 512;
 using EvictShared = dev::SelectShared<11>;
@@ -79,9 +81,9 @@ __global__ void __launch_bounds__(kSelect) kv_evict_select_kernel(const EvictArg
 // read before any is written (a barrier of the cluster between), and later
 // rounds' tokens lie behind its places (kept[i] >= i); into other pages, the
 // warps need not wait for one another.
-// 64 heads' 8192 of 65536 keys: 58 us into other pages, 66 in place; the choice 30.  The 84 MB that move are read as
-// some 235: a token of 160 bytes lies in ten sectors (its pair's value codes, scales and minimums beside its own),
-// and memory gives 64 bytes at a time: 47 us at a copy's rate.
+// 64 heads' 8192 of 65536 keys: the call 88 us into other pages, 97 in place (the choice among them some 32: keeping one
+// key takes 35).  The 84 MB that move are read as some 235: a token of 160 bytes lies in ten sectors (its pair's value
+// codes, scales and minimums beside its own), and memory gives 64 bytes at a time: 47 us at a copy's rate.
 constexpr int kMoveWarps = 16, kMove = 32 * kMoveWarps;
 
 // The tokens of a tile: lane i (and i + 16) has the i-th.

@@ -267,8 +267,10 @@ __device__ __forceinline__ void rotate_queries(const RotaryArgs& a, const float*
 constexpr int kTokens = 16;   // of a writing block; twice as many of a rotating one
 
 // Measured, 65536 tokens of 32 query and 8 key/value heads of 128 in bf16: 254 us, 5.4 TB/s of the 1.37 GB that
-// have to move (a copy reaches 6.8).  A block a head, each with its tokens' angles and slots read anew, took 577 us:
-// a chain of three reads for 4 KB of keys and values.  One token: 3 us, the same chain.
+// have to move (a copy reaches 6.8); in fp32 464 us.  A block a head, each with its tokens' angles and slots read anew,
+// took 577 us: a chain of three reads for 4 KB of keys and values.  One token: 2.4 us, the same chain.
+// Not WIDE (rot no multiple of 16, or rows off 16-byte boundaries): element by element, angles and partners read anew
+// for each head.  96 wide, bf16: 48 elements rotated 209 us, 24 of them 657.
 template <class T, int D, bool WIDE, bool NEAR>
 __global__ void __launch_bounds__(kTokens * D / 8, 3) kv_write_rotary_kernel(const RotaryArgs a) {
   dev::pdl_wait();

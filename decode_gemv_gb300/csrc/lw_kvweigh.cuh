@@ -17,10 +17,11 @@
 // registers (one token of a group of up to 8 heads; more rows take the keys once
 // a block); else up to 64 rows in shared memory.
 //
-// Bound by instruction issue where keys are many: 250 instructions a tile of 16 keys (a third restores the codes),
-// in 60 % of the slots (waits on the matrix instructions' results, 4 warps a scheduler; 6 of 80 registers spill: 142
-// us where this takes 129).  8 sequences of 20000 to 131072 keys (8 heads of 128 with 4 query heads each, bf16): 129
-// us, 0.47 GB of keys and weights, 3.6 TB/s.  4097 keys of one sequence: 5 us, a chain of reads.
+// Where keys are many: 250 instructions a tile of 16 keys (a third restores the codes) in 60 % of the issue slots; the
+// rest are waits on the matrix instructions' results, 4 warps a scheduler (6 warps of 80 registers spill: 142 us
+// where this takes 129).  8 sequences of 20000 to 131072 keys (8 heads of 128 with 4 query heads each): bf16 130
+// us, 0.47 GB of keys and weights, 3.6 TB/s; fp32 161.  Under a window of 129 keys 44, the weights of 32 keys a warp at a
+// time.  4097 keys of one sequence: 5.5 us, a chain of reads.
 #pragma once
 
 #include "lw_kvfew.cuh"

@@ -13,21 +13,21 @@
 //
 // Two kernels.  kv_weigh_rows_kernel writes the rows as operand tiles, once for
 // all units (a unit would spend as many instructions on them as on its
-// exponentials), with each row's scale and lse in log2 units.  kv_weigh_many_kernel
-// is a CTA a unit:
+// exponentials), with each row's scale and lse in log2 units.  A CTA of
+// kv_weigh_many_kernel takes every so many-th unit of a head of a sequence:
 //  * warp 0 fetches row tiles by bulk copies (a tile is one contiguous image);
 //  * warp 1 issues the products, into three accumulators of 128 columns: the keys are the operand in tensor
 //    memory (both in shared memory are 8 KB for 64 cycles of products, all that it gives: 379 us where this takes
 //    350);
-//  * 8 warps restore the keys, then two groups of four take the tiles in turn:
+//  * 8 warps restore the unit's keys and send for the next one's, then two groups of four take the tiles in turn:
 //    a thread reads its key's 128 scores and adds 2^(s f - lse) of those that it is
 //    seen by.  A key is seen by a contiguous range of rows (causal: from some row
 //    on, windowed: up to some row), so only tiles across an end of it are masked.
-// 2048 tokens on 14336 keys (8 heads of 128 with 4 query heads each, bf16): 360 us, 716 TFLOP/s of useful
-// products, of which two are carried out for one: 1430, 84 % of what the tensor cores sustain; a tile's exponentials
-// take about as long as its products.  8 sequences of 32768 keys, 64 tokens each: 522 us, a unit 4.8 us, of which 1 is
-// products: its start (keys restored, tensor memory written) and its end.  The next unit's keys are fetched while this
-// one's rows run (603 -> 550 us at 48 tokens).
+// 2048 tokens on 14336 keys (8 heads of 128 with 4 query heads each): bf16 369 us, both kernels, 699 TFLOP/s of
+// useful products, of which two are carried out for one: 1400, 80 % of what the tensor cores sustain; a tile's
+// exponentials take about as long as its products.  fp32, three for one: 492.  8 sequences of 32768 keys, 64 tokens
+// each, bf16: 530 us, a unit 4.9 us, of which 1 is products: its start (keys restored, tensor memory written) and its
+// end.  The next unit's keys are fetched while this one's rows run (603 -> 553 us at 48 tokens).
 // Units are few where keys are: then a cluster shares a unit's row tiles, and rank 0
 // adds the ranks' sums in order.
 #pragma once

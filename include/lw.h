@@ -756,12 +756,16 @@ lw_status lw_kv_write_rotary(const lw_kv_cache* c, const lw_kv_rotated* a, int32
  * over the rows (token t of sequence b, query head of h's group) that see key j:
  * q, lse, q_start, kv_len, page_table, scale, causal and window as they were in
  * lw_kv_attention, after which lse is there.  add_to may be NULL (0) or weights
- * itself.  Entries j < kv_len[b] are written, the others left.  Sums and
+ * itself; else the two share no byte.  Entries j < kv_len[b] are written, the others left.  Sums and
  * exponentials are fp32, the order of the sum is fixed (deterministic on a given
  * device); products carry 22 bits of fp32 queries, all of 16-bit ones (down to
- * 2^-23 of a row's largest).  A NaN in a key or in lse is in the weights that
- * the formula puts it in.  Keys in pages outside the cache weigh nothing.
+ * 2^-23 of a row's largest), and the keys as they are cached; where max_q asks for
+ * the kernel of many rows, 22 bits of them, and a row's lse is rounded once more, to fp32
+ * in units of log 2 (a weight is then off by some 2^-24 |lse| more).  A NaN in a key or in
+ * lse is in the weights that the formula puts it in.  Pages that no row sees are not read;
+ * a page outside the cache that one sees is reported (LW_DEV_BAD_PAGE), its keys weigh nothing.
  * kv_len past w_keys is reported (LW_DEV_BAD_SEQ); those keys are not written.
+ * Without room for a key (table_width or w_keys 0) nothing is launched or reported.
  * Limits as in lw_kv_attention.
  */
 typedef struct {
@@ -806,7 +810,7 @@ lw_status lw_kv_weigh(const lw_kv_cache* c, const lw_kv_weights* a, void* ws, si
  * Keys that were rotated stay so: their positions are the original ones.
  * out_table may be page_table's own pages in the same places (in place: the
  * pages beyond token m are then free), or pages that no sequence of the call
- * names; out_weights may be weights itself.  A page that is written must be one
+ * names; out_weights may be weights itself, else they share no byte.  A page that is written must be one
  * sequence's alone.  out_len must not be kv_len.  Tokens of pages outside the cache are not moved,
  * and reported (LW_DEV_BAD_PAGE).  The places of tokens past m are left as they were.  kv_len past the page table or
  * w_keys is clamped (LW_DEV_BAD_SEQ).  first, recent >= 0, 1 <= keep, first +
@@ -874,7 +878,7 @@ lw_status lw_kv_summarise(const lw_kv_cache* c, const lw_kv_summaries* a, int32_
  * rows of tokens outside every sequence are left.
  * 1 <= recent, 0 <= first, first + recent <= blocks; table_width, blocks <= 40960;
  * q_heads / kv_heads <= 128; q_tokens * kv_heads <= 65535; n_pages * kv_heads * page_tokens < 2^32 (else LW_ERR_SHAPE).
- * max_q is not used.  Everything else, lse too, as in lw_kv_attention.
+ * max_q is not used.  Everything else, lse and the bits that operands keep too, as in lw_kv_attention.
  */
 typedef struct {
   const void* summary;
